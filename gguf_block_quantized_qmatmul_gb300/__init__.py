@@ -14,6 +14,7 @@ Entry points mirror the C ABI names:
   block_sums(wq, x, wtype)        exact per-block integer sums of the int8_act form
   matmul_batch(items, wtype, mode)  many independent small matmuls in one launch
   matmul_batch_typed(items, mode)   the same, each item with its own weight type
+  q4g_*, moe_*                    4-bit group-scale weights and mixture-of-experts layers (q4g.py)
 """
 from __future__ import annotations
 
@@ -36,7 +37,9 @@ STATUS = {0: "QMM_OK", 1: "QMM_ERR_NULL", 2: "QMM_ERR_SHAPE", 3: "QMM_ERR_TYPE",
 EXPORTS = ["qmm_block_values", "qmm_block_bytes", "qmm_row_bytes", "qmm_quantize_weights", "qmm_quantize_act",
            "qmm_dequantize", "qmm_matmul_workspace", "qmm_matmul_launches", "qmm_matmul", "qmm_matmul_static_workspace",
            "qmm_block_sums", "qmm_matmul_batch", "qmm_matmul_batch_typed", "qmm_test_inject", "qmm_test_set_wait_limit",
-           "qmm_last_device_error", "qmm_status_string"]
+           "qmm_last_device_error", "qmm_status_string", "qmm_q4g_bytes", "qmm_q4g_pack", "qmm_q4g_pack_q4_0",
+           "qmm_q4g_dequantize", "qmm_q4g_matmul_workspace", "qmm_q4g_matmul", "qmm_moe_route_workspace", "qmm_moe_route",
+           "qmm_moe_gate_up_workspace", "qmm_moe_gate_up", "qmm_moe_down_workspace", "qmm_moe_down"]
 INJECT = {"off": 0, "launch_failure": 1, "stall": 2}
 
 
@@ -69,6 +72,7 @@ def _load() -> ctypes.CDLL:
     lib.qmm_test_set_wait_limit.argtypes, lib.qmm_test_set_wait_limit.restype = [i32], i32
     lib.qmm_last_device_error.argtypes, lib.qmm_last_device_error.restype = [], i32
     lib.qmm_status_string.argtypes, lib.qmm_status_string.restype = [i32], ctypes.c_char_p
+    q4g.declare(lib)
     return lib
 
 
@@ -262,3 +266,8 @@ def test_set_wait_limit(log2_clocks: int) -> None:
     """Failure-test hook: spin limit of the device's bounded waits, 2^log2
     SM clocks (0 restores the default of about one second)."""
     _check(_lib().qmm_test_set_wait_limit(log2_clocks), "qmm_test_set_wait_limit")
+
+
+from . import q4g  # noqa: E402  (uses the helpers above)
+from .q4g import (Q4GWeights, Route, moe_down, moe_gate_up, moe_route, q4g_dequantize, q4g_matmul,  # noqa: E402,F401
+                  q4g_matmul_workspace, q4g_pack, q4g_pack_q4_0)

@@ -260,6 +260,10 @@ qmm_status stream_call(qmm_type wtype, int am, int epi, const void* wq, const fl
 
 }  // namespace
 
+namespace qmm {
+cudaError_t device_constants(unsigned** err, int* sms, int* smem) { return device_info(err, sms, smem); }
+}  // namespace qmm
+
 extern "C" {
 
 int64_t qmm_block_values(qmm_type t) {

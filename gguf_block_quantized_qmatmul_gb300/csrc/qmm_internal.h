@@ -35,6 +35,9 @@ cudaError_t launch_tcx_f32(int wt, const TcxPlan& plan, const void* wq, const fl
 bool make_map(CUtensorMap* m, CUtensorMapDataType dt, const void* base, unsigned long long inner, unsigned long long outer,
               unsigned long long row_bytes, unsigned box_inner, unsigned box_outer, CUtensorMapSwizzle swz);
 
+// The current device's error word, SM count and opt-in shared memory (looked up once per device).
+cudaError_t device_constants(unsigned** err, int* sms, int* smem);
+
 // largest activation batch served by the per-thread dp4a GEMV (int8_act,
 // Q8_0 weights only); larger decode batches, Q4_K weights and every f32_act
 // decode batch up to 8 use the 16-row-tile tensor-core kernel
@@ -62,10 +65,10 @@ inline cudaError_t ensure_smem(F* kernel, int smem_max, unsigned long long& done
 // bounded wait that needs such data; only constant inputs (the weights) are
 // read before it.
 template <typename... KArgs, typename... Args>
-inline cudaError_t launch_pdl(void (*kernel)(KArgs...), unsigned grid, unsigned block, size_t smem, cudaStream_t s,
-                              Args... args) {
+inline cudaError_t launch_pdl_2d(void (*kernel)(KArgs...), unsigned gx, unsigned gy, unsigned block, size_t smem,
+                                 cudaStream_t s, Args... args) {
     cudaLaunchConfig_t cfg = {};
-    cfg.gridDim = dim3(grid);
+    cfg.gridDim = dim3(gx, gy);
     cfg.blockDim = dim3(block);
     cfg.dynamicSmemBytes = smem;
     cfg.stream = s;
@@ -75,6 +78,11 @@ inline cudaError_t launch_pdl(void (*kernel)(KArgs...), unsigned grid, unsigned 
     cfg.attrs = attr;
     cfg.numAttrs = 1;
     return cudaLaunchKernelEx(&cfg, kernel, args...);
+}
+template <typename... KArgs, typename... Args>
+inline cudaError_t launch_pdl(void (*kernel)(KArgs...), unsigned grid, unsigned block, size_t smem, cudaStream_t s,
+                              Args... args) {
+    return launch_pdl_2d(kernel, grid, 1u, block, smem, s, args...);
 }
 
 }  // namespace qmm

@@ -1,0 +1,490 @@
+// qmm_q4g_gemm.cuh -- products of 4-bit group-scale weights with many
+// activation rows on tcgen05: prompts through a dense linear, and the
+// experts' products of a batch (grouped by expert, any number of rows each).
+//
+// Mathematics.  Weight rows and activation rows are brought into f16's range
+// by a power of two each (the weights' at layout time, the activations' by the
+// preparation launch; f16 activations are taken as they are), and
+//   y = 2^-(a + b) sum_k f16(s 2^a (q - z)) (x 2^b).
+// s 2^a and q - z are exact in f16, their product is rounded to 11 bits: half
+// of the products (codes 0, +-1, 2, 4, 8 off the zero point) are exact, so the
+// sum's error is below that of rounding an f16 result, and far below a bf16
+// one.  bf16 activations are exact in f16 after scaling (values under 2^-29 of
+// their row's largest lose bits).  f32 activations take two pieces of both
+// operands, v = hi + lo, and three MMAs, hi hi + hi lo + lo hi: s (q - z) has
+// at most 16 significant bits, so the weights' pieces are exact; the
+// activations keep 22 bits.
+//
+// One persistent block per SM over units: 128 weight rows (8 row blocks, the
+// MMA's M) x up to bx activation rows of one expert (its N, rounded up to 16).
+//   warp 0      activation tiles (64 K, 128-byte swizzle): for a dense call one
+//               2-D box, for experts gathered rows, four to a copy
+//   warp 1      one thread: four MMAs (twelve with two pieces) per 64 K, A in
+//               tensor memory, B in shared memory
+//   warp 2      raw weights: eight 1-D copies (a row block's two segments each)
+//               per 256 K
+//   warps 3-10  epilogue: accumulator columns to registers, scaled; the experts'
+//               first product takes its up row from the lane eight away (paired
+//               layout) for silu(g) u
+//   warps 11-18 conversion: a lane's uint4 of codes becomes fragment registers
+//               and goes to tensor memory as they are (16-lane x 128-bit
+//               stores); two groups, even and odd 64-K tiles
+// The weights are bound for tensor memory, so shared memory feeds only the
+// activation tiles to the MMAs.  With two pieces the tensor core's truncating
+// f32 accumulation would show: the accumulator is restarted every kQgChunk
+// tiles and the epilogue adds the chunks in registers.
+#pragma once
+
+#include "qmm_q4g_rows.cuh"
+
+namespace qmm {
+
+constexpr int kQgThreads = 19 * 32;
+constexpr int kQgEpi0 = 3, kQgConv0 = 11;
+constexpr int kQgRawMax = 4, kQgStageMax = 8;
+constexpr int kQgChunk = 4;      // 64-K tiles per accumulation chunk (two pieces)
+constexpr int kQgMaxE = 512;     // experts of a grouped call
+constexpr int kQgWCol0 = 256;    // weight pieces in tensor memory from this column
+
+struct QgGemmParams {
+    QgCall c;
+    float* part;          // P_DOWN: [T top_k][N]
+    const float* xs;      // 2^-b per activation row; NULL: 1
+    const float* wis;     // 2^-a per weight row, layout order
+    unsigned* err;
+    int xrows;            // rows of an activation plane (the lo plane follows)
+    int bx, nacc, mtiles, ntiles, kt, nraw, nstage, grid;
+    int off_raw, off_bar;
+};
+
+// four gathered rows of a 2-D tensor map (box: one row), completing on an mbarrier
+__device__ __forceinline__ void tma_gather4(uint32_t dst, const CUtensorMap* map, int x, int y0, int y1, int y2, int y3, uint32_t bar) {
+    asm volatile(
+        "cp.async.bulk.tensor.2d.shared::cluster.global.tile::gather4.mbarrier::complete_tx::bytes [%0], [%1, {%2, %3, %4, %5, %6}], [%7];" ::"r"(
+            dst),
+        "l"(map), "r"(x), "r"(y0), "r"(y1), "r"(y2), "r"(y3), "r"(bar)
+        : "memory");
+}
+// 32 columns of 16 lanes from fragment registers: lane 4 g + t's registers 2 j, 2 j + 1 are column 4 j + t of lanes g, g + 8
+__device__ __forceinline__ void tc_st_frag(uint32_t taddr, const uint32_t v[16]) {
+    asm volatile(
+        "tcgen05.st.sync.aligned.16x128b.x8.b32 [%0], {%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,%15,%16};" ::"r"(taddr),
+        "r"(v[0]), "r"(v[1]), "r"(v[2]), "r"(v[3]), "r"(v[4]), "r"(v[5]), "r"(v[6]), "r"(v[7]), "r"(v[8]), "r"(v[9]),
+        "r"(v[10]), "r"(v[11]), "r"(v[12]), "r"(v[13]), "r"(v[14]), "r"(v[15])
+        : "memory");
+}
+
+// One 64-K tile h of a segment of one row block: fragment registers of its f16 weights (and their rests).
+template <int NP, int NG>
+__device__ __forceinline__ void qg_convert(const uint8_t* seg, int h, int lane, float m0, float m1, uint32_t hi[16], uint32_t lo[16]) {
+    const uint4 q = *reinterpret_cast<const uint4*>(seg + h * kQgTile + lane * 16);
+    const uint32_t word[4] = {q.x, q.y, q.z, q.w};
+    const uint32_t* sw = reinterpret_cast<const uint32_t*>(seg + 2 * kQgTile + (lane >> 2) * (8 * NG));
+    uint32_t zl = 0, zh = 0;
+    __half2 s0, s1;
+#pragma unroll
+    for (int s = 0; s < 4; ++s) {
+        if (s == 0 || (NG == 4 && s == 2)) {
+            const int gi = NG == 1 ? 0 : NG == 2 ? h : 2 * h + (s >> 1);
+            const uint2 v = *reinterpret_cast<const uint2*>(sw + 2 * gi);
+            zl = qg_zero<false>(v.x, false);
+            zh = qg_zero<false>(v.y, true);
+            s0 = __float2half2_rn(qg_scale(v.x) * m0);
+            s1 = __float2half2_rn(qg_scale(v.y) * m1);
+        }
+        uint32_t a[4];
+        qg_codes<false>(word[s], zl, zh, a);
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+            const __half2 c = *reinterpret_cast<__half2*>(&a[i]);
+            const __half2 sc = i & 1 ? s1 : s0;
+            const __half2 p = __hmul2(c, sc);
+            hi[4 * s + i] = *reinterpret_cast<const uint32_t*>(&p);
+            if (NP == 2) {
+                const __half2 r = __hfma2(c, sc, __hneg2(p));
+                lo[4 * s + i] = *reinterpret_cast<const uint32_t*>(&r);
+            }
+        }
+    }
+}
+
+// a unit's place
+struct QgUnit {
+    int e, p0, n, nt;  // expert, first position (row of x in a dense call), activation rows, row tile
+};
+
+template <int NP, int NG>
+__global__ void __launch_bounds__(kQgThreads, 1) q4g_gemm_kernel(const __grid_constant__ CUtensorMap tx, const QgGemmParams p) {
+    extern __shared__ __align__(1024) uint8_t smraw[];
+    uint8_t* sm = smraw + ((1024 - (smem_u32(smraw) & 1023)) & 1023);
+    const QgCall& c = p.c;
+    const QgWeights& w = c.w;
+    const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
+    uint64_t* bars = reinterpret_cast<uint64_t*>(sm + p.off_bar);
+    uint64_t* full = bars;                         // activation tile landed and weight pieces in tensor memory
+    uint64_t* empty = full + kQgStageMax;          // stage consumed by the MMAs (commit)
+    uint64_t* r_full = empty + kQgStageMax;        // raw weights landed
+    uint64_t* r_empty = r_full + kQgRawMax;        // raw stage converted
+    uint64_t* acc_full = r_empty + kQgRawMax;      // accumulator complete (commit)
+    uint64_t* acc_empty = acc_full + 2;            // accumulator read
+    static_assert((2 * kQgStageMax + 2 * kQgRawMax + 4) * 8 <= 256, "mbarriers overlap the TMEM slot");
+    uint32_t* tslot = reinterpret_cast<uint32_t*>(sm + p.off_bar + 256);
+    volatile int* flags = reinterpret_cast<volatile int*>(sm + p.off_bar + 320);
+    int* col_slot = reinterpret_cast<int*>(sm + p.off_bar + 512);      // [8 warps][128]
+    float* col_scale = reinterpret_cast<float*>(col_slot + 8 * 128);   // [8 warps][128]
+    int* ts = reinterpret_cast<int*>(col_scale + 8 * 128);             // [E + 1] activation tiles before each expert
+    const bool grouped = c.op != P_DENSE;
+    const int slots = grouped ? c.r.T * c.r.top_k : c.M;
+    if (tid == 0) {
+        for (int i = 0; i < kQgStageMax; ++i) {
+            mbar_init(smem_u32(&full[i]), 1 + 4);
+            mbar_init(smem_u32(&empty[i]), 1);
+        }
+        for (int i = 0; i < kQgRawMax; ++i) {
+            mbar_init(smem_u32(&r_full[i]), 1);
+            mbar_init(smem_u32(&r_empty[i]), 8);
+        }
+        for (int i = 0; i < 2; ++i) {
+            mbar_init(smem_u32(&acc_full[i]), 1);
+            mbar_init(smem_u32(&acc_empty[i]), 8);
+        }
+        flags[0] = 0;
+        fence_mbar_init();
+    }
+    if (warp == 1) {
+        asm volatile("tcgen05.alloc.cta_group::1.sync.aligned.shared::cta.b32 [%0], %1;" ::"r"(smem_u32(tslot)), "n"(kTcTmemCols)
+                     : "memory");
+        asm volatile("tcgen05.relinquish_alloc_permit.cta_group::1.sync.aligned;" ::: "memory");
+    }
+    grid_dep_launch();
+    if (grouped) grid_dep_wait();
+    if (warp == 0) {
+        if (grouped) {
+            const int per = (w.E + 31) / 32;
+            int mine = 0;
+            for (int i = 0; i < per; ++i) {
+                const int e = lane * per + i;
+                if (e < w.E) mine += (max(min(c.r.offsets[e + 1], slots) - max(c.r.offsets[e], 0), 0) + p.bx - 1) / p.bx;
+            }
+            int pre = mine;
+#pragma unroll
+            for (int o = 1; o < 32; o <<= 1) {
+                const int u = __shfl_up_sync(0xffffffffu, pre, o);
+                if (lane >= o) pre += u;
+            }
+            if (lane == 31) ts[w.E] = pre;
+            pre -= mine;
+            for (int i = 0; i < per; ++i) {
+                const int e = lane * per + i;
+                if (e >= w.E) break;
+                ts[e] = pre;
+                pre += (max(min(c.r.offsets[e + 1], slots) - max(c.r.offsets[e], 0), 0) + p.bx - 1) / p.bx;
+            }
+        } else if (lane == 0) {
+            ts[0] = 0;
+            ts[1] = p.mtiles;
+        }
+    }
+    tc_fence_before();
+    __syncthreads();
+    tc_fence_after();
+    const uint32_t tmem = *tslot;
+    const int units = ts[w.E] * p.ntiles;
+    auto place = [&](int u) {
+        QgUnit un;
+        const int st = u / p.ntiles;
+        un.nt = u - st * p.ntiles;
+        int lo = 0, hi = w.E;  // ts[lo] <= st < ts[hi]
+        while (hi - lo > 1) {
+            const int mid = (lo + hi) >> 1;
+            if (ts[mid] <= st) lo = mid;
+            else hi = mid;
+        }
+        un.e = lo;
+        const int first = grouped ? max(c.r.offsets[lo], 0) : 0;
+        const int end = grouped ? min(c.r.offsets[lo + 1], slots) : c.M;
+        un.p0 = first + (st - ts[lo]) * p.bx;
+        un.n = min(p.bx, end - un.p0);
+        return un;
+    };
+    if (!grouped && warp != 2) grid_dep_wait();  // weights are constant: their copies may start at once
+    const int piece = p.bx * 128;
+    auto stage = [&](int s) { return sm + s * NP * piece; };
+    const int seg_bytes = qg_seg_bytes(NG);
+    auto raw = [&](int s) { return sm + p.off_raw + s * 16 * seg_bytes; };
+
+    if (warp == 0) {
+        // ------------------------------ activations ------------------------------
+        long long g = 0;
+        bool ok = true;
+        for (int u = blockIdx.x; u < units && ok; u += gridDim.x) {
+            const QgUnit un = place(u);
+            const int ngather = (un.n + 3) / 4;
+            int row[2][4];  // this lane's gathered rows: copies lane and lane + 32
+            if (grouped) {
+#pragma unroll
+                for (int h = 0; h < 2; ++h)
+#pragma unroll
+                    for (int i = 0; i < 4; ++i) {
+                        const int col = min(4 * (lane + 32 * h) + i, un.n - 1);
+                        int slot = c.r.order[un.p0 + col];
+                        if (slot < 0 || slot >= slots) slot = 0;
+                        row[h][i] = c.op == P_GATE_UP ? slot / c.r.top_k : slot;
+                    }
+            }
+            const uint32_t bytes = (uint32_t)(NP * (grouped ? ngather * 512 : piece));
+            for (int j = 0; j < p.kt && ok; ++j, ++g) {
+                const int s = (int)(g % p.nstage);
+                if (g >= p.nstage) ok = mbar_wait(smem_u32(&empty[s]), (uint32_t)(((g / p.nstage) - 1) & 1), flags, p.err);
+                if (!ok) break;
+                const uint32_t bar = smem_u32(&full[s]);
+                if (lane == 0) mbar_arrive_tx(bar, bytes);
+                __syncwarp();
+                if (!grouped) {
+                    if (lane < NP) tma_2d(smem_u32(stage(s)) + lane * piece, &tx, j * 64, lane * p.xrows + un.p0, bar);
+                } else {
+#pragma unroll
+                    for (int h = 0; h < 2; ++h)
+                        if (lane + 32 * h < ngather)
+#pragma unroll
+                            for (int pc = 0; pc < NP; ++pc)
+                                tma_gather4(smem_u32(stage(s)) + pc * piece + (lane + 32 * h) * 512, &tx, j * 64,
+                                            row[h][0] + pc * p.xrows, row[h][1] + pc * p.xrows, row[h][2] + pc * p.xrows,
+                                            row[h][3] + pc * p.xrows, bar);
+                }
+                __syncwarp();
+            }
+        }
+        // let every copy land before the block can exit
+        if (lane == 0)
+            for (long long q = g > p.nstage ? g - p.nstage : 0; q < g; ++q)
+                mbar_drain(smem_u32(&full[q % p.nstage]), (uint32_t)((q / p.nstage) & 1), flags, p.err);
+    } else if (warp == 1) {
+        // ------------------------------ MMA issuer ------------------------------
+        if (lane == 0) {
+            const uint64_t d0 = tc_sdesc128(smem_u32(stage(0)));
+            const uint32_t lo0 = (uint32_t)d0, dhi = (uint32_t)(d0 >> 32);
+            long long g = 0;
+            int cc = 0;
+            bool ok = true;
+            uint32_t ready = 0;
+            for (int u = blockIdx.x; u < units && ok; u += gridDim.x) {
+                const QgUnit un = place(u);
+                const uint32_t idesc = tc_idesc((un.n + 15) / 16 * 16);
+                const int chunk = NP == 2 ? kQgChunk : p.kt;
+                for (int c0 = 0; c0 < p.kt && ok; c0 += chunk, ++cc) {
+                    const int ab = p.nacc == 2 ? (cc & 1) : 0, use = p.nacc == 2 ? (cc >> 1) : cc;
+                    if (use > 0) ok = mbar_wait(smem_u32(&acc_empty[ab]), (uint32_t)((use - 1) & 1), flags, p.err);
+                    if (!ok) break;
+                    tc_fence_after();
+                    const uint32_t dt = tmem + (uint32_t)(ab * 128);
+                    const int n = min(chunk, p.kt - c0);
+                    for (int i = 0; i < n; ++i, ++g) {
+                        const int s = (int)(g % p.nstage);
+                        const uint32_t nxt = mbar_test(smem_u32(&full[(g + 1) % p.nstage]), (uint32_t)(((g + 1) / p.nstage) & 1));
+                        if (!ready) ok = mbar_wait(smem_u32(&full[s]), (uint32_t)((g / p.nstage) & 1), flags, p.err);
+                        if (!ok) break;
+                        tc_fence_after();
+                        const uint32_t xhi = lo0 + (uint32_t)((s * NP * piece) >> 4), xlo = xhi + (uint32_t)(piece >> 4);
+                        const uint32_t whi = tmem + (uint32_t)(kQgWCol0 + 32 * NP * s), wlo = whi + 32;
+#pragma unroll
+                        for (int pass = 0; pass < 2 * NP - 1; ++pass) {
+                            const uint32_t wa = pass == 2 ? wlo : whi, xb = pass == 1 ? xlo : xhi;
+#pragma unroll
+                            for (int kk = 0; kk < 4; ++kk)
+                                tc_mma(dt, wa + 8 * kk, ((uint64_t)dhi << 32) | (xb + 2 * kk), idesc, (i | pass | kk) != 0 ? 1u : 0u);
+                        }
+                        tc_commit(smem_u32(&empty[s]));
+                        ready = nxt;
+                    }
+                    if (!ok) break;
+                    tc_commit(smem_u32(&acc_full[ab]));
+                }
+            }
+            // the last commits must land before tensor memory is released
+            if (g > 0) mbar_drain(smem_u32(&empty[(g - 1) % p.nstage]), (uint32_t)(((g - 1) / p.nstage) & 1), flags, p.err);
+        }
+    } else if (warp == 2) {
+        // ------------------------------ raw weights ------------------------------
+        long long r = 0;
+        bool ok = true;
+        const int nr = (w.KS + 1) / 2;
+        for (int u = blockIdx.x; u < units && ok; u += gridDim.x) {
+            const QgUnit un = place(u);
+            const int nrb = min(8, w.RB - 8 * un.nt);
+            const uint8_t* src = w.data + (long long)un.e * w.expert_stride + ((long long)(8 * un.nt + lane) * w.KS) * seg_bytes;
+            for (int j = 0; j < nr && ok; ++j, ++r) {
+                const int s = (int)(r % p.nraw);
+                if (r >= p.nraw) ok = mbar_wait(smem_u32(&r_empty[s]), (uint32_t)(((r / p.nraw) - 1) & 1), flags, p.err);
+                if (!ok) break;
+                const int nseg = min(2, w.KS - 2 * j);
+                const uint32_t bar = smem_u32(&r_full[s]);
+                if (lane == 0) mbar_arrive_tx(bar, (uint32_t)(nrb * nseg * seg_bytes));
+                __syncwarp();
+                if (lane < nrb) bulk_g2s(smem_u32(raw(s)) + lane * 2 * seg_bytes, src + (long long)(2 * j) * seg_bytes, (uint32_t)(nseg * seg_bytes), bar);
+                __syncwarp();
+            }
+        }
+        if (lane == 0)
+            for (long long q = r > p.nraw ? r - p.nraw : 0; q < r; ++q)
+                mbar_drain(smem_u32(&r_full[q % p.nraw]), (uint32_t)((q / p.nraw) & 1), flags, p.err);
+    } else if (warp < kQgConv0) {
+        // ------------------------------ epilogue ------------------------------
+        const int ew = warp - kQgEpi0, q = warp & 3, half = ew >> 2;
+        const uint32_t tq = (uint32_t)(32 * q) << 16;
+        int* my_slot = col_slot + ew * 128;
+        float* my_scale = col_scale + ew * 128;
+        int cc = 0;
+        bool ok = true;
+        const int chunk = NP == 2 ? kQgChunk : p.kt;
+        const int F = w.N / 2;
+        for (int u = blockIdx.x; u < units && ok; u += gridDim.x) {
+            const QgUnit un = place(u);
+            const int nch = (un.n + 15) / 16;
+            const int rb = 8 * un.nt + 2 * q + (lane >> 4);
+            const int n = rb < w.RB ? qg_row(w, rb, lane & 15) : -1;
+            const float wsn = rb < w.RB ? __ldg(p.wis + ((long long)un.e * w.RB + rb) * 16 + (lane & 15)) : 0.0f;
+            // this warp's columns: 16-column chunks half, half + 2, ...
+            __syncwarp();
+#pragma unroll
+            for (int k = 0; k < 4; ++k) {
+                const int j = 32 * k + lane, col = 16 * (half + 2 * (j >> 4)) + (j & 15);
+                int slot = -1;
+                float xsc = 0.0f;
+                if (col < un.n) {
+                    slot = un.p0 + col;
+                    if (grouped) {
+                        slot = c.r.order[slot];
+                        if (slot >= slots) slot = -1;
+                    }
+                    if (slot >= 0) xsc = p.xs ? __ldcg(p.xs + (c.op == P_GATE_UP ? slot / c.r.top_k : slot)) : 1.0f;
+                }
+                my_slot[j] = slot;
+                my_scale[j] = xsc;
+            }
+            __syncwarp();
+            auto put = [&](int k, const float v[16]) {  // the k-th of this warp's column chunks
+                if (c.op == P_GATE_UP) {
+                    // lanes r < 8 have gate rows, r + 8 their up rows; each finishes one of two columns
+                    const bool up = (lane & 8) != 0;
+                    const int f = rb * 8 + (lane & 7);
+#pragma unroll
+                    for (int i = 0; i < 16; i += 2) {
+                        const float give = up ? v[i] : v[i + 1];
+                        const float got = __shfl_xor_sync(0xffffffffu, give, 8);
+                        const float other = __shfl_xor_sync(0xffffffffu, wsn, 8);
+                        const int col = 16 * k + i + (up ? 1 : 0);
+                        const int slot = my_slot[col];
+                        const float xsc = my_scale[col];
+                        const float mine = (up ? v[i + 1] : v[i]) * wsn * xsc, theirs = got * other * xsc;
+                        if (slot >= 0 && rb < w.RB && f < F)
+                            x_store(c.y, c.xt, (long long)slot * F + f, up ? swiglu(theirs, mine) : swiglu(mine, theirs));
+                    }
+                } else if (n >= 0) {
+#pragma unroll
+                    for (int i = 0; i < 16; ++i) {
+                        const int slot = my_slot[16 * k + i];
+                        if (slot < 0) continue;
+                        const float r = v[i] * wsn * my_scale[16 * k + i];
+                        if (c.op == P_DOWN) p.part[(long long)slot * w.N + n] = r;
+                        else x_store(c.y, c.xt, (long long)slot * w.N + n, r);
+                    }
+                }
+            };
+            float sum[NP == 2 ? 4 : 1][16];
+            for (int c0 = 0; c0 < p.kt; c0 += chunk, ++cc) {
+                const int ab = p.nacc == 2 ? (cc & 1) : 0, use = p.nacc == 2 ? (cc >> 1) : cc;
+                if (!(ok = mbar_wait(smem_u32(&acc_full[ab]), (uint32_t)(use & 1), flags, p.err))) break;
+                tc_fence_after();
+                __syncwarp();
+                const uint32_t acol = tmem + tq + (uint32_t)(ab * 128);
+                if (NP == 2) {
+#pragma unroll
+                    for (int k = 0; k < 4; ++k) {
+                        uint32_t r[16];
+                        if (half + 2 * k < nch) {
+                            tc_ld16(acol + 16 * (half + 2 * k), r);
+                            tc_wait_ld();
+#pragma unroll
+                            for (int i = 0; i < 16; ++i) sum[NP == 2 ? k : 0][i] = c0 == 0 ? __uint_as_float(r[i]) : sum[NP == 2 ? k : 0][i] + __uint_as_float(r[i]);
+                        }
+                    }
+                } else {
+                    uint32_t r[16];
+                    if (half < nch) tc_ld16(acol + 16 * half, r);
+                    for (int ch = half, k = 0; ch < nch; ch += 2, ++k) {
+                        tc_wait_ld();
+                        float v[16];
+#pragma unroll
+                        for (int i = 0; i < 16; ++i) v[i] = __uint_as_float(r[i]);
+                        if (ch + 2 < nch) tc_ld16(acol + 16 * (ch + 2), r);
+                        put(k, v);
+                    }
+                }
+                __syncwarp();
+                tc_fence_before();
+                __syncwarp();
+                if (lane == 0) mbar_arrive(smem_u32(&acc_empty[ab]));
+            }
+            if (!ok) break;
+            if (NP == 2) {
+#pragma unroll
+                for (int k = 0; k < 4; ++k)
+                    if (half + 2 * k < nch) put(k, sum[NP == 2 ? k : 0]);
+            }
+        }
+    } else {
+        // ------------------------------ conversion ------------------------------
+        const int cw = warp - kQgConv0, q = warp & 3, grp = cw >> 2;
+        long long g = 0, r = 0;
+        bool ok = true;
+        for (int u = blockIdx.x; u < units && ok; u += gridDim.x) {
+            const QgUnit un = place(u);
+            float m[2][2];  // 2^a of rows g, g + 8 of this warp's two row blocks
+#pragma unroll
+            for (int hh = 0; hh < 2; ++hh) {
+                const int rb = min(8 * un.nt + 2 * q + hh, w.RB - 1);
+                const float* is = p.wis + ((long long)un.e * w.RB + rb) * 16 + (lane >> 2);
+                m[hh][0] = __frcp_rn(__ldg(is));
+                m[hh][1] = __frcp_rn(__ldg(is + 8));
+            }
+            for (int j = 0; j < p.kt && ok; j += 4, ++r) {
+                const int rs = (int)(r % p.nraw);
+                ok = mbar_wait(smem_u32(&r_full[rs]), (uint32_t)((r / p.nraw) & 1), flags, p.err);
+                if (!ok) break;
+                const int n = min(4, p.kt - j);
+                for (int i = 0; i < n; ++i, ++g) {
+                    if ((int)(g & 1) != grp) continue;
+                    const int s = (int)(g % p.nstage);
+                    uint32_t hi[16], lo[16];
+                    const uint8_t* seg = raw(rs) + 2 * q * 2 * seg_bytes + (i >> 1) * seg_bytes;
+                    qg_convert<NP, NG>(seg, i & 1, lane, m[0][0], m[0][1], hi, lo);
+                    if (g >= p.nstage) ok = mbar_wait(smem_u32(&empty[s]), (uint32_t)(((g / p.nstage) - 1) & 1), flags, p.err);
+                    if (!ok) break;
+                    tc_fence_after();
+                    __syncwarp();
+                    const uint32_t col = tmem + ((uint32_t)(32 * q) << 16) + (uint32_t)(kQgWCol0 + 32 * NP * s);
+                    tc_st_frag(col, hi);
+                    if (NP == 2) tc_st_frag(col + 32, lo);
+                    qg_convert<NP, NG>(seg + 2 * seg_bytes, i & 1, lane, m[1][0], m[1][1], hi, lo);
+                    tc_st_frag(col + (16u << 16), hi);
+                    if (NP == 2) tc_st_frag(col + (16u << 16) + 32, lo);
+                    asm volatile("tcgen05.wait::st.sync.aligned;" ::: "memory");
+                    tc_fence_before();
+                    __syncwarp();
+                    if (lane == 0) mbar_arrive(smem_u32(&full[s]));
+                }
+                __syncwarp();
+                if (lane == 0) mbar_arrive(smem_u32(&r_empty[rs]));
+            }
+        }
+    }
+    tc_fence_before();
+    __syncthreads();
+    if (warp == 1) {
+        tc_fence_after();
+        asm volatile("tcgen05.dealloc.cta_group::1.sync.aligned.b32 %0, %1;" ::"r"(tmem), "n"(kTcTmemCols) : "memory");
+    }
+}
+
+}  // namespace qmm

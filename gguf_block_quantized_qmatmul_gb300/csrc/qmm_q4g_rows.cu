@@ -1,0 +1,112 @@
+// qmm_q4g_rows.cu -- host side of the row kernel (its plan), and the kernel
+// that adds the experts' partial rows of a token.
+#include "qmm_q4g_rows.cuh"
+
+namespace qmm {
+
+cudaError_t launch_q4g_rows_1(const QgRowsPlan& pl, const QgRowsParams& p, int smem_max, cudaStream_t s);
+cudaError_t launch_q4g_rows_2(const QgRowsPlan& pl, const QgRowsParams& p, int smem_max, cudaStream_t s);
+cudaError_t launch_q4g_rows_4(const QgRowsPlan& pl, const QgRowsParams& p, int smem_max, cudaStream_t s);
+
+namespace {
+
+__global__ void __launch_bounds__(256) q4g_combine_kernel(const float* __restrict__ part, QgRoute r, int E, int N, void* y, int xt) {
+    grid_dep_launch();
+    grid_dep_wait();
+    const int t = blockIdx.x;
+    const int n = blockIdx.y * 256 + threadIdx.x;
+    if (n >= N) return;
+    float v = 0.0f;
+    for (int j = 0; j < r.top_k; ++j) {
+        const long long slot = (long long)t * r.top_k + j;
+        const int e = __ldg(r.ids + slot);
+        if (e >= 0 && e < E) v = fmaf(__ldg(r.weights + slot), __ldcg(part + slot * N + n), v);
+    }
+    x_store(y, xt, (long long)t * N + n, v);
+}
+
+}  // namespace
+
+cudaError_t launch_q4g_combine(const float* part, const QgRoute& r, int E, int N, void* y, int xt, cudaStream_t s) {
+    return launch_pdl_2d(q4g_combine_kernel, (unsigned)r.T, (unsigned)((N + 255) / 256), 256, 0, s, part, r, E, N, y, xt);
+}
+
+QgRowsPlan plan_q4g_rows(const QgCall& c, int sms, int smem_max) {
+    QgRowsPlan pl;
+    pl.np = c.xt == X_F32 ? 3 : 1;
+    const long long row_bytes = (long long)pl.np * c.w.KS * kQgSegK * 2;  // staged bytes of one activation row
+    const int max_cols = 32 / pl.np;
+    const long long slots = c.M;
+    long long items = 1;
+    if (c.op == P_DENSE) {
+        pl.cols = c.M < max_cols ? c.M : max_cols;
+    } else {
+        // one slot (one token) a block while few slots share an expert: no plan to search, and no
+        // partial sums; by expert, a block serves up to `cols` of its slots with one weight stream
+        pl.by_slot = c.r.T <= 4 && c.r.top_k <= kQgMaxK && (c.op == P_GATE_UP || row_bytes * c.r.top_k <= 96 * 1024);
+        const long long avg = (slots + c.w.E - 1) / c.w.E;
+        pl.cols = pl.by_slot ? 1 : avg * pl.np <= 4 ? (8 / pl.np) : avg * pl.np <= 8 ? 16 / pl.np : max_cols;
+    }
+    auto red = [&](int nb, int warps) { return 2ll * warps * nb * 128 * 4; };
+    auto nb_of = [&](int cols) { const int b = (cols * pl.np + 7) / 8; return b <= 1 ? 1 : b <= 2 ? 2 : 4; };
+    const long long rows_mul = c.op == P_DOWN && pl.by_slot ? c.r.top_k : 1;
+    // as many columns as shared memory holds
+    while (pl.cols > 1 && pl.cols * row_bytes + red(nb_of(pl.cols), 16) > smem_max - 2048) --pl.cols;
+    if (pl.cols * row_bytes * rows_mul + red(nb_of(pl.cols), 16) > smem_max - 2048) return pl;
+    if (c.op == P_DENSE) {
+        items = (c.M + pl.cols - 1) / pl.cols;
+        pl.cols = (int)((c.M + items - 1) / items);
+        pl.gy = (int)items;
+    } else if (pl.by_slot) {
+        pl.gy = c.op == P_GATE_UP ? (int)slots : c.r.T;
+        items = pl.gy;
+    } else {
+        // an expert's last item may be partial: at most E + slots / cols items
+        const long long most = c.w.E + slots / pl.cols;
+        pl.gy = (int)(most < slots ? most : slots);
+        items = slots < c.w.E ? slots : c.w.E;
+    }
+    if (pl.gy > 65535) return pl;
+    pl.nb = nb_of(pl.cols);
+    const long long xb = pl.cols * row_bytes * rows_mul;
+    // two blocks of 8 warps an SM, or one of 16 where the activations take more than half its shared memory
+    pl.warps = xb + red(pl.nb, 8) <= (smem_max - 4096) / 2 ? 8 : 16;
+    const int resident = pl.warps == 8 ? 2 : 1;
+    const int VS = (int)(c.w.KS * rows_mul);
+    double best = 0;
+    for (int wk = 1; wk <= pl.warps; wk *= 2) {
+        const int wr = pl.warps / wk, groups = (c.w.RB + wr - 1) / wr, nit = (VS + wk - 1) / wk;
+        long long most = (long long)resident * sms / items;
+        if (most < 1) most = 1;
+        const int gx = groups < most ? groups : (int)most;
+        // segments a warp takes in turn, and per row block a barrier that costs about one more
+        const double cost = (double)((groups + gx - 1) / gx) * (nit + 1.0);
+        if (wk == 1 || cost <= best) {
+            best = cost;
+            pl.wk = wk;
+            pl.gx = gx;
+        }
+    }
+    pl.smem = (size_t)xb + (size_t)red(pl.nb, pl.warps);
+    if (c.op == P_DOWN && !pl.by_slot) pl.workspace = (size_t)slots * c.w.N * 4;
+    pl.ok = true;
+    return pl;
+}
+
+cudaError_t launch_q4g_rows(const QgRowsPlan& pl, const QgCall& c, void* ws, int smem_max, cudaStream_t s) {
+    QgRowsParams p;
+    p.c = c;
+    p.part = static_cast<float*>(ws);
+    p.by_slot = pl.by_slot;
+    p.cols = pl.cols;
+    p.np = pl.np;
+    p.wk = pl.wk;
+    p.off_red = (int)(pl.smem - 2ull * pl.warps * pl.nb * 128 * 4);
+    cudaError_t e = pl.nb == 1   ? launch_q4g_rows_1(pl, p, smem_max, s)
+                    : pl.nb == 2 ? launch_q4g_rows_2(pl, p, smem_max, s)
+                                 : launch_q4g_rows_4(pl, p, smem_max, s);
+    if (e != cudaSuccess || c.op != P_DOWN || pl.by_slot) return e;
+    return launch_q4g_combine(p.part, c.r, c.w.E, c.w.N, c.y, c.xt, s);
+}
+
+}  // namespace qmm

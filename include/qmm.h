@@ -259,6 +259,120 @@ qmm_status qmm_matmul_batch_typed(qmm_act_mode mode, const qmm_matmul_typed_desc
 qmm_status qmm_matmul_static_workspace(qmm_type wtype, qmm_act_mode mode, const void* wq, const float* x, float* y,
                                        int64_t M, int64_t N, int64_t K, qmm_stream_t stream);
 
+/* ---------------------------------------------------------------------------
+   4-bit weights with group scales, and mixture-of-experts layers.
+   (The pages stop at GGUF blocks and dense models: these are additions of this
+   library, for checkpoints that keep 4-bit codes and scales apart and for
+   models whose MLP is a set of experts.)
+
+   A weight is w[n][k] = s[n][k / group] (q[n][k] - z[n][k / group]) with codes
+   and zero points in 0..15 (z = 8 where there are none).  A program lays its
+   weights out once (qmm_q4g_pack) and keeps the laid-out form; every product
+   reads that.  Activations and outputs are f32, f16 or bf16, one type per
+   call; sums are f32 and are rounded once, at the end.
+
+   Accuracy: up to 32 activation rows (f32: 10) per weight matrix no weight is
+   rounded; beyond, f16 and bf16 calls round each weight s (q - z) to f16's 11
+   bits, which is below the rounding of the output, and f32 calls keep 22 bits
+   of the activations and all of the weights.  A row of x with an infinity or
+   a NaN gives a row of outputs that are not finite; no other row is touched.
+   Results do not depend on the run: no sum's order varies. */
+
+typedef enum { QMM_FLOAT_F32 = 0, QMM_FLOAT_F16 = 1, QMM_FLOAT_BF16 = 2 } qmm_float;
+
+/* Laid-out weights of `experts` matrices [N, K] (1: a dense linear). */
+typedef struct {
+    const void* data;   /* device memory, qmm_q4g_bytes(...) bytes, 16-byte aligned */
+    int64_t experts, N, K;
+    int32_t group;      /* inputs per scale: a multiple of 32 that divides K */
+    int32_t paired;     /* 1: N = 2 F, rows 0..F-1 are gate rows, F..2F-1 up rows (qmm_moe_gate_up) */
+} qmm_q4g;
+
+/* Bytes of the laid-out form; 0 for an invalid shape (group not a multiple of
+   32, K not a multiple of group, an odd N that is paired, sizes out of range:
+   experts <= 65535, N <= 2^23, K <= 2^20). */
+size_t qmm_q4g_bytes(int64_t experts, int64_t N, int64_t K, int group, int paired);
+
+/* Lays weights out.  codes: uint8 [experts][N][K / 2], even k in the low
+   nibble; scales: f16 or bf16 [experts][N][K / group]; zeros: uint8 of the same
+   shape (their low 4 bits count), or NULL.  Exact: no scale or code changes.
+   Errors: TYPE (scale type), SHAPE, NULL, ALIGN (out 16, scales 2), CUDA. */
+qmm_status qmm_q4g_pack(const uint8_t* codes, const void* scales, qmm_float scale_type, const uint8_t* zeros, int64_t experts, int64_t N,
+                        int64_t K, int group, int paired, void* out, qmm_stream_t stream);
+
+/* The same from GGUF Q4_0 blocks (experts x N rows of qmm_row_bytes(QMM_Q4_0, K)
+   bytes): group 32, zero point 8, exact. */
+qmm_status qmm_q4g_pack_q4_0(const void* wq, int64_t experts, int64_t N, int64_t K, int paired, void* out, qmm_stream_t stream);
+
+/* Laid-out weights -> out [experts][N][K] f32, exact (rows in their own order). */
+qmm_status qmm_q4g_dequantize(const qmm_q4g* w, float* out, qmm_stream_t stream);
+
+/* y [M, N] = x [M, K] . W^T for one weight matrix (experts = 1, not paired).
+   Rows of x are ldx elements apart (ldx >= K, a multiple of 16 bytes); y is
+   contiguous.  workspace: qmm_q4g_matmul_workspace(...) bytes (0 up to 32 rows,
+   f32: 10), uninitialised; calls that may overlap need one each.
+   Errors: TYPE, NULL, SHAPE, ALIGN, WORKSPACE, CUDA. */
+size_t qmm_q4g_matmul_workspace(const qmm_q4g* w, qmm_float xtype, int64_t M);
+qmm_status qmm_q4g_matmul(const qmm_q4g* w, qmm_float xtype, const void* x, int64_t ldx, int64_t M, void* y, void* workspace,
+                          size_t workspace_bytes, qmm_stream_t stream);
+
+#define QMM_MOE_MAX_EXPERTS 512
+#define QMM_MOE_MAX_TOP_K 32
+
+typedef enum { QMM_SCORE_SOFTMAX = 0, QMM_SCORE_SIGMOID = 1 } qmm_score;
+typedef enum { QMM_GROUP_MAX = 0, QMM_GROUP_TOP2 = 1 } qmm_group_score;
+typedef struct {
+    int32_t score;       /* qmm_score */
+    int32_t top_k;       /* experts per token */
+    int32_t groups;      /* groups of consecutive experts (1: none); divides E, at most 32 */
+    int32_t top_groups;  /* groups a token's experts may come from; top_k <= top_groups E / groups */
+    int32_t group_score; /* qmm_group_score: a group's value is its largest pick, or the sum of its two largest */
+    int32_t renorm;      /* 1: weights are divided by their sum */
+    float scale;         /* factor of every weight */
+} qmm_route_config;
+
+/* Routes T tokens to top_k of E experts each.  logits [T][E], rows ldl elements
+   apart.  In f32: score = softmax(l) or 1 / (1 + exp(-l)); what is compared is
+   the logit (softmax without bias), the score (sigmoid without bias) or
+   score + bias[e]; ties go to the lowest index; a NaN logit counts as -inf.
+   ids [T][top_k], best first; weights [T][top_k] = scale * score (not biased),
+   divided by the sum of the token's chosen scores with renorm (weights 0 where
+   that sum is 0: a row of -inf has softmax scores 0).
+   offsets [E + 1] and order [T top_k] (both or neither): the slots t top_k + j
+   sorted by expert, in slot order within one; expert e's are
+   order[offsets[e] .. offsets[e + 1]).  workspace: only with them,
+   qmm_moe_route_workspace(...) bytes.  T = 0 writes zero offsets.
+   Errors: TYPE, SHAPE, NULL, ALIGN, WORKSPACE, CUDA. */
+size_t qmm_moe_route_workspace(int64_t T, int64_t E, int64_t top_k);
+qmm_status qmm_moe_route(const qmm_route_config* cfg, qmm_float type, const void* logits, int64_t ldl, int64_t T, int64_t E,
+                         const float* bias, int32_t* ids, float* weights, int32_t* offsets, int32_t* order, void* workspace,
+                         size_t workspace_bytes, qmm_stream_t stream);
+
+/* A routing, all device memory, as qmm_moe_route writes it.  A program may
+   make its own: a slot whose id is outside [0, experts) is skipped and must
+   not be in `order` (offsets[experts] is then less than T top_k). */
+typedef struct {
+    const int32_t* ids;      /* [T][top_k] */
+    const float* weights;    /* [T][top_k]; qmm_moe_down */
+    const int32_t* offsets;  /* [experts + 1] */
+    const int32_t* order;    /* [T top_k] */
+    int64_t T, top_k;
+} qmm_routing;
+
+/* h [T][top_k][F] = silu(x_t . Wg_e^T) * (x_t . Wu_e^T) for the experts e of
+   each token; w paired, N = 2 F.  A skipped slot's row of h is not written.
+   Errors as qmm_q4g_matmul. */
+size_t qmm_moe_gate_up_workspace(const qmm_q4g* w, qmm_float xtype, int64_t T, int64_t top_k);
+qmm_status qmm_moe_gate_up(const qmm_q4g* w, qmm_float xtype, const void* x, int64_t ldx, const qmm_routing* r, void* h, void* workspace,
+                           size_t workspace_bytes, qmm_stream_t stream);
+
+/* y [T][N] = sum over j of weights[t][j] (h[t][j] . W_e^T), in the order of j;
+   rows (slots) of h are ldh elements apart.  A skipped slot adds nothing.
+   Errors as qmm_q4g_matmul. */
+size_t qmm_moe_down_workspace(const qmm_q4g* w, qmm_float xtype, int64_t T, int64_t top_k);
+qmm_status qmm_moe_down(const qmm_q4g* w, qmm_float xtype, const void* h, int64_t ldh, const qmm_routing* r, void* y, void* workspace,
+                        size_t workspace_bytes, qmm_stream_t stream);
+
 /* Failure-test hooks.  (The pages have no counterpart: these exist so that
    the library's failure paths can be exercised without faulting a GPU.)
    qmm_test_inject arms an injected failure, consumed by the next `count`
