@@ -7,14 +7,28 @@ namespace {
 
 // One row per block: f16 values (pieces) scaled by 2^b, and 2^-b.  The scale
 // comes from the row's largest finite magnitude; infinities and NaN stay what
-// they are (their rests are 0).
+// they are (their rests are 0).  For experts row p is the activations of slot
+// order[p].
 template <int NP>
-__global__ void __launch_bounds__(256) q4g_prep_kernel(const void* x, int xt, long long ldx, int rows, int K, __half* out, float* xs) {
+__global__ void __launch_bounds__(256) q4g_prep_kernel(const QgCall c, int rows, __half* out, float* xs) {
     __shared__ float red[8];
     grid_dep_launch();
     grid_dep_wait();
-    const int row = blockIdx.x, tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
-    const long long at = (long long)row * ldx;
+    const int row = blockIdx.x, tid = threadIdx.x, lane = tid & 31, warp = tid >> 5, K = c.w.K, xt = c.xt;
+    const void* x = c.x;
+    int from = row;
+    if (c.op != P_DENSE) {
+        if (row >= c.r.offsets[c.w.E]) return;
+        from = c.r.order[row];
+        if (from < 0 || from >= rows) return;
+        if (c.op == P_GATE_UP) from /= c.r.top_k;
+    }
+    const long long at = (long long)from * c.ldx;
+    if (xt == X_F16) {
+        for (int k = 8 * tid; k < K; k += 8 * 256)
+            *reinterpret_cast<uint4*>(out + (long long)row * K + k) = *reinterpret_cast<const uint4*>(static_cast<const uint16_t*>(x) + at + k);
+        return;
+    }
     auto load8 = [&](int k, float f[8]) {
         if (xt == X_F32) {
             const float4 a = *reinterpret_cast<const float4*>(static_cast<const float*>(x) + at + k);
@@ -75,18 +89,15 @@ cudaError_t gemm_one(const QgGemmPlan& pl, const CUtensorMap& tx, const QgGemmPa
     return launch_pdl(k, (unsigned)pl.grid, kQgThreads, pl.smem, s, tx, p);
 }
 
-int source_rows(const QgCall& c) { return c.op == P_GATE_UP ? c.r.T : c.M; }
-
 }  // namespace
 
 QgGemmPlan plan_q4g_gemm(const QgCall& c, int sms, int smem_max) {
     QgGemmPlan pl;
     const bool grouped = c.op != P_DENSE;
     if (grouped && c.w.E > kQgMaxE) return pl;
-    const long long rows = source_rows(c);
-    if (rows > (1 << 28)) return pl;
+    const long long rows = c.M;
     pl.np = c.xt == X_F32 ? 2 : 1;
-    pl.prep = c.xt != X_F16;
+    pl.prep = grouped || c.xt != X_F16;
     const long long per = grouped ? (c.M + c.w.E - 1) / c.w.E : c.M;  // activation rows per weight matrix
     pl.ntiles = (c.w.RB + 7) / 8;
     // tiles of 256 rows amortise the weights' conversion best; two accumulators of 128 columns
@@ -98,6 +109,7 @@ QgGemmPlan plan_q4g_gemm(const QgCall& c, int sms, int smem_max) {
         const int tiles = (int)((per + most - 1) / most);
         pl.bx = (int)((per + tiles - 1) / tiles + 15) / 16 * 16;
     }
+    pl.box = grouped && pl.bx > 64 ? 64 : pl.bx;  // an expert's tile is any size: no more copied than 63 rows too many
     pl.nacc = pl.bx <= 128 ? 2 : 1;
     pl.mtiles = grouped ? 0 : (int)((per + pl.bx - 1) / pl.bx);
     pl.nraw = 3;
@@ -122,22 +134,22 @@ QgGemmPlan plan_q4g_gemm(const QgCall& c, int sms, int smem_max) {
 
 cudaError_t launch_q4g_gemm(const QgGemmPlan& pl, const QgCall& c, void* ws, unsigned* err, int smem_max, cudaStream_t s) {
     uint8_t* wsb = static_cast<uint8_t*>(ws);
-    const int rows = source_rows(c), K = c.w.K;
+    const int rows = c.M, K = c.w.K;
     const void* xsrc = c.x;
     long long pitch = c.ldx * 2;
     float* xs = nullptr;
     if (pl.prep) {
         __half* xh = reinterpret_cast<__half*>(wsb + pl.ws_x);
-        xs = reinterpret_cast<float*>(wsb + pl.ws_xs);
-        const cudaError_t e = pl.np == 2 ? launch_pdl(q4g_prep_kernel<2>, (unsigned)rows, 256, 0, s, c.x, c.xt, c.ldx, rows, K, xh, xs)
-                                         : launch_pdl(q4g_prep_kernel<1>, (unsigned)rows, 256, 0, s, c.x, c.xt, c.ldx, rows, K, xh, xs);
+        if (c.xt != X_F16) xs = reinterpret_cast<float*>(wsb + pl.ws_xs);
+        const cudaError_t e = pl.np == 2 ? launch_pdl(q4g_prep_kernel<2>, (unsigned)rows, 256, 0, s, c, rows, xh, xs)
+                                         : launch_pdl(q4g_prep_kernel<1>, (unsigned)rows, 256, 0, s, c, rows, xh, xs);
         if (e != cudaSuccess) return e;
         xsrc = xh;
         pitch = (long long)K * 2;
     }
     CUtensorMap tx;
     if (!make_map(&tx, CU_TENSOR_MAP_DATA_TYPE_FLOAT16, xsrc, (unsigned long long)K, (unsigned long long)rows * pl.np, (unsigned long long)pitch,
-                  64, c.op == P_DENSE ? (unsigned)pl.bx : 1u, CU_TENSOR_MAP_SWIZZLE_128B))
+                  64, (unsigned)pl.box, CU_TENSOR_MAP_SWIZZLE_128B))
         return cudaErrorInvalidValue;
     QgGemmParams p;
     p.c = c;
@@ -147,6 +159,7 @@ cudaError_t launch_q4g_gemm(const QgGemmPlan& pl, const QgCall& c, void* ws, uns
     p.err = err;
     p.xrows = rows;
     p.bx = pl.bx;
+    p.box = pl.box;
     p.nacc = pl.nacc;
     p.mtiles = pl.mtiles;
     p.ntiles = pl.ntiles;

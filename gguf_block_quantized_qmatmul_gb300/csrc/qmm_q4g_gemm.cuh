@@ -4,7 +4,7 @@
 //
 // Mathematics.  Weight rows and activation rows are brought into f16's range
 // by a power of two each (the weights' at layout time, the activations' by the
-// preparation launch; f16 activations are taken as they are), and
+// preparation launch; f16 activations keep theirs), and
 //   y = 2^-(a + b) sum_k f16(s 2^a (q - z)) (x 2^b).
 // s 2^a and q - z are exact in f16, their product is rounded to 11 bits: half
 // of the products (codes 0, +-1, 2, 4, 8 off the zero point) are exact, so the
@@ -17,8 +17,10 @@
 //
 // One persistent block per SM over units: 128 weight rows (8 row blocks, the
 // MMA's M) x up to bx activation rows of one expert (its N, rounded up to 16).
-//   warp 0      activation tiles (64 K, 128-byte swizzle): for a dense call one
-//               2-D box, for experts gathered rows, four to a copy
+//   warp 0      one thread: activation tiles (64 K, 128-byte swizzle), 2-D boxes; the
+//               experts' rows were put in sorted order by the preparation launch
+//               (gathering four rows a copy here measured 90 cycles a copy: 643 us
+//               against the whole of 2048 tokens x 8 of 64 experts, 2048 -> 2 x 1024)
 //   warp 1      one thread: four MMAs (twelve with two pieces) per 64 K, A in
 //               tensor memory, B in shared memory
 //   warp 2      raw weights: eight 1-D copies (a row block's two segments each)
@@ -49,22 +51,14 @@ constexpr int kQgWCol0 = 256;    // weight pieces in tensor memory from this col
 struct QgGemmParams {
     QgCall c;
     float* part;          // P_DOWN: [T top_k][N]
-    const float* xs;      // 2^-b per activation row; NULL: 1
+    const float* xs;      // 2^-b per activation row (experts: per sorted position); NULL: 1
     const float* wis;     // 2^-a per weight row, layout order
     unsigned* err;
     int xrows;            // rows of an activation plane (the lo plane follows)
-    int bx, nacc, mtiles, ntiles, kt, nraw, nstage, grid;
+    int bx, box, nacc, mtiles, ntiles, kt, nraw, nstage, grid;
     int off_raw, off_bar;
 };
 
-// four gathered rows of a 2-D tensor map (box: one row), completing on an mbarrier
-__device__ __forceinline__ void tma_gather4(uint32_t dst, const CUtensorMap* map, int x, int y0, int y1, int y2, int y3, uint32_t bar) {
-    asm volatile(
-        "cp.async.bulk.tensor.2d.shared::cluster.global.tile::gather4.mbarrier::complete_tx::bytes [%0], [%1, {%2, %3, %4, %5, %6}], [%7];" ::"r"(
-            dst),
-        "l"(map), "r"(x), "r"(y0), "r"(y1), "r"(y2), "r"(y3), "r"(bar)
-        : "memory");
-}
 // 32 columns of 16 lanes from fragment registers: lane 4 g + t's registers 2 j, 2 j + 1 are column 4 j + t of lanes g, g + 8
 __device__ __forceinline__ void tc_st_frag(uint32_t taddr, const uint32_t v[16]) {
     asm volatile(
@@ -106,6 +100,26 @@ __device__ __forceinline__ void qg_convert(const uint8_t* seg, int h, int lane, 
             }
         }
     }
+}
+
+// A place in a ring of n stages: its index and the parity of its current use.
+// A producer waits for a stage's release with ph ^ 1, which a fresh barrier
+// passes.  (Counting uses and dividing by a run-time n costs the MMA thread
+// more than its four MMAs.)
+struct QgRing {
+    int s = 0;
+    uint32_t ph = 0;
+    __device__ __forceinline__ void next(int n) {
+        if (++s == n) {
+            s = 0;
+            ph ^= 1u;
+        }
+    }
+};
+// After the last use: waits for the copies of every stage still in flight.
+__device__ __forceinline__ void qg_drain(const QgRing& r, bool wrapped, int n, uint64_t* bars, volatile int* flags, unsigned* err) {
+    for (int q = 0; q < n; ++q)
+        if (q < r.s || wrapped) mbar_drain(smem_u32(&bars[q]), q < r.s ? r.ph : r.ph ^ 1u, flags, err);
 }
 
 // a unit's place
@@ -203,8 +217,11 @@ __global__ void __launch_bounds__(kQgThreads, 1) q4g_gemm_kernel(const __grid_co
         un.e = lo;
         const int first = grouped ? max(c.r.offsets[lo], 0) : 0;
         const int end = grouped ? min(c.r.offsets[lo + 1], slots) : c.M;
-        un.p0 = first + (st - ts[lo]) * p.bx;
-        un.n = min(p.bx, end - un.p0);
+        // an expert's rows in tiles of one size (a multiple of 16), not full ones and a rest
+        const int tiles = ts[lo + 1] - ts[lo];
+        const int size = ((end - first + tiles - 1) / tiles + 15) & ~15;
+        un.p0 = first + (st - ts[lo]) * size;
+        un.n = min(size, end - un.p0);
         return un;
     };
     if (!grouped && warp != 2) grid_dep_wait();  // weights are constant: their copies may start at once
@@ -215,57 +232,35 @@ __global__ void __launch_bounds__(kQgThreads, 1) q4g_gemm_kernel(const __grid_co
 
     if (warp == 0) {
         // ------------------------------ activations ------------------------------
-        long long g = 0;
-        bool ok = true;
-        for (int u = blockIdx.x; u < units && ok; u += gridDim.x) {
-            const QgUnit un = place(u);
-            const int ngather = (un.n + 3) / 4;
-            int row[2][4];  // this lane's gathered rows: copies lane and lane + 32
-            if (grouped) {
-#pragma unroll
-                for (int h = 0; h < 2; ++h)
-#pragma unroll
-                    for (int i = 0; i < 4; ++i) {
-                        const int col = min(4 * (lane + 32 * h) + i, un.n - 1);
-                        int slot = c.r.order[un.p0 + col];
-                        if (slot < 0 || slot >= slots) slot = 0;
-                        row[h][i] = c.op == P_GATE_UP ? slot / c.r.top_k : slot;
+        if (lane == 0) {
+            QgRing g;
+            bool ok = true, wrapped = false;
+            for (int u = blockIdx.x; u < units && ok; u += gridDim.x) {
+                const QgUnit un = place(u);
+                const int boxes = (un.n + p.box - 1) / p.box;
+                for (int j = 0; j < p.kt; ++j) {
+                    if (!(ok = mbar_wait(smem_u32(&empty[g.s]), g.ph ^ 1u, flags, p.err))) break;
+                    const uint32_t bar = smem_u32(&full[g.s]), to = smem_u32(stage(g.s));
+                    mbar_arrive_tx(bar, (uint32_t)(NP * boxes * p.box * 128));
+                    for (int i = 0; i < boxes; ++i) {
+                        tma_2d(to + i * p.box * 128, &tx, j * 64, un.p0 + i * p.box, bar);
+                        if (NP == 2) tma_2d(to + piece + i * p.box * 128, &tx, j * 64, p.xrows + un.p0 + i * p.box, bar);
                     }
-            }
-            const uint32_t bytes = (uint32_t)(NP * (grouped ? ngather * 512 : piece));
-            for (int j = 0; j < p.kt && ok; ++j, ++g) {
-                const int s = (int)(g % p.nstage);
-                if (g >= p.nstage) ok = mbar_wait(smem_u32(&empty[s]), (uint32_t)(((g / p.nstage) - 1) & 1), flags, p.err);
-                if (!ok) break;
-                const uint32_t bar = smem_u32(&full[s]);
-                if (lane == 0) mbar_arrive_tx(bar, bytes);
-                __syncwarp();
-                if (!grouped) {
-                    if (lane < NP) tma_2d(smem_u32(stage(s)) + lane * piece, &tx, j * 64, lane * p.xrows + un.p0, bar);
-                } else {
-#pragma unroll
-                    for (int h = 0; h < 2; ++h)
-                        if (lane + 32 * h < ngather)
-#pragma unroll
-                            for (int pc = 0; pc < NP; ++pc)
-                                tma_gather4(smem_u32(stage(s)) + pc * piece + (lane + 32 * h) * 512, &tx, j * 64,
-                                            row[h][0] + pc * p.xrows, row[h][1] + pc * p.xrows, row[h][2] + pc * p.xrows,
-                                            row[h][3] + pc * p.xrows, bar);
+                    g.next(p.nstage);
+                    wrapped |= g.s == 0;
                 }
-                __syncwarp();
             }
+            // let every copy land before the block can exit
+            qg_drain(g, wrapped, p.nstage, full, flags, p.err);
         }
-        // let every copy land before the block can exit
-        if (lane == 0)
-            for (long long q = g > p.nstage ? g - p.nstage : 0; q < g; ++q)
-                mbar_drain(smem_u32(&full[q % p.nstage]), (uint32_t)((q / p.nstage) & 1), flags, p.err);
     } else if (warp == 1) {
         // ------------------------------ MMA issuer ------------------------------
         if (lane == 0) {
             const uint64_t d0 = tc_sdesc128(smem_u32(stage(0)));
             const uint32_t lo0 = (uint32_t)d0, dhi = (uint32_t)(d0 >> 32);
-            long long g = 0;
-            int cc = 0;
+            QgRing g;
+            int cc = 0, last = -1;  // accumulator uses; the last stage issued
+            uint32_t last_ph = 0;
             bool ok = true;
             uint32_t ready = 0;
             for (int u = blockIdx.x; u < units && ok; u += gridDim.x) {
@@ -279,10 +274,12 @@ __global__ void __launch_bounds__(kQgThreads, 1) q4g_gemm_kernel(const __grid_co
                     tc_fence_after();
                     const uint32_t dt = tmem + (uint32_t)(ab * 128);
                     const int n = min(chunk, p.kt - c0);
-                    for (int i = 0; i < n; ++i, ++g) {
-                        const int s = (int)(g % p.nstage);
-                        const uint32_t nxt = mbar_test(smem_u32(&full[(g + 1) % p.nstage]), (uint32_t)(((g + 1) / p.nstage) & 1));
-                        if (!ready) ok = mbar_wait(smem_u32(&full[s]), (uint32_t)((g / p.nstage) & 1), flags, p.err);
+                    for (int i = 0; i < n; ++i) {
+                        const int s = g.s;
+                        const uint32_t ph = g.ph;
+                        g.next(p.nstage);
+                        const uint32_t nxt = mbar_test(smem_u32(&full[g.s]), g.ph);
+                        if (!ready) ok = mbar_wait(smem_u32(&full[s]), ph, flags, p.err);
                         if (!ok) break;
                         tc_fence_after();
                         const uint32_t xhi = lo0 + (uint32_t)((s * NP * piece) >> 4), xlo = xhi + (uint32_t)(piece >> 4);
@@ -295,6 +292,8 @@ __global__ void __launch_bounds__(kQgThreads, 1) q4g_gemm_kernel(const __grid_co
                                 tc_mma(dt, wa + 8 * kk, ((uint64_t)dhi << 32) | (xb + 2 * kk), idesc, (i | pass | kk) != 0 ? 1u : 0u);
                         }
                         tc_commit(smem_u32(&empty[s]));
+                        last = s;
+                        last_ph = ph;
                         ready = nxt;
                     }
                     if (!ok) break;
@@ -302,32 +301,31 @@ __global__ void __launch_bounds__(kQgThreads, 1) q4g_gemm_kernel(const __grid_co
                 }
             }
             // the last commits must land before tensor memory is released
-            if (g > 0) mbar_drain(smem_u32(&empty[(g - 1) % p.nstage]), (uint32_t)(((g - 1) / p.nstage) & 1), flags, p.err);
+            if (last >= 0) mbar_drain(smem_u32(&empty[last]), last_ph, flags, p.err);
         }
     } else if (warp == 2) {
         // ------------------------------ raw weights ------------------------------
-        long long r = 0;
-        bool ok = true;
+        QgRing r;
+        bool ok = true, wrapped = false;
         const int nr = (w.KS + 1) / 2;
         for (int u = blockIdx.x; u < units && ok; u += gridDim.x) {
             const QgUnit un = place(u);
             const int nrb = min(8, w.RB - 8 * un.nt);
             const uint8_t* src = w.data + (long long)un.e * w.expert_stride + ((long long)(8 * un.nt + lane) * w.KS) * seg_bytes;
-            for (int j = 0; j < nr && ok; ++j, ++r) {
-                const int s = (int)(r % p.nraw);
-                if (r >= p.nraw) ok = mbar_wait(smem_u32(&r_empty[s]), (uint32_t)(((r / p.nraw) - 1) & 1), flags, p.err);
-                if (!ok) break;
+            for (int j = 0; j < nr; ++j) {
+                const int s = r.s;
+                if (!(ok = mbar_wait(smem_u32(&r_empty[s]), r.ph ^ 1u, flags, p.err))) break;
                 const int nseg = min(2, w.KS - 2 * j);
                 const uint32_t bar = smem_u32(&r_full[s]);
                 if (lane == 0) mbar_arrive_tx(bar, (uint32_t)(nrb * nseg * seg_bytes));
                 __syncwarp();
                 if (lane < nrb) bulk_g2s(smem_u32(raw(s)) + lane * 2 * seg_bytes, src + (long long)(2 * j) * seg_bytes, (uint32_t)(nseg * seg_bytes), bar);
                 __syncwarp();
+                r.next(p.nraw);
+                wrapped |= r.s == 0;
             }
         }
-        if (lane == 0)
-            for (long long q = r > p.nraw ? r - p.nraw : 0; q < r; ++q)
-                mbar_drain(smem_u32(&r_full[q % p.nraw]), (uint32_t)((q / p.nraw) & 1), flags, p.err);
+        if (lane == 0) qg_drain(r, wrapped, p.nraw, r_full, flags, p.err);
     } else if (warp < kQgConv0) {
         // ------------------------------ epilogue ------------------------------
         const int ew = warp - kQgEpi0, q = warp & 3, half = ew >> 2;
@@ -357,7 +355,7 @@ __global__ void __launch_bounds__(kQgThreads, 1) q4g_gemm_kernel(const __grid_co
                         slot = c.r.order[slot];
                         if (slot >= slots) slot = -1;
                     }
-                    if (slot >= 0) xsc = p.xs ? __ldcg(p.xs + (c.op == P_GATE_UP ? slot / c.r.top_k : slot)) : 1.0f;
+                    xsc = p.xs ? __ldcg(p.xs + un.p0 + col) : 1.0f;
                 }
                 my_slot[j] = slot;
                 my_scale[j] = xsc;
@@ -436,7 +434,8 @@ __global__ void __launch_bounds__(kQgThreads, 1) q4g_gemm_kernel(const __grid_co
     } else {
         // ------------------------------ conversion ------------------------------
         const int cw = warp - kQgConv0, q = warp & 3, grp = cw >> 2;
-        long long g = 0, r = 0;
+        QgRing g, r;
+        int mine = grp;  // tiles until this group's next one
         bool ok = true;
         for (int u = blockIdx.x; u < units && ok; u += gridDim.x) {
             const QgUnit un = place(u);
@@ -448,19 +447,20 @@ __global__ void __launch_bounds__(kQgThreads, 1) q4g_gemm_kernel(const __grid_co
                 m[hh][0] = __frcp_rn(__ldg(is));
                 m[hh][1] = __frcp_rn(__ldg(is + 8));
             }
-            for (int j = 0; j < p.kt && ok; j += 4, ++r) {
-                const int rs = (int)(r % p.nraw);
-                ok = mbar_wait(smem_u32(&r_full[rs]), (uint32_t)((r / p.nraw) & 1), flags, p.err);
-                if (!ok) break;
+            for (int j = 0; j < p.kt && ok; j += 4) {
+                const int rs = r.s;
+                if (!(ok = mbar_wait(smem_u32(&r_full[rs]), r.ph, flags, p.err))) break;
+                r.next(p.nraw);
                 const int n = min(4, p.kt - j);
-                for (int i = 0; i < n; ++i, ++g) {
-                    if ((int)(g & 1) != grp) continue;
-                    const int s = (int)(g % p.nstage);
+                for (int i = 0; i < n; ++i, mine ^= 1) {
+                    const int s = g.s;
+                    const uint32_t ph = g.ph;
+                    g.next(p.nstage);
+                    if (mine) continue;
                     uint32_t hi[16], lo[16];
                     const uint8_t* seg = raw(rs) + 2 * q * 2 * seg_bytes + (i >> 1) * seg_bytes;
                     qg_convert<NP, NG>(seg, i & 1, lane, m[0][0], m[0][1], hi, lo);
-                    if (g >= p.nstage) ok = mbar_wait(smem_u32(&empty[s]), (uint32_t)(((g / p.nstage) - 1) & 1), flags, p.err);
-                    if (!ok) break;
+                    if (!(ok = mbar_wait(smem_u32(&empty[s]), ph ^ 1u, flags, p.err))) break;
                     tc_fence_after();
                     __syncwarp();
                     const uint32_t col = tmem + ((uint32_t)(32 * q) << 16) + (uint32_t)(kQgWCol0 + 32 * NP * s);
