@@ -50,13 +50,24 @@ __device__ __forceinline__ void route_token(const RouteCall& c, long long tok, f
     uint32_t key[EPL];
     const long long base = tok * c.ldl;
     float m = -INFINITY;
+    // the type is told apart outside of the loads, so that they are in flight together
+    if (c.xt == X_F32) {
+#pragma unroll
+        for (int i = 0; i < EPL; ++i) score[i] = lane + 32 * i < c.E ? static_cast<const float*>(c.logits)[base + lane + 32 * i] : -INFINITY;
+    } else {
+        uint16_t raw[EPL];
+#pragma unroll
+        for (int i = 0; i < EPL; ++i) raw[i] = lane + 32 * i < c.E ? static_cast<const uint16_t*>(c.logits)[base + lane + 32 * i] : (uint16_t)0;
+#pragma unroll
+        for (int i = 0; i < EPL; ++i)
+            score[i] = lane + 32 * i >= c.E   ? -INFINITY
+                       : c.xt == X_F16 ? __half2float(__ushort_as_half(raw[i]))
+                                       : __uint_as_float((uint32_t)raw[i] << 16);
+    }
 #pragma unroll
     for (int i = 0; i < EPL; ++i) {
-        const int e = lane + 32 * i;
-        float l = e < c.E ? x_load(c.logits, c.xt, base + e) : -INFINITY;
-        if (l != l) l = -INFINITY;  // a NaN logit is a masked one
-        score[i] = l;
-        m = fmaxf(m, l);
+        if (score[i] != score[i]) score[i] = -INFINITY;  // a NaN logit is a masked one
+        m = fmaxf(m, score[i]);
     }
     float total = 0.0f;
     if (!c.sigmoid) {
@@ -155,11 +166,11 @@ __device__ __forceinline__ void route_token(const RouteCall& c, long long tok, f
         const uint32_t id = __reduce_min_sync(0xffffffffu, b == best ? (uint32_t)(lane + 32 * bi) : 0xffffffffu);
         float s = 0.0f;
 #pragma unroll
-        for (int i = 0; i < EPL; ++i)
-            if ((int)(id >> 5) == i) {
-                s = score[i];
-                if (lane == (int)(id & 31u)) key[i] = 0u;
-            }
+        for (int i = 0; i < EPL; ++i) {
+            const bool here = (int)id == lane + 32 * i;
+            s = here ? score[i] : s;
+            key[i] = here ? 0u : key[i];
+        }
         s = __shfl_sync(0xffffffffu, s, (int)(id & 31u));
         sum += s;
         if (lane == j) {

@@ -94,7 +94,17 @@ __device__ __forceinline__ void x_store(void* p, int xt, long long i, float v) {
     else static_cast<__nv_bfloat16*>(p)[i] = __float2bfloat16_rn(v);
 }
 
-// silu(g) u
+template <typename Y>
+__device__ __forceinline__ Y to_type(float v);
+template <>
+__device__ __forceinline__ float to_type<float>(float v) { return v; }
+template <>
+__device__ __forceinline__ __half to_type<__half>(float v) { return __float2half_rn(v); }
+template <>
+__device__ __forceinline__ __nv_bfloat16 to_type<__nv_bfloat16>(float v) { return __float2bfloat16_rn(v); }
+
+// silu(g) u; the fast form (a few units of 2^-22) where the result is rounded to 16 bits
+__device__ __forceinline__ float swiglu_fast(float g, float u) { return __fdividef(g, 1.0f + __expf(-g)) * u; }
 __device__ __forceinline__ float swiglu(float g, float u) { return g / (1.0f + expf(-g)) * u; }
 
 }  // namespace qmm

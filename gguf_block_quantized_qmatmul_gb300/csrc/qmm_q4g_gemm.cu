@@ -5,17 +5,16 @@
 namespace qmm {
 namespace {
 
-// One row per block: f16 values (pieces) scaled by 2^b, and 2^-b.  The scale
+// One row per warp: f16 values (pieces) scaled by 2^b, and 2^-b.  The scale
 // comes from the row's largest finite magnitude; infinities and NaN stay what
 // they are (their rests are 0).  For experts row p is the activations of slot
-// order[p].
-template <int NP>
+// order[p].  Bound by the rows' bytes; four 16-byte loads a lane are in flight.
+template <int NP, int XT>
 __global__ void __launch_bounds__(256) q4g_prep_kernel(const QgCall c, int rows, __half* out, float* xs) {
-    __shared__ float red[8];
     grid_dep_launch();
     grid_dep_wait();
-    const int row = blockIdx.x, tid = threadIdx.x, lane = tid & 31, warp = tid >> 5, K = c.w.K, xt = c.xt;
-    const void* x = c.x;
+    const int row = blockIdx.x * 8 + (threadIdx.x >> 5), lane = threadIdx.x & 31, K = c.w.K;
+    if (row >= rows) return;
     int from = row;
     if (c.op != P_DENSE) {
         if (row >= c.r.offsets[c.w.E]) return;
@@ -23,60 +22,80 @@ __global__ void __launch_bounds__(256) q4g_prep_kernel(const QgCall c, int rows,
         if (from < 0 || from >= rows) return;
         if (c.op == P_GATE_UP) from /= c.r.top_k;
     }
-    const long long at = (long long)from * c.ldx;
-    if (xt == X_F16) {
-        for (int k = 8 * tid; k < K; k += 8 * 256)
-            *reinterpret_cast<uint4*>(out + (long long)row * K + k) = *reinterpret_cast<const uint4*>(static_cast<const uint16_t*>(x) + at + k);
+    constexpr int V = XT == X_F32 ? 4 : 8;  // values in 16 bytes
+    const uint4* x = reinterpret_cast<const uint4*>(static_cast<const uint8_t*>(c.x) + (long long)from * c.ldx * (16 / V));
+    const int n = K / V;
+    __half* hr = out + (long long)row * K;
+    if (XT == X_F16) {
+        for (int i = lane; i < n; i += 128) {
+            uint4 v[4];
+#pragma unroll
+            for (int j = 0; j < 4; ++j)
+                if (i + 32 * j < n) v[j] = __ldg(x + i + 32 * j);
+#pragma unroll
+            for (int j = 0; j < 4; ++j)
+                if (i + 32 * j < n) reinterpret_cast<uint4*>(hr)[i + 32 * j] = v[j];
+        }
         return;
     }
-    auto load8 = [&](int k, float f[8]) {
-        if (xt == X_F32) {
-            const float4 a = *reinterpret_cast<const float4*>(static_cast<const float*>(x) + at + k);
-            const float4 b = *reinterpret_cast<const float4*>(static_cast<const float*>(x) + at + k + 4);
-            f[0] = a.x; f[1] = a.y; f[2] = a.z; f[3] = a.w;
-            f[4] = b.x; f[5] = b.y; f[6] = b.z; f[7] = b.w;
-        } else {
-            const uint4 u = *reinterpret_cast<const uint4*>(static_cast<const uint16_t*>(x) + at + k);
-            const uint32_t v[4] = {u.x, u.y, u.z, u.w};
+    auto unpack = [](const uint4& u, float f[8]) {
+        const uint32_t w[4] = {u.x, u.y, u.z, u.w};
 #pragma unroll
-            for (int j = 0; j < 4; ++j) {
-                f[2 * j] = __uint_as_float(v[j] << 16);
-                f[2 * j + 1] = __uint_as_float(v[j] & 0xffff0000u);
+        for (int j = 0; j < 4; ++j) {
+            if (XT == X_F32) {
+                f[j] = __uint_as_float(w[j]);
+            } else {
+                f[2 * j] = __uint_as_float(w[j] << 16);
+                f[2 * j + 1] = __uint_as_float(w[j] & 0xffff0000u);
             }
         }
     };
     float m = 0.0f;
-    for (int k = 8 * tid; k < K; k += 8 * 256) {
-        float f[8];
-        load8(k, f);
+    for (int i = lane; i < n; i += 128) {
+        uint4 v[4];
 #pragma unroll
-        for (int j = 0; j < 8; ++j) m = fabsf(f[j]) < INFINITY ? fmaxf(m, fabsf(f[j])) : m;
+        for (int j = 0; j < 4; ++j) v[j] = i + 32 * j < n ? __ldg(x + i + 32 * j) : make_uint4(0u, 0u, 0u, 0u);
+#pragma unroll
+        for (int j = 0; j < 4; ++j) {
+            float f[8];
+            unpack(v[j], f);
+#pragma unroll
+            for (int e = 0; e < V; ++e) m = fabsf(f[e]) < INFINITY ? fmaxf(m, fabsf(f[e])) : m;
+        }
     }
 #pragma unroll
     for (int o = 16; o; o >>= 1) m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, o));
-    if (lane == 0) red[warp] = m;
-    __syncthreads();
-#pragma unroll
-    for (int i = 0; i < 8; ++i) m = fmaxf(m, red[i]);
     const float is = tc_row_iscale(m), sc = __frcp_rn(is);
-    if (tid == 0) xs[row] = is;
-    for (int k = 8 * tid; k < K; k += 8 * 256) {
-        float f[8];
-        load8(k, f);
-        uint32_t h[4], l[4];
+    if (lane == 0) xs[row] = is;
+    for (int i = lane; i < n; i += 128) {
+        uint4 v[4];
+#pragma unroll
+        for (int j = 0; j < 4; ++j)
+            if (i + 32 * j < n) v[j] = __ldg(x + i + 32 * j);
 #pragma unroll
         for (int j = 0; j < 4; ++j) {
-            const float a = f[2 * j] * sc, b = f[2 * j + 1] * sc;
-            const __half2 v = __floats2half2_rn(a, b);
-            h[j] = *reinterpret_cast<const uint32_t*>(&v);
-            if (NP == 2) {
-                const float2 vf = __half22float2(v);
-                const __half2 r = __floats2half2_rn(fabsf(a) < INFINITY ? a - vf.x : 0.0f, fabsf(b) < INFINITY ? b - vf.y : 0.0f);
-                l[j] = *reinterpret_cast<const uint32_t*>(&r);
+            if (i + 32 * j >= n) continue;
+            float f[8];
+            unpack(v[j], f);
+            uint32_t h[V / 2], l[V / 2];
+#pragma unroll
+            for (int e = 0; e < V / 2; ++e) {
+                const float a = f[2 * e] * sc, b = f[2 * e + 1] * sc;
+                const __half2 hv = __floats2half2_rn(a, b);
+                h[e] = *reinterpret_cast<const uint32_t*>(&hv);
+                if (NP == 2) {
+                    const float2 vf = __half22float2(hv);
+                    const __half2 r = __floats2half2_rn(fabsf(a) < INFINITY ? a - vf.x : 0.0f, fabsf(b) < INFINITY ? b - vf.y : 0.0f);
+                    l[e] = *reinterpret_cast<const uint32_t*>(&r);
+                }
+            }
+            if constexpr (V == 8) {
+                reinterpret_cast<uint4*>(hr)[i + 32 * j] = make_uint4(h[0], h[1], h[2], h[3]);
+            } else {
+                reinterpret_cast<uint2*>(hr)[i + 32 * j] = make_uint2(h[0], h[1]);
+                reinterpret_cast<uint2*>(hr + (long long)rows * K)[i + 32 * j] = make_uint2(l[0], l[1]);
             }
         }
-        *reinterpret_cast<uint4*>(out + (long long)row * K + k) = make_uint4(h[0], h[1], h[2], h[3]);
-        if (NP == 2) *reinterpret_cast<uint4*>(out + ((long long)rows + row) * K + k) = make_uint4(l[0], l[1], l[2], l[3]);
     }
 }
 
@@ -100,34 +119,55 @@ QgGemmPlan plan_q4g_gemm(const QgCall& c, int sms, int smem_max) {
     pl.prep = grouped || c.xt != X_F16;
     const long long per = grouped ? (c.M + c.w.E - 1) / c.w.E : c.M;  // activation rows per weight matrix
     pl.ntiles = (c.w.RB + 7) / 8;
-    // tiles of 256 rows amortise the weights' conversion best; two accumulators of 128 columns
-    // let the epilogue run beside the next unit's MMAs
-    const int most = pl.np == 2 ? 128 : 256;
+    // Two accumulators, so that the epilogue runs beside the next unit's MMAs: at most 192
+    // columns each (with two pieces 64: the epilogue's running sums are registers), the weight
+    // pieces' stages in the columns left.
+    const int most = pl.np == 2 ? kQgBX2 : kQgBX1;
+    pl.ks = 1;
     if (grouped) {
-        pl.bx = per >= 192 && most == 256 ? 256 : per > 48 ? 128 : per > 24 ? 64 : 32;
+        pl.bx = per > 64 ? most : per > 32 ? 64 : 32;
     } else {
-        const int tiles = (int)((per + most - 1) / most);
-        pl.bx = (int)((per + tiles - 1) / tiles + 15) / 16 * 16;
+        // Modelled cycles: a 64-K tile costs its MMAs (2 cycles a column and pass) or its
+        // conversion (about 300, 500 with two pieces), a unit about 2000 more; slices of K
+        // cost their partial sums' traffic and a launch (about 4000).
+        const int kt = (c.w.K + 63) / 64, nr = (c.w.KS + 1) / 2;
+        double best = 0;
+        for (int tiles = (int)((per + most - 1) / most); tiles <= 8 + (per + most - 1) / most; ++tiles) {
+            const int bx = (int)((per + tiles - 1) / tiles + 15) / 16 * 16;
+            const long long un = (long long)pl.ntiles * ((per + bx - 1) / bx);
+            const double mma = 2.0 * bx * (2 * pl.np - 1), conv = pl.np == 2 ? 500.0 : 300.0, tile = mma > conv ? mma : conv;
+            for (int ks = 1; ks <= nr && ks <= 16 && (ks == 1 || un * ks <= 2 * sms); ++ks) {
+                const double waves = (double)((un * ks + sms - 1) / sms);
+                const double cost = waves * ((double)kt / ks * tile + 2000.0) + (ks > 1 ? 4000.0 + 8.0 * ks * per * c.w.N / 3000.0 : 0.0);
+                if (best == 0 || cost < 0.98 * best) {
+                    best = cost;
+                    pl.bx = bx;
+                    pl.ks = ks;
+                }
+            }
+            if (bx == 16) break;
+        }
     }
     pl.box = grouped && pl.bx > 64 ? 64 : pl.bx;  // an expert's tile is any size: no more copied than 63 rows too many
-    pl.nacc = pl.bx <= 128 ? 2 : 1;
+    pl.accw = (pl.bx + 31) / 32 * 32;
     pl.mtiles = grouped ? 0 : (int)((per + pl.bx - 1) / pl.bx);
     pl.nraw = 3;
     const int raw = 16 * qg_seg_bytes(c.w.ng), stage = pl.bx * 128 * pl.np;
-    const int fixed = 512 + 2 * 8 * 128 * 4 + (c.w.E + 1) * 4 + 1024;
+    const int fixed = 512 + 2 * kQgEpiWarps * kQgBX1 * 4 + (c.w.E + 1) * 4 + 1024;
     pl.nstage = (smem_max - fixed - pl.nraw * raw) / stage;
-    const int cap = 8 / pl.np;
+    const int cap = (kTcTmemCols - 2 * pl.accw) / (32 * pl.np);
     if (pl.nstage > cap) pl.nstage = cap;
-    if (pl.nstage < 2) return pl;
+    if (pl.nstage > kQgStageMax) pl.nstage = kQgStageMax;
+    if (pl.nstage < kQgGroups || pl.nstage < 2) return pl;
     pl.smem = (size_t)pl.nstage * stage + (size_t)pl.nraw * raw + fixed;
-    const long long units = grouped ? ((long long)c.w.E + c.M / pl.bx) * pl.ntiles : (long long)pl.mtiles * pl.ntiles;
+    const long long units = grouped ? ((long long)c.w.E + c.M / pl.bx) * pl.ntiles : (long long)pl.mtiles * pl.ntiles * pl.ks;
     if (units > (1ll << 30)) return pl;
     pl.grid = (int)(units < sms ? units : sms);
     auto r256 = [](size_t v) { return (v + 255) / 256 * 256; };
     pl.ws_x = 0;
     pl.ws_xs = pl.prep ? r256((size_t)pl.np * rows * c.w.K * 2) : 0;
     pl.ws_part = pl.ws_xs + (pl.prep ? r256((size_t)rows * 4) : 0);
-    pl.workspace = pl.ws_part + (c.op == P_DOWN ? (size_t)c.M * c.w.N * 4 : 0);
+    pl.workspace = pl.ws_part + (c.op == P_DOWN || pl.ks > 1 ? (size_t)pl.ks * c.M * c.w.N * 4 : 0);
     pl.ok = true;
     return pl;
 }
@@ -141,8 +181,10 @@ cudaError_t launch_q4g_gemm(const QgGemmPlan& pl, const QgCall& c, void* ws, uns
     if (pl.prep) {
         __half* xh = reinterpret_cast<__half*>(wsb + pl.ws_x);
         if (c.xt != X_F16) xs = reinterpret_cast<float*>(wsb + pl.ws_xs);
-        const cudaError_t e = pl.np == 2 ? launch_pdl(q4g_prep_kernel<2>, (unsigned)rows, 256, 0, s, c, rows, xh, xs)
-                                         : launch_pdl(q4g_prep_kernel<1>, (unsigned)rows, 256, 0, s, c, rows, xh, xs);
+        const unsigned blocks = (unsigned)((rows + 7) / 8);
+        const cudaError_t e = c.xt == X_F32   ? launch_pdl(q4g_prep_kernel<2, X_F32>, blocks, 256, 0, s, c, rows, xh, xs)
+                              : c.xt == X_F16 ? launch_pdl(q4g_prep_kernel<1, X_F16>, blocks, 256, 0, s, c, rows, xh, xs)
+                                              : launch_pdl(q4g_prep_kernel<1, X_BF16>, blocks, 256, 0, s, c, rows, xh, xs);
         if (e != cudaSuccess) return e;
         xsrc = xh;
         pitch = (long long)K * 2;
@@ -160,12 +202,13 @@ cudaError_t launch_q4g_gemm(const QgGemmPlan& pl, const QgCall& c, void* ws, uns
     p.xrows = rows;
     p.bx = pl.bx;
     p.box = pl.box;
-    p.nacc = pl.nacc;
+    p.accw = pl.accw;
     p.mtiles = pl.mtiles;
     p.ntiles = pl.ntiles;
     p.kt = (K + 63) / 64;
     p.nraw = pl.nraw;
     p.nstage = pl.nstage;
+    p.ks = pl.ks;
     p.grid = pl.grid;
     p.off_raw = pl.nstage * pl.bx * 128 * pl.np;
     p.off_bar = p.off_raw + pl.nraw * 16 * qg_seg_bytes(c.w.ng);
@@ -178,6 +221,7 @@ cudaError_t launch_q4g_gemm(const QgGemmPlan& pl, const QgCall& c, void* ws, uns
         e = c.w.ng == 1   ? gemm_one<1, 1>(pl, tx, p, smem_max, s)
             : c.w.ng == 2 ? gemm_one<1, 2>(pl, tx, p, smem_max, s)
                           : gemm_one<1, 4>(pl, tx, p, smem_max, s);
+    if (e == cudaSuccess && pl.ks > 1) return launch_q4g_sum(p.part, pl.ks, (long long)c.M * c.w.N, c.y, c.xt, s);
     if (e != cudaSuccess || c.op != P_DOWN) return e;
     return launch_q4g_combine(p.part, c.r, c.w.E, c.w.N, c.y, c.xt, s);
 }

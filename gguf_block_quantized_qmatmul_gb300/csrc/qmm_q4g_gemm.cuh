@@ -21,32 +21,39 @@
 //               experts' rows were put in sorted order by the preparation launch
 //               (gathering four rows a copy here measured 90 cycles a copy: 643 us
 //               against the whole of 2048 tokens x 8 of 64 experts, 2048 -> 2 x 1024)
-//   warp 1      one thread: four MMAs (twelve with two pieces) per 64 K, A in
+//   warp 1      one elected lane: four MMAs (twelve with two pieces) per 64 K, A in
 //               tensor memory, B in shared memory
 //   warp 2      raw weights: eight 1-D copies (a row block's two segments each)
 //               per 256 K
-//   warps 3-10  epilogue: accumulator columns to registers, scaled; the experts'
+//   warps 3-6   epilogue: accumulator columns to registers, scaled; the experts'
 //               first product takes its up row from the lane eight away (paired
 //               layout) for silu(g) u
-//   warps 11-18 conversion: a lane's uint4 of codes becomes fragment registers
+//   warps 7-22  conversion: a lane's uint4 of codes becomes fragment registers
 //               and goes to tensor memory as they are (16-lane x 128-bit
-//               stores); two groups, even and odd 64-K tiles
+//               stores); four groups of four warps, one 64-K tile of a raw stage
+//               each (a tile takes a group about 1400 cycles from end to end, and 192
+//               rows' MMAs 384: with two groups those waited for it)
 // The weights are bound for tensor memory, so shared memory feeds only the
 // activation tiles to the MMAs.  With two pieces the tensor core's truncating
 // f32 accumulation would show: the accumulator is restarted every kQgChunk
-// tiles and the epilogue adds the chunks in registers.
+// tiles and the epilogue adds the chunks in registers.  A dense call with fewer
+// units than SMs is split over K as well, and a last launch adds the slices.
 #pragma once
+
+#include <type_traits>
 
 #include "qmm_q4g_rows.cuh"
 
 namespace qmm {
 
-constexpr int kQgThreads = 19 * 32;
-constexpr int kQgEpi0 = 3, kQgConv0 = 11;
+constexpr int kQgEpiWarps = 8, kQgConvWarps = 8;
+constexpr int kQgEpiHalves = kQgEpiWarps / 4, kQgGroups = kQgConvWarps / 4;  // warps per TMEM lane quarter
+constexpr int kQgEpi0 = 3, kQgConv0 = kQgEpi0 + kQgEpiWarps;
+constexpr int kQgThreads = (kQgConv0 + kQgConvWarps) * 32;
+constexpr int kQgBX1 = 192, kQgBX2 = 64;  // activation rows per tile, at most: one piece, two pieces
 constexpr int kQgRawMax = 4, kQgStageMax = 8;
 constexpr int kQgChunk = 4;      // 64-K tiles per accumulation chunk (two pieces)
 constexpr int kQgMaxE = 512;     // experts of a grouped call
-constexpr int kQgWCol0 = 256;    // weight pieces in tensor memory from this column
 
 struct QgGemmParams {
     QgCall c;
@@ -55,7 +62,8 @@ struct QgGemmParams {
     const float* wis;     // 2^-a per weight row, layout order
     unsigned* err;
     int xrows;            // rows of an activation plane (the lo plane follows)
-    int bx, box, nacc, mtiles, ntiles, kt, nraw, nstage, grid;
+    int bx, box, accw, mtiles, ntiles, kt, nraw, nstage, grid;
+    int ks;               // K slices (dense): f32 partial outputs [ks][M][N]
     int off_raw, off_bar;
 };
 
@@ -66,6 +74,13 @@ __device__ __forceinline__ void tc_st_frag(uint32_t taddr, const uint32_t v[16])
         "r"(v[0]), "r"(v[1]), "r"(v[2]), "r"(v[3]), "r"(v[4]), "r"(v[5]), "r"(v[6]), "r"(v[7]), "r"(v[8]), "r"(v[9]),
         "r"(v[10]), "r"(v[11]), "r"(v[12]), "r"(v[13]), "r"(v[14]), "r"(v[15])
         : "memory");
+}
+
+// true in one lane of a converged warp
+__device__ __forceinline__ bool elect_one() {
+    uint32_t p;
+    asm volatile("{\n\t.reg .pred p;\n\telect.sync _|p, 0xffffffff;\n\tselp.u32 %0, 1, 0, p;\n\t}" : "=r"(p));
+    return p != 0;
 }
 
 // One 64-K tile h of a segment of one row block: fragment registers of its f16 weights (and their rests).
@@ -102,6 +117,25 @@ __device__ __forceinline__ void qg_convert(const uint8_t* seg, int h, int lane, 
     }
 }
 
+// Bounded wait whose tries suspend the warp (for up to 2 us each) instead of
+// returning at once: 20 waiting warps that spin take a third of the issue slots
+// that the converting ones need.
+__device__ __forceinline__ bool qg_wait(uint32_t bar, uint32_t parity, volatile int* abort_flag, unsigned* err) {
+    if (mbar_try(bar, parity)) return true;
+    const long long t0 = clock64();
+    while (true) {
+        uint32_t ok;
+        asm volatile(
+            "{\n\t.reg .pred p;\n\tmbarrier.try_wait.parity.shared::cta.b64 p, [%1], %2, %3;\n\tselp.u32 %0, 1, 0, p;\n\t}"
+            : "=r"(ok)
+            : "r"(bar), "r"(parity), "r"(2000u)
+            : "memory");
+        if (ok) return true;
+        if (*abort_flag) return false;
+        if (clock64() - t0 > kWaitLimitCheck) return mbar_spin(bar, parity, abort_flag, err, false);  // raises the error in the end
+    }
+}
+
 // A place in a ring of n stages: its index and the parity of its current use.
 // A producer waits for a stage's release with ph ^ 1, which a fresh barrier
 // passes.  (Counting uses and dividing by a run-time n costs the MMA thread
@@ -115,6 +149,9 @@ struct QgRing {
             ph ^= 1u;
         }
     }
+    __device__ __forceinline__ void skip(int k, int n) {
+        for (s += k; s >= n; s -= n) ph ^= 1u;
+    }
 };
 // After the last use: waits for the copies of every stage still in flight.
 __device__ __forceinline__ void qg_drain(const QgRing& r, bool wrapped, int n, uint64_t* bars, volatile int* flags, unsigned* err) {
@@ -125,6 +162,7 @@ __device__ __forceinline__ void qg_drain(const QgRing& r, bool wrapped, int n, u
 // a unit's place
 struct QgUnit {
     int e, p0, n, nt;  // expert, first position (row of x in a dense call), activation rows, row tile
+    int split, j0, j1; // K slice, its 64-K tiles
 };
 
 template <int NP, int NG>
@@ -144,9 +182,9 @@ __global__ void __launch_bounds__(kQgThreads, 1) q4g_gemm_kernel(const __grid_co
     static_assert((2 * kQgStageMax + 2 * kQgRawMax + 4) * 8 <= 256, "mbarriers overlap the TMEM slot");
     uint32_t* tslot = reinterpret_cast<uint32_t*>(sm + p.off_bar + 256);
     volatile int* flags = reinterpret_cast<volatile int*>(sm + p.off_bar + 320);
-    int* col_slot = reinterpret_cast<int*>(sm + p.off_bar + 512);      // [8 warps][128]
-    float* col_scale = reinterpret_cast<float*>(col_slot + 8 * 128);   // [8 warps][128]
-    int* ts = reinterpret_cast<int*>(col_scale + 8 * 128);             // [E + 1] activation tiles before each expert
+    int* col_slot = reinterpret_cast<int*>(sm + p.off_bar + 512);             // [warps][kQgBX1]
+    float* col_scale = reinterpret_cast<float*>(col_slot + kQgEpiWarps * kQgBX1);  // [warps][kQgBX1]
+    int* ts = reinterpret_cast<int*>(col_scale + kQgEpiWarps * kQgBX1);       // [E + 1] activation tiles before each expert
     const bool grouped = c.op != P_DENSE;
     const int slots = grouped ? c.r.T * c.r.top_k : c.M;
     if (tid == 0) {
@@ -156,11 +194,11 @@ __global__ void __launch_bounds__(kQgThreads, 1) q4g_gemm_kernel(const __grid_co
         }
         for (int i = 0; i < kQgRawMax; ++i) {
             mbar_init(smem_u32(&r_full[i]), 1);
-            mbar_init(smem_u32(&r_empty[i]), 8);
+            mbar_init(smem_u32(&r_empty[i]), kQgConvWarps);
         }
         for (int i = 0; i < 2; ++i) {
             mbar_init(smem_u32(&acc_full[i]), 1);
-            mbar_init(smem_u32(&acc_empty[i]), 8);
+            mbar_init(smem_u32(&acc_empty[i]), kQgEpiWarps);
         }
         flags[0] = 0;
         fence_mbar_init();
@@ -203,9 +241,14 @@ __global__ void __launch_bounds__(kQgThreads, 1) q4g_gemm_kernel(const __grid_co
     __syncthreads();
     tc_fence_after();
     const uint32_t tmem = *tslot;
-    const int units = ts[w.E] * p.ntiles;
+    const int tiles_all = ts[w.E] * p.ntiles, units = tiles_all * p.ks;
     auto place = [&](int u) {
         QgUnit un;
+        un.split = u / tiles_all;
+        u -= un.split * tiles_all;
+        const int nr = (w.KS + 1) / 2;  // raw stages
+        un.j0 = 4 * (int)((long long)un.split * nr / p.ks);
+        un.j1 = min(p.kt, 4 * (int)((long long)(un.split + 1) * nr / p.ks));
         const int st = u / p.ntiles;
         un.nt = u - st * p.ntiles;
         int lo = 0, hi = w.E;  // ts[lo] <= st < ts[hi]
@@ -238,8 +281,8 @@ __global__ void __launch_bounds__(kQgThreads, 1) q4g_gemm_kernel(const __grid_co
             for (int u = blockIdx.x; u < units && ok; u += gridDim.x) {
                 const QgUnit un = place(u);
                 const int boxes = (un.n + p.box - 1) / p.box;
-                for (int j = 0; j < p.kt; ++j) {
-                    if (!(ok = mbar_wait(smem_u32(&empty[g.s]), g.ph ^ 1u, flags, p.err))) break;
+                for (int j = un.j0; j < un.j1; ++j) {
+                    if (!(ok = qg_wait(smem_u32(&empty[g.s]), g.ph ^ 1u, flags, p.err))) break;
                     const uint32_t bar = smem_u32(&full[g.s]), to = smem_u32(stage(g.s));
                     mbar_arrive_tx(bar, (uint32_t)(NP * boxes * p.box * 128));
                     for (int i = 0; i < boxes; ++i) {
@@ -255,35 +298,40 @@ __global__ void __launch_bounds__(kQgThreads, 1) q4g_gemm_kernel(const __grid_co
         }
     } else if (warp == 1) {
         // ------------------------------ MMA issuer ------------------------------
-        if (lane == 0) {
-            const uint64_t d0 = tc_sdesc128(smem_u32(stage(0)));
-            const uint32_t lo0 = (uint32_t)d0, dhi = (uint32_t)(d0 >> 32);
-            QgRing g;
-            int cc = 0, last = -1;  // accumulator uses; the last stage issued
-            uint32_t last_ph = 0;
-            bool ok = true;
-            uint32_t ready = 0;
-            for (int u = blockIdx.x; u < units && ok; u += gridDim.x) {
-                const QgUnit un = place(u);
-                const uint32_t idesc = tc_idesc((un.n + 15) / 16 * 16);
-                const int chunk = NP == 2 ? kQgChunk : p.kt;
-                for (int c0 = 0; c0 < p.kt && ok; c0 += chunk, ++cc) {
-                    const int ab = p.nacc == 2 ? (cc & 1) : 0, use = p.nacc == 2 ? (cc >> 1) : cc;
-                    if (use > 0) ok = mbar_wait(smem_u32(&acc_empty[ab]), (uint32_t)((use - 1) & 1), flags, p.err);
+        // The whole warp runs the loop, so that its values are uniform, and one elected lane
+        // issues: inside a one-lane branch every MMA's operands take detours to uniform
+        // registers (58 cycles an MMA and 410 a tile, against 128 cycles of MMAs at 64 rows).
+        const bool lead = elect_one();
+        const uint64_t d0 = tc_sdesc128(smem_u32(stage(0)));
+        const uint32_t lo0 = (uint32_t)d0, dhi = (uint32_t)(d0 >> 32);
+        QgRing g;
+        int cc = 0, last = -1;  // accumulator uses; the last stage issued
+        uint32_t last_ph = 0;
+        bool ok = true;
+        uint32_t ready = 0;
+        for (int u = blockIdx.x; u < units && ok; u += gridDim.x) {
+            const QgUnit un = place(u);
+            const uint32_t idesc = tc_idesc((un.n + 15) / 16 * 16);
+            const int chunk = NP == 2 ? kQgChunk : p.kt;
+            for (int c0 = un.j0; c0 < un.j1 && ok; c0 += chunk, ++cc) {
+                const int ab = cc & 1, use = cc >> 1;
+                if (use > 0) ok = qg_wait(smem_u32(&acc_empty[ab]), (uint32_t)((use - 1) & 1), flags, p.err);
+                if (!ok) break;
+                tc_fence_after();
+                const uint32_t dt = tmem + (uint32_t)(ab * p.accw);
+                const int n = min(chunk, un.j1 - c0);
+                for (int i = 0; i < n; ++i) {
+                    const int s = g.s;
+                    const uint32_t ph = g.ph;
+                    g.next(p.nstage);
+                    const uint32_t nxt = mbar_test(smem_u32(&full[g.s]), g.ph);
+                    if (!ready) ok = qg_wait(smem_u32(&full[s]), ph, flags, p.err);
                     if (!ok) break;
                     tc_fence_after();
-                    const uint32_t dt = tmem + (uint32_t)(ab * 128);
-                    const int n = min(chunk, p.kt - c0);
-                    for (int i = 0; i < n; ++i) {
-                        const int s = g.s;
-                        const uint32_t ph = g.ph;
-                        g.next(p.nstage);
-                        const uint32_t nxt = mbar_test(smem_u32(&full[g.s]), g.ph);
-                        if (!ready) ok = mbar_wait(smem_u32(&full[s]), ph, flags, p.err);
-                        if (!ok) break;
-                        tc_fence_after();
-                        const uint32_t xhi = lo0 + (uint32_t)((s * NP * piece) >> 4), xlo = xhi + (uint32_t)(piece >> 4);
-                        const uint32_t whi = tmem + (uint32_t)(kQgWCol0 + 32 * NP * s), wlo = whi + 32;
+                    const uint32_t xhi = lo0 + (uint32_t)((s * NP * piece) >> 4), xlo = xhi + (uint32_t)(piece >> 4);
+                    const uint32_t whi = tmem + (uint32_t)(2 * p.accw + 32 * NP * s), wlo = whi + 32;
+                    __syncwarp();
+                    if (lead) {
 #pragma unroll
                         for (int pass = 0; pass < 2 * NP - 1; ++pass) {
                             const uint32_t wa = pass == 2 ? wlo : whi, xb = pass == 1 ? xlo : xhi;
@@ -292,29 +340,28 @@ __global__ void __launch_bounds__(kQgThreads, 1) q4g_gemm_kernel(const __grid_co
                                 tc_mma(dt, wa + 8 * kk, ((uint64_t)dhi << 32) | (xb + 2 * kk), idesc, (i | pass | kk) != 0 ? 1u : 0u);
                         }
                         tc_commit(smem_u32(&empty[s]));
-                        last = s;
-                        last_ph = ph;
-                        ready = nxt;
                     }
-                    if (!ok) break;
-                    tc_commit(smem_u32(&acc_full[ab]));
+                    last = s;
+                    last_ph = ph;
+                    ready = nxt;
                 }
+                if (!ok) break;
+                if (lead) tc_commit(smem_u32(&acc_full[ab]));
             }
-            // the last commits must land before tensor memory is released
-            if (last >= 0) mbar_drain(smem_u32(&empty[last]), last_ph, flags, p.err);
         }
+        // the last commits must land before tensor memory is released
+        if (last >= 0) mbar_drain(smem_u32(&empty[last]), last_ph, flags, p.err);
     } else if (warp == 2) {
         // ------------------------------ raw weights ------------------------------
         QgRing r;
         bool ok = true, wrapped = false;
-        const int nr = (w.KS + 1) / 2;
         for (int u = blockIdx.x; u < units && ok; u += gridDim.x) {
             const QgUnit un = place(u);
             const int nrb = min(8, w.RB - 8 * un.nt);
             const uint8_t* src = w.data + (long long)un.e * w.expert_stride + ((long long)(8 * un.nt + lane) * w.KS) * seg_bytes;
-            for (int j = 0; j < nr; ++j) {
+            for (int j = un.j0 / 4; 4 * j < un.j1; ++j) {
                 const int s = r.s;
-                if (!(ok = mbar_wait(smem_u32(&r_empty[s]), r.ph ^ 1u, flags, p.err))) break;
+                if (!(ok = qg_wait(smem_u32(&r_empty[s]), r.ph ^ 1u, flags, p.err))) break;
                 const int nseg = min(2, w.KS - 2 * j);
                 const uint32_t bar = smem_u32(&r_full[s]);
                 if (lane == 0) mbar_arrive_tx(bar, (uint32_t)(nrb * nseg * seg_bytes));
@@ -328,10 +375,10 @@ __global__ void __launch_bounds__(kQgThreads, 1) q4g_gemm_kernel(const __grid_co
         if (lane == 0) qg_drain(r, wrapped, p.nraw, r_full, flags, p.err);
     } else if (warp < kQgConv0) {
         // ------------------------------ epilogue ------------------------------
-        const int ew = warp - kQgEpi0, q = warp & 3, half = ew >> 2;
+        const int ew = warp - kQgEpi0, q = warp & 3, half = ew >> 2;  // column chunks half, half + kQgEpiHalves, ...
         const uint32_t tq = (uint32_t)(32 * q) << 16;
-        int* my_slot = col_slot + ew * 128;
-        float* my_scale = col_scale + ew * 128;
+        int* my_slot = col_slot + ew * kQgBX1;
+        float* my_scale = col_scale + ew * kQgBX1;
         int cc = 0;
         bool ok = true;
         const int chunk = NP == 2 ? kQgChunk : p.kt;
@@ -342,11 +389,8 @@ __global__ void __launch_bounds__(kQgThreads, 1) q4g_gemm_kernel(const __grid_co
             const int rb = 8 * un.nt + 2 * q + (lane >> 4);
             const int n = rb < w.RB ? qg_row(w, rb, lane & 15) : -1;
             const float wsn = rb < w.RB ? __ldg(p.wis + ((long long)un.e * w.RB + rb) * 16 + (lane & 15)) : 0.0f;
-            // this warp's columns: 16-column chunks half, half + 2, ...
             __syncwarp();
-#pragma unroll
-            for (int k = 0; k < 4; ++k) {
-                const int j = 32 * k + lane, col = 16 * (half + 2 * (j >> 4)) + (j & 15);
+            for (int col = lane; col < 16 * nch; col += 32) {
                 int slot = -1;
                 float xsc = 0.0f;
                 if (col < un.n) {
@@ -357,65 +401,71 @@ __global__ void __launch_bounds__(kQgThreads, 1) q4g_gemm_kernel(const __grid_co
                     }
                     xsc = p.xs ? __ldcg(p.xs + un.p0 + col) : 1.0f;
                 }
-                my_slot[j] = slot;
-                my_scale[j] = xsc;
+                my_slot[col] = slot;
+                my_scale[col] = xsc;
             }
             __syncwarp();
-            auto put = [&](int k, const float v[16]) {  // the k-th of this warp's column chunks
+            const float wup = __shfl_xor_sync(0xffffffffu, wsn, 8);  // the paired row's factor
+            auto put_as = [&](auto* y, int k, const float v[16]) {  // columns 16 k..
+                using Y = typename std::remove_pointer<decltype(y)>::type;
                 if (c.op == P_GATE_UP) {
                     // lanes r < 8 have gate rows, r + 8 their up rows; each finishes one of two columns
                     const bool up = (lane & 8) != 0;
                     const int f = rb * 8 + (lane & 7);
+                    const bool on = rb < w.RB && f < F;
 #pragma unroll
                     for (int i = 0; i < 16; i += 2) {
-                        const float give = up ? v[i] : v[i + 1];
-                        const float got = __shfl_xor_sync(0xffffffffu, give, 8);
-                        const float other = __shfl_xor_sync(0xffffffffu, wsn, 8);
+                        const float got = __shfl_xor_sync(0xffffffffu, up ? v[i] : v[i + 1], 8);
                         const int col = 16 * k + i + (up ? 1 : 0);
                         const int slot = my_slot[col];
                         const float xsc = my_scale[col];
-                        const float mine = (up ? v[i + 1] : v[i]) * wsn * xsc, theirs = got * other * xsc;
-                        if (slot >= 0 && rb < w.RB && f < F)
-                            x_store(c.y, c.xt, (long long)slot * F + f, up ? swiglu(theirs, mine) : swiglu(mine, theirs));
+                        const float mine = (up ? v[i + 1] : v[i]) * wsn * xsc, theirs = got * wup * xsc;
+                        const float r = NP == 2 ? swiglu(up ? theirs : mine, up ? mine : theirs) : swiglu_fast(up ? theirs : mine, up ? mine : theirs);
+                        if (on && slot >= 0) y[(long long)slot * F + f] = to_type<Y>(r);
                     }
                 } else if (n >= 0) {
 #pragma unroll
                     for (int i = 0; i < 16; ++i) {
                         const int slot = my_slot[16 * k + i];
-                        if (slot < 0) continue;
                         const float r = v[i] * wsn * my_scale[16 * k + i];
-                        if (c.op == P_DOWN) p.part[(long long)slot * w.N + n] = r;
-                        else x_store(c.y, c.xt, (long long)slot * w.N + n, r);
+                        if (slot >= 0) y[(long long)slot * w.N + n] = to_type<Y>(r);
                     }
                 }
             };
-            float sum[NP == 2 ? 4 : 1][16];
-            for (int c0 = 0; c0 < p.kt; c0 += chunk, ++cc) {
-                const int ab = p.nacc == 2 ? (cc & 1) : 0, use = p.nacc == 2 ? (cc >> 1) : cc;
-                if (!(ok = mbar_wait(smem_u32(&acc_full[ab]), (uint32_t)(use & 1), flags, p.err))) break;
+            auto put = [&](int k, const float v[16]) {
+                if (c.op == P_DOWN || p.ks > 1) put_as(p.part + (long long)un.split * c.M * w.N, k, v);
+                else if (NP == 2) put_as(static_cast<float*>(c.y), k, v);
+                else if (c.xt == X_F16) put_as(static_cast<__half*>(c.y), k, v);
+                else put_as(static_cast<__nv_bfloat16*>(c.y), k, v);
+            };
+            constexpr int kSums = kQgBX2 / 16 / kQgEpiHalves;
+            float sum[NP == 2 ? kSums : 1][16];
+            for (int c0 = un.j0; c0 < un.j1; c0 += chunk, ++cc) {
+                const int ab = cc & 1, use = cc >> 1;
+                if (!(ok = qg_wait(smem_u32(&acc_full[ab]), (uint32_t)(use & 1), flags, p.err))) break;
                 tc_fence_after();
                 __syncwarp();
-                const uint32_t acol = tmem + tq + (uint32_t)(ab * 128);
+                const uint32_t acol = tmem + tq + (uint32_t)(ab * p.accw);
                 if (NP == 2) {
 #pragma unroll
-                    for (int k = 0; k < 4; ++k) {
+                    for (int k = 0; k < kSums; ++k) {
                         uint32_t r[16];
-                        if (half + 2 * k < nch) {
-                            tc_ld16(acol + 16 * (half + 2 * k), r);
+                        if (half + kQgEpiHalves * k < nch) {
+                            tc_ld16(acol + 16 * (half + kQgEpiHalves * k), r);
                             tc_wait_ld();
 #pragma unroll
-                            for (int i = 0; i < 16; ++i) sum[NP == 2 ? k : 0][i] = c0 == 0 ? __uint_as_float(r[i]) : sum[NP == 2 ? k : 0][i] + __uint_as_float(r[i]);
+                            for (int i = 0; i < 16; ++i) sum[NP == 2 ? k : 0][i] = c0 == un.j0 ? __uint_as_float(r[i]) : sum[NP == 2 ? k : 0][i] + __uint_as_float(r[i]);
                         }
                     }
                 } else {
                     uint32_t r[16];
                     if (half < nch) tc_ld16(acol + 16 * half, r);
-                    for (int ch = half, k = 0; ch < nch; ch += 2, ++k) {
+                    for (int k = half; k < nch; k += kQgEpiHalves) {
                         tc_wait_ld();
                         float v[16];
 #pragma unroll
                         for (int i = 0; i < 16; ++i) v[i] = __uint_as_float(r[i]);
-                        if (ch + 2 < nch) tc_ld16(acol + 16 * (ch + 2), r);
+                        if (k + kQgEpiHalves < nch) tc_ld16(acol + 16 * (k + kQgEpiHalves), r);
                         put(k, v);
                     }
                 }
@@ -427,15 +477,15 @@ __global__ void __launch_bounds__(kQgThreads, 1) q4g_gemm_kernel(const __grid_co
             if (!ok) break;
             if (NP == 2) {
 #pragma unroll
-                for (int k = 0; k < 4; ++k)
-                    if (half + 2 * k < nch) put(k, sum[NP == 2 ? k : 0]);
+                for (int k = 0; k < kSums; ++k)
+                    if (half + kQgEpiHalves * k < nch) put(half + kQgEpiHalves * k, sum[NP == 2 ? k : 0]);
             }
         }
     } else {
         // ------------------------------ conversion ------------------------------
         const int cw = warp - kQgConv0, q = warp & 3, grp = cw >> 2;
-        QgRing g, r;
-        int mine = grp;  // tiles until this group's next one
+        QgRing g, r;  // of the raw stage's first tile; of raw stages
+        int count = 0;  // tiles before this raw stage
         bool ok = true;
         for (int u = blockIdx.x; u < units && ok; u += gridDim.x) {
             const QgUnit un = place(u);
@@ -447,23 +497,23 @@ __global__ void __launch_bounds__(kQgThreads, 1) q4g_gemm_kernel(const __grid_co
                 m[hh][0] = __frcp_rn(__ldg(is));
                 m[hh][1] = __frcp_rn(__ldg(is + 8));
             }
-            for (int j = 0; j < p.kt && ok; j += 4) {
-                const int rs = r.s;
-                if (!(ok = mbar_wait(smem_u32(&r_full[rs]), r.ph, flags, p.err))) break;
+            for (int j = un.j0; j < un.j1; j += 4) {
+                const int rs = r.s, n = min(4, un.j1 - j);
+                if (!(ok = qg_wait(smem_u32(&r_full[rs]), r.ph, flags, p.err))) break;
                 r.next(p.nraw);
-                const int n = min(4, p.kt - j);
-                for (int i = 0; i < n; ++i, mine ^= 1) {
-                    const int s = g.s;
-                    const uint32_t ph = g.ph;
-                    g.next(p.nstage);
-                    if (mine) continue;
+                // The groups take tiles in turn, whatever a unit's number of them: a group that waits
+                // for the release of tile t - nstage has waited for t - groups - nstage, so that with
+                // nstage >= groups the stage's barrier is at most one phase behind the wait's parity.
+                for (int i = (grp - count) & (kQgGroups - 1); i < n; i += kQgGroups) {
+                    QgRing at = g;
+                    at.skip(i, p.nstage);
                     uint32_t hi[16], lo[16];
                     const uint8_t* seg = raw(rs) + 2 * q * 2 * seg_bytes + (i >> 1) * seg_bytes;
                     qg_convert<NP, NG>(seg, i & 1, lane, m[0][0], m[0][1], hi, lo);
-                    if (!(ok = mbar_wait(smem_u32(&empty[s]), ph ^ 1u, flags, p.err))) break;
+                    if (!(ok = qg_wait(smem_u32(&empty[at.s]), at.ph ^ 1u, flags, p.err))) break;
                     tc_fence_after();
                     __syncwarp();
-                    const uint32_t col = tmem + ((uint32_t)(32 * q) << 16) + (uint32_t)(kQgWCol0 + 32 * NP * s);
+                    const uint32_t col = tmem + ((uint32_t)(32 * q) << 16) + (uint32_t)(2 * p.accw + 32 * NP * at.s);
                     tc_st_frag(col, hi);
                     if (NP == 2) tc_st_frag(col + 32, lo);
                     qg_convert<NP, NG>(seg + 2 * seg_bytes, i & 1, lane, m[1][0], m[1][1], hi, lo);
@@ -472,8 +522,11 @@ __global__ void __launch_bounds__(kQgThreads, 1) q4g_gemm_kernel(const __grid_co
                     asm volatile("tcgen05.wait::st.sync.aligned;" ::: "memory");
                     tc_fence_before();
                     __syncwarp();
-                    if (lane == 0) mbar_arrive(smem_u32(&full[s]));
+                    if (lane == 0) mbar_arrive(smem_u32(&full[at.s]));
                 }
+                if (!ok) break;
+                g.skip(n, p.nstage);
+                count += n;
                 __syncwarp();
                 if (lane == 0) mbar_arrive(smem_u32(&r_empty[rs]));
             }

@@ -58,7 +58,7 @@ cudaError_t launch_q4g_rows(const QgRowsPlan& pl, const QgCall& c, void* ws, int
 struct QgGemmPlan {
     bool ok = false;
     int np = 0;            // pieces per operand: 1, or 2 (f32 activations: hi and lo)
-    int bx = 0, box = 0, nacc = 0, mtiles = 0, ntiles = 0, nraw = 0, nstage = 0, grid = 0;
+    int bx = 0, box = 0, accw = 0, mtiles = 0, ntiles = 0, nraw = 0, nstage = 0, grid = 0, ks = 0;
     int prep = 0;          // activations go through the preparation launch (f32, bf16)
     size_t smem = 0, ws_x = 0, ws_xs = 0, ws_part = 0, workspace = 0;
 };
@@ -67,6 +67,9 @@ cudaError_t launch_q4g_gemm(const QgGemmPlan& pl, const QgCall& c, void* ws, uns
 
 // y [T, N] = sum_j weight[t][j] part[t top_k + j], in the order of j
 cudaError_t launch_q4g_combine(const float* part, const QgRoute& r, int E, int N, void* y, int xt, cudaStream_t s);
+
+// y [n] = the sum of ks slices of part [ks][n], in order
+cudaError_t launch_q4g_sum(const float* part, int ks, long long n, void* y, int xt, cudaStream_t s);
 
 struct RouteCall {
     const void* logits;

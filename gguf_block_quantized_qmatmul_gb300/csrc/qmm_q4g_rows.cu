@@ -1,5 +1,7 @@
 // qmm_q4g_rows.cu -- host side of the row kernel (its plan), and the kernel
 // that adds the experts' partial rows of a token.
+#include <cmath>
+
 #include "qmm_q4g_rows.cuh"
 
 namespace qmm {
@@ -10,25 +12,76 @@ cudaError_t launch_q4g_rows_4(const QgRowsPlan& pl, const QgRowsParams& p, int s
 
 namespace {
 
+// Bound by the partial rows' bytes (4 top_k a value): eight independent loads a
+// thread, V values wide.  Skipped slots have weight 0 and are not read.
+template <int V>
 __global__ void __launch_bounds__(256) q4g_combine_kernel(const float* __restrict__ part, QgRoute r, int E, int N, void* y, int xt) {
     grid_dep_launch();
     grid_dep_wait();
     const int t = blockIdx.x;
-    const int n = blockIdx.y * 256 + threadIdx.x;
+    const int n = (blockIdx.y * 256 + threadIdx.x) * V;
     if (n >= N) return;
-    float v = 0.0f;
-    for (int j = 0; j < r.top_k; ++j) {
-        const long long slot = (long long)t * r.top_k + j;
-        const int e = __ldg(r.ids + slot);
-        if (e >= 0 && e < E) v = fmaf(__ldg(r.weights + slot), __ldcg(part + slot * N + n), v);
+    float v[V];
+#pragma unroll
+    for (int i = 0; i < V; ++i) v[i] = 0.0f;
+    for (int j0 = 0; j0 < r.top_k; j0 += 8) {
+        float wt[8], u[8][V];
+#pragma unroll
+        for (int j = 0; j < 8; ++j) {
+            const long long slot = (long long)t * r.top_k + j0 + j;
+            bool on = j0 + j < r.top_k;
+            if (on) {
+                const int e = __ldg(r.ids + slot);
+                on = e >= 0 && e < E;
+            }
+            wt[j] = on ? __ldg(r.weights + slot) : 0.0f;
+            if (V == 4) {
+                const float4 f = on ? __ldcg(reinterpret_cast<const float4*>(part + slot * N + n)) : make_float4(0.f, 0.f, 0.f, 0.f);
+                u[j][0] = f.x;
+                u[j][1 % V] = f.y;
+                u[j][2 % V] = f.z;
+                u[j][3 % V] = f.w;
+            } else {
+                u[j][0] = on ? __ldcg(part + slot * N + n) : 0.0f;
+            }
+        }
+#pragma unroll
+        for (int j = 0; j < 8; ++j)
+#pragma unroll
+            for (int i = 0; i < V; ++i) v[i] = fmaf(wt[j], u[j][i], v[i]);
     }
-    x_store(y, xt, (long long)t * N + n, v);
+#pragma unroll
+    for (int i = 0; i < V; ++i) x_store(y, xt, (long long)t * N + n + i, v[i]);
+}
+
+// four loads in flight a thread
+__global__ void __launch_bounds__(256) q4g_sum_kernel(const float* __restrict__ part, int ks, long long n, void* y, int xt) {
+    grid_dep_launch();
+    grid_dep_wait();
+    const long long i = (long long)blockIdx.x * 256 + threadIdx.x;
+    if (i >= n) return;
+    float v = 0.0f;
+    for (int s0 = 0; s0 < ks; s0 += 4) {
+        float u[4];
+#pragma unroll
+        for (int s = 0; s < 4; ++s) u[s] = s0 + s < ks ? __ldcg(part + (s0 + s) * n + i) : 0.0f;
+#pragma unroll
+        for (int s = 0; s < 4; ++s) v += u[s];
+    }
+    x_store(y, xt, i, v);
 }
 
 }  // namespace
 
+cudaError_t launch_q4g_sum(const float* part, int ks, long long n, void* y, int xt, cudaStream_t s) {
+    return launch_pdl(q4g_sum_kernel, (unsigned)((n + 255) / 256), 256, 0, s, part, ks, n, y, xt);
+}
+
 cudaError_t launch_q4g_combine(const float* part, const QgRoute& r, int E, int N, void* y, int xt, cudaStream_t s) {
-    return launch_pdl_2d(q4g_combine_kernel, (unsigned)r.T, (unsigned)((N + 255) / 256), 256, 0, s, part, r, E, N, y, xt);
+    const int V = N % 4 == 0 ? 4 : 1;  // rows that start on 16 bytes
+    const unsigned gy = (unsigned)((N / V + 255) / 256);
+    return V == 4 ? launch_pdl_2d(q4g_combine_kernel<4>, (unsigned)r.T, gy, 256, 0, s, part, r, E, N, y, xt)
+                  : launch_pdl_2d(q4g_combine_kernel<1>, (unsigned)r.T, gy, 256, 0, s, part, r, E, N, y, xt);
 }
 
 QgRowsPlan plan_q4g_rows(const QgCall& c, int sms, int smem_max) {
@@ -64,7 +117,9 @@ QgRowsPlan plan_q4g_rows(const QgCall& c, int sms, int smem_max) {
         // an expert's last item may be partial: at most E + slots / cols items
         const long long most = c.w.E + slots / pl.cols;
         pl.gy = (int)(most < slots ? most : slots);
-        items = slots < c.w.E ? slots : c.w.E;
+        // the experts that some slot chose, under even routing
+        items = (long long)(c.w.E * (1.0 - pow(1.0 - 1.0 / c.w.E, (double)slots)) + 0.999);
+        if (items < 1) items = 1;
     }
     if (pl.gy > 65535) return pl;
     pl.nb = nb_of(pl.cols);
@@ -76,7 +131,8 @@ QgRowsPlan plan_q4g_rows(const QgCall& c, int sms, int smem_max) {
     double best = 0;
     for (int wk = 1; wk <= pl.warps; wk *= 2) {
         const int wr = pl.warps / wk, groups = (c.w.RB + wr - 1) / wr, nit = (VS + wk - 1) / wk;
-        long long most = (long long)resident * sms / items;
+        // by expert, items differ in their rows: twice the blocks even that out
+        long long most = (long long)resident * sms * (c.op == P_DENSE || pl.by_slot ? 1 : 2) / items;
         if (most < 1) most = 1;
         const int gx = groups < most ? groups : (int)most;
         // segments a warp takes in turn, and per row block a barrier that costs about one more
@@ -87,7 +143,7 @@ QgRowsPlan plan_q4g_rows(const QgCall& c, int sms, int smem_max) {
             pl.gx = gx;
         }
     }
-    pl.smem = (size_t)xb + (size_t)red(pl.nb, pl.warps);
+    pl.smem = (size_t)xb + 16 + (size_t)red(pl.nb, pl.warps);
     if (c.op == P_DOWN && !pl.by_slot) pl.workspace = (size_t)slots * c.w.N * 4;
     pl.ok = true;
     return pl;

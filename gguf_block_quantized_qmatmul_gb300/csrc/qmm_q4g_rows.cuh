@@ -34,12 +34,19 @@ struct QgRowsParams {
     int by_slot, cols, np, wk, off_red;
 };
 
-template <bool BF>
+// FIRST: d = A B, else d += A B
+template <bool BF, bool FIRST>
 __device__ __forceinline__ void qg_mma(float d[4], const uint32_t a[4], uint32_t b0, uint32_t b1) {
-    if (BF)
+    if (BF && FIRST)
+        asm("mma.sync.aligned.m16n8k16.row.col.f32.bf16.bf16.f32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, {%8,%9}, {%10,%10,%10,%10};"
+            : "=f"(d[0]), "=f"(d[1]), "=f"(d[2]), "=f"(d[3])
+            : "r"(a[0]), "r"(a[1]), "r"(a[2]), "r"(a[3]), "r"(b0), "r"(b1), "f"(0.0f));
+    else if (BF)
         asm("mma.sync.aligned.m16n8k16.row.col.f32.bf16.bf16.f32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, {%8,%9}, {%0,%1,%2,%3};"
             : "+f"(d[0]), "+f"(d[1]), "+f"(d[2]), "+f"(d[3])
             : "r"(a[0]), "r"(a[1]), "r"(a[2]), "r"(a[3]), "r"(b0), "r"(b1));
+    else if (FIRST)
+        mma_f16_z(d, a[0], a[1], a[2], a[3], b0, b1);
     else
         mma_f16(d, a[0], a[1], a[2], a[3], b0, b1);
 }
@@ -154,72 +161,85 @@ __device__ __forceinline__ void qg_stage(uint8_t* sm, const void* x, int xt, lon
 
 constexpr int kQgMaxK = 32;  // slots of one token, at most
 
-template <int NB, bool BF, int NG>
+// TOK: P_DOWN with a token per item, whose experts' segments are taken end to end.
+template <int NB, bool BF, int NG, bool TOK>
 __global__ void __launch_bounds__(512) q4g_rows_kernel(const QgRowsParams p) {
     extern __shared__ __align__(16) uint8_t sm[];
-    __shared__ int s_e[kQgMaxK];      // the item's experts (-1: none), one but for a token's item
-    __shared__ float s_wt[kQgMaxK];   // their weights (a token's item)
-    __shared__ int s_row[64];         // by expert: the columns' slots
-    __shared__ int s_item[3];         // by expert: expert, first position, columns
+    __shared__ int s_e[kQgMaxK];       // TOK: the token's experts (-1: skipped)
+    __shared__ float s_wt[kQgMaxK];    // and their weights
+    __shared__ int s_row[64];          // by expert: the columns' slots
+    __shared__ int s_item[3];          // expert, first position, columns
     const QgCall& c = p.c;
     const QgWeights& w = c.w;
     const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31, g = lane >> 2, t = lane & 3, nthr = blockDim.x;
     const int wk = p.wk, wr = nthr / 32 / wk, kw = warp % wk, rw = warp / wk;
-    const int seg_bytes = qg_seg_bytes(NG);
-    constexpr int segk = 128 / NG;
+    constexpr int seg_bytes = qg_seg_bytes(NG), segk = 128 / NG;
     // this block's row blocks
     const int rb0 = (int)((long long)blockIdx.x * w.RB / gridDim.x), rb1 = (int)((long long)(blockIdx.x + 1) * w.RB / gridDim.x);
-    const bool token = c.op == P_DOWN && p.by_slot;
-    const int nex = token ? c.r.top_k : 1;
-    const int VS = nex * w.KS;                        // virtual segments: the item's experts end to end
+    const int nex = TOK ? c.r.top_k : 1;
+    const int VS = nex * w.KS;                        // virtual segments
     const int nit = (VS + wk - 1) / wk;               // segments per warp and row block
     const int total = ((rb1 - rb0) + wr - 1) / wr * nit;
 
     grid_dep_launch();
     QgSeg<NG> st[kQgDepth];
-    // load cursor: iteration li of row block rb0 + lr wr + rw
-    int li = 0, lr = 0;
-    const uint8_t* base0 = w.data;
+    // load cursor: segment lv of row block lrb, at lp (TOK: expert lj, its segment lseg)
+    int li = 0, lv = kw, lrb = rb0 + rw, lj = 0, lseg = kw;
+    const long long row_bytes = (long long)w.KS * seg_bytes;
+    const uint8_t* base = w.data;
+    const uint8_t* lp = nullptr;
+    auto load_start = [&]() { lp = base + lrb * row_bytes + kw * seg_bytes; };
     auto load = [&](int d) {
-        const int rb = rb0 + lr * wr + rw, v = li * wk + kw;
-        if (rb < rb1 && v < VS) {
-            const uint8_t* b = base0;
-            int seg = v;
-            if (token) {
-                const int j = v / w.KS;
-                seg = v - j * w.KS;
-                b = w.data + (long long)max(s_e[j], 0) * w.expert_stride;
+        if (lrb < rb1 && lv < VS) {
+            if (TOK) {
+                while (lseg >= w.KS) {
+                    lseg -= w.KS;
+                    ++lj;
+                }
+                lp = w.data + (long long)max(s_e[lj], 0) * w.expert_stride + lrb * row_bytes + lseg * seg_bytes;
             }
-            qg_load<NG>(st[d], b + ((long long)rb * w.KS + seg) * seg_bytes, lane);
+            qg_load<NG>(st[d], lp, lane);
         }
+        lv += wk;
+        if (TOK) lseg += wk;
+        else lp += wk * seg_bytes;
         if (++li == nit) {
             li = 0;
-            ++lr;
+            lv = kw;
+            lrb += wr;
+            if (TOK) {
+                lj = 0;
+                lseg = kw;
+            } else {
+                lp += wr * row_bytes - nit * wk * seg_bytes;
+            }
         }
     };
     if (c.op == P_DENSE) {
+        load_start();
 #pragma unroll
         for (int d = 0; d < kQgDepth; ++d)
             if (d < total) load(d);
     }
+    if (tid == 0) *reinterpret_cast<uint4*>(sm + p.off_red - 16) = make_uint4(0u, 0u, 0u, 0u);  // what lanes without a column read
     grid_dep_wait();
 
     // the item: its experts and columns
     int rows = 1;
-    if (c.op == P_DENSE) {
-        rows = min(p.cols, c.M - (int)blockIdx.y * p.cols);
-    } else if (p.by_slot) {
+    if (TOK) {
         if (tid < nex) {
             const int slot = (int)blockIdx.y * nex + tid;
             const int e = c.r.ids[slot];
             s_e[tid] = e >= 0 && e < w.E ? e : -1;
-            s_wt[tid] = token ? c.r.weights[slot] : 1.0f;
+            s_wt[tid] = c.r.weights[slot];
         }
         __syncthreads();
-        if (!token) {
-            if (s_e[0] < 0) return;
-            base0 = w.data + (long long)s_e[0] * w.expert_stride;
-        }
+    } else if (c.op == P_DENSE) {
+        rows = min(p.cols, c.M - (int)blockIdx.y * p.cols);
+    } else if (p.by_slot) {
+        const int e = c.r.ids[blockIdx.y];
+        if (e < 0 || e >= w.E) return;
+        base = w.data + e * w.expert_stride;
     } else {
         if (warp == 0) {
             // expert e has ceil(count / cols) items; lane l takes experts l per.. l per + per
@@ -254,21 +274,22 @@ __global__ void __launch_bounds__(512) q4g_rows_kernel(const QgRowsParams p) {
         __syncthreads();
         if (s_item[0] < 0) return;
         rows = s_item[2];
-        base0 = w.data + (long long)s_item[0] * w.expert_stride;
+        base = w.data + s_item[0] * w.expert_stride;
         if (tid < rows) {
             const int slot = c.r.order[s_item[1] + tid];
             s_row[tid] = slot >= 0 && slot < c.r.T * c.r.top_k ? slot : 0;
         }
-        __syncthreads();
     }
     if (c.op != P_DENSE) {
+        load_start();
 #pragma unroll
         for (int d = 0; d < kQgDepth; ++d)
             if (d < total) load(d);
+        if (!p.by_slot) __syncthreads();  // the slots
     }
     // activations
     const int ncol = rows * p.np;
-    if (token) {
+    if (TOK) {
         for (int j = 0; j < nex; ++j)
             qg_stage(sm, c.x, c.xt, ((long long)blockIdx.y * nex + j) * c.ldx, w.K, w.KS, ncol, j * w.KS, 0, tid, nthr);
     } else {
@@ -282,28 +303,39 @@ __global__ void __launch_bounds__(512) q4g_rows_kernel(const QgRowsParams p) {
     }
     __syncthreads();
 
-    float acc[NB][4], gr[NB][4];
+    float acc[NB][4];
 #pragma unroll
     for (int b = 0; b < NB; ++b)
 #pragma unroll
-        for (int i = 0; i < 4; ++i) acc[b][i] = gr[b][i] = 0.0f;
+        for (int i = 0; i < 4; ++i) acc[b][i] = 0.0f;
     float* red = reinterpret_cast<float*>(sm + p.off_red);
     constexpr int kRed = NB * 128;  // sums of a warp: [column][16 rows]
-    int ci = 0, cr = 0;             // compute cursor
+    // compute cursor; this lane's columns (8 b + g) at offset xp, xq bytes from 32 K to the next (0: it has no column)
+    int ci = 0, cr = 0, cv = kw, crb = rb0 + rw, cj = 0, cseg = kw;
+    int xp[NB], xq[NB];
+#pragma unroll
+    for (int b = 0; b < NB; ++b) {
+        const bool on = 8 * b + g < ncol;
+        xq[b] = on ? ncol * 64 : 0;
+        xp[b] = on ? kw * 4 * xq[b] + (8 * b + g) * 64 + t * 16 : p.off_red - 16;
+    }
     for (int it = 0; it < total; it += kQgDepth) {
 #pragma unroll
         for (int d = 0; d < kQgDepth; ++d) {
             if (it + d >= total) break;
-            const int rb = rb0 + cr * wr + rw, v = ci * wk + kw;
-            if (rb < rb1 && v < VS) {
+            if (crb < rb1 && cv < VS) {
                 float wt = 1.0f;
                 bool on = true;
-                if (token) {
-                    const int j = v / w.KS;
-                    on = s_e[j] >= 0;
-                    wt = s_wt[j];
+                if (TOK) {
+                    while (cseg >= w.KS) {
+                        cseg -= w.KS;
+                        ++cj;
+                    }
+                    on = s_e[cj] >= 0;
+                    wt = s_wt[cj];
                 }
                 if (on) {
+                    float gr[NB][4];
 #pragma unroll
                     for (int q4 = 0; q4 < 4; ++q4) {  // 32 K a step
                         const int gi = q4 * 32 / segk;
@@ -313,29 +345,32 @@ __global__ void __launch_bounds__(512) q4g_rows_kernel(const QgRowsParams p) {
                         uint32_t a0[4], a1[4];
                         qg_codes<BF>(q4 & 1 ? cw.z : cw.x, zl, zh, a0);
                         qg_codes<BF>(q4 & 1 ? cw.w : cw.y, zl, zh, a1);
-                        const uint8_t* xs = sm + (size_t)(v * 4 + q4) * ncol * 64 + t * 16;
+                        const bool first = q4 * 32 % segk == 0;
 #pragma unroll
                         for (int b = 0; b < NB; ++b) {
-                            uint4 xv = make_uint4(0u, 0u, 0u, 0u);
-                            if (8 * b + g < ncol) xv = *reinterpret_cast<const uint4*>(xs + (8 * b + g) * 64);
-                            qg_mma<BF>(gr[b], a0, xv.x, xv.y);
-                            qg_mma<BF>(gr[b], a1, xv.z, xv.w);
+                            const uint4 xv = *reinterpret_cast<const uint4*>(sm + xp[b] + q4 * xq[b]);
+                            if (first) qg_mma<BF, true>(gr[b], a0, xv.x, xv.y);
+                            else qg_mma<BF, false>(gr[b], a0, xv.x, xv.y);
+                            qg_mma<BF, false>(gr[b], a1, xv.z, xv.w);
                         }
                         if ((q4 + 1) * 32 % segk == 0) {  // the group's end
-                            const float s0 = qg_scale(sw0) * wt, s1 = qg_scale(sw1) * wt;
+                            const float s0 = TOK ? qg_scale(sw0) * wt : qg_scale(sw0), s1 = TOK ? qg_scale(sw1) * wt : qg_scale(sw1);
 #pragma unroll
                             for (int b = 0; b < NB; ++b) {
                                 acc[b][0] = fmaf(s0, gr[b][0], acc[b][0]);
                                 acc[b][1] = fmaf(s0, gr[b][1], acc[b][1]);
                                 acc[b][2] = fmaf(s1, gr[b][2], acc[b][2]);
                                 acc[b][3] = fmaf(s1, gr[b][3], acc[b][3]);
-                                gr[b][0] = gr[b][1] = gr[b][2] = gr[b][3] = 0.0f;
                             }
                         }
                     }
                 }
             }
             if (it + d + kQgDepth < total) load(d);
+            cv += wk;
+            if (TOK) cseg += wk;
+#pragma unroll
+            for (int b = 0; b < NB; ++b) xp[b] += wk * 4 * xq[b];
             if (++ci == nit) {  // the row block's sums
                 float* mine = red + ((cr & 1) * (nthr / 32) + warp) * kRed;
 #pragma unroll
@@ -350,33 +385,36 @@ __global__ void __launch_bounds__(512) q4g_rows_kernel(const QgRowsParams p) {
                         mine[(col + 1) * 16 + g + 8] = acc[b][3];
                     }
                     acc[b][0] = acc[b][1] = acc[b][2] = acc[b][3] = 0.0f;
+                    xp[b] -= nit * wk * 4 * xq[b];
                 }
                 __syncthreads();
-                if (rb < rb1) {
+                if (crb < rb1) {
                     const float* from = red + ((cr & 1) * (nthr / 32) + rw * wk) * kRed;
                     const int per = w.paired ? 8 : 16;
                     auto sum = [&](int r, int row) {
                         float v2 = 0.0f;
                         for (int pc = 0; pc < p.np; ++pc) {
                             const float* f = from + (r * p.np + pc) * 16 + row;
+#pragma unroll 4
                             for (int k2 = 0; k2 < wk; ++k2) v2 += f[k2 * kRed];
                         }
                         return v2;
                     };
-                    for (int o = kw * 32 + lane; o < per * rows; o += wk * 32) {
+                    // the warps take turns at a short row block's sums
+                    for (int o = ((kw + cr) & (wk - 1)) * 32 + lane; o < per * rows; o += wk * 32) {
                         const int row = o % per, r = o / per;
                         const float v0 = sum(r, row);
                         if (c.op == P_GATE_UP) {
                             const float u = sum(r, row + 8);
-                            const int f = rb * 8 + row, F = w.N / 2;
+                            const int f = crb * 8 + row, F = w.N / 2;
                             const long long slot = p.by_slot ? (long long)blockIdx.y : (long long)s_row[r];
                             if (f < F) x_store(c.y, c.xt, slot * F + f, swiglu(v0, u));
                         } else {
-                            const int n = rb * 16 + row;
+                            const int n = crb * 16 + row;
                             if (n < w.N) {
                                 if (c.op == P_DENSE)
                                     x_store(c.y, c.xt, ((long long)blockIdx.y * p.cols + r) * w.N + n, v0);
-                                else if (token)
+                                else if (TOK)
                                     x_store(c.y, c.xt, (long long)blockIdx.y * w.N + n, v0);
                                 else
                                     p.part[(long long)s_row[r] * w.N + n] = v0;
@@ -386,6 +424,12 @@ __global__ void __launch_bounds__(512) q4g_rows_kernel(const QgRowsParams p) {
                 }
                 ci = 0;
                 ++cr;
+                cv = kw;
+                crb += wr;
+                if (TOK) {
+                    cj = 0;
+                    cseg = kw;
+                }
             }
         }
     }
