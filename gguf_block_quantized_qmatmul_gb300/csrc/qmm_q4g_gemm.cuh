@@ -117,42 +117,6 @@ __device__ __forceinline__ void qg_convert(const uint8_t* seg, int h, int lane, 
     }
 }
 
-// Bounded wait whose tries suspend the warp (for up to 2 us each) instead of
-// returning at once: 20 waiting warps that spin take a third of the issue slots
-// that the converting ones need.
-__device__ __forceinline__ bool qg_wait(uint32_t bar, uint32_t parity, volatile int* abort_flag, unsigned* err) {
-    if (mbar_try(bar, parity)) return true;
-    const long long t0 = clock64();
-    while (true) {
-        uint32_t ok;
-        asm volatile(
-            "{\n\t.reg .pred p;\n\tmbarrier.try_wait.parity.shared::cta.b64 p, [%1], %2, %3;\n\tselp.u32 %0, 1, 0, p;\n\t}"
-            : "=r"(ok)
-            : "r"(bar), "r"(parity), "r"(2000u)
-            : "memory");
-        if (ok) return true;
-        if (*abort_flag) return false;
-        if (clock64() - t0 > kWaitLimitCheck) return mbar_spin(bar, parity, abort_flag, err, false);  // raises the error in the end
-    }
-}
-
-// A place in a ring of n stages: its index and the parity of its current use.
-// A producer waits for a stage's release with ph ^ 1, which a fresh barrier
-// passes.  (Counting uses and dividing by a run-time n costs the MMA thread
-// more than its four MMAs.)
-struct QgRing {
-    int s = 0;
-    uint32_t ph = 0;
-    __device__ __forceinline__ void next(int n) {
-        if (++s == n) {
-            s = 0;
-            ph ^= 1u;
-        }
-    }
-    __device__ __forceinline__ void skip(int k, int n) {
-        for (s += k; s >= n; s -= n) ph ^= 1u;
-    }
-};
 // After the last use: waits for the copies of every stage still in flight.
 __device__ __forceinline__ void qg_drain(const QgRing& r, bool wrapped, int n, uint64_t* bars, volatile int* flags, unsigned* err) {
     for (int q = 0; q < n; ++q)

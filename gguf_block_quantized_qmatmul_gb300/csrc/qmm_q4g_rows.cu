@@ -87,77 +87,99 @@ cudaError_t launch_q4g_combine(const float* part, const QgRoute& r, int E, int N
 QgRowsPlan plan_q4g_rows(const QgCall& c, int sms, int smem_max) {
     QgRowsPlan pl;
     pl.np = c.xt == X_F32 ? 3 : 1;
+    if (c.op != P_DENSE && c.w.E > kQgRowMaxE) return pl;
     const long long row_bytes = (long long)pl.np * c.w.KS * kQgSegK * 2;  // staged bytes of one activation row
     const int max_cols = 32 / pl.np;
     const long long slots = c.M;
-    long long items = 1;
     if (c.op == P_DENSE) {
         pl.cols = c.M < max_cols ? c.M : max_cols;
     } else {
-        // one slot (one token) a block while few slots share an expert: no plan to search, and no
-        // partial sums; by expert, a block serves up to `cols` of its slots with one weight stream
+        // one slot (one token) an item while few slots share an expert: no items to look up, and no
+        // partial sums; by expert, an item is up to `cols` of its slots with one weight stream
         pl.by_slot = c.r.T <= 4 && c.r.top_k <= kQgMaxK && (c.op == P_GATE_UP || row_bytes * c.r.top_k <= 96 * 1024);
         const long long avg = (slots + c.w.E - 1) / c.w.E;
         pl.cols = pl.by_slot ? 1 : avg * pl.np <= 4 ? (8 / pl.np) : avg * pl.np <= 8 ? 16 / pl.np : max_cols;
     }
-    auto red = [&](int nb, int warps) { return 2ll * warps * nb * 128 * 4; };
+    const bool token = c.op == P_DOWN && pl.by_slot;
+    const long long rows_mul = token ? c.r.top_k : 1;
+    const int seg = qg_seg_bytes(c.w.ng), VS = (int)(c.w.KS * rows_mul);
     auto nb_of = [&](int cols) { const int b = (cols * pl.np + 7) / 8; return b <= 1 ? 1 : b <= 2 ? 2 : 4; };
-    const long long rows_mul = c.op == P_DOWN && pl.by_slot ? c.r.top_k : 1;
-    // as many columns as shared memory holds
-    while (pl.cols > 1 && pl.cols * row_bytes + red(nb_of(pl.cols), 16) > smem_max - 2048) --pl.cols;
-    if (pl.cols * row_bytes * rows_mul + red(nb_of(pl.cols), 16) > smem_max - 2048) return pl;
+    auto red = [&](int nb, int warps) { return 2ll * warps * nb * 128 * 4; };
+    // shared memory: activations, the warps' sums, rings of `depth` units and their barriers
+    auto need = [&](int cols, int warps, int useg, int depth) {
+        return cols * row_bytes * rows_mul + 16 + red(nb_of(cols), warps) + (long long)warps * depth * (useg * seg + 8);
+    };
+    const long long room = smem_max - kQgRowStatic - 1024;
+    // as many columns as shared memory holds beside two single segments a warp
+    while (pl.cols > 1 && need(pl.cols, 8, 1, 2) > room) --pl.cols;
+    if (need(pl.cols, 8, 1, 2) > room) return pl;
+    long long items, most = 0;  // items expected, and at most
     if (c.op == P_DENSE) {
         items = (c.M + pl.cols - 1) / pl.cols;
         pl.cols = (int)((c.M + items - 1) / items);
-        pl.gy = (int)items;
     } else if (pl.by_slot) {
-        pl.gy = c.op == P_GATE_UP ? (int)slots : c.r.T;
-        items = pl.gy;
+        items = c.op == P_GATE_UP ? slots : c.r.T;
     } else {
-        // an expert's last item may be partial: at most E + slots / cols items
-        const long long most = c.w.E + slots / pl.cols;
-        pl.gy = (int)(most < slots ? most : slots);
-        // the experts that some slot chose, under even routing
-        items = (long long)(c.w.E * (1.0 - pow(1.0 - 1.0 / c.w.E, (double)slots)) + 0.999);
-        if (items < 1) items = 1;
+        // the experts that some slot chose, under even routing; an expert's last item may be partial
+        items = (long long)(c.w.E * (1.0 - pow(1.0 - 1.0 / c.w.E, (double)slots)) + 0.999) + slots / pl.cols;
+        most = c.w.E + slots / pl.cols;
+        if (items > most) items = most;
+        if (items > slots) items = slots;
     }
-    if (pl.gy > 65535) return pl;
+    if (items < 1) items = 1;
     pl.nb = nb_of(pl.cols);
-    const long long xb = pl.cols * row_bytes * rows_mul;
-    // two blocks of 8 warps an SM, or one of 16 where the activations take more than half its shared memory
-    pl.warps = xb + red(pl.nb, 8) <= (smem_max - 4096) / 2 ? 8 : 16;
-    const int resident = pl.warps == 8 ? 2 : 1;
-    const int VS = (int)(c.w.KS * rows_mul);
     double best = 0;
-    for (int wk = 1; wk <= pl.warps; wk *= 2) {
-        const int wr = pl.warps / wk, groups = (c.w.RB + wr - 1) / wr, nit = (VS + wk - 1) / wk;
-        // by expert, items differ in their rows: twice the blocks even that out
-        long long most = (long long)resident * sms * (c.op == P_DENSE || pl.by_slot ? 1 : 2) / items;
-        if (most < 1) most = 1;
-        const int gx = groups < most ? groups : (int)most;
-        // segments a warp takes in turn, and per row block a barrier that costs about one more
-        const double cost = (double)((groups + gx - 1) / gx) * (nit + 1.0);
-        if (wk == 1 || cost <= best) {
-            best = cost;
-            pl.wk = wk;
-            pl.gx = gx;
+    for (int warps : {24, 16, 8}) {
+        if (warps > qg_row_warps(pl.nb)) continue;
+        int useg = token ? 1 : 2, depth = kQgDepthMax;
+        while (depth > 2 && need(pl.cols, warps, useg, depth) > room) --depth;
+        if (need(pl.cols, warps, useg, depth) > room) useg = 1;
+        while (useg == 1 && depth > 2 && need(pl.cols, warps, useg, depth) > room) --depth;
+        if (need(pl.cols, warps, useg, depth) > room) continue;
+        for (int wk = 1; wk <= 8; wk *= 2) {
+            const int us = useg == 2 && (VS + 2 * wk - 1) / (2 * wk) * 2 > (VS + wk - 1) / wk ? 1 : useg;
+            const int wr = warps / wk, nit = (VS + wk * us - 1) / (wk * us);
+            if (wr > 15 && wk > 1) continue;  // named barriers
+            const long long work = items * c.w.RB, blocks = work < sms ? work : sms;
+            const double share = (double)work / blocks;  // row blocks per block
+            // segments a warp takes in turn, its row blocks' barriers and sums (about one each); more warps share an SM's issue slots
+            const double cost = ceil(share / wr) * (nit * us + 1.0) * (warps >= 16 ? warps / 16.0 : 1.0);
+            if (best == 0 || cost < 0.999 * best || (cost <= 1.001 * best && wk > pl.wk)) {
+                best = cost;
+                pl.warps = warps;
+                pl.wk = wk;
+                pl.useg = us;
+                pl.depth = depth;
+                pl.blocks = (int)blocks;
+            }
         }
     }
-    pl.smem = (size_t)xb + 16 + (size_t)red(pl.nb, pl.warps);
+    if (best == 0) return pl;
+    pl.smem = (size_t)need(pl.cols, pl.warps, pl.useg, pl.depth);
+    pl.off_zero = (int)(pl.cols * row_bytes * rows_mul);
+    pl.off_red = pl.off_zero + 16;
+    pl.off_ring = pl.off_red + (int)red(pl.nb, pl.warps);
+    pl.off_bar = pl.off_ring + pl.warps * pl.depth * pl.useg * seg;
     if (c.op == P_DOWN && !pl.by_slot) pl.workspace = (size_t)slots * c.w.N * 4;
     pl.ok = true;
     return pl;
 }
 
-cudaError_t launch_q4g_rows(const QgRowsPlan& pl, const QgCall& c, void* ws, int smem_max, cudaStream_t s) {
+cudaError_t launch_q4g_rows(const QgRowsPlan& pl, const QgCall& c, void* ws, unsigned* err, int smem_max, cudaStream_t s) {
     QgRowsParams p;
     p.c = c;
     p.part = static_cast<float*>(ws);
+    p.err = err;
     p.by_slot = pl.by_slot;
     p.cols = pl.cols;
     p.np = pl.np;
     p.wk = pl.wk;
-    p.off_red = (int)(pl.smem - 2ull * pl.warps * pl.nb * 128 * 4);
+    p.useg = pl.useg;
+    p.depth = pl.depth;
+    p.off_zero = pl.off_zero;
+    p.off_red = pl.off_red;
+    p.off_ring = pl.off_ring;
+    p.off_bar = pl.off_bar;
     cudaError_t e = pl.nb == 1   ? launch_q4g_rows_1(pl, p, smem_max, s)
                     : pl.nb == 2 ? launch_q4g_rows_2(pl, p, smem_max, s)
                                  : launch_q4g_rows_4(pl, p, smem_max, s);

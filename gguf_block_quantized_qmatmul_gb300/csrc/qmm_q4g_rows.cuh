@@ -10,28 +10,40 @@
 // truncation (exact, and no overflow), in three columns whose sums are added
 // at the end.
 //
-// The kernel is bound by the weight stream (0.5 + 4 / G bytes a weight).  A
-// warp's tile of 16 rows x 64 K is one coalesced 512-byte load straight into
-// the fragment registers (no shared memory, no shuffles): about 9 (f16) or 11
-// (bf16) instructions per word of eight codes turn it into MMA operands.
-// kQgDepth segments of 128 K per warp are in flight, across row blocks; a
-// block's warps split K (wk) and row blocks, and add their sums through
-// shared memory with one barrier per row block.  Activations are staged once
-// per block in the order the MMAs read them (16 bytes a lane, conflict-free).
-// Weights are constant, so a dense call's first loads are issued before the
-// grid it depends on has completed.
+// The kernel is bound by the weight stream (0.5 + 4 / G bytes a weight).  The
+// work, items (a group of activation rows with their weight matrix) times row
+// blocks, is dealt to one block an SM in equal contiguous shares.  Every warp
+// has its own ring of shared-memory stages, each filled by one bulk copy of a
+// unit (up to two consecutive segments of a row block) that one lane issues;
+// a tile of 16 rows x 64 K is then one conflict-free 16-byte load a lane, in
+// fragment order, and about 9 (f16) or 11 (bf16) instructions turn a word of
+// eight codes into MMA operands.  (Loads straight into registers, four segments
+// ahead, measured 44 us at 1 x 28672 x 8192: the stages' registers left 16 warps an SM, and waiting for the
+// oldest load waited for younger ones too.)  wk warps split a row block's K and
+// add their sums through shared memory, one barrier among them per row block.
+// Activations are staged once per item in the order the MMAs read them (16
+// bytes a lane, conflict-free).  Weights are constant, so a dense call's first
+// copies are issued before the grid it depends on has completed.
 #pragma once
 
 #include "qmm_q4g_internal.h"
 
 namespace qmm {
 
-constexpr int kQgDepth = 4;
+constexpr int kQgDepthMax = 4;     // stages of a warp's ring, at most
+// warps per block, at most: more columns need more registers
+__host__ __device__ constexpr int qg_row_warps(int nb) { return nb == 1 ? 24 : 16; }
+constexpr int kQgRowMaxE = 512;    // experts whose items a block can look up
+constexpr int kQgRowStatic = 4096; // the kernel's static arrays, rounded up
 
 struct QgRowsParams {
     QgCall c;
     float* part;   // P_DOWN by expert: [T top_k][N]
-    int by_slot, cols, np, wk, off_red;
+    unsigned* err;
+    int by_slot, cols, np, wk;
+    int useg;      // segments per unit
+    int depth;     // stages per warp
+    int off_zero, off_red, off_ring, off_bar;
 };
 
 // FIRST: d = A B, else d += A B
@@ -87,52 +99,39 @@ __device__ __forceinline__ uint32_t qg_zero(uint32_t sw, bool second) {
     return second ? (z * 0x00100010u) + 0xD400D400u : (z * 0x00010001u | 0x64006400u);
 }
 
-template <int NG>
-struct QgSeg {
-    uint4 c[2];
-    uint32_t sw[2 * NG];
-};
-
-template <int NG>
-__device__ __forceinline__ void qg_load(QgSeg<NG>& s, const uint8_t* p, int lane) {
-    s.c[0] = __ldg(reinterpret_cast<const uint4*>(p) + lane);
-    s.c[1] = __ldg(reinterpret_cast<const uint4*>(p + kQgTile) + lane);
-    const uint8_t* q = p + 2 * kQgTile + (lane >> 2) * (8 * NG);
-    if (NG == 1) {
-        const uint2 v = __ldg(reinterpret_cast<const uint2*>(q));
-        s.sw[0] = v.x;
-        s.sw[1] = v.y;
-    } else {
-#pragma unroll
-        for (int i = 0; i < NG / 2; ++i) {
-            const uint4 v = __ldg(reinterpret_cast<const uint4*>(q) + i);
-            s.sw[4 * i] = v.x;
-            s.sw[4 * i + 1] = v.y;
-            s.sw[4 * i + 2] = v.z;
-            s.sw[4 * i + 3] = v.w;
-        }
-    }
+// Staged activations: 32 K of a column are 64 bytes, thread t's 16 at 16 t (the
+// words of K 2 t, 8 + 2 t, 16 + 2 t, 24 + 2 t and their successors); the columns
+// of the same 32 K are next to each other, then the next 32 K.
+//
+// A quad of lanes has 32 K of a row, 8 each (words j = K 8 lane + 2 j): a 4 x 4
+// transposition among them makes each lane's four words the ones it stores.
+__device__ __forceinline__ uint4 qg_quad_transpose(uint32_t w0, uint32_t w1, uint32_t w2, uint32_t w3, int lane) {
+    const bool b0 = lane & 1, b1 = lane & 2;
+    // lanes one apart: even ones keep words 0, 2 and take the partner's 0, 2
+    uint32_t s0 = __shfl_xor_sync(0xffffffffu, b0 ? w0 : w1, 1), s1 = __shfl_xor_sync(0xffffffffu, b0 ? w2 : w3, 1);
+    uint32_t x0 = b0 ? s0 : w0, x1 = b0 ? w1 : s0, y0 = b0 ? s1 : w2, y1 = b0 ? w3 : s1;
+    // (x0, x1): word b0 of lanes 2 i, 2 i + 1; (y0, y1): word 2 + b0
+    s0 = __shfl_xor_sync(0xffffffffu, b1 ? x0 : y0, 2);
+    s1 = __shfl_xor_sync(0xffffffffu, b1 ? x1 : y1, 2);
+    return b1 ? make_uint4(s0, s1, y0, y1) : make_uint4(x0, x1, s0, s1);
 }
 
-// 16-bit words of columns in fragment order: K position k of virtual segment v
-// of column c.  Per 32 K a column has 64 bytes, thread t's 16 at 16 t.
-__device__ __forceinline__ uint32_t* qg_xword(uint8_t* sm, int ncol, int v, int col, int k) {
-    const int h = k >> 5, s = (k >> 4) & 1, hi = (k >> 3) & 1, t = (k & 7) >> 1;
-    return reinterpret_cast<uint32_t*>(sm + ((size_t)(v * 4 + h) * ncol + col) * 64 + t * 16 + (2 * s + hi) * 4);
-}
-
-// Stage one row of x as column(s) col.. of virtual segments v0..: eight values a step.
-__device__ __forceinline__ void qg_stage(uint8_t* sm, const void* x, int xt, long long at, int K, int KS, int ncol, int v0, int col,
-                                         int tid, int nthr) {
-    for (int i = tid; i < KS * (kQgSegK / 8); i += nthr) {
-        const int k = 8 * i;
+// Stage `rows` rows of x (row r at element offset at(r)) as columns of virtual segments v0..
+template <class At>
+__device__ __forceinline__ void qg_stage(uint8_t* sm, const void* x, int xt, int K, int KS, int rows, int np, int v0, At at, int tid, int nthr) {
+    const int ncol = rows * np, n = KS * 4 * rows * 4;  // quads: (32 K, row)
+    for (int i0 = 0; i0 < n; i0 += nthr) {
+        const int i = i0 + tid, j = i & 3, quad = i >> 2;
+        const int h = quad / rows, r = quad - h * rows, k = 32 * h + 8 * j;
+        const bool on = i < n && k < K;
+        uint8_t* to = sm + ((size_t)(v0 * 4 + h) * ncol + r * np) * 64 + j * 16;
         if (xt == X_F32) {
             float f[8];
 #pragma unroll
-            for (int j = 0; j < 8; ++j) f[j] = 0.0f;
-            if (k < K) {
-                const float4 a = *reinterpret_cast<const float4*>(static_cast<const float*>(x) + at + k);
-                const float4 b = *reinterpret_cast<const float4*>(static_cast<const float*>(x) + at + k + 4);
+            for (int e = 0; e < 8; ++e) f[e] = 0.0f;
+            if (on) {
+                const float4* src = reinterpret_cast<const float4*>(static_cast<const float*>(x) + at(r) + k);
+                const float4 a = src[0], b = src[1];
                 f[0] = a.x; f[1] = a.y; f[2] = a.z; f[3] = a.w;
                 f[4] = b.x; f[5] = b.y; f[6] = b.z; f[7] = b.w;
             }
@@ -140,21 +139,20 @@ __device__ __forceinline__ void qg_stage(uint8_t* sm, const void* x, int xt, lon
             for (int pc = 0; pc < 3; ++pc) {
                 uint32_t w[4];
 #pragma unroll
-                for (int j = 0; j < 8; ++j) {
-                    const uint32_t u = __float_as_uint(f[j]) & 0xffff0000u;
-                    w[j >> 1] = j & 1 ? w[j >> 1] | u : u >> 16;
+                for (int e = 0; e < 8; ++e) {
+                    const uint32_t u = __float_as_uint(f[e]) & 0xffff0000u;
+                    w[e >> 1] = e & 1 ? w[e >> 1] | u : u >> 16;
                     // the rest is exact; an infinity or NaN has none
-                    f[j] = (u & 0x7f800000u) == 0x7f800000u ? 0.0f : f[j] - __uint_as_float(u);
+                    f[e] = (u & 0x7f800000u) == 0x7f800000u ? 0.0f : f[e] - __uint_as_float(u);
                 }
-#pragma unroll
-                for (int j = 0; j < 4; ++j) *qg_xword(sm, ncol, v0 + (k >> 7), col + pc, (k & 127) + 2 * j) = w[j];
+                const uint4 q = qg_quad_transpose(w[0], w[1], w[2], w[3], j);
+                if (i < n) *reinterpret_cast<uint4*>(to + pc * 64) = q;
             }
         } else {
             uint4 u = make_uint4(0u, 0u, 0u, 0u);
-            if (k < K) u = *reinterpret_cast<const uint4*>(static_cast<const uint16_t*>(x) + at + k);
-            const uint32_t w[4] = {u.x, u.y, u.z, u.w};
-#pragma unroll
-            for (int j = 0; j < 4; ++j) *qg_xword(sm, ncol, v0 + (k >> 7), col, (k & 127) + 2 * j) = w[j];
+            if (on) u = *reinterpret_cast<const uint4*>(static_cast<const uint16_t*>(x) + at(r) + k);
+            const uint4 q = qg_quad_transpose(u.x, u.y, u.z, u.w, j);
+            if (i < n) *reinterpret_cast<uint4*>(to) = q;
         }
     }
 }
@@ -163,86 +161,42 @@ constexpr int kQgMaxK = 32;  // slots of one token, at most
 
 // TOK: P_DOWN with a token per item, whose experts' segments are taken end to end.
 template <int NB, bool BF, int NG, bool TOK>
-__global__ void __launch_bounds__(512) q4g_rows_kernel(const QgRowsParams p) {
+__global__ void __launch_bounds__(qg_row_warps(NB) * 32, 1) q4g_rows_kernel(const QgRowsParams p) {
     extern __shared__ __align__(16) uint8_t sm[];
     __shared__ int s_e[kQgMaxK];       // TOK: the token's experts (-1: skipped)
     __shared__ float s_wt[kQgMaxK];    // and their weights
     __shared__ int s_row[64];          // by expert: the columns' slots
-    __shared__ int s_item[3];          // expert, first position, columns
+    __shared__ int ts[kQgRowMaxE + 1]; // by expert: items before each
+    __shared__ int s_abort;
     const QgCall& c = p.c;
     const QgWeights& w = c.w;
     const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31, g = lane >> 2, t = lane & 3, nthr = blockDim.x;
     const int wk = p.wk, wr = nthr / 32 / wk, kw = warp % wk, rw = warp / wk;
     constexpr int seg_bytes = qg_seg_bytes(NG), segk = 128 / NG;
-    // this block's row blocks
-    const int rb0 = (int)((long long)blockIdx.x * w.RB / gridDim.x), rb1 = (int)((long long)(blockIdx.x + 1) * w.RB / gridDim.x);
-    const int nex = TOK ? c.r.top_k : 1;
-    const int VS = nex * w.KS;                        // virtual segments
-    const int nit = (VS + wk - 1) / wk;               // segments per warp and row block
-    const int total = ((rb1 - rb0) + wr - 1) / wr * nit;
-
-    grid_dep_launch();
-    QgSeg<NG> st[kQgDepth];
-    // load cursor: segment lv of row block lrb, at lp (TOK: expert lj, its segment lseg)
-    int li = 0, lv = kw, lrb = rb0 + rw, lj = 0, lseg = kw;
-    const long long row_bytes = (long long)w.KS * seg_bytes;
-    const uint8_t* base = w.data;
-    const uint8_t* lp = nullptr;
-    auto load_start = [&]() { lp = base + lrb * row_bytes + kw * seg_bytes; };
-    auto load = [&](int d) {
-        if (lrb < rb1 && lv < VS) {
-            if (TOK) {
-                while (lseg >= w.KS) {
-                    lseg -= w.KS;
-                    ++lj;
-                }
-                lp = w.data + (long long)max(s_e[lj], 0) * w.expert_stride + lrb * row_bytes + lseg * seg_bytes;
-            }
-            qg_load<NG>(st[d], lp, lane);
-        }
-        lv += wk;
-        if (TOK) lseg += wk;
-        else lp += wk * seg_bytes;
-        if (++li == nit) {
-            li = 0;
-            lv = kw;
-            lrb += wr;
-            if (TOK) {
-                lj = 0;
-                lseg = kw;
-            } else {
-                lp += wr * row_bytes - nit * wk * seg_bytes;
-            }
-        }
-    };
-    if (c.op == P_DENSE) {
-        load_start();
-#pragma unroll
-        for (int d = 0; d < kQgDepth; ++d)
-            if (d < total) load(d);
+    const int unit_bytes = p.useg * seg_bytes;
+    uint64_t* full = reinterpret_cast<uint64_t*>(sm + p.off_bar) + warp * p.depth;
+    uint8_t* ring = sm + p.off_ring + warp * p.depth * unit_bytes;
+    if (lane == 0) {
+        for (int i = 0; i < p.depth; ++i) mbar_init(smem_u32(&full[i]), 1);
+        fence_mbar_init();
     }
-    if (tid == 0) *reinterpret_cast<uint4*>(sm + p.off_red - 16) = make_uint4(0u, 0u, 0u, 0u);  // what lanes without a column read
-    grid_dep_wait();
+    if (tid == 0) {
+        s_abort = 0;
+        *reinterpret_cast<uint4*>(sm + p.off_zero) = make_uint4(0u, 0u, 0u, 0u);  // what lanes without a column read
+    }
+    __syncthreads();
+    grid_dep_launch();
 
-    // the item: its experts and columns
-    int rows = 1;
-    if (TOK) {
-        if (tid < nex) {
-            const int slot = (int)blockIdx.y * nex + tid;
-            const int e = c.r.ids[slot];
-            s_e[tid] = e >= 0 && e < w.E ? e : -1;
-            s_wt[tid] = c.r.weights[slot];
-        }
-        __syncthreads();
-    } else if (c.op == P_DENSE) {
-        rows = min(p.cols, c.M - (int)blockIdx.y * p.cols);
-    } else if (p.by_slot) {
-        const int e = c.r.ids[blockIdx.y];
-        if (e < 0 || e >= w.E) return;
-        base = w.data + e * w.expert_stride;
-    } else {
+    const int nex = TOK ? c.r.top_k : 1;
+    const int VS = nex * w.KS;                             // virtual segments: TOK's experts end to end
+    const int nit = (VS + wk * p.useg - 1) / (wk * p.useg);  // units per warp and row block
+    const long long rb_bytes = (long long)w.KS * seg_bytes;
+    const bool by_expert = c.op != P_DENSE && !p.by_slot;
+    int items = c.op == P_DENSE ? (c.M + p.cols - 1) / p.cols : TOK ? c.r.T : c.r.T * c.r.top_k;
+    if (by_expert) {
+        grid_dep_wait();
         if (warp == 0) {
-            // expert e has ceil(count / cols) items; lane l takes experts l per.. l per + per
+            // expert e has ceil(count / cols) items; lane l adds up experts l per.. l per + per
             const int per = (w.E + 31) / 32, slots = c.r.T * c.r.top_k;
             int mine = 0;
             for (int i = 0; i < per; ++i) {
@@ -255,54 +209,25 @@ __global__ void __launch_bounds__(512) q4g_rows_kernel(const QgRowsParams p) {
                 const int u = __shfl_up_sync(0xffffffffu, pre, o);
                 if (lane >= o) pre += u;
             }
-            if (lane == 31 && (int)blockIdx.y >= pre) s_item[0] = -1;
+            if (lane == 31) ts[w.E] = pre;
             pre -= mine;
-            if ((int)blockIdx.y >= pre && (int)blockIdx.y < pre + mine)
-                for (int i = 0; i < per; ++i) {
-                    const int e = lane * per + i;
-                    if (e >= w.E) break;
-                    const int p0 = max(c.r.offsets[e], 0), n = max(min(c.r.offsets[e + 1], slots) - p0, 0);
-                    const int items = (n + p.cols - 1) / p.cols, at = (int)blockIdx.y - pre;
-                    if (at >= 0 && at < items) {
-                        s_item[0] = e;
-                        s_item[1] = p0 + at * p.cols;
-                        s_item[2] = min(p.cols, n - at * p.cols);
-                    }
-                    pre += items;
-                }
+            for (int i = 0; i < per; ++i) {
+                const int e = lane * per + i;
+                if (e >= w.E) break;
+                ts[e] = pre;
+                pre += (max(min(c.r.offsets[e + 1], slots) - max(c.r.offsets[e], 0), 0) + p.cols - 1) / p.cols;
+            }
         }
         __syncthreads();
-        if (s_item[0] < 0) return;
-        rows = s_item[2];
-        base = w.data + s_item[0] * w.expert_stride;
-        if (tid < rows) {
-            const int slot = c.r.order[s_item[1] + tid];
-            s_row[tid] = slot >= 0 && slot < c.r.T * c.r.top_k ? slot : 0;
-        }
+        items = ts[w.E];
     }
-    if (c.op != P_DENSE) {
-        load_start();
-#pragma unroll
-        for (int d = 0; d < kQgDepth; ++d)
-            if (d < total) load(d);
-        if (!p.by_slot) __syncthreads();  // the slots
-    }
-    // activations
-    const int ncol = rows * p.np;
-    if (TOK) {
-        for (int j = 0; j < nex; ++j)
-            qg_stage(sm, c.x, c.xt, ((long long)blockIdx.y * nex + j) * c.ldx, w.K, w.KS, ncol, j * w.KS, 0, tid, nthr);
-    } else {
-        for (int r = 0; r < rows; ++r) {
-            const long long xr = c.op == P_DENSE ? (long long)blockIdx.y * p.cols + r
-                                 : p.by_slot     ? (long long)blockIdx.y / c.r.top_k
-                                 : c.op == P_GATE_UP ? (long long)s_row[r] / c.r.top_k
-                                                     : (long long)s_row[r];
-            qg_stage(sm, c.x, c.xt, xr * c.ldx, w.K, w.KS, ncol, 0, r * p.np, tid, nthr);
-        }
-    }
-    __syncthreads();
+    // this block's share: row blocks of items, end to end
+    const long long work = (long long)items * w.RB;
+    const long long w0 = (long long)blockIdx.x * work / gridDim.x, w1 = (long long)(blockIdx.x + 1) * work / gridDim.x;
 
+    QgRing lr, cr;       // the ring's next stage to fill, to read
+    int in_flight = 0;   // copies issued and not yet waited for
+    bool ok = true, waited = by_expert;
     float acc[NB][4];
 #pragma unroll
     for (int b = 0; b < NB; ++b)
@@ -310,129 +235,249 @@ __global__ void __launch_bounds__(512) q4g_rows_kernel(const QgRowsParams p) {
         for (int i = 0; i < 4; ++i) acc[b][i] = 0.0f;
     float* red = reinterpret_cast<float*>(sm + p.off_red);
     constexpr int kRed = NB * 128;  // sums of a warp: [column][16 rows]
-    // compute cursor; this lane's columns (8 b + g) at offset xp, xq bytes from 32 K to the next (0: it has no column)
-    int ci = 0, cr = 0, cv = kw, crb = rb0 + rw, cj = 0, cseg = kw;
-    int xp[NB], xq[NB];
-#pragma unroll
-    for (int b = 0; b < NB; ++b) {
-        const bool on = 8 * b + g < ncol;
-        xq[b] = on ? ncol * 64 : 0;
-        xp[b] = on ? kw * 4 * xq[b] + (8 * b + g) * 64 + t * 16 : p.off_red - 16;
-    }
-    for (int it = 0; it < total; it += kQgDepth) {
-#pragma unroll
-        for (int d = 0; d < kQgDepth; ++d) {
-            if (it + d >= total) break;
-            if (crb < rb1 && cv < VS) {
-                float wt = 1.0f;
-                bool on = true;
-                if (TOK) {
-                    while (cseg >= w.KS) {
-                        cseg -= w.KS;
-                        ++cj;
+    int flip = 0;                   // which of its two areas a row block's sums use
+
+    for (long long at = w0; at < w1;) {
+        const int item = (int)(at / w.RB), rb0 = (int)(at - (long long)item * w.RB);
+        const int rb1 = (int)min((long long)w.RB, rb0 + (w1 - at));
+        at += rb1 - rb0;
+        // the item: its experts and columns
+        int rows = 1, expert = 0, first = 0;
+        if (!waited && c.op != P_DENSE) {
+            grid_dep_wait();
+            waited = true;
+        }
+        if (TOK) {
+            __syncthreads();  // the last item's experts are no longer read
+            if (tid < nex) {
+                const int slot = item * nex + tid;
+                const int e = c.r.ids[slot];
+                s_e[tid] = e >= 0 && e < w.E ? e : -1;
+                s_wt[tid] = c.r.weights[slot];
+            }
+            __syncthreads();
+        } else if (c.op == P_DENSE) {
+            rows = min(p.cols, c.M - item * p.cols);
+        } else if (p.by_slot) {
+            expert = c.r.ids[item];
+            if (expert < 0 || expert >= w.E) continue;
+        } else {
+            int lo = 0, hi = w.E;  // ts[lo] <= item < ts[hi]
+            while (hi - lo > 1) {
+                const int mid = (lo + hi) >> 1;
+                if (ts[mid] <= item) lo = mid;
+                else hi = mid;
+            }
+            expert = lo;
+            const int slots = c.r.T * c.r.top_k, p0 = max(c.r.offsets[lo], 0), n = max(min(c.r.offsets[lo + 1], slots) - p0, 0);
+            first = p0 + (item - ts[lo]) * p.cols;
+            rows = min(p.cols, n - (item - ts[lo]) * p.cols);
+        }
+        const uint8_t* base = w.data + expert * w.expert_stride;
+        const int groups = (rb1 - rb0 + wr - 1) / wr, total = rb0 + rw < rb1 ? ((rb1 - rb0 - rw + wr - 1) / wr) * nit : 0;
+        // load cursor: unit li of row block lrb
+        int li = 0, lrb = rb0 + rw, lj = 0, lseg = kw * p.useg;
+        auto load = [&]() {
+            const int v = (kw + li * wk) * p.useg;
+            if (v < VS) {
+                const uint8_t* src;
+                int nseg = min(p.useg, VS - v);
+                if (TOK) {  // one segment a unit
+                    while (lseg >= w.KS) {
+                        lseg -= w.KS;
+                        ++lj;
                     }
-                    on = s_e[cj] >= 0;
-                    wt = s_wt[cj];
+                    src = w.data + (long long)max(s_e[lj], 0) * w.expert_stride + lrb * rb_bytes + lseg * seg_bytes;
+                } else {
+                    src = base + lrb * rb_bytes + v * seg_bytes;
                 }
-                if (on) {
-                    float gr[NB][4];
+                if (lane == 0) {
+                    const uint32_t bar = smem_u32(&full[lr.s]);
+                    mbar_arrive_tx(bar, (uint32_t)(nseg * seg_bytes));
+                    bulk_g2s(smem_u32(ring + lr.s * unit_bytes), src, (uint32_t)(nseg * seg_bytes), bar);
+                }
+                lr.next(p.depth);
+                ++in_flight;
+            }
+            lseg += wk;
+            if (++li == nit) {
+                li = 0;
+                lrb += wr;
+                lj = 0;
+                lseg = kw;
+            }
+        };
+        int ahead = 0;  // iterations whose unit has been asked for
+        for (; ok && ahead < p.depth && ahead < total; ++ahead) load();
+        if (!waited) {
+            grid_dep_wait();
+            waited = true;
+        }
+        __syncthreads();  // the last item's activations are no longer read
+        if (by_expert) {
+            if (tid < rows) {
+                const int slot = c.r.order[first + tid];
+                s_row[tid] = slot >= 0 && slot < c.r.T * c.r.top_k ? slot : 0;
+            }
+            __syncthreads();
+        }
+        const int ncol = rows * p.np;
+        if (TOK) {
+            for (int j = 0; j < nex; ++j)
+                qg_stage(sm, c.x, c.xt, w.K, w.KS, 1, p.np, j * w.KS, [&](int) { return ((long long)item * nex + j) * c.ldx; }, tid, nthr);
+        } else {
+            qg_stage(sm, c.x, c.xt, w.K, w.KS, rows, p.np, 0, [&](int r) {
+                const long long xr = c.op == P_DENSE ? (long long)item * p.cols + r
+                                     : p.by_slot     ? (long long)item / c.r.top_k
+                                     : c.op == P_GATE_UP ? (long long)s_row[r] / c.r.top_k
+                                                         : (long long)s_row[r];
+                return xr * c.ldx;
+            }, tid, nthr);
+        }
+        __syncthreads();
+
+        // this lane's columns (8 b + g) at offset xp, xq bytes from 32 K to the next (0: it has no column)
+        int xp[NB], xq[NB];
 #pragma unroll
-                    for (int q4 = 0; q4 < 4; ++q4) {  // 32 K a step
-                        const int gi = q4 * 32 / segk;
-                        const uint32_t sw0 = st[d].sw[2 * gi], sw1 = st[d].sw[2 * gi + 1];
-                        const uint32_t zl = qg_zero<BF>(sw0, false), zh = qg_zero<BF>(sw1, true);
-                        const uint4 cw = st[d].c[q4 >> 1];
-                        uint32_t a0[4], a1[4];
-                        qg_codes<BF>(q4 & 1 ? cw.z : cw.x, zl, zh, a0);
-                        qg_codes<BF>(q4 & 1 ? cw.w : cw.y, zl, zh, a1);
-                        const bool first = q4 * 32 % segk == 0;
-#pragma unroll
-                        for (int b = 0; b < NB; ++b) {
-                            const uint4 xv = *reinterpret_cast<const uint4*>(sm + xp[b] + q4 * xq[b]);
-                            if (first) qg_mma<BF, true>(gr[b], a0, xv.x, xv.y);
-                            else qg_mma<BF, false>(gr[b], a0, xv.x, xv.y);
-                            qg_mma<BF, false>(gr[b], a1, xv.z, xv.w);
+        for (int b = 0; b < NB; ++b) {
+            const bool on = 8 * b + g < ncol;
+            xq[b] = on ? ncol * 64 : 0;
+            xp[b] = on ? (8 * b + g) * 64 + t * 16 : p.off_zero;
+        }
+        int crb = rb0 + rw;
+        for (int gi = 0; gi < groups; ++gi, crb += wr, flip ^= 1) {
+            if (crb >= rb1) continue;
+            int cj = 0, cseg = kw;
+            for (int ci = 0; ci < nit; ++ci) {
+                const int v = (kw + ci * wk) * p.useg;
+                if (v < VS) {
+                    if (ok) ok = qg_wait(smem_u32(&full[cr.s]), cr.ph, &s_abort, p.err);
+                    if (!ok) continue;
+                    --in_flight;
+                    float wt = 1.0f;
+                    bool on = true;
+                    if (TOK) {
+                        while (cseg >= w.KS) {
+                            cseg -= w.KS;
+                            ++cj;
                         }
-                        if ((q4 + 1) * 32 % segk == 0) {  // the group's end
-                            const float s0 = TOK ? qg_scale(sw0) * wt : qg_scale(sw0), s1 = TOK ? qg_scale(sw1) * wt : qg_scale(sw1);
+                        on = s_e[cj] >= 0;
+                        wt = s_wt[cj];
+                    }
+                    const uint8_t* sp = ring + cr.s * unit_bytes;
+                    cr.next(p.depth);
+                    const int nseg = on ? min(p.useg, VS - v) : 0;
+                    for (int sg = 0; sg < nseg; ++sg, sp += seg_bytes) {
+                        const uint4 c0 = reinterpret_cast<const uint4*>(sp)[lane], c1 = reinterpret_cast<const uint4*>(sp + kQgTile)[lane];
+                        uint32_t sw[2 * NG];
+                        const uint8_t* sq = sp + 2 * kQgTile + g * (8 * NG);
+                        if (NG == 1) {
+                            const uint2 u = *reinterpret_cast<const uint2*>(sq);
+                            sw[0] = u.x;
+                            sw[1] = u.y;
+                        } else {
+#pragma unroll
+                            for (int i = 0; i < NG / 2; ++i) {
+                                const uint4 u = reinterpret_cast<const uint4*>(sq)[i];
+                                sw[4 * i] = u.x;
+                                sw[4 * i + 1] = u.y;
+                                sw[4 * i + 2] = u.z;
+                                sw[4 * i + 3] = u.w;
+                            }
+                        }
+                        float gr[NB][4];
+#pragma unroll
+                        for (int q4 = 0; q4 < 4; ++q4) {  // 32 K a step
+                            const int gi4 = q4 * 32 / segk;
+                            const uint32_t sw0 = sw[2 * gi4], sw1 = sw[2 * gi4 + 1];
+                            const uint32_t zl = qg_zero<BF>(sw0, false), zh = qg_zero<BF>(sw1, true);
+                            const uint4 cw = q4 < 2 ? c0 : c1;
+                            uint32_t a0[4], a1[4];
+                            qg_codes<BF>(q4 & 1 ? cw.z : cw.x, zl, zh, a0);
+                            qg_codes<BF>(q4 & 1 ? cw.w : cw.y, zl, zh, a1);
+                            const bool start = q4 * 32 % segk == 0;
 #pragma unroll
                             for (int b = 0; b < NB; ++b) {
-                                acc[b][0] = fmaf(s0, gr[b][0], acc[b][0]);
-                                acc[b][1] = fmaf(s0, gr[b][1], acc[b][1]);
-                                acc[b][2] = fmaf(s1, gr[b][2], acc[b][2]);
-                                acc[b][3] = fmaf(s1, gr[b][3], acc[b][3]);
+                                const uint4 xv = *reinterpret_cast<const uint4*>(sm + xp[b] + ((v + sg) * 4 + q4) * xq[b]);
+                                if (start) qg_mma<BF, true>(gr[b], a0, xv.x, xv.y);
+                                else qg_mma<BF, false>(gr[b], a0, xv.x, xv.y);
+                                qg_mma<BF, false>(gr[b], a1, xv.z, xv.w);
+                            }
+                            if ((q4 + 1) * 32 % segk == 0) {  // the group's end
+                                const float s0 = TOK ? qg_scale(sw0) * wt : qg_scale(sw0), s1 = TOK ? qg_scale(sw1) * wt : qg_scale(sw1);
+#pragma unroll
+                                for (int b = 0; b < NB; ++b) {
+                                    acc[b][0] = fmaf(s0, gr[b][0], acc[b][0]);
+                                    acc[b][1] = fmaf(s0, gr[b][1], acc[b][1]);
+                                    acc[b][2] = fmaf(s1, gr[b][2], acc[b][2]);
+                                    acc[b][3] = fmaf(s1, gr[b][3], acc[b][3]);
+                                }
                             }
                         }
                     }
+                }
+                if (TOK) cseg += wk;
+                __syncwarp();  // the stage has been read
+                if (ahead < total) {
+                    load();
+                    ++ahead;
                 }
             }
-            if (it + d + kQgDepth < total) load(d);
-            cv += wk;
-            if (TOK) cseg += wk;
+            // the row block's sums
+            float* mine = red + (flip * (nthr / 32) + warp) * kRed;
 #pragma unroll
-            for (int b = 0; b < NB; ++b) xp[b] += wk * 4 * xq[b];
-            if (++ci == nit) {  // the row block's sums
-                float* mine = red + ((cr & 1) * (nthr / 32) + warp) * kRed;
-#pragma unroll
-                for (int b = 0; b < NB; ++b) {
-                    const int col = 8 * b + 2 * t;
-                    if (col < ncol) {
-                        mine[col * 16 + g] = acc[b][0];
-                        mine[col * 16 + g + 8] = acc[b][2];
-                    }
-                    if (col + 1 < ncol) {
-                        mine[(col + 1) * 16 + g] = acc[b][1];
-                        mine[(col + 1) * 16 + g + 8] = acc[b][3];
-                    }
-                    acc[b][0] = acc[b][1] = acc[b][2] = acc[b][3] = 0.0f;
-                    xp[b] -= nit * wk * 4 * xq[b];
+            for (int b = 0; b < NB; ++b) {
+                const int col = 8 * b + 2 * t;
+                if (col < ncol) {
+                    mine[col * 16 + g] = acc[b][0];
+                    mine[col * 16 + g + 8] = acc[b][2];
                 }
-                __syncthreads();
-                if (crb < rb1) {
-                    const float* from = red + ((cr & 1) * (nthr / 32) + rw * wk) * kRed;
-                    const int per = w.paired ? 8 : 16;
-                    auto sum = [&](int r, int row) {
-                        float v2 = 0.0f;
-                        for (int pc = 0; pc < p.np; ++pc) {
-                            const float* f = from + (r * p.np + pc) * 16 + row;
+                if (col + 1 < ncol) {
+                    mine[(col + 1) * 16 + g] = acc[b][1];
+                    mine[(col + 1) * 16 + g + 8] = acc[b][3];
+                }
+                acc[b][0] = acc[b][1] = acc[b][2] = acc[b][3] = 0.0f;
+            }
+            if (wk == 1) __syncwarp();
+            else asm volatile("bar.sync %0, %1;" ::"r"(1 + rw), "r"(wk * 32) : "memory");
+            const float* from = red + (flip * (nthr / 32) + rw * wk) * kRed;
+            const int per = w.paired ? 8 : 16;
+            auto sum = [&](int r, int row) {
+                float v2 = 0.0f;
+                for (int pc = 0; pc < p.np; ++pc) {
+                    const float* f = from + (r * p.np + pc) * 16 + row;
 #pragma unroll 4
-                            for (int k2 = 0; k2 < wk; ++k2) v2 += f[k2 * kRed];
-                        }
-                        return v2;
-                    };
-                    // the warps take turns at a short row block's sums
-                    for (int o = ((kw + cr) & (wk - 1)) * 32 + lane; o < per * rows; o += wk * 32) {
-                        const int row = o % per, r = o / per;
-                        const float v0 = sum(r, row);
-                        if (c.op == P_GATE_UP) {
-                            const float u = sum(r, row + 8);
-                            const int f = crb * 8 + row, F = w.N / 2;
-                            const long long slot = p.by_slot ? (long long)blockIdx.y : (long long)s_row[r];
-                            if (f < F) x_store(c.y, c.xt, slot * F + f, swiglu(v0, u));
-                        } else {
-                            const int n = crb * 16 + row;
-                            if (n < w.N) {
-                                if (c.op == P_DENSE)
-                                    x_store(c.y, c.xt, ((long long)blockIdx.y * p.cols + r) * w.N + n, v0);
-                                else if (TOK)
-                                    x_store(c.y, c.xt, (long long)blockIdx.y * w.N + n, v0);
-                                else
-                                    p.part[(long long)s_row[r] * w.N + n] = v0;
-                            }
-                        }
-                    }
+                    for (int k2 = 0; k2 < wk; ++k2) v2 += f[k2 * kRed];
                 }
-                ci = 0;
-                ++cr;
-                cv = kw;
-                crb += wr;
-                if (TOK) {
-                    cj = 0;
-                    cseg = kw;
+                return v2;
+            };
+            // the warps take turns at a short row block's sums
+            for (int o = ((kw + gi) & (wk - 1)) * 32 + lane; o < per * rows; o += wk * 32) {
+                const int row = o % per, r = o / per;
+                const float v0 = sum(r, row);
+                if (c.op == P_GATE_UP) {
+                    const float u = sum(r, row + 8);
+                    const int f = crb * 8 + row, F = w.N / 2;
+                    const long long slot = p.by_slot ? (long long)item : (long long)s_row[r];
+                    if (f < F) x_store(c.y, c.xt, slot * F + f, swiglu(v0, u));
+                } else {
+                    const int n = crb * 16 + row;
+                    if (n < w.N) {
+                        if (c.op == P_DENSE)
+                            x_store(c.y, c.xt, ((long long)item * p.cols + r) * w.N + n, v0);
+                        else if (TOK)
+                            x_store(c.y, c.xt, (long long)item * w.N + n, v0);
+                        else
+                            p.part[(long long)s_row[r] * w.N + n] = v0;
+                    }
                 }
             }
         }
     }
+    if (!waited) grid_dep_wait();
+    // after a wait that gave up, the copies still in flight must land before the block can exit
+    if (lane == 0)
+        for (; in_flight > 0; --in_flight, cr.next(p.depth)) mbar_drain(smem_u32(&full[cr.s]), cr.ph, &s_abort, p.err);
 }
 
 }  // namespace qmm

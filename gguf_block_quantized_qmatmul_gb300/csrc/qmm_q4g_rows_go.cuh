@@ -9,9 +9,9 @@ template <int NB, bool BF, int NG, bool TOK = false>
 cudaError_t q4g_rows_one(const QgRowsPlan& pl, const QgRowsParams& p, int smem_max, cudaStream_t s) {
     static unsigned long long done = 0;
     auto* k = q4g_rows_kernel<NB, BF, NG, TOK>;
-    const cudaError_t e = ensure_smem(k, smem_max - 1024, done);  // less the static arrays
+    const cudaError_t e = ensure_smem(k, smem_max - kQgRowStatic, done);
     if (e != cudaSuccess) return e;
-    return launch_pdl_2d(k, (unsigned)pl.gx, (unsigned)pl.gy, (unsigned)(pl.warps * 32), pl.smem, s, p);
+    return launch_pdl(k, (unsigned)pl.blocks, (unsigned)(pl.warps * 32), pl.smem, s, p);
 }
 
 template <int NB>
