@@ -14,8 +14,8 @@
 // warp-wide integer reductions (redux) on order-preserving keys, the second
 // one settling ties.
 //
-// The order (a stable counting sort of the T k slots by expert) takes no
-// atomics, so it is the same on every run: each block counts its tokens'
+// The order (a stable counting sort of the T k slots by expert) hands out no
+// place by an atomic, so it is the same on every run: each block counts its tokens'
 // slots by expert; in the second launch a block adds up the counts of all
 // blocks (its own base positions and the offsets), and its warps rank their
 // 32 consecutive slots at a time by matching lanes.  A call that fits one
@@ -25,14 +25,17 @@
 namespace qmm {
 namespace {
 
-constexpr int kRouteWarps = 16;
-constexpr int kRouteThreads = kRouteWarps * 32;
+constexpr int kRouteTile = 32;  // tokens per block, up to 256 blocks
+constexpr int kRouteMaxBlocks = 256;
+// a warp per token of the tile, unless the picks of over 256 experts take too many registers
+__host__ __device__ constexpr int route_warps(int epl) { return epl <= 8 ? 32 : 16; }
 
 
 struct RouteParams {
     RouteCall c;
     int tile;      // tokens per block
     int blocks;
+    unsigned group_magic;  // 2^22 / (experts per group), rounded up: e / group size for e < 512
     unsigned* counts;  // [blocks][E] slots of each block by expert (more than one block)
 };
 
@@ -43,9 +46,11 @@ __device__ __forceinline__ uint32_t pick_key(float f) {
     return u & 0x80000000u ? ~u : u | 0x80000000u;
 }
 
-// One token: EPL experts per lane.  sp: the warp's row of picks in shared memory (with groups).
+// One token: EPL experts per lane.  sk: the warp's row of picks in shared memory (with groups).
+// Lane j < top_k returns choice j.
 template <int EPL>
-__device__ __forceinline__ void route_token(const RouteCall& c, long long tok, float* sp, int lane) {
+__device__ __forceinline__ int route_token(const RouteParams& p, long long tok, uint32_t* sk, int lane) {
+    const RouteCall& c = p.c;
     float score[EPL];
     uint32_t key[EPL];
     const long long base = tok * c.ldl;
@@ -111,7 +116,6 @@ __device__ __forceinline__ void route_token(const RouteCall& c, long long tok, f
         const int gs = c.E / c.groups;
         int lpg = 32;
         while (lpg * c.groups > 32) lpg >>= 1;
-        uint32_t* sk = reinterpret_cast<uint32_t*>(sp);
         __syncwarp();
 #pragma unroll
         for (int i = 0; i < EPL; ++i)
@@ -147,21 +151,27 @@ __device__ __forceinline__ void route_token(const RouteCall& c, long long tok, f
 #pragma unroll
         for (int i = 0; i < EPL; ++i) {
             const int e = lane + 32 * i;
-            if (e < c.E && !((kept >> (e / gs)) & 1u)) key[i] = 0u;
+            if (e < c.E && !((kept >> ((e * p.group_magic) >> 22)) & 1u)) key[i] = 0u;
         }
     }
-    // the k largest: lane j ends up with choice j
+    // the k largest: lane j ends up with choice j; a lane looks for its own largest again
+    // only after it gave it away
     int my_id = 0;
     float my_score = 0.0f, sum = 0.0f;
-    for (int j = 0; j < c.top_k; ++j) {
-        uint32_t b = 0u;
-        int bi = 0;
+    uint32_t b = 0u;
+    int bi = 0;
+    auto local = [&]() {
+        b = 0u;
+        bi = 0;
 #pragma unroll
-        for (int i = 0; i < EPL; ++i)
-            if (key[i] > b) {
-                b = key[i];
-                bi = i;
-            }
+        for (int i = 0; i < EPL; ++i) {
+            const bool more = key[i] > b;
+            b = more ? key[i] : b;
+            bi = more ? i : bi;
+        }
+    };
+    local();
+    for (int j = 0; j < c.top_k; ++j) {
         const uint32_t best = __reduce_max_sync(0xffffffffu, b);
         const uint32_t id = __reduce_min_sync(0xffffffffu, b == best ? (uint32_t)(lane + 32 * bi) : 0xffffffffu);
         float s = 0.0f;
@@ -172,6 +182,7 @@ __device__ __forceinline__ void route_token(const RouteCall& c, long long tok, f
             key[i] = here ? 0u : key[i];
         }
         s = __shfl_sync(0xffffffffu, s, (int)(id & 31u));
+        if (lane == (int)(id & 31u)) local();
         sum += s;
         if (lane == j) {
             my_id = (int)id;
@@ -183,9 +194,11 @@ __device__ __forceinline__ void route_token(const RouteCall& c, long long tok, f
         c.ids[tok * c.top_k + lane] = my_id;
         c.weights[tok * c.top_k + lane] = c.scale == 1.0f ? v : v * c.scale;
     }
+    return my_id;
 }
 
 // exclusive prefix sum of a[0..n) in shared memory by the whole block, n <= 512; returns the total
+template <int W>
 __device__ __forceinline__ int block_scan(int* a, int n, int* tmp, int tid) {
     const int lane = tid & 31, warp = tid >> 5;
     int v = tid < n ? a[tid] : 0;
@@ -198,7 +211,7 @@ __device__ __forceinline__ int block_scan(int* a, int n, int* tmp, int tid) {
     if (lane == 31) tmp[warp] = incl;
     __syncthreads();
     int before = 0, all = 0;
-    for (int i = 0; i < kRouteWarps; ++i) {
+    for (int i = 0; i < W; ++i) {
         const int u = tmp[i];
         if (i < warp) before += u;
         all += u;
@@ -208,20 +221,22 @@ __device__ __forceinline__ int block_scan(int* a, int n, int* tmp, int tid) {
     return all;
 }
 
-// Counts the ids of slots [s0, s1) by expert, a row of `hist` [kRouteWarps][E]
-// per warp; warp v has the v-th sixteenth of the 32-slot steps.  Matching
-// lanes are counted together; no two warps share a counter.
+// Counts n ids by expert, a row of `hist` [W][E] per warp; each warp has a
+// consecutive part of the 32-slot steps.  Matching lanes are counted together;
+// no two warps share a counter.
+template <int W>
 __device__ __forceinline__ void warp_range(int n, int warp, int& c0, int& c1) {
     const int steps = (n + 31) / 32;
-    c0 = (int)((long long)warp * steps / kRouteWarps) * 32;
-    c1 = min(n, (int)((long long)(warp + 1) * steps / kRouteWarps) * 32);
+    c0 = (int)((long long)warp * steps / W) * 32;
+    c1 = min(n, (int)((long long)(warp + 1) * steps / W) * 32);
 }
+template <int W>
 __device__ __forceinline__ void count_slots(const int* ids, int n, int E, int* hist, int warp, int lane) {
     int* h = hist + warp * E;
     for (int e = lane; e < E; e += 32) h[e] = 0;
     __syncwarp();
     int c0, c1;
-    warp_range(n, warp, c0, c1);
+    warp_range<W>(n, warp, c0, c1);
     for (int i = c0; i < c1; i += 32) {
         const int id = i + lane < c1 ? ids[i + lane] : -1;
         const unsigned same = __match_any_sync(0xffffffffu, id);
@@ -230,10 +245,11 @@ __device__ __forceinline__ void count_slots(const int* ids, int n, int E, int* h
     }
 }
 // After the rows of hist hold each warp's first position per expert: the slots to their places.
+template <int W>
 __device__ __forceinline__ void place_slots(const int* ids, int n, int E, int* hist, long long slot0, int* order, int warp, int lane) {
     int* h = hist + warp * E;
     int c0, c1;
-    warp_range(n, warp, c0, c1);
+    warp_range<W>(n, warp, c0, c1);
     for (int i = c0; i < c1; i += 32) {
         const int id = i + lane < c1 ? ids[i + lane] : -1;
         const unsigned same = __match_any_sync(0xffffffffu, id);
@@ -247,27 +263,54 @@ __device__ __forceinline__ void place_slots(const int* ids, int n, int E, int* h
     }
 }
 
+// One token: one warp does it all, with no barrier.
 template <int EPL>
-__global__ void __launch_bounds__(kRouteThreads) moe_route_kernel(const RouteParams p) {
-    extern __shared__ __align__(16) int sm[];  // [kRouteWarps][E] picks, then counters; [E] totals
-    __shared__ int tmp[kRouteWarps];
+__global__ void __launch_bounds__(32) moe_route_one_kernel(const RouteParams p) {
+    extern __shared__ __align__(16) uint32_t sk[];
+    const RouteCall& c = p.c;
+    const int lane = threadIdx.x;
+    grid_dep_launch();
+    grid_dep_wait();
+    const int id = route_token<EPL>(p, 0, sk, lane);
+    if (!c.order) return;
+    int rank = 0, below[EPL];  // slots of lower experts than lane + 32 i (a token's experts differ)
+#pragma unroll
+    for (int i = 0; i < EPL; ++i) below[i] = 0;
+    for (int j = 0; j < c.top_k; ++j) {
+        const int other = __shfl_sync(0xffffffffu, id, j);
+        rank += other < id;
+#pragma unroll
+        for (int i = 0; i < EPL; ++i) below[i] += other < lane + 32 * i;
+    }
+    if (lane < c.top_k) c.order[rank] = lane;
+#pragma unroll
+    for (int i = 0; i < EPL; ++i)
+        if (lane + 32 * i < c.E) c.offsets[lane + 32 * i] = below[i];
+    if (lane == 0) c.offsets[c.E] = c.top_k;
+}
+
+template <int EPL>
+__global__ void __launch_bounds__(route_warps(EPL) * 32) moe_route_kernel(const RouteParams p) {
+    extern __shared__ __align__(16) int sm[];  // [W][E] picks, then counters; [E] totals
+    constexpr int W = route_warps(EPL), kThreads = W * 32;
+    __shared__ int tmp[W];
     const RouteCall& c = p.c;
     const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
     grid_dep_launch();
     grid_dep_wait();
     const int t0 = blockIdx.x * p.tile, t1 = min(c.T, t0 + p.tile);
-    for (int t = t0 + warp; t < t1; t += kRouteWarps) route_token<EPL>(c, t, reinterpret_cast<float*>(sm) + warp * c.E, lane);
+    for (int t = t0 + warp; t < t1; t += W) route_token<EPL>(p, t, reinterpret_cast<uint32_t*>(sm) + warp * c.E, lane);
     if (!c.order) return;
     __syncthreads();  // the ids of this block's tokens are written
     const int n = (t1 - t0) * c.top_k;
     const int* ids = c.ids + (long long)t0 * c.top_k;
-    count_slots(ids, n, c.E, sm, warp, lane);
+    count_slots<W>(ids, n, c.E, sm, warp, lane);
     __syncthreads();
-    int* tot = sm + kRouteWarps * c.E;
-    for (int e = tid; e < c.E; e += kRouteThreads) {
+    int* tot = sm + W * c.E;
+    for (int e = tid; e < c.E; e += kThreads) {
         int v = 0;
 #pragma unroll
-        for (int w = 0; w < kRouteWarps; ++w) {
+        for (int w = 0; w < W; ++w) {
             const int u = sm[w * c.E + e];
             sm[w * c.E + e] = v;
             v += u;
@@ -277,53 +320,68 @@ __global__ void __launch_bounds__(kRouteThreads) moe_route_kernel(const RoutePar
     }
     if (p.blocks > 1) return;
     __syncthreads();
-    const int all = block_scan(tot, c.E, tmp, tid);
-    for (int e = tid; e < c.E; e += kRouteThreads) {
+    const int all = block_scan<W>(tot, c.E, tmp, tid);
+    for (int e = tid; e < c.E; e += kThreads) {
         c.offsets[e] = tot[e];
 #pragma unroll
-        for (int w = 0; w < kRouteWarps; ++w) sm[w * c.E + e] += tot[e];
+        for (int w = 0; w < W; ++w) sm[w * c.E + e] += tot[e];
     }
     if (tid == 0) c.offsets[c.E] = all;
     __syncthreads();
-    place_slots(ids, n, c.E, sm, 0, c.order, warp, lane);
+    place_slots<W>(ids, n, c.E, sm, 0, c.order, warp, lane);
 }
 
-__global__ void __launch_bounds__(kRouteThreads) moe_order_kernel(const RouteParams p) {
-    extern __shared__ __align__(16) int sm[];
-    __shared__ int tmp[kRouteWarps];
+constexpr int kOrderWarps = 16, kOrderThreads = kOrderWarps * 32;
+__global__ void __launch_bounds__(kOrderThreads) moe_order_kernel(const RouteParams p) {
+    extern __shared__ __align__(16) int sm[];  // [W][E] counters; [E] totals; [E] slots in earlier blocks
+    __shared__ int tmp[kOrderWarps];
     const RouteCall& c = p.c;
-    const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
+    const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31, E = c.E;
     const int t0 = blockIdx.x * p.tile, t1 = min(c.T, t0 + p.tile);
     const int n = (t1 - t0) * c.top_k;
     const int* ids = c.ids + (long long)t0 * c.top_k;
     grid_dep_launch();
-    grid_dep_wait();
-    // slots of expert e in the blocks before this one, and in all
-    int* tot = sm + kRouteWarps * c.E;
-    int before = 0, all = 0;
-    if (tid < c.E)
-        for (int b = 0; b < p.blocks; ++b) {
-            const int v = (int)__ldcg(p.counts + (long long)b * c.E + tid);
-            before += b < (int)blockIdx.x ? v : 0;
-            all += v;
-        }
-    if (tid < c.E) tot[tid] = all;
-    count_slots(ids, n, c.E, sm, warp, lane);
+    int* tot = sm + kOrderWarps * E;
+    int* pre = tot + E;
+    for (int e = tid; e < 2 * E; e += kOrderThreads) tot[e] = 0;
     __syncthreads();
-    const int every = block_scan(tot, c.E, tmp, tid);
-    if (tid < c.E) {
-        if (blockIdx.x == 0) c.offsets[tid] = tot[tid];
-        int v = tot[tid] + before;
+    grid_dep_wait();
+    // slots of every expert in all blocks and in those before this one: a warp adds up every
+    // sixteenth block's counts, eight rows in flight (integer sums: their order does not matter)
+    for (int e = lane; e < E; e += 32) {
+        int before = 0, all = 0;
+        for (int b0 = warp; b0 < p.blocks; b0 += 8 * kOrderWarps) {
+            int v[8];
 #pragma unroll
-        for (int w = 0; w < kRouteWarps; ++w) {
-            const int u = sm[w * c.E + tid];
-            sm[w * c.E + tid] = v;
+            for (int i = 0; i < 8; ++i) {
+                const int b = b0 + i * kOrderWarps;
+                v[i] = b < p.blocks ? (int)__ldcg(p.counts + (long long)b * E + e) : 0;
+            }
+#pragma unroll
+            for (int i = 0; i < 8; ++i) {
+                before += b0 + i * kOrderWarps < (int)blockIdx.x ? v[i] : 0;
+                all += v[i];
+            }
+        }
+        atomicAdd(&tot[e], all);
+        atomicAdd(&pre[e], before);
+    }
+    count_slots<kOrderWarps>(ids, n, E, sm, warp, lane);
+    __syncthreads();
+    const int every = block_scan<kOrderWarps>(tot, E, tmp, tid);
+    for (int e = tid; e < E; e += kOrderThreads) {
+        if (blockIdx.x == 0) c.offsets[e] = tot[e];
+        int v = tot[e] + pre[e];
+#pragma unroll
+        for (int w = 0; w < kOrderWarps; ++w) {
+            const int u = sm[w * E + e];
+            sm[w * E + e] = v;
             v += u;
         }
     }
-    if (blockIdx.x == 0 && tid == 0) c.offsets[c.E] = every;
+    if (blockIdx.x == 0 && tid == 0) c.offsets[E] = every;
     __syncthreads();
-    place_slots(ids, n, c.E, sm, (long long)t0 * c.top_k, c.order, warp, lane);
+    place_slots<kOrderWarps>(ids, n, E, sm, (long long)t0 * c.top_k, c.order, warp, lane);
 }
 
 __global__ void moe_no_tokens_kernel(int* offsets, int E) {
@@ -331,9 +389,15 @@ __global__ void moe_no_tokens_kernel(int* offsets, int E) {
     for (int e = threadIdx.x; e <= E; e += blockDim.x) offsets[e] = 0;
 }
 
-// 32 tokens a block (two a warp) up to 256 blocks; the second launch reads
-// every block's counts, so more blocks cost it more than they save
-int route_tile(int T) { return T <= 32 * 256 ? 32 : (T + 255) / 256; }
+// the second launch reads every block's counts, so that more blocks would cost it more than they save
+int route_tile(int T) { return T <= kRouteTile * kRouteMaxBlocks ? kRouteTile : (T + kRouteMaxBlocks - 1) / kRouteMaxBlocks; }
+
+template <int EPL>
+cudaError_t route_go(const RouteParams& p, cudaStream_t s) {
+    if (p.c.T == 1) return launch_pdl(moe_route_one_kernel<EPL>, 1u, 32u, (size_t)p.c.E * 4, s, p);
+    const size_t smem = (size_t)(route_warps(EPL) + 1) * p.c.E * 4;  // at most 35 KB
+    return launch_pdl(moe_route_kernel<EPL>, (unsigned)p.blocks, (unsigned)(route_warps(EPL) * 32), smem, s, p);
+}
 
 }  // namespace
 
@@ -353,16 +417,16 @@ cudaError_t launch_route(const RouteCall& c, void* ws, cudaStream_t s) {
     p.tile = route_tile(c.T);
     p.blocks = (c.T + p.tile - 1) / p.tile;
     p.counts = static_cast<unsigned*>(ws);
-    const size_t smem = (size_t)(kRouteWarps + 1) * c.E * 4;  // at most 34 KB
-    const unsigned g = (unsigned)p.blocks;
+    const int gs = c.E / c.groups;
+    p.group_magic = ((1u << 22) + gs - 1) / gs;
     const int epl = (c.E + 31) / 32;
-    cudaError_t e = epl <= 1   ? launch_pdl(moe_route_kernel<1>, g, kRouteThreads, smem, s, p)
-                    : epl <= 2 ? launch_pdl(moe_route_kernel<2>, g, kRouteThreads, smem, s, p)
-                    : epl <= 4 ? launch_pdl(moe_route_kernel<4>, g, kRouteThreads, smem, s, p)
-                    : epl <= 8 ? launch_pdl(moe_route_kernel<8>, g, kRouteThreads, smem, s, p)
-                               : launch_pdl(moe_route_kernel<16>, g, kRouteThreads, smem, s, p);
+    const cudaError_t e = epl <= 1   ? route_go<1>(p, s)
+                          : epl <= 2 ? route_go<2>(p, s)
+                          : epl <= 4 ? route_go<4>(p, s)
+                          : epl <= 8 ? route_go<8>(p, s)
+                                     : route_go<16>(p, s);
     if (e != cudaSuccess || !c.order || p.blocks == 1) return e;
-    return launch_pdl(moe_order_kernel, g, kRouteThreads, smem, s, p);
+    return launch_pdl(moe_order_kernel, (unsigned)p.blocks, kOrderThreads, (size_t)(kOrderWarps + 2) * c.E * 4, s, p);
 }
 
 }  // namespace qmm

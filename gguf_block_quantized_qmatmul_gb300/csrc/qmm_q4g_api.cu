@@ -72,7 +72,7 @@ qmm_status product(const QgCall& c, void* ws, size_t ws_bytes, qmm_stream_t stre
         if (!aligned(ws, 16)) return QMM_ERR_ALIGN;
     }
     cudaStream_t s = reinterpret_cast<cudaStream_t>(stream);
-    const cudaError_t e = ch.gemm ? launch_q4g_gemm(ch.mm, c, ws, err, smem, s) : launch_q4g_rows(ch.rows, c, ws, err, smem, s);
+    const cudaError_t e = ch.gemm ? launch_q4g_gemm(ch.mm, c, ws, err, smem, s) : launch_q4g_rows(ch.rows, c, ws, smem, s);
     return e == cudaSuccess ? QMM_OK : QMM_ERR_CUDA;
 }
 

@@ -85,7 +85,7 @@ __device__ __forceinline__ bool elect_one() {
 
 // One 64-K tile h of a segment of one row block: fragment registers of its f16 weights (and their rests).
 template <int NP, int NG>
-__device__ __forceinline__ void qg_convert(const uint8_t* seg, int h, int lane, float m0, float m1, uint32_t hi[16], uint32_t lo[16]) {
+__device__ __forceinline__ void qg_convert(const uint8_t* seg, int h, int lane, uint32_t magic, float m0, float m1, uint32_t hi[16], uint32_t lo[16]) {
     const uint4 q = *reinterpret_cast<const uint4*>(seg + h * kQgTile + lane * 16);
     const uint32_t word[4] = {q.x, q.y, q.z, q.w};
     const uint32_t* sw = reinterpret_cast<const uint32_t*>(seg + 2 * kQgTile + (lane >> 2) * (8 * NG));
@@ -102,7 +102,7 @@ __device__ __forceinline__ void qg_convert(const uint8_t* seg, int h, int lane, 
             s1 = __float2half2_rn(qg_scale(v.y) * m1);
         }
         uint32_t a[4];
-        qg_codes<false>(word[s], zl, zh, a);
+        qg_codes<false>(word[s], magic, zl, zh, a);
 #pragma unroll
         for (int i = 0; i < 4; ++i) {
             const __half2 c = *reinterpret_cast<__half2*>(&a[i]);
@@ -450,6 +450,7 @@ __global__ void __launch_bounds__(kQgThreads, 1) q4g_gemm_kernel(const __grid_co
         const int cw = warp - kQgConv0, q = warp & 3, grp = cw >> 2;
         QgRing g, r;  // of the raw stage's first tile; of raw stages
         int count = 0;  // tiles before this raw stage
+        const uint32_t magic = opaque(0x64006400u);
         bool ok = true;
         for (int u = blockIdx.x; u < units && ok; u += gridDim.x) {
             const QgUnit un = place(u);
@@ -473,14 +474,14 @@ __global__ void __launch_bounds__(kQgThreads, 1) q4g_gemm_kernel(const __grid_co
                     at.skip(i, p.nstage);
                     uint32_t hi[16], lo[16];
                     const uint8_t* seg = raw(rs) + 2 * q * 2 * seg_bytes + (i >> 1) * seg_bytes;
-                    qg_convert<NP, NG>(seg, i & 1, lane, m[0][0], m[0][1], hi, lo);
+                    qg_convert<NP, NG>(seg, i & 1, lane, magic, m[0][0], m[0][1], hi, lo);
                     if (!(ok = qg_wait(smem_u32(&empty[at.s]), at.ph ^ 1u, flags, p.err))) break;
                     tc_fence_after();
                     __syncwarp();
                     const uint32_t col = tmem + ((uint32_t)(32 * q) << 16) + (uint32_t)(2 * p.accw + 32 * NP * at.s);
                     tc_st_frag(col, hi);
                     if (NP == 2) tc_st_frag(col + 32, lo);
-                    qg_convert<NP, NG>(seg + 2 * seg_bytes, i & 1, lane, m[1][0], m[1][1], hi, lo);
+                    qg_convert<NP, NG>(seg + 2 * seg_bytes, i & 1, lane, magic, m[1][0], m[1][1], hi, lo);
                     tc_st_frag(col + (16u << 16), hi);
                     if (NP == 2) tc_st_frag(col + (16u << 16) + 32, lo);
                     asm volatile("tcgen05.wait::st.sync.aligned;" ::: "memory");

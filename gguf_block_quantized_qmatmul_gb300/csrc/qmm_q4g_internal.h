@@ -47,14 +47,13 @@ struct QgRowsPlan {
     int nb = 0;            // 8-column MMA blocks
     int np = 0;            // 16-bit pieces per activation value
     int warps = 0, wk = 0; // warps per block, warps that split K
-    int useg = 0, depth = 0; // segments per unit, units in a warp's ring
     int blocks = 0;
-    int off_zero = 0, off_red = 0, off_ring = 0, off_bar = 0;
+    int off_zero = 0, off_red = 0, off_ring = 0;
     size_t smem = 0;
     size_t workspace = 0;  // P_DOWN by expert: f32 partial rows [T top_k][N]
 };
 QgRowsPlan plan_q4g_rows(const QgCall& c, int sms, int smem_max);
-cudaError_t launch_q4g_rows(const QgRowsPlan& pl, const QgCall& c, void* ws, unsigned* err, int smem_max, cudaStream_t s);
+cudaError_t launch_q4g_rows(const QgRowsPlan& pl, const QgCall& c, void* ws, int smem_max, cudaStream_t s);
 
 // The tcgen05 GEMM.
 struct QgGemmPlan {

@@ -105,14 +105,14 @@ QgRowsPlan plan_q4g_rows(const QgCall& c, int sms, int smem_max) {
     const int seg = qg_seg_bytes(c.w.ng), VS = (int)(c.w.KS * rows_mul);
     auto nb_of = [&](int cols) { const int b = (cols * pl.np + 7) / 8; return b <= 1 ? 1 : b <= 2 ? 2 : 4; };
     auto red = [&](int nb, int warps) { return 2ll * warps * nb * 128 * 4; };
-    // shared memory: activations, the warps' sums, rings of `depth` units and their barriers
-    auto need = [&](int cols, int warps, int useg, int depth) {
-        return cols * row_bytes * rows_mul + 16 + red(nb_of(cols), warps) + (long long)warps * depth * (useg * seg + 8);
+    // shared memory: activations, the warps' sums, their rings
+    auto need = [&](int cols, int warps) {
+        return cols * row_bytes * rows_mul + 16 + red(nb_of(cols), warps) + (long long)warps * kQgDepth * seg;
     };
     const long long room = smem_max - kQgRowStatic - 1024;
-    // as many columns as shared memory holds beside two single segments a warp
-    while (pl.cols > 1 && need(pl.cols, 8, 1, 2) > room) --pl.cols;
-    if (need(pl.cols, 8, 1, 2) > room) return pl;
+    // as many columns as shared memory holds beside eight warps
+    while (pl.cols > 1 && need(pl.cols, 8) > room) --pl.cols;
+    if (need(pl.cols, 8) > room) return pl;
     long long items, most = 0;  // items expected, and at most
     if (c.op == P_DENSE) {
         items = (c.M + pl.cols - 1) / pl.cols;
@@ -131,55 +131,45 @@ QgRowsPlan plan_q4g_rows(const QgCall& c, int sms, int smem_max) {
     double best = 0;
     for (int warps : {24, 16, 8}) {
         if (warps > qg_row_warps(pl.nb)) continue;
-        int useg = token ? 1 : 2, depth = kQgDepthMax;
-        while (depth > 2 && need(pl.cols, warps, useg, depth) > room) --depth;
-        if (need(pl.cols, warps, useg, depth) > room) useg = 1;
-        while (useg == 1 && depth > 2 && need(pl.cols, warps, useg, depth) > room) --depth;
-        if (need(pl.cols, warps, useg, depth) > room) continue;
+        if (need(pl.cols, warps) > room) continue;
         for (int wk = 1; wk <= 8; wk *= 2) {
-            const int us = useg == 2 && (VS + 2 * wk - 1) / (2 * wk) * 2 > (VS + wk - 1) / wk ? 1 : useg;
-            const int wr = warps / wk, nit = (VS + wk * us - 1) / (wk * us);
+            const int wr = warps / wk, nit = (VS + wk - 1) / wk;
             if (wr > 15 && wk > 1) continue;  // named barriers
             const long long work = items * c.w.RB, blocks = work < sms ? work : sms;
             const double share = (double)work / blocks;  // row blocks per block
             // segments a warp takes in turn, its row blocks' barriers and sums (about one each); more warps share an SM's issue slots
-            const double cost = ceil(share / wr) * (nit * us + 1.0) * (warps >= 16 ? warps / 16.0 : 1.0);
+            const double cost = ceil(share / wr) * (nit + 1.0) * (warps >= 16 ? warps / 16.0 : 1.0);
             if (best == 0 || cost < 0.999 * best || (cost <= 1.001 * best && wk > pl.wk)) {
                 best = cost;
                 pl.warps = warps;
                 pl.wk = wk;
-                pl.useg = us;
-                pl.depth = depth;
                 pl.blocks = (int)blocks;
             }
         }
     }
     if (best == 0) return pl;
-    pl.smem = (size_t)need(pl.cols, pl.warps, pl.useg, pl.depth);
+    pl.smem = (size_t)need(pl.cols, pl.warps);
     pl.off_zero = (int)(pl.cols * row_bytes * rows_mul);
     pl.off_red = pl.off_zero + 16;
     pl.off_ring = pl.off_red + (int)red(pl.nb, pl.warps);
-    pl.off_bar = pl.off_ring + pl.warps * pl.depth * pl.useg * seg;
     if (c.op == P_DOWN && !pl.by_slot) pl.workspace = (size_t)slots * c.w.N * 4;
     pl.ok = true;
     return pl;
 }
 
-cudaError_t launch_q4g_rows(const QgRowsPlan& pl, const QgCall& c, void* ws, unsigned* err, int smem_max, cudaStream_t s) {
+cudaError_t launch_q4g_rows(const QgRowsPlan& pl, const QgCall& c, void* ws, int smem_max, cudaStream_t s) {
     QgRowsParams p;
     p.c = c;
     p.part = static_cast<float*>(ws);
-    p.err = err;
     p.by_slot = pl.by_slot;
     p.cols = pl.cols;
     p.np = pl.np;
     p.wk = pl.wk;
-    p.useg = pl.useg;
-    p.depth = pl.depth;
+    p.wr = pl.warps / pl.wk;
+    p.wk_log2 = pl.wk == 1 ? 0 : pl.wk == 2 ? 1 : pl.wk == 4 ? 2 : 3;
     p.off_zero = pl.off_zero;
     p.off_red = pl.off_red;
     p.off_ring = pl.off_ring;
-    p.off_bar = pl.off_bar;
     cudaError_t e = pl.nb == 1   ? launch_q4g_rows_1(pl, p, smem_max, s)
                     : pl.nb == 2 ? launch_q4g_rows_2(pl, p, smem_max, s)
                                  : launch_q4g_rows_4(pl, p, smem_max, s);

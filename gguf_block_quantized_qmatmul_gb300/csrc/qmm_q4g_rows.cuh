@@ -13,14 +13,15 @@
 // The kernel is bound by the weight stream (0.5 + 4 / G bytes a weight).  The
 // work, items (a group of activation rows with their weight matrix) times row
 // blocks, is dealt to one block an SM in equal contiguous shares.  Every warp
-// has its own ring of shared-memory stages, each filled by one bulk copy of a
-// unit (up to two consecutive segments of a row block) that one lane issues;
-// a tile of 16 rows x 64 K is then one conflict-free 16-byte load a lane, in
-// fragment order, and about 9 (f16) or 11 (bf16) instructions turn a word of
-// eight codes into MMA operands.  (Loads straight into registers, four segments
-// ahead, measured 44 us at 1 x 28672 x 8192: the stages' registers left 16 warps an SM, and waiting for the
-// oldest load waited for younger ones too.)  wk warps split a row block's K and
-// add their sums through shared memory, one barrier among them per row block.
+// has its own ring of kQgDepth segments in shared memory, filled by asynchronous
+// 16-byte copies (codes: each lane copies what it will read); a tile of 16 rows x
+// 64 K is then one conflict-free 16-byte load a lane, in fragment order, and
+// about 9 (f16) or 11 (bf16) instructions turn a word of eight codes into MMA
+// operands.  Measured at 1 x 28672 x 8192 (f16, G = 64): loads straight into
+// registers, four segments ahead, 44 us (16 warps an SM, and waiting for the
+// oldest load waited for younger ones too); one bulk copy per two segments 35
+// us, and still 30 us with no arithmetic at all.  wk warps split a row block's K
+// and add their sums through shared memory, one barrier among them per row block.
 // Activations are staged once per item in the order the MMAs read them (16
 // bytes a lane, conflict-free).  Weights are constant, so a dense call's first
 // copies are issued before the grid it depends on has completed.
@@ -30,7 +31,7 @@
 
 namespace qmm {
 
-constexpr int kQgDepthMax = 4;     // stages of a warp's ring, at most
+constexpr int kQgDepth = 4;        // segments in a warp's ring
 // warps per block, at most: more columns need more registers
 __host__ __device__ constexpr int qg_row_warps(int nb) { return nb == 1 ? 24 : 16; }
 constexpr int kQgRowMaxE = 512;    // experts whose items a block can look up
@@ -39,13 +40,24 @@ constexpr int kQgRowStatic = 4096; // the kernel's static arrays, rounded up
 struct QgRowsParams {
     QgCall c;
     float* part;   // P_DOWN by expert: [T top_k][N]
-    unsigned* err;
-    int by_slot, cols, np, wk;
-    int useg;      // segments per unit
-    int depth;     // stages per warp
-    int off_zero, off_red, off_ring, off_bar;
+    int by_slot, cols, np, wk, wk_log2, wr;
+    int off_zero, off_red, off_ring;
 };
 
+__device__ __forceinline__ void cp_async16(uint32_t dst, const void* src) {
+    asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" ::"r"(dst), "l"(src) : "memory");
+}
+__device__ __forceinline__ void cp_async_commit() { asm volatile("cp.async.commit_group;" ::: "memory"); }
+template <int N>
+__device__ __forceinline__ void cp_async_wait() { asm volatile("cp.async.wait_group %0;" ::"n"(N) : "memory"); }
+
+// (v & mask) | c in one instruction: c stays in a register (with two constants the compiler takes two)
+template <uint32_t MASK>
+__device__ __forceinline__ uint32_t and_or(uint32_t v, uint32_t c) {
+    uint32_t d;
+    asm("lop3.b32 %0, %1, %2, %3, 0xea;" : "=r"(d) : "r"(v), "n"(MASK), "r"(c));
+    return d;
+}
 // FIRST: d = A B, else d += A B
 template <bool BF, bool FIRST>
 __device__ __forceinline__ void qg_mma(float d[4], const uint32_t a[4], uint32_t b0, uint32_t b1) {
@@ -67,13 +79,14 @@ __device__ __forceinline__ void qg_mma(float d[4], const uint32_t a[4], uint32_t
 // registers.  f16: 0x6400 | q is 1024 + q and 0x6400 | q << 4 is 1024 + 16 q
 // (one less shift); bf16: 0x4300 | q is 128 + q.  zl, zh: the constants of
 // rows g and g + 8 (qg_zero).
+// magic: 0x64006400 (f16) or 0x43004300 (bf16) in a register.
 template <bool BF>
-__device__ __forceinline__ void qg_codes(uint32_t w, uint32_t zl, uint32_t zh, uint32_t a[4]) {
+__device__ __forceinline__ void qg_codes(uint32_t w, uint32_t magic, uint32_t zl, uint32_t zh, uint32_t a[4]) {
     if (BF) {
         const __nv_bfloat162 l = *reinterpret_cast<__nv_bfloat162*>(&zl), h = *reinterpret_cast<__nv_bfloat162*>(&zh);
 #pragma unroll
         for (int i = 0; i < 4; ++i) {
-            uint32_t v = ((w >> (4 * i)) & 0x000f000fu) | 0x43004300u;
+            uint32_t v = and_or<0x000f000fu>(w >> (4 * i), magic);
             const __nv_bfloat162 r = __hsub2(*reinterpret_cast<__nv_bfloat162*>(&v), i & 1 ? h : l);
             a[i] = *reinterpret_cast<const uint32_t*>(&r);
         }
@@ -83,7 +96,7 @@ __device__ __forceinline__ void qg_codes(uint32_t w, uint32_t zl, uint32_t zh, u
 #pragma unroll
         for (int i = 0; i < 2; ++i) {
             const uint32_t v = i ? w >> 8 : w;
-            uint32_t lo = (v & 0x000f000fu) | 0x64006400u, hi = (v & 0x00f000f0u) | 0x64006400u;
+            uint32_t lo = and_or<0x000f000fu>(v, magic), hi = and_or<0x00f000f0u>(v, magic);
             const __half2 r0 = __hsub2(*reinterpret_cast<__half2*>(&lo), l);
             const __half2 r1 = __hfma2(*reinterpret_cast<__half2*>(&hi), sixteenth, h);
             a[2 * i] = *reinterpret_cast<const uint32_t*>(&r0);
@@ -167,29 +180,20 @@ __global__ void __launch_bounds__(qg_row_warps(NB) * 32, 1) q4g_rows_kernel(cons
     __shared__ float s_wt[kQgMaxK];    // and their weights
     __shared__ int s_row[64];          // by expert: the columns' slots
     __shared__ int ts[kQgRowMaxE + 1]; // by expert: items before each
-    __shared__ int s_abort;
     const QgCall& c = p.c;
     const QgWeights& w = c.w;
-    const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31, g = lane >> 2, t = lane & 3, nthr = blockDim.x;
-    const int wk = p.wk, wr = nthr / 32 / wk, kw = warp % wk, rw = warp / wk;
+    // the warp's index from one lane, so that what follows from it is known to be uniform
+    const int tid = threadIdx.x, warp = __shfl_sync(0xffffffffu, tid >> 5, 0), lane = tid & 31, g = lane >> 2, t = lane & 3, nthr = blockDim.x;
+    const int wk = p.wk, wr = p.wr, kw = warp & (wk - 1), rw = warp >> p.wk_log2;
     constexpr int seg_bytes = qg_seg_bytes(NG), segk = 128 / NG;
-    const int unit_bytes = p.useg * seg_bytes;
-    uint64_t* full = reinterpret_cast<uint64_t*>(sm + p.off_bar) + warp * p.depth;
-    uint8_t* ring = sm + p.off_ring + warp * p.depth * unit_bytes;
-    if (lane == 0) {
-        for (int i = 0; i < p.depth; ++i) mbar_init(smem_u32(&full[i]), 1);
-        fence_mbar_init();
-    }
-    if (tid == 0) {
-        s_abort = 0;
-        *reinterpret_cast<uint4*>(sm + p.off_zero) = make_uint4(0u, 0u, 0u, 0u);  // what lanes without a column read
-    }
-    __syncthreads();
+    uint8_t* ring = sm + p.off_ring + warp * (kQgDepth * seg_bytes);
+    const uint32_t magic = opaque(BF ? 0x43004300u : 0x64006400u);
+    if (tid == 0) *reinterpret_cast<uint4*>(sm + p.off_zero) = make_uint4(0u, 0u, 0u, 0u);  // what lanes without a column read
     grid_dep_launch();
 
     const int nex = TOK ? c.r.top_k : 1;
     const int VS = nex * w.KS;                             // virtual segments: TOK's experts end to end
-    const int nit = (VS + wk * p.useg - 1) / (wk * p.useg);  // units per warp and row block
+    const int nit = (VS + wk - 1) >> p.wk_log2;            // segments per warp and row block
     const long long rb_bytes = (long long)w.KS * seg_bytes;
     const bool by_expert = c.op != P_DENSE && !p.by_slot;
     int items = c.op == P_DENSE ? (c.M + p.cols - 1) / p.cols : TOK ? c.r.T : c.r.T * c.r.top_k;
@@ -225,9 +229,7 @@ __global__ void __launch_bounds__(qg_row_warps(NB) * 32, 1) q4g_rows_kernel(cons
     const long long work = (long long)items * w.RB;
     const long long w0 = (long long)blockIdx.x * work / gridDim.x, w1 = (long long)(blockIdx.x + 1) * work / gridDim.x;
 
-    QgRing lr, cr;       // the ring's next stage to fill, to read
-    int in_flight = 0;   // copies issued and not yet waited for
-    bool ok = true, waited = by_expert;
+    bool waited = by_expert;
     float acc[NB][4];
 #pragma unroll
     for (int b = 0; b < NB; ++b)
@@ -238,6 +240,7 @@ __global__ void __launch_bounds__(qg_row_warps(NB) * 32, 1) q4g_rows_kernel(cons
     int flip = 0;                   // which of its two areas a row block's sums use
 
     for (long long at = w0; at < w1;) {
+        cp_async_wait<0>();  // the last item's (empty) groups
         const int item = (int)(at / w.RB), rb0 = (int)(at - (long long)item * w.RB);
         const int rb1 = (int)min((long long)w.RB, rb0 + (w1 - at));
         at += rb1 - rb0;
@@ -275,40 +278,47 @@ __global__ void __launch_bounds__(qg_row_warps(NB) * 32, 1) q4g_rows_kernel(cons
         }
         const uint8_t* base = w.data + expert * w.expert_stride;
         const int groups = (rb1 - rb0 + wr - 1) / wr, total = rb0 + rw < rb1 ? ((rb1 - rb0 - rw + wr - 1) / wr) * nit : 0;
-        // load cursor: unit li of row block lrb
-        int li = 0, lrb = rb0 + rw, lj = 0, lseg = kw * p.useg;
-        auto load = [&]() {
-            const int v = (kw + li * wk) * p.useg;
-            if (v < VS) {
-                const uint8_t* src;
-                int nseg = min(p.useg, VS - v);
-                if (TOK) {  // one segment a unit
-                    while (lseg >= w.KS) {
-                        lseg -= w.KS;
-                        ++lj;
+        // load cursor: virtual segment lv of row block lrb; this lane's bytes of it at lp; ring place ls
+        int left = total, li = 0, lv = kw, ls = 0, lrb = rb0 + rw, lj = 0, lseg = kw;
+        const uint8_t* lp = base + lrb * rb_bytes + kw * seg_bytes + lane * 16;
+        const long long lback = wr * rb_bytes - (long long)nit * wk * seg_bytes;
+        const uint32_t to = smem_u32(ring) + lane * 16;
+        auto load = [&]() {  // a group of copies, empty past the end, so that the groups' count is the ring's
+            if (left > 0) {
+                --left;
+                if (lv < VS) {
+                    if (TOK) {
+                        while (lseg >= w.KS) {
+                            lseg -= w.KS;
+                            ++lj;
+                        }
+                        lp = w.data + (long long)max(s_e[lj], 0) * w.expert_stride + lrb * rb_bytes + lseg * seg_bytes + lane * 16;
                     }
-                    src = w.data + (long long)max(s_e[lj], 0) * w.expert_stride + lrb * rb_bytes + lseg * seg_bytes;
-                } else {
-                    src = base + lrb * rb_bytes + v * seg_bytes;
+                    const uint32_t d = to + ls * seg_bytes;
+                    cp_async16(d, lp);
+                    cp_async16(d + kQgTile, lp + kQgTile);
+                    if (lane < 4 * NG) cp_async16(d + 2 * kQgTile, lp + 2 * kQgTile);
                 }
-                if (lane == 0) {
-                    const uint32_t bar = smem_u32(&full[lr.s]);
-                    mbar_arrive_tx(bar, (uint32_t)(nseg * seg_bytes));
-                    bulk_g2s(smem_u32(ring + lr.s * unit_bytes), src, (uint32_t)(nseg * seg_bytes), bar);
+                lv += wk;
+                if (TOK) lseg += wk;
+                else lp += wk * seg_bytes;
+                if (++li == nit) {
+                    li = 0;
+                    lv = kw;
+                    if (TOK) {
+                        lrb += wr;
+                        lj = 0;
+                        lseg = kw;
+                    } else {
+                        lp += lback;
+                    }
                 }
-                lr.next(p.depth);
-                ++in_flight;
             }
-            lseg += wk;
-            if (++li == nit) {
-                li = 0;
-                lrb += wr;
-                lj = 0;
-                lseg = kw;
-            }
+            ls = ls + 1 == kQgDepth ? 0 : ls + 1;
+            cp_async_commit();
         };
-        int ahead = 0;  // iterations whose unit has been asked for
-        for (; ok && ahead < p.depth && ahead < total; ++ahead) load();
+#pragma unroll
+        for (int i = 0; i < kQgDepth - 1; ++i) load();
         if (!waited) {
             grid_dep_wait();
             waited = true;
@@ -344,84 +354,84 @@ __global__ void __launch_bounds__(qg_row_warps(NB) * 32, 1) q4g_rows_kernel(cons
             xq[b] = on ? ncol * 64 : 0;
             xp[b] = on ? (8 * b + g) * 64 + t * 16 : p.off_zero;
         }
-        int crb = rb0 + rw;
+        int crb = rb0 + rw, cs = 0;  // row block, ring place
         for (int gi = 0; gi < groups; ++gi, crb += wr, flip ^= 1) {
             if (crb >= rb1) continue;
-            int cj = 0, cseg = kw;
-            for (int ci = 0; ci < nit; ++ci) {
-                const int v = (kw + ci * wk) * p.useg;
-                if (v < VS) {
-                    if (ok) ok = qg_wait(smem_u32(&full[cr.s]), cr.ph, &s_abort, p.err);
-                    if (!ok) continue;
-                    --in_flight;
-                    float wt = 1.0f;
-                    bool on = true;
-                    if (TOK) {
-                        while (cseg >= w.KS) {
-                            cseg -= w.KS;
-                            ++cj;
-                        }
-                        on = s_e[cj] >= 0;
-                        wt = s_wt[cj];
+            int cj = 0, cseg = kw, v = kw;
+            int xo[NB];
+#pragma unroll
+            for (int b = 0; b < NB; ++b) xo[b] = xp[b] + kw * 4 * xq[b];
+            for (int ci = 0; ci < nit; ++ci, v += wk) {
+                cp_async_wait<kQgDepth - 2>();
+                __syncwarp();  // every lane's copies of this segment have landed, and the last one has been read
+                load();
+                const uint8_t* sp = ring + cs * seg_bytes;
+                cs = cs + 1 == kQgDepth ? 0 : cs + 1;
+                bool on = v < VS;
+                float wt = 1.0f;
+                if (TOK && on) {
+                    while (cseg >= w.KS) {
+                        cseg -= w.KS;
+                        ++cj;
                     }
-                    const uint8_t* sp = ring + cr.s * unit_bytes;
-                    cr.next(p.depth);
-                    const int nseg = on ? min(p.useg, VS - v) : 0;
-                    for (int sg = 0; sg < nseg; ++sg, sp += seg_bytes) {
-                        const uint4 c0 = reinterpret_cast<const uint4*>(sp)[lane], c1 = reinterpret_cast<const uint4*>(sp + kQgTile)[lane];
-                        uint32_t sw[2 * NG];
-                        const uint8_t* sq = sp + 2 * kQgTile + g * (8 * NG);
-                        if (NG == 1) {
-                            const uint2 u = *reinterpret_cast<const uint2*>(sq);
-                            sw[0] = u.x;
-                            sw[1] = u.y;
-                        } else {
-#pragma unroll
-                            for (int i = 0; i < NG / 2; ++i) {
-                                const uint4 u = reinterpret_cast<const uint4*>(sq)[i];
-                                sw[4 * i] = u.x;
-                                sw[4 * i + 1] = u.y;
-                                sw[4 * i + 2] = u.z;
-                                sw[4 * i + 3] = u.w;
-                            }
-                        }
-                        float gr[NB][4];
-#pragma unroll
-                        for (int q4 = 0; q4 < 4; ++q4) {  // 32 K a step
-                            const int gi4 = q4 * 32 / segk;
-                            const uint32_t sw0 = sw[2 * gi4], sw1 = sw[2 * gi4 + 1];
-                            const uint32_t zl = qg_zero<BF>(sw0, false), zh = qg_zero<BF>(sw1, true);
-                            const uint4 cw = q4 < 2 ? c0 : c1;
-                            uint32_t a0[4], a1[4];
-                            qg_codes<BF>(q4 & 1 ? cw.z : cw.x, zl, zh, a0);
-                            qg_codes<BF>(q4 & 1 ? cw.w : cw.y, zl, zh, a1);
-                            const bool start = q4 * 32 % segk == 0;
-#pragma unroll
-                            for (int b = 0; b < NB; ++b) {
-                                const uint4 xv = *reinterpret_cast<const uint4*>(sm + xp[b] + ((v + sg) * 4 + q4) * xq[b]);
-                                if (start) qg_mma<BF, true>(gr[b], a0, xv.x, xv.y);
-                                else qg_mma<BF, false>(gr[b], a0, xv.x, xv.y);
-                                qg_mma<BF, false>(gr[b], a1, xv.z, xv.w);
-                            }
-                            if ((q4 + 1) * 32 % segk == 0) {  // the group's end
-                                const float s0 = TOK ? qg_scale(sw0) * wt : qg_scale(sw0), s1 = TOK ? qg_scale(sw1) * wt : qg_scale(sw1);
-#pragma unroll
-                                for (int b = 0; b < NB; ++b) {
-                                    acc[b][0] = fmaf(s0, gr[b][0], acc[b][0]);
-                                    acc[b][1] = fmaf(s0, gr[b][1], acc[b][1]);
-                                    acc[b][2] = fmaf(s1, gr[b][2], acc[b][2]);
-                                    acc[b][3] = fmaf(s1, gr[b][3], acc[b][3]);
-                                }
-                            }
-                        }
-                    }
+                    on = s_e[cj] >= 0;
+                    wt = s_wt[cj];
                 }
                 if (TOK) cseg += wk;
-                __syncwarp();  // the stage has been read
-                if (ahead < total) {
-                    load();
-                    ++ahead;
+                if (on) {
+                    const uint4 c0 = reinterpret_cast<const uint4*>(sp)[lane], c1 = reinterpret_cast<const uint4*>(sp + kQgTile)[lane];
+                    uint32_t sw[2 * NG];
+                    const uint8_t* sq = sp + 2 * kQgTile + g * (8 * NG);
+                    if (NG == 1) {
+                        const uint2 u = *reinterpret_cast<const uint2*>(sq);
+                        sw[0] = u.x;
+                        sw[1] = u.y;
+                    } else {
+#pragma unroll
+                        for (int i = 0; i < NG / 2; ++i) {
+                            const uint4 u = reinterpret_cast<const uint4*>(sq)[i];
+                            sw[4 * i] = u.x;
+                            sw[4 * i + 1] = u.y;
+                            sw[4 * i + 2] = u.z;
+                            sw[4 * i + 3] = u.w;
+                        }
+                    }
+                    float gr[NB][4];
+                    uint32_t zl = 0, zh = 0;
+#pragma unroll
+                    for (int q4 = 0; q4 < 4; ++q4) {  // 32 K a step
+                        const int gi4 = q4 * 32 / segk;
+                        const uint32_t sw0 = sw[2 * gi4], sw1 = sw[2 * gi4 + 1];
+                        const bool start = q4 * 32 % segk == 0;
+                        if (start) {
+                            zl = qg_zero<BF>(sw0, false);
+                            zh = qg_zero<BF>(sw1, true);
+                        }
+                        const uint4 cw = q4 < 2 ? c0 : c1;
+                        uint32_t a0[4], a1[4];
+                        qg_codes<BF>(q4 & 1 ? cw.z : cw.x, magic, zl, zh, a0);
+                        qg_codes<BF>(q4 & 1 ? cw.w : cw.y, magic, zl, zh, a1);
+#pragma unroll
+                        for (int b = 0; b < NB; ++b) {
+                            const uint4 xv = *reinterpret_cast<const uint4*>(sm + xo[b] + q4 * xq[b]);
+                            if (start) qg_mma<BF, true>(gr[b], a0, xv.x, xv.y);
+                            else qg_mma<BF, false>(gr[b], a0, xv.x, xv.y);
+                            qg_mma<BF, false>(gr[b], a1, xv.z, xv.w);
+                        }
+                        if ((q4 + 1) * 32 % segk == 0) {  // the group's end
+                            const float s0 = TOK ? qg_scale(sw0) * wt : qg_scale(sw0), s1 = TOK ? qg_scale(sw1) * wt : qg_scale(sw1);
+#pragma unroll
+                            for (int b = 0; b < NB; ++b) {
+                                acc[b][0] = fmaf(s0, gr[b][0], acc[b][0]);
+                                acc[b][1] = fmaf(s0, gr[b][1], acc[b][1]);
+                                acc[b][2] = fmaf(s1, gr[b][2], acc[b][2]);
+                                acc[b][3] = fmaf(s1, gr[b][3], acc[b][3]);
+                            }
+                        }
+                    }
                 }
+#pragma unroll
+                for (int b = 0; b < NB; ++b) xo[b] += wk * 4 * xq[b];
             }
             // the row block's sums
             float* mine = red + (flip * (nthr / 32) + warp) * kRed;
@@ -441,7 +451,7 @@ __global__ void __launch_bounds__(qg_row_warps(NB) * 32, 1) q4g_rows_kernel(cons
             if (wk == 1) __syncwarp();
             else asm volatile("bar.sync %0, %1;" ::"r"(1 + rw), "r"(wk * 32) : "memory");
             const float* from = red + (flip * (nthr / 32) + rw * wk) * kRed;
-            const int per = w.paired ? 8 : 16;
+            const int per_log2 = w.paired ? 3 : 4;  // rows of y per row block
             auto sum = [&](int r, int row) {
                 float v2 = 0.0f;
                 for (int pc = 0; pc < p.np; ++pc) {
@@ -452,8 +462,8 @@ __global__ void __launch_bounds__(qg_row_warps(NB) * 32, 1) q4g_rows_kernel(cons
                 return v2;
             };
             // the warps take turns at a short row block's sums
-            for (int o = ((kw + gi) & (wk - 1)) * 32 + lane; o < per * rows; o += wk * 32) {
-                const int row = o % per, r = o / per;
+            for (int o = ((kw + gi) & (wk - 1)) * 32 + lane; o < rows << per_log2; o += wk * 32) {
+                const int row = o & ((1 << per_log2) - 1), r = o >> per_log2;
                 const float v0 = sum(r, row);
                 if (c.op == P_GATE_UP) {
                     const float u = sum(r, row + 8);
@@ -475,9 +485,6 @@ __global__ void __launch_bounds__(qg_row_warps(NB) * 32, 1) q4g_rows_kernel(cons
         }
     }
     if (!waited) grid_dep_wait();
-    // after a wait that gave up, the copies still in flight must land before the block can exit
-    if (lane == 0)
-        for (; in_flight > 0; --in_flight, cr.next(p.depth)) mbar_drain(smem_u32(&full[cr.s]), cr.ph, &s_abort, p.err);
 }
 
 }  // namespace qmm
