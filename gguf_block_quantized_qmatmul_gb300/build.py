@@ -2,7 +2,8 @@
 
 Translation units are compiled in parallel and linked into
 ``gguf_block_quantized_qmatmul_gb300/_build/libqmm.so``.  No fast-math flags:
-the quantizers rely on IEEE round-to-nearest intrinsics.
+the quantizers rely on IEEE round-to-nearest intrinsics.  Beside it the host
+compiler builds ``_qmm_torch.so``, the CPython extension that q4g.py calls.
 """
 from __future__ import annotations
 
@@ -15,6 +16,7 @@ HERE = os.path.dirname(os.path.abspath(__file__))
 CSRC = os.path.join(HERE, "csrc")
 BUILD = os.path.join(HERE, "_build")
 LIB = os.path.join(BUILD, "libqmm.so")
+BINDING = os.path.join(BUILD, "_qmm_torch.so")  # CPython extension of q4g.py's calls
 ROOT = os.path.dirname(HERE)
 UNITS = ["qmm_api", "qmm_quant", "qmm_stream_q8_0", "qmm_stream_q4_k", "qmm_stream_x_0", "qmm_stream_q6_k", "qmm_gemv_q8_0", "qmm_gemv_q4_k", "qmm_dmma", "qmm_dmma_x_0", "qmm_dmma_q6_k", "qmm_tc", "qmm_tcx", "qmm_tcx_f32", "qmm_static_ws", "qmm_batch", "qmm_batch_mix", "qmm_q4g_api", "qmm_q4g_layout", "qmm_q4g_rows", "qmm_q4g_rows_1", "qmm_q4g_rows_2", "qmm_q4g_rows_4",
          "qmm_q4g_gemm", "qmm_moe_route"]
@@ -36,10 +38,25 @@ def _deps():
     return out
 
 
+def _binding_command(out: str) -> list[str]:
+    """Host compiler command for the CPython extension, linked against this torch and libqmm.so."""
+    import sysconfig
+
+    import torch
+    from torch.utils import cpp_extension
+    cuda = os.path.dirname(os.path.dirname(_nvcc()))
+    inc = [*cpp_extension.include_paths(), sysconfig.get_paths()["include"], os.path.join(cuda, "include")]
+    lib = os.path.join(os.path.dirname(torch.__file__), "lib")
+    return [os.environ.get("CXX", "g++"), "-O2", "-std=c++17", "-fPIC", "-shared", "-w",
+            f"-D_GLIBCXX_USE_CXX11_ABI={int(torch.compiled_with_cxx11_abi())}", *(f"-I{i}" for i in inc),
+            os.path.join(CSRC, "qmm_torch.cpp"), "-o", out, f"-L{lib}", "-lc10", "-lc10_cuda", "-ltorch_cpu", "-ltorch_cuda", "-ltorch",
+            "-ltorch_python", f"-Wl,-rpath,{lib}", f"-L{BUILD}", "-Wl,--no-as-needed", "-l:libqmm.so", "-Wl,-rpath,$ORIGIN"]
+
+
 def up_to_date() -> bool:
-    if not os.path.exists(LIB):
+    if not os.path.exists(LIB) or not os.path.exists(BINDING):
         return False
-    t = os.path.getmtime(LIB)
+    t = min(os.path.getmtime(LIB), os.path.getmtime(BINDING))
     return all(os.path.getmtime(d) <= t for d in _deps())
 
 
@@ -54,12 +71,21 @@ def build(force: bool = False, verbose: bool = False) -> str:
         log = open(os.path.join(BUILD, u + ".ptxas.txt"), "w")
         cmd = [nvcc, *ARCH, *FLAGS, "-c", os.path.join(CSRC, u + ".cu"), "-o", obj]
         procs.append((u, subprocess.Popen(cmd, stdout=log, stderr=subprocess.STDOUT), log))
+    # the extension needs libqmm.so's name only: it is linked against an empty one while that compiles
+    tmp_b = BINDING + f".tmp{os.getpid()}"
+    stub = not os.path.exists(LIB)
+    if stub:
+        subprocess.run([os.environ.get("CXX", "g++"), "-shared", "-fPIC", "-x", "c++", "/dev/null", "-o", LIB], check=True)
+    log = open(os.path.join(BUILD, "qmm_torch.ptxas.txt"), "w")
+    procs.append(("qmm_torch", subprocess.Popen(_binding_command(tmp_b), stdout=log, stderr=subprocess.STDOUT), log))
     failed = []
     for u, p, log in procs:
         p.wait()
         log.close()
         if p.returncode != 0:
             failed.append(u)
+    if stub:
+        os.remove(LIB)
     if failed:
         msgs = "".join(open(os.path.join(BUILD, u + ".ptxas.txt")).read()[-4000:] for u in failed)
         raise RuntimeError(f"nvcc failed for {failed}:\n{msgs}")
@@ -67,6 +93,9 @@ def build(force: bool = False, verbose: bool = False) -> str:
     cmd = [nvcc, *ARCH, "-shared", "-o", tmp] + [os.path.join(BUILD, u + ".o") for u in UNITS]
     subprocess.run(cmd, check=True)
     os.replace(tmp, LIB)
+    os.replace(tmp_b, BINDING)
+    for f in (LIB, BINDING):
+        os.utime(f)
     if verbose:
         print(f"built {LIB}", file=sys.stderr)
     return LIB

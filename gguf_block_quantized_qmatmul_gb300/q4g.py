@@ -12,17 +12,21 @@ its types, limits and errors).
 
 Tensors are CUDA tensors; activations are f32, f16 or bf16 with their last
 dimension contiguous (rows may be further apart).  Work goes to the current
-stream, or to `stream` (temporaries and outputs are then allocated on it).
+stream, or to `stream` (temporaries and outputs are then allocated on it).  The
+products and the routing are called through ``_build/_qmm_torch.so`` (a CPython
+extension over the same C ABI), which costs a call less than ctypes.
 """
 from __future__ import annotations
 
 import contextlib
 import ctypes
+import importlib.util
+import os
 from typing import NamedTuple, Optional
 
 import torch
 
-from . import _check, _lib
+from . import _build, _check, _lib
 
 FLOATS = {torch.float32: 0, torch.float16: 1, torch.bfloat16: 2}
 SCORES = {"softmax": 0, "sigmoid": 1}
@@ -67,8 +71,33 @@ def declare(lib) -> None:
         f.argtypes, f.restype = args, res
 
 
-_raw_stream = torch._C._cuda_getCurrentRawStream if hasattr(torch._C, "_cuda_getCurrentRawStream") else (
-    lambda device: torch.cuda.current_stream(device).cuda_stream)
+def _load_binding():
+    path = _build.BINDING
+    if not os.path.exists(path):
+        raise ImportError(f"{os.path.basename(path)} is not built ({path}); run __graft_entry__.build() or "
+                          f"python -m gguf_block_quantized_qmatmul_gb300.build")
+    _lib()
+    spec = importlib.util.spec_from_file_location("_qmm_torch", path)
+    module = importlib.util.module_from_spec(spec)
+    spec.loader.exec_module(module)
+    return module
+
+
+class _Binding:
+    """The extension's functions, loaded at the first call."""
+
+    def __getattr__(self, name):
+        module = _load_binding()
+        for f in ("matmul", "route", "gate_up", "down"):
+            setattr(self, f, getattr(module, f))
+        return getattr(module, name)
+
+
+_binding = _Binding()
+
+
+def _raw_stream(device: int) -> int:
+    return torch.cuda.current_stream(device).cuda_stream
 
 
 def _on(stream):
@@ -91,16 +120,6 @@ class Q4GWeights:
         self.device = data.get_device()
         self._desc = _Desc(data.data_ptr(), experts, N, K, group, int(gate_up))
         self._ptr = ctypes.addressof(self._desc)
-        self._workspace = {}  # bytes by (call, type, rows, top_k)
-
-    def _workspace_bytes(self, name: str, *args) -> int:
-        key = (name,) + args
-        n = self._workspace.get(key)
-        if n is None:
-            if len(self._workspace) > 4096:
-                self._workspace.clear()
-            n = self._workspace[key] = int(getattr(_lib(), name + "_workspace")(self._ptr, *args))
-        return n
 
 
 class Route(NamedTuple):
@@ -166,54 +185,20 @@ def q4g_dequantize(w: Q4GWeights, out: torch.Tensor | None = None, stream=None) 
     return out
 
 
-def _activations(w: Q4GWeights, x: torch.Tensor, dims: int) -> tuple[int, int]:
-    """(type, elements from a row to the next) of activations [.., K]."""
-    xt = FLOATS.get(x.dtype)
-    if xt is None or x.dim() != dims or x.shape[-1] != w.K or x.get_device() != w.device:
-        raise ValueError(f"activations are f32, f16 or bf16, {dims}-dimensional, {w.K} wide, on the weights' device")
-    if x.is_contiguous():
-        return xt, w.K
-    _need(x.stride(-1) == 1 and (dims == 2 or x.shape[1] == 1 or x.shape[0] == 1 or x.stride(0) == x.shape[1] * x.stride(1)),
-          "rows of activations are contiguous and evenly apart")
-    return xt, x.stride(0) if dims == 2 or x.shape[1] == 1 else x.stride(1)
-
-
-def _output(out, shape, x):
-    if out is None:
-        return torch.empty(shape, dtype=x.dtype, device=x.device)
-    _need(tuple(out.shape) == tuple(shape) and out.dtype == x.dtype and out.is_contiguous() and out.get_device() == x.get_device(),
-          f"out is contiguous {tuple(shape)}, of the activations' type and device")
-    return out
-
-
-def _buffer(workspace, need, x):
-    """(pointer, bytes, tensor): a caller's workspace as it is (the library checks its size), else a new one."""
-    if workspace is not None:
-        return workspace.data_ptr(), workspace.numel() * workspace.element_size(), workspace
-    if not need:
-        return 0, 0, None
-    t = torch.empty(need, dtype=torch.uint8, device=x.device)
-    return t.data_ptr(), need, t
-
-
 def q4g_matmul(w: Q4GWeights, x: torch.Tensor, out: torch.Tensor | None = None, workspace: torch.Tensor | None = None,
                stream=None) -> torch.Tensor:
     """y [M, N] = x [M, K] . W^T (one weight matrix)."""
     if stream is not None:
         with _on(stream):
             return q4g_matmul(w, x, out, workspace)
-    xt, ld = _activations(w, x, 2)
-    M = x.shape[0]
-    out = _output(out, (M, w.N), x)
-    ptr, size, keep = _buffer(workspace, w._workspace_bytes("qmm_q4g_matmul", xt, M), x)
-    status = _lib().qmm_q4g_matmul(w._ptr, xt, x.data_ptr(), ld, M, out.data_ptr(), ptr, size, _raw_stream(w.device))
-    if status:
-        _check(status, "qmm_q4g_matmul")
-    return out
+    y = _binding.matmul(w._ptr, w.device, x, out, workspace)
+    if type(y) is int:
+        _check(y, "qmm_q4g_matmul")
+    return y
 
 
 def q4g_matmul_workspace(w: Q4GWeights, dtype: torch.dtype, M: int) -> int:
-    return w._workspace_bytes("qmm_q4g_matmul", FLOATS[dtype], M)
+    return int(_lib().qmm_q4g_matmul_workspace(w._ptr, FLOATS[dtype], M))
 
 
 def moe_route(logits: torch.Tensor, top_k: int, score: str = "softmax", bias: torch.Tensor | None = None, groups: int = 1,
@@ -225,41 +210,10 @@ def moe_route(logits: torch.Tensor, top_k: int, score: str = "softmax", bias: to
     if stream is not None:
         with _on(stream):
             return moe_route(logits, top_k, score, bias, groups, top_groups, group_score, renorm, scale, order, workspace)
-    xt = FLOATS.get(logits.dtype)
-    _need(xt is not None and logits.dim() == 2 and logits.is_cuda and logits.stride(1) == 1, "logits are CUDA f32, f16 or bf16 [T, experts]")
-    T, E = logits.shape
-    device = logits.get_device()
-    _need(bias is None or (bias.dtype == torch.float32 and bias.shape == (E,) and bias.is_contiguous() and bias.get_device() == device),
-          "bias is f32 [experts]")
-    cfg = _RouteConfig(SCORES[score], top_k, groups, top_groups, GROUP_SCORES[group_score], renorm, scale)
-    dev, k = logits.device, max(top_k, 0)
-    ids = torch.empty((T, k), dtype=torch.int32, device=dev)
-    weights = torch.empty((T, k), dtype=torch.float32, device=dev)
-    offsets = slots = None
-    need = 0
-    if order:
-        offsets = torch.empty(E + 1, dtype=torch.int32, device=dev)
-        slots = torch.empty(T * k, dtype=torch.int32, device=dev)
-        if T > 32:
-            need = _lib().qmm_moe_route_workspace(T, E, top_k)
-    ptr, size, keep = _buffer(workspace, need, logits)
-    status = _lib().qmm_moe_route(ctypes.addressof(cfg), xt, logits.data_ptr(), logits.stride(0) if T > 1 else E, T, E,
-                                  0 if bias is None else bias.data_ptr(), ids.data_ptr(), weights.data_ptr(),
-                                  0 if offsets is None else offsets.data_ptr(), 0 if slots is None else slots.data_ptr(), ptr, size,
-                                  _raw_stream(device))
-    if status:
-        _check(status, "qmm_moe_route")
-    return Route(ids, weights, offsets, slots)
-
-
-def _routing(w: Q4GWeights, r: Route, weights: bool) -> _Routing:
-    T, k = r.ids.shape
-    ok = r.offsets is not None and r.order is not None
-    for t in r:
-        ok = ok and (t.dtype == torch.float32 if t is r.weights else t.dtype == torch.int32) and t.is_contiguous() and t.get_device() == w.device
-    _need(ok and r.offsets.numel() == w.experts + 1 and r.order.numel() == T * k and r.weights.shape == r.ids.shape,
-          "a Route has int32 ids [T, top_k], f32 weights, int32 offsets [experts + 1] and order [T top_k], contiguous, on the weights' device")
-    return _Routing(r.ids.data_ptr(), r.weights.data_ptr(), r.offsets.data_ptr(), r.order.data_ptr(), T, k)
+    r = _binding.route(logits, bias, top_k, SCORES[score], groups, top_groups, GROUP_SCORES[group_score], renorm, scale, order, workspace)
+    if type(r) is int:
+        _check(r, "qmm_moe_route")
+    return Route(*r)
 
 
 def moe_gate_up(w: Q4GWeights, x: torch.Tensor, route: Route, out: torch.Tensor | None = None,
@@ -268,15 +222,10 @@ def moe_gate_up(w: Q4GWeights, x: torch.Tensor, route: Route, out: torch.Tensor 
     if stream is not None:
         with _on(stream):
             return moe_gate_up(w, x, route, out, workspace)
-    xt, ld = _activations(w, x, 2)
-    r = _routing(w, route, False)
-    _need(r.T == x.shape[0], "route and x have the same tokens")
-    out = _output(out, (r.T, r.top_k, w.N // 2), x)
-    ptr, size, keep = _buffer(workspace, w._workspace_bytes("qmm_moe_gate_up", xt, r.T, r.top_k), x)
-    status = _lib().qmm_moe_gate_up(w._ptr, xt, x.data_ptr(), ld, ctypes.addressof(r), out.data_ptr(), ptr, size, _raw_stream(w.device))
-    if status:
-        _check(status, "qmm_moe_gate_up")
-    return out
+    h = _binding.gate_up(w._ptr, w.device, x, *route, out, workspace)
+    if type(h) is int:
+        _check(h, "qmm_moe_gate_up")
+    return h
 
 
 def moe_down(w: Q4GWeights, h: torch.Tensor, route: Route, out: torch.Tensor | None = None,
@@ -285,12 +234,7 @@ def moe_down(w: Q4GWeights, h: torch.Tensor, route: Route, out: torch.Tensor | N
     if stream is not None:
         with _on(stream):
             return moe_down(w, h, route, out, workspace)
-    xt, ld = _activations(w, h, 3)
-    r = _routing(w, route, True)
-    _need((r.T, r.top_k) == tuple(h.shape[:2]), "route and h have the same slots")
-    out = _output(out, (r.T, w.N), h)
-    ptr, size, keep = _buffer(workspace, w._workspace_bytes("qmm_moe_down", xt, r.T, r.top_k), h)
-    status = _lib().qmm_moe_down(w._ptr, xt, h.data_ptr(), ld, ctypes.addressof(r), out.data_ptr(), ptr, size, _raw_stream(w.device))
-    if status:
-        _check(status, "qmm_moe_down")
-    return out
+    y = _binding.down(w._ptr, w.device, h, *route, out, workspace)
+    if type(y) is int:
+        _check(y, "qmm_moe_down")
+    return y
