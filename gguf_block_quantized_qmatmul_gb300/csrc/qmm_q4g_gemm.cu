@@ -13,7 +13,7 @@ template <int NP, int XT>
 __global__ void __launch_bounds__(256) q4g_prep_kernel(const QgCall c, int rows, __half* out, float* xs) {
     grid_dep_launch();
     grid_dep_wait();
-    const int row = blockIdx.x * 8 + (threadIdx.x >> 5), lane = threadIdx.x & 31, K = c.w.K;
+    const int row = blockIdx.x * 8 + (threadIdx.x >> 5), lane = threadIdx.x & 31, K = c.w.K, pitch = (K + 63) / 64 * 64;
     if (row >= rows) return;
     int from = row;
     if (c.op != P_DENSE) {
@@ -25,7 +25,11 @@ __global__ void __launch_bounds__(256) q4g_prep_kernel(const QgCall c, int rows,
     constexpr int V = XT == X_F32 ? 4 : 8;  // values in 16 bytes
     const uint4* x = reinterpret_cast<const uint4*>(static_cast<const uint8_t*>(c.x) + (long long)from * c.ldx * (16 / V));
     const int n = K / V;
-    __half* hr = out + (long long)row * K;
+    __half* hr = out + (long long)row * pitch;
+    if (pitch != K && lane < 4) {  // the other half of the last 64 K
+        reinterpret_cast<uint4*>(hr + K)[lane] = make_uint4(0u, 0u, 0u, 0u);
+        if (NP == 2) reinterpret_cast<uint4*>(hr + (long long)rows * pitch + K)[lane] = make_uint4(0u, 0u, 0u, 0u);
+    }
     if (XT == X_F16) {
         for (int i = lane; i < n; i += 128) {
             uint4 v[4];
@@ -93,19 +97,33 @@ __global__ void __launch_bounds__(256) q4g_prep_kernel(const QgCall c, int rows,
                 reinterpret_cast<uint4*>(hr)[i + 32 * j] = make_uint4(h[0], h[1], h[2], h[3]);
             } else {
                 reinterpret_cast<uint2*>(hr)[i + 32 * j] = make_uint2(h[0], h[1]);
-                reinterpret_cast<uint2*>(hr + (long long)rows * K)[i + 32 * j] = make_uint2(l[0], l[1]);
+                reinterpret_cast<uint2*>(hr + (long long)rows * pitch)[i + 32 * j] = make_uint2(l[0], l[1]);
             }
         }
     }
 }
 
-template <int NP, int NG>
-cudaError_t gemm_one(const QgGemmPlan& pl, const CUtensorMap& tx, const QgGemmParams& p, int smem_max, cudaStream_t s) {
+template <int NP, int NG, int CG>
+cudaError_t gemm_one(const QgGemmPlan& pl, const CUtensorMap& tx, const CUtensorMap& tw, const QgGemmParams& p, int smem_max, cudaStream_t s) {
     static unsigned long long done = 0;
-    auto* k = q4g_gemm_kernel<NP, NG>;
+    auto* k = q4g_gemm_kernel<NP, NG, CG>;
     const cudaError_t e = ensure_smem(k, smem_max, done);
     if (e != cudaSuccess) return e;
-    return launch_pdl(k, (unsigned)pl.grid, kQgThreads, pl.smem, s, tx, p);
+    cudaLaunchConfig_t cfg = {};
+    cfg.gridDim = dim3((unsigned)pl.grid);
+    cfg.blockDim = dim3(kQgThreads);
+    cfg.dynamicSmemBytes = pl.smem;
+    cfg.stream = s;
+    cudaLaunchAttribute attr[2];
+    attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+    attr[0].val.programmaticStreamSerializationAllowed = 1;
+    attr[1].id = cudaLaunchAttributeClusterDimension;
+    attr[1].val.clusterDim.x = CG;
+    attr[1].val.clusterDim.y = 1;
+    attr[1].val.clusterDim.z = 1;
+    cfg.attrs = attr;
+    cfg.numAttrs = CG == 1 ? 1 : 2;
+    return cudaLaunchKernelEx(&cfg, k, tx, tw, p);
 }
 
 }  // namespace
@@ -116,56 +134,63 @@ QgGemmPlan plan_q4g_gemm(const QgCall& c, int sms, int smem_max) {
     if (grouped && c.w.E > kQgMaxE) return pl;
     const long long rows = c.M;
     pl.np = c.xt == X_F32 ? 2 : 1;
-    pl.prep = grouped || c.xt != X_F16;
+    pl.prep = grouped || c.xt != X_F16 || c.w.K % 64 != 0;  // K that does not fill its last 64 is padded there
     const long long per = grouped ? (c.M + c.w.E - 1) / c.w.E : c.M;  // activation rows per weight matrix
-    pl.ntiles = (c.w.RB + 7) / 8;
-    // Two accumulators, so that the epilogue runs beside the next unit's MMAs: at most 192
-    // columns each (with two pieces 64: the epilogue's running sums are registers), the weight
-    // pieces' stages in the columns left.
-    const int most = pl.np == 2 ? kQgBX2 : kQgBX1;
+    pl.cg = pl.np == 1 ? 2 : 1;
+    pl.ntiles = (c.w.RB + 8 * pl.cg - 1) / (8 * pl.cg);
+    const int workers = sms / pl.cg, unit = 16 * pl.cg;  // pairs; the MMA's N is a multiple of this
+    // Modelled cycles (fitted to GB300 timings): a tile of 128 K costs its MMAs (half a cycle a
+    // column, at least 40 each) or its conversion (900; two pieces 1400); a unit costs its
+    // prologue and, where there is no second accumulator, the epilogue that the next unit's
+    // MMAs wait for; slices of K cost their partial sums' traffic and a launch.
+    const int most = pl.np == 2 ? kQgBX2 : kQgBX1;  // two pieces: the epilogue's running sums are registers
     pl.ks = 1;
     if (grouped) {
-        pl.bx = per > 64 ? most : per > 32 ? 64 : 32;
+        // two accumulators: K is short, and a second one hides the epilogue (2048 tokens x 8 of 64,
+        // 2048 -> 2 x 1024: 171 us with tiles of up to 192 rows, 185 with 256)
+        pl.bx = per > 96 ? (most < 192 ? most : 192) : per > 48 ? (most < 128 ? most : 128) : per > 24 ? 64 : 32;
     } else {
-        // Modelled cycles: a 64-K tile costs its MMAs (2 cycles a column and pass) or its
-        // conversion (about 300, 500 with two pieces), a unit about 2000 more; slices of K
-        // cost their partial sums' traffic and a launch (about 4000).
-        const int kt = (c.w.K + 63) / 64, nr = (c.w.KS + 1) / 2;
         double best = 0;
         for (int tiles = (int)((per + most - 1) / most); tiles <= 8 + (per + most - 1) / most; ++tiles) {
-            const int bx = (int)((per + tiles - 1) / tiles + 15) / 16 * 16;
+            const int bx = (int)((per + tiles - 1) / tiles + unit - 1) / unit * unit;
             const long long un = (long long)pl.ntiles * ((per + bx - 1) / bx);
-            const double mma = 2.0 * bx * (2 * pl.np - 1), conv = pl.np == 2 ? 500.0 : 300.0, tile = mma > conv ? mma : conv;
-            for (int ks = 1; ks <= nr && ks <= 16 && (ks == 1 || un * ks <= 2 * sms); ++ks) {
-                const double waves = (double)((un * ks + sms - 1) / sms);
-                const double cost = waves * ((double)kt / ks * tile + 2000.0) + (ks > 1 ? 4000.0 + 8.0 * ks * per * c.w.N / 3000.0 : 0.0);
+            const double mma = 8.0 * (2 * pl.np - 1) * (bx < 80 ? 40.0 : bx / 2.0), conv = pl.np == 2 ? 1400.0 : 900.0, tile = mma > conv ? mma : conv;
+            const double once = bx > 192 ? 1500.0 + 12.0 * bx : 1500.0;
+            for (int ks = 1; ks <= c.w.KS && ks <= 16 && (ks == 1 || un * ks <= 2 * workers); ++ks) {
+                const double waves = (double)((un * ks + workers - 1) / workers);
+                const double cost = waves * ((double)((c.w.KS + ks - 1) / ks) * tile + once) + (ks > 1 ? 4000.0 + 8.0 * ks * per * c.w.N / 3000.0 : 0.0);
                 if (best == 0 || cost < 0.98 * best) {
                     best = cost;
                     pl.bx = bx;
                     pl.ks = ks;
                 }
             }
-            if (bx == 16) break;
+            if (bx == unit) break;
         }
     }
-    pl.box = grouped && pl.bx > 64 ? 64 : pl.bx;  // an expert's tile is any size: no more copied than 63 rows too many
     pl.accw = (pl.bx + 31) / 32 * 32;
+    pl.nacc = pl.bx <= 192 ? 2 : 1;  // with two accumulators the epilogue runs beside the next unit's MMAs
     pl.mtiles = grouped ? 0 : (int)((per + pl.bx - 1) / pl.bx);
-    pl.nraw = 3;
-    const int raw = 16 * qg_seg_bytes(c.w.ng), stage = pl.bx * 128 * pl.np;
-    const int fixed = 512 + 2 * kQgEpiWarps * kQgBX1 * 4 + (c.w.E + 1) * 4 + 1024;
-    pl.nstage = (smem_max - fixed - pl.nraw * raw) / stage;
-    const int cap = (kTcTmemCols - 2 * pl.accw) / (32 * pl.np);
-    if (pl.nstage > cap) pl.nstage = cap;
+    // converted weights in the tensor memory that the accumulators leave; activations and raw
+    // weights share the shared memory
+    pl.nstage = (kTcTmemCols - pl.nacc * pl.accw) / (64 * pl.np);
     if (pl.nstage > kQgStageMax) pl.nstage = kQgStageMax;
-    if (pl.nstage < kQgGroups || pl.nstage < 2) return pl;
-    pl.smem = (size_t)pl.nstage * stage + (size_t)pl.nraw * raw + fixed;
+    const int raw = 8 * qg_seg_bytes(c.w.ng), stage = pl.bx / pl.cg * 256 * pl.np;
+    const int room = smem_max - (512 + 2 * kQgEpiWarps * kQgBX1 * 4 + (c.w.E + 1) * 4 + 1024);
+    // Both rings are multiples of the converting groups, so that whoever waits for a stage's next
+    // filling has waited for its last one (copies may land out of order).
+    pl.nx = (room - 4 * raw) / stage / kQgGroups * kQgGroups;
+    if (pl.nx > kQgXMax) pl.nx = kQgXMax;
+    pl.nraw = (room - pl.nx * stage) / raw / kQgGroups * kQgGroups;
+    if (pl.nraw > kQgRawMax) pl.nraw = kQgRawMax;
+    if (pl.nstage < kQgGroups || pl.nx < kQgGroups || pl.nraw < kQgGroups) return pl;
+    pl.smem = (size_t)pl.nx * stage + (size_t)pl.nraw * raw + (smem_max - room);
     const long long units = grouped ? ((long long)c.w.E + c.M / pl.bx) * pl.ntiles : (long long)pl.mtiles * pl.ntiles * pl.ks;
     if (units > (1ll << 30)) return pl;
-    pl.grid = (int)(units < sms ? units : sms);
+    pl.grid = (int)(units < workers ? units : workers) * pl.cg;
     auto r256 = [](size_t v) { return (v + 255) / 256 * 256; };
     pl.ws_x = 0;
-    pl.ws_xs = pl.prep ? r256((size_t)pl.np * rows * c.w.K * 2) : 0;
+    pl.ws_xs = pl.prep ? r256((size_t)pl.np * rows * ((c.w.K + 63) / 64 * 64) * 2) : 0;
     pl.ws_part = pl.ws_xs + (pl.prep ? r256((size_t)rows * 4) : 0);
     pl.workspace = pl.ws_part + (c.op == P_DOWN || pl.ks > 1 ? (size_t)pl.ks * c.M * c.w.N * 4 : 0);
     pl.ok = true;
@@ -187,11 +212,18 @@ cudaError_t launch_q4g_gemm(const QgGemmPlan& pl, const QgCall& c, void* ws, uns
                                               : launch_pdl(q4g_prep_kernel<1, X_BF16>, blocks, 256, 0, s, c, rows, xh, xs);
         if (e != cudaSuccess) return e;
         xsrc = xh;
-        pitch = (long long)K * 2;
+        pitch = (long long)(K + 63) / 64 * 64 * 2;
     }
+    // activations: 64 K x rows x K / 64, a box of half a pair's rows and two of the last
     CUtensorMap tx;
-    if (!make_map(&tx, CU_TENSOR_MAP_DATA_TYPE_FLOAT16, xsrc, (unsigned long long)K, (unsigned long long)rows * pl.np, (unsigned long long)pitch,
-                  64, (unsigned)pl.box, CU_TENSOR_MAP_SWIZZLE_128B))
+    if (!make_map_3d(&tx, CU_TENSOR_MAP_DATA_TYPE_FLOAT16, xsrc, 64, (unsigned long long)rows * pl.np, (unsigned long long)(K + 63) / 64,
+                     (unsigned long long)pitch, 128, 64, (unsigned)(pl.bx / pl.cg), 2, CU_TENSOR_MAP_SWIZZLE_128B))
+        return cudaErrorInvalidValue;
+    // raw weights: row blocks of all experts, 8-byte elements, a box of a segment of eight of them
+    CUtensorMap tw;
+    const unsigned seg = (unsigned)qg_seg_bytes(c.w.ng);
+    if (!make_map(&tw, CU_TENSOR_MAP_DATA_TYPE_UINT64, c.w.data, (unsigned long long)c.w.KS * (seg / 8), (unsigned long long)c.w.E * c.w.RB,
+                  (unsigned long long)c.w.KS * seg, seg / 8, 8, CU_TENSOR_MAP_SWIZZLE_NONE))
         return cudaErrorInvalidValue;
     QgGemmParams p;
     p.c = c;
@@ -201,26 +233,25 @@ cudaError_t launch_q4g_gemm(const QgGemmPlan& pl, const QgCall& c, void* ws, uns
     p.err = err;
     p.xrows = rows;
     p.bx = pl.bx;
-    p.box = pl.box;
+    p.nacc = pl.nacc;
     p.accw = pl.accw;
     p.mtiles = pl.mtiles;
     p.ntiles = pl.ntiles;
-    p.kt = (K + 63) / 64;
     p.nraw = pl.nraw;
+    p.nx = pl.nx;
     p.nstage = pl.nstage;
     p.ks = pl.ks;
-    p.grid = pl.grid;
-    p.off_raw = pl.nstage * pl.bx * 128 * pl.np;
-    p.off_bar = p.off_raw + pl.nraw * 16 * qg_seg_bytes(c.w.ng);
+    p.off_raw = pl.nx * (pl.bx / pl.cg) * 256 * pl.np;
+    p.off_bar = p.off_raw + pl.nraw * 8 * qg_seg_bytes(c.w.ng);
     cudaError_t e;
     if (pl.np == 2)
-        e = c.w.ng == 1   ? gemm_one<2, 1>(pl, tx, p, smem_max, s)
-            : c.w.ng == 2 ? gemm_one<2, 2>(pl, tx, p, smem_max, s)
-                          : gemm_one<2, 4>(pl, tx, p, smem_max, s);
+        e = c.w.ng == 1   ? gemm_one<2, 1, 1>(pl, tx, tw, p, smem_max, s)
+            : c.w.ng == 2 ? gemm_one<2, 2, 1>(pl, tx, tw, p, smem_max, s)
+                          : gemm_one<2, 4, 1>(pl, tx, tw, p, smem_max, s);
     else
-        e = c.w.ng == 1   ? gemm_one<1, 1>(pl, tx, p, smem_max, s)
-            : c.w.ng == 2 ? gemm_one<1, 2>(pl, tx, p, smem_max, s)
-                          : gemm_one<1, 4>(pl, tx, p, smem_max, s);
+        e = c.w.ng == 1   ? gemm_one<1, 1, 2>(pl, tx, tw, p, smem_max, s)
+            : c.w.ng == 2 ? gemm_one<1, 2, 2>(pl, tx, tw, p, smem_max, s)
+                          : gemm_one<1, 4, 2>(pl, tx, tw, p, smem_max, s);
     if (e == cudaSuccess && pl.ks > 1) return launch_q4g_sum(p.part, pl.ks, (long long)c.M * c.w.N, c.y, c.xt, s);
     if (e != cudaSuccess || c.op != P_DOWN) return e;
     return launch_q4g_combine(p.part, c.r, c.w.E, c.w.N, c.y, c.xt, s);

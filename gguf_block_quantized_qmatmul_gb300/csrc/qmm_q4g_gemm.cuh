@@ -17,22 +17,29 @@
 //
 // One persistent block per SM over units: 128 weight rows (8 row blocks, the
 // MMA's M) x up to bx activation rows of one expert (its N, rounded up to 16).
-//   warp 0      one thread: activation tiles (64 K, 128-byte swizzle), 2-D boxes; the
-//               experts' rows were put in sorted order by the preparation launch
+// With one piece, two blocks work as a pair (cta_group::2) on 256 weight rows:
+// each converts its own 128, holds half of the activation rows and reads out its
+// own accumulator rows; rank 0's MMA thread works for both.  A block alone has to
+// write and read every activation row of its tile in its shared memory for 128
+// weight rows, 128 bytes a cycle at the MMAs' peak, all that there is.
+//   warp 0      one thread: activation tiles (128 K, two halves with 128-byte
+//               swizzle), one 3-D box each (several made this thread's issue the
+//               limit, 850 cycles a tile); the experts' rows were put in sorted order by the preparation launch
 //               (gathering four rows a copy here measured 90 cycles a copy: 643 us
 //               against the whole of 2048 tokens x 8 of 64 experts, 2048 -> 2 x 1024)
-//   warp 1      one elected lane: four MMAs (twelve with two pieces) per 64 K, A in
-//               tensor memory, B in shared memory
-//   warp 2      raw weights: eight 1-D copies (a row block's two segments each)
-//               per 256 K
-//   warps 3-6   epilogue: accumulator columns to registers, scaled; the experts'
+//   warp 1      one elected lane: eight MMAs (24 with two pieces) per tile of 128 K, A
+//               in tensor memory, B in shared memory.  (With tiles of 64 K its wait,
+//               commits and bookkeeping, about 300 cycles a tile alone and 500 beside
+//               the other warps, held the MMAs up.)
+//   warp 2      one thread: raw weights, a 2-D box of eight row blocks per segment
+//               (a copy per row block took 300 cycles)
+//   warps 3-10  epilogue: accumulator columns to registers, scaled; the experts'
 //               first product takes its up row from the lane eight away (paired
 //               layout) for silu(g) u
-//   warps 7-22  conversion: a lane's uint4 of codes becomes fragment registers
+//   warps 11-26 conversion: a lane's uint4 of codes becomes fragment registers
 //               and goes to tensor memory as they are (16-lane x 128-bit
-//               stores); four groups of four warps, one 64-K tile of a raw stage
-//               each (a tile takes a group about 1400 cycles from end to end, and 192
-//               rows' MMAs 384: with two groups those waited for it)
+//               stores); two groups of eight warps, a row block each, every other
+//               tile
 // The weights are bound for tensor memory, so shared memory feeds only the
 // activation tiles to the MMAs.  With two pieces the tensor core's truncating
 // f32 accumulation would show: the accumulator is restarted every kQgChunk
@@ -46,13 +53,14 @@
 
 namespace qmm {
 
-constexpr int kQgEpiWarps = 8, kQgConvWarps = 8;
-constexpr int kQgEpiHalves = kQgEpiWarps / 4, kQgGroups = kQgConvWarps / 4;  // warps per TMEM lane quarter
+constexpr int kQgEpiWarps = 8, kQgConvWarps = 16;
+constexpr int kQgEpiHalves = kQgEpiWarps / 4;   // epilogue warps per TMEM lane quarter
+constexpr int kQgGroups = kQgConvWarps / 8;     // converting groups: a warp per row block of a tile
 constexpr int kQgEpi0 = 3, kQgConv0 = kQgEpi0 + kQgEpiWarps;
 constexpr int kQgThreads = (kQgConv0 + kQgConvWarps) * 32;
-constexpr int kQgBX1 = 192, kQgBX2 = 64;  // activation rows per tile, at most: one piece, two pieces
-constexpr int kQgRawMax = 4, kQgStageMax = 8;
-constexpr int kQgChunk = 4;      // 64-K tiles per accumulation chunk (two pieces)
+constexpr int kQgBX1 = 256, kQgBX2 = 64;  // activation rows per tile, at most: one piece, two pieces
+constexpr int kQgRawMax = 6, kQgXMax = 8, kQgStageMax = 8;  // stages, at most: raw weights, activations, converted weights
+constexpr int kQgChunk = 2;      // tiles per accumulation chunk (two pieces)
 constexpr int kQgMaxE = 512;     // experts of a grouped call
 
 struct QgGemmParams {
@@ -62,7 +70,7 @@ struct QgGemmParams {
     const float* wis;     // 2^-a per weight row, layout order
     unsigned* err;
     int xrows;            // rows of an activation plane (the lo plane follows)
-    int bx, box, accw, mtiles, ntiles, kt, nraw, nstage, grid;
+    int bx, nacc, accw, mtiles, ntiles, nraw, nx, nstage;
     int ks;               // K slices (dense): f32 partial outputs [ks][M][N]
     int off_raw, off_bar;
 };
@@ -74,6 +82,74 @@ __device__ __forceinline__ void tc_st_frag(uint32_t taddr, const uint32_t v[16])
         "r"(v[0]), "r"(v[1]), "r"(v[2]), "r"(v[3]), "r"(v[4]), "r"(v[5]), "r"(v[6]), "r"(v[7]), "r"(v[8]), "r"(v[9]),
         "r"(v[10]), "r"(v[11]), "r"(v[12]), "r"(v[13]), "r"(v[14]), "r"(v[15])
         : "memory");
+}
+// the same, 64 columns
+__device__ __forceinline__ void tc_st_frag64(uint32_t taddr, const uint32_t v[32]) {
+    asm volatile(
+        "tcgen05.st.sync.aligned.16x128b.x16.b32 [%0], {%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,%15,%16,"
+        "%17,%18,%19,%20,%21,%22,%23,%24,%25,%26,%27,%28,%29,%30,%31,%32};" ::"r"(taddr),
+        "r"(v[0]), "r"(v[1]), "r"(v[2]), "r"(v[3]), "r"(v[4]), "r"(v[5]), "r"(v[6]), "r"(v[7]), "r"(v[8]), "r"(v[9]),
+        "r"(v[10]), "r"(v[11]), "r"(v[12]), "r"(v[13]), "r"(v[14]), "r"(v[15]), "r"(v[16]), "r"(v[17]), "r"(v[18]), "r"(v[19]),
+        "r"(v[20]), "r"(v[21]), "r"(v[22]), "r"(v[23]), "r"(v[24]), "r"(v[25]), "r"(v[26]), "r"(v[27]), "r"(v[28]), "r"(v[29]),
+        "r"(v[30]), "r"(v[31])
+        : "memory");
+}
+
+// Pairs of blocks (cta_group::2): a cluster of two, whose rank 0 issues the MMAs of both.
+__device__ __forceinline__ uint32_t cluster_rank() {
+    uint32_t r;
+    asm volatile("mov.u32 %0, %%cluster_ctarank;" : "=r"(r));
+    return r;
+}
+__device__ __forceinline__ void cluster_sync() {
+    asm volatile("barrier.cluster.arrive.release.aligned;" ::: "memory");
+    asm volatile("barrier.cluster.wait.acquire.aligned;" ::: "memory");
+}
+// the address, in the cluster's shared memory, of rank 0's copy of a shared variable
+__device__ __forceinline__ uint32_t leader_addr(uint32_t a) {
+    uint32_t r;
+    asm("mapa.shared::cluster.u32 %0, %1, 0;" : "=r"(r) : "r"(a));
+    return r;
+}
+// What these arrivals announce is tensor memory (ordered by the tcgen05 fences before them and
+// after the wait); with cluster-scope release and acquire a tile took 990 cycles, not 670.
+__device__ __forceinline__ void mbar_arrive_cluster(uint32_t a) {
+    asm volatile("mbarrier.arrive.relaxed.cluster.shared::cluster.b64 _, [%0];" ::"r"(a) : "memory");
+}
+// load one TMA box of a 3-D tensor map
+__device__ __forceinline__ void tma_3d(uint32_t dst, const CUtensorMap* map, int x, int y, int z, uint32_t bar) {
+    asm volatile(
+        "cp.async.bulk.tensor.3d.shared::cluster.global.mbarrier::complete_tx::bytes [%0], [%1, {%2, %3, %4}], [%5];" ::"r"(dst),
+        "l"(map), "r"(x), "r"(y), "r"(z), "r"(bar)
+        : "memory");
+}
+// the same, completing on a barrier of the pair's leader
+__device__ __forceinline__ void tma_3d_pair(uint32_t dst, const CUtensorMap* map, int x, int y, int z, uint32_t bar) {
+    asm volatile(
+        "cp.async.bulk.tensor.3d.cta_group::2.shared::cluster.global.mbarrier::complete_tx::bytes [%0], [%1, {%2, %3, %4}], [%5];" ::"r"(dst),
+        "l"(map), "r"(x), "r"(y), "r"(z), "r"(bar)
+        : "memory");
+}
+template <int CG>
+__device__ __forceinline__ void qg_mma_tc(uint32_t tmem, uint32_t ta, uint64_t db, uint32_t idesc, uint32_t accumulate) {
+    if (CG == 1)
+        tc_mma(tmem, ta, db, idesc, accumulate);
+    else
+        asm volatile(
+            "{\n\t.reg .pred p;\n\tsetp.ne.u32 p, %4, 0;\n\t"
+            "tcgen05.mma.cta_group::2.kind::f16 [%0], [%1], %2, %3, p;\n\t}" ::"r"(tmem),
+            "r"(ta), "l"(db), "r"(idesc), "r"(accumulate)
+            : "memory");
+}
+// the completion of the MMAs before it arrives on this barrier, in both blocks of a pair
+template <int CG>
+__device__ __forceinline__ void qg_commit(uint32_t bar) {
+    if (CG == 1)
+        tc_commit(bar);
+    else
+        asm volatile("tcgen05.commit.cta_group::2.mbarrier::arrive::one.shared::cluster.multicast::cluster.b64 [%0], %1;" ::"r"(bar),
+                     "h"((uint16_t)3)
+                     : "memory");
 }
 
 // true in one lane of a converged warp
@@ -125,52 +201,68 @@ __device__ __forceinline__ void qg_drain(const QgRing& r, bool wrapped, int n, u
 
 // a unit's place
 struct QgUnit {
-    int e, p0, n, nt;  // expert, first position (row of x in a dense call), activation rows, row tile
-    int split, j0, j1; // K slice, its 64-K tiles
+    int e, p0, n, nt;  // expert, first position (row of x in a dense call), activation rows, this block's row tile
+    int split, j0, j1; // K slice, its tiles (segments of 128 K)
 };
 
-template <int NP, int NG>
-__global__ void __launch_bounds__(kQgThreads, 1) q4g_gemm_kernel(const __grid_constant__ CUtensorMap tx, const QgGemmParams p) {
+template <int NP, int NG, int CG>
+__global__ void __launch_bounds__(kQgThreads, 1) q4g_gemm_kernel(const __grid_constant__ CUtensorMap tx, const __grid_constant__ CUtensorMap tw, const QgGemmParams p) {
     extern __shared__ __align__(1024) uint8_t smraw[];
     uint8_t* sm = smraw + ((1024 - (smem_u32(smraw) & 1023)) & 1023);
     const QgCall& c = p.c;
     const QgWeights& w = c.w;
     const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
     uint64_t* bars = reinterpret_cast<uint64_t*>(sm + p.off_bar);
-    uint64_t* full = bars;                         // activation tile landed and weight pieces in tensor memory
-    uint64_t* empty = full + kQgStageMax;          // stage consumed by the MMAs (commit)
+    uint64_t* x_full = bars;                       // activation tile landed (of a pair: both halves)
+    uint64_t* x_empty = x_full + kQgXMax;          // and read by the MMAs (commit)
+    uint64_t* full = x_empty + kQgXMax;            // converted weights in tensor memory
+    uint64_t* empty = full + kQgStageMax;          // and read by the MMAs (commit)
     uint64_t* r_full = empty + kQgStageMax;        // raw weights landed
     uint64_t* r_empty = r_full + kQgRawMax;        // raw stage converted
     uint64_t* acc_full = r_empty + kQgRawMax;      // accumulator complete (commit)
     uint64_t* acc_empty = acc_full + 2;            // accumulator read
-    static_assert((2 * kQgStageMax + 2 * kQgRawMax + 4) * 8 <= 256, "mbarriers overlap the TMEM slot");
-    uint32_t* tslot = reinterpret_cast<uint32_t*>(sm + p.off_bar + 256);
-    volatile int* flags = reinterpret_cast<volatile int*>(sm + p.off_bar + 320);
+    static_assert(kQgXMax % kQgGroups == 0 && kQgRawMax % kQgGroups == 0, "rings of whole turns");
+    static_assert((2 * kQgXMax + 2 * kQgStageMax + 2 * kQgRawMax + 4) * 8 <= 448, "mbarriers overlap the TMEM slot");
+    uint32_t* tslot = reinterpret_cast<uint32_t*>(sm + p.off_bar + 448);
+    volatile int* flags = reinterpret_cast<volatile int*>(sm + p.off_bar + 480);
     int* col_slot = reinterpret_cast<int*>(sm + p.off_bar + 512);             // [warps][kQgBX1]
     float* col_scale = reinterpret_cast<float*>(col_slot + kQgEpiWarps * kQgBX1);  // [warps][kQgBX1]
     int* ts = reinterpret_cast<int*>(col_scale + kQgEpiWarps * kQgBX1);       // [E + 1] activation tiles before each expert
+    const uint32_t rank = CG == 2 ? cluster_rank() : 0u;
+    constexpr int kUnit = 16 * CG;  // the MMA's N is a multiple of 16, a pair's of 32
+    const int first_unit = blockIdx.x / CG, unit_step = gridDim.x / CG;
     const bool grouped = c.op != P_DENSE;
     const int slots = grouped ? c.r.T * c.r.top_k : c.M;
     if (tid == 0) {
+        for (int i = 0; i < kQgXMax; ++i) {
+            mbar_init(smem_u32(&x_full[i]), 1);
+            mbar_init(smem_u32(&x_empty[i]), 1);
+        }
         for (int i = 0; i < kQgStageMax; ++i) {
-            mbar_init(smem_u32(&full[i]), 1 + 4);
+            mbar_init(smem_u32(&full[i]), 8 * CG);
             mbar_init(smem_u32(&empty[i]), 1);
         }
         for (int i = 0; i < kQgRawMax; ++i) {
             mbar_init(smem_u32(&r_full[i]), 1);
-            mbar_init(smem_u32(&r_empty[i]), kQgConvWarps);
+            mbar_init(smem_u32(&r_empty[i]), 8);
         }
         for (int i = 0; i < 2; ++i) {
             mbar_init(smem_u32(&acc_full[i]), 1);
-            mbar_init(smem_u32(&acc_empty[i]), kQgEpiWarps);
+            mbar_init(smem_u32(&acc_empty[i]), kQgEpiWarps * CG);
         }
         flags[0] = 0;
         fence_mbar_init();
     }
     if (warp == 1) {
-        asm volatile("tcgen05.alloc.cta_group::1.sync.aligned.shared::cta.b32 [%0], %1;" ::"r"(smem_u32(tslot)), "n"(kTcTmemCols)
-                     : "memory");
-        asm volatile("tcgen05.relinquish_alloc_permit.cta_group::1.sync.aligned;" ::: "memory");
+        if (CG == 1) {
+            asm volatile("tcgen05.alloc.cta_group::1.sync.aligned.shared::cta.b32 [%0], %1;" ::"r"(smem_u32(tslot)), "n"(kTcTmemCols)
+                         : "memory");
+            asm volatile("tcgen05.relinquish_alloc_permit.cta_group::1.sync.aligned;" ::: "memory");
+        } else {
+            asm volatile("tcgen05.alloc.cta_group::2.sync.aligned.shared::cta.b32 [%0], %1;" ::"r"(smem_u32(tslot)), "n"(kTcTmemCols)
+                         : "memory");
+            asm volatile("tcgen05.relinquish_alloc_permit.cta_group::2.sync.aligned;" ::: "memory");
+        }
     }
     grid_dep_launch();
     if (grouped) grid_dep_wait();
@@ -203,6 +295,7 @@ __global__ void __launch_bounds__(kQgThreads, 1) q4g_gemm_kernel(const __grid_co
     }
     tc_fence_before();
     __syncthreads();
+    if (CG == 2) cluster_sync();  // the pair's barriers are initialised, its tensor memory is allocated
     tc_fence_after();
     const uint32_t tmem = *tslot;
     const int tiles_all = ts[w.E] * p.ntiles, units = tiles_all * p.ks;
@@ -210,11 +303,10 @@ __global__ void __launch_bounds__(kQgThreads, 1) q4g_gemm_kernel(const __grid_co
         QgUnit un;
         un.split = u / tiles_all;
         u -= un.split * tiles_all;
-        const int nr = (w.KS + 1) / 2;  // raw stages
-        un.j0 = 4 * (int)((long long)un.split * nr / p.ks);
-        un.j1 = min(p.kt, 4 * (int)((long long)(un.split + 1) * nr / p.ks));
+        un.j0 = (int)((long long)un.split * w.KS / p.ks);
+        un.j1 = (int)((long long)(un.split + 1) * w.KS / p.ks);
         const int st = u / p.ntiles;
-        un.nt = u - st * p.ntiles;
+        un.nt = (u - st * p.ntiles) * CG + (int)rank;
         int lo = 0, hi = w.E;  // ts[lo] <= st < ts[hi]
         while (hi - lo > 1) {
             const int mid = (lo + hi) >> 1;
@@ -224,119 +316,131 @@ __global__ void __launch_bounds__(kQgThreads, 1) q4g_gemm_kernel(const __grid_co
         un.e = lo;
         const int first = grouped ? max(c.r.offsets[lo], 0) : 0;
         const int end = grouped ? min(c.r.offsets[lo + 1], slots) : c.M;
-        // an expert's rows in tiles of one size (a multiple of 16), not full ones and a rest
+        // an expert's rows in tiles of one size, not full ones and a rest
         const int tiles = ts[lo + 1] - ts[lo];
-        const int size = ((end - first + tiles - 1) / tiles + 15) & ~15;
+        const int size = ((end - first + tiles - 1) / tiles + kUnit - 1) & ~(kUnit - 1);
         un.p0 = first + (st - ts[lo]) * size;
         un.n = min(size, end - un.p0);
         return un;
     };
     if (!grouped && warp != 2) grid_dep_wait();  // weights are constant: their copies may start at once
-    const int piece = p.bx * 128;
-    auto stage = [&](int s) { return sm + s * NP * piece; };
+    // an activation stage: per piece two 64-K halves; of a pair, each block has half the rows
+    const int half = p.bx / CG * 128;
+    auto stage = [&](int s) { return sm + s * 2 * NP * half; };
     const int seg_bytes = qg_seg_bytes(NG);
-    auto raw = [&](int s) { return sm + p.off_raw + s * 16 * seg_bytes; };
+    auto raw = [&](int s) { return sm + p.off_raw + s * 8 * seg_bytes; };
+    // 64-K halves of tile j that hold any K
+    auto halves = [&](int j) { return w.K - j * kQgSegK > 64 ? 2 : 1; };
 
     if (warp == 0) {
         // ------------------------------ activations ------------------------------
         if (lane == 0) {
             QgRing g;
             bool ok = true, wrapped = false;
-            for (int u = blockIdx.x; u < units && ok; u += gridDim.x) {
+            for (int u = first_unit; u < units && ok; u += unit_step) {
                 const QgUnit un = place(u);
-                const int boxes = (un.n + p.box - 1) / p.box;
+                const int p0 = un.p0 + (int)rank * ((un.n + kUnit - 1) / kUnit * kUnit / CG);
                 for (int j = un.j0; j < un.j1; ++j) {
-                    if (!(ok = qg_wait(smem_u32(&empty[g.s]), g.ph ^ 1u, flags, p.err))) break;
-                    const uint32_t bar = smem_u32(&full[g.s]), to = smem_u32(stage(g.s));
-                    mbar_arrive_tx(bar, (uint32_t)(NP * boxes * p.box * 128));
-                    for (int i = 0; i < boxes; ++i) {
-                        tma_2d(to + i * p.box * 128, &tx, j * 64, un.p0 + i * p.box, bar);
-                        if (NP == 2) tma_2d(to + piece + i * p.box * 128, &tx, j * 64, p.xrows + un.p0 + i * p.box, bar);
+                    if (!(ok = qg_wait(smem_u32(&x_empty[g.s]), g.ph ^ 1u, flags, p.err))) break;
+                    uint32_t bar = smem_u32(&x_full[g.s]);
+                    const uint32_t to = smem_u32(stage(g.s));
+                    if (rank == 0) mbar_arrive_tx(bar, (uint32_t)(CG * NP * 2 * half));
+                    if (CG == 2) bar = leader_addr(bar);
+#pragma unroll
+                    for (int pc = 0; pc < NP; ++pc) {
+                        if (CG == 2) tma_3d_pair(to + 2 * pc * half, &tx, 0, pc * p.xrows + p0, 2 * j, bar);
+                        else tma_3d(to + 2 * pc * half, &tx, 0, pc * p.xrows + p0, 2 * j, bar);
                     }
-                    g.next(p.nstage);
+                    g.next(p.nx);
                     wrapped |= g.s == 0;
                 }
             }
-            // let every copy land before the block can exit
-            qg_drain(g, wrapped, p.nstage, full, flags, p.err);
+            // let every copy land before the block can exit (rank 0's barriers have both blocks')
+            if (rank == 0) qg_drain(g, wrapped, p.nx, x_full, flags, p.err);
         }
     } else if (warp == 1) {
         // ------------------------------ MMA issuer ------------------------------
-        // The whole warp runs the loop, so that its values are uniform, and one elected lane
-        // issues: inside a one-lane branch every MMA's operands take detours to uniform
-        // registers (58 cycles an MMA and 410 a tile, against 128 cycles of MMAs at 64 rows).
-        const bool lead = elect_one();
-        const uint64_t d0 = tc_sdesc128(smem_u32(stage(0)));
-        const uint32_t lo0 = (uint32_t)d0, dhi = (uint32_t)(d0 >> 32);
-        QgRing g;
-        int cc = 0, last = -1;  // accumulator uses; the last stage issued
-        uint32_t last_ph = 0;
-        bool ok = true;
-        uint32_t ready = 0;
-        for (int u = blockIdx.x; u < units && ok; u += gridDim.x) {
-            const QgUnit un = place(u);
-            const uint32_t idesc = tc_idesc((un.n + 15) / 16 * 16);
-            const int chunk = NP == 2 ? kQgChunk : p.kt;
-            for (int c0 = un.j0; c0 < un.j1 && ok; c0 += chunk, ++cc) {
-                const int ab = cc & 1, use = cc >> 1;
-                if (use > 0) ok = qg_wait(smem_u32(&acc_empty[ab]), (uint32_t)((use - 1) & 1), flags, p.err);
-                if (!ok) break;
-                tc_fence_after();
-                const uint32_t dt = tmem + (uint32_t)(ab * p.accw);
-                const int n = min(chunk, un.j1 - c0);
-                for (int i = 0; i < n; ++i) {
-                    const int s = g.s;
-                    const uint32_t ph = g.ph;
-                    g.next(p.nstage);
-                    const uint32_t nxt = mbar_test(smem_u32(&full[g.s]), g.ph);
-                    if (!ready) ok = qg_wait(smem_u32(&full[s]), ph, flags, p.err);
+        if (rank == 0) {
+            // The whole warp runs the loop, so that its values are uniform, and one elected lane
+            // issues: inside a one-lane branch every MMA's operands take detours to uniform
+            // registers (58 cycles an MMA and 410 a tile, against 128 cycles of MMAs at 64 rows).
+            const bool lead = elect_one();
+            const uint64_t d0 = tc_sdesc128(smem_u32(stage(0)));
+            const uint32_t lo0 = (uint32_t)d0, dhi = (uint32_t)(d0 >> 32);
+            QgRing g;
+            QgRing gx;              // activation stage
+            int cc = 0, last = -1;  // accumulator uses; the last weight stage issued
+            uint32_t last_ph = 0;
+            bool ok = true;
+            uint32_t ready = 0;  // the next stage's barrier, tested before this tile's MMAs are issued
+            for (int u = first_unit; u < units && ok; u += unit_step) {
+                const QgUnit un = place(u);
+                const uint32_t idesc = tc_idesc((un.n + kUnit - 1) / kUnit * kUnit) + ((uint32_t)((CG - 1) * (kTcBW >> 4)) << 24);  // a pair: M = 256
+                const int chunk = NP == 2 ? kQgChunk : w.KS;
+                for (int c0 = un.j0; c0 < un.j1 && ok; c0 += chunk, ++cc) {
+                    const int ab = p.nacc == 2 ? (cc & 1) : 0, use = p.nacc == 2 ? (cc >> 1) : cc;
+                    if (use > 0) ok = qg_wait(smem_u32(&acc_empty[ab]), (uint32_t)((use - 1) & 1), flags, p.err);
                     if (!ok) break;
                     tc_fence_after();
-                    const uint32_t xhi = lo0 + (uint32_t)((s * NP * piece) >> 4), xlo = xhi + (uint32_t)(piece >> 4);
-                    const uint32_t whi = tmem + (uint32_t)(2 * p.accw + 32 * NP * s), wlo = whi + 32;
-                    __syncwarp();
-                    if (lead) {
+                    const uint32_t dt = tmem + (uint32_t)(ab * p.accw);
+                    const int n = min(chunk, un.j1 - c0);
+                    for (int i = 0; i < n; ++i) {
+                        const int s = g.s;
+                        const uint32_t ph = g.ph;
+                        g.next(p.nstage);
+                        const uint32_t next = mbar_test(smem_u32(&full[g.s]), g.ph);
+                        if (!(ok = qg_wait(smem_u32(&x_full[gx.s]), gx.ph, flags, p.err))) break;
+                        if (!ready && !(ok = qg_wait(smem_u32(&full[s]), ph, flags, p.err))) break;
+                        const int sx = gx.s;
+                        gx.next(p.nx);
+                        ready = next;
+                        tc_fence_after();
+                        const uint32_t x0 = lo0 + (uint32_t)((sx * 2 * NP * half) >> 4), a0 = tmem + (uint32_t)(p.nacc * p.accw + 64 * NP * s);
+                        const int nh = halves(c0 + i);
+                        __syncwarp();
+                        if (lead) {
 #pragma unroll
-                        for (int pass = 0; pass < 2 * NP - 1; ++pass) {
-                            const uint32_t wa = pass == 2 ? wlo : whi, xb = pass == 1 ? xlo : xhi;
+                            for (int h = 0; h < 2; ++h) {
+                                if (h == 1 && nh == 1) break;
 #pragma unroll
-                            for (int kk = 0; kk < 4; ++kk)
-                                tc_mma(dt, wa + 8 * kk, ((uint64_t)dhi << 32) | (xb + 2 * kk), idesc, (i | pass | kk) != 0 ? 1u : 0u);
+                                for (int pass = 0; pass < 2 * NP - 1; ++pass) {  // hi hi, hi lo, lo hi
+                                    const uint32_t wa = a0 + 32 * h + (pass == 2 ? 64 : 0), xb = x0 + (uint32_t)(((pass == 1 ? 2 : 0) + h) * half >> 4);
+#pragma unroll
+                                    for (int kk = 0; kk < 4; ++kk)
+                                        qg_mma_tc<CG>(dt, wa + 8 * kk, ((uint64_t)dhi << 32) | (xb + 2 * kk), idesc, (i | h | pass | kk) != 0 ? 1u : 0u);
+                                }
+                            }
+                            qg_commit<CG>(smem_u32(&empty[s]));
+                            qg_commit<CG>(smem_u32(&x_empty[sx]));
                         }
-                        tc_commit(smem_u32(&empty[s]));
+                        last = s;
+                        last_ph = ph;
                     }
-                    last = s;
-                    last_ph = ph;
-                    ready = nxt;
+                    if (!ok) break;
+                    if (lead) qg_commit<CG>(smem_u32(&acc_full[ab]));
                 }
-                if (!ok) break;
-                if (lead) tc_commit(smem_u32(&acc_full[ab]));
             }
+            // the last commits must land before tensor memory is released
+            if (last >= 0) mbar_drain(smem_u32(&empty[last]), last_ph, flags, p.err);
         }
-        // the last commits must land before tensor memory is released
-        if (last >= 0) mbar_drain(smem_u32(&empty[last]), last_ph, flags, p.err);
     } else if (warp == 2) {
         // ------------------------------ raw weights ------------------------------
-        QgRing r;
-        bool ok = true, wrapped = false;
-        for (int u = blockIdx.x; u < units && ok; u += gridDim.x) {
-            const QgUnit un = place(u);
-            const int nrb = min(8, w.RB - 8 * un.nt);
-            const uint8_t* src = w.data + (long long)un.e * w.expert_stride + ((long long)(8 * un.nt + lane) * w.KS) * seg_bytes;
-            for (int j = un.j0 / 4; 4 * j < un.j1; ++j) {
-                const int s = r.s;
-                if (!(ok = qg_wait(smem_u32(&r_empty[s]), r.ph ^ 1u, flags, p.err))) break;
-                const int nseg = min(2, w.KS - 2 * j);
-                const uint32_t bar = smem_u32(&r_full[s]);
-                if (lane == 0) mbar_arrive_tx(bar, (uint32_t)(nrb * nseg * seg_bytes));
-                __syncwarp();
-                if (lane < nrb) bulk_g2s(smem_u32(raw(s)) + lane * 2 * seg_bytes, src + (long long)(2 * j) * seg_bytes, (uint32_t)(nseg * seg_bytes), bar);
-                __syncwarp();
-                r.next(p.nraw);
-                wrapped |= r.s == 0;
+        if (lane == 0) {
+            QgRing r;
+            bool ok = true, wrapped = false;
+            for (int u = first_unit; u < units && ok; u += unit_step) {
+                const QgUnit un = place(u);
+                for (int j = un.j0; j < un.j1; ++j) {
+                    if (!(ok = qg_wait(smem_u32(&r_empty[r.s]), r.ph ^ 1u, flags, p.err))) break;
+                    const uint32_t bar = smem_u32(&r_full[r.s]);
+                    mbar_arrive_tx(bar, (uint32_t)(8 * seg_bytes));
+                    tma_2d(smem_u32(raw(r.s)), &tw, j * (seg_bytes / 8), un.e * w.RB + 8 * un.nt, bar);
+                    r.next(p.nraw);
+                    wrapped |= r.s == 0;
+                }
             }
+            qg_drain(r, wrapped, p.nraw, r_full, flags, p.err);
         }
-        if (lane == 0) qg_drain(r, wrapped, p.nraw, r_full, flags, p.err);
     } else if (warp < kQgConv0) {
         // ------------------------------ epilogue ------------------------------
         const int ew = warp - kQgEpi0, q = warp & 3, half = ew >> 2;  // column chunks half, half + kQgEpiHalves, ...
@@ -345,9 +449,9 @@ __global__ void __launch_bounds__(kQgThreads, 1) q4g_gemm_kernel(const __grid_co
         float* my_scale = col_scale + ew * kQgBX1;
         int cc = 0;
         bool ok = true;
-        const int chunk = NP == 2 ? kQgChunk : p.kt;
+        const int chunk = NP == 2 ? kQgChunk : w.KS;
         const int F = w.N / 2;
-        for (int u = blockIdx.x; u < units && ok; u += gridDim.x) {
+        for (int u = first_unit; u < units && ok; u += unit_step) {
             const QgUnit un = place(u);
             const int nch = (un.n + 15) / 16;
             const int rb = 8 * un.nt + 2 * q + (lane >> 4);
@@ -405,7 +509,7 @@ __global__ void __launch_bounds__(kQgThreads, 1) q4g_gemm_kernel(const __grid_co
             constexpr int kSums = kQgBX2 / 16 / kQgEpiHalves;
             float sum[NP == 2 ? kSums : 1][16];
             for (int c0 = un.j0; c0 < un.j1; c0 += chunk, ++cc) {
-                const int ab = cc & 1, use = cc >> 1;
+                const int ab = p.nacc == 2 ? (cc & 1) : 0, use = p.nacc == 2 ? (cc >> 1) : cc;
                 if (!(ok = qg_wait(smem_u32(&acc_full[ab]), (uint32_t)(use & 1), flags, p.err))) break;
                 tc_fence_after();
                 __syncwarp();
@@ -436,7 +540,10 @@ __global__ void __launch_bounds__(kQgThreads, 1) q4g_gemm_kernel(const __grid_co
                 __syncwarp();
                 tc_fence_before();
                 __syncwarp();
-                if (lane == 0) mbar_arrive(smem_u32(&acc_empty[ab]));
+                if (lane == 0) {
+                    if (CG == 2) mbar_arrive_cluster(leader_addr(smem_u32(&acc_empty[ab])));
+                    else mbar_arrive(smem_u32(&acc_empty[ab]));
+                }
             }
             if (!ok) break;
             if (NP == 2) {
@@ -447,61 +554,76 @@ __global__ void __launch_bounds__(kQgThreads, 1) q4g_gemm_kernel(const __grid_co
         }
     } else {
         // ------------------------------ conversion ------------------------------
-        const int cw = warp - kQgConv0, q = warp & 3, grp = cw >> 2;
-        QgRing g, r;  // of the raw stage's first tile; of raw stages
-        int count = 0;  // tiles before this raw stage
+        const int cw = warp - kQgConv0, q = warp & 3, hh = (cw >> 2) & 1, grp = cw >> 3;  // row block 2 q + hh of a tile
+        QgRing g, r;      // the next tile's weight and raw stage
+        int turn = 0;     // the group that it is for
+        int stored = -1;  // the stage of this warp's last tile, whose stores have not been waited for
+        auto announce = [&]() {
+            if (stored < 0) return;
+            asm volatile("tcgen05.wait::st.sync.aligned;" ::: "memory");
+            tc_fence_before();
+            __syncwarp();
+            if (lane == 0) {
+                if (CG == 2) mbar_arrive_cluster(leader_addr(smem_u32(&full[stored])));
+                else mbar_arrive(smem_u32(&full[stored]));
+            }
+            stored = -1;
+        };
         const uint32_t magic = opaque(0x64006400u);
         bool ok = true;
-        for (int u = blockIdx.x; u < units && ok; u += gridDim.x) {
+        for (int u = first_unit; u < units && ok; u += unit_step) {
             const QgUnit un = place(u);
-            float m[2][2];  // 2^a of rows g, g + 8 of this warp's two row blocks
-#pragma unroll
-            for (int hh = 0; hh < 2; ++hh) {
-                const int rb = min(8 * un.nt + 2 * q + hh, w.RB - 1);
-                const float* is = p.wis + ((long long)un.e * w.RB + rb) * 16 + (lane >> 2);
-                m[hh][0] = __frcp_rn(__ldg(is));
-                m[hh][1] = __frcp_rn(__ldg(is + 8));
-            }
-            for (int j = un.j0; j < un.j1; j += 4) {
-                const int rs = r.s, n = min(4, un.j1 - j);
-                if (!(ok = qg_wait(smem_u32(&r_full[rs]), r.ph, flags, p.err))) break;
+            const int rb = min(8 * un.nt + 2 * q + hh, w.RB - 1);
+            const float* is = p.wis + ((long long)un.e * w.RB + rb) * 16 + (lane >> 2);
+            const float m0 = __frcp_rn(__ldg(is)), m1 = __frcp_rn(__ldg(is + 8));  // 2^a of rows g, g + 8
+            // The groups take tiles in turn, whatever a unit's number of them: a group that waits for
+            // the release of tile t - nstage has waited for t - groups - nstage, so that with nstage >=
+            // groups the stage's barrier is at most one phase behind the wait's parity.
+            for (int j = un.j0; j < un.j1; ++j, turn = turn + 1 == kQgGroups ? 0 : turn + 1) {
+                const QgRing at = g, ar = r;
+                g.next(p.nstage);
                 r.next(p.nraw);
-                // The groups take tiles in turn, whatever a unit's number of them: a group that waits
-                // for the release of tile t - nstage has waited for t - groups - nstage, so that with
-                // nstage >= groups the stage's barrier is at most one phase behind the wait's parity.
-                for (int i = (grp - count) & (kQgGroups - 1); i < n; i += kQgGroups) {
-                    QgRing at = g;
-                    at.skip(i, p.nstage);
-                    uint32_t hi[16], lo[16];
-                    const uint8_t* seg = raw(rs) + 2 * q * 2 * seg_bytes + (i >> 1) * seg_bytes;
-                    qg_convert<NP, NG>(seg, i & 1, lane, magic, m[0][0], m[0][1], hi, lo);
-                    if (!(ok = qg_wait(smem_u32(&empty[at.s]), at.ph ^ 1u, flags, p.err))) break;
-                    tc_fence_after();
+                if (turn != grp) continue;
+                if (!(ok = qg_wait(smem_u32(&r_full[ar.s]), ar.ph, flags, p.err))) break;
+                const uint8_t* seg = raw(ar.s) + (2 * q + hh) * seg_bytes;
+                const uint32_t col = tmem + ((uint32_t)(32 * q + 16 * hh) << 16) + (uint32_t)(p.nacc * p.accw + 64 * NP * at.s);
+                // what needs no free stage comes before the wait for one, and before the last
+                // tile's stores are waited for
+                uint32_t hi[32], lo[16];
+                qg_convert<NP, NG>(seg, 0, lane, magic, m0, m1, hi, lo);
+                if (NP == 1) {
+                    qg_convert<NP, NG>(seg, 1, lane, magic, m0, m1, hi + 16, lo);
                     __syncwarp();
-                    const uint32_t col = tmem + ((uint32_t)(32 * q) << 16) + (uint32_t)(2 * p.accw + 32 * NP * at.s);
-                    tc_st_frag(col, hi);
-                    if (NP == 2) tc_st_frag(col + 32, lo);
-                    qg_convert<NP, NG>(seg + 2 * seg_bytes, i & 1, lane, magic, m[1][0], m[1][1], hi, lo);
-                    tc_st_frag(col + (16u << 16), hi);
-                    if (NP == 2) tc_st_frag(col + (16u << 16) + 32, lo);
-                    asm volatile("tcgen05.wait::st.sync.aligned;" ::: "memory");
-                    tc_fence_before();
-                    __syncwarp();
-                    if (lane == 0) mbar_arrive(smem_u32(&full[at.s]));
+                    if (lane == 0) mbar_arrive(smem_u32(&r_empty[ar.s]));
                 }
-                if (!ok) break;
-                g.skip(n, p.nstage);
-                count += n;
+                announce();
+                if (!(ok = qg_wait(smem_u32(&empty[at.s]), at.ph ^ 1u, flags, p.err))) break;
+                tc_fence_after();
                 __syncwarp();
-                if (lane == 0) mbar_arrive(smem_u32(&r_empty[rs]));
+                if (NP == 1) {
+                    tc_st_frag64(col, hi);
+                } else {
+                    tc_st_frag(col, hi);
+                    tc_st_frag(col + 64, lo);
+                    qg_convert<NP, NG>(seg, 1, lane, magic, m0, m1, hi, lo);
+                    __syncwarp();
+                    if (lane == 0) mbar_arrive(smem_u32(&r_empty[ar.s]));
+                    tc_st_frag(col + 32, hi);
+                    tc_st_frag(col + 96, lo);
+                }
+                stored = at.s;
+                if (p.nstage <= kQgGroups) announce();  // no stage to spare
             }
         }
+        announce();
     }
     tc_fence_before();
     __syncthreads();
+    if (CG == 2) cluster_sync();  // neither block leaves while the other's MMAs, copies or arrivals may reach it
     if (warp == 1) {
         tc_fence_after();
-        asm volatile("tcgen05.dealloc.cta_group::1.sync.aligned.b32 %0, %1;" ::"r"(tmem), "n"(kTcTmemCols) : "memory");
+        if (CG == 1) asm volatile("tcgen05.dealloc.cta_group::1.sync.aligned.b32 %0, %1;" ::"r"(tmem), "n"(kTcTmemCols) : "memory");
+        else asm volatile("tcgen05.dealloc.cta_group::2.sync.aligned.b32 %0, %1;" ::"r"(tmem), "n"(kTcTmemCols) : "memory");
     }
 }
 
