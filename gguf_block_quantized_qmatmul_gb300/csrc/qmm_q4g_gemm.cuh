@@ -458,6 +458,7 @@ __global__ void __launch_bounds__(kQgThreads, 1) q4g_gemm_kernel(const __grid_co
             const int n = rb < w.RB ? qg_row(w, rb, lane & 15) : -1;
             const float wsn = rb < w.RB ? __ldg(p.wis + ((long long)un.e * w.RB + rb) * 16 + (lane & 15)) : 0.0f;
             __syncwarp();
+            bool valid = true;
             for (int col = lane; col < 16 * nch; col += 32) {
                 int slot = -1;
                 float xsc = 0.0f;
@@ -465,39 +466,63 @@ __global__ void __launch_bounds__(kQgThreads, 1) q4g_gemm_kernel(const __grid_co
                     slot = un.p0 + col;
                     if (grouped) {
                         slot = c.r.order[slot];
-                        if (slot >= slots) slot = -1;
+                        if (slot < 0 || slot >= slots) slot = -1;
+                        valid &= slot >= 0;
                     }
                     xsc = p.xs ? __ldcg(p.xs + un.p0 + col) : 1.0f;
                 }
                 my_slot[col] = slot;
                 my_scale[col] = xsc;
             }
-            __syncwarp();
+            const bool whole = __all_sync(0xffffffffu, valid);  // every column has a row to go to
             const float wup = __shfl_xor_sync(0xffffffffu, wsn, 8);  // the paired row's factor
+            const bool up = (lane & 8) != 0;  // of a pair of rows: lanes r < 8 have gate rows, r + 8 their up rows
+            const float wg = up ? wup : wsn, wu = up ? wsn : wup;
             auto put_as = [&](auto* y, int k, const float v[16]) {  // columns 16 k..
                 using Y = typename std::remove_pointer<decltype(y)>::type;
                 if (c.op == P_GATE_UP) {
-                    // lanes r < 8 have gate rows, r + 8 their up rows; each finishes one of two columns
-                    const bool up = (lane & 8) != 0;
+                    // the lane with the gate row finishes columns 0..7, the one with the up row 8..15
                     const int f = rb * 8 + (lane & 7);
                     const bool on = rb < w.RB && f < F;
+                    const uint32_t row = (uint32_t)F * (uint32_t)sizeof(Y);
+                    char* base = reinterpret_cast<char*>(y + f);
+                    const int4* ps = reinterpret_cast<const int4*>(my_slot + 16 * k + (up ? 8 : 0));
+                    const float4* pc = reinterpret_cast<const float4*>(my_scale + 16 * k + (up ? 8 : 0));
 #pragma unroll
-                    for (int i = 0; i < 16; i += 2) {
-                        const float got = __shfl_xor_sync(0xffffffffu, up ? v[i] : v[i + 1], 8);
-                        const int col = 16 * k + i + (up ? 1 : 0);
-                        const int slot = my_slot[col];
-                        const float xsc = my_scale[col];
-                        const float mine = (up ? v[i + 1] : v[i]) * wsn * xsc, theirs = got * wup * xsc;
-                        const float r = NP == 2 ? swiglu(up ? theirs : mine, up ? mine : theirs) : swiglu_fast(up ? theirs : mine, up ? mine : theirs);
-                        if (on && slot >= 0) y[(long long)slot * F + f] = to_type<Y>(r);
+                    for (int j = 0; j < 2; ++j) {
+                        const int4 s4 = ps[j];
+                        const float4 x4 = pc[j];
+                        const int sl[4] = {s4.x, s4.y, s4.z, s4.w};
+                        const float xc[4] = {x4.x, x4.y, x4.z, x4.w};
+#pragma unroll
+                        for (int i = 0; i < 4; ++i) {
+                            const float lo8 = v[4 * j + i], hi8 = v[4 * j + i + 8];
+                            const float got = __shfl_xor_sync(0xffffffffu, up ? lo8 : hi8, 8), mine = up ? hi8 : lo8;
+                            const float gt = (up ? got : mine) * (wg * xc[i]), ut = (up ? mine : got) * (wu * xc[i]);
+                            const float r = NP == 2 ? swiglu(gt, ut) : swiglu_fast(gt, ut);
+                            if (on && sl[i] >= 0) *reinterpret_cast<Y*>(base + (uint64_t)(uint32_t)sl[i] * row) = to_type<Y>(r);
+                        }
                     }
                 } else if (n >= 0) {
+                    const uint32_t row = (uint32_t)w.N * (uint32_t)sizeof(Y);
+                    char* base = reinterpret_cast<char*>(y + n);
+                    const int4* ps = reinterpret_cast<const int4*>(my_slot + 16 * k);
+                    const float4* pc = reinterpret_cast<const float4*>(my_scale + 16 * k);
+                    auto all = [&](auto guard) {
 #pragma unroll
-                    for (int i = 0; i < 16; ++i) {
-                        const int slot = my_slot[16 * k + i];
-                        const float r = v[i] * wsn * my_scale[16 * k + i];
-                        if (slot >= 0) y[(long long)slot * w.N + n] = to_type<Y>(r);
-                    }
+                        for (int j = 0; j < 4; ++j) {
+                            const int4 s4 = ps[j];
+                            const float4 x4 = pc[j];
+                            const int sl[4] = {s4.x, s4.y, s4.z, s4.w};
+                            const float xc[4] = {x4.x, x4.y, x4.z, x4.w};
+#pragma unroll
+                            for (int i = 0; i < 4; ++i)
+                                if (!decltype(guard)::value || sl[i] >= 0)
+                                    *reinterpret_cast<Y*>(base + (uint64_t)(uint32_t)sl[i] * row) = to_type<Y>(v[4 * j + i] * (wsn * xc[i]));
+                        }
+                    };
+                    if (whole && 16 * k + 16 <= un.n) all(std::false_type());
+                    else all(std::true_type());
                 }
             };
             auto put = [&](int k, const float v[16]) {
@@ -557,6 +582,7 @@ __global__ void __launch_bounds__(kQgThreads, 1) q4g_gemm_kernel(const __grid_co
         const int cw = warp - kQgConv0, q = warp & 3, hh = (cw >> 2) & 1, grp = cw >> 3;  // row block 2 q + hh of a tile
         QgRing g, r;      // the next tile's weight and raw stage
         int turn = 0;     // the group that it is for
+        uint32_t r_ready = 0;  // this group's next raw stage was seen to have landed
         int stored = -1;  // the stage of this warp's last tile, whose stores have not been waited for
         auto announce = [&]() {
             if (stored < 0) return;
@@ -584,7 +610,9 @@ __global__ void __launch_bounds__(kQgThreads, 1) q4g_gemm_kernel(const __grid_co
                 g.next(p.nstage);
                 r.next(p.nraw);
                 if (turn != grp) continue;
-                if (!(ok = qg_wait(smem_u32(&r_full[ar.s]), ar.ph, flags, p.err))) break;
+                if (!r_ready && !(ok = qg_wait(smem_u32(&r_full[ar.s]), ar.ph, flags, p.err))) break;
+                // tested here, needed after the conversion
+                const uint32_t e_ready = mbar_test(smem_u32(&empty[at.s]), at.ph ^ 1u);
                 const uint8_t* seg = raw(ar.s) + (2 * q + hh) * seg_bytes;
                 const uint32_t col = tmem + ((uint32_t)(32 * q + 16 * hh) << 16) + (uint32_t)(p.nacc * p.accw + 64 * NP * at.s);
                 // what needs no free stage comes before the wait for one, and before the last
@@ -597,7 +625,10 @@ __global__ void __launch_bounds__(kQgThreads, 1) q4g_gemm_kernel(const __grid_co
                     if (lane == 0) mbar_arrive(smem_u32(&r_empty[ar.s]));
                 }
                 announce();
-                if (!(ok = qg_wait(smem_u32(&empty[at.s]), at.ph ^ 1u, flags, p.err))) break;
+                if (!e_ready && !(ok = qg_wait(smem_u32(&empty[at.s]), at.ph ^ 1u, flags, p.err))) break;
+                QgRing rn = r;  // this group's next raw stage
+                rn.skip(kQgGroups - 1, p.nraw);
+                r_ready = mbar_test(smem_u32(&r_full[rn.s]), rn.ph);
                 tc_fence_after();
                 __syncwarp();
                 if (NP == 1) {
