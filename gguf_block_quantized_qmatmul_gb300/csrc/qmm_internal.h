@@ -35,9 +35,9 @@ cudaError_t launch_tcx_f32(int wt, const TcxPlan& plan, const void* wq, const fl
 bool make_map(CUtensorMap* m, CUtensorMapDataType dt, const void* base, unsigned long long inner, unsigned long long outer,
               unsigned long long row_bytes, unsigned box_inner, unsigned box_outer, CUtensorMapSwizzle swz);
 
-// The same for 3 dimensions (strides of the second and third in bytes).
-bool make_map_3d(CUtensorMap* m, CUtensorMapDataType dt, const void* base, unsigned long long d0, unsigned long long d1, unsigned long long d2,
-                 unsigned long long stride1, unsigned long long stride2, unsigned box0, unsigned box1, unsigned box2, CUtensorMapSwizzle swz);
+// The same for `rank` dimensions (strides of the second and later ones in bytes).
+bool make_map_nd(CUtensorMap* m, CUtensorMapDataType dt, const void* base, int rank, const unsigned long long* dims,
+                 const unsigned long long* strides, const unsigned* box, CUtensorMapSwizzle swz);
 
 // The current device's error word, SM count and opt-in shared memory (looked up once per device).
 cudaError_t device_constants(unsigned** err, int* sms, int* smem);

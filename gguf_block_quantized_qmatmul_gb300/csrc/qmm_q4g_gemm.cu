@@ -5,15 +5,15 @@
 namespace qmm {
 namespace {
 
-// One row per warp: f16 values (pieces) scaled by 2^b, and 2^-b.  The scale
+// TPR threads per row (a warp where there are many, else a block): f16 values (pieces) scaled by 2^b, and 2^-b.  The scale
 // comes from the row's largest finite magnitude; infinities and NaN stay what
 // they are (their rests are 0).  For experts row p is the activations of slot
 // order[p].  Bound by the rows' bytes; four 16-byte loads a lane are in flight.
-template <int NP, int XT>
+template <int NP, int XT, int TPR>
 __global__ void __launch_bounds__(256) q4g_prep_kernel(const QgCall c, int rows, __half* out, float* xs) {
     grid_dep_launch();
     grid_dep_wait();
-    const int row = blockIdx.x * 8 + (threadIdx.x >> 5), lane = threadIdx.x & 31, K = c.w.K, pitch = (K + 63) / 64 * 64;
+    const int row = blockIdx.x * (256 / TPR) + threadIdx.x / TPR, lane = threadIdx.x % TPR, K = c.w.K, pitch = (K + 63) / 64 * 64;
     if (row >= rows) return;
     int from = row;
     if (c.op != P_DENSE) {
@@ -31,14 +31,14 @@ __global__ void __launch_bounds__(256) q4g_prep_kernel(const QgCall c, int rows,
         if (NP == 2) reinterpret_cast<uint4*>(hr + (long long)rows * pitch + K)[lane] = make_uint4(0u, 0u, 0u, 0u);
     }
     if (XT == X_F16) {
-        for (int i = lane; i < n; i += 128) {
+        for (int i = lane; i < n; i += 4 * TPR) {
             uint4 v[4];
 #pragma unroll
             for (int j = 0; j < 4; ++j)
-                if (i + 32 * j < n) v[j] = __ldg(x + i + 32 * j);
+                if (i + TPR * j < n) v[j] = __ldg(x + i + TPR * j);
 #pragma unroll
             for (int j = 0; j < 4; ++j)
-                if (i + 32 * j < n) reinterpret_cast<uint4*>(hr)[i + 32 * j] = v[j];
+                if (i + TPR * j < n) reinterpret_cast<uint4*>(hr)[i + TPR * j] = v[j];
         }
         return;
     }
@@ -55,10 +55,10 @@ __global__ void __launch_bounds__(256) q4g_prep_kernel(const QgCall c, int rows,
         }
     };
     float m = 0.0f;
-    for (int i = lane; i < n; i += 128) {
+    for (int i = lane; i < n; i += 4 * TPR) {
         uint4 v[4];
 #pragma unroll
-        for (int j = 0; j < 4; ++j) v[j] = i + 32 * j < n ? __ldg(x + i + 32 * j) : make_uint4(0u, 0u, 0u, 0u);
+        for (int j = 0; j < 4; ++j) v[j] = i + TPR * j < n ? __ldg(x + i + TPR * j) : make_uint4(0u, 0u, 0u, 0u);
 #pragma unroll
         for (int j = 0; j < 4; ++j) {
             float f[8];
@@ -69,16 +69,23 @@ __global__ void __launch_bounds__(256) q4g_prep_kernel(const QgCall c, int rows,
     }
 #pragma unroll
     for (int o = 16; o; o >>= 1) m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, o));
+    if (TPR > 32) {
+        __shared__ float red[8];
+        if ((threadIdx.x & 31) == 0) red[threadIdx.x >> 5] = m;
+        __syncthreads();
+#pragma unroll
+        for (int i = 0; i < 8; ++i) m = fmaxf(m, red[i]);
+    }
     const float is = tc_row_iscale(m), sc = __frcp_rn(is);
     if (lane == 0) xs[row] = is;
-    for (int i = lane; i < n; i += 128) {
+    for (int i = lane; i < n; i += 4 * TPR) {
         uint4 v[4];
 #pragma unroll
         for (int j = 0; j < 4; ++j)
-            if (i + 32 * j < n) v[j] = __ldg(x + i + 32 * j);
+            if (i + TPR * j < n) v[j] = __ldg(x + i + TPR * j);
 #pragma unroll
         for (int j = 0; j < 4; ++j) {
-            if (i + 32 * j >= n) continue;
+            if (i + TPR * j >= n) continue;
             float f[8];
             unpack(v[j], f);
             uint32_t h[V / 2], l[V / 2];
@@ -94,10 +101,10 @@ __global__ void __launch_bounds__(256) q4g_prep_kernel(const QgCall c, int rows,
                 }
             }
             if constexpr (V == 8) {
-                reinterpret_cast<uint4*>(hr)[i + 32 * j] = make_uint4(h[0], h[1], h[2], h[3]);
+                reinterpret_cast<uint4*>(hr)[i + TPR * j] = make_uint4(h[0], h[1], h[2], h[3]);
             } else {
-                reinterpret_cast<uint2*>(hr)[i + 32 * j] = make_uint2(h[0], h[1]);
-                reinterpret_cast<uint2*>(hr + (long long)rows * pitch)[i + 32 * j] = make_uint2(l[0], l[1]);
+                reinterpret_cast<uint2*>(hr)[i + TPR * j] = make_uint2(h[0], h[1]);
+                reinterpret_cast<uint2*>(hr + (long long)rows * pitch)[i + TPR * j] = make_uint2(l[0], l[1]);
             }
         }
     }
@@ -206,19 +213,24 @@ cudaError_t launch_q4g_gemm(const QgGemmPlan& pl, const QgCall& c, void* ws, uns
     if (pl.prep) {
         __half* xh = reinterpret_cast<__half*>(wsb + pl.ws_x);
         if (c.xt != X_F16) xs = reinterpret_cast<float*>(wsb + pl.ws_xs);
-        const unsigned blocks = (unsigned)((rows + 7) / 8);
-        const cudaError_t e = c.xt == X_F32   ? launch_pdl(q4g_prep_kernel<2, X_F32>, blocks, 256, 0, s, c, rows, xh, xs)
-                              : c.xt == X_F16 ? launch_pdl(q4g_prep_kernel<1, X_F16>, blocks, 256, 0, s, c, rows, xh, xs)
-                                              : launch_pdl(q4g_prep_kernel<1, X_BF16>, blocks, 256, 0, s, c, rows, xh, xs);
+        // a warp per row needs some 5000 rows to fill the GPU; a few rows take 9 us that way, 3 with a block each
+        const bool many = rows >= 4096;
+        const unsigned blocks = (unsigned)(many ? (rows + 7) / 8 : rows);
+        auto* k = c.xt == X_F32   ? (many ? q4g_prep_kernel<2, X_F32, 32> : q4g_prep_kernel<2, X_F32, 256>)
+                  : c.xt == X_F16 ? (many ? q4g_prep_kernel<1, X_F16, 32> : q4g_prep_kernel<1, X_F16, 256>)
+                                  : (many ? q4g_prep_kernel<1, X_BF16, 32> : q4g_prep_kernel<1, X_BF16, 256>);
+        const cudaError_t e = launch_pdl(k, blocks, 256, 0, s, c, rows, xh, xs);
         if (e != cudaSuccess) return e;
         xsrc = xh;
         pitch = (long long)(K + 63) / 64 * 64 * 2;
     }
-    // activations: 64 K x rows x K / 64, a box of half a pair's rows and two of the last
+    // activations: 64 K x rows x pieces x K / 64; a box has a block's rows (half a pair's), all
+    // pieces and two of the last
     CUtensorMap tx;
-    if (!make_map_3d(&tx, CU_TENSOR_MAP_DATA_TYPE_FLOAT16, xsrc, 64, (unsigned long long)rows * pl.np, (unsigned long long)(K + 63) / 64,
-                     (unsigned long long)pitch, 128, 64, (unsigned)(pl.bx / pl.cg), 2, CU_TENSOR_MAP_SWIZZLE_128B))
-        return cudaErrorInvalidValue;
+    const unsigned long long xdims[4] = {64, (unsigned long long)rows, (unsigned long long)pl.np, (unsigned long long)(K + 63) / 64};
+    const unsigned long long xstrides[3] = {(unsigned long long)pitch, (unsigned long long)pitch * rows, 128};
+    const unsigned xbox[4] = {64, (unsigned)(pl.bx / pl.cg), (unsigned)pl.np, 2};
+    if (!make_map_nd(&tx, CU_TENSOR_MAP_DATA_TYPE_FLOAT16, xsrc, 4, xdims, xstrides, xbox, CU_TENSOR_MAP_SWIZZLE_128B)) return cudaErrorInvalidValue;
     // raw weights: row blocks of all experts, 8-byte elements, a box of a segment of eight of them
     CUtensorMap tw;
     const unsigned seg = (unsigned)qg_seg_bytes(c.w.ng);
@@ -231,7 +243,6 @@ cudaError_t launch_q4g_gemm(const QgGemmPlan& pl, const QgCall& c, void* ws, uns
     p.xs = xs;
     p.wis = reinterpret_cast<const float*>(c.w.data + c.w.iscale_off);
     p.err = err;
-    p.xrows = rows;
     p.bx = pl.bx;
     p.nacc = pl.nacc;
     p.accw = pl.accw;

@@ -23,10 +23,10 @@
 // write and read every activation row of its tile in its shared memory for 128
 // weight rows, 128 bytes a cycle at the MMAs' peak, all that there is.
 //   warp 0      one thread: activation tiles (128 K, two halves with 128-byte
-//               swizzle), one 3-D box each (several made this thread's issue the
-//               limit, 850 cycles a tile); the experts' rows were put in sorted order by the preparation launch
-//               (gathering four rows a copy here measured 90 cycles a copy: 643 us
-//               against the whole of 2048 tokens x 8 of 64 experts, 2048 -> 2 x 1024)
+//               swizzle), one 4-D box each (several made this thread's issue the
+//               limit, 850 cycles a tile); the experts' rows were put in sorted
+//               order by the preparation launch (gathering four rows a copy here
+//               took 90 cycles a copy)
 //   warp 1      one elected lane: eight MMAs (24 with two pieces) per tile of 128 K, A
 //               in tensor memory, B in shared memory.  (With tiles of 64 K its wait,
 //               commits and bookkeeping, about 300 cycles a tile alone and 500 beside
@@ -69,7 +69,6 @@ struct QgGemmParams {
     const float* xs;      // 2^-b per activation row (experts: per sorted position); NULL: 1
     const float* wis;     // 2^-a per weight row, layout order
     unsigned* err;
-    int xrows;            // rows of an activation plane (the lo plane follows)
     int bx, nacc, accw, mtiles, ntiles, nraw, nx, nstage;
     int ks;               // K slices (dense): f32 partial outputs [ks][M][N]
     int off_raw, off_bar;
@@ -116,19 +115,20 @@ __device__ __forceinline__ uint32_t leader_addr(uint32_t a) {
 __device__ __forceinline__ void mbar_arrive_cluster(uint32_t a) {
     asm volatile("mbarrier.arrive.relaxed.cluster.shared::cluster.b64 _, [%0];" ::"r"(a) : "memory");
 }
-// load one TMA box of a 3-D tensor map
-__device__ __forceinline__ void tma_3d(uint32_t dst, const CUtensorMap* map, int x, int y, int z, uint32_t bar) {
-    asm volatile(
-        "cp.async.bulk.tensor.3d.shared::cluster.global.mbarrier::complete_tx::bytes [%0], [%1, {%2, %3, %4}], [%5];" ::"r"(dst),
-        "l"(map), "r"(x), "r"(y), "r"(z), "r"(bar)
-        : "memory");
-}
-// the same, completing on a barrier of the pair's leader
-__device__ __forceinline__ void tma_3d_pair(uint32_t dst, const CUtensorMap* map, int x, int y, int z, uint32_t bar) {
-    asm volatile(
-        "cp.async.bulk.tensor.3d.cta_group::2.shared::cluster.global.mbarrier::complete_tx::bytes [%0], [%1, {%2, %3, %4}], [%5];" ::"r"(dst),
-        "l"(map), "r"(x), "r"(y), "r"(z), "r"(bar)
-        : "memory");
+// One TMA box of a 4-D tensor map; CG = 2: completing on a barrier of the pair's leader.
+template <int CG>
+__device__ __forceinline__ void tma_4d(uint32_t dst, const CUtensorMap* map, int x, int y, int z, int t, uint32_t bar) {
+    if (CG == 1)
+        asm volatile(
+            "cp.async.bulk.tensor.4d.shared::cluster.global.mbarrier::complete_tx::bytes [%0], [%1, {%2, %3, %4, %5}], [%6];" ::"r"(dst),
+            "l"(map), "r"(x), "r"(y), "r"(z), "r"(t), "r"(bar)
+            : "memory");
+    else
+        asm volatile(
+            "cp.async.bulk.tensor.4d.cta_group::2.shared::cluster.global.mbarrier::complete_tx::bytes [%0], [%1, {%2, %3, %4, %5}], [%6];" ::"r"(
+                dst),
+            "l"(map), "r"(x), "r"(y), "r"(z), "r"(t), "r"(bar)
+            : "memory");
 }
 template <int CG>
 __device__ __forceinline__ void qg_mma_tc(uint32_t tmem, uint32_t ta, uint64_t db, uint32_t idesc, uint32_t accumulate) {
@@ -324,7 +324,7 @@ __global__ void __launch_bounds__(kQgThreads, 1) q4g_gemm_kernel(const __grid_co
         return un;
     };
     if (!grouped && warp != 2) grid_dep_wait();  // weights are constant: their copies may start at once
-    // an activation stage: per piece two 64-K halves; of a pair, each block has half the rows
+    // an activation stage: two 64-K halves of the rows' pieces; of a pair, each block has half the rows
     const int half = p.bx / CG * 128;
     auto stage = [&](int s) { return sm + s * 2 * NP * half; };
     const int seg_bytes = qg_seg_bytes(NG);
@@ -346,11 +346,7 @@ __global__ void __launch_bounds__(kQgThreads, 1) q4g_gemm_kernel(const __grid_co
                     const uint32_t to = smem_u32(stage(g.s));
                     if (rank == 0) mbar_arrive_tx(bar, (uint32_t)(CG * NP * 2 * half));
                     if (CG == 2) bar = leader_addr(bar);
-#pragma unroll
-                    for (int pc = 0; pc < NP; ++pc) {
-                        if (CG == 2) tma_3d_pair(to + 2 * pc * half, &tx, 0, pc * p.xrows + p0, 2 * j, bar);
-                        else tma_3d(to + 2 * pc * half, &tx, 0, pc * p.xrows + p0, 2 * j, bar);
-                    }
+                    tma_4d<CG>(to, &tx, 0, p0, 0, 2 * j, bar);
                     g.next(p.nx);
                     wrapped |= g.s == 0;
                 }
@@ -404,7 +400,7 @@ __global__ void __launch_bounds__(kQgThreads, 1) q4g_gemm_kernel(const __grid_co
                                 if (h == 1 && nh == 1) break;
 #pragma unroll
                                 for (int pass = 0; pass < 2 * NP - 1; ++pass) {  // hi hi, hi lo, lo hi
-                                    const uint32_t wa = a0 + 32 * h + (pass == 2 ? 64 : 0), xb = x0 + (uint32_t)(((pass == 1 ? 2 : 0) + h) * half >> 4);
+                                    const uint32_t wa = a0 + 32 * h + (pass == 2 ? 64 : 0), xb = x0 + (uint32_t)((h * NP + (pass == 1)) * half >> 4);
 #pragma unroll
                                     for (int kk = 0; kk < 4; ++kk)
                                         qg_mma_tc<CG>(dt, wa + 8 * kk, ((uint64_t)dhi << 32) | (xb + 2 * kk), idesc, (i | h | pass | kk) != 0 ? 1u : 0u);
@@ -543,8 +539,9 @@ __global__ void __launch_bounds__(kQgThreads, 1) q4g_gemm_kernel(const __grid_co
 #pragma unroll
                     for (int k = 0; k < kSums; ++k) {
                         uint32_t r[16];
-                        if (half + kQgEpiHalves * k < nch) {
-                            tc_ld16(acol + 16 * (half + kQgEpiHalves * k), r);
+                        const int ch = half + kQgEpiHalves * k;
+                        if (ch < nch) {
+                            tc_ld16(acol + 16 * ch, r);
                             tc_wait_ld();
 #pragma unroll
                             for (int i = 0; i < 16; ++i) sum[NP == 2 ? k : 0][i] = c0 == un.j0 ? __uint_as_float(r[i]) : sum[NP == 2 ? k : 0][i] + __uint_as_float(r[i]);

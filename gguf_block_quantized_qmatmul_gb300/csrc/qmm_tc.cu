@@ -77,15 +77,19 @@ bool make_map(CUtensorMap* m, CUtensorMapDataType dt, const void* base, unsigned
               CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
 }
 
-bool make_map_3d(CUtensorMap* m, CUtensorMapDataType dt, const void* base, unsigned long long d0, unsigned long long d1, unsigned long long d2,
-                 unsigned long long stride1, unsigned long long stride2, unsigned box0, unsigned box1, unsigned box2, CUtensorMapSwizzle swz) {
+bool make_map_nd(CUtensorMap* m, CUtensorMapDataType dt, const void* base, int rank, const unsigned long long* dims,
+                 const unsigned long long* strides, const unsigned* box, CUtensorMapSwizzle swz) {
     auto fn = encode_fn();
-    if (!fn) return false;
-    const cuuint64_t dims[3] = {d0, d1, d2};
-    const cuuint64_t strides[2] = {stride1, stride2};
-    const cuuint32_t box[3] = {box0, box1, box2};
-    const cuuint32_t es[3] = {1, 1, 1};
-    return fn(m, dt, 3, const_cast<void*>(base), dims, strides, box, es, CU_TENSOR_MAP_INTERLEAVE_NONE, swz,
+    if (!fn || rank < 1 || rank > 5) return false;
+    cuuint64_t d[5], st[5];
+    cuuint32_t b[5], es[5];
+    for (int i = 0; i < rank; ++i) {
+        d[i] = dims[i];
+        if (i + 1 < rank) st[i] = strides[i];
+        b[i] = box[i];
+        es[i] = 1;
+    }
+    return fn(m, dt, (cuuint32_t)rank, const_cast<void*>(base), d, st, b, es, CU_TENSOR_MAP_INTERLEAVE_NONE, swz,
               CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
 }
 
