@@ -31,9 +31,14 @@ qmm_status check_rows(const void* x, int xt, int64_t ldx, int64_t K) {
 }
 
 // The kernel a product goes to.  The row kernel streams the weights once per
-// `cols` activation rows and turns every code into an MMA operand once per
-// eight; past 32 columns (16-bit activations; an f32 row is three) the GEMM,
-// whose conversion serves up to 256 rows, is faster.
+// item of a few activation rows and turns every code into an MMA operand once
+// per 8 columns (an f32 row is three): about 3 us + 4e-8 us per weight and
+// column.  The GEMM's conversion serves up to 256 rows, but a call has some 8
+// us of fixed cost.  Measured (row kernel / GEMM, us): 4096 x 4096 bf16, 8 rows
+// 8.4 / 11.3, 16 rows 17.0 / 11.0; 14336 x 4096 f32, 8 rows 23.0 / 24.0, 10
+// rows 29.9 / 24.0; 1000 x 2048 bf16, 64 rows 7.5 / 9.5; 4096 x 14336 bf16, 8
+// rows (two items) 23.7 / 20.4; gate_up of 64 experts, 2048 -> 2 x 1024 bf16,
+// 8 slots an expert 60 / 69, 16 slots 123 / 70; f32, 4 slots 106 / 98.
 struct Choice {
     bool gemm = false;
     QgRowsPlan rows;
@@ -44,8 +49,12 @@ struct Choice {
 Choice choose(const QgCall& c, int sms, int smem) {
     Choice ch;
     const int np = c.xt == X_F32 ? 3 : 1;
-    const bool few = c.op == P_DENSE ? (long long)c.M * np <= 32 : (long long)c.M * np <= 8ll * c.w.E;
+    const long long columns = (long long)c.M * np, size = (long long)c.w.N * c.w.K;
+    const bool small = columns * size <= 160000000;
+    const bool few = c.op == P_DENSE ? columns <= 8 || (columns <= 24 && np == 3) || small : columns <= 8ll * c.w.E;
     if (few) ch.rows = plan_q4g_rows(c, sms, smem);
+    // activations that do not fit one pass over a large matrix
+    if (ch.rows.ok && c.op == P_DENSE && ch.rows.items > 1 && !small && (ch.mm = plan_q4g_gemm(c, sms, smem)).ok) ch.rows.ok = false;
     if (!ch.rows.ok) ch.mm = plan_q4g_gemm(c, sms, smem);
     if (!ch.rows.ok && !ch.mm.ok) ch.rows = plan_q4g_rows(c, sms, smem);
     ch.gemm = !ch.rows.ok && ch.mm.ok;

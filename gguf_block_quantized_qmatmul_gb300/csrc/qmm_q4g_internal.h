@@ -48,6 +48,7 @@ struct QgRowsPlan {
     int np = 0;            // 16-bit pieces per activation value
     int warps = 0, wk = 0; // warps per block, warps that split K
     int blocks = 0;
+    long long items = 0;
     int off_zero = 0, off_red = 0, off_ring = 0;
     size_t smem = 0;
     size_t workspace = 0;  // P_DOWN by expert: f32 partial rows [T top_k][N]

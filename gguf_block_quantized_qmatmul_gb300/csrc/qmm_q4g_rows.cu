@@ -89,16 +89,11 @@ QgRowsPlan plan_q4g_rows(const QgCall& c, int sms, int smem_max) {
     pl.np = c.xt == X_F32 ? 3 : 1;
     if (c.op != P_DENSE && c.w.E > kQgRowMaxE) return pl;
     const long long row_bytes = (long long)pl.np * c.w.KS * kQgSegK * 2;  // staged bytes of one activation row
-    const int max_cols = 32 / pl.np;
     const long long slots = c.M;
-    if (c.op == P_DENSE) {
-        pl.cols = c.M < max_cols ? c.M : max_cols;
-    } else {
+    if (c.op != P_DENSE) {
         // one slot (one token) an item while few slots share an expert: no items to look up, and no
         // partial sums; by expert, an item is up to `cols` of its slots with one weight stream
         pl.by_slot = c.r.T <= 4 && c.r.top_k <= kQgMaxK && (c.op == P_GATE_UP || row_bytes * c.r.top_k <= 96 * 1024);
-        const long long avg = (slots + c.w.E - 1) / c.w.E;
-        pl.cols = pl.by_slot ? 1 : avg * pl.np <= 4 ? (8 / pl.np) : avg * pl.np <= 8 ? 16 / pl.np : max_cols;
     }
     const bool token = c.op == P_DOWN && pl.by_slot;
     const long long rows_mul = token ? c.r.top_k : 1;
@@ -110,40 +105,52 @@ QgRowsPlan plan_q4g_rows(const QgCall& c, int sms, int smem_max) {
         return cols * row_bytes * rows_mul + 16 + red(nb_of(cols), warps) + (long long)warps * kQgDepth * seg;
     };
     const long long room = smem_max - kQgRowStatic - 1024;
-    // as many columns as shared memory holds beside eight warps
-    while (pl.cols > 1 && need(pl.cols, 8) > room) --pl.cols;
-    if (need(pl.cols, 8) > room) return pl;
-    long long items, most = 0;  // items expected, and at most
-    if (c.op == P_DENSE) {
-        items = (c.M + pl.cols - 1) / pl.cols;
-        pl.cols = (int)((c.M + items - 1) / items);
-    } else if (pl.by_slot) {
-        items = c.op == P_GATE_UP ? slots : c.r.T;
-    } else {
-        // the experts that some slot chose, under even routing; an expert's last item may be partial
-        items = (long long)(c.w.E * (1.0 - pow(1.0 - 1.0 / c.w.E, (double)slots)) + 0.999) + slots / pl.cols;
-        most = c.w.E + slots / pl.cols;
-        if (items > most) items = most;
-        if (items > slots) items = slots;
+    // Rows of x per item: full MMA column blocks, or what there is.  A second block of columns costs
+    // a segment about half as much again, four about 1.3 times as much again.
+    int choices[3] = {8 / pl.np, 16 / pl.np, 32 / pl.np}, nchoice = 3;
+    if (c.op != P_DENSE) {
+        const long long avg = (slots + c.w.E - 1) / c.w.E;
+        choices[0] = pl.by_slot ? 1 : avg * pl.np <= 4 ? 8 / pl.np : avg * pl.np <= 8 ? 16 / pl.np : 32 / pl.np;
+        nchoice = 1;
     }
-    if (items < 1) items = 1;
-    pl.nb = nb_of(pl.cols);
     double best = 0;
-    for (int warps : {24, 16, 8}) {
-        if (warps > qg_row_warps(pl.nb)) continue;
-        if (need(pl.cols, warps) > room) continue;
-        for (int wk = 1; wk <= 8; wk *= 2) {
-            const int wr = warps / wk, nit = (VS + wk - 1) / wk;
-            if (wr > 15 && wk > 1) continue;  // named barriers
-            const long long work = items * c.w.RB, blocks = work < sms ? work : sms;
-            const double share = (double)work / blocks;  // row blocks per block
-            // segments a warp takes in turn, its row blocks' barriers and sums (about one each); more warps share an SM's issue slots
-            const double cost = ceil(share / wr) * (nit + 1.0) * (warps >= 16 ? warps / 16.0 : 1.0);
-            if (best == 0 || cost < 0.999 * best || (cost <= 1.001 * best && wk > pl.wk)) {
-                best = cost;
-                pl.warps = warps;
-                pl.wk = wk;
-                pl.blocks = (int)blocks;
+    for (int ch = 0; ch < nchoice; ++ch) {
+        int cols = c.op == P_DENSE && c.M < choices[ch] ? c.M : choices[ch];
+        while (cols > 1 && need(cols, 8) > room) --cols;  // as many as shared memory holds beside eight warps
+        if (need(cols, 8) > room) continue;
+        long long items;  // expected
+        if (c.op == P_DENSE) {
+            items = (c.M + cols - 1) / cols;
+            cols = (int)((c.M + items - 1) / items);
+        } else if (pl.by_slot) {
+            items = c.op == P_GATE_UP ? slots : c.r.T;
+        } else {
+            // the experts that some slot chose, under even routing; an expert's last item may be partial
+            items = (long long)(c.w.E * (1.0 - pow(1.0 - 1.0 / c.w.E, (double)slots)) + 0.999) + slots / cols;
+            if (items > c.w.E + slots / cols) items = c.w.E + slots / cols;
+            if (items > slots) items = slots;
+        }
+        if (items < 1) items = 1;
+        const int nb = nb_of(cols);
+        for (int warps : {24, 16, 8}) {
+            if (warps > qg_row_warps(nb) || need(cols, warps) > room) continue;
+            for (int wk = 1; wk <= 8; wk *= 2) {
+                const int wr = warps / wk, nit = (VS + wk - 1) / wk;
+                if (wr > 15 && wk > 1) continue;  // named barriers
+                const long long work = items * c.w.RB, blocks = work < sms ? work : sms;
+                const double share = (double)work / blocks;  // row blocks per block
+                // segments a warp takes in turn, its row blocks' barriers and sums (about one each);
+                // more warps share an SM's issue slots
+                const double cost = ceil(share / wr) * (nit + 1.0) * (warps >= 16 ? warps / 16.0 : 1.0) * (nb == 1 ? 1.0 : nb == 2 ? 1.5 : 2.3);
+                if (best == 0 || cost < 0.999 * best || (cost <= 1.001 * best && nb <= pl.nb && wk > pl.wk)) {
+                    best = cost;
+                    pl.cols = cols;
+                    pl.nb = nb;
+                    pl.warps = warps;
+                    pl.wk = wk;
+                    pl.blocks = (int)blocks;
+                    pl.items = items;
+                }
             }
         }
     }

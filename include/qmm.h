@@ -271,11 +271,13 @@ qmm_status qmm_matmul_static_workspace(qmm_type wtype, qmm_act_mode mode, const 
    reads that.  Activations and outputs are f32, f16 or bf16, one type per
    call; sums are f32 and are rounded once, at the end.
 
-   Accuracy: up to 32 activation rows (f32: 10) per weight matrix no weight is
-   rounded; beyond, f16 and bf16 calls round each weight s (q - z) to f16's 11
-   bits, which is below the rounding of the output, and f32 calls keep 22 bits
-   of the activations and all of the weights.  A row of x with an infinity or
-   a NaN gives a row of outputs that are not finite; no other row is touched.
+   Accuracy: one activation row of up to 16384 values rounds no weight, nor do
+   more rows times a small matrix.  Otherwise (the choice depends on the type
+   and the sizes alone) f16 and bf16 calls round each weight s (q - z) to f16's
+   11 bits, which is below the rounding of the output in bf16, and f32 calls
+   keep 22 bits of the activations and all of the weights.  A row of x with an
+   infinity or a NaN gives a row of outputs that are not finite; no other row
+   is touched.
    Results do not depend on the run: no sum's order varies. */
 
 typedef enum { QMM_FLOAT_F32 = 0, QMM_FLOAT_F16 = 1, QMM_FLOAT_BF16 = 2 } qmm_float;
@@ -309,8 +311,8 @@ qmm_status qmm_q4g_dequantize(const qmm_q4g* w, float* out, qmm_stream_t stream)
 
 /* y [M, N] = x [M, K] . W^T for one weight matrix (experts = 1, not paired).
    Rows of x are ldx elements apart (ldx >= K, a multiple of 16 bytes); y is
-   contiguous.  workspace: qmm_q4g_matmul_workspace(...) bytes (0 up to 32 rows,
-   f32: 10), uninitialised; calls that may overlap need one each.
+   contiguous.  workspace: qmm_q4g_matmul_workspace(...) bytes (0 for few rows),
+   uninitialised; calls that may overlap need one each.
    Errors: TYPE, NULL, SHAPE, ALIGN, WORKSPACE, CUDA. */
 size_t qmm_q4g_matmul_workspace(const qmm_q4g* w, qmm_float xtype, int64_t M);
 qmm_status qmm_q4g_matmul(const qmm_q4g* w, qmm_float xtype, const void* x, int64_t ldx, int64_t M, void* y, void* workspace,

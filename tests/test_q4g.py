@@ -93,17 +93,19 @@ def test_pack_q4_0_is_the_block_format(q):
 # ------------------------------------------------------------------ dense product
 
 DENSE = [
-    # M, N, K, G, zeros, dt: the row kernel
+    # M, N, K, G, zeros, dt: few rows or a small matrix
     (1, 576, 576, 32, False, "f32"), (1, 1, 32, 32, True, "f16"), (1, 15, 64, 64, False, "bf16"), (2, 17, 96, 32, True, "f32"),
     (3, 100, 1536, 128, True, "bf16"), (7, 33, 160, 32, True, "f16"), (8, 192, 576, 64, False, "bf16"), (9, 48, 128, 128, True, "f16"),
     (10, 40, 320, 64, True, "f32"), (16, 300, 1024, 128, False, "f16"), (31, 70, 192, 64, True, "bf16"), (32, 576, 576, 32, True, "f16"),
     (1, 96, 16384, 128, True, "f32"), (5, 40, 14336, 128, True, "f32"), (32, 24, 14336, 64, True, "bf16"), (1, 9000, 128, 128, True, "f16"),
     (1, 5000, 256, 64, False, "bf16"),
-    # the GEMM
+    # more
     (33, 128, 256, 128, True, "f16"), (33, 17, 32, 32, True, "bf16"), (64, 130, 96, 32, False, "f16"), (100, 576, 576, 64, True, "bf16"),
     (129, 257, 320, 64, True, "f16"), (257, 300, 1536, 128, True, "bf16"), (300, 129, 160, 32, True, "f16"), (1000, 64, 128, 128, False, "bf16"),
     (11, 40, 64, 64, True, "f32"), (37, 300, 1024, 32, True, "f32"), (130, 200, 576, 64, True, "f32"), (300, 144, 1600, 32, False, "f32"),
-    (33, 40, 14336, 128, True, "f32"), (40, 2500, 320, 64, True, "f16"), (530, 2000, 256, 128, True, "bf16")]
+    (33, 40, 14336, 128, True, "f32"), (40, 2500, 320, 64, True, "f16"), (530, 2000, 256, 128, True, "bf16"),
+    (17, 4100, 4096, 64, True, "f16"), (12, 6000, 2048, 32, True, "f32"), (260, 4000, 1088, 64, True, "f16"), (65, 9000, 320, 64, True, "bf16"),
+    (200, 1030, 4160, 32, False, "bf16"), (70, 4500, 672, 32, True, "f32"), (1100, 500, 2048, 128, True, "f16"), (700, 3000, 96, 32, True, "bf16")]
 
 
 @pytest.mark.parametrize("M,N,K,G,zeros,dt", DENSE)
@@ -117,15 +119,15 @@ def test_matmul(q, M, N, K, G, zeros, dt):
     y = q.q4g_matmul(w, x.cuda())
     W, xd = t[3][0], x.double()
     ref, T = xd @ W.T, xd.abs() @ W.abs().T
-    gemm = q.q4g_matmul_workspace(w, DT[dt], M) > 0 or (dt == "f16" and M > 32)
+    gemm = M > 8  # may round weights
     check(y, ref, tolerance(dt, ref, T, gemm), norm_tolerance(dt, gemm))
     assert torch.equal(y, q.q4g_matmul(w, x.cuda()))  # the same on every run
     assert q.last_device_error() == 0
 
 
-@pytest.mark.parametrize("M,dt", [(3, "f16"), (9, "f32"), (70, "f16"), (70, "bf16"), (70, "f32")])
+@pytest.mark.parametrize("M,dt", [(3, "f16"), (9, "f32"), (300, "f16"), (300, "bf16"), (300, "f32")])
 def test_matmul_rows_apart_and_canary(q, M, dt):
-    N, K = 70, 320
+    N, K = 1900, 320
     t = make(1, N, K, 64, True, "f16", 9)
     w = pack(q, t)
     wide = torch.full((M, K + 64), float("nan"), dtype=DT[dt], device="cuda")
@@ -138,9 +140,9 @@ def test_matmul_rows_apart_and_canary(q, M, dt):
     assert bool((buf[M * N:] == 7).all())
 
 
-@pytest.mark.parametrize("M,dt", [(4, "f16"), (4, "bf16"), (4, "f32"), (80, "f16"), (80, "bf16"), (80, "f32")])
+@pytest.mark.parametrize("M,dt", [(4, "f16"), (4, "bf16"), (4, "f32"), (600, "f16"), (600, "bf16"), (600, "f32")])
 def test_matmul_keeps_bad_rows_to_themselves(q, M, dt):
-    N, K = 150, 192
+    N, K = 1500, 192
     w = pack(q, make(1, N, K, 64, True, "bf16", 4))
     x = torch.randn((M, K), generator=rng(2)).to(DT[dt]).cuda()
     bad = x.clone()
@@ -152,10 +154,10 @@ def test_matmul_keeps_bad_rows_to_themselves(q, M, dt):
     assert torch.equal(y[keep], z[keep])
 
 
-@pytest.mark.parametrize("dt,M", [("f32", 2), ("bf16", 2), ("bf16", 40), ("f32", 40), ("f16", 2), ("f16", 40)])
+@pytest.mark.parametrize("dt,M", [("f32", 2), ("bf16", 2), ("bf16", 700), ("f32", 700), ("f16", 2), ("f16", 700)])
 def test_matmul_extreme_magnitudes(q, dt, M):
     """Scales and activations near the ends of their types' ranges."""
-    N, K = 40, 256
+    N, K = 1000, 256
     sdt = "f16" if dt == "f16" else "bf16"
     for scale, xs in ((1e-4, 1e3), (100.0, 1e-3)) if dt == "f16" else ((1e-25, 1e20), (1e20, 1e-25)):
         t = make(1, N, K, 64, True, sdt, 5, scale)
@@ -168,7 +170,7 @@ def test_matmul_extreme_magnitudes(q, dt, M):
 def test_matmul_empty_and_streams(q):
     w = pack(q, make(1, 64, 128, 64, True, "f16", 4))
     assert q.q4g_matmul(w, torch.empty((0, 128), dtype=torch.float16, device="cuda")).shape == (0, 64)
-    for M in (3, 90):
+    for M in (3, 20000):
         x = torch.randn((M, 128), generator=rng(2)).to(torch.bfloat16).cuda()
         y = q.q4g_matmul(w, x)
         side = torch.cuda.Stream()
@@ -178,9 +180,9 @@ def test_matmul_empty_and_streams(q):
         assert torch.equal(y, z)
 
 
-@pytest.mark.parametrize("M", [2, 90])
+@pytest.mark.parametrize("M", [2, 400])
 def test_matmul_in_a_graph(q, M):
-    w = pack(q, make(1, 300, 256, 64, True, "f16", 4))
+    w = pack(q, make(1, 2000, 256, 64, True, "f16", 4))
     x = torch.randn((M, 256), generator=rng(2)).cuda()
     y = q.q4g_matmul(w, x)
     g = torch.cuda.CUDAGraph()
@@ -441,7 +443,7 @@ def test_refused_tensors(q):
         q.q4g_matmul(w, torch.zeros((2, 132), dtype=torch.float16, device="cuda")[:, 1:129])
     with pytest.raises(ValueError):
         q.q4g_matmul(w, x, out=torch.empty((2, 63), dtype=torch.float16, device="cuda"))
-    y = torch.zeros((90, 128), dtype=torch.bfloat16, device="cuda")
+    y = torch.zeros((20000, 128), dtype=torch.bfloat16, device="cuda")
     with pytest.raises(q.QmmError) as err:
         q.q4g_matmul(w, y, workspace=torch.empty(16, dtype=torch.uint8, device="cuda"))
     assert err.value.status == 5
