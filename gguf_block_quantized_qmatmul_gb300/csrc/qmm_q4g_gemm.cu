@@ -110,10 +110,10 @@ __global__ void __launch_bounds__(256) q4g_prep_kernel(const QgCall c, int rows,
     }
 }
 
-template <int NP, int NG, int CG>
+template <int PA, int PX, int NG, int CG>
 cudaError_t gemm_one(const QgGemmPlan& pl, const CUtensorMap& tx, const CUtensorMap& tw, const QgGemmParams& p, int smem_max, cudaStream_t s) {
     static unsigned long long done = 0;
-    auto* k = q4g_gemm_kernel<NP, NG, CG>;
+    auto* k = q4g_gemm_kernel<PA, PX, NG, CG>;
     const cudaError_t e = ensure_smem(k, smem_max, done);
     if (e != cudaSuccess) return e;
     cudaLaunchConfig_t cfg = {};
@@ -141,6 +141,9 @@ QgGemmPlan plan_q4g_gemm(const QgCall& c, int sms, int smem_max) {
     if (grouped && c.w.E > kQgMaxE) return pl;
     const long long rows = c.M;
     pl.np = c.xt == X_F32 ? 2 : 1;
+    // f16 gate and up products: their weights' roundings would meet in the product of the two, 1.6
+    // times the error of rounding the f16 output
+    pl.pa = pl.np == 2 || (c.op == P_GATE_UP && c.xt == X_F16) ? 2 : 1;
     pl.prep = grouped || c.xt != X_F16 || c.w.K % 64 != 0;  // K that does not fill its last 64 is padded there
     const long long per = grouped ? (c.M + c.w.E - 1) / c.w.E : c.M;  // activation rows per weight matrix
     pl.cg = pl.np == 1 ? 2 : 1;
@@ -150,7 +153,7 @@ QgGemmPlan plan_q4g_gemm(const QgCall& c, int sms, int smem_max) {
     // column, at least 40 each) or its conversion (900; two pieces 1400); a unit costs its
     // prologue and, where there is no second accumulator, the epilogue that the next unit's
     // MMAs wait for; slices of K cost their partial sums' traffic and a launch.
-    const int most = pl.np == 2 ? kQgBX2 : kQgBX1;  // two pieces: the epilogue's running sums are registers
+    const int most = pl.np == 2 ? kQgBX2 : pl.pa == 2 ? kQgBXA : kQgBX1;  // two pieces: the epilogue's running sums are registers
     pl.ks = 1;
     if (grouped) {
         // two accumulators: K is short, and a second one hides the epilogue (2048 tokens x 8 of 64,
@@ -161,7 +164,7 @@ QgGemmPlan plan_q4g_gemm(const QgCall& c, int sms, int smem_max) {
         for (int tiles = (int)((per + most - 1) / most); tiles <= 8 + (per + most - 1) / most; ++tiles) {
             const int bx = (int)((per + tiles - 1) / tiles + unit - 1) / unit * unit;
             const long long un = (long long)pl.ntiles * ((per + bx - 1) / bx);
-            const double mma = 8.0 * (2 * pl.np - 1) * (bx < 80 ? 40.0 : bx / 2.0), conv = pl.np == 2 ? 1400.0 : 900.0, tile = mma > conv ? mma : conv;
+            const double mma = 8.0 * (pl.pa + pl.np - 1) * (bx < 80 ? 40.0 : bx / 2.0), conv = pl.pa == 2 ? 1400.0 : 900.0, tile = mma > conv ? mma : conv;
             const double once = bx > 192 ? 1500.0 + 12.0 * bx : 1500.0;
             for (int ks = 1; ks <= c.w.KS && ks <= 16 && (ks == 1 || un * ks <= 2 * workers); ++ks) {
                 const double waves = (double)((un * ks + workers - 1) / workers);
@@ -180,7 +183,7 @@ QgGemmPlan plan_q4g_gemm(const QgCall& c, int sms, int smem_max) {
     pl.mtiles = grouped ? 0 : (int)((per + pl.bx - 1) / pl.bx);
     // converted weights in the tensor memory that the accumulators leave; activations and raw
     // weights share the shared memory
-    pl.nstage = (kTcTmemCols - pl.nacc * pl.accw) / (64 * pl.np);
+    pl.nstage = (kTcTmemCols - pl.nacc * pl.accw) / (64 * pl.pa);
     if (pl.nstage > kQgStageMax) pl.nstage = kQgStageMax;
     const int raw = 8 * qg_seg_bytes(c.w.ng), stage = pl.bx / pl.cg * 256 * pl.np;
     const int room = smem_max - (512 + 2 * kQgEpiWarps * kQgBX1 * 4 + (c.w.E + 1) * 4 + 1024);
@@ -256,13 +259,17 @@ cudaError_t launch_q4g_gemm(const QgGemmPlan& pl, const QgCall& c, void* ws, uns
     p.off_bar = p.off_raw + pl.nraw * 8 * qg_seg_bytes(c.w.ng);
     cudaError_t e;
     if (pl.np == 2)
-        e = c.w.ng == 1   ? gemm_one<2, 1, 1>(pl, tx, tw, p, smem_max, s)
-            : c.w.ng == 2 ? gemm_one<2, 2, 1>(pl, tx, tw, p, smem_max, s)
-                          : gemm_one<2, 4, 1>(pl, tx, tw, p, smem_max, s);
+        e = c.w.ng == 1   ? gemm_one<2, 2, 1, 1>(pl, tx, tw, p, smem_max, s)
+            : c.w.ng == 2 ? gemm_one<2, 2, 2, 1>(pl, tx, tw, p, smem_max, s)
+                          : gemm_one<2, 2, 4, 1>(pl, tx, tw, p, smem_max, s);
+    else if (pl.pa == 2)
+        e = c.w.ng == 1   ? gemm_one<2, 1, 1, 2>(pl, tx, tw, p, smem_max, s)
+            : c.w.ng == 2 ? gemm_one<2, 1, 2, 2>(pl, tx, tw, p, smem_max, s)
+                          : gemm_one<2, 1, 4, 2>(pl, tx, tw, p, smem_max, s);
     else
-        e = c.w.ng == 1   ? gemm_one<1, 1, 2>(pl, tx, tw, p, smem_max, s)
-            : c.w.ng == 2 ? gemm_one<1, 2, 2>(pl, tx, tw, p, smem_max, s)
-                          : gemm_one<1, 4, 2>(pl, tx, tw, p, smem_max, s);
+        e = c.w.ng == 1   ? gemm_one<1, 1, 1, 2>(pl, tx, tw, p, smem_max, s)
+            : c.w.ng == 2 ? gemm_one<1, 1, 2, 2>(pl, tx, tw, p, smem_max, s)
+                          : gemm_one<1, 1, 4, 2>(pl, tx, tw, p, smem_max, s);
     if (e == cudaSuccess && pl.ks > 1) return launch_q4g_sum(p.part, pl.ks, (long long)c.M * c.w.N, c.y, c.xt, s);
     if (e != cudaSuccess || c.op != P_DOWN) return e;
     return launch_q4g_combine(p.part, c.r, c.w.E, c.w.N, c.y, c.xt, s);

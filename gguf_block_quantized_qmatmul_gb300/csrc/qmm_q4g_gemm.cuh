@@ -58,9 +58,9 @@ constexpr int kQgEpiHalves = kQgEpiWarps / 4;   // epilogue warps per TMEM lane 
 constexpr int kQgGroups = kQgConvWarps / 8;     // converting groups: a warp per row block of a tile
 constexpr int kQgEpi0 = 3, kQgConv0 = kQgEpi0 + kQgEpiWarps;
 constexpr int kQgThreads = (kQgConv0 + kQgConvWarps) * 32;
-constexpr int kQgBX1 = 256, kQgBX2 = 64;  // activation rows per tile, at most: one piece, two pieces
+constexpr int kQgBX1 = 256, kQgBXA = 128, kQgBX2 = 64;  // activation rows per tile, at most: one piece, two of the weights, two of both
 constexpr int kQgRawMax = 6, kQgXMax = 8, kQgStageMax = 8;  // stages, at most: raw weights, activations, converted weights
-constexpr int kQgChunk = 2;      // tiles per accumulation chunk (two pieces)
+constexpr int kQgChunk = 1;      // tiles per accumulation chunk (two pieces of the activations)
 constexpr int kQgMaxE = 512;     // experts of a grouped call
 
 struct QgGemmParams {
@@ -205,7 +205,8 @@ struct QgUnit {
     int split, j0, j1; // K slice, its tiles (segments of 128 K)
 };
 
-template <int NP, int NG, int CG>
+// PA pieces of the weights, PX of the activations
+template <int PA, int PX, int NG, int CG>
 __global__ void __launch_bounds__(kQgThreads, 1) q4g_gemm_kernel(const __grid_constant__ CUtensorMap tx, const __grid_constant__ CUtensorMap tw, const QgGemmParams p) {
     extern __shared__ __align__(1024) uint8_t smraw[];
     uint8_t* sm = smraw + ((1024 - (smem_u32(smraw) & 1023)) & 1023);
@@ -326,7 +327,7 @@ __global__ void __launch_bounds__(kQgThreads, 1) q4g_gemm_kernel(const __grid_co
     if (!grouped && warp != 2) grid_dep_wait();  // weights are constant: their copies may start at once
     // an activation stage: two 64-K halves of the rows' pieces; of a pair, each block has half the rows
     const int half = p.bx / CG * 128;
-    auto stage = [&](int s) { return sm + s * 2 * NP * half; };
+    auto stage = [&](int s) { return sm + s * 2 * PX * half; };
     const int seg_bytes = qg_seg_bytes(NG);
     auto raw = [&](int s) { return sm + p.off_raw + s * 8 * seg_bytes; };
     // 64-K halves of tile j that hold any K
@@ -344,7 +345,7 @@ __global__ void __launch_bounds__(kQgThreads, 1) q4g_gemm_kernel(const __grid_co
                     if (!(ok = qg_wait(smem_u32(&x_empty[g.s]), g.ph ^ 1u, flags, p.err))) break;
                     uint32_t bar = smem_u32(&x_full[g.s]);
                     const uint32_t to = smem_u32(stage(g.s));
-                    if (rank == 0) mbar_arrive_tx(bar, (uint32_t)(CG * NP * 2 * half));
+                    if (rank == 0) mbar_arrive_tx(bar, (uint32_t)(CG * PX * 2 * half));
                     if (CG == 2) bar = leader_addr(bar);
                     tma_4d<CG>(to, &tx, 0, p0, 0, 2 * j, bar);
                     g.next(p.nx);
@@ -372,7 +373,7 @@ __global__ void __launch_bounds__(kQgThreads, 1) q4g_gemm_kernel(const __grid_co
             for (int u = first_unit; u < units && ok; u += unit_step) {
                 const QgUnit un = place(u);
                 const uint32_t idesc = tc_idesc((un.n + kUnit - 1) / kUnit * kUnit) + ((uint32_t)((CG - 1) * (kTcBW >> 4)) << 24);  // a pair: M = 256
-                const int chunk = NP == 2 ? kQgChunk : w.KS;
+                const int chunk = PX == 2 ? kQgChunk : w.KS;
                 for (int c0 = un.j0; c0 < un.j1 && ok; c0 += chunk, ++cc) {
                     const int ab = p.nacc == 2 ? (cc & 1) : 0, use = p.nacc == 2 ? (cc >> 1) : cc;
                     if (use > 0) ok = qg_wait(smem_u32(&acc_empty[ab]), (uint32_t)((use - 1) & 1), flags, p.err);
@@ -391,16 +392,19 @@ __global__ void __launch_bounds__(kQgThreads, 1) q4g_gemm_kernel(const __grid_co
                         gx.next(p.nx);
                         ready = next;
                         tc_fence_after();
-                        const uint32_t x0 = lo0 + (uint32_t)((sx * 2 * NP * half) >> 4), a0 = tmem + (uint32_t)(p.nacc * p.accw + 64 * NP * s);
+                        const uint32_t x0 = lo0 + (uint32_t)((sx * 2 * PX * half) >> 4), a0 = tmem + (uint32_t)(p.nacc * p.accw + 64 * PA * s);
                         const int nh = halves(c0 + i);
                         __syncwarp();
                         if (lead) {
+// The small products first, while the accumulator is small: adding to it truncates.
+                            constexpr int kPasses = PA + PX - 1;  // weights, activations: hi lo, lo hi, hi hi (one piece: hi)
 #pragma unroll
-                            for (int h = 0; h < 2; ++h) {
-                                if (h == 1 && nh == 1) break;
+                            for (int pass = 0; pass < kPasses; ++pass) {
+                                const bool wlo = PA == 2 && pass == kPasses - 2, xlo = PX == 2 && pass == 0;
 #pragma unroll
-                                for (int pass = 0; pass < 2 * NP - 1; ++pass) {  // hi hi, hi lo, lo hi
-                                    const uint32_t wa = a0 + 32 * h + (pass == 2 ? 64 : 0), xb = x0 + (uint32_t)((h * NP + (pass == 1)) * half >> 4);
+                                for (int h = 0; h < 2; ++h) {
+                                    if (h == 1 && nh == 1) break;
+                                    const uint32_t wa = a0 + 32 * h + (wlo ? 64 : 0), xb = x0 + (uint32_t)((h * PX + (xlo ? 1 : 0)) * half >> 4);
 #pragma unroll
                                     for (int kk = 0; kk < 4; ++kk)
                                         qg_mma_tc<CG>(dt, wa + 8 * kk, ((uint64_t)dhi << 32) | (xb + 2 * kk), idesc, (i | h | pass | kk) != 0 ? 1u : 0u);
@@ -445,7 +449,7 @@ __global__ void __launch_bounds__(kQgThreads, 1) q4g_gemm_kernel(const __grid_co
         float* my_scale = col_scale + ew * kQgBX1;
         int cc = 0;
         bool ok = true;
-        const int chunk = NP == 2 ? kQgChunk : w.KS;
+        const int chunk = PX == 2 ? kQgChunk : w.KS;
         const int F = w.N / 2;
         for (int u = first_unit; u < units && ok; u += unit_step) {
             const QgUnit un = place(u);
@@ -495,7 +499,7 @@ __global__ void __launch_bounds__(kQgThreads, 1) q4g_gemm_kernel(const __grid_co
                             const float lo8 = v[4 * j + i], hi8 = v[4 * j + i + 8];
                             const float got = __shfl_xor_sync(0xffffffffu, up ? lo8 : hi8, 8), mine = up ? hi8 : lo8;
                             const float gt = (up ? got : mine) * (wg * xc[i]), ut = (up ? mine : got) * (wu * xc[i]);
-                            const float r = NP == 2 ? swiglu(gt, ut) : swiglu_fast(gt, ut);
+                            const float r = PX == 2 ? swiglu(gt, ut) : swiglu_fast(gt, ut);
                             if (on && sl[i] >= 0) *reinterpret_cast<Y*>(base + (uint64_t)(uint32_t)sl[i] * row) = to_type<Y>(r);
                         }
                     }
@@ -523,19 +527,19 @@ __global__ void __launch_bounds__(kQgThreads, 1) q4g_gemm_kernel(const __grid_co
             };
             auto put = [&](int k, const float v[16]) {
                 if (c.op == P_DOWN || p.ks > 1) put_as(p.part + (long long)un.split * c.M * w.N, k, v);
-                else if (NP == 2) put_as(static_cast<float*>(c.y), k, v);
+                else if (PX == 2) put_as(static_cast<float*>(c.y), k, v);
                 else if (c.xt == X_F16) put_as(static_cast<__half*>(c.y), k, v);
                 else put_as(static_cast<__nv_bfloat16*>(c.y), k, v);
             };
             constexpr int kSums = kQgBX2 / 16 / kQgEpiHalves;
-            float sum[NP == 2 ? kSums : 1][16];
+            float sum[PX == 2 ? kSums : 1][16];
             for (int c0 = un.j0; c0 < un.j1; c0 += chunk, ++cc) {
                 const int ab = p.nacc == 2 ? (cc & 1) : 0, use = p.nacc == 2 ? (cc >> 1) : cc;
                 if (!(ok = qg_wait(smem_u32(&acc_full[ab]), (uint32_t)(use & 1), flags, p.err))) break;
                 tc_fence_after();
                 __syncwarp();
                 const uint32_t acol = tmem + tq + (uint32_t)(ab * p.accw);
-                if (NP == 2) {
+                if (PX == 2) {
 #pragma unroll
                     for (int k = 0; k < kSums; ++k) {
                         uint32_t r[16];
@@ -544,7 +548,7 @@ __global__ void __launch_bounds__(kQgThreads, 1) q4g_gemm_kernel(const __grid_co
                             tc_ld16(acol + 16 * ch, r);
                             tc_wait_ld();
 #pragma unroll
-                            for (int i = 0; i < 16; ++i) sum[NP == 2 ? k : 0][i] = c0 == un.j0 ? __uint_as_float(r[i]) : sum[NP == 2 ? k : 0][i] + __uint_as_float(r[i]);
+                            for (int i = 0; i < 16; ++i) sum[PX == 2 ? k : 0][i] = c0 == un.j0 ? __uint_as_float(r[i]) : sum[PX == 2 ? k : 0][i] + __uint_as_float(r[i]);
                         }
                     }
                 } else {
@@ -568,10 +572,10 @@ __global__ void __launch_bounds__(kQgThreads, 1) q4g_gemm_kernel(const __grid_co
                 }
             }
             if (!ok) break;
-            if (NP == 2) {
+            if (PX == 2) {
 #pragma unroll
                 for (int k = 0; k < kSums; ++k)
-                    if (half + kQgEpiHalves * k < nch) put(half + kQgEpiHalves * k, sum[NP == 2 ? k : 0]);
+                    if (half + kQgEpiHalves * k < nch) put(half + kQgEpiHalves * k, sum[PX == 2 ? k : 0]);
             }
         }
     } else {
@@ -611,13 +615,13 @@ __global__ void __launch_bounds__(kQgThreads, 1) q4g_gemm_kernel(const __grid_co
                 // tested here, needed after the conversion
                 const uint32_t e_ready = mbar_test(smem_u32(&empty[at.s]), at.ph ^ 1u);
                 const uint8_t* seg = raw(ar.s) + (2 * q + hh) * seg_bytes;
-                const uint32_t col = tmem + ((uint32_t)(32 * q + 16 * hh) << 16) + (uint32_t)(p.nacc * p.accw + 64 * NP * at.s);
+                const uint32_t col = tmem + ((uint32_t)(32 * q + 16 * hh) << 16) + (uint32_t)(p.nacc * p.accw + 64 * PA * at.s);
                 // what needs no free stage comes before the wait for one, and before the last
                 // tile's stores are waited for
                 uint32_t hi[32], lo[16];
-                qg_convert<NP, NG>(seg, 0, lane, magic, m0, m1, hi, lo);
-                if (NP == 1) {
-                    qg_convert<NP, NG>(seg, 1, lane, magic, m0, m1, hi + 16, lo);
+                qg_convert<PA, NG>(seg, 0, lane, magic, m0, m1, hi, lo);
+                if (PA == 1) {
+                    qg_convert<PA, NG>(seg, 1, lane, magic, m0, m1, hi + 16, lo);
                     __syncwarp();
                     if (lane == 0) mbar_arrive(smem_u32(&r_empty[ar.s]));
                 }
@@ -628,12 +632,12 @@ __global__ void __launch_bounds__(kQgThreads, 1) q4g_gemm_kernel(const __grid_co
                 r_ready = mbar_test(smem_u32(&r_full[rn.s]), rn.ph);
                 tc_fence_after();
                 __syncwarp();
-                if (NP == 1) {
+                if (PA == 1) {
                     tc_st_frag64(col, hi);
                 } else {
                     tc_st_frag(col, hi);
                     tc_st_frag(col + 64, lo);
-                    qg_convert<NP, NG>(seg, 1, lane, magic, m0, m1, hi, lo);
+                    qg_convert<PA, NG>(seg, 1, lane, magic, m0, m1, hi, lo);
                     __syncwarp();
                     if (lane == 0) mbar_arrive(smem_u32(&r_empty[ar.s]));
                     tc_st_frag(col + 32, hi);

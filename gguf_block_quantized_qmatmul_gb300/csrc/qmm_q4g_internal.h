@@ -59,7 +59,7 @@ cudaError_t launch_q4g_rows(const QgRowsPlan& pl, const QgCall& c, void* ws, int
 // The tcgen05 GEMM.
 struct QgGemmPlan {
     bool ok = false;
-    int np = 0;            // pieces per operand: 1, or 2 (f32 activations: hi and lo)
+    int np = 0, pa = 0;    // pieces (hi, or hi and lo) of the activations: 2 for f32; of the weights
     int cg = 0, bx = 0, nacc = 0, accw = 0, mtiles = 0, ntiles = 0, nraw = 0, nx = 0, nstage = 0, grid = 0, ks = 0;
     int prep = 0;          // activations go through the preparation launch (f32, bf16)
     size_t smem = 0, ws_x = 0, ws_xs = 0, ws_part = 0, workspace = 0;
