@@ -531,6 +531,15 @@ __global__ void __launch_bounds__(kQgThreads, 1) q4g_gemm_kernel(const __grid_co
                 else if (c.xt == X_F16) put_as(static_cast<__half*>(c.y), k, v);
                 else put_as(static_cast<__nv_bfloat16*>(c.y), k, v);
             };
+            auto release = [&](int ab) {
+                __syncwarp();
+                tc_fence_before();
+                __syncwarp();
+                if (lane == 0) {
+                    if (CG == 2) mbar_arrive_cluster(leader_addr(smem_u32(&acc_empty[ab])));
+                    else mbar_arrive(smem_u32(&acc_empty[ab]));
+                }
+            };
             constexpr int kSums = kQgBX2 / 16 / kQgEpiHalves;
             float sum[PX == 2 ? kSums : 1][16];
             for (int c0 = un.j0; c0 < un.j1; c0 += chunk, ++cc) {
@@ -540,17 +549,23 @@ __global__ void __launch_bounds__(kQgThreads, 1) q4g_gemm_kernel(const __grid_co
                 __syncwarp();
                 const uint32_t acol = tmem + tq + (uint32_t)(ab * p.accw);
                 if (PX == 2) {
+                    // all of the chunk to registers, the accumulator given back, then the sums
+                    uint32_t r[kSums][16] = {};
 #pragma unroll
-                    for (int k = 0; k < kSums; ++k) {
-                        uint32_t r[16];
-                        const int ch = half + kQgEpiHalves * k;
-                        if (ch < nch) {
-                            tc_ld16(acol + 16 * ch, r);
-                            tc_wait_ld();
+                    for (int k = 0; k < kSums; ++k)
+                        if (half + kQgEpiHalves * k < nch) tc_ld16(acol + 16 * (half + kQgEpiHalves * k), r[k]);
+                    tc_wait_ld();
 #pragma unroll
-                            for (int i = 0; i < 16; ++i) sum[PX == 2 ? k : 0][i] = c0 == un.j0 ? __uint_as_float(r[i]) : sum[PX == 2 ? k : 0][i] + __uint_as_float(r[i]);
-                        }
-                    }
+                    for (int k = 0; k < kSums; ++k)
+#pragma unroll
+                        for (int i = 0; i < 16; ++i) asm volatile("" : "+r"(r[k][i]));  // not used before the wait
+                    release(ab);
+#pragma unroll
+                    for (int k = 0; k < kSums; ++k)
+                        if (half + kQgEpiHalves * k < nch)
+#pragma unroll
+                            for (int i = 0; i < 16; ++i)
+                                sum[PX == 2 ? k : 0][i] = c0 == un.j0 ? __uint_as_float(r[k][i]) : sum[PX == 2 ? k : 0][i] + __uint_as_float(r[k][i]);
                 } else {
                     uint32_t r[16];
                     if (half < nch) tc_ld16(acol + 16 * half, r);
@@ -562,13 +577,7 @@ __global__ void __launch_bounds__(kQgThreads, 1) q4g_gemm_kernel(const __grid_co
                         if (k + kQgEpiHalves < nch) tc_ld16(acol + 16 * (k + kQgEpiHalves), r);
                         put(k, v);
                     }
-                }
-                __syncwarp();
-                tc_fence_before();
-                __syncwarp();
-                if (lane == 0) {
-                    if (CG == 2) mbar_arrive_cluster(leader_addr(smem_u32(&acc_empty[ab])));
-                    else mbar_arrive(smem_u32(&acc_empty[ab]));
+                    release(ab);
                 }
             }
             if (!ok) break;
