@@ -62,6 +62,7 @@ constexpr int kQgBX1 = 256, kQgBXA = 128, kQgBX2 = 64;  // activation rows per t
 constexpr int kQgRawMax = 6, kQgXMax = 8, kQgStageMax = 8;  // stages, at most: raw weights, activations, converted weights
 constexpr int kQgChunk = 1;      // tiles per accumulation chunk (two pieces of the activations)
 constexpr int kQgMaxE = 512;     // experts of a grouped call
+constexpr int kQgTab = 64;       // units of a block that are looked up at its start; later ones when they are taken
 
 struct QgGemmParams {
     QgCall c;
@@ -228,7 +229,9 @@ __global__ void __launch_bounds__(kQgThreads, 1) q4g_gemm_kernel(const __grid_co
     volatile int* flags = reinterpret_cast<volatile int*>(sm + p.off_bar + 480);
     int* col_slot = reinterpret_cast<int*>(sm + p.off_bar + 512);             // [warps][kQgBX1]
     float* col_scale = reinterpret_cast<float*>(col_slot + kQgEpiWarps * kQgBX1);  // [warps][kQgBX1]
-    int* ts = reinterpret_cast<int*>(col_scale + kQgEpiWarps * kQgBX1);       // [E + 1] activation tiles before each expert
+    int4* tab = reinterpret_cast<int4*>(col_scale + kQgEpiWarps * kQgBX1);    // [kQgTab] this block's units: expert and slice, p0, n, nt
+    int* ts = reinterpret_cast<int*>(tab + kQgTab);                           // [E + 1] activation tiles before each expert
+    int* po = ts + w.E + 1;                                                   // [E + 1] activation rows before each expert
     const uint32_t rank = CG == 2 ? cluster_rank() : 0u;
     constexpr int kUnit = 16 * CG;  // the MMA's N is a multiple of 16, a pair's of 32
     const int first_unit = blockIdx.x / CG, unit_step = gridDim.x / CG;
@@ -269,11 +272,13 @@ __global__ void __launch_bounds__(kQgThreads, 1) q4g_gemm_kernel(const __grid_co
     if (grouped) grid_dep_wait();
     if (warp == 0) {
         if (grouped) {
+            for (int e = lane; e <= w.E; e += 32) po[e] = min(max(__ldg(c.r.offsets + e), 0), slots);
+            __syncwarp();
             const int per = (w.E + 31) / 32;
             int mine = 0;
             for (int i = 0; i < per; ++i) {
                 const int e = lane * per + i;
-                if (e < w.E) mine += (max(min(c.r.offsets[e + 1], slots) - max(c.r.offsets[e], 0), 0) + p.bx - 1) / p.bx;
+                if (e < w.E) mine += (max(po[e + 1] - po[e], 0) + p.bx - 1) / p.bx;
             }
             int pre = mine;
 #pragma unroll
@@ -287,11 +292,13 @@ __global__ void __launch_bounds__(kQgThreads, 1) q4g_gemm_kernel(const __grid_co
                 const int e = lane * per + i;
                 if (e >= w.E) break;
                 ts[e] = pre;
-                pre += (max(min(c.r.offsets[e + 1], slots) - max(c.r.offsets[e], 0), 0) + p.bx - 1) / p.bx;
+                pre += (max(po[e + 1] - po[e], 0) + p.bx - 1) / p.bx;
             }
         } else if (lane == 0) {
             ts[0] = 0;
             ts[1] = p.mtiles;
+            po[0] = 0;
+            po[1] = c.M;
         }
     }
     tc_fence_before();
@@ -300,12 +307,10 @@ __global__ void __launch_bounds__(kQgThreads, 1) q4g_gemm_kernel(const __grid_co
     tc_fence_after();
     const uint32_t tmem = *tslot;
     const int tiles_all = ts[w.E] * p.ntiles, units = tiles_all * p.ks;
-    auto place = [&](int u) {
+    auto find = [&](int u) {
         QgUnit un;
         un.split = u / tiles_all;
         u -= un.split * tiles_all;
-        un.j0 = (int)((long long)un.split * w.KS / p.ks);
-        un.j1 = (int)((long long)(un.split + 1) * w.KS / p.ks);
         const int st = u / p.ntiles;
         un.nt = (u - st * p.ntiles) * CG + (int)rank;
         int lo = 0, hi = w.E;  // ts[lo] <= st < ts[hi]
@@ -315,13 +320,39 @@ __global__ void __launch_bounds__(kQgThreads, 1) q4g_gemm_kernel(const __grid_co
             else hi = mid;
         }
         un.e = lo;
-        const int first = grouped ? max(c.r.offsets[lo], 0) : 0;
-        const int end = grouped ? min(c.r.offsets[lo + 1], slots) : c.M;
+        const int first = po[lo], end = po[lo + 1];
         // an expert's rows in tiles of one size, not full ones and a rest
         const int tiles = ts[lo + 1] - ts[lo];
         const int size = ((end - first + tiles - 1) / tiles + kUnit - 1) & ~(kUnit - 1);
         un.p0 = first + (st - ts[lo]) * size;
         un.n = min(size, end - un.p0);
+        return un;
+    };
+    // Looked up once, not by each of the warps that take the unit: that was a tenth of all instructions
+    // and 1500 cycles at each unit's start.
+    for (int i = tid; i < kQgTab && first_unit + i * unit_step < units; i += kQgThreads) {
+        const QgUnit un = find(first_unit + i * unit_step);
+        tab[i] = make_int4(un.e | un.split << 16, un.p0, un.n, un.nt);
+    }
+    __syncthreads();
+    auto place = [&](int u, int i) {  // u: the block's unit i
+        QgUnit un;
+        if (i < kQgTab) {
+            const int4 v = tab[i];
+            un.e = v.x & 0xffff;
+            un.split = v.x >> 16;
+            un.p0 = v.y;
+            un.n = v.z;
+            un.nt = v.w;
+        } else {
+            un = find(u);
+        }
+        un.j0 = 0;
+        un.j1 = w.KS;
+        if (p.ks > 1) {
+            un.j0 = un.split * w.KS / p.ks;
+            un.j1 = (un.split + 1) * w.KS / p.ks;
+        }
         return un;
     };
     if (!grouped && warp != 2) grid_dep_wait();  // weights are constant: their copies may start at once
@@ -338,8 +369,8 @@ __global__ void __launch_bounds__(kQgThreads, 1) q4g_gemm_kernel(const __grid_co
         if (lane == 0) {
             QgRing g;
             bool ok = true, wrapped = false;
-            for (int u = first_unit; u < units && ok; u += unit_step) {
-                const QgUnit un = place(u);
+            for (int u = first_unit, ui = 0; u < units && ok; u += unit_step, ++ui) {
+                const QgUnit un = place(u, ui);
                 const int p0 = un.p0 + (int)rank * ((un.n + kUnit - 1) / kUnit * kUnit / CG);
                 for (int j = un.j0; j < un.j1; ++j) {
                     if (!(ok = qg_wait(smem_u32(&x_empty[g.s]), g.ph ^ 1u, flags, p.err))) break;
@@ -370,8 +401,8 @@ __global__ void __launch_bounds__(kQgThreads, 1) q4g_gemm_kernel(const __grid_co
             uint32_t last_ph = 0;
             bool ok = true;
             uint32_t ready = 0;  // the next stage's barrier, tested before this tile's MMAs are issued
-            for (int u = first_unit; u < units && ok; u += unit_step) {
-                const QgUnit un = place(u);
+            for (int u = first_unit, ui = 0; u < units && ok; u += unit_step, ++ui) {
+                const QgUnit un = place(u, ui);
                 const uint32_t idesc = tc_idesc((un.n + kUnit - 1) / kUnit * kUnit) + ((uint32_t)((CG - 1) * (kTcBW >> 4)) << 24);  // a pair: M = 256
                 const int chunk = PX == 2 ? kQgChunk : w.KS;
                 for (int c0 = un.j0; c0 < un.j1 && ok; c0 += chunk, ++cc) {
@@ -428,8 +459,8 @@ __global__ void __launch_bounds__(kQgThreads, 1) q4g_gemm_kernel(const __grid_co
         if (lane == 0) {
             QgRing r;
             bool ok = true, wrapped = false;
-            for (int u = first_unit; u < units && ok; u += unit_step) {
-                const QgUnit un = place(u);
+            for (int u = first_unit, ui = 0; u < units && ok; u += unit_step, ++ui) {
+                const QgUnit un = place(u, ui);
                 for (int j = un.j0; j < un.j1; ++j) {
                     if (!(ok = qg_wait(smem_u32(&r_empty[r.s]), r.ph ^ 1u, flags, p.err))) break;
                     const uint32_t bar = smem_u32(&r_full[r.s]);
@@ -451,8 +482,8 @@ __global__ void __launch_bounds__(kQgThreads, 1) q4g_gemm_kernel(const __grid_co
         bool ok = true;
         const int chunk = PX == 2 ? kQgChunk : w.KS;
         const int F = w.N / 2;
-        for (int u = first_unit; u < units && ok; u += unit_step) {
-            const QgUnit un = place(u);
+        for (int u = first_unit, ui = 0; u < units && ok; u += unit_step, ++ui) {
+            const QgUnit un = place(u, ui);
             const int nch = (un.n + 15) / 16;
             const int rb = 8 * un.nt + 2 * q + (lane >> 4);
             const int n = rb < w.RB ? qg_row(w, rb, lane & 15) : -1;
@@ -607,11 +638,25 @@ __global__ void __launch_bounds__(kQgThreads, 1) q4g_gemm_kernel(const __grid_co
         };
         const uint32_t magic = opaque(0x64006400u);
         bool ok = true;
-        for (int u = first_unit; u < units && ok; u += unit_step) {
-            const QgUnit un = place(u);
-            const int rb = min(8 * un.nt + 2 * q + hh, w.RB - 1);
-            const float* is = p.wis + ((long long)un.e * w.RB + rb) * 16 + (lane >> 2);
-            const float m0 = __frcp_rn(__ldg(is)), m1 = __frcp_rn(__ldg(is + 8));  // 2^a of rows g, g + 8
+        // 2^-a of rows g, g + 8, asked for a unit ahead
+        float is0 = 1.0f, is1 = 1.0f;
+        auto ask = [&](const QgUnit& un) {
+            const float* is = p.wis + ((long long)un.e * w.RB + min(8 * un.nt + 2 * q + hh, w.RB - 1)) * 16 + (lane >> 2);
+            is0 = __ldg(is);
+            is1 = __ldg(is + 8);
+        };
+        QgUnit un = {}, un_next = {};
+        if (first_unit < units) {
+            un_next = place(first_unit, 0);
+            ask(un_next);
+        }
+        for (int u = first_unit, ui = 0; u < units && ok; u += unit_step, ++ui) {
+            un = un_next;
+            const float m0 = __frcp_rn(is0), m1 = __frcp_rn(is1);
+            if (u + unit_step < units) {
+                un_next = place(u + unit_step, ui + 1);
+                ask(un_next);
+            }
             // The groups take tiles in turn, whatever a unit's number of them: a group that waits for
             // the release of tile t - nstage has waited for t - groups - nstage, so that with nstage >=
             // groups the stage's barrier is at most one phase behind the wait's parity.
