@@ -186,7 +186,7 @@ QgGemmPlan plan_q4g_gemm(const QgCall& c, int sms, int smem_max) {
     pl.nstage = (kTcTmemCols - pl.nacc * pl.accw) / (64 * pl.pa);
     if (pl.nstage > kQgStageMax) pl.nstage = kQgStageMax;
     const int raw = 8 * qg_seg_bytes(c.w.ng), stage = pl.bx / pl.cg * 256 * pl.np;
-    const int room = smem_max - (512 + 2 * kQgEpiWarps * kQgBX1 * 4 + (c.w.E + 1) * 8 + kQgTab * 16 + 1024);
+    const int room = smem_max - (512 + 4 * kQgBX1 * 4 + (c.w.E + 1) * 8 + kQgTab * 16 + 1024);
     // Both rings are multiples of the converting groups, so that whoever waits for a stage's next
     // filling has waited for its last one (copies may land out of order).
     pl.nx = (room - 4 * raw) / stage / kQgGroups * kQgGroups;

@@ -61,6 +61,7 @@ constexpr int kQgThreads = (kQgConv0 + kQgConvWarps) * 32;
 constexpr int kQgBX1 = 256, kQgBXA = 128, kQgBX2 = 64;  // activation rows per tile, at most: one piece, two of the weights, two of both
 constexpr int kQgRawMax = 6, kQgXMax = 8, kQgStageMax = 8;  // stages, at most: raw weights, activations, converted weights
 constexpr int kQgChunk = 1;      // tiles per accumulation chunk (two pieces of the activations)
+constexpr int kCols = 8;         // accumulator columns that an epilogue warp takes at a time (with 16, 170 bytes a thread were spilled)
 constexpr int kQgMaxE = 512;     // experts of a grouped call
 constexpr int kQgTab = 64;       // units of a block that are looked up at its start; later ones when they are taken
 
@@ -83,18 +84,6 @@ __device__ __forceinline__ void tc_st_frag(uint32_t taddr, const uint32_t v[16])
         "r"(v[10]), "r"(v[11]), "r"(v[12]), "r"(v[13]), "r"(v[14]), "r"(v[15])
         : "memory");
 }
-// the same, 64 columns
-__device__ __forceinline__ void tc_st_frag64(uint32_t taddr, const uint32_t v[32]) {
-    asm volatile(
-        "tcgen05.st.sync.aligned.16x128b.x16.b32 [%0], {%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,%15,%16,"
-        "%17,%18,%19,%20,%21,%22,%23,%24,%25,%26,%27,%28,%29,%30,%31,%32};" ::"r"(taddr),
-        "r"(v[0]), "r"(v[1]), "r"(v[2]), "r"(v[3]), "r"(v[4]), "r"(v[5]), "r"(v[6]), "r"(v[7]), "r"(v[8]), "r"(v[9]),
-        "r"(v[10]), "r"(v[11]), "r"(v[12]), "r"(v[13]), "r"(v[14]), "r"(v[15]), "r"(v[16]), "r"(v[17]), "r"(v[18]), "r"(v[19]),
-        "r"(v[20]), "r"(v[21]), "r"(v[22]), "r"(v[23]), "r"(v[24]), "r"(v[25]), "r"(v[26]), "r"(v[27]), "r"(v[28]), "r"(v[29]),
-        "r"(v[30]), "r"(v[31])
-        : "memory");
-}
-
 // Pairs of blocks (cta_group::2): a cluster of two, whose rank 0 issues the MMAs of both.
 __device__ __forceinline__ uint32_t cluster_rank() {
     uint32_t r;
@@ -151,6 +140,12 @@ __device__ __forceinline__ void qg_commit(uint32_t bar) {
         asm volatile("tcgen05.commit.cta_group::2.mbarrier::arrive::one.shared::cluster.multicast::cluster.b64 [%0], %1;" ::"r"(bar),
                      "h"((uint16_t)3)
                      : "memory");
+}
+
+__device__ __forceinline__ void tc_ld8(uint32_t taddr, uint32_t r[8]) {
+    asm volatile("tcgen05.ld.sync.aligned.32x32b.x8.b32 {%0,%1,%2,%3,%4,%5,%6,%7}, [%8];"
+                 : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]), "=r"(r[4]), "=r"(r[5]), "=r"(r[6]), "=r"(r[7])
+                 : "r"(taddr));
 }
 
 // true in one lane of a converged warp
@@ -224,12 +219,13 @@ __global__ void __launch_bounds__(kQgThreads, 1) q4g_gemm_kernel(const __grid_co
     uint64_t* acc_full = r_empty + kQgRawMax;      // accumulator complete (commit)
     uint64_t* acc_empty = acc_full + 2;            // accumulator read
     static_assert(kQgXMax % kQgGroups == 0 && kQgRawMax % kQgGroups == 0, "rings of whole turns");
-    static_assert((2 * kQgXMax + 2 * kQgStageMax + 2 * kQgRawMax + 4) * 8 <= 448, "mbarriers overlap the TMEM slot");
+    uint64_t* tab_full = acc_empty + 2;            // a unit's column tables, of the epilogue
+    static_assert((2 * kQgXMax + 2 * kQgStageMax + 2 * kQgRawMax + 6) * 8 <= 448, "mbarriers overlap the TMEM slot");
     uint32_t* tslot = reinterpret_cast<uint32_t*>(sm + p.off_bar + 448);
     volatile int* flags = reinterpret_cast<volatile int*>(sm + p.off_bar + 480);
-    int* col_slot = reinterpret_cast<int*>(sm + p.off_bar + 512);             // [warps][kQgBX1]
-    float* col_scale = reinterpret_cast<float*>(col_slot + kQgEpiWarps * kQgBX1);  // [warps][kQgBX1]
-    int4* tab = reinterpret_cast<int4*>(col_scale + kQgEpiWarps * kQgBX1);    // [kQgTab] this block's units: expert and slice, p0, n, nt
+    int* col_slot = reinterpret_cast<int*>(sm + p.off_bar + 512);             // [2][kQgBX1]
+    float* col_scale = reinterpret_cast<float*>(col_slot + 2 * kQgBX1);       // [2][kQgBX1]
+    int4* tab = reinterpret_cast<int4*>(col_scale + 2 * kQgBX1);                 // [kQgTab] this block's units: expert and slice, p0, n, nt
     int* ts = reinterpret_cast<int*>(tab + kQgTab);                           // [E + 1] activation tiles before each expert
     int* po = ts + w.E + 1;                                                   // [E + 1] activation rows before each expert
     const uint32_t rank = CG == 2 ? cluster_rank() : 0u;
@@ -253,6 +249,7 @@ __global__ void __launch_bounds__(kQgThreads, 1) q4g_gemm_kernel(const __grid_co
         for (int i = 0; i < 2; ++i) {
             mbar_init(smem_u32(&acc_full[i]), 1);
             mbar_init(smem_u32(&acc_empty[i]), kQgEpiWarps * CG);
+            mbar_init(smem_u32(&tab_full[i]), kQgEpiWarps);
         }
         flags[0] = 0;
         fence_mbar_init();
@@ -476,89 +473,98 @@ __global__ void __launch_bounds__(kQgThreads, 1) q4g_gemm_kernel(const __grid_co
         // ------------------------------ epilogue ------------------------------
         const int ew = warp - kQgEpi0, q = warp & 3, half = ew >> 2;  // column chunks half, half + kQgEpiHalves, ...
         const uint32_t tq = (uint32_t)(32 * q) << 16;
-        int* my_slot = col_slot + ew * kQgBX1;
-        float* my_scale = col_scale + ew * kQgBX1;
         int cc = 0;
         bool ok = true;
         const int chunk = PX == 2 ? kQgChunk : w.KS;
         const int F = w.N / 2;
+        // A unit's column tables (slot or row, factor): a thread a column, copied a unit ahead (loaded
+        // at the unit's start they took 4000 cycles of some 17000).  And the factor of this lane's row.
+        static_assert(kQgEpiWarps * 32 >= kQgBX1, "a thread per column");
+        float wsn_next = 0.0f;
+        auto ask = [&](const QgUnit& un, int b) {
+            const int col = ew * 32 + lane;
+            int* ds = col_slot + b * kQgBX1 + col;
+            float* dc = col_scale + b * kQgBX1 + col;
+            const bool on = col < un.n;
+            if (on && grouped) cp_async4(smem_u32(ds), c.r.order + un.p0 + col);
+            else *ds = on ? un.p0 + col : -1;
+            if (on && p.xs) cp_async4(smem_u32(dc), p.xs + un.p0 + col);
+            else *dc = 1.0f;
+            cp_async_commit();
+            const int rb = 8 * un.nt + 2 * q + (lane >> 4);
+            wsn_next = rb < w.RB ? __ldg(p.wis + ((long long)un.e * w.RB + rb) * 16 + (lane & 15)) : 0.0f;
+        };
+        QgUnit un_next = {};
+        if (first_unit < units) {
+            un_next = place(first_unit, 0);
+            ask(un_next, 0);
+        }
         for (int u = first_unit, ui = 0; u < units && ok; u += unit_step, ++ui) {
-            const QgUnit un = place(u, ui);
-            const int nch = (un.n + 15) / 16;
+            const QgUnit un = un_next;
+            const float wsn = wsn_next;
+            const int nch = (un.n + kCols - 1) / kCols;
             const int rb = 8 * un.nt + 2 * q + (lane >> 4);
             const int n = rb < w.RB ? qg_row(w, rb, lane & 15) : -1;
-            const float wsn = rb < w.RB ? __ldg(p.wis + ((long long)un.e * w.RB + rb) * 16 + (lane & 15)) : 0.0f;
+            const int* my_slot = col_slot + (ui & 1) * kQgBX1;
+            const float* my_scale = col_scale + (ui & 1) * kQgBX1;
+            // This warp's part of the tables has landed, and it no longer reads the last unit's; once all
+            // have, the next unit's may be asked for.
+            cp_async_wait<0>();
             __syncwarp();
-            bool valid = true;
-            for (int col = lane; col < 16 * nch; col += 32) {
-                int slot = -1;
-                float xsc = 0.0f;
-                if (col < un.n) {
-                    slot = un.p0 + col;
-                    if (grouped) {
-                        slot = c.r.order[slot];
-                        if (slot < 0 || slot >= slots) slot = -1;
-                        valid &= slot >= 0;
-                    }
-                    xsc = p.xs ? __ldcg(p.xs + un.p0 + col) : 1.0f;
-                }
-                my_slot[col] = slot;
-                my_scale[col] = xsc;
+            if (lane == 0) mbar_arrive(smem_u32(&tab_full[ui & 1]));
+            if (!(ok = qg_wait(smem_u32(&tab_full[ui & 1]), (uint32_t)(ui >> 1) & 1u, flags, p.err))) break;
+            __syncwarp();
+            if (u + unit_step < units) {
+                un_next = place(u + unit_step, ui + 1);
+                ask(un_next, (ui + 1) & 1);
             }
-            const bool whole = __all_sync(0xffffffffu, valid);  // every column has a row to go to
             const float wup = __shfl_xor_sync(0xffffffffu, wsn, 8);  // the paired row's factor
             const bool up = (lane & 8) != 0;  // of a pair of rows: lanes r < 8 have gate rows, r + 8 their up rows
             const float wg = up ? wup : wsn, wu = up ? wsn : wup;
-            auto put_as = [&](auto* y, int k, const float v[16]) {  // columns 16 k..
+            auto put_as = [&](auto* y, int k, const float v[kCols]) {  // columns kCols k..
                 using Y = typename std::remove_pointer<decltype(y)>::type;
                 if (c.op == P_GATE_UP) {
-                    // the lane with the gate row finishes columns 0..7, the one with the up row 8..15
+                    // the lane with the gate row finishes columns 0..3, the one with the up row 4..7
                     const int f = rb * 8 + (lane & 7);
                     const bool on = rb < w.RB && f < F;
                     const uint32_t row = (uint32_t)F * (uint32_t)sizeof(Y);
                     char* base = reinterpret_cast<char*>(y + f);
-                    const int4* ps = reinterpret_cast<const int4*>(my_slot + 16 * k + (up ? 8 : 0));
-                    const float4* pc = reinterpret_cast<const float4*>(my_scale + 16 * k + (up ? 8 : 0));
+                    const int4 s4 = *reinterpret_cast<const int4*>(my_slot + kCols * k + (up ? 4 : 0));
+                    const float4 x4 = *reinterpret_cast<const float4*>(my_scale + kCols * k + (up ? 4 : 0));
+                    const int sl[4] = {s4.x, s4.y, s4.z, s4.w};
+                    const float xc[4] = {x4.x, x4.y, x4.z, x4.w};
 #pragma unroll
-                    for (int j = 0; j < 2; ++j) {
-                        const int4 s4 = ps[j];
-                        const float4 x4 = pc[j];
-                        const int sl[4] = {s4.x, s4.y, s4.z, s4.w};
-                        const float xc[4] = {x4.x, x4.y, x4.z, x4.w};
-#pragma unroll
-                        for (int i = 0; i < 4; ++i) {
-                            const float lo8 = v[4 * j + i], hi8 = v[4 * j + i + 8];
-                            const float got = __shfl_xor_sync(0xffffffffu, up ? lo8 : hi8, 8), mine = up ? hi8 : lo8;
-                            const float gt = (up ? got : mine) * (wg * xc[i]), ut = (up ? mine : got) * (wu * xc[i]);
-                            const float r = PX == 2 ? swiglu(gt, ut) : swiglu_fast(gt, ut);
-                            if (on && sl[i] >= 0) *reinterpret_cast<Y*>(base + (uint64_t)(uint32_t)sl[i] * row) = to_type<Y>(r);
-                        }
+                    for (int i = 0; i < 4; ++i) {
+                        const float got = __shfl_xor_sync(0xffffffffu, up ? v[i] : v[i + 4], 8), mine = up ? v[i + 4] : v[i];
+                        const float gt = (up ? got : mine) * (wg * xc[i]), ut = (up ? mine : got) * (wu * xc[i]);
+                        const float r = PX == 2 ? swiglu(gt, ut) : swiglu_fast(gt, ut);
+                        if (on && (unsigned)sl[i] < (unsigned)slots) *reinterpret_cast<Y*>(base + (uint64_t)(uint32_t)sl[i] * row) = to_type<Y>(r);
                     }
                 } else if (n >= 0) {
                     const uint32_t row = (uint32_t)w.N * (uint32_t)sizeof(Y);
                     char* base = reinterpret_cast<char*>(y + n);
-                    const int4* ps = reinterpret_cast<const int4*>(my_slot + 16 * k);
-                    const float4* pc = reinterpret_cast<const float4*>(my_scale + 16 * k);
+                    const int4* ps = reinterpret_cast<const int4*>(my_slot + kCols * k);
+                    const float4* pc = reinterpret_cast<const float4*>(my_scale + kCols * k);
                     auto all = [&](auto guard) {
 #pragma unroll
-                        for (int j = 0; j < 4; ++j) {
+                        for (int j = 0; j < kCols / 4; ++j) {
                             const int4 s4 = ps[j];
                             const float4 x4 = pc[j];
                             const int sl[4] = {s4.x, s4.y, s4.z, s4.w};
                             const float xc[4] = {x4.x, x4.y, x4.z, x4.w};
 #pragma unroll
                             for (int i = 0; i < 4; ++i)
-                                if (!decltype(guard)::value || sl[i] >= 0)
+                                if (!decltype(guard)::value || (unsigned)sl[i] < (unsigned)slots)
                                     *reinterpret_cast<Y*>(base + (uint64_t)(uint32_t)sl[i] * row) = to_type<Y>(v[4 * j + i] * (wsn * xc[i]));
                         }
                     };
-                    if (whole && 16 * k + 16 <= un.n) all(std::false_type());
+                    if (!grouped && kCols * k + kCols <= un.n) all(std::false_type());
                     else all(std::true_type());
                 }
             };
-            auto put = [&](int k, const float v[16]) {
-                if (c.op == P_DOWN || p.ks > 1) put_as(p.part + (long long)un.split * c.M * w.N, k, v);
-                else if (PX == 2) put_as(static_cast<float*>(c.y), k, v);
+            auto put = [&](int k, const float v[kCols]) {
+                if (PX == 2) put_as(c.op == P_DOWN || p.ks > 1 ? p.part + (long long)un.split * c.M * w.N : static_cast<float*>(c.y), k, v);
+                else if (c.op == P_DOWN || p.ks > 1) put_as(p.part + (long long)un.split * c.M * w.N, k, v);
                 else if (c.xt == X_F16) put_as(static_cast<__half*>(c.y), k, v);
                 else put_as(static_cast<__nv_bfloat16*>(c.y), k, v);
             };
@@ -571,8 +577,8 @@ __global__ void __launch_bounds__(kQgThreads, 1) q4g_gemm_kernel(const __grid_co
                     else mbar_arrive(smem_u32(&acc_empty[ab]));
                 }
             };
-            constexpr int kSums = kQgBX2 / 16 / kQgEpiHalves;
-            float sum[PX == 2 ? kSums : 1][16];
+            constexpr int kSums = PX == 2 ? kQgBX2 / kCols / kQgEpiHalves : 1;
+            float sum[kSums][kCols];
             for (int c0 = un.j0; c0 < un.j1; c0 += chunk, ++cc) {
                 const int ab = p.nacc == 2 ? (cc & 1) : 0, use = p.nacc == 2 ? (cc >> 1) : cc;
                 if (!(ok = qg_wait(smem_u32(&acc_full[ab]), (uint32_t)(use & 1), flags, p.err))) break;
@@ -580,32 +586,32 @@ __global__ void __launch_bounds__(kQgThreads, 1) q4g_gemm_kernel(const __grid_co
                 __syncwarp();
                 const uint32_t acol = tmem + tq + (uint32_t)(ab * p.accw);
                 if (PX == 2) {
-                    // all of the chunk to registers, the accumulator given back, then the sums
-                    uint32_t r[kSums][16] = {};
 #pragma unroll
-                    for (int k = 0; k < kSums; ++k)
-                        if (half + kQgEpiHalves * k < nch) tc_ld16(acol + 16 * (half + kQgEpiHalves * k), r[k]);
-                    tc_wait_ld();
+                    for (int k = 0; k < kSums; k += 2) {
+                        uint32_t r[2][kCols] = {};
 #pragma unroll
-                    for (int k = 0; k < kSums; ++k)
+                        for (int h = 0; h < 2; ++h)
+                            if (half + kQgEpiHalves * (k + h) < nch) tc_ld8(acol + kCols * (half + kQgEpiHalves * (k + h)), r[h]);
+                        tc_wait_ld();
+                        if (k + 2 >= kSums) release(ab);
 #pragma unroll
-                        for (int i = 0; i < 16; ++i) asm volatile("" : "+r"(r[k][i]));  // not used before the wait
-                    release(ab);
+                        for (int h = 0; h < 2; ++h)
 #pragma unroll
-                    for (int k = 0; k < kSums; ++k)
-                        if (half + kQgEpiHalves * k < nch)
-#pragma unroll
-                            for (int i = 0; i < 16; ++i)
-                                sum[PX == 2 ? k : 0][i] = c0 == un.j0 ? __uint_as_float(r[k][i]) : sum[PX == 2 ? k : 0][i] + __uint_as_float(r[k][i]);
+                            for (int i = 0; i < kCols; ++i) {
+                                asm volatile("" : "+r"(r[h][i]));  // not used before the wait
+                                float& to = sum[PX == 2 ? k + h : 0][i];
+                                to = c0 == un.j0 ? __uint_as_float(r[h][i]) : to + __uint_as_float(r[h][i]);
+                            }
+                    }
                 } else {
-                    uint32_t r[16];
-                    if (half < nch) tc_ld16(acol + 16 * half, r);
+                    uint32_t r[kCols];
+                    if (half < nch) tc_ld8(acol + kCols * half, r);
                     for (int k = half; k < nch; k += kQgEpiHalves) {
                         tc_wait_ld();
-                        float v[16];
+                        float v[kCols];
 #pragma unroll
-                        for (int i = 0; i < 16; ++i) v[i] = __uint_as_float(r[i]);
-                        if (k + kQgEpiHalves < nch) tc_ld16(acol + 16 * (k + kQgEpiHalves), r);
+                        for (int i = 0; i < kCols; ++i) v[i] = __uint_as_float(r[i]);
+                        if (k + kQgEpiHalves < nch) tc_ld8(acol + kCols * (k + kQgEpiHalves), r);
                         put(k, v);
                     }
                     release(ab);
@@ -613,9 +619,15 @@ __global__ void __launch_bounds__(kQgThreads, 1) q4g_gemm_kernel(const __grid_co
             }
             if (!ok) break;
             if (PX == 2) {
+                // one copy of the code: four side by side do not fit the registers
+#pragma unroll 1
+                for (int k = half; k < nch; k += kQgEpiHalves) {
+                    put(k, sum[0]);
 #pragma unroll
-                for (int k = 0; k < kSums; ++k)
-                    if (half + kQgEpiHalves * k < nch) put(half + kQgEpiHalves * k, sum[PX == 2 ? k : 0]);
+                    for (int j = 0; j + 1 < kSums; ++j)
+#pragma unroll
+                        for (int i = 0; i < kCols; ++i) sum[j][i] = sum[j + 1][i];
+                }
             }
         }
     } else {
@@ -672,13 +684,8 @@ __global__ void __launch_bounds__(kQgThreads, 1) q4g_gemm_kernel(const __grid_co
                 const uint32_t col = tmem + ((uint32_t)(32 * q + 16 * hh) << 16) + (uint32_t)(p.nacc * p.accw + 64 * PA * at.s);
                 // what needs no free stage comes before the wait for one, and before the last
                 // tile's stores are waited for
-                uint32_t hi[32], lo[16];
+                uint32_t hi[16], lo[16];
                 qg_convert<PA, NG>(seg, 0, lane, magic, m0, m1, hi, lo);
-                if (PA == 1) {
-                    qg_convert<PA, NG>(seg, 1, lane, magic, m0, m1, hi + 16, lo);
-                    __syncwarp();
-                    if (lane == 0) mbar_arrive(smem_u32(&r_empty[ar.s]));
-                }
                 announce();
                 if (!e_ready && !(ok = qg_wait(smem_u32(&empty[at.s]), at.ph ^ 1u, flags, p.err))) break;
                 QgRing rn = r;  // this group's next raw stage
@@ -687,7 +694,11 @@ __global__ void __launch_bounds__(kQgThreads, 1) q4g_gemm_kernel(const __grid_co
                 tc_fence_after();
                 __syncwarp();
                 if (PA == 1) {
-                    tc_st_frag64(col, hi);
+                    tc_st_frag(col, hi);
+                    qg_convert<PA, NG>(seg, 1, lane, magic, m0, m1, hi, lo);
+                    __syncwarp();
+                    if (lane == 0) mbar_arrive(smem_u32(&r_empty[ar.s]));
+                    tc_st_frag(col + 32, hi);
                 } else {
                     tc_st_frag(col, hi);
                     tc_st_frag(col + 64, lo);
