@@ -156,32 +156,35 @@ __device__ __forceinline__ bool elect_one() {
 }
 
 // One 64-K tile h of a segment of one row block: fragment registers of its f16 weights (and their rests).
-template <int NP, int NG>
-__device__ __forceinline__ void qg_convert(const uint8_t* seg, int h, int lane, uint32_t magic, float m0, float m1, uint32_t hi[16], uint32_t lo[16]) {
+// g: the group's constants (with one group a segment, those of tile 0 serve tile 1).
+struct QgGroup {
+    uint32_t zl, zh;
+    __half2 s0, s1;
+};
+template <int PA, int NG>
+__device__ __forceinline__ void qg_convert(const uint8_t* seg, int h, int lane, uint32_t magic, float m0, float m1, QgGroup& g, uint32_t hi[16], uint32_t lo[16]) {
     const uint4 q = *reinterpret_cast<const uint4*>(seg + h * kQgTile + lane * 16);
     const uint32_t word[4] = {q.x, q.y, q.z, q.w};
     const uint32_t* sw = reinterpret_cast<const uint32_t*>(seg + 2 * kQgTile + (lane >> 2) * (8 * NG));
-    uint32_t zl = 0, zh = 0;
-    __half2 s0, s1;
 #pragma unroll
     for (int s = 0; s < 4; ++s) {
-        if (s == 0 || (NG == 4 && s == 2)) {
+        if ((s == 0 && (NG != 1 || h == 0)) || (NG == 4 && s == 2)) {
             const int gi = NG == 1 ? 0 : NG == 2 ? h : 2 * h + (s >> 1);
             const uint2 v = *reinterpret_cast<const uint2*>(sw + 2 * gi);
-            zl = qg_zero<false>(v.x, false);
-            zh = qg_zero<false>(v.y, true);
-            s0 = __float2half2_rn(qg_scale(v.x) * m0);
-            s1 = __float2half2_rn(qg_scale(v.y) * m1);
+            g.zl = qg_zero<false>(v.x, false);
+            g.zh = qg_zero<false>(v.y, true);
+            g.s0 = __float2half2_rn(qg_scale(v.x) * m0);
+            g.s1 = __float2half2_rn(qg_scale(v.y) * m1);
         }
         uint32_t a[4];
-        qg_codes<false>(word[s], magic, zl, zh, a);
+        qg_codes<false>(word[s], magic, g.zl, g.zh, a);
 #pragma unroll
         for (int i = 0; i < 4; ++i) {
             const __half2 c = *reinterpret_cast<__half2*>(&a[i]);
-            const __half2 sc = i & 1 ? s1 : s0;
+            const __half2 sc = i & 1 ? g.s1 : g.s0;
             const __half2 p = __hmul2(c, sc);
             hi[4 * s + i] = *reinterpret_cast<const uint32_t*>(&p);
-            if (NP == 2) {
+            if (PA == 2) {
                 const __half2 r = __hfma2(c, sc, __hneg2(p));
                 lo[4 * s + i] = *reinterpret_cast<const uint32_t*>(&r);
             }
@@ -685,7 +688,8 @@ __global__ void __launch_bounds__(kQgThreads, 1) q4g_gemm_kernel(const __grid_co
                 // what needs no free stage comes before the wait for one, and before the last
                 // tile's stores are waited for
                 uint32_t hi[16], lo[16];
-                qg_convert<PA, NG>(seg, 0, lane, magic, m0, m1, hi, lo);
+                QgGroup gc;
+                qg_convert<PA, NG>(seg, 0, lane, magic, m0, m1, gc, hi, lo);
                 announce();
                 if (!e_ready && !(ok = qg_wait(smem_u32(&empty[at.s]), at.ph ^ 1u, flags, p.err))) break;
                 QgRing rn = r;  // this group's next raw stage
@@ -695,14 +699,14 @@ __global__ void __launch_bounds__(kQgThreads, 1) q4g_gemm_kernel(const __grid_co
                 __syncwarp();
                 if (PA == 1) {
                     tc_st_frag(col, hi);
-                    qg_convert<PA, NG>(seg, 1, lane, magic, m0, m1, hi, lo);
+                    qg_convert<PA, NG>(seg, 1, lane, magic, m0, m1, gc, hi, lo);
                     __syncwarp();
                     if (lane == 0) mbar_arrive(smem_u32(&r_empty[ar.s]));
                     tc_st_frag(col + 32, hi);
                 } else {
                     tc_st_frag(col, hi);
                     tc_st_frag(col + 64, lo);
-                    qg_convert<PA, NG>(seg, 1, lane, magic, m0, m1, hi, lo);
+                    qg_convert<PA, NG>(seg, 1, lane, magic, m0, m1, gc, hi, lo);
                     __syncwarp();
                     if (lane == 0) mbar_arrive(smem_u32(&r_empty[ar.s]));
                     tc_st_frag(col + 32, hi);
