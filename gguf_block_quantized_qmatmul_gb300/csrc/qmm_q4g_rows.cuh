@@ -14,13 +14,18 @@
 // work, items (a group of activation rows with their weight matrix) times row
 // blocks, is dealt to one block an SM in equal contiguous shares.  Every warp
 // has its own ring of kQgDepth segments in shared memory, filled by asynchronous
-// 16-byte copies (codes: each lane copies what it will read); a tile of 16 rows x
+// 16-byte copies (each lane copies the codes that it will read); a tile of 16 rows x
 // 64 K is then one conflict-free 16-byte load a lane, in fragment order, and
 // about 9 (f16) or 11 (bf16) instructions turn a word of eight codes into MMA
 // operands.  Measured at 1 x 28672 x 8192 (f16, G = 64): loads straight into
 // registers, four segments ahead, 44 us (16 warps an SM, and waiting for the
 // oldest load waited for younger ones too); one bulk copy per two segments 35
-// us, and still 30 us with no arithmetic at all.  wk warps split a row block's K
+// us, and still 30 us with no arithmetic at all; these rings 27.2 us (4.6 TB/s,
+// 62 % of the issue slots).  14336 x 4096 bf16 with 8 rows: 11.6 us, of which the
+// launch and the staging of 64 KB of activations a block are some 4 (12.5 us with
+// one staging load a thread in flight and a division an address); one row of
+// 4096 x 4096 bf16: 5.3 us; 28 us for 16 tokens' second products of 8 of 128
+// experts (768 -> 2048, G = 32), with the launch that adds a token's.  wk warps split a row block's K
 // and add their sums through shared memory, one barrier among them per row block.
 // Activations are staged once per item in the order the MMAs read them (16
 // bytes a lane, conflict-free).  Weights are constant, so a dense call's first
@@ -133,44 +138,57 @@ __device__ __forceinline__ uint4 qg_quad_transpose(uint32_t w0, uint32_t w1, uin
 }
 
 // Stage `rows` rows of x (row r at element offset at(r)) as columns of virtual segments v0..
-template <class At>
-__device__ __forceinline__ void qg_stage(uint8_t* sm, const void* x, int xt, int K, int KS, int rows, int np, int v0, At at, int tid, int nthr) {
+// B 16-byte loads (f32: pairs of them) a thread are in flight.
+template <int B, bool F32, class At>
+__device__ __forceinline__ void qg_stage_as(uint8_t* sm, const void* x, int K, int KS, int rows, int np, int v0, At at, int tid, int nthr) {
     const int ncol = rows * np, n = KS * 4 * rows * 4;  // quads: (32 K, row)
-    for (int i0 = 0; i0 < n; i0 += nthr) {
-        const int i = i0 + tid, j = i & 3, quad = i >> 2;
-        const int h = quad / rows, r = quad - h * rows, k = 32 * h + 8 * j;
-        const bool on = i < n && k < K;
-        uint8_t* to = sm + ((size_t)(v0 * 4 + h) * ncol + r * np) * 64 + j * 16;
-        if (xt == X_F32) {
-            float f[8];
+    const uint32_t magic = 0xffffffffu / (uint32_t)rows + 1u;  // quad / rows = umulhi(quad, magic): quad rows < 2^32; 0 for one row
+    for (int i0 = 0; i0 < n; i0 += B * nthr) {
+        uint4 u[B][F32 ? 2 : 1];
+        uint8_t* to[B];
 #pragma unroll
-            for (int e = 0; e < 8; ++e) f[e] = 0.0f;
-            if (on) {
-                const float4* src = reinterpret_cast<const float4*>(static_cast<const float*>(x) + at(r) + k);
-                const float4 a = src[0], b = src[1];
-                f[0] = a.x; f[1] = a.y; f[2] = a.z; f[3] = a.w;
-                f[4] = b.x; f[5] = b.y; f[6] = b.z; f[7] = b.w;
+        for (int b = 0; b < B; ++b) {
+            const int i = i0 + b * nthr + tid, j = i & 3, quad = i >> 2;
+            const int h = magic ? (int)__umulhi((uint32_t)quad, magic) : quad, r = quad - h * rows, k = 32 * h + 8 * j;
+            const bool on = i < n && k < K;
+            to[b] = i < n ? sm + ((size_t)(v0 * 4 + h) * ncol + r * np) * 64 + j * 16 : nullptr;
+#pragma unroll
+            for (int q = 0; q < (F32 ? 2 : 1); ++q) {
+                u[b][q] = make_uint4(0u, 0u, 0u, 0u);
+                if (on) u[b][q] = reinterpret_cast<const uint4*>(static_cast<const uint8_t*>(x) + (at(r) + k) * (F32 ? 4 : 2))[q];
             }
+        }
 #pragma unroll
-            for (int pc = 0; pc < 3; ++pc) {
-                uint32_t w[4];
+        for (int b = 0; b < B; ++b) {
+            const int i = i0 + b * nthr + tid, j = i & 3;
+            if (i - (tid & 31) >= n) break;  // the whole warp is done
+            if constexpr (F32) {
+                float f[8] = {__uint_as_float(u[b][0].x), __uint_as_float(u[b][0].y), __uint_as_float(u[b][0].z), __uint_as_float(u[b][0].w),
+                              __uint_as_float(u[b][1].x), __uint_as_float(u[b][1].y), __uint_as_float(u[b][1].z), __uint_as_float(u[b][1].w)};
 #pragma unroll
-                for (int e = 0; e < 8; ++e) {
-                    const uint32_t u = __float_as_uint(f[e]) & 0xffff0000u;
-                    w[e >> 1] = e & 1 ? w[e >> 1] | u : u >> 16;
-                    // the rest is exact; an infinity or NaN has none
-                    f[e] = (u & 0x7f800000u) == 0x7f800000u ? 0.0f : f[e] - __uint_as_float(u);
+                for (int pc = 0; pc < 3; ++pc) {
+                    uint32_t w[4];
+#pragma unroll
+                    for (int e = 0; e < 8; ++e) {
+                        const uint32_t v = __float_as_uint(f[e]) & 0xffff0000u;
+                        w[e >> 1] = e & 1 ? w[e >> 1] | v : v >> 16;
+                        // the rest is exact; an infinity or NaN has none
+                        f[e] = (v & 0x7f800000u) == 0x7f800000u ? 0.0f : f[e] - __uint_as_float(v);
+                    }
+                    const uint4 q = qg_quad_transpose(w[0], w[1], w[2], w[3], j);
+                    if (i < n) *reinterpret_cast<uint4*>(to[b] + pc * 64) = q;
                 }
-                const uint4 q = qg_quad_transpose(w[0], w[1], w[2], w[3], j);
-                if (i < n) *reinterpret_cast<uint4*>(to + pc * 64) = q;
+            } else {
+                const uint4 q = qg_quad_transpose(u[b][0].x, u[b][0].y, u[b][0].z, u[b][0].w, j);
+                if (i < n) *reinterpret_cast<uint4*>(to[b]) = q;
             }
-        } else {
-            uint4 u = make_uint4(0u, 0u, 0u, 0u);
-            if (on) u = *reinterpret_cast<const uint4*>(static_cast<const uint16_t*>(x) + at(r) + k);
-            const uint4 q = qg_quad_transpose(u.x, u.y, u.z, u.w, j);
-            if (i < n) *reinterpret_cast<uint4*>(to) = q;
         }
     }
+}
+template <class At>
+__device__ __forceinline__ void qg_stage(uint8_t* sm, const void* x, int xt, int K, int KS, int rows, int np, int v0, At at, int tid, int nthr) {
+    if (xt == X_F32) qg_stage_as<2, true>(sm, x, K, KS, rows, np, v0, at, tid, nthr);
+    else qg_stage_as<4, false>(sm, x, K, KS, rows, np, v0, at, tid, nthr);
 }
 
 constexpr int kQgMaxK = 32;  // slots of one token, at most

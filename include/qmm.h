@@ -274,8 +274,9 @@ qmm_status qmm_matmul_static_workspace(qmm_type wtype, qmm_act_mode mode, const 
    Accuracy: one activation row of up to 16384 values rounds no weight, nor do
    more rows times a small matrix.  Otherwise (the choice depends on the type
    and the sizes alone) f16 and bf16 calls round each weight s (q - z) to f16's
-   11 bits, which is below the rounding of the output in bf16, and f32 calls
-   keep 22 bits of the activations and all of the weights.  A row of x with an
+   11 bits, less than the rounding of the output (not qmm_moe_gate_up in f16,
+   whose weights are exact), and f32 calls keep 22 bits of the activations and
+   all of the weights.  A row of x with an
    infinity or a NaN gives a row of outputs that are not finite; no other row
    is touched.
    Results do not depend on the run: no sum's order varies. */
