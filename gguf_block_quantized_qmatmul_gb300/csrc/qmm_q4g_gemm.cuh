@@ -441,7 +441,7 @@ __global__ void __launch_bounds__(kQgThreads, 1) q4g_gemm_kernel(const __grid_co
                         const int nh = halves(c0 + i);
                         __syncwarp();
                         if (lead) {
-// The small products first, while the accumulator is small: adding to it truncates.
+                            // the small products first, while the accumulator is small: adding to it truncates
                             constexpr int kPasses = PA + PX - 1;  // weights, activations: hi lo, lo hi, hi hi (one piece: hi)
 #pragma unroll
                             for (int pass = 0; pass < kPasses; ++pass) {
@@ -647,6 +647,7 @@ __global__ void __launch_bounds__(kQgThreads, 1) q4g_gemm_kernel(const __grid_co
                 }
             }
         }
+        cp_async_wait<0>();  // after a wait that gave up, the next tables are still on their way
     } else {
         // ------------------------------ conversion ------------------------------
         const int cw = warp - kQgConv0, q = warp & 3, hh = (cw >> 2) & 1, grp = cw >> 3;  // row block 2 q + hh of a tile

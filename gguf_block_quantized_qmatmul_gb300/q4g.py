@@ -130,6 +130,9 @@ class Route(NamedTuple):
     order: Optional[torch.Tensor] = None
 
 
+_tuple_new = tuple.__new__
+
+
 def _laid_out(experts, N, K, group, gate_up, device):
     n = int(_lib().qmm_q4g_bytes(experts, N, K, group, int(gate_up)))
     return torch.empty(n, dtype=torch.uint8, device=device)
@@ -213,7 +216,7 @@ def moe_route(logits: torch.Tensor, top_k: int, score: str = "softmax", bias: to
     r = _binding.route(logits, bias, top_k, SCORES[score], groups, top_groups, GROUP_SCORES[group_score], renorm, scale, order, workspace)
     if type(r) is int:
         _check(r, "qmm_moe_route")
-    return Route(*r)
+    return _tuple_new(Route, r)  # a third of the time of Route(*r)
 
 
 def moe_gate_up(w: Q4GWeights, x: torch.Tensor, route: Route, out: torch.Tensor | None = None,

@@ -458,6 +458,19 @@ def test_gemm_keeps_the_precision(q, dt, G):
     assert q.last_device_error() == 0
 
 
+def test_matmul_of_many_tiles(q):
+    """More tiles to a block than it looks up at its start."""
+    M, N, K = 40000, 2050, 32
+    t = make(1, N, K, 32, True, "f16", 41)
+    x = torch.randn((M, K), generator=rng(42)).cuda()
+    y = q.q4g_matmul(pack(q, t), x)
+    ref = x.double() @ t[3][0].cuda().T
+    T = x.double().abs() @ t[3][0].cuda().abs().T
+    assert bool(((y.double() - ref).abs() <= 1e-5 * T).all())
+    assert float((y.double() - ref).norm() / ref.norm()) < 1e-6
+    assert q.last_device_error() == 0
+
+
 def test_refused_tensors(q):
     w = pack(q, make(1, 64, 128, 64, True, "f16", 4))
     x = torch.zeros((2, 128), dtype=torch.float16, device="cuda")
