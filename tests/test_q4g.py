@@ -471,6 +471,21 @@ def test_matmul_of_many_tiles(q):
     assert q.last_device_error() == 0
 
 
+def test_route_tensors_are_ordinary(q):
+    """Parts of one allocation: apart, 16-byte aligned, and alive by themselves."""
+    r = q.moe_route(torch.randn((5, 7), generator=rng(50)).cuda(), 3)
+    spans = sorted((v.data_ptr(), v.data_ptr() + 4 * v.numel()) for v in r)
+    assert all(a % 16 == 0 for a, _ in spans) and all(x[1] <= y[0] for x, y in zip(spans, spans[1:]))
+    assert [v.dtype for v in r] == [torch.int32, torch.float32, torch.int32, torch.int32]
+    assert all(v.is_contiguous() and v._version == 0 and not v.requires_grad for v in r)
+    ids, kept = r.ids, r.ids.clone()
+    del r
+    torch.full((4096,), -1, dtype=torch.int32, device="cuda")
+    assert torch.equal(ids, kept) and torch.equal(ids.add(1).sub_(1), kept) and torch.equal(ids.t().contiguous(), kept.t().contiguous())
+    one = q.moe_route(torch.randn((5, 7), generator=rng(50)).cuda(), 3, order=False)
+    assert one.offsets is None and one.order is None and torch.equal(one.ids, kept)
+
+
 def test_refused_tensors(q):
     w = pack(q, make(1, 64, 128, 64, True, "f16", 4))
     x = torch.zeros((2, 128), dtype=torch.float16, device="cuda")
