@@ -90,14 +90,22 @@ struct QgGemmParams {
     int off_raw, off_bar;
 };
 
-// 32 columns of 16 lanes from fragment registers: lane 4 g + t's registers 2 j, 2 j + 1 are column 4 j + t of lanes g, g + 8
-__device__ __forceinline__ void tc_st_frag(uint32_t taddr, const uint32_t v[16]) {
-    asm volatile(
-        "tcgen05.st.sync.aligned.16x128b.x8.b32 [%0], {%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,%15,%16};" ::"r"(taddr),
-        "r"(v[0]), "r"(v[1]), "r"(v[2]), "r"(v[3]), "r"(v[4]), "r"(v[5]), "r"(v[6]), "r"(v[7]), "r"(v[8]), "r"(v[9]),
-        "r"(v[10]), "r"(v[11]), "r"(v[12]), "r"(v[13]), "r"(v[14]), "r"(v[15])
-        : "memory");
+// 2 R columns of 16 lanes from R fragment registers: lane 4 g + t's registers 2 j, 2 j + 1 are column 4 j + t of lanes g, g + 8
+template <int R>
+__device__ __forceinline__ void tc_st_frag(uint32_t taddr, const uint32_t* v) {
+    static_assert(R == 16 || R == 8, "one or two pieces");
+    if constexpr (R == 16)
+        asm volatile(
+            "tcgen05.st.sync.aligned.16x128b.x8.b32 [%0], {%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,%15,%16};" ::"r"(taddr),
+            "r"(v[0]), "r"(v[1]), "r"(v[2]), "r"(v[3]), "r"(v[4]), "r"(v[5]), "r"(v[6]), "r"(v[7]), "r"(v[8]), "r"(v[9]),
+            "r"(v[10]), "r"(v[11]), "r"(v[12]), "r"(v[13]), "r"(v[14]), "r"(v[15])
+            : "memory");
+    else
+        asm volatile("tcgen05.st.sync.aligned.16x128b.x4.b32 [%0], {%1,%2,%3,%4,%5,%6,%7,%8};" ::"r"(taddr), "r"(v[0]), "r"(v[1]),
+                     "r"(v[2]), "r"(v[3]), "r"(v[4]), "r"(v[5]), "r"(v[6]), "r"(v[7])
+                     : "memory");
 }
+
 // Pairs of blocks (cta_group::2): a cluster of two, whose rank 0 issues the MMAs of both.
 __device__ __forceinline__ uint32_t cluster_rank() {
     uint32_t r;
@@ -169,19 +177,20 @@ __device__ __forceinline__ bool elect_one() {
     return p != 0;
 }
 
-// One 64-K tile h of a segment of one row block: fragment registers of its f16 weights (and their rests).
-// g: the group's constants (with one group a segment, those of tile 0 serve tile 1).
+// Words s0 .. s0 + WORDS - 1 of a lane's four of 64-K tile h of a segment: fragment registers of
+// their f16 weights (and their rests).  g: the group's constants (with one group a segment, those
+// of tile 0 serve tile 1).
 struct QgGroup {
     uint32_t zl, zh;
     __half2 s0, s1;
 };
-template <int PA, int NG>
-__device__ __forceinline__ void qg_convert(const uint8_t* seg, int h, int lane, uint32_t magic, float m0, float m1, QgGroup& g, uint32_t hi[16], uint32_t lo[16]) {
-    const uint4 q = *reinterpret_cast<const uint4*>(seg + h * kQgTile + lane * 16);
+template <int PA, int NG, int WORDS>
+__device__ __forceinline__ void qg_convert(const uint8_t* seg, const uint4& q, int h, int s0, int lane, uint32_t magic, float m0, float m1, QgGroup& g, uint32_t* hi,
+                                           uint32_t* lo) {
     const uint32_t word[4] = {q.x, q.y, q.z, q.w};
     const uint32_t* sw = reinterpret_cast<const uint32_t*>(seg + 2 * kQgTile + (lane >> 2) * (8 * NG));
 #pragma unroll
-    for (int s = 0; s < 4; ++s) {
+    for (int s = s0; s < s0 + WORDS; ++s) {
         if ((s == 0 && (NG != 1 || h == 0)) || (NG == 4 && s == 2)) {
             const int gi = NG == 1 ? 0 : NG == 2 ? h : 2 * h + (s >> 1);
             const uint2 v = *reinterpret_cast<const uint2*>(sw + 2 * gi);
@@ -197,10 +206,10 @@ __device__ __forceinline__ void qg_convert(const uint8_t* seg, int h, int lane, 
             const __half2 c = *reinterpret_cast<__half2*>(&a[i]);
             const __half2 sc = i & 1 ? g.s1 : g.s0;
             const __half2 p = __hmul2(c, sc);
-            hi[4 * s + i] = *reinterpret_cast<const uint32_t*>(&p);
+            hi[4 * (s - s0) + i] = *reinterpret_cast<const uint32_t*>(&p);
             if (PA == 2) {
                 const __half2 r = __hfma2(c, sc, __hneg2(p));
-                lo[4 * s + i] = *reinterpret_cast<const uint32_t*>(&r);
+                lo[4 * (s - s0) + i] = *reinterpret_cast<const uint32_t*>(&r);
             }
         }
     }
@@ -702,9 +711,12 @@ __global__ void __launch_bounds__(kQgThreads, 1) q4g_gemm_kernel(const __grid_co
                 const uint32_t col = tmem + ((uint32_t)(32 * q + 16 * hh) << 16) + (uint32_t)(p.nacc * p.accw + 64 * PA * at.s);
                 // what needs no free stage comes before the wait for one, and before the last
                 // tile's stores are waited for
-                uint32_t hi[16], lo[16];
+                // with two pieces half of a 64-K tile's registers at a time: all of them were spilled
+                constexpr int kWords = PA == 1 ? 4 : 2, kSteps = 8 / kWords;
+                uint32_t hi[4 * kWords], lo[4 * kWords];
                 QgGroup gc;
-                qg_convert<PA, NG>(seg, 0, lane, magic, m0, m1, gc, hi, lo);
+                uint4 codes = reinterpret_cast<const uint4*>(seg)[lane];
+                qg_convert<PA, NG, kWords>(seg, codes, 0, 0, lane, magic, m0, m1, gc, hi, lo);
                 announce();
                 if (!e_ready && !(ok = qg_wait(smem_u32(&empty[at.s]), at.ph ^ 1u, flags, p.err))) break;
                 QgRing rn = r;  // this group's next raw stage
@@ -712,20 +724,18 @@ __global__ void __launch_bounds__(kQgThreads, 1) q4g_gemm_kernel(const __grid_co
                 r_ready = mbar_test(smem_u32(&r_full[rn.s]), rn.ph);
                 tc_fence_after();
                 __syncwarp();
-                if (PA == 1) {
-                    tc_st_frag(col, hi);
-                    qg_convert<PA, NG>(seg, 1, lane, magic, m0, m1, gc, hi, lo);
-                    __syncwarp();
-                    if (lane == 0) mbar_arrive(smem_u32(&r_empty[ar.s]));
-                    tc_st_frag(col + 32, hi);
-                } else {
-                    tc_st_frag(col, hi);
-                    tc_st_frag(col + 64, lo);
-                    qg_convert<PA, NG>(seg, 1, lane, magic, m0, m1, gc, hi, lo);
-                    __syncwarp();
-                    if (lane == 0) mbar_arrive(smem_u32(&r_empty[ar.s]));
-                    tc_st_frag(col + 32, hi);
-                    tc_st_frag(col + 96, lo);
+#pragma unroll
+                for (int step = 0; step < kSteps; ++step) {
+                    if (step > 0) {
+                        if (step * 2 == kSteps) codes = reinterpret_cast<const uint4*>(seg + kQgTile)[lane];
+                        qg_convert<PA, NG, kWords>(seg, codes, step * 2 / kSteps, step * kWords % 4, lane, magic, m0, m1, gc, hi, lo);
+                        if (step == kSteps - 1) {
+                            __syncwarp();
+                            if (lane == 0) mbar_arrive(smem_u32(&r_empty[ar.s]));
+                        }
+                    }
+                    tc_st_frag<4 * kWords>(col + 8 * kWords * step, hi);
+                    if (PA == 2) tc_st_frag<4 * kWords>(col + 64 + 8 * kWords * step, lo);
                 }
                 stored = at.s;
                 if (p.nstage <= kQgGroups) announce();  // no stage to spare
