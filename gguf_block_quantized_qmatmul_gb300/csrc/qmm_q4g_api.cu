@@ -32,13 +32,15 @@ qmm_status check_rows(const void* x, int xt, int64_t ldx, int64_t K) {
 
 // The kernel a product goes to.  The row kernel streams the weights once per
 // item of a few activation rows and turns every code into an MMA operand once
-// per 8 columns (an f32 row is three): about 3 us + 4e-8 us per weight and
-// column.  The GEMM's conversion serves up to 256 rows, but a call has some 8
-// us of fixed cost.  Measured (row kernel / GEMM, us): 4096 x 4096 bf16, 8 rows
-// 8.4 / 11.3, 16 rows 17.0 / 11.0; 14336 x 4096 f32, 8 rows 23.0 / 24.0, 10
-// rows 29.9 / 24.0; 1000 x 2048 bf16, 64 rows 7.5 / 9.5; 4096 x 14336 bf16, 8
-// rows (two items) 23.7 / 20.4; gate_up of 64 experts, 2048 -> 2 x 1024 bf16,
-// 8 slots an expert 60 / 69, 16 slots 123 / 70; f32, 4 slots 106 / 98.
+// per 8 columns (an f32 row is three).  The GEMM's conversion serves up to 256
+// rows (f32: 64), but a call has some 8 us of fixed cost.  Measured (row kernel
+// / GEMM, us): 4096 x 4096 bf16, 8 rows 7.2 / 10.4, 12 rows 8.5 / 10.2; 14336 x
+// 4096 bf16, 12 rows 15.3 / 18.2, 16 rows 19.3 / 18.3; 4096 x 14336 bf16, 8 rows
+// (two items) 22.3 / 19.5; 14336 x 4096 f32, 8 rows (two items) 23.1 / 28.1, 10
+// rows 46 / 28; 1000 x 2048 bf16, 64 rows 6.2 / 8.7.  gate_up and down of 64
+// experts, 2048 -> 2 x 1024 -> 2048, bf16: 8 slots an expert 59 + 41 / 59 + 37,
+// 16 slots 117 + 60 / 59 + 38; f32: 4 slots 103 + 49 / 100 + 58, 8 slots 124 + 60
+// / 101 + 59; of 128 experts with 768, f32: 4 slots 142 + 69 / 152 + 86.
 struct Choice {
     bool gemm = false;
     QgRowsPlan rows;
@@ -51,10 +53,11 @@ Choice choose(const QgCall& c, int sms, int smem) {
     const int np = c.xt == X_F32 ? 3 : 1;
     const long long columns = (long long)c.M * np, size = (long long)c.w.N * c.w.K;
     const bool small = columns * size <= 160000000;
-    const bool few = c.op == P_DENSE ? columns <= 8 || (columns <= 24 && np == 3) || small : columns <= 8ll * c.w.E;
+    const bool few = c.op == P_DENSE ? columns <= (np == 3 ? 24 : 12) || small : columns <= (np == 3 ? 12ll : 8ll) * c.w.E;
     if (few) ch.rows = plan_q4g_rows(c, sms, smem);
-    // activations that do not fit one pass over a large matrix
-    if (ch.rows.ok && c.op == P_DENSE && ch.rows.items > 1 && !small && (ch.mm = plan_q4g_gemm(c, sms, smem)).ok) ch.rows.ok = false;
+    // activations that do not fit one pass (f32: two) over a large matrix
+    if (ch.rows.ok && c.op == P_DENSE && ch.rows.items > (np == 3 ? 2 : 1) && !small && (ch.mm = plan_q4g_gemm(c, sms, smem)).ok)
+        ch.rows.ok = false;
     if (!ch.rows.ok) ch.mm = plan_q4g_gemm(c, sms, smem);
     if (!ch.rows.ok && !ch.mm.ok) ch.rows = plan_q4g_rows(c, sms, smem);
     ch.gemm = !ch.rows.ok && ch.mm.ok;
