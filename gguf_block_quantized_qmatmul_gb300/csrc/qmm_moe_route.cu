@@ -380,9 +380,13 @@ __global__ void __launch_bounds__(kOrderThreads) moe_order_kernel(const RoutePar
     // halves (at most 1000 of up to 32 in either half warp), then the warps' sums.
     for (int base = 0; base < p.blocks; base += kOrderRows) {
         const int end = min(p.blocks, base + kOrderRows);
-        for (int e0 = 16 * (lane & 15); e0 < p.stride; e0 += 256)
+        for (int c0 = 0; c0 < p.stride; c0 += 256)
             for (int half = 0; half < 2; ++half) {
-                const int from = half ? max(base, min(b0, end)) : base, to = half ? end : min(b0, end);
+                // The half warps' trip counts differ, and nothing brings them together after the loop
+                // but the shuffle itself: every lane takes part in it, those without experts too.
+                const int e0 = c0 + 16 * (lane & 15);
+                const bool on = e0 < p.stride;
+                const int from = half ? max(base, min(b0, end)) : base, to = !on ? from : half ? end : min(b0, end);
                 uint32_t s8[8] = {};
                 for (int b = from + 2 * warp + (lane >> 4); b < to; b += 8 * kOrderWarps) {
                     uint4 v[4];
@@ -401,10 +405,9 @@ __global__ void __launch_bounds__(kOrderThreads) moe_order_kernel(const RoutePar
                         }
                     }
                 }
-                const unsigned here = __activemask();
 #pragma unroll
-                for (int q = 0; q < 8; ++q) s8[q] += __shfl_xor_sync(here, s8[q], 16);
-                if (lane < 16) {
+                for (int q = 0; q < 8; ++q) s8[q] += __shfl_xor_sync(0xffffffffu, s8[q], 16);
+                if (on && lane < 16) {
                     uint4* to4 = reinterpret_cast<uint4*>(sums + (half * kOrderWarps + warp) * words + e0 / 2);
                     to4[0] = make_uint4(s8[0], s8[1], s8[2], s8[3]);
                     to4[1] = make_uint4(s8[4], s8[5], s8[6], s8[7]);
