@@ -256,9 +256,10 @@ def last_device_error() -> int:
 
 def test_inject(kind: str, count: int = 1, arg: int = 0) -> None:
     """Failure-test hook: arm an injected failure ("launch_failure": the next
-    `count` matmul calls return QMM_ERR_CUDA without touching the device;
-    "stall": the next decode-kernel launch withholds its first block's weight
-    stages from stage `arg` on, so a bounded wait times out; "off")."""
+    `count` matmul, routing or experts' calls return QMM_ERR_CUDA without
+    touching the device; "stall": the next launch of the decode kernel or of
+    the 4-bit GEMM withholds a block's weight stages from stage `arg` on, so a
+    bounded wait times out; "off")."""
     _check(_lib().qmm_test_inject(INJECT[kind], count, arg), "qmm_test_inject")
 
 

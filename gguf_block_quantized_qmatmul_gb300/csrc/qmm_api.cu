@@ -208,7 +208,7 @@ qmm_status stream_call(qmm_type wtype, int am, int epi, const void* wq, const fl
         dp.p.y = y;
         dp.p.sums = sums;
         dp.p.err = err;
-        dp.p.stall_stage = take_injection(g_inject_stalls) ? g_inject_stall_stage.load(std::memory_order_relaxed) + 1 : 0;
+        dp.p.stall_stage = injected_stall();
         const bool split = epi == E_Y && dp.p.kslices > 1;
         if (split || dp.ext_bytes) {
             if (!ws || ws_bytes < dp.workspace) return QMM_ERR_WORKSPACE;
@@ -262,6 +262,8 @@ qmm_status stream_call(qmm_type wtype, int am, int epi, const void* wq, const fl
 
 namespace qmm {
 cudaError_t device_constants(unsigned** err, int* sms, int* smem) { return device_info(err, sms, smem); }
+bool injected_launch_failure() { return take_injection(g_inject_launch_failures); }
+int injected_stall() { return take_injection(g_inject_stalls) ? g_inject_stall_stage.load(std::memory_order_relaxed) + 1 : 0; }
 }  // namespace qmm
 
 extern "C" {

@@ -42,6 +42,10 @@ bool make_map_nd(CUtensorMap* m, CUtensorMapDataType dt, const void* base, int r
 // The current device's error word, SM count and opt-in shared memory (looked up once per device).
 cudaError_t device_constants(unsigned** err, int* sms, int* smem);
 
+// Take a pending injection of qmm_test_inject: a launch failure; a stall, as one more than the stages that are issued (0: none).
+bool injected_launch_failure();
+int injected_stall();
+
 // largest activation batch served by the per-thread dp4a GEMV (int8_act,
 // Q8_0 weights only); larger decode batches, Q4_K weights and every f32_act
 // decode batch up to 8 use the 16-row-tile tensor-core kernel

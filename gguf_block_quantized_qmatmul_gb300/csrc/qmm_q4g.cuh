@@ -112,6 +112,13 @@ __device__ __forceinline__ bool qg_wait(uint32_t bar, uint32_t parity, volatile 
         if (clock64() - t0 > kWaitLimitCheck) return mbar_spin(bar, parity, abort_flag, err, false);  // raises the error in the end
     }
 }
+// The same for a whole warp, with one answer for all of its lanes: each lane's own depends on its
+// tries, clock and reading of the abort flag, and a warp that left its loop in part would wait
+// without end at the next instruction that all lanes take part in.  ready: the phase was seen
+// complete before.
+__device__ __forceinline__ bool qg_wait_warp(uint32_t bar, uint32_t parity, bool ready, volatile int* abort_flag, unsigned* err) {
+    return __all_sync(0xffffffffu, ready || qg_wait(bar, parity, abort_flag, err));
+}
 
 // A place in a ring of n stages: its index and the parity of its current use.
 // A producer waits for a stage's release with ph ^ 1, which a fresh barrier

@@ -74,6 +74,7 @@ size_t workspace_of(QgCall c) {
 }
 
 qmm_status product(const QgCall& c, void* ws, size_t ws_bytes, qmm_stream_t stream) {
+    if (injected_launch_failure()) return QMM_ERR_CUDA;  // test hook: no CUDA call made
     unsigned* err = nullptr;
     int sms = 0, smem = 0;
     if (device_constants(&err, &sms, &smem) != cudaSuccess) return QMM_ERR_CUDA;
@@ -84,7 +85,7 @@ qmm_status product(const QgCall& c, void* ws, size_t ws_bytes, qmm_stream_t stre
         if (!aligned(ws, 16)) return QMM_ERR_ALIGN;
     }
     cudaStream_t s = reinterpret_cast<cudaStream_t>(stream);
-    const cudaError_t e = ch.gemm ? launch_q4g_gemm(ch.mm, c, ws, err, smem, s) : launch_q4g_rows(ch.rows, c, ws, smem, s);
+    const cudaError_t e = ch.gemm ? launch_q4g_gemm(ch.mm, c, ws, err, injected_stall(), smem, s) : launch_q4g_rows(ch.rows, c, ws, smem, s);
     return e == cudaSuccess ? QMM_OK : QMM_ERR_CUDA;
 }
 
@@ -242,6 +243,7 @@ qmm_status qmm_moe_route(const qmm_route_config* cfg, qmm_float type, const void
         if (need && (!workspace || workspace_bytes < need)) return QMM_ERR_WORKSPACE;
         if (need && !aligned(workspace, 16)) return QMM_ERR_ALIGN;
     }
+    if (injected_launch_failure()) return QMM_ERR_CUDA;
     RouteCall c;
     c.logits = logits;
     c.xt = (int)type;

@@ -210,7 +210,7 @@ QgGemmPlan plan_q4g_gemm(const QgCall& c, int sms, int smem_max) {
     return pl;
 }
 
-cudaError_t launch_q4g_gemm(const QgGemmPlan& pl, const QgCall& c, void* ws, unsigned* err, int smem_max, cudaStream_t s) {
+cudaError_t launch_q4g_gemm(const QgGemmPlan& pl, const QgCall& c, void* ws, unsigned* err, int stall, int smem_max, cudaStream_t s) {
     uint8_t* wsb = static_cast<uint8_t*>(ws);
     const int rows = c.M, K = c.w.K;
     const void* xsrc = c.x;
@@ -258,6 +258,8 @@ cudaError_t launch_q4g_gemm(const QgGemmPlan& pl, const QgCall& c, void* ws, uns
     p.nx = pl.nx;
     p.nstage = pl.nstage;
     p.ks = pl.ks;
+    p.stall = stall;
+    p.stall_block = (unsigned)pl.cg - 1u;  // of a pair the second one, whose partner finds out by its own waits
     p.off_raw = pl.nx * (pl.bx / pl.cg) * 256 * pl.np;
     p.off_bar = p.off_raw + pl.nraw * 8 * qg_seg_bytes(c.w.ng);
     cudaError_t e;

@@ -77,6 +77,7 @@ constexpr int kQgRawMax = 6, kQgXMax = 8, kQgStageMax = 8;  // stages, at most: 
 constexpr int kQgChunk = 1;      // tiles per accumulation chunk (two pieces of the activations)
 constexpr int kCols = 8;         // accumulator columns that an epilogue warp takes at a time (with 16, 170 bytes a thread were spilled)
 constexpr int kQgMaxE = 512;     // experts of a grouped call
+constexpr long long kQgQuiet = 1ll << 16;  // clocks (some 35 us) that a pair stays after a wait that gave up
 constexpr int kQgTab = 64;       // units of a block that are looked up at its start; later ones when they are taken
 
 struct QgGemmParams {
@@ -88,6 +89,8 @@ struct QgGemmParams {
     int bx, nacc, accw, mtiles, ntiles, nraw, nx, nstage;
     int ks;               // K slices (dense): f32 partial outputs [ks][M][N]
     int off_raw, off_bar;
+    int stall;             // test hook: block stall_block copies only stall - 1 tiles of its raw weights; 0: all
+    unsigned stall_block;
 };
 
 // 2 R columns of 16 lanes from R fragment registers: lane 4 g + t's registers 2 j, 2 j + 1 are column 4 j + t of lanes g, g + 8
@@ -415,6 +418,8 @@ __global__ void __launch_bounds__(kQgThreads, 1) q4g_gemm_kernel(const __grid_co
             // The whole warp runs the loop, so that its values are uniform, and one elected lane
             // issues: inside a one-lane branch every MMA's operands take detours to uniform
             // registers (58 cycles an MMA and 410 a tile, against 128 cycles of MMAs at 64 rows).
+            // That lane alone waits: after a wait that gave up it goes through the loop with the
+            // others and does nothing more.  (Votes on its waits: 37 x 14336 x 4096 f32 34.2 us, not 33.1.)
             const bool lead = elect_one();
             const uint64_t d0 = tc_sdesc128(smem_u32(stage(0)));
             const uint32_t lo0 = (uint32_t)d0, dhi = (uint32_t)(d0 >> 32);
@@ -424,15 +429,13 @@ __global__ void __launch_bounds__(kQgThreads, 1) q4g_gemm_kernel(const __grid_co
             uint32_t last_ph = 0;
             bool ok = true;
             uint32_t ready = 0;  // the next stage's barrier, tested before this tile's MMAs are issued
-            for (int u = first_unit, ui = 0; u < units && ok; u += unit_step, ++ui) {
+            for (int u = first_unit, ui = 0; u < units; u += unit_step, ++ui) {
                 const QgUnit un = place(u, ui);
                 const uint32_t idesc = tc_idesc((un.n + kUnit - 1) / kUnit * kUnit) + ((uint32_t)((CG - 1) * (kTcBW >> 4)) << 24);  // a pair: M = 256
                 const int chunk = PX == 2 ? kQgChunk : w.KS;
-                for (int c0 = un.j0; c0 < un.j1 && ok; c0 += chunk, ++cc) {
+                for (int c0 = un.j0; c0 < un.j1; c0 += chunk, ++cc) {
                     const int ab = p.nacc == 2 ? (cc & 1) : 0, use = p.nacc == 2 ? (cc >> 1) : cc;
-                    if (use > 0) ok = qg_wait(smem_u32(&acc_empty[ab]), (uint32_t)((use - 1) & 1), flags, p.err);
-                    if (!ok) break;
-                    tc_fence_after();
+                    if (lead && ok && use > 0) ok = qg_wait(smem_u32(&acc_empty[ab]), (uint32_t)((use - 1) & 1), flags, p.err);
                     const uint32_t dt = tmem + (uint32_t)(ab * p.accw);
                     const int n = min(chunk, un.j1 - c0);
                     for (int i = 0; i < n; ++i) {
@@ -440,8 +443,7 @@ __global__ void __launch_bounds__(kQgThreads, 1) q4g_gemm_kernel(const __grid_co
                         const uint32_t ph = g.ph;
                         g.next(p.nstage);
                         const uint32_t next = mbar_test(smem_u32(&full[g.s]), g.ph);
-                        if (!(ok = qg_wait(smem_u32(&x_full[gx.s]), gx.ph, flags, p.err))) break;
-                        if (!ready && !(ok = qg_wait(smem_u32(&full[s]), ph, flags, p.err))) break;
+                        if (lead && ok) ok = qg_wait(smem_u32(&x_full[gx.s]), gx.ph, flags, p.err) && (ready || qg_wait(smem_u32(&full[s]), ph, flags, p.err));
                         const int sx = gx.s;
                         gx.next(p.nx);
                         ready = next;
@@ -449,7 +451,7 @@ __global__ void __launch_bounds__(kQgThreads, 1) q4g_gemm_kernel(const __grid_co
                         const uint32_t x0 = lo0 + (uint32_t)((sx * 2 * PX * half) >> 4), a0 = tmem + (uint32_t)(p.nacc * p.accw + 64 * PA * s);
                         const int nh = halves(c0 + i);
                         __syncwarp();
-                        if (lead) {
+                        if (lead && ok) {
                             // the small products first, while the accumulator is small: adding to it truncates
                             constexpr int kPasses = PA + PX - 1;  // weights, activations: hi lo, lo hi, hi hi (one piece: hi)
 #pragma unroll
@@ -466,12 +468,11 @@ __global__ void __launch_bounds__(kQgThreads, 1) q4g_gemm_kernel(const __grid_co
                             }
                             qg_commit<CG>(smem_u32(&empty[s]));
                             qg_commit<CG>(smem_u32(&x_empty[sx]));
+                            last = s;
+                            last_ph = ph;
                         }
-                        last = s;
-                        last_ph = ph;
                     }
-                    if (!ok) break;
-                    if (lead) qg_commit<CG>(smem_u32(&acc_full[ab]));
+                    if (lead && ok) qg_commit<CG>(smem_u32(&acc_full[ab]));
                 }
             }
             // the last commits must land before tensor memory is released
@@ -482,10 +483,13 @@ __global__ void __launch_bounds__(kQgThreads, 1) q4g_gemm_kernel(const __grid_co
         if (lane == 0) {
             QgRing r;
             bool ok = true, wrapped = false;
+            int left = p.stall - 1;
             for (int u = first_unit, ui = 0; u < units && ok; u += unit_step, ++ui) {
                 const QgUnit un = place(u, ui);
                 for (int j = un.j0; j < un.j1; ++j) {
-                    if (!(ok = qg_wait(smem_u32(&r_empty[r.s]), r.ph ^ 1u, flags, p.err))) break;
+                    // injected stall: this block's raw weights end here
+                    if (p.stall && blockIdx.x == p.stall_block && --left < 0) ok = false;
+                    if (!ok || !(ok = qg_wait(smem_u32(&r_empty[r.s]), r.ph ^ 1u, flags, p.err))) break;
                     const uint32_t bar = smem_u32(&r_full[r.s]);
                     mbar_arrive_tx(bar, (uint32_t)(8 * seg_bytes));
                     tma_2d(smem_u32(raw(r.s)), &tw, j * (seg_bytes / 8), un.e * w.RB + 8 * un.nt, bar);
@@ -538,7 +542,7 @@ __global__ void __launch_bounds__(kQgThreads, 1) q4g_gemm_kernel(const __grid_co
             cp_async_wait<0>();
             __syncwarp();
             if (lane == 0) mbar_arrive(smem_u32(&tab_full[ui & 1]));
-            if (!(ok = qg_wait(smem_u32(&tab_full[ui & 1]), (uint32_t)(ui >> 1) & 1u, flags, p.err))) break;
+            if (!(ok = qg_wait_warp(smem_u32(&tab_full[ui & 1]), (uint32_t)(ui >> 1) & 1u, false, flags, p.err))) break;
             __syncwarp();
             if (u + unit_step < units) {
                 un_next = place(u + unit_step, ui + 1);
@@ -607,7 +611,7 @@ __global__ void __launch_bounds__(kQgThreads, 1) q4g_gemm_kernel(const __grid_co
             float sum[kSums][kCols];
             for (int c0 = un.j0; c0 < un.j1; c0 += chunk, ++cc) {
                 const int ab = p.nacc == 2 ? (cc & 1) : 0, use = p.nacc == 2 ? (cc >> 1) : cc;
-                if (!(ok = qg_wait(smem_u32(&acc_full[ab]), (uint32_t)(use & 1), flags, p.err))) break;
+                if (!(ok = qg_wait_warp(smem_u32(&acc_full[ab]), (uint32_t)(use & 1), false, flags, p.err))) break;
                 tc_fence_after();
                 __syncwarp();
                 const uint32_t acol = tmem + tq + (uint32_t)(ab * p.accw);
@@ -704,7 +708,7 @@ __global__ void __launch_bounds__(kQgThreads, 1) q4g_gemm_kernel(const __grid_co
                 g.next(p.nstage);
                 r.next(p.nraw);
                 if (turn != grp) continue;
-                if (!r_ready && !(ok = qg_wait(smem_u32(&r_full[ar.s]), ar.ph, flags, p.err))) break;
+                if (!(ok = qg_wait_warp(smem_u32(&r_full[ar.s]), ar.ph, r_ready, flags, p.err))) break;
                 // tested here, needed after the conversion
                 const uint32_t e_ready = mbar_test(smem_u32(&empty[at.s]), at.ph ^ 1u);
                 const uint8_t* seg = raw(ar.s) + (2 * q + hh) * seg_bytes;
@@ -718,7 +722,7 @@ __global__ void __launch_bounds__(kQgThreads, 1) q4g_gemm_kernel(const __grid_co
                 uint4 codes = reinterpret_cast<const uint4*>(seg)[lane];
                 qg_convert<PA, NG, kWords>(seg, codes, 0, 0, lane, magic, m0, m1, gc, hi, lo);
                 announce();
-                if (!e_ready && !(ok = qg_wait(smem_u32(&empty[at.s]), at.ph ^ 1u, flags, p.err))) break;
+                if (!(ok = qg_wait_warp(smem_u32(&empty[at.s]), at.ph ^ 1u, e_ready, flags, p.err))) break;
                 QgRing rn = r;  // this group's next raw stage
                 rn.skip(kQgGroups - 1, p.nraw);
                 r_ready = mbar_test(smem_u32(&r_full[rn.s]), rn.ph);
@@ -745,7 +749,16 @@ __global__ void __launch_bounds__(kQgThreads, 1) q4g_gemm_kernel(const __grid_co
     }
     tc_fence_before();
     __syncthreads();
-    if (CG == 2) cluster_sync();  // neither block leaves while the other's MMAs, copies or arrivals may reach it
+    if (CG == 2) {
+        // After a wait that gave up, rank 1's last copies, which complete on rank 0's barriers, may be
+        // ones that rank 0 never counted: both blocks stay for many times a copy's duration.
+        if (flags[0]) {
+            const long long t0 = clock64();
+            while (clock64() - t0 < kQgQuiet) __nanosleep(1000);
+            __syncwarp();
+        }
+        cluster_sync();  // neither block leaves while the other's MMAs, copies or arrivals may reach it
+    }
     if (warp == 1) {
         tc_fence_after();
         if (CG == 1) asm volatile("tcgen05.dealloc.cta_group::1.sync.aligned.b32 %0, %1;" ::"r"(tmem), "n"(kTcTmemCols) : "memory");

@@ -65,7 +65,8 @@ struct QgGemmPlan {
     size_t smem = 0, ws_x = 0, ws_xs = 0, ws_part = 0, workspace = 0;
 };
 QgGemmPlan plan_q4g_gemm(const QgCall& c, int sms, int smem_max);
-cudaError_t launch_q4g_gemm(const QgGemmPlan& pl, const QgCall& c, void* ws, unsigned* err, int smem_max, cudaStream_t s);
+// stall: 0, or (test hook) one more than the tiles of raw weights that one block copies
+cudaError_t launch_q4g_gemm(const QgGemmPlan& pl, const QgCall& c, void* ws, unsigned* err, int stall, int smem_max, cudaStream_t s);
 
 // y [T, N] = sum_j weight[t][j] part[t top_k + j], in the order of j
 cudaError_t launch_q4g_combine(const float* part, const QgRoute& r, int E, int N, void* y, int xt, cudaStream_t s);

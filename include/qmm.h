@@ -380,15 +380,18 @@ qmm_status qmm_moe_down(const qmm_q4g* w, qmm_float xtype, const void* h, int64_
    the library's failure paths can be exercised without faulting a GPU.)
    qmm_test_inject arms an injected failure, consumed by the next `count`
    calls that reach it; QMM_INJECT_OFF disarms every kind.
-   - QMM_INJECT_LAUNCH_FAILURE: qmm_matmul / qmm_block_sums return
-     QMM_ERR_CUDA at once, as if the launch had failed, without any CUDA call
+   - QMM_INJECT_LAUNCH_FAILURE: qmm_matmul, qmm_block_sums, qmm_q4g_matmul,
+     qmm_moe_route, qmm_moe_gate_up and qmm_moe_down return QMM_ERR_CUDA at once, as if the launch had failed, without any CUDA call
      (the outputs are not touched).
    - QMM_INJECT_STALL: the next decode-kernel launch (qmm_dmma_kernel, the
      M <= 16 warp-MMA path) issues no weight stage from stage `arg` on in its
      first block, so that block's consumers wait in vain: their bounded wait
      gives up, the block drains the copies it did issue and exits, and
      qmm_last_device_error then reports QMM_ERR_TIMEOUT.  The call's output
-     is undefined; later calls are unaffected.
+     is undefined; later calls are unaffected.  The next launch of the 4-bit
+     GEMM stalls in the same way: one block (of its pairs, where it works in
+     pairs, the second of the first) copies `arg` tiles of its weights and no
+     more.  Whichever of the two is launched first takes the injection.
    qmm_test_set_wait_limit sets the bounded waits' spin limit on the current
    device to 2^log2_clocks SM clocks (16..31; 0 restores the default 2^31,
    about one second), so that an injected stall ends in milliseconds.  It
