@@ -74,15 +74,21 @@ at::Tensor output(PyObject* o, at::IntArrayRef sizes, const at::Tensor& x) {
     return t;
 }
 
-// a caller's workspace as it is (the library checks its size), else a new one
+// a caller's workspace (the library checks its size and alignment; its bytes have to be one piece of
+// this device's memory), else a new one
 struct Workspace {
     at::Tensor t;
     void* p = nullptr;
     size_t n = 0;
     Workspace(PyObject* o, size_t size, const at::Tensor& like) {
-        if (o != Py_None) t = tensor(o, "workspace is a tensor");
-        else if (size) t = empty({(int64_t)size}, at::kByte, like.device());
-        else return;
+        if (o != Py_None) {
+            t = tensor(o, "workspace is a tensor");
+            need(t.is_cuda() && t.device() == like.device() && t.is_contiguous(), "workspace is a contiguous tensor on the activations' device");
+        } else if (size) {
+            t = empty({(int64_t)size}, at::kByte, like.device());
+        } else {
+            return;
+        }
         p = t.data_ptr();
         n = t.nbytes();
     }

@@ -34,3 +34,49 @@ def test_route_order_of_uneven_tiles(q, T, E, k):
     order = np.argsort(flat, kind="stable")
     assert np.array_equal(r.order.cpu().numpy(), order)
     assert np.array_equal(r.offsets.cpu().numpy(), np.searchsorted(flat[order], np.arange(E + 1)))
+
+
+# ------------------------------------------------------------------ what a caller hands over
+
+
+def make(E, N, K, G, zeros, sdt, seed, scale=0.01):
+    """Checkpoint tensors on the CPU, and the weights in 64 bits."""
+    g = rng(seed)
+    q4 = torch.randint(0, 16, (E, N, K), generator=g)
+    s = (scale * (0.25 + torch.rand((E, N, K // G), generator=g))).to(sdt)
+    z = torch.randint(0, 16, (E, N, K // G), generator=g) if zeros else None
+    zd = 8.0 if z is None else z.double().repeat_interleave(G, 2)
+    w = s.double().repeat_interleave(G, 2) * (q4.double() - zd)
+    codes = (q4[..., 0::2] | (q4[..., 1::2] << 4)).to(torch.uint8)
+    return codes, s, None if z is None else z.to(torch.uint8), w
+
+
+def pack(q, t, gate_up=False):
+    codes, s, z, _ = t
+    return q.q4g_pack(codes.cuda(), s.cuda(), None if z is None else z.cuda(), gate_up=gate_up)
+
+
+def test_refused_workspaces(q):
+    """Memory of the host, and views whose bytes are not one piece: refused before any launch."""
+    T, E, k, F = 600, 4, 2, 64
+    x = torch.zeros((T, 128), dtype=torch.bfloat16, device="cuda")
+    h = torch.zeros((T, k, F), dtype=torch.bfloat16, device="cuda")
+    logits = torch.zeros((T, E), device="cuda")
+    wm = pack(q, make(1, 5000, 128, 64, True, torch.float16, 4))
+    wg, wd = pack(q, make(E, 2 * F, 128, 64, True, torch.float16, 4), True), pack(q, make(E, 128, F, 64, True, torch.float16, 4))
+    r = q.moe_route(logits, k)
+    calls = (lambda ws: q.q4g_matmul(wm, x, workspace=ws), lambda ws: q.moe_route(logits, k, workspace=ws),
+             lambda ws: q.moe_gate_up(wg, x, r, workspace=ws), lambda ws: q.moe_down(wd, h, r, workspace=ws))
+    n = 1 << 22  # bytes, enough for each of them
+    good = torch.empty(n, dtype=torch.uint8, device="cuda")
+    for bad in (torch.empty(n, dtype=torch.uint8), torch.empty((n, 2), dtype=torch.uint8, device="cuda")[:, 0],
+                torch.empty(1, dtype=torch.uint8, device="cuda").expand(n), torch.empty((16, n // 16), dtype=torch.uint8, device="cuda").t(),
+                good.tolist()[:3]):
+        for f in calls:
+            with pytest.raises(ValueError):
+                f(bad)
+    for f in calls:
+        a, b = f(None), f(good)
+        for u, v in zip(a, b) if isinstance(a, tuple) else ((a, b),):
+            assert torch.equal(u, v)
+        assert torch.equal(f(good.view(torch.float32))[0], f(None)[0])
