@@ -100,11 +100,19 @@ def _raw_stream(device: int) -> int:
     return torch.cuda.current_stream(device).cuda_stream
 
 
-def _on(stream):
-    """The context in which a call with stream=... allocates and launches."""
-    if stream is None:
-        return contextlib.nullcontext()
-    return torch.cuda.stream(stream if isinstance(stream, torch.cuda.Stream) else torch.cuda.ExternalStream(int(stream)))
+@contextlib.contextmanager
+def _on(device: int, stream):
+    """Where a call allocates and launches: the device of its tensors, and there `stream` (a torch stream or a raw
+    handle of that device) or the current one."""
+    with torch.cuda.device(device):
+        if stream is None:
+            yield
+            return
+        if not isinstance(stream, torch.cuda.Stream):
+            stream = torch.cuda.ExternalStream(int(getattr(stream, "cuda_stream", stream)), device=device)
+        _need(stream.device.index == device, "stream is one of the tensors' device")
+        with torch.cuda.stream(stream):
+            yield
 
 
 def _need(ok: bool, text: str) -> None:
@@ -156,7 +164,7 @@ def q4g_pack(codes: torch.Tensor, scales: torch.Tensor, zeros: torch.Tensor | No
     _need(codes.is_cuda and scales.get_device() == codes.get_device() and (zeros is None or zeros.get_device() == codes.get_device()),
           "tensors are on one CUDA device")
     group = K // groups
-    with _on(stream):
+    with _on(codes.get_device(), stream):
         codes, scales = codes.contiguous(), scales.contiguous()
         zeros = None if zeros is None else zeros.contiguous()
         out = _laid_out(E, N, K, group, gate_up, codes.device)
@@ -172,14 +180,14 @@ def q4g_pack_q4_0(wq: torch.Tensor, K: int, gate_up: bool = False, stream=None) 
     _need(wq.dim() == 3 and wq.dtype == torch.uint8 and wq.is_cuda and wq.is_contiguous() and K % 32 == 0 and wq.shape[2] == K // 32 * 18,
           "wq is contiguous uint8 [.., N, K / 32 * 18]")
     E, N = wq.shape[:2]
-    with _on(stream):
+    with _on(wq.get_device(), stream):
         out = _laid_out(E, N, K, 32, gate_up, wq.device)
         _check(_lib().qmm_q4g_pack_q4_0(wq.data_ptr(), E, N, K, int(gate_up), out.data_ptr(), _raw_stream(wq.get_device())), "qmm_q4g_pack_q4_0")
     return Q4GWeights(out, E, N, K, 32, gate_up)
 
 
 def q4g_dequantize(w: Q4GWeights, out: torch.Tensor | None = None, stream=None) -> torch.Tensor:
-    with _on(stream):
+    with _on(w.device, stream):
         if out is None:
             out = torch.empty((w.experts, w.N, w.K), dtype=torch.float32, device=w.data.device)
         _need(out.dtype == torch.float32 and out.is_contiguous() and out.numel() == w.experts * w.N * w.K and out.get_device() == w.device,
@@ -192,7 +200,7 @@ def q4g_matmul(w: Q4GWeights, x: torch.Tensor, out: torch.Tensor | None = None, 
                stream=None) -> torch.Tensor:
     """y [M, N] = x [M, K] . W^T (one weight matrix)."""
     if stream is not None:
-        with _on(stream):
+        with _on(w.device, stream):
             return q4g_matmul(w, x, out, workspace)
     y = _binding.matmul(w._ptr, w.device, x, out, workspace)
     if type(y) is int:
@@ -201,7 +209,8 @@ def q4g_matmul(w: Q4GWeights, x: torch.Tensor, out: torch.Tensor | None = None, 
 
 
 def q4g_matmul_workspace(w: Q4GWeights, dtype: torch.dtype, M: int) -> int:
-    return int(_lib().qmm_q4g_matmul_workspace(w._ptr, FLOATS[dtype], M))
+    with torch.cuda.device(w.device):  # a plan depends on its device
+        return int(_lib().qmm_q4g_matmul_workspace(w._ptr, FLOATS[dtype], M))
 
 
 def moe_route(logits: torch.Tensor, top_k: int, score: str = "softmax", bias: torch.Tensor | None = None, groups: int = 1,
@@ -212,7 +221,7 @@ def moe_route(logits: torch.Tensor, top_k: int, score: str = "softmax", bias: to
     leaves the sorted slots (offsets, order) out.  The tensors share one
     allocation."""
     if stream is not None:
-        with _on(stream):
+        with _on(logits.get_device(), stream):
             return moe_route(logits, top_k, score, bias, groups, top_groups, group_score, renorm, scale, order, workspace)
     r = _binding.route(logits, bias, top_k, SCORES[score], groups, top_groups, GROUP_SCORES[group_score], renorm, scale, order, workspace)
     if type(r) is int:
@@ -224,7 +233,7 @@ def moe_gate_up(w: Q4GWeights, x: torch.Tensor, route: Route, out: torch.Tensor 
                 workspace: torch.Tensor | None = None, stream=None) -> torch.Tensor:
     """h [T, top_k, F] of x [T, K]; w packed with gate_up=True, N = 2 F."""
     if stream is not None:
-        with _on(stream):
+        with _on(w.device, stream):
             return moe_gate_up(w, x, route, out, workspace)
     h = _binding.gate_up(w._ptr, w.device, x, *route, out, workspace)
     if type(h) is int:
@@ -236,7 +245,7 @@ def moe_down(w: Q4GWeights, h: torch.Tensor, route: Route, out: torch.Tensor | N
              workspace: torch.Tensor | None = None, stream=None) -> torch.Tensor:
     """y [T, N] of h [T, top_k, K] and the route's weights."""
     if stream is not None:
-        with _on(stream):
+        with _on(w.device, stream):
             return moe_down(w, h, route, out, workspace)
     y = _binding.down(w._ptr, w.device, h, *route, out, workspace)
     if type(y) is int:
