@@ -54,6 +54,17 @@ at::Tensor part(const at::Tensor& buffer, int64_t at, at::IntArrayRef sizes, at:
     return v;
 }
 
+// the weights that `o` describes, at where their tensor's data is now; the tensor's device
+qmm_q4g weights(PyObject* o, PyObject* data, int64_t& device) {
+    qmm_q4g w = *reinterpret_cast<const qmm_q4g*>(integer(o));
+    const at::Tensor& t = tensor(data, "laid-out weights are a tensor");
+    need(t.is_cuda() && t.is_contiguous() && t.nbytes() >= qmm_q4g_bytes(w.experts, w.N, w.K, w.group, w.paired),
+         "the weights are on a CUDA device, whole");
+    device = t.get_device();
+    w.data = t.data_ptr();
+    return w;
+}
+
 // type and row distance (elements) of activations [.., K]: rows contiguous and evenly apart
 void activations(const qmm_q4g& w, int64_t device, const at::Tensor& x, int64_t dims, qmm_float& xt, int64_t& ld) {
     need(x.is_cuda() && x.get_device() == device && x.dim() == dims && x.size(dims - 1) == w.K && float_type(x.scalar_type(), xt),
@@ -111,12 +122,12 @@ PyObject* guarded(F f) {
     END_HANDLE_TH_ERRORS
 }
 
-// (weights, device, x, out, workspace)
+// (weights, their data, x, out, workspace)
 PyObject* matmul(PyObject*, PyObject* const* a, Py_ssize_t n) {
     return guarded([&]() -> PyObject* {
         need(n == 5, "matmul takes 5 arguments");
-        const qmm_q4g& w = *reinterpret_cast<const qmm_q4g*>(integer(a[0]));
-        const int64_t device = integer(a[1]);
+        int64_t device;
+        const qmm_q4g w = weights(a[0], a[1], device);
         const at::Tensor& x = tensor(a[2], "x is a tensor");
         qmm_float xt;
         int64_t ld;
@@ -133,13 +144,13 @@ bool index_tensor(const at::Tensor& t, int64_t device) {
     return t.is_cuda() && t.get_device() == device && t.scalar_type() == at::kInt && t.is_contiguous();
 }
 
-// (weights, device, x, ids, route weights, offsets, order, out, workspace)
+// (weights, their data, x, ids, route weights, offsets, order, out, workspace)
 template <bool DOWN>
 PyObject* experts(PyObject*, PyObject* const* a, Py_ssize_t n) {
     return guarded([&]() -> PyObject* {
         need(n == 9, "9 arguments");
-        const qmm_q4g& w = *reinterpret_cast<const qmm_q4g*>(integer(a[0]));
-        const int64_t device = integer(a[1]);
+        int64_t device;
+        const qmm_q4g w = weights(a[0], a[1], device);
         const at::Tensor& x = tensor(a[2], "activations are a tensor");
         qmm_float xt;
         int64_t ld;

@@ -121,13 +121,43 @@ def _need(ok: bool, text: str) -> None:
 
 
 class Q4GWeights:
-    """Laid-out weights: `data` (uint8) and what they are.  Made by q4g_pack or q4g_pack_q4_0."""
+    """Laid-out weights: `data` (uint8, qmm_q4g_bytes bytes) and what they are.  Made by q4g_pack or q4g_pack_q4_0, or
+    from such data that a program kept.  Can be copied, pickled and saved; `data` may be set anew (moved, reloaded), on
+    the CPU too, where it only waits to be moved.  What the weights are does not change."""
 
     def __init__(self, data: torch.Tensor, experts: int, N: int, K: int, group: int, gate_up: bool):
-        self.data, self.experts, self.N, self.K, self.group, self.gate_up = data, experts, N, K, group, gate_up
-        self.device = data.get_device()
-        self._desc = _Desc(data.data_ptr(), experts, N, K, group, int(gate_up))
+        self._desc = _Desc(0, experts, N, K, group, int(bool(gate_up)))
         self._ptr = ctypes.addressof(self._desc)
+        n = int(_lib().qmm_q4g_bytes(experts, N, K, group, int(bool(gate_up))))
+        _need(n > 0 or N == 0, "experts, N, K and group are a shape that q4g_pack takes")
+        self._bytes = n
+        self.data = data
+
+    experts = property(lambda self: self._desc.experts)
+    N = property(lambda self: self._desc.N)
+    K = property(lambda self: self._desc.K)
+    group = property(lambda self: self._desc.group)
+    gate_up = property(lambda self: bool(self._desc.paired))
+    device = property(lambda self: self._data.get_device(), doc="index of the CUDA device, -1 on the CPU")
+
+    @property
+    def data(self) -> torch.Tensor:
+        return self._data
+
+    @data.setter
+    def data(self, t: torch.Tensor) -> None:
+        _need(t.dtype == torch.uint8 and t.is_contiguous() and t.numel() == self._bytes and t.data_ptr() % 16 == 0,
+              "laid-out weights are qmm_q4g_bytes contiguous bytes (uint8) from a 16-byte boundary on")
+        self._data = t
+
+    def _descriptor(self) -> int:
+        """Address of the qmm_q4g, at where the data is now."""
+        _need(self._data.is_cuda and self._data.numel() == self._bytes, "the weights are on a CUDA device")
+        self._desc.data = self._data.data_ptr()
+        return self._ptr
+
+    def __reduce__(self):
+        return Q4GWeights, (self._data, self.experts, self.N, self.K, self.group, self.gate_up)
 
 
 class Route(NamedTuple):
@@ -192,7 +222,7 @@ def q4g_dequantize(w: Q4GWeights, out: torch.Tensor | None = None, stream=None) 
             out = torch.empty((w.experts, w.N, w.K), dtype=torch.float32, device=w.data.device)
         _need(out.dtype == torch.float32 and out.is_contiguous() and out.numel() == w.experts * w.N * w.K and out.get_device() == w.device,
               "out is contiguous f32 [experts, N, K] on the weights' device")
-        _check(_lib().qmm_q4g_dequantize(w._ptr, out.data_ptr(), _raw_stream(w.device)), "qmm_q4g_dequantize")
+        _check(_lib().qmm_q4g_dequantize(w._descriptor(), out.data_ptr(), _raw_stream(w.device)), "qmm_q4g_dequantize")
     return out
 
 
@@ -202,7 +232,7 @@ def q4g_matmul(w: Q4GWeights, x: torch.Tensor, out: torch.Tensor | None = None, 
     if stream is not None:
         with _on(w.device, stream):
             return q4g_matmul(w, x, out, workspace)
-    y = _binding.matmul(w._ptr, w.device, x, out, workspace)
+    y = _binding.matmul(w._ptr, w._data, x, out, workspace)
     if type(y) is int:
         _check(y, "qmm_q4g_matmul")
     return y
@@ -210,7 +240,7 @@ def q4g_matmul(w: Q4GWeights, x: torch.Tensor, out: torch.Tensor | None = None, 
 
 def q4g_matmul_workspace(w: Q4GWeights, dtype: torch.dtype, M: int) -> int:
     with torch.cuda.device(w.device):  # a plan depends on its device
-        return int(_lib().qmm_q4g_matmul_workspace(w._ptr, FLOATS[dtype], M))
+        return int(_lib().qmm_q4g_matmul_workspace(w._descriptor(), FLOATS[dtype], M))
 
 
 def moe_route(logits: torch.Tensor, top_k: int, score: str = "softmax", bias: torch.Tensor | None = None, groups: int = 1,
@@ -235,7 +265,7 @@ def moe_gate_up(w: Q4GWeights, x: torch.Tensor, route: Route, out: torch.Tensor 
     if stream is not None:
         with _on(w.device, stream):
             return moe_gate_up(w, x, route, out, workspace)
-    h = _binding.gate_up(w._ptr, w.device, x, *route, out, workspace)
+    h = _binding.gate_up(w._ptr, w._data, x, *route, out, workspace)
     if type(h) is int:
         _check(h, "qmm_moe_gate_up")
     return h
@@ -247,7 +277,7 @@ def moe_down(w: Q4GWeights, h: torch.Tensor, route: Route, out: torch.Tensor | N
     if stream is not None:
         with _on(w.device, stream):
             return moe_down(w, h, route, out, workspace)
-    y = _binding.down(w._ptr, w.device, h, *route, out, workspace)
+    y = _binding.down(w._ptr, w._data, h, *route, out, workspace)
     if type(y) is int:
         _check(y, "qmm_moe_down")
     return y

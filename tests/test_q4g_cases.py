@@ -80,3 +80,35 @@ def test_refused_workspaces(q):
         for u, v in zip(a, b) if isinstance(a, tuple) else ((a, b),):
             assert torch.equal(u, v)
         assert torch.equal(f(good.view(torch.float32))[0], f(None)[0])
+
+
+def test_weights_are_read_where_they_are_now(q):
+    """Reassigned, moved, copied and saved weights give the same products; on the CPU they are refused."""
+    import copy
+    import io
+    t = make(1, 200, 256, 64, True, torch.float16, 5)
+    x = torch.randn((300, 256), generator=rng(6)).half().cuda()
+    w = pack(q, t)
+    ref = q.q4g_matmul(w, x)
+    old = w.data
+    w.data = old.clone()
+    old.zero_()
+    assert torch.equal(q.q4g_matmul(w, x), ref) and torch.equal(q.q4g_matmul(w, x[:1]), q.q4g_matmul(pack(q, t), x[:1]))
+    kept = w.data
+    w.data.data = kept.clone()  # the storage under the same tensor
+    assert torch.equal(q.q4g_matmul(w, x), ref) and torch.equal(q.q4g_dequantize(w).double().cpu(), t[3])
+    c = copy.deepcopy(w)
+    w.data.zero_()
+    assert torch.equal(q.q4g_matmul(c, x), ref)
+    f = io.BytesIO()
+    torch.save(c, f)
+    f.seek(0)
+    c = torch.load(f, weights_only=False, map_location="cpu")
+    for call in (lambda: q.q4g_matmul(c, x), lambda: q.q4g_dequantize(c), lambda: q.q4g_matmul_workspace(c, torch.float16, 9)):
+        with pytest.raises(ValueError):
+            call()
+    c.data = c.data.cuda()
+    assert torch.equal(q.q4g_matmul(c, x), ref)
+    c.data.resize_(16)  # no longer whole
+    with pytest.raises(ValueError):
+        q.q4g_matmul(c, x)

@@ -2,6 +2,8 @@
 and stream a call is made on.  The library, torch's device and stream contexts
 and CUDA tensors are stand-ins."""
 import contextlib
+import copy
+import pickle
 
 import pytest
 
@@ -65,7 +67,8 @@ class World:
 
     def __getattr__(self, name):  # an entry point of the library
         def call(*args):
-            self.calls.append((name, self.device, args[-1]))
+            if name != "qmm_q4g_bytes":  # arithmetic, wherever it is made
+                self.calls.append((name, self.device, args[-1]))
             return 4096 if name.endswith("bytes") or name.endswith("workspace") else 0
         return call
 
@@ -129,3 +132,60 @@ def test_another_devices_stream_is_refused(m, world):
         with pytest.raises(ValueError):
             f(FakeStream(5, 0))
     assert len(world.calls) == n
+
+
+# ------------------------------------------------------------------ laid-out weights as an object
+
+
+def laid_out(m, E=2, N=40, K=192, group=64, gate_up=True):
+    n = m._lib().qmm_q4g_bytes(E, N, K, group, int(gate_up))
+    return m.Q4GWeights(torch.randint(0, 256, (n,), dtype=torch.uint8), E, N, K, group, gate_up)
+
+
+def same(a, b):
+    return torch.equal(a.data, b.data) and all(getattr(a, f) == getattr(b, f) for f in ("experts", "N", "K", "group", "gate_up"))
+
+
+def test_weights_can_be_copied_and_saved(m, tmp_path):
+    w = laid_out(m)
+    holder = torch.nn.Module()
+    holder.w = w
+    for c in (copy.deepcopy(w), pickle.loads(pickle.dumps(w)), copy.deepcopy(holder).w):
+        assert same(c, w) and c.data.data_ptr() != w.data.data_ptr() and c._ptr != w._ptr
+    assert copy.copy(w).data is w.data
+    torch.save({"w": w}, tmp_path / "w.pt")
+    assert same(torch.load(tmp_path / "w.pt", weights_only=False)["w"], w)
+    with torch.serialization.safe_globals([m.Q4GWeights]):
+        assert same(torch.load(tmp_path / "w.pt", weights_only=True)["w"], w)
+
+
+def test_weights_follow_their_data(m, monkeypatch):
+    """The descriptor that a call gets holds where the data is at that call."""
+    w = laid_out(m)
+    monkeypatch.setattr(m, "_need", lambda ok, text: None)  # the data is on the CPU here
+    seen = lambda: m._Desc.from_address(w._descriptor()).data  # noqa: E731
+    assert seen() == w.data.data_ptr()
+    w.data = w.data.clone()
+    assert seen() == w.data.data_ptr()
+    other = w.data.clone()
+    w.data.data = other  # as torch.nn.Module.to moves a parameter
+    assert seen() == other.data_ptr()
+
+
+def test_weights_refuse_other_data(m):
+    w = laid_out(m)
+    n = w.data.numel()
+    for bad in (torch.zeros(n - 1, dtype=torch.uint8), torch.zeros(n + 1, dtype=torch.uint8), torch.zeros(n, dtype=torch.int8),
+                torch.zeros((n, 2), dtype=torch.uint8)[:, 0], torch.zeros(n + 8, dtype=torch.uint8)[8:]):
+        with pytest.raises(ValueError):
+            w.data = bad
+        with pytest.raises(ValueError):
+            m.Q4GWeights(bad, 2, 40, 192, 64, True)
+    with pytest.raises(ValueError):
+        m.Q4GWeights(w.data, 2, 40, 192, 48, True)  # no such group
+    for name in ("experts", "N", "K", "group", "gate_up", "device"):
+        with pytest.raises(AttributeError):
+            setattr(w, name, 1)
+    assert w.device == -1
+    with pytest.raises(ValueError):
+        m.q4g_dequantize(w)  # not on a GPU
