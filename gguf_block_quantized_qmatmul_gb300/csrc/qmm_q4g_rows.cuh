@@ -85,9 +85,15 @@ __device__ __forceinline__ void qg_mma(float d[4], const uint32_t a[4], uint32_t
 
 // The eight codes of one word less their zero points, exact, as fragment
 // registers.  f16: 0x6400 | q is 1024 + q and 0x6400 | q << 4 is 1024 + 16 q
-// (one less shift); bf16: 0x4300 | q is 128 + q.  zl, zh: the constants of
-// rows g and g + 8 (qg_zero).
-// magic: 0x64006400 (f16) or 0x43004300 (bf16) in a register.
+// (one less shift); bf16: 0x3D80 | q is 2^-4 + q 2^-11, so that these codes are
+// (q - z) 2^-11: a group's sum of 128 products with up to 15 times an activation
+// near the end of the f32 and bf16 range stays in that range (f16 activations
+// do not reach it), and the rows' sums are multiplied by 2^11 at their end.
+// zl, zh: the constants of rows g and g + 8 (qg_zero).
+// magic: kQgMagic in a register.
+template <bool BF>
+constexpr uint32_t kQgMagic = BF ? 0x3D803D80u : 0x64006400u;
+constexpr float kQgCodeUnit = 1.0f / 2048.0f;  // what a bf16 code's unit is
 template <bool BF>
 __device__ __forceinline__ void qg_codes(uint32_t w, uint32_t magic, uint32_t zl, uint32_t zh, uint32_t a[4]) {
     if (BF) {
@@ -112,11 +118,11 @@ __device__ __forceinline__ void qg_codes(uint32_t w, uint32_t magic, uint32_t zl
         }
     }
 }
-// f16: 1024 + z for row g, -(64 + z) for row g + 8; bf16: 128 + z for both
+// f16: 1024 + z for row g, -(64 + z) for row g + 8; bf16: 2^-4 + z 2^-11 for both
 template <bool BF>
 __device__ __forceinline__ uint32_t qg_zero(uint32_t sw, bool second) {
     const uint32_t z = sw & 15u;
-    if (BF) return z * 0x00010001u | 0x43004300u;
+    if (BF) return z * 0x00010001u | kQgMagic<true>;
     return second ? (z * 0x00100010u) + 0xD400D400u : (z * 0x00010001u | 0x64006400u);
 }
 
@@ -208,7 +214,7 @@ __global__ void __launch_bounds__(qg_row_warps(NB) * 32, 1) q4g_rows_kernel(cons
     const int wk = p.wk, wr = p.wr, kw = warp & (wk - 1), rw = warp >> p.wk_log2;
     constexpr int seg_bytes = qg_seg_bytes(NG), segk = 128 / NG;
     uint8_t* ring = sm + p.off_ring + warp * (kQgDepth * seg_bytes);
-    const uint32_t magic = opaque(BF ? 0x43004300u : 0x64006400u);
+    const uint32_t magic = opaque(kQgMagic<BF>);
     if (tid == 0) *reinterpret_cast<uint4*>(sm + p.off_zero) = make_uint4(0u, 0u, 0u, 0u);  // what lanes without a column read
     grid_dep_launch();
 
@@ -480,7 +486,7 @@ __global__ void __launch_bounds__(qg_row_warps(NB) * 32, 1) q4g_rows_kernel(cons
 #pragma unroll 4
                     for (int k2 = 0; k2 < wk; ++k2) v2 += f[k2 * kRed];
                 }
-                return v2;
+                return BF ? v2 * (1.0f / kQgCodeUnit) : v2;
             };
             // the warps take turns at a short row block's sums
             for (int o = ((kw + gi) & (wk - 1)) * 32 + lane; o < rows << per_log2; o += wk * 32) {

@@ -112,3 +112,43 @@ def test_weights_are_read_where_they_are_now(q):
     c.data.resize_(16)  # no longer whole
     with pytest.raises(ValueError):
         q.q4g_matmul(c, x)
+
+
+# ------------------------------------------------------------------ magnitudes
+# Tolerances: those of test_q4g.py (u |y| + 1e-5 T, and 2^-11 T for weights that the GEMM rounds),
+# and 2^-140 for f32 sums of results near the end of the f32 range: 2^11 times the smallest f32 number,
+# which is the unit of the row kernel's sums for results that are below 2^-115.
+
+U = {torch.float32: 2.0 ** -24, torch.bfloat16: 2.0 ** -8}
+
+
+def near(y, ref, T, dt, gemm):
+    tol = U[dt] * ref.abs() + 1e-5 * T + (2.0 ** -11 * T if gemm and dt != torch.float32 else 0) + 2.0 ** -138
+    y = y.double().cpu()
+    bad = ~((y - ref).abs() <= tol)
+    assert not bad.any(), f"{int(bad.sum())} of {bad.numel()}, first {y[bad][:3]} for {ref[bad][:3]}"
+
+
+# the scales' magnitude, the activations'
+MAGNITUDES = [(1e-5, 1e37), (1e-6, 3e37), (1e-2, 1e35), (1e-25, 1e-10), (1e-20, 1e3), (1e20, 1e-30), (1e3, 1e-30)]
+
+
+@pytest.mark.parametrize("scale,xs", MAGNITUDES)
+@pytest.mark.parametrize("dt", [torch.float32, torch.bfloat16])
+@pytest.mark.parametrize("G", [32, 128])
+def test_magnitudes_of_few_rows(q, scale, xs, dt, G):
+    """Every way through the row kernel: dense, by slot, by token, by expert."""
+    E, k, K, N = 4, 2, 256, 96
+    t = make(E, N, K, G, True, torch.bfloat16, 21, scale)
+    x = (xs * torch.randn((20, k, K), generator=rng(22)).clamp(-3, 3)).to(dt)
+    xd = x.double()
+    w1 = pack(q, tuple(v if v is None else v[:1] for v in t))
+    for M in (1, 2, 9):
+        near(q.q4g_matmul(w1, x[:M, 0].cuda()), xd[:M, 0] @ t[3][0].T, xd[:M, 0].abs() @ t[3][0].abs().T, dt, False)
+    w = pack(q, t)
+    for T in (1, 16, 20):  # 40 slots of four experts: the GEMM in bf16
+        r = q.moe_route(torch.randn((T, E), generator=rng(23)).cuda(), k)
+        W = t[3][r.ids.long().cpu()]
+        wt = r.weights.double().cpu()[..., None]
+        ref, A = (wt * (W @ xd[:T, :, :, None])[..., 0]).sum(1), (wt * (W.abs() @ xd[:T, :, :, None].abs())[..., 0]).sum(1)
+        near(q.moe_down(w, x[:T].cuda(), r), ref, A, dt, T == 20)
