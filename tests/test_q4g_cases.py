@@ -152,3 +152,43 @@ def test_magnitudes_of_few_rows(q, scale, xs, dt, G):
         wt = r.weights.double().cpu()[..., None]
         ref, A = (wt * (W @ xd[:T, :, :, None])[..., 0]).sum(1), (wt * (W.abs() @ xd[:T, :, :, None].abs())[..., 0]).sum(1)
         near(q.moe_down(w, x[:T].cuda(), r), ref, A, dt, T == 20)
+
+
+SMALL_AND_LARGE = MAGNITUDES + [(1e-25, 1e-13), (1e-25, 1e-14), (1e-30, 1e-7), (1e-12, 1e-25), (1e30, 1e5), (1e37, 1e-3)]
+
+
+@pytest.mark.parametrize("scale,xs", SMALL_AND_LARGE)
+@pytest.mark.parametrize("dt", [torch.float32, torch.bfloat16])
+def test_magnitudes_of_many_rows(q, scale, xs, dt):
+    """The GEMM, dense and by expert: results down to the end of the f32 range."""
+    E, k, K, N, T = 3, 2, 256, 1000, 700
+    t = make(E, N, K, 64, True, torch.bfloat16, 24, scale)
+    x = (xs * torch.randn((T, k, K), generator=rng(25)).clamp(-3, 3)).to(dt)
+    xd = x.double()
+    w1 = pack(q, tuple(v if v is None else v[:1] for v in t))
+    near(q.q4g_matmul(w1, x[:, 0].contiguous().cuda()), xd[:, 0] @ t[3][0].T, xd[:, 0].abs() @ t[3][0].abs().T, dt, True)
+    r = q.moe_route(torch.randn((T, E), generator=rng(26)).cuda(), k)
+    ids, wt = r.ids.long().cpu(), r.weights.double().cpu()
+    ref, A = torch.zeros((T, N), dtype=torch.float64), torch.zeros((T, N), dtype=torch.float64)
+    for e in range(E):
+        a, j = torch.nonzero(ids == e, as_tuple=True)
+        ref.index_add_(0, a, wt[a, j, None] * (xd[a, j] @ t[3][e].T))
+        A.index_add_(0, a, wt[a, j, None] * (xd[a, j].abs() @ t[3][e].abs().T))
+    near(q.moe_down(pack(q, t), x.cuda(), r), ref, A, dt, True)
+
+
+@pytest.mark.parametrize("dt", [torch.float32, torch.bfloat16])
+def test_large_rows_of_weights_and_activations_that_do_not_meet(q, dt):
+    """Weights of 1e25 and activations of 1e25, where each is zero beside the other: the results are exactly zero."""
+    N, K, T = 600, 256, 500
+    codes, s, z, _ = make(1, N, K, 64, True, torch.bfloat16, 27, 1e25)
+    codes[..., :64] = 0x55  # the first 128 weights of a row are 5 - 5
+    z[..., :2] = 5
+    x = torch.zeros((T, K))
+    x[:, :128] = 1e25 * torch.randn((T, 128), generator=rng(28)).clamp(-3, 3)
+    for M in (2, T):
+        assert bool((q.q4g_matmul(pack(q, (codes, s, z, None)), x[:M].to(dt).cuda()) == 0).all())
+    w = pack(q, (codes, s, z, None), gate_up=True)
+    for M in (2, T):
+        r = q.moe_route(torch.zeros((M, 1)).cuda(), 1)
+        assert bool((q.moe_gate_up(w, x[:M].to(dt).cuda(), r) == 0).all())
