@@ -12,6 +12,7 @@
 #include <torch/csrc/Exceptions.h>
 #include <torch/csrc/autograd/python_variable.h>
 
+#include <algorithm>
 #include <stdexcept>
 
 #include "../../include/qmm.h"
@@ -41,6 +42,13 @@ int64_t integer(PyObject* o) {
     const long long v = PyLong_AsLongLong(o);
     if (v == -1 && PyErr_Occurred()) throw python_error();
     return v;
+}
+// an integer of the C ABI's 32 bits; what does not fit stays out of every valid range
+int32_t integer32(PyObject* o) { return (int32_t)std::min<int64_t>(std::max<int64_t>(integer(o), INT32_MIN), INT32_MAX); }
+bool truth(PyObject* o) {
+    const int v = PyObject_IsTrue(o);
+    if (v < 0) throw python_error();
+    return v == 1;
 }
 at::Tensor empty(at::IntArrayRef sizes, at::ScalarType t, const at::Device& d) {
     return at::detail::empty_cuda(sizes, t, d, std::nullopt);
@@ -193,17 +201,19 @@ PyObject* route(PyObject*, PyObject* const* a, Py_ssize_t n) {
             bias = b.data_ptr<float>();
         }
         qmm_route_config cfg;
-        cfg.top_k = (int32_t)integer(a[2]);
-        cfg.score = (int32_t)integer(a[3]);
-        cfg.groups = (int32_t)integer(a[4]);
-        cfg.top_groups = (int32_t)integer(a[5]);
-        cfg.group_score = (int32_t)integer(a[6]);
-        cfg.renorm = PyObject_IsTrue(a[7]) == 1;
+        cfg.top_k = integer32(a[2]);
+        cfg.score = integer32(a[3]);
+        cfg.groups = integer32(a[4]);
+        cfg.top_groups = integer32(a[5]);
+        cfg.group_score = integer32(a[6]);
+        cfg.renorm = truth(a[7]);
         cfg.scale = (float)PyFloat_AsDouble(a[8]);
         if (PyErr_Occurred()) throw python_error();
-        const bool sorted = PyObject_IsTrue(a[9]) == 1;
+        const bool sorted = truth(a[9]);
+        // what the library refuses whatever else it is given: not first the memory for it
+        if (E < 1 || E > QMM_MOE_MAX_EXPERTS || cfg.top_k < 1 || cfg.top_k > QMM_MOE_MAX_TOP_K || cfg.top_k > E) return PyLong_FromLong(QMM_ERR_SHAPE);
         const c10::cuda::CUDAGuard guard((c10::DeviceIndex)device);
-        const int64_t k = cfg.top_k > 0 ? cfg.top_k : 0;
+        const int64_t k = cfg.top_k;
         // one allocation, 16-byte steps: ids, weights, offsets, order
         const int64_t n1 = (T * k + 3) / 4 * 4, n2 = (E + 4) / 4 * 4;
         const at::Tensor all = empty({sorted ? 3 * n1 + n2 : 2 * n1}, at::kInt, l.device());

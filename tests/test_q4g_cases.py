@@ -192,3 +192,20 @@ def test_large_rows_of_weights_and_activations_that_do_not_meet(q, dt):
     for M in (2, T):
         r = q.moe_route(torch.zeros((M, 1)).cuda(), 1)
         assert bool((q.moe_gate_up(w, x[:M].to(dt).cuda(), r) == 0).all())
+
+
+def test_route_refuses_numbers_that_do_not_fit(q):
+    """Integers past 32 bits are not cut to fewer, and no memory is asked for a routing that is refused."""
+    l = torch.zeros((5, 8), device="cuda")
+    many = torch.zeros((1 << 20, 8), device="cuda")
+    for call in (lambda: q.moe_route(l, (1 << 32) + 2), lambda: q.moe_route(l, 2, groups=(1 << 32) + 1), lambda: q.moe_route(l, 2, groups=2, top_groups=(1 << 32) + 1),
+                 lambda: q.moe_route(l, -(1 << 32) + 2), lambda: q.moe_route(l, 0), lambda: q.moe_route(l, 9), lambda: q.moe_route(many, 1 << 21),
+                 lambda: q.moe_route(torch.zeros((5, 513), device="cuda"), 2), lambda: q.moe_route(l[:, :0], 1)):
+        with pytest.raises(q.QmmError) as e:
+            call()
+        assert e.value.status == 2
+    with pytest.raises(RuntimeError):  # a tensor that is neither true nor false
+        q.moe_route(l, 2, order=torch.zeros(2))
+    with pytest.raises(RuntimeError):
+        q.moe_route(l, 2, renorm=torch.zeros(2))
+    assert torch.equal(q.moe_route(l, 2).ids.cpu(), torch.tensor([[0, 1]] * 5, dtype=torch.int32))
