@@ -54,9 +54,9 @@ at::Tensor empty(at::IntArrayRef sizes, at::ScalarType t, const at::Device& d) {
     return at::detail::empty_cuda(sizes, t, d, std::nullopt);
 }
 
-// `sizes` 4-byte elements of a buffer from element `at` on, as a tensor of their own (a fifth of an allocation's time)
-at::Tensor part(const at::Tensor& buffer, int64_t at, at::IntArrayRef sizes, at::ScalarType t) {
-    at::Tensor v = at::detail::make_tensor<c10::TensorImpl>(c10::Storage(buffer.storage()), buffer.key_set(), c10::scalarTypeToTypeMeta(t));
+// `sizes` elements of a buffer from element `at` on, as a tensor of their own (a fifth of an allocation's time)
+at::Tensor part(const at::Tensor& buffer, int64_t at, at::IntArrayRef sizes) {
+    at::Tensor v = at::detail::make_tensor<c10::TensorImpl>(c10::Storage(buffer.storage()), buffer.key_set(), buffer.dtype());
     v.unsafeGetTensorImpl()->set_storage_offset(at);
     v.unsafeGetTensorImpl()->set_sizes_contiguous(sizes);
     return v;
@@ -214,14 +214,18 @@ PyObject* route(PyObject*, PyObject* const* a, Py_ssize_t n) {
         if (E < 1 || E > QMM_MOE_MAX_EXPERTS || cfg.top_k < 1 || cfg.top_k > QMM_MOE_MAX_TOP_K || cfg.top_k > E) return PyLong_FromLong(QMM_ERR_SHAPE);
         const c10::cuda::CUDAGuard guard((c10::DeviceIndex)device);
         const int64_t k = cfg.top_k;
-        // one allocation, 16-byte steps: ids, weights, offsets, order
-        const int64_t n1 = (T * k + 3) / 4 * 4, n2 = (E + 4) / 4 * 4;
-        const at::Tensor all = empty({sorted ? 3 * n1 + n2 : 2 * n1}, at::kInt, l.device());
-        const at::Tensor ids = part(all, 0, {T, k}, at::kInt), wt = part(all, n1, {T, k}, at::kFloat);
-        at::Tensor off, order;
+        // the integers are parts of one allocation, in 16-byte steps: ids, offsets, order.  The weights are not one:
+        // torch.save takes no storage that is seen as two types
+        const at::Tensor wt = empty({T, k}, at::kFloat, l.device());
+        at::Tensor ids, off, order;
         if (sorted) {
-            off = part(all, 2 * n1, {E + 1}, at::kInt);
-            order = part(all, 2 * n1 + n2, {T * k}, at::kInt);
+            const int64_t n1 = (T * k + 3) / 4 * 4, n2 = (E + 4) / 4 * 4;
+            const at::Tensor all = empty({2 * n1 + n2}, at::kInt, l.device());
+            ids = part(all, 0, {T, k});
+            off = part(all, n1, {E + 1});
+            order = part(all, n1 + n2, {T * k});
+        } else {
+            ids = empty({T, k}, at::kInt, l.device());
         }
         const Workspace ws(a[10], sorted && a[10] == Py_None ? qmm_moe_route_workspace(T, E, k) : 0, l);
         const qmm_status s = qmm_moe_route(&cfg, t, l.data_ptr(), ld, T, E, bias, ids.data_ptr<int32_t>(), wt.data_ptr<float>(),

@@ -248,8 +248,8 @@ def moe_route(logits: torch.Tensor, top_k: int, score: str = "softmax", bias: to
               workspace: torch.Tensor | None = None, stream=None) -> Route:
     """Route logits [T, experts] to top_k experts each.  bias f32 [experts] is
     added to the scores that are compared, not to the weights.  order=False
-    leaves the sorted slots (offsets, order) out.  The tensors share one
-    allocation."""
+    leaves the sorted slots (offsets, order) out.  ids, offsets and order share
+    one allocation."""
     if stream is not None:
         with _on(logits.get_device(), stream):
             return moe_route(logits, top_k, score, bias, groups, top_groups, group_score, renorm, scale, order, workspace)

@@ -209,3 +209,15 @@ def test_route_refuses_numbers_that_do_not_fit(q):
     with pytest.raises(RuntimeError):
         q.moe_route(l, 2, renorm=torch.zeros(2))
     assert torch.equal(q.moe_route(l, 2).ids.cpu(), torch.tensor([[0, 1]] * 5, dtype=torch.int32))
+
+
+def test_a_route_can_be_saved(q, tmp_path):
+    """With and without the sorted slots, as a tuple and in parts."""
+    l = torch.randn((37, 16), generator=rng(60)).cuda()
+    for order in (True, False):
+        r = q.moe_route(l, 3, order=order)
+        torch.save(tuple(r), tmp_path / "r.pt")
+        for a, b in zip(torch.load(tmp_path / "r.pt"), r):
+            assert b is None and a is None or torch.equal(a, b)
+        torch.save({"route": r._asdict()}, tmp_path / "r.pt")
+        assert torch.equal(torch.load(tmp_path / "r.pt")["route"]["weights"], r.weights)
