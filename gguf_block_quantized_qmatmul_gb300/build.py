@@ -11,6 +11,7 @@ import os
 import shutil
 import subprocess
 import sys
+import tempfile
 
 HERE = os.path.dirname(os.path.abspath(__file__))
 CSRC = os.path.join(HERE, "csrc")
@@ -38,8 +39,8 @@ def _deps():
     return out
 
 
-def _binding_command(out: str) -> list[str]:
-    """Host compiler command for the CPython extension, linked against this torch and libqmm.so."""
+def _binding_command(out: str, lib_dir: str) -> list[str]:
+    """Host compiler command for the CPython extension, linked against this torch and the libqmm.so of lib_dir."""
     import sysconfig
 
     import torch
@@ -50,7 +51,7 @@ def _binding_command(out: str) -> list[str]:
     return [os.environ.get("CXX", "g++"), "-O2", "-std=c++17", "-fPIC", "-shared", "-w",
             f"-D_GLIBCXX_USE_CXX11_ABI={int(torch.compiled_with_cxx11_abi())}", *(f"-I{i}" for i in inc),
             os.path.join(CSRC, "qmm_torch.cpp"), "-o", out, f"-L{lib}", "-lc10", "-lc10_cuda", "-ltorch_cpu", "-ltorch_cuda", "-ltorch",
-            "-ltorch_python", f"-Wl,-rpath,{lib}", f"-L{BUILD}", "-Wl,--no-as-needed", "-l:libqmm.so", "-Wl,-rpath,$ORIGIN"]
+            "-ltorch_python", f"-Wl,-rpath,{lib}", f"-L{lib_dir}", "-Wl,--no-as-needed", "-l:libqmm.so", "-Wl,-rpath,$ORIGIN"]
 
 
 def up_to_date() -> bool:
@@ -66,34 +67,34 @@ def build(force: bool = False, verbose: bool = False) -> str:
     os.makedirs(BUILD, exist_ok=True)
     nvcc = _nvcc()
     procs = []
-    for u in UNITS:
-        obj = os.path.join(BUILD, u + ".o")
-        log = open(os.path.join(BUILD, u + ".ptxas.txt"), "w")
-        cmd = [nvcc, *ARCH, *FLAGS, "-c", os.path.join(CSRC, u + ".cu"), "-o", obj]
-        procs.append((u, subprocess.Popen(cmd, stdout=log, stderr=subprocess.STDOUT), log))
-    # the extension needs libqmm.so's name only: it is linked against an empty one while that compiles
-    tmp_b = BINDING + f".tmp{os.getpid()}"
-    stub = not os.path.exists(LIB)
-    if stub:
-        subprocess.run([os.environ.get("CXX", "g++"), "-shared", "-fPIC", "-x", "c++", "/dev/null", "-o", LIB], check=True)
-    log = open(os.path.join(BUILD, "qmm_torch.ptxas.txt"), "w")
-    procs.append(("qmm_torch", subprocess.Popen(_binding_command(tmp_b), stdout=log, stderr=subprocess.STDOUT), log))
-    failed = []
-    for u, p, log in procs:
-        p.wait()
-        log.close()
-        if p.returncode != 0:
-            failed.append(u)
-    if stub:
-        os.remove(LIB)
-    if failed:
-        msgs = "".join(open(os.path.join(BUILD, u + ".ptxas.txt")).read()[-4000:] for u in failed)
-        raise RuntimeError(f"nvcc failed for {failed}:\n{msgs}")
-    tmp = LIB + f".tmp{os.getpid()}"
-    cmd = [nvcc, *ARCH, "-shared", "-o", tmp] + [os.path.join(BUILD, u + ".o") for u in UNITS]
-    subprocess.run(cmd, check=True)
-    os.replace(tmp, LIB)
-    os.replace(tmp_b, BINDING)
+    # Libraries are made in a folder of their own and moved to their places when all are whole: what other processes
+    # load, and what up_to_date() sees, is the last build's or this one's.
+    with tempfile.TemporaryDirectory(prefix="link.", dir=BUILD) as tmp:
+        try:
+            for u in UNITS:
+                obj = os.path.join(tmp, u + ".o")
+                log = open(os.path.join(BUILD, u + ".ptxas.txt"), "w")
+                cmd = [nvcc, *ARCH, *FLAGS, "-c", os.path.join(CSRC, u + ".cu"), "-o", obj]
+                procs.append((u, subprocess.Popen(cmd, stdout=log, stderr=subprocess.STDOUT), log))
+            # the extension needs libqmm.so's name only: it is linked against an empty one while that compiles
+            stub, binding, lib = os.path.join(tmp, "stub"), os.path.join(tmp, "binding.so"), os.path.join(tmp, "lib.so")
+            os.mkdir(stub)
+            subprocess.run([os.environ.get("CXX", "g++"), "-shared", "-fPIC", "-x", "c++", "/dev/null", "-o", os.path.join(stub, "libqmm.so")], check=True)
+            log = open(os.path.join(BUILD, "qmm_torch.ptxas.txt"), "w")
+            procs.append(("qmm_torch", subprocess.Popen(_binding_command(binding, stub), stdout=log, stderr=subprocess.STDOUT), log))
+            failed = [u for u, p, _ in procs if p.wait() != 0]
+        finally:
+            for _, p, log in procs:
+                if p.poll() is None:
+                    p.kill()
+                    p.wait()
+                log.close()
+        if failed:
+            msgs = "".join(open(os.path.join(BUILD, u + ".ptxas.txt")).read()[-4000:] for u in failed)
+            raise RuntimeError(f"nvcc failed for {failed}:\n{msgs}")
+        subprocess.run([nvcc, *ARCH, "-shared", "-o", lib] + [os.path.join(tmp, u + ".o") for u in UNITS], check=True)
+        os.replace(lib, LIB)
+        os.replace(binding, BINDING)
     for f in (LIB, BINDING):
         os.utime(f)
     if verbose:
