@@ -221,3 +221,80 @@ def test_a_route_can_be_saved(q, tmp_path):
             assert b is None and a is None or torch.equal(a, b)
         torch.save({"route": r._asdict()}, tmp_path / "r.pt")
         assert torch.equal(torch.load(tmp_path / "r.pt")["route"]["weights"], r.weights)
+
+
+# ------------------------------------------------------------------ sizes at which a kernel takes another way
+
+
+@pytest.mark.parametrize("M", [9, 10, 11, 12])
+@pytest.mark.parametrize("dt", [torch.float16, torch.bfloat16])
+def test_nine_to_twelve_rows_round_no_weight(q, dt, M):
+    """Over a matrix that takes the row kernel one pass (where it would take two, as of 5000 x 4096, the GEMM is used)."""
+    N, K = 9000, 2048
+    t = make(1, N, K, 64, True, torch.float16, 31)
+    x = torch.randn((M, K), generator=rng(32)).to(dt)
+    y = q.q4g_matmul(pack(q, t), x.cuda()).double().cpu()
+    ref, T = x.double() @ t[3][0].T, x.double().abs() @ t[3][0].abs().T
+    u = 2.0 ** -11 if dt == torch.float16 else 2.0 ** -8
+    assert bool(((y - ref).abs() <= u * ref.abs() + 1e-5 * T).all())
+
+
+@pytest.mark.parametrize("dt,top_k", [("f32", 8), ("f32", 32), ("f16", 7), ("f16", 17), ("f16", 32), ("bf16", 31), ("bf16", 32)])
+@pytest.mark.parametrize("T", [1, 4])
+def test_down_of_a_token_with_many_experts(q, dt, top_k, T):
+    """A token's experts end to end (f32: as far as their activations fit)."""
+    E, K, N = 40, 96 if dt == "f32" else 352, 75
+    dt = {"f32": torch.float32, "f16": torch.float16, "bf16": torch.bfloat16}[dt]
+    t = make(E, N, K, 32, True, torch.float16, 33)
+    h = torch.randn((T, top_k, K), generator=rng(34)).to(dt)
+    r = q.moe_route(torch.randn((T, E), generator=rng(35)).cuda(), top_k)
+    y = q.moe_down(pack(q, t), h.cuda(), r).double().cpu()
+    W, wt = t[3][r.ids.long().cpu()], r.weights.double().cpu()[..., None]
+    ref, A = (wt * (W @ h.double()[..., None])[..., 0]).sum(1), (wt * (W.abs() @ h.double().abs()[..., None])[..., 0]).sum(1)
+    u = {torch.float32: 2.0 ** -24, torch.float16: 2.0 ** -11, torch.bfloat16: 2.0 ** -8}[dt]
+    assert bool(((y - ref).abs() <= u * ref.abs() + 1e-5 * A).all())
+
+
+@pytest.mark.parametrize("dt", [torch.float16, torch.bfloat16, torch.float32])
+def test_pairs_with_more_units_than_are_looked_up(q, dt):
+    """More than 64 units a pair of blocks: later ones are looked up when they are taken."""
+    M, N, K = 40000, 9000, 32
+    t = make(1, N, K, 32, True, torch.float16, 36)
+    x = torch.randn((M, K), generator=rng(37)).to(dt).cuda()
+    y = q.q4g_matmul(pack(q, t), x)
+    W = t[3][0].cuda()
+    u = {torch.float32: 2.0 ** -24, torch.float16: 2.0 ** -11, torch.bfloat16: 2.0 ** -8}[dt]
+    for m in range(0, M, 4000):
+        xd = x[m:m + 4000].double()
+        ref, T = xd @ W.T, xd.abs() @ W.abs().T
+        assert bool(((y[m:m + 4000].double() - ref).abs() <= u * ref.abs() + (1e-5 + (0 if dt == torch.float32 else 2.0 ** -11)) * T).all())
+    assert q.last_device_error() == 0
+
+
+@pytest.mark.parametrize("dt", [torch.float16, torch.bfloat16, torch.float32])
+def test_experts_with_more_units_than_are_looked_up(q, dt):
+    """The same for gate_up and down, with experts of very different numbers of rows, one without any."""
+    T, E, K, F = 40000, 5, 32, 4100
+    g = rng(38)
+    pick = torch.tensor([0] * 5 + [1] * 3 + [2] + [4])[torch.randint(0, 10, (T,), generator=g)]
+    logits = torch.zeros((T, E)).scatter_(1, pick[:, None], 4.0).cuda()
+    r = q.moe_route(logits, 1)
+    assert torch.equal(r.ids[:, 0].cpu().long(), pick)
+    x = torch.randn((T, K), generator=g).to(dt).cuda()
+    u = {torch.float32: 2.0 ** -24, torch.float16: 2.0 ** -11, torch.bfloat16: 2.0 ** -8}[dt]
+    w = 1e-5 + (0 if dt == torch.float32 else 2.0 ** -11)
+    t = make(E, 2 * F, K, 32, True, torch.float16, 39)
+    h = q.moe_gate_up(pack(q, t, True), x, r)
+    d = q.moe_down(pack(q, t), x[:, None], r)
+    for m in range(0, T, 4000):
+        e = pick[m:m + 4000]
+        y, A = torch.empty((len(e), 2 * F), dtype=torch.float64, device="cuda"), torch.empty((len(e), 2 * F), dtype=torch.float64, device="cuda")
+        for i in range(E):
+            at, W = (e == i).nonzero()[:, 0].cuda(), t[3][i].cuda()
+            y[at], A[at] = x[m + at].double() @ W.T, x[m + at].double().abs() @ W.abs().T
+        assert bool(((d[m:m + 4000].double() - y).abs() <= u * y.abs() + w * A).all())
+        eg, eu, gate, up = w * A[:, :F], w * A[:, F:], y[:, :F], y[:, F:]
+        s = gate * torch.sigmoid(gate)
+        tol = 1.1 * up.abs() * eg + s.abs() * eu + 1.1 * eg * eu + (u + 1e-6) * (s * up).abs() + 2.0 ** -24
+        assert bool(((h[m:m + 4000, 0].double() - s * up).abs() <= tol).all())
+    assert q.last_device_error() == 0
