@@ -12,7 +12,9 @@ job), roofline of the streaming kernel against the measured HBM copy
 bandwidth, the oracle's throughput on the host cores on a bounded sample, an
 end-to-end figure through the public API with pinned host buffers (each step
 copies its activation batches in and all 128 outputs out), SM clocks sampled during the timed region,
-and a per-(type, form, M) breakdown.  A prefill section times the Llama-shaped
+and a per-(type, form, M) breakdown.  The line stays below 4 KB, which a reader
+that keeps the end of the output has whole; the points behind it (DETAILS) are
+a second JSON line, on stderr.  A prefill section times the Llama-shaped
 GEMMs in both forms (4096 x 4096 and 14336 x 4096 weights, M = 16, 37, 64, 256,
 1024) as TOPS, with the tensor work of the three f16 passes against the
 measured bf16 peak.
@@ -218,6 +220,15 @@ def host_sample_inputs(rows: int):
     wq = {t: oracle.quantize(t, w) for t in TYPES}
     xs = {M: qmm_synth.activations(M, K_DEC) for M in MS}
     return wq, xs
+
+
+DETAILS = ("dequantize_all", "prefill_points", "small_configs", "next_types", "oracle_configs")
+
+
+def emit(line: dict) -> None:
+    """The result on stdout, one line; its details on stderr, another."""
+    print(json.dumps({k: line[k] for k in DETAILS if k in line}), file=sys.stderr, flush=True)
+    print(json.dumps({k: v for k, v in line.items() if k not in DETAILS}), flush=True)
 
 
 def run_reference(args):
@@ -806,7 +817,7 @@ def run_ours(args):
                 "gpu_launches": launches * args.steps,
                 "clocks": ck, "sweep_GBps": sweep, "prefill": prefill, "prefill_points": prefill_points,
                 "small_configs": small, "next_types": nxt, "oracle_configs": oracle_cfg}
-        print(json.dumps(line), flush=True)
+        emit(line)
     if world > 1:
         import torch.distributed as dist
         dist.destroy_process_group()
