@@ -10,9 +10,10 @@
 //
 // The work is a few operations per logit, so a small call is bound by latency
 // and a large one by the selection's instructions.  One warp per token holds
-// its picks in registers (expert lane + 32 i); a selection step is two
-// warp-wide integer reductions (redux) on order-preserving keys, the second
-// one settling ties.
+// its picks in registers, consecutive experts a lane, and every lane knows its
+// largest; a selection step is one warp-wide integer reduction (redux) of
+// those on order-preserving keys and a ballot, whose lowest lane has the
+// lowest expert of equals and looks for its next largest.
 //
 // The order (a stable counting sort of the T k slots by expert) hands out no
 // place by an atomic, so it is the same on every run.  A tile is up to 32

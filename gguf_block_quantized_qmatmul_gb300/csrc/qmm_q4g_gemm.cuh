@@ -6,10 +6,12 @@
 // by a power of two each (the weights' at layout time, the activations' by the
 // preparation launch; f16 activations keep theirs), and
 //   y = 2^-(a + b) sum_k f16(s 2^a (q - z)) (x 2^b).
-// s 2^a and q - z are exact in f16, their product is rounded to 11 bits: half
-// of the products (codes 0, +-1, 2, 4, 8 off the zero point) are exact, so the
-// sum's error is below that of rounding an f16 result (with it 1.33 times the
-// error of that rounding alone, measured), and far below a bf16 one.  f16 gate
+// s 2^a and q - z are exact in f16, their product is rounded to 11 bits.  It is
+// exact where |q - z| is 0 or a power of two (half of the codes with a zero
+// point of 8, five of sixteen with one of 0 or 15), and with a bf16 scale up to
+// 8 and at the even ones.  So the sum's error is below that of rounding an f16
+// result (with it 1.33 times the error of that rounding alone, measured with
+// zero points of 6 to 9 and f16 scales), and far below a bf16 one.  f16 gate
 // and up products would multiply two such sums (1.6 times), so they take the
 // weights' rests as well, v = hi + lo, which makes s (q - z), of at most 16
 // significant bits, exact.  bf16 activations are exact in f16 after scaling
@@ -47,18 +49,23 @@
 // while the accumulator is small, the accumulator is restarted every kQgChunk
 // tiles, and the epilogue adds the chunks in registers (error of 37 x 14336 x
 // 4096: 9.8e-7 with the three passes in turn and two tiles a chunk, 6.6e-7 with
-// the small ones first, 2.2e-7 with one tile as well, for 32.0 us instead of
-// 30.5).  A dense call with fewer units than SMs is split over K as well, and a
+// the small ones first, 2.2e-7 with one tile as well, for 1.5 us more; the call
+// takes 33.7).  The chunks' sums do not fit the epilogue's 72 registers: f32
+// calls keep 216 bytes a thread in local memory.  A dense call with fewer units than SMs is split over K as well, and a
 // last launch adds the slices.
 //
-// Measured: 1024 x 14336 x 4096 f16 76 us (1.58 PFLOP/s; the tensor pipe 66 % of
-// all cycles, the MMAs are the bound and the rest is three units a pair that do
-// not overlap their last epilogue); 2048 tokens x 8 of 64 experts, 2048 -> 2 x
-// 1024 bf16 143 us with its preparation (12 us), 1024 -> 2048 f16 122 us with
-// preparation (12) and combination (25).  There 256 rows an expert do not repay
-// one conversion of its weights: 62 % of the issue slots are taken, four
-// converting warps and two epilogue warps a scheduler share them, and the
-// epilogue gets an instruction every 13 cycles.
+// Measured, in a graph: 1024 x 14336 x 4096 f16 75 us (1.60 PFLOP/s; the tensor
+// pipe 65 % of all cycles, the MMAs are the bound and the rest is three units a
+// pair that do not overlap their last epilogue); 2048 tokens x 8 of 64 experts,
+// 2048 -> 2 x 1024 bf16 139 us with its preparation (12 us), 1024 -> 2048 f16 125
+// us with preparation (12) and combination (25).  There 256 rows an expert do
+// not repay one conversion of its weights: two thirds of the issue slots are
+// taken, and four converting warps and two epilogue warps a scheduler share them.
+//
+// Waits are bounded.  One that gives up raises the error word and the block's
+// abort flag, its warp leaves its role, every other wait of the block ends with
+// the flag and the other block's by its own limit; copies and MMAs that were
+// issued are waited for before shared and tensor memory are given back.
 #pragma once
 
 #include <type_traits>

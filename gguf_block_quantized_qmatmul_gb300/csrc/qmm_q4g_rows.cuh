@@ -20,11 +20,11 @@
 // operands.  Measured at 1 x 28672 x 8192 (f16, G = 64): loads straight into
 // registers, four segments ahead, 44 us (16 warps an SM, and waiting for the
 // oldest load waited for younger ones too); one bulk copy per two segments 35
-// us, and still 30 us with no arithmetic at all; these rings 27.2 us (4.6 TB/s,
-// 62 % of the issue slots).  14336 x 4096 bf16 with 8 rows: 11.6 us, of which the
+// us, and still 30 us with no arithmetic at all; these rings 28 us (4.5 TB/s,
+// 62 % of the issue slots; groups of 64 keep 40 bytes a thread in local memory).  14336 x 4096 bf16 with 8 rows: 11.6 us, of which the
 // launch and the staging of 64 KB of activations a block are some 4 (12.5 us with
 // one staging load a thread in flight and a division an address); one row of
-// 4096 x 4096 bf16: 5.3 us; 28 us for 16 tokens' second products of 8 of 128
+// 4096 x 4096 bf16: 5.4 us; 29 us for 16 tokens' second products of 8 of 128
 // experts (768 -> 2048, G = 32), with the launch that adds a token's.  wk warps split a row block's K
 // and add their sums through shared memory, one barrier among them per row block.
 // Activations are staged once per item in the order the MMAs read them (16

@@ -276,10 +276,15 @@ qmm_status qmm_matmul_static_workspace(qmm_type wtype, qmm_act_mode mode, const 
    and the sizes alone) f16 and bf16 calls round each weight s (q - z) to f16's
    11 bits, less than the rounding of the output (not qmm_moe_gate_up in f16,
    whose weights are exact), and f32 calls keep 22 bits of the activations and
-   all of the weights.  A row of x with an
-   infinity or a NaN gives a row of outputs that are not finite; no other row
-   is touched.
-   Results do not depend on the run: no sum's order varies. */
+   all of the weights.  (There, values below 2^-29 of their row's largest, of
+   weights as of activations, keep fewer bits.)
+   A row's product with a weight matrix neither overflows nor vanishes on its
+   way where it is in f32's range itself; f32 results below 2^-115 have an
+   error of up to 2^-138 besides.  A row of x with an infinity or a NaN gives a
+   row of outputs that are not finite; no other row is touched.
+   Results do not depend on the run: the order of a sum follows from types,
+   sizes and the device's number of SMs.  A call with more rows may round in
+   another way than one with fewer. */
 
 typedef enum { QMM_FLOAT_F32 = 0, QMM_FLOAT_F16 = 1, QMM_FLOAT_BF16 = 2 } qmm_float;
 
@@ -369,8 +374,10 @@ size_t qmm_moe_gate_up_workspace(const qmm_q4g* w, qmm_float xtype, int64_t T, i
 qmm_status qmm_moe_gate_up(const qmm_q4g* w, qmm_float xtype, const void* x, int64_t ldx, const qmm_routing* r, void* h, void* workspace,
                            size_t workspace_bytes, qmm_stream_t stream);
 
-/* y [T][N] = sum over j of weights[t][j] (h[t][j] . W_e^T), in the order of j;
-   rows (slots) of h are ldh elements apart.  A skipped slot adds nothing.
+/* y [T][N] = sum over j of weights[t][j] (h[t][j] . W_e^T); rows (slots) of h
+   are ldh elements apart.  The slots' products are added in the order of j, but
+   for up to 4 tokens the terms of all slots may be one sum, in an order of its
+   own.  A skipped slot adds nothing.
    Errors as qmm_q4g_matmul. */
 size_t qmm_moe_down_workspace(const qmm_q4g* w, qmm_float xtype, int64_t T, int64_t top_k);
 qmm_status qmm_moe_down(const qmm_q4g* w, qmm_float xtype, const void* h, int64_t ldh, const qmm_routing* r, void* y, void* workspace,
