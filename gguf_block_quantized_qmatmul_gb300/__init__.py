@@ -15,6 +15,7 @@ Entry points mirror the C ABI names:
   matmul_batch(items, wtype, mode)  many independent small matmuls in one launch
   matmul_batch_typed(items, mode)   the same, each item with its own weight type
   q4g_*, moe_*                    4-bit group-scale weights and mixture-of-experts layers (q4g.py)
+  q8c_*, block_norm               8-bit channel-scaled products, norms around a block (q8c.py)
 """
 from __future__ import annotations
 
@@ -39,7 +40,8 @@ EXPORTS = ["qmm_block_values", "qmm_block_bytes", "qmm_row_bytes", "qmm_quantize
            "qmm_block_sums", "qmm_matmul_batch", "qmm_matmul_batch_typed", "qmm_test_inject", "qmm_test_set_wait_limit",
            "qmm_last_device_error", "qmm_status_string", "qmm_q4g_bytes", "qmm_q4g_pack", "qmm_q4g_pack_q4_0",
            "qmm_q4g_dequantize", "qmm_q4g_matmul_workspace", "qmm_q4g_matmul", "qmm_moe_route_workspace", "qmm_moe_route",
-           "qmm_moe_gate_up_workspace", "qmm_moe_gate_up", "qmm_moe_down_workspace", "qmm_moe_down"]
+           "qmm_moe_gate_up_workspace", "qmm_moe_gate_up", "qmm_moe_down_workspace", "qmm_moe_down", "qmm_q8c_bytes",
+           "qmm_q8c_pack", "qmm_q8c_dequantize", "qmm_q8c_quantize", "qmm_q8c_matmul_workspace", "qmm_q8c_matmul", "qmm_block_norm"]
 INJECT = {"off": 0, "launch_failure": 1, "stall": 2}
 
 
@@ -73,6 +75,7 @@ def _load() -> ctypes.CDLL:
     lib.qmm_last_device_error.argtypes, lib.qmm_last_device_error.restype = [], i32
     lib.qmm_status_string.argtypes, lib.qmm_status_string.restype = [i32], ctypes.c_char_p
     q4g.declare(lib)
+    q8c.declare(lib)
     return lib
 
 
@@ -256,9 +259,9 @@ def last_device_error() -> int:
 
 def test_inject(kind: str, count: int = 1, arg: int = 0) -> None:
     """Failure-test hook: arm an injected failure ("launch_failure": the next
-    `count` matmul, routing or experts' calls return QMM_ERR_CUDA without
+    `count` matmul, routing, experts', quantizing or norm calls return QMM_ERR_CUDA without
     touching the device; "stall": the next launch of the decode kernel or of
-    the 4-bit GEMM withholds a block's weight stages from stage `arg` on, so a
+    the 4-bit or 8-bit GEMM withholds a block's weight stages from stage `arg` on, so a
     bounded wait times out; "off")."""
     _check(_lib().qmm_test_inject(INJECT[kind], count, arg), "qmm_test_inject")
 
@@ -269,6 +272,8 @@ def test_set_wait_limit(log2_clocks: int) -> None:
     _check(_lib().qmm_test_set_wait_limit(log2_clocks), "qmm_test_set_wait_limit")
 
 
-from . import q4g  # noqa: E402  (uses the helpers above)
+from . import q4g, q8c  # noqa: E402  (use the helpers above)
 from .q4g import (Q4GWeights, Route, moe_down, moe_gate_up, moe_route, q4g_dequantize, q4g_matmul,  # noqa: E402,F401
                   q4g_matmul_workspace, q4g_pack, q4g_pack_q4_0)
+from .q8c import (Q8CWeights, Rows8, block_norm, q8c_dequantize, q8c_matmul, q8c_matmul_workspace, q8c_pack,  # noqa: E402,F401
+                  q8c_quantize)

@@ -1,0 +1,552 @@
+// qmm_q8c_gemm.cu -- 8-bit channel-scaled products of many activation rows on
+// tcgen05.
+//
+// Mathematics.  sm_103a's tensor cores multiply 8-bit integers at a twelfth of
+// their f16 rate (warp MMAs) or not at all (tcgen05), so the codes become f16,
+// exactly, and their products are added in f32.  A sum of integers is exact
+// there while no partial sum passes 2^24, and by Cauchy and Schwarz none does
+// where (sum of squares of a weight row)(sum of squares of an activation row) <
+// 2^48: the weights' largest sum of squares is in their layout, the
+// activations' are computed with their codes.  Rows as models have them (sigma
+// about 30 codes, 16384 K) fulfil it and are accumulated in one go.  In a call
+// where some row does not, the accumulator is restarted every 1024 K (1024 x
+// 2^14 = 2^24: at most 127 x 128 a product of quantized activations; given codes
+// of -128 twice reach 2^24 itself, which f32 holds) and the parts are added as
+// integers.  So y is the same as the row kernel's, bit for bit.
+//
+// The structure is the 4-bit GEMM's (qmm_q4g_gemm.cuh): one persistent block an
+// SM, pairs of blocks (cta_group::2) on 256 weight rows x up to 256 activation
+// rows; converted weights are the A operand in tensor memory, activations come
+// by TMA in 128-byte swizzled tiles.  19 warps' roles:
+//   warp 0      activation tiles, 128 K each
+//   warp 1      eight MMAs a tile
+//   warp 2      raw weights, a box of eight row blocks x 128 K (16 KB)
+//   warps 3-10  epilogue: results from the accumulator, scaled
+//   warps 11-26 conversion: 32 codes a lane and tile of 64 K, ten instructions for eight
+// Calls with few tiles are split over K; the slices' integer sums go to the
+// workspace and a last launch adds and scales them.
+//
+// Waits are bounded, as in the 4-bit GEMM: one that gives up raises the error
+// word, every other role ends, and what was issued is waited for.
+#include "qmm_q8c.cuh"
+#include "qmm_q4g_gemm.cuh"
+
+namespace qmm {
+namespace {
+
+constexpr int kRaw = 8 * kQcSeg;      // bytes of a raw stage
+constexpr int kRestart = 8;           // tiles of 128 K per accumulation where sums may pass 2^24
+constexpr int kMaxBX = 256;
+
+struct GemmParams {
+    QcCall c;
+    int* part;              // K slices: integer sums [ks][M][N]
+    const float* xs;        // scales of the activation rows
+    const uint32_t* xn;     // their sums of squares
+    unsigned* err;
+    int bx, nacc, accw, mtiles, ntiles, nraw, nx, nstage, ks;
+    int off_raw, off_bar;
+    int stall;
+    unsigned stall_block;
+};
+
+struct Unit {
+    int p0, n, nt;      // first activation row, their number, this block's row tile
+    int split, j0, j1;  // K slice, its tiles
+};
+
+template <int CG>
+__global__ void __launch_bounds__(kQgThreads, 1) q8c_gemm_kernel(const __grid_constant__ CUtensorMap tx, const __grid_constant__ CUtensorMap tw, const GemmParams p) {
+    extern __shared__ __align__(1024) uint8_t smraw[];
+    uint8_t* sm = smraw + ((1024 - (smem_u32(smraw) & 1023)) & 1023);
+    const QcCall& c = p.c;
+    const QcWeights& w = c.w;
+    const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31, M = c.a.M;
+    uint64_t* bars = reinterpret_cast<uint64_t*>(sm + p.off_bar);
+    uint64_t* x_full = bars;                       // activation tile landed (of a pair: both halves)
+    uint64_t* x_empty = x_full + kQgXMax;          // and read by the MMAs (commit)
+    uint64_t* full = x_empty + kQgXMax;            // converted weights in tensor memory
+    uint64_t* empty = full + kQgStageMax;          // and read by the MMAs (commit)
+    uint64_t* r_full = empty + kQgStageMax;        // raw weights landed
+    uint64_t* r_empty = r_full + kQgRawMax;        // raw stage converted
+    uint64_t* acc_full = r_empty + kQgRawMax;      // accumulator complete (commit)
+    uint64_t* acc_empty = acc_full + 2;            // accumulator read
+    static_assert((2 * kQgXMax + 2 * kQgStageMax + 2 * kQgRawMax + 4) * 8 <= 448, "mbarriers overlap the TMEM slot");
+    uint32_t* tslot = reinterpret_cast<uint32_t*>(sm + p.off_bar + 448);
+    uint32_t* s_norm = reinterpret_cast<uint32_t*>(sm + p.off_bar + 464);
+    volatile int* flags = reinterpret_cast<volatile int*>(sm + p.off_bar + 480);
+    const uint32_t rank = CG == 2 ? cluster_rank() : 0u;
+    constexpr int kUnit = 16 * CG;  // the MMA's N is a multiple of 16, a pair's of 32
+    const int first_unit = blockIdx.x / CG, unit_step = gridDim.x / CG;
+    if (tid == 0) {
+        for (int i = 0; i < kQgXMax; ++i) {
+            mbar_init(smem_u32(&x_full[i]), 1);
+            mbar_init(smem_u32(&x_empty[i]), 1);
+        }
+        for (int i = 0; i < kQgStageMax; ++i) {
+            mbar_init(smem_u32(&full[i]), 8 * CG);
+            mbar_init(smem_u32(&empty[i]), 1);
+        }
+        for (int i = 0; i < kQgRawMax; ++i) {
+            mbar_init(smem_u32(&r_full[i]), 1);
+            mbar_init(smem_u32(&r_empty[i]), 8);
+        }
+        for (int i = 0; i < 2; ++i) {
+            mbar_init(smem_u32(&acc_full[i]), 1);
+            mbar_init(smem_u32(&acc_empty[i]), kQgEpiWarps * CG);
+        }
+        flags[0] = 0;
+        *s_norm = 0u;
+        fence_mbar_init();
+    }
+    if (warp == 1) {
+        if (CG == 1) {
+            asm volatile("tcgen05.alloc.cta_group::1.sync.aligned.shared::cta.b32 [%0], %1;" ::"r"(smem_u32(tslot)), "n"(kTcTmemCols)
+                         : "memory");
+            asm volatile("tcgen05.relinquish_alloc_permit.cta_group::1.sync.aligned;" ::: "memory");
+        } else {
+            asm volatile("tcgen05.alloc.cta_group::2.sync.aligned.shared::cta.b32 [%0], %1;" ::"r"(smem_u32(tslot)), "n"(kTcTmemCols)
+                         : "memory");
+            asm volatile("tcgen05.relinquish_alloc_permit.cta_group::2.sync.aligned;" ::: "memory");
+        }
+    }
+    grid_dep_launch();
+    tc_fence_before();
+    __syncthreads();
+    if (CG == 2) cluster_sync();  // the pair's barriers are initialised, its tensor memory is allocated
+    tc_fence_after();
+    const uint32_t tmem = *tslot;
+    const int tiles_all = p.mtiles * p.ntiles, units = tiles_all * p.ks;
+    // activation rows in tiles of one size, not full ones and a rest
+    const int size = ((M + p.mtiles - 1) / p.mtiles + kUnit - 1) & ~(kUnit - 1);
+    auto place = [&](int u) {
+        Unit un;
+        un.split = u / tiles_all;
+        u -= un.split * tiles_all;
+        const int st = u / p.ntiles;
+        un.nt = (u - st * p.ntiles) * CG + (int)rank;
+        un.p0 = st * size;
+        un.n = max(min(size, M - un.p0), 0);
+        un.j0 = (int)((long long)un.split * w.KS / p.ks);
+        un.j1 = (int)((long long)(un.split + 1) * w.KS / p.ks);
+        return un;
+    };
+    // an activation stage: two 64-K halves of the rows; of a pair, each block has half the rows
+    const int half = p.bx / CG * 128;
+    auto stage = [&](int s) { return sm + s * 2 * half; };
+    auto raw = [&](int s) { return sm + p.off_raw + s * kRaw; };
+    // 64-K halves of tile j that hold any K
+    auto halves = [&](int j) { return w.K - j * 128 > 64 ? 2 : 1; };
+
+    if (warp == 2) {
+        // ------------------------------ raw weights: constant, so at once ------------------------------
+        if (lane == 0) {
+            QgRing r;
+            bool ok = true, wrapped = false;
+            int left = p.stall - 1;
+            for (int u = first_unit; u < units && ok; u += unit_step) {
+                const Unit un = place(u);
+                for (int j = un.j0; j < un.j1; ++j) {
+                    // injected stall: this block's raw weights end here
+                    if (p.stall && blockIdx.x == p.stall_block && --left < 0) ok = false;
+                    if (!ok || !(ok = qg_wait(smem_u32(&r_empty[r.s]), r.ph ^ 1u, flags, p.err))) break;
+                    const uint32_t bar = smem_u32(&r_full[r.s]);
+                    mbar_arrive_tx(bar, (uint32_t)kRaw);
+                    tma_2d(smem_u32(raw(r.s)), &tw, j * (kQcSeg / 8), 8 * un.nt, bar);
+                    r.next(p.nraw);
+                    wrapped |= r.s == 0;
+                }
+            }
+            qg_drain(r, wrapped, p.nraw, r_full, flags, p.err);
+        }
+    } else if (warp == 0) {
+        // ------------------------------ activations ------------------------------
+        if (lane == 0) {
+            grid_dep_wait();
+            QgRing g;
+            bool ok = true, wrapped = false;
+            for (int u = first_unit; u < units && ok; u += unit_step) {
+                const Unit un = place(u);
+                const int p0 = un.p0 + (int)rank * ((un.n + kUnit - 1) / kUnit * kUnit / CG);
+                for (int j = un.j0; j < un.j1; ++j) {
+                    if (!(ok = qg_wait(smem_u32(&x_empty[g.s]), g.ph ^ 1u, flags, p.err))) break;
+                    uint32_t bar = smem_u32(&x_full[g.s]);
+                    const uint32_t to = smem_u32(stage(g.s));
+                    if (rank == 0) mbar_arrive_tx(bar, (uint32_t)(CG * 2 * half));
+                    if (CG == 2) bar = leader_addr(bar);
+                    tma_4d<CG>(to, &tx, 0, p0, 0, 2 * j, bar);
+                    g.next(p.nx);
+                    wrapped |= g.s == 0;
+                }
+            }
+            // let every copy land before the block can exit (rank 0's barriers have both blocks')
+            if (rank == 0) qg_drain(g, wrapped, p.nx, x_full, flags, p.err);
+        }
+    } else if (warp < kQgConv0) {
+        // whether a sum may pass 2^24: the epilogue's and the MMAs' warps look for themselves
+        grid_dep_wait();
+        uint32_t top = 0;
+        for (int i = (warp == 1 ? 0 : warp - kQgEpi0 + 1) * 32 + lane; i < M; i += (kQgEpiWarps + 1) * 32) top = max(top, __ldg(p.xn + i));
+        top = __reduce_max_sync(0xffffffffu, top);
+        if (lane == 0) atomicMax(s_norm, top);
+        asm volatile("bar.sync 1, %0;" ::"n"((kQgEpiWarps + 1) * 32) : "memory");
+        const uint32_t wnorm = __ldg(reinterpret_cast<const uint32_t*>(w.data + w.norm_off));
+        const bool restart = (unsigned long long)*reinterpret_cast<volatile uint32_t*>(s_norm) * wnorm >= 1ull << 48;
+        const int chunk = restart ? kRestart : w.KS;
+        if (warp == 1) {
+            // ------------------------------ MMA issuer ------------------------------
+            if (rank == 0) {
+                // the whole warp runs the loop, so that its values are uniform, and one elected lane waits and issues
+                const bool lead = elect_one();
+                const uint64_t d0 = tc_sdesc128(smem_u32(stage(0)));
+                const uint32_t lo0 = (uint32_t)d0, dhi = (uint32_t)(d0 >> 32);
+                QgRing g, gx;
+                int cc = 0, last = -1;  // accumulator uses; the last weight stage issued
+                uint32_t last_ph = 0, ready = 0;  // the next stage's barrier, tested before this tile's MMAs are issued
+                bool ok = true;
+                for (int u = first_unit; u < units; u += unit_step) {
+                    const Unit un = place(u);
+                    const uint32_t idesc = tc_idesc((un.n + kUnit - 1) / kUnit * kUnit) + ((uint32_t)((CG - 1) * (kTcBW >> 4)) << 24);  // a pair: M = 256
+                    for (int c0 = un.j0; c0 < un.j1; c0 += chunk, ++cc) {
+                        const int ab = p.nacc == 2 ? (cc & 1) : 0, use = p.nacc == 2 ? (cc >> 1) : cc;
+                        if (lead && ok && use > 0) ok = qg_wait(smem_u32(&acc_empty[ab]), (uint32_t)((use - 1) & 1), flags, p.err);
+                        const uint32_t dt = tmem + (uint32_t)(ab * p.accw);
+                        const int n = min(chunk, un.j1 - c0);
+                        for (int i = 0; i < n; ++i) {
+                            const int s = g.s;
+                            const uint32_t ph = g.ph;
+                            g.next(p.nstage);
+                            const uint32_t next = mbar_test(smem_u32(&full[g.s]), g.ph);
+                            if (lead && ok) ok = qg_wait(smem_u32(&x_full[gx.s]), gx.ph, flags, p.err) && (ready || qg_wait(smem_u32(&full[s]), ph, flags, p.err));
+                            const int sx = gx.s;
+                            gx.next(p.nx);
+                            ready = next;
+                            tc_fence_after();
+                            const uint32_t x0 = lo0 + (uint32_t)((sx * 2 * half) >> 4), a0 = tmem + (uint32_t)(p.nacc * p.accw + 64 * s);
+                            const int nh = halves(c0 + i);
+                            __syncwarp();
+                            if (lead && ok) {
+#pragma unroll
+                                for (int h = 0; h < 2; ++h) {
+                                    if (h == 1 && nh == 1) break;
+#pragma unroll
+                                    for (int kk = 0; kk < 4; ++kk)
+                                        qg_mma_tc<CG>(dt, a0 + 32 * h + 8 * kk, ((uint64_t)dhi << 32) | (x0 + (uint32_t)(h * half >> 4) + 2 * kk), idesc,
+                                                      (i | h | kk) != 0 ? 1u : 0u);
+                                }
+                                qg_commit<CG>(smem_u32(&empty[s]));
+                                qg_commit<CG>(smem_u32(&x_empty[sx]));
+                                last = s;
+                                last_ph = ph;
+                            }
+                        }
+                        if (lead && ok) qg_commit<CG>(smem_u32(&acc_full[ab]));
+                    }
+                }
+                // the last commits must land before tensor memory is released
+                if (last >= 0) mbar_drain(smem_u32(&empty[last]), last_ph, flags, p.err);
+            }
+        } else {
+            // ------------------------------ epilogue ------------------------------
+            const int ew = warp - kQgEpi0, q = warp & 3, part = ew >> 2;  // columns part * 8, then every (kQgEpiHalves * 8)th
+            const uint32_t tq = (uint32_t)(32 * q) << 16;
+            int cc = 0;
+            bool ok = true;
+            const float* sw = reinterpret_cast<const float*>(w.data + w.scale_off);
+            for (int u = first_unit; u < units && ok; u += unit_step) {
+                const Unit un = place(u);
+                const int nch = (un.n + kCols - 1) / kCols;
+                const int n = (8 * un.nt + 2 * q) * 16 + lane;  // the tile's 128 rows are the lanes of the four quarters
+                const bool on = n < w.N;
+                const float wn = on ? __ldg(sw + n) : 0.0f, bias = on && c.bias ? __ldg(c.bias + n) : 0.0f;
+                auto put = [&](int k, const int v[kCols]) {  // columns kCols k..
+                    const int m = un.p0 + kCols * k, left = min(kCols, un.n - kCols * k);
+                    if (!on) return;
+                    if (p.ks > 1) {
+                        int* to = p.part + ((long long)un.split * M + m) * w.N + n;
+#pragma unroll
+                        for (int i = 0; i < kCols; ++i)
+                            if (i < left) to[(long long)i * w.N] = v[i];
+                        return;
+                    }
+                    auto as = [&](auto* y) {
+                        using Y = typename std::remove_pointer<decltype(y)>::type;
+                        Y* to = y + (long long)m * w.N + n;
+#pragma unroll
+                        for (int i = 0; i < kCols; ++i)
+                            if (i < left) to[(long long)i * w.N] = to_type<Y>(qc_scale(v[i], wn, __ldg(p.xs + m + i), bias));
+                    };
+                    if (c.yt == X_F32) as(static_cast<float*>(c.y));
+                    else if (c.yt == X_F16) as(static_cast<__half*>(c.y));
+                    else as(static_cast<__nv_bfloat16*>(c.y));
+                };
+                int sums[kMaxBX / kQgEpiHalves];  // local memory; restarted accumulations only
+                for (int c0 = un.j0; c0 < un.j1; c0 += chunk, ++cc) {
+                    const int ab = p.nacc == 2 ? (cc & 1) : 0, use = p.nacc == 2 ? (cc >> 1) : cc;
+                    if (!(ok = qg_wait_warp(smem_u32(&acc_full[ab]), (uint32_t)(use & 1), false, flags, p.err))) break;
+                    tc_fence_after();
+                    __syncwarp();
+                    const uint32_t acol = tmem + tq + (uint32_t)(ab * p.accw);
+                    const bool begin = c0 == un.j0, end = c0 + chunk >= un.j1;
+                    uint32_t r[kCols];
+                    if (part < nch) tc_ld8(acol + kCols * part, r);
+#pragma unroll 1
+                    for (int k = part, at = 0; k < nch; k += kQgEpiHalves, at += kCols) {
+                        tc_wait_ld();
+                        int v[kCols];
+#pragma unroll
+                        for (int i = 0; i < kCols; ++i) {
+                            asm volatile("" : "+r"(r[i]));  // not used before the wait
+                            v[i] = __float2int_rn(__uint_as_float(r[i]));
+                        }
+                        if (k + kQgEpiHalves < nch) tc_ld8(acol + kCols * (k + kQgEpiHalves), r);
+                        if (!begin) {
+#pragma unroll
+                            for (int i = 0; i < kCols; ++i) v[i] += sums[at + i];
+                        }
+                        if (end) {
+                            put(k, v);
+                        } else {
+#pragma unroll
+                            for (int i = 0; i < kCols; ++i) sums[at + i] = v[i];
+                        }
+                    }
+                    __syncwarp();
+                    tc_fence_before();
+                    __syncwarp();
+                    if (lane == 0) {
+                        if (CG == 2) mbar_arrive_cluster(leader_addr(smem_u32(&acc_empty[ab])));
+                        else mbar_arrive(smem_u32(&acc_empty[ab]));
+                    }
+                }
+            }
+        }
+    } else {
+        // ------------------------------ conversion ------------------------------
+        const int cw = warp - kQgConv0, q = warp & 3, hh = (cw >> 2) & 1, grp = cw >> 3;  // row block 2 q + hh of a tile
+        QgRing g, r;      // the next tile's weight and raw stage
+        int turn = 0;     // the group that it is for
+        uint32_t r_ready = 0;  // this group's next raw stage was seen to have landed
+        int stored = -1;  // the stage of this warp's last tile, whose stores have not been waited for
+        auto announce = [&]() {
+            if (stored < 0) return;
+            asm volatile("tcgen05.wait::st.sync.aligned;" ::: "memory");
+            tc_fence_before();
+            __syncwarp();
+            if (lane == 0) {
+                if (CG == 2) mbar_arrive_cluster(leader_addr(smem_u32(&full[stored])));
+                else mbar_arrive(smem_u32(&full[stored]));
+            }
+            stored = -1;
+        };
+        // a 64-K tile's fragment registers: row g's in the even ones, row g + 8's in the odd ones
+        auto convert = [&](const uint8_t* tile, uint32_t v[16]) {
+            const uint4 a = reinterpret_cast<const uint4*>(tile)[lane], b = reinterpret_cast<const uint4*>(tile + 512)[lane];
+            qc_half4(a.x, v[0], v[2]);
+            qc_half4(b.x, v[1], v[3]);
+            qc_half4(a.y, v[4], v[6]);
+            qc_half4(b.y, v[5], v[7]);
+            qc_half4(a.z, v[8], v[10]);
+            qc_half4(b.z, v[9], v[11]);
+            qc_half4(a.w, v[12], v[14]);
+            qc_half4(b.w, v[13], v[15]);
+        };
+        bool ok = true;
+        for (int u = first_unit; u < units && ok; u += unit_step) {
+            const Unit un = place(u);
+            // The groups take tiles in turn, whatever a unit's number of them: a group that waits for
+            // the release of tile t - nstage has waited for t - groups - nstage, so that with nstage >=
+            // groups the stage's barrier is at most one phase behind the wait's parity.
+            for (int j = un.j0; j < un.j1; ++j, turn = turn + 1 == kQgGroups ? 0 : turn + 1) {
+                const QgRing at = g, ar = r;
+                g.next(p.nstage);
+                r.next(p.nraw);
+                if (turn != grp) continue;
+                if (!(ok = qg_wait_warp(smem_u32(&r_full[ar.s]), ar.ph, r_ready, flags, p.err))) break;
+                // tested here, needed after the conversion
+                const uint32_t e_ready = mbar_test(smem_u32(&empty[at.s]), at.ph ^ 1u);
+                const uint8_t* seg = raw(ar.s) + (2 * q + hh) * kQcSeg;
+                const uint32_t col = tmem + ((uint32_t)(32 * q + 16 * hh) << 16) + (uint32_t)(p.nacc * p.accw + 64 * at.s);
+                uint32_t v[16];
+                convert(seg, v);
+                announce();
+                if (!(ok = qg_wait_warp(smem_u32(&empty[at.s]), at.ph ^ 1u, e_ready, flags, p.err))) break;
+                QgRing rn = r;  // this group's next raw stage
+                rn.skip(kQgGroups - 1, p.nraw);
+                r_ready = mbar_test(smem_u32(&r_full[rn.s]), rn.ph);
+                tc_fence_after();
+                __syncwarp();
+                tc_st_frag<16>(col, v);
+                convert(seg + 1024, v);
+                __syncwarp();
+                if (lane == 0) mbar_arrive(smem_u32(&r_empty[ar.s]));
+                tc_st_frag<16>(col + 32, v);
+                stored = at.s;
+                if (p.nstage <= kQgGroups) announce();  // no stage to spare
+            }
+        }
+        announce();
+    }
+    tc_fence_before();
+    __syncthreads();
+    if (CG == 2) {
+        // After a wait that gave up, rank 1's last copies, which complete on rank 0's barriers, may be
+        // ones that rank 0 never counted: both blocks stay for many times a copy's duration.
+        if (flags[0]) {
+            const long long t0 = clock64();
+            while (clock64() - t0 < kQgQuiet) __nanosleep(1000);
+            __syncwarp();
+        }
+        cluster_sync();  // neither block leaves while the other's MMAs, copies or arrivals may reach it
+    }
+    if (warp == 1) {
+        tc_fence_after();
+        if (CG == 1) asm volatile("tcgen05.dealloc.cta_group::1.sync.aligned.b32 %0, %1;" ::"r"(tmem), "n"(kTcTmemCols) : "memory");
+        else asm volatile("tcgen05.dealloc.cta_group::2.sync.aligned.b32 %0, %1;" ::"r"(tmem), "n"(kTcTmemCols) : "memory");
+    }
+}
+
+// y of the K slices' integer sums
+__global__ void __launch_bounds__(256) q8c_sum_kernel(const int* part, int ks, int M, int N, const float* sw, const float* xs, const float* bias, void* y, int yt) {
+    grid_dep_launch();
+    grid_dep_wait();
+    const int n = blockIdx.x * 256 + threadIdx.x, m = blockIdx.y;
+    if (n >= N) return;
+    const long long all = (long long)M * N, i = (long long)m * N + n;
+    int v = 0;
+    for (int s0 = 0; s0 < ks; s0 += 4) {
+        int u[4];
+#pragma unroll
+        for (int s = 0; s < 4; ++s) u[s] = s0 + s < ks ? __ldcg(part + (s0 + s) * all + i) : 0;
+#pragma unroll
+        for (int s = 0; s < 4; ++s) v += u[s];
+    }
+    x_store(y, yt, i, qc_scale(v, __ldg(sw + n), __ldg(xs + m), bias ? __ldg(bias + n) : 0.0f));
+}
+
+template <int CG>
+cudaError_t gemm_go(const QcGemmPlan& pl, const CUtensorMap& tx, const CUtensorMap& tw, const GemmParams& p, int smem_max, cudaStream_t s) {
+    static unsigned long long done = 0;
+    auto* k = q8c_gemm_kernel<CG>;
+    const cudaError_t e = ensure_smem(k, smem_max, done);
+    if (e != cudaSuccess) return e;
+    cudaLaunchConfig_t cfg = {};
+    cfg.gridDim = dim3((unsigned)pl.grid);
+    cfg.blockDim = dim3(kQgThreads);
+    cfg.dynamicSmemBytes = pl.smem;
+    cfg.stream = s;
+    cudaLaunchAttribute attr[2];
+    attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+    attr[0].val.programmaticStreamSerializationAllowed = 1;
+    attr[1].id = cudaLaunchAttributeClusterDimension;
+    attr[1].val.clusterDim.x = CG;
+    attr[1].val.clusterDim.y = 1;
+    attr[1].val.clusterDim.z = 1;
+    cfg.attrs = attr;
+    cfg.numAttrs = CG == 1 ? 1 : 2;
+    return cudaLaunchKernelEx(&cfg, k, tx, tw, p);
+}
+
+}  // namespace
+
+QcGemmPlan plan_q8c_gemm(const QcCall& c, int sms, int smem_max) {
+    QcGemmPlan pl;
+    const QcWeights& w = c.w;
+    const long long M = c.a.M;
+    // Modelled cycles: a tile of 128 K costs its MMAs (half a cycle a column, at least 40 each) or its
+    // conversion (800); a unit its prologue and, without a second accumulator, the epilogue that the
+    // next unit's MMAs wait for; slices of K their sums' traffic and a launch.
+    double best = 0;
+    for (int cg = 1; cg <= 2; ++cg) {
+        const int unit = 16 * cg, workers = sms / cg, most = cg == 2 ? kMaxBX : 128;
+        const int ntiles = (w.RB + 8 * cg - 1) / (8 * cg);
+        for (long long tiles = (M + most - 1) / most; tiles <= 8 + (M + most - 1) / most; ++tiles) {
+            const int bx = (int)((M + tiles - 1) / tiles + unit - 1) / unit * unit;
+            const long long mt = (M + bx - 1) / bx, un = (long long)ntiles * mt;
+            const double mma = 8.0 * (cg == 1 ? (bx < 40 ? 40.0 : (double)bx) : bx < 80 ? 40.0 : bx / 2.0), tile = mma > 800.0 ? mma : 800.0;
+            const double once = bx > 192 ? 1500.0 + 12.0 * bx : 1500.0;
+            for (int ks = 1; ks <= w.KS && ks <= 16 && (ks == 1 || un * ks <= 2 * workers); ++ks) {
+                const double waves = (double)((un * ks + workers - 1) / workers);
+                const double cost = waves * ((double)((w.KS + ks - 1) / ks) * tile + once) + (ks > 1 ? 4000.0 + 8.0 * ks * M * w.N / 3000.0 : 0.0);
+                if (best == 0 || cost < 0.98 * best) {
+                    best = cost;
+                    pl.cg = cg;
+                    pl.bx = bx;
+                    pl.ks = ks;
+                    pl.mtiles = (int)mt;
+                    pl.ntiles = ntiles;
+                }
+            }
+            if (bx == unit) break;
+        }
+    }
+    pl.accw = (pl.bx + 31) / 32 * 32;
+    pl.nacc = pl.bx <= 192 ? 2 : 1;  // with two accumulators the epilogue runs beside the next unit's MMAs
+    pl.nstage = (kTcTmemCols - pl.nacc * pl.accw) / 64;
+    if (pl.nstage > kQgStageMax) pl.nstage = kQgStageMax;
+    const int stage = pl.bx / pl.cg * 256, room = smem_max - 512 - 1024;
+    // Both rings are multiples of the converting groups, so that whoever waits for a stage's next
+    // filling has waited for its last one (copies may land out of order).
+    pl.nx = (room - 4 * kRaw) / stage / kQgGroups * kQgGroups;
+    if (pl.nx > kQgXMax) pl.nx = kQgXMax;
+    pl.nraw = (room - pl.nx * stage) / kRaw / kQgGroups * kQgGroups;
+    if (pl.nraw > kQgRawMax) pl.nraw = kQgRawMax;
+    if (pl.nstage < kQgGroups || pl.nx < kQgGroups || pl.nraw < kQgGroups) return pl;
+    pl.smem = (size_t)pl.nx * stage + (size_t)pl.nraw * kRaw + 512 + 1024;
+    const long long units = (long long)pl.mtiles * pl.ntiles * pl.ks, workers = sms / pl.cg;
+    if (units > (1ll << 30)) return pl;
+    pl.grid = (int)(units < workers ? units : workers) * pl.cg;
+    auto r256 = [](size_t v) { return (v + 255) / 256 * 256; };
+    pl.ws_scale = r256((size_t)M * w.KS * 256);
+    pl.ws_norm = pl.ws_scale + r256((size_t)M * 4);
+    pl.ws_part = pl.ws_norm + r256((size_t)M * 4);
+    pl.workspace = pl.ws_part + (pl.ks > 1 ? (size_t)pl.ks * M * w.N * 4 : 0);
+    pl.ok = true;
+    return pl;
+}
+
+cudaError_t launch_q8c_gemm(const QcGemmPlan& pl, const QcCall& c, void* ws, unsigned* err, int stall, int smem_max, cudaStream_t s) {
+    uint8_t* wsb = static_cast<uint8_t*>(ws);
+    const int M = c.a.M;
+    const long long pitch = (long long)c.w.KS * 128;
+    float* xs = reinterpret_cast<float*>(wsb + pl.ws_scale);
+    uint32_t* xn = reinterpret_cast<uint32_t*>(wsb + pl.ws_norm);
+    cudaError_t e = launch_q8c_prep(c.a, c.w.K, QcPrep{wsb, xs, xn, pitch}, true, s);
+    if (e != cudaSuccess) return e;
+    // activations: 64 K x rows x 1 x pitch / 64; a box has a block's rows (half a pair's) and two of the last
+    CUtensorMap tx, tw;
+    const unsigned long long xdims[4] = {64, (unsigned long long)M, 1, (unsigned long long)pitch / 64};
+    const unsigned long long xstrides[3] = {(unsigned long long)pitch * 2, (unsigned long long)pitch * 2 * M, 128};
+    const unsigned xbox[4] = {64, (unsigned)(pl.bx / pl.cg), 1, 2};
+    if (!make_map_nd(&tx, CU_TENSOR_MAP_DATA_TYPE_FLOAT16, wsb, 4, xdims, xstrides, xbox, CU_TENSOR_MAP_SWIZZLE_128B)) return cudaErrorInvalidValue;
+    // raw weights: row blocks, 8-byte elements, a box of a segment of eight of them
+    if (!make_map(&tw, CU_TENSOR_MAP_DATA_TYPE_UINT64, c.w.data, (unsigned long long)c.w.KS * (kQcSeg / 8), (unsigned long long)c.w.RB,
+                  (unsigned long long)c.w.KS * kQcSeg, kQcSeg / 8, 8, CU_TENSOR_MAP_SWIZZLE_NONE))
+        return cudaErrorInvalidValue;
+    GemmParams p;
+    p.c = c;
+    p.part = reinterpret_cast<int*>(wsb + pl.ws_part);
+    p.xs = xs;
+    p.xn = xn;
+    p.err = err;
+    p.bx = pl.bx;
+    p.nacc = pl.nacc;
+    p.accw = pl.accw;
+    p.mtiles = pl.mtiles;
+    p.ntiles = pl.ntiles;
+    p.nraw = pl.nraw;
+    p.nx = pl.nx;
+    p.nstage = pl.nstage;
+    p.ks = pl.ks;
+    p.stall = stall;
+    p.stall_block = (unsigned)pl.cg - 1u;  // of a pair the second one, whose partner finds out by its own waits
+    p.off_raw = pl.nx * (pl.bx / pl.cg) * 256;
+    p.off_bar = p.off_raw + pl.nraw * kRaw;
+    e = pl.cg == 2 ? gemm_go<2>(pl, tx, tw, p, smem_max, s) : gemm_go<1>(pl, tx, tw, p, smem_max, s);
+    if (e != cudaSuccess || pl.ks == 1) return e;
+    const dim3 grid((unsigned)((c.w.N + 255) / 256), (unsigned)M);
+    return launch_pdl_2d(q8c_sum_kernel, grid.x, grid.y, 256, 0, s, (const int*)p.part, pl.ks, M, c.w.N, reinterpret_cast<const float*>(c.w.data + c.w.scale_off),
+                         (const float*)xs, c.bias, c.y, c.yt);
+}
+
+}  // namespace qmm

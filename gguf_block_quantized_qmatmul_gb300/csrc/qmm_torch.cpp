@@ -1,14 +1,15 @@
-// qmm_torch.cpp -- the calls of q4g.py that a decode step makes many times, as
+// qmm_torch.cpp -- the calls of q4g.py and q8c.py that a decode step makes many times, as
 // a CPython extension: argument checks on torch tensors, output and workspace
 // allocation and the library call.  (The same in Python over ctypes costs 8 to
 // 18 us a call, more than the kernels; this costs about 4.)  It computes
 // nothing: every kernel is libqmm.so's, through include/qmm.h.
 //
 // A call returns its tensor(s), or the library's status as an int when that is
-// not QMM_OK (q4g.py raises it); tensors that do not fit raise ValueError.
+// not QMM_OK (the module raises it); tensors that do not fit raise ValueError.
 #include <ATen/cuda/EmptyTensor.h>
 #include <c10/cuda/CUDAGuard.h>
 #include <c10/cuda/CUDAStream.h>
+#include <torch/csrc/Dtype.h>
 #include <torch/csrc/Exceptions.h>
 #include <torch/csrc/autograd/python_variable.h>
 
@@ -242,11 +243,140 @@ PyObject* route(PyObject*, PyObject* const* a, Py_ssize_t n) {
     });
 }
 
+// elements from a row of [rows, K] to the next; rows are contiguous and apart
+int64_t row_distance(const at::Tensor& t, const char* text) {
+    need(t.dim() == 2 && (t.size(1) <= 1 || t.stride(1) == 1), text);
+    const int64_t ld = t.size(0) > 1 ? t.stride(0) : t.size(1);
+    need(ld >= t.size(1), text);
+    return ld;
+}
+bool on(const at::Tensor& t, int64_t device) { return t.is_cuda() && t.get_device() == device; }
+
+at::ScalarType scalar_type(PyObject* o) {
+    need(THPDtype_Check(o), "dtype is a torch.dtype");
+    return reinterpret_cast<THPDtype*>(o)->scalar_type;
+}
+
+// (weights, their data, x, scales of the rows, bias, dtype, out, workspace)
+PyObject* matmul8(PyObject*, PyObject* const* a, Py_ssize_t n) {
+    return guarded([&]() -> PyObject* {
+        need(n == 8, "matmul8 takes 8 arguments");
+        qmm_q8c w = *reinterpret_cast<const qmm_q8c*>(integer(a[0]));
+        const at::Tensor& data = tensor(a[1], "laid-out weights are a tensor");
+        need(data.is_cuda() && data.is_contiguous() && data.nbytes() >= qmm_q8c_bytes(w.N, w.K), "the weights are on a CUDA device, whole");
+        w.data = data.data_ptr();
+        const int64_t device = data.get_device();
+        const at::Tensor& x = tensor(a[2], "x is a tensor, or Rows8");
+        const bool codes = a[3] != Py_None;
+        qmm_float xt = QMM_FLOAT_F32, yt;
+        const char* text = codes ? "x's codes are int8 [rows, K], rows contiguous, on the weights' device" : "activations are f32, f16 or bf16 [rows, K] on the weights' device, rows contiguous";
+        need(on(x, device) && x.dim() == 2 && x.size(1) == w.K && (codes ? x.scalar_type() == at::kChar : float_type(x.scalar_type(), xt)), text);
+        const int64_t M = x.size(0), ld = row_distance(x, text);
+        const float* scales = nullptr;
+        if (codes) {
+            const at::Tensor& s = tensor(a[3], "scales are a tensor");
+            need(on(s, device) && s.scalar_type() == at::kFloat && s.dim() == 1 && s.size(0) == M && s.is_contiguous(), "x's scales are f32 [rows] on the weights' device");
+            scales = s.data_ptr<float>();
+        }
+        const float* bias = nullptr;
+        if (a[4] != Py_None) {
+            const at::Tensor& b = tensor(a[4], "bias is a tensor");
+            need(on(b, device) && b.scalar_type() == at::kFloat && b.dim() == 1 && b.size(0) == w.N && b.is_contiguous(), "bias is f32 [N] on the weights' device");
+            bias = b.data_ptr<float>();
+        }
+        at::ScalarType ys = a[5] != Py_None ? scalar_type(a[5]) : a[6] != Py_None ? tensor(a[6], "out is a tensor").scalar_type() : codes ? at::kFloat : x.scalar_type();
+        need(float_type(ys, yt), "the result is f32, f16 or bf16");
+        const c10::cuda::CUDAGuard guard((c10::DeviceIndex)device);
+        at::Tensor y;
+        if (a[6] == Py_None) {
+            y = empty({M, w.N}, ys, x.device());
+        } else {
+            y = tensor(a[6], "out is a tensor");
+            need(y.dim() == 2 && y.size(0) == M && y.size(1) == w.N && y.scalar_type() == ys && y.is_contiguous() && on(y, device),
+                 "out is contiguous, of the result's shape, type and device");
+        }
+        // few values in aligned rows need no workspace (include/qmm.h)
+        const bool direct = M <= 16 && w.K % 16 == 0 && (reinterpret_cast<uintptr_t>(x.data_ptr()) | (uintptr_t)(ld * x.element_size())) % 16 == 0 &&
+                            (codes || M * w.K <= QMM_Q8C_DIRECT);
+        const Workspace ws(a[7], a[7] == Py_None && !direct ? qmm_q8c_matmul_workspace(&w, codes, M) : 0, x);
+        return result(qmm_q8c_matmul(&w, xt, x.data_ptr(), ld, scales, M, bias, yt, y.data_ptr(), ws.p, ws.n, stream_of(device)), y);
+    });
+}
+
+// (y, weight, residual, post weight, gate, scale, eps, weight offset, quantize, out, residual out) -> (r', h) or (r', codes, scales)
+PyObject* norm(PyObject*, PyObject* const* a, Py_ssize_t n) {
+    return guarded([&]() -> PyObject* {
+        need(n == 11, "norm takes 11 arguments");
+        const at::Tensor& y = tensor(a[0], "y is a tensor");
+        qmm_norm p = {};
+        need(y.is_cuda() && y.dim() == 2 && float_type(y.scalar_type(), p.type), "y is CUDA f32, f16 or bf16 [T, K]");
+        const int64_t T = y.size(0), K = y.size(1), device = y.get_device();
+        const char* text = "y, residual and outputs are [T, K] of one type and device, rows contiguous";
+        auto rows = [&](const at::Tensor& t, int64_t& ld) {
+            need(on(t, device) && t.sizes() == y.sizes() && t.scalar_type() == y.scalar_type(), text);
+            ld = row_distance(t, text);
+            return t.data_ptr();
+        };
+        p.y = rows(y, p.ldy);
+        const at::Tensor& w = tensor(a[1], "weight is a tensor");
+        need(float_type(w.scalar_type(), p.weight_type) && on(w, device) && w.dim() == 1 && w.size(0) == K && w.is_contiguous(), "weight is f32, f16 or bf16 [K] on y's device");
+        p.weight = w.data_ptr();
+        if (a[2] != Py_None) p.residual = rows(tensor(a[2], "residual is a tensor"), p.ldr);
+        if (a[3] != Py_None) {
+            const at::Tensor& t = tensor(a[3], "post_weight is a tensor");
+            need(t.scalar_type() == w.scalar_type() && on(t, device) && t.sizes() == w.sizes() && t.is_contiguous(), "post_weight is as weight");
+            p.post_weight = t.data_ptr();
+        }
+        if (a[4] != Py_None) {
+            const at::Tensor& t = tensor(a[4], "gate is a tensor");
+            if (t.dim() == 1) {
+                need(on(t, device) && t.size(0) == K && t.scalar_type() == y.scalar_type() && t.is_contiguous(), "gate is [K] or [T, K] of y's type and device");
+                p.gate = t.data_ptr();
+            } else {
+                p.gate = rows(t, p.ldg);
+            }
+        }
+        p.scale = (float)PyFloat_AsDouble(a[5]);
+        p.eps = (float)PyFloat_AsDouble(a[6]);
+        p.weight_offset = (float)PyFloat_AsDouble(a[7]);
+        if (PyErr_Occurred()) throw python_error();
+        const bool quantize = truth(a[8]);
+        need(!quantize || a[9] == Py_None, "quantized rows are allocated by the call: no out");
+        if (K < 1 || K > QMM_NORM_MAX_K) return PyLong_FromLong(QMM_ERR_SHAPE);
+        const c10::cuda::CUDAGuard guard((c10::DeviceIndex)device);
+        const at::Tensor r = a[10] == Py_None ? empty({T, K}, y.scalar_type(), y.device()) : tensor(a[10], "residual_out is a tensor");
+        p.residual_out = rows(r, p.ldro);
+        at::Tensor h, scales;
+        if (quantize) {
+            const int64_t pitch = (K + 15) / 16 * 16;
+            h = empty({T, pitch}, at::kChar, y.device());
+            if (pitch != K) h = h.narrow(1, 0, K);
+            scales = empty({T}, at::kFloat, y.device());
+            p.codes = static_cast<int8_t*>(h.data_ptr());
+            p.scales = scales.data_ptr<float>();
+            p.ldh = pitch;
+        } else {
+            h = a[9] == Py_None ? empty({T, K}, y.scalar_type(), y.device()) : tensor(a[9], "out is a tensor");
+            p.h = rows(h, p.ldh);
+        }
+        const qmm_status s = qmm_block_norm(&p, T, K, stream_of(device));
+        if (s != QMM_OK) return PyLong_FromLong(s);
+        PyObject* t = PyTuple_New(quantize ? 3 : 2);
+        if (!t) return nullptr;
+        PyTuple_SET_ITEM(t, 0, THPVariable_Wrap(r));
+        PyTuple_SET_ITEM(t, 1, THPVariable_Wrap(h));
+        if (quantize) PyTuple_SET_ITEM(t, 2, THPVariable_Wrap(scales));
+        return t;
+    });
+}
+
 PyMethodDef methods[] = {
     {"matmul", reinterpret_cast<PyCFunction>(reinterpret_cast<void (*)()>(matmul)), METH_FASTCALL, nullptr},
     {"route", reinterpret_cast<PyCFunction>(reinterpret_cast<void (*)()>(route)), METH_FASTCALL, nullptr},
     {"gate_up", reinterpret_cast<PyCFunction>(reinterpret_cast<void (*)()>(experts<false>)), METH_FASTCALL, nullptr},
     {"down", reinterpret_cast<PyCFunction>(reinterpret_cast<void (*)()>(experts<true>)), METH_FASTCALL, nullptr},
+    {"matmul8", reinterpret_cast<PyCFunction>(reinterpret_cast<void (*)()>(matmul8)), METH_FASTCALL, nullptr},
+    {"norm", reinterpret_cast<PyCFunction>(reinterpret_cast<void (*)()>(norm)), METH_FASTCALL, nullptr},
     {nullptr, nullptr, 0, nullptr}};
 PyModuleDef module = {PyModuleDef_HEAD_INIT, "_qmm_torch", nullptr, -1, methods, nullptr, nullptr, nullptr, nullptr};
 

@@ -88,7 +88,7 @@ class _Binding:
 
     def __getattr__(self, name):
         module = _load_binding()
-        for f in ("matmul", "route", "gate_up", "down"):
+        for f in ("matmul", "route", "gate_up", "down", "matmul8", "norm"):
             setattr(self, f, getattr(module, f))
         return getattr(module, name)
 

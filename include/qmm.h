@@ -383,12 +383,92 @@ size_t qmm_moe_down_workspace(const qmm_q4g* w, qmm_float xtype, int64_t T, int6
 qmm_status qmm_moe_down(const qmm_q4g* w, qmm_float xtype, const void* h, int64_t ldh, const qmm_routing* r, void* y, void* workspace,
                         size_t workspace_bytes, qmm_stream_t stream);
 
+/* ---------------------------------------------------------------------------
+   8-bit products with one scale per output channel and one per activation row.
+   (The pages pair Q8_0 weights with activations quantized in blocks of 32; here
+   a whole row is one block, as checkpoints of 8-bit linears keep them.)
+
+   y[m][n] = (sum_k a[m][k] w[n][k]) sw[n] sx[m] (+ bias[n]), w and a in
+   -128..127.  The sum is formed exactly; y = ((sum sw) sx) + bias in f32, each
+   step rounded, and one rounding to y's type.  So a row's result depends on that
+   row and the weights alone: not on M, the other rows or the kernel.
+   Activations given as floats are quantized in the call: sx = max|x| / 127,
+   a = round(x (1 / sx)), halves away from zero, in f32 (the rule of
+   qmm_quantize_act).  A row with an infinity or a NaN gives a row of NaN; no
+   other row is touched. */
+
+/* Laid-out weights. */
+typedef struct {
+    const void* data;   /* device memory, qmm_q8c_bytes(N, K) bytes, 16-byte aligned */
+    int64_t N, K;       /* 1 <= K < 2^17, N <= 2^23 */
+} qmm_q8c;
+
+#define QMM_Q8C_DIRECT 32768
+
+/* Bytes of the laid-out form; 0 for an invalid shape. */
+size_t qmm_q8c_bytes(int64_t N, int64_t K);
+
+/* Lays weights out: codes int8 [N][K], rows ldc bytes apart; scales f32 [N].
+   Errors: NULL, SHAPE, ALIGN (out 16, scales 4), CUDA. */
+qmm_status qmm_q8c_pack(const int8_t* codes, int64_t ldc, const float* scales, int64_t N, int64_t K, void* out, qmm_stream_t stream);
+
+/* Laid-out weights -> out [N][K] f32, w sw. */
+qmm_status qmm_q8c_dequantize(const qmm_q8c* w, float* out, qmm_stream_t stream);
+
+/* Rows of floats (ldx elements apart) -> int8 codes (rows ldc bytes apart) and
+   f32 scales [M], by the rule above; for weights (a row per output channel) as
+   for activations.  Rows need no alignment beyond their elements'. */
+qmm_status qmm_q8c_quantize(qmm_float xtype, const void* x, int64_t ldx, int64_t M, int64_t K, int8_t* codes, int64_t ldc, float* scales,
+                            qmm_stream_t stream);
+
+/* The product.  x: floats of xtype, or, with x_scales (f32 [M]), int8 codes
+   (xtype is then not read); rows ldx elements apart, aligned as their elements
+   are.  bias: f32 [N] or NULL.  y [M, N] of ytype, contiguous.
+   workspace: qmm_q8c_matmul_workspace(w, x_scales != NULL, M) bytes,
+   uninitialised; calls that may overlap need one each.  None is needed for up
+   to 16 rows that start on 16-byte boundaries where K is a multiple of 16 and
+   x is codes, or M K <= QMM_Q8C_DIRECT floats.
+   Errors: TYPE, NULL, SHAPE, ALIGN, WORKSPACE, CUDA. */
+size_t qmm_q8c_matmul_workspace(const qmm_q8c* w, int quantized, int64_t M);
+qmm_status qmm_q8c_matmul(const qmm_q8c* w, qmm_float xtype, const void* x, int64_t ldx, const float* x_scales, int64_t M, const float* bias,
+                          qmm_float ytype, void* y, void* workspace, size_t workspace_bytes, qmm_stream_t stream);
+
+/* What stands between two blocks, in one pass over T rows of K values, in f32:
+     v  = y / sqrt(mean(y^2) + eps) (weight_offset + post_weight)   (without post_weight: y)
+     r' = residual + scale gate v                                   (without: 0; 1)
+     h  = r' / sqrt(mean(r'^2) + eps) (weight_offset + weight)
+   residual_out takes r' (NULL: not kept); either h or codes and scales take h,
+   the latter quantized row by row as qmm_q8c_matmul does.  h is made of r'
+   before that is rounded to its type.  y, residual, gate, residual_out and h
+   are of `type`, the weights of weight_type.  Rows are ld* elements apart
+   (gate: 0 for one row for all).  residual_out may be residual or y, h may be y
+   or residual: a row is read whole before it is written; otherwise outputs
+   overlap nothing.  Rows need no alignment beyond their elements'.
+   Errors: NULL, TYPE, SHAPE, ALIGN, CUDA. */
+#define QMM_NORM_MAX_K 32768
+typedef struct {
+    const void* y;
+    const void* residual;     /* or NULL */
+    const void* gate;         /* or NULL */
+    const void* post_weight;  /* [K] or NULL */
+    const void* weight;       /* [K] */
+    void* residual_out;       /* or NULL */
+    void* h;                  /* this, */
+    int8_t* codes;            /* or this */
+    float* scales;            /* and this [T] */
+    int64_t ldy, ldr, ldg, ldro, ldh;  /* ldh: of h or codes */
+    qmm_float type, weight_type;
+    float scale, eps, weight_offset;
+} qmm_norm;
+qmm_status qmm_block_norm(const qmm_norm* n, int64_t T, int64_t K, qmm_stream_t stream);
+
 /* Failure-test hooks.  (The pages have no counterpart: these exist so that
    the library's failure paths can be exercised without faulting a GPU.)
    qmm_test_inject arms an injected failure, consumed by the next `count`
    calls that reach it; QMM_INJECT_OFF disarms every kind.
    - QMM_INJECT_LAUNCH_FAILURE: qmm_matmul, qmm_block_sums, qmm_q4g_matmul,
-     qmm_moe_route, qmm_moe_gate_up and qmm_moe_down return QMM_ERR_CUDA at once, as if the launch had failed, without any CUDA call
+     qmm_moe_route, qmm_moe_gate_up, qmm_moe_down, qmm_q8c_quantize, qmm_q8c_matmul
+     and qmm_block_norm return QMM_ERR_CUDA at once, as if the launch had failed, without any CUDA call
      (the outputs are not touched).
    - QMM_INJECT_STALL: the next decode-kernel launch (qmm_dmma_kernel, the
      M <= 16 warp-MMA path) issues no weight stage from stage `arg` on in its
@@ -396,9 +476,9 @@ qmm_status qmm_moe_down(const qmm_q4g* w, qmm_float xtype, const void* h, int64_
      gives up, the block drains the copies it did issue and exits, and
      qmm_last_device_error then reports QMM_ERR_TIMEOUT.  The call's output
      is undefined; later calls are unaffected.  The next launch of the 4-bit
-     GEMM stalls in the same way: one block (of its pairs, where it works in
+     or the 8-bit GEMM stalls in the same way: one block (of its pairs, where it works in
      pairs, the second of the first) copies `arg` tiles of its weights and no
-     more.  Whichever of the two is launched first takes the injection.
+     more.  Whichever is launched first takes the injection.
    qmm_test_set_wait_limit sets the bounded waits' spin limit on the current
    device to 2^log2_clocks SM clocks (16..31; 0 restores the default 2^31,
    about one second), so that an injected stall ends in milliseconds.  It
