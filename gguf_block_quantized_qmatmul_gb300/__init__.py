@@ -41,7 +41,8 @@ EXPORTS = ["qmm_block_values", "qmm_block_bytes", "qmm_row_bytes", "qmm_quantize
            "qmm_last_device_error", "qmm_status_string", "qmm_q4g_bytes", "qmm_q4g_pack", "qmm_q4g_pack_q4_0",
            "qmm_q4g_dequantize", "qmm_q4g_matmul_workspace", "qmm_q4g_matmul", "qmm_moe_route_workspace", "qmm_moe_route",
            "qmm_moe_gate_up_workspace", "qmm_moe_gate_up", "qmm_moe_down_workspace", "qmm_moe_down", "qmm_q8c_bytes",
-           "qmm_q8c_pack", "qmm_q8c_dequantize", "qmm_q8c_quantize", "qmm_q8c_matmul_workspace", "qmm_q8c_matmul", "qmm_block_norm"]
+           "qmm_q8c_pack", "qmm_q8c_dequantize", "qmm_q8c_quantize", "qmm_q8c_matmul_workspace", "qmm_q8c_matmul", "qmm_block_norm",
+           "qmm_moe_layer_workspace", "qmm_moe_layer"]
 INJECT = {"off": 0, "launch_failure": 1, "stall": 2}
 
 
@@ -261,8 +262,8 @@ def test_inject(kind: str, count: int = 1, arg: int = 0) -> None:
     """Failure-test hook: arm an injected failure ("launch_failure": the next
     `count` matmul, routing, experts', quantizing or norm calls return QMM_ERR_CUDA without
     touching the device; "stall": the next launch of the decode kernel or of
-    the 4-bit or 8-bit GEMM withholds a block's weight stages from stage `arg` on, so a
-    bounded wait times out; "off")."""
+    the 4-bit or 8-bit GEMM withholds a block's weight stages from stage `arg` on (of
+    moe_layer: a report), so a bounded wait times out; "off")."""
     _check(_lib().qmm_test_inject(INJECT[kind], count, arg), "qmm_test_inject")
 
 
@@ -273,7 +274,7 @@ def test_set_wait_limit(log2_clocks: int) -> None:
 
 
 from . import q4g, q8c  # noqa: E402  (use the helpers above)
-from .q4g import (Q4GWeights, Route, moe_down, moe_gate_up, moe_route, q4g_dequantize, q4g_matmul,  # noqa: E402,F401
+from .q4g import (Q4GWeights, Route, moe_down, moe_gate_up, moe_layer, moe_layer_workspace, moe_route, q4g_dequantize, q4g_matmul,  # noqa: E402,F401
                   q4g_matmul_workspace, q4g_pack, q4g_pack_q4_0)
 from .q8c import (Q8CWeights, Rows8, block_norm, q8c_dequantize, q8c_matmul, q8c_matmul_workspace, q8c_pack,  # noqa: E402,F401
                   q8c_quantize)

@@ -1,0 +1,169 @@
+// qmm_moe_layer.cu -- host side of the mixture-of-experts layer for a few
+// tokens (qmm_moe_layer.cuh), and the router's product.
+#include "qmm_moe_layer.cuh"
+
+namespace qmm {
+
+cudaError_t launch_moe_layer_f16(const MoePlan& pl, const MoeParams& p, int smem_max, cudaStream_t s);
+cudaError_t launch_moe_layer_bf16(const MoePlan& pl, const MoeParams& p, int smem_max, cudaStream_t s);
+
+namespace {
+
+__device__ __forceinline__ void router_load8(const void* row, int type, int k, float f[8]) {
+    if (type == X_F32) {
+        const float4 a = __ldg(reinterpret_cast<const float4*>(static_cast<const float*>(row) + k));
+        const float4 b = __ldg(reinterpret_cast<const float4*>(static_cast<const float*>(row) + k) + 1);
+        f[0] = a.x, f[1] = a.y, f[2] = a.z, f[3] = a.w, f[4] = b.x, f[5] = b.y, f[6] = b.z, f[7] = b.w;
+        return;
+    }
+    const uint4 u = __ldg(reinterpret_cast<const uint4*>(static_cast<const uint16_t*>(row) + k));
+    const uint32_t w[4] = {u.x, u.y, u.z, u.w};
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+        if (type == X_F16) {
+            const float2 v = __half22float2(*reinterpret_cast<const __half2*>(&w[i]));
+            f[2 * i] = v.x;
+            f[2 * i + 1] = v.y;
+        } else {
+            f[2 * i] = __uint_as_float(w[i] << 16);
+            f[2 * i + 1] = __uint_as_float(w[i] & 0xffff0000u);
+        }
+    }
+}
+
+// Logits of all tokens for one expert a block: f32 products and sums in a fixed order, eight tokens at
+// a time.  Bound by latency (one trip to memory, one reduction).  The first block clears the next
+// launch's counters.
+__global__ void __launch_bounds__(256) moe_router_kernel(const void* x, int xt, long long ldx, int T, int K, const void* router, int rt, float* logits, int ldl,
+                                                         unsigned* counters) {
+    __shared__ float red[8][8];
+    const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31, e = blockIdx.x;
+    grid_dep_launch();
+    const uint8_t* w = static_cast<const uint8_t*>(router) + (long long)e * K * x_size(rt);
+    grid_dep_wait();
+    if (e == 0 && tid < 4) counters[tid] = 0u;
+    for (int t0 = 0; t0 < T; t0 += 8) {
+        float acc[8];
+#pragma unroll
+        for (int t = 0; t < 8; ++t) acc[t] = 0.0f;
+        for (int k = 8 * tid; k < K; k += 2048) {
+            float f[8];
+            router_load8(w, rt, k, f);
+#pragma unroll
+            for (int t = 0; t < 8; ++t) {
+                if (t0 + t >= T) break;
+                float v[8];
+                router_load8(static_cast<const uint8_t*>(x) + (t0 + t) * ldx * x_size(xt), xt, k, v);
+#pragma unroll
+                for (int i = 0; i < 8; ++i) acc[t] = fmaf(f[i], v[i], acc[t]);
+            }
+        }
+#pragma unroll
+        for (int t = 0; t < 8; ++t) {
+            if (t0 + t >= T) break;
+#pragma unroll
+            for (int o = 16; o; o >>= 1) acc[t] += __shfl_xor_sync(0xffffffffu, acc[t], o);
+            if (lane == 0) red[t][warp] = acc[t];
+        }
+        __syncthreads();
+        if (tid < 8 && t0 + tid < T) {
+            float v = 0.0f;
+#pragma unroll
+            for (int i = 0; i < 8; ++i) v += red[tid][i];
+            logits[(long long)(t0 + tid) * ldl + e] = v;
+        }
+        __syncthreads();
+    }
+}
+
+QgCall call_of(int op, const QgWeights& w, int xt, int T, int k) {
+    QgCall c = {};
+    c.op = op;
+    c.w = w;
+    c.xt = xt;
+    c.ldx = w.K;
+    c.M = T * k;
+    c.r.T = T;
+    c.r.top_k = k;
+    return c;
+}
+
+QgRowsParams params_of(const QgRowsPlan& pl, const QgCall& c, void* part) {
+    QgRowsParams p;
+    p.c = c;
+    p.part = static_cast<float*>(part);
+    p.by_slot = pl.by_slot;
+    p.cols = pl.cols;
+    p.np = pl.np;
+    p.wk = pl.wk;
+    p.wr = pl.warps / pl.wk;
+    p.wk_log2 = pl.wk == 1 ? 0 : pl.wk == 2 ? 1 : pl.wk == 4 ? 2 : 3;
+    p.off_zero = pl.off_zero;
+    p.off_red = pl.off_red;
+    p.off_ring = pl.off_ring;
+    return p;
+}
+
+}  // namespace
+
+MoePlan plan_moe_layer(const MoeCall& c, int sms, int smem_max) {
+    MoePlan pl;
+    const int T = c.T, k = c.route.top_k, S = T * k, E = c.up.E;
+    if (T < 1 || T > kMoeMaxTokens || E > kQgRowMaxE) return pl;
+    const int route = round_up((3 * S + 2 * E + 1) * 4, 16), room = smem_max - 4096 - route;
+    // one number of column blocks for both products; a second one pays where experts have more rows than one holds
+    const int np = c.xt == X_F32 ? 3 : 1;
+    for (int nb = (S + E - 1) / E * np > 8 ? 2 : 1; nb >= 1 && !pl.ok; --nb) {
+        pl.up = plan_q4g_rows(call_of(P_GATE_UP, c.up, c.xt, T, k), sms, room, kMoeWarps, nb);
+        pl.down = plan_q4g_rows(call_of(P_DOWN, c.down, c.xt, T, k), sms, room, kMoeWarps, nb);
+        pl.nb = nb;
+        pl.ok = pl.up.ok && pl.down.ok;
+    }
+    if (!pl.ok) return pl;
+    pl.blocks = sms;
+    size_t most = pl.up.smem > pl.down.smem ? pl.up.smem : pl.down.smem;
+    const size_t picks = (size_t)kMoeWarps * E * 4;
+    if (most < picks) most = picks;
+    pl.off_route = (int)((most + 15) / 16 * 16);
+    pl.smem = (size_t)pl.off_route + route;
+    auto r256 = [](size_t v) { return (v + 255) / 256 * 256; };
+    pl.ws_logits = 256;
+    pl.ws_h = pl.ws_logits + r256((size_t)T * ((E + 3) / 4 * 4) * 4);
+    pl.ws_part = pl.ws_h + r256((size_t)S * c.down.K * x_size(c.xt));
+    pl.workspace = pl.ws_part + pl.down.workspace;
+    return pl;
+}
+
+cudaError_t launch_moe_layer(const MoePlan& pl, const MoeCall& c, void* ws, unsigned* err, int stall, int smem_max, cudaStream_t s) {
+    uint8_t* b = static_cast<uint8_t*>(ws);
+    unsigned* counters = reinterpret_cast<unsigned*>(b);
+    float* logits = reinterpret_cast<float*>(b + pl.ws_logits);
+    const int E = c.up.E, ldl = (E + 3) / 4 * 4;
+    cudaError_t e = launch_pdl(moe_router_kernel, (unsigned)E, 256, 0, s, c.x, c.xt, c.ldx, c.T, c.up.K, c.router, c.rt, logits, ldl, counters);
+    if (e != cudaSuccess) return e;
+    MoeParams p;
+    p.route = RouteParams();
+    p.route.c = c.route;
+    p.route.c.logits = logits;
+    p.route.c.xt = X_F32;
+    p.route.c.ldl = ldl;
+    p.route.c.T = c.T;
+    p.route.c.E = E;
+    p.epl16 = E > 128;
+    route_lanes(p.route, p.epl16 ? 16 : 4);
+    QgCall up = call_of(P_GATE_UP, c.up, c.xt, c.T, c.route.top_k), down = call_of(P_DOWN, c.down, c.xt, c.T, c.route.top_k);
+    up.x = c.x;
+    up.ldx = c.ldx;
+    up.y = b + pl.ws_h;
+    down.x = up.y;
+    down.y = c.y;
+    p.up = params_of(pl.up, up, nullptr);
+    p.down = params_of(pl.down, down, b + pl.ws_part);
+    p.counters = counters;
+    p.err = err;
+    p.off_route = pl.off_route;
+    p.stall = stall;
+    return c.xt == X_F16 ? launch_moe_layer_f16(pl, p, smem_max, s) : launch_moe_layer_bf16(pl, p, smem_max, s);
+}
+
+}  // namespace qmm

@@ -213,6 +213,25 @@ qmm_status qmm_q4g_matmul(const qmm_q4g* wd, qmm_float xtype, const void* x, int
     return product(c, workspace, workspace_bytes, stream);
 }
 
+static qmm_status route_config(const qmm_route_config* cfg, int64_t E) {
+    if ((cfg->score != QMM_SCORE_SOFTMAX && cfg->score != QMM_SCORE_SIGMOID) ||
+        (cfg->group_score != QMM_GROUP_MAX && cfg->group_score != QMM_GROUP_TOP2))
+        return QMM_ERR_TYPE;
+    if (cfg->groups < 1 || cfg->groups > 32 || E % cfg->groups != 0 || cfg->top_groups < 1 || cfg->top_groups > cfg->groups ||
+        cfg->top_k > cfg->top_groups * (E / cfg->groups))
+        return QMM_ERR_SHAPE;
+    return QMM_OK;
+}
+static void route_choice(const qmm_route_config* cfg, RouteCall& c) {
+    c.top_k = cfg->top_k;
+    c.sigmoid = cfg->score == QMM_SCORE_SIGMOID;
+    c.renorm = cfg->renorm != 0;
+    c.groups = cfg->groups;
+    c.top_groups = cfg->top_groups;
+    c.top2 = cfg->group_score == QMM_GROUP_TOP2;
+    c.scale = cfg->scale;
+}
+
 static bool route_shape(int64_t T, int64_t E, int64_t top_k) {
     return T >= 0 && E >= 1 && E <= QMM_MOE_MAX_EXPERTS && top_k >= 1 && top_k <= QMM_MOE_MAX_TOP_K && top_k <= E && T * top_k <= INT32_MAX;
 }
@@ -226,13 +245,12 @@ qmm_status qmm_moe_route(const qmm_route_config* cfg, qmm_float type, const void
                          size_t workspace_bytes, qmm_stream_t stream) {
     if (!cfg) return QMM_ERR_NULL;
     if (!float_type(type)) return QMM_ERR_TYPE;
-    if ((cfg->score != QMM_SCORE_SOFTMAX && cfg->score != QMM_SCORE_SIGMOID) ||
-        (cfg->group_score != QMM_GROUP_MAX && cfg->group_score != QMM_GROUP_TOP2))
-        return QMM_ERR_TYPE;
-    if (!route_shape(T, E, cfg->top_k) || ldl < E) return QMM_ERR_SHAPE;
-    if (cfg->groups < 1 || cfg->groups > 32 || E % cfg->groups != 0 || cfg->top_groups < 1 || cfg->top_groups > cfg->groups ||
-        cfg->top_k > cfg->top_groups * (E / cfg->groups))
-        return QMM_ERR_SHAPE;
+    if (!route_shape(T, E, cfg->top_k) || ldl < E) {
+        const qmm_status bad = route_config(cfg, 1);
+        return bad == QMM_ERR_TYPE ? bad : QMM_ERR_SHAPE;
+    }
+    const qmm_status st = route_config(cfg, E);
+    if (st != QMM_OK) return st;
     if (T > 0 && (offsets == nullptr) != (order == nullptr)) return QMM_ERR_NULL;
     if (T > 0 && (!logits || !ids || !weights)) return QMM_ERR_NULL;
     if (!aligned(logits, x_size((int)type)) || !aligned(ids, 4) || !aligned(weights, 4) || !aligned(offsets, 4) || !aligned(order, 4) ||
@@ -250,19 +268,71 @@ qmm_status qmm_moe_route(const qmm_route_config* cfg, qmm_float type, const void
     c.ldl = ldl;
     c.T = (int)T;
     c.E = (int)E;
-    c.top_k = cfg->top_k;
-    c.sigmoid = cfg->score == QMM_SCORE_SIGMOID;
-    c.renorm = cfg->renorm != 0;
-    c.groups = cfg->groups;
-    c.top_groups = cfg->top_groups;
-    c.top2 = cfg->group_score == QMM_GROUP_TOP2;
+    route_choice(cfg, c);
     c.bias = bias;
-    c.scale = cfg->scale;
     c.ids = ids;
     c.weights = weights;
     c.offsets = offsets;
     c.order = order;
     return launch_route(c, workspace, reinterpret_cast<cudaStream_t>(stream)) == cudaSuccess ? QMM_OK : QMM_ERR_CUDA;
+}
+
+// the weights, types and sizes of a layer call; c.T = 0 where there is nothing to do
+static qmm_status layer_of(const qmm_q4g* up, const qmm_q4g* down, qmm_float xtype, int64_t T, int64_t top_k, MoeCall& c) {
+    if (!float_type(xtype)) return QMM_ERR_TYPE;
+    c = MoeCall();
+    qmm_status st = describe(up, c.up);
+    if (st == QMM_OK) st = describe(down, c.down);
+    if (st != QMM_OK) return st;
+    if (up->N == 0 || up->paired == 0 || down->paired != 0 || down->experts != up->experts || down->K != up->N / 2 || up->experts > QMM_MOE_MAX_EXPERTS)
+        return QMM_ERR_SHAPE;
+    if (T < 0 || T > QMM_MOE_LAYER_MAX_TOKENS || top_k < 1 || top_k > QMM_MOE_MAX_TOP_K || top_k > up->experts) return QMM_ERR_SHAPE;
+    c.xt = (int)xtype;
+    c.T = down->N == 0 ? 0 : (int)T;
+    c.route.top_k = (int)top_k;
+    return QMM_OK;
+}
+
+size_t qmm_moe_layer_workspace(const qmm_q4g* up, const qmm_q4g* down, qmm_float xtype, int64_t T, int64_t top_k) {
+    MoeCall c;
+    int sms = 0, smem = 0;
+    if (layer_of(up, down, xtype, T, top_k, c) != QMM_OK || c.T == 0 || device_constants(nullptr, &sms, &smem) != cudaSuccess) return 0;
+    const MoePlan pl = plan_moe_layer(c, sms, smem);
+    return pl.ok ? pl.workspace : 0;
+}
+
+qmm_status qmm_moe_layer(const qmm_q4g* up, const qmm_q4g* down, const qmm_route_config* cfg, qmm_float router_type, const void* router, const float* bias,
+                         qmm_float xtype, const void* x, int64_t ldx, int64_t T, void* y, int32_t* ids, float* weights, void* workspace,
+                         size_t workspace_bytes, qmm_stream_t stream) {
+    if (!cfg || !up || !down) return QMM_ERR_NULL;
+    if (!float_type(router_type)) return QMM_ERR_TYPE;
+    MoeCall c;
+    qmm_status st = layer_of(up, down, xtype, T, cfg->top_k, c);
+    if (st != QMM_OK) return st;
+    if ((st = route_config(cfg, up->experts)) != QMM_OK) return st;
+    if (c.T == 0) return QMM_OK;
+    if (!router || !x || !y || (ids == nullptr) != (weights == nullptr)) return QMM_ERR_NULL;
+    if ((st = check_data(up)) != QMM_OK || (st = check_data(down)) != QMM_OK) return st;
+    if ((st = check_rows(x, (int)xtype, ldx, up->K)) != QMM_OK) return st;
+    if (!aligned(router, 16) || !aligned(bias, 4) || !aligned(y, x_size((int)xtype)) || !aligned(ids, 4) || !aligned(weights, 4)) return QMM_ERR_ALIGN;
+    if (injected_launch_failure()) return QMM_ERR_CUDA;
+    unsigned* err = nullptr;
+    int sms = 0, smem = 0;
+    if (device_constants(&err, &sms, &smem) != cudaSuccess) return QMM_ERR_CUDA;
+    const MoePlan pl = plan_moe_layer(c, sms, smem);
+    if (!pl.ok) return QMM_ERR_SHAPE;
+    if (!workspace || workspace_bytes < pl.workspace) return QMM_ERR_WORKSPACE;
+    if (!aligned(workspace, 16)) return QMM_ERR_ALIGN;
+    route_choice(cfg, c.route);
+    c.route.bias = bias;
+    c.route.ids = ids;
+    c.route.weights = weights;
+    c.router = router;
+    c.rt = (int)router_type;
+    c.x = x;
+    c.ldx = ldx;
+    c.y = y;
+    return launch_moe_layer(pl, c, workspace, err, injected_stall(), smem, reinterpret_cast<cudaStream_t>(stream)) == cudaSuccess ? QMM_OK : QMM_ERR_CUDA;
 }
 
 size_t qmm_moe_gate_up_workspace(const qmm_q4g* w, qmm_float xtype, int64_t T, int64_t top_k) {

@@ -53,7 +53,8 @@ struct QgRowsPlan {
     size_t smem = 0;
     size_t workspace = 0;  // P_DOWN by expert: f32 partial rows [T top_k][N]
 };
-QgRowsPlan plan_q4g_rows(const QgCall& c, int sms, int smem_max);
+// warps_only: 0, or the one number of warps that may be chosen; nb_most: column blocks, at most
+QgRowsPlan plan_q4g_rows(const QgCall& c, int sms, int smem_max, int warps_only = 0, int nb_most = 4);
 cudaError_t launch_q4g_rows(const QgRowsPlan& pl, const QgCall& c, void* ws, int smem_max, cudaStream_t s);
 
 // The tcgen05 GEMM.
@@ -87,6 +88,31 @@ struct RouteCall {
     int* offsets;  // NULL: no sorted order wanted
     int* order;
 };
+
+// A whole layer of few tokens (include/qmm.h, qmm_moe_layer).
+constexpr int kMoeMaxTokens = 32;
+struct MoeCall {
+    QgWeights up, down;
+    RouteCall route;     // logits: of the workspace; ids, weights: for the caller, or NULL
+    const void* router;  // [E][K]
+    int rt;              // its type
+    const void* x;
+    int xt;
+    long long ldx;
+    int T;
+    void* y;
+};
+struct MoePlan {
+    bool ok = false;
+    QgRowsPlan up, down;
+    int blocks = 0, nb = 0;
+    int off_route = 0;
+    size_t smem = 0, ws_logits = 0, ws_h = 0, ws_part = 0, workspace = 0;
+};
+MoePlan plan_moe_layer(const MoeCall& c, int sms, int smem_max);
+// stall: test hook: the first share of the first products is never reported done
+cudaError_t launch_moe_layer(const MoePlan& pl, const MoeCall& c, void* ws, unsigned* err, int stall, int smem_max, cudaStream_t s);
+
 size_t route_workspace(int T, int E, int top_k);
 cudaError_t launch_route(const RouteCall& c, void* ws, cudaStream_t s);
 

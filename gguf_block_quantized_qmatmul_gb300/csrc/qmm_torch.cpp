@@ -243,6 +243,60 @@ PyObject* route(PyObject*, PyObject* const* a, Py_ssize_t n) {
     });
 }
 
+// (up, its data, down, its data, router, x, bias, top_k, score, groups, top_groups, group_score, renorm, scale, route, out, workspace)
+// -> y or (y, ids, weights)
+PyObject* layer(PyObject*, PyObject* const* a, Py_ssize_t n) {
+    return guarded([&]() -> PyObject* {
+        need(n == 17, "layer takes 17 arguments");
+        int64_t device, device2;
+        const qmm_q4g up = weights(a[0], a[1], device), down = weights(a[2], a[3], device2);
+        need(device == device2, "both weights are on one device");
+        const at::Tensor &router = tensor(a[4], "router is a tensor"), &x = tensor(a[5], "x is a tensor");
+        qmm_float rt, xt;
+        need(router.is_cuda() && router.get_device() == device && router.dim() == 2 && router.size(0) == up.experts && router.size(1) == up.K &&
+                 router.is_contiguous() && float_type(router.scalar_type(), rt),
+             "router is contiguous f32, f16 or bf16 [experts, K] on the weights' device");
+        int64_t ld;
+        activations(up, device, x, 2, xt, ld);
+        const float* bias = nullptr;
+        if (a[6] != Py_None) {
+            const at::Tensor& b = tensor(a[6], "bias is a tensor");
+            need(b.is_cuda() && b.get_device() == device && b.scalar_type() == at::kFloat && b.dim() == 1 && b.size(0) == up.experts && b.is_contiguous(),
+                 "bias is f32 [experts] on the weights' device");
+            bias = b.data_ptr<float>();
+        }
+        qmm_route_config cfg;
+        cfg.top_k = integer32(a[7]);
+        cfg.score = integer32(a[8]);
+        cfg.groups = integer32(a[9]);
+        cfg.top_groups = integer32(a[10]);
+        cfg.group_score = integer32(a[11]);
+        cfg.renorm = truth(a[12]);
+        cfg.scale = (float)PyFloat_AsDouble(a[13]);
+        if (PyErr_Occurred()) throw python_error();
+        const bool route = truth(a[14]);
+        const int64_t T = x.size(0);
+        if (T > QMM_MOE_LAYER_MAX_TOKENS || cfg.top_k < 1 || cfg.top_k > QMM_MOE_MAX_TOP_K) return PyLong_FromLong(QMM_ERR_SHAPE);
+        const c10::cuda::CUDAGuard guard((c10::DeviceIndex)device);
+        const at::Tensor y = output(a[15], {T, down.N}, x);
+        at::Tensor ids, wt;
+        if (route) {
+            ids = empty({T, cfg.top_k}, at::kInt, x.device());
+            wt = empty({T, cfg.top_k}, at::kFloat, x.device());
+        }
+        const Workspace ws(a[16], a[16] == Py_None ? qmm_moe_layer_workspace(&up, &down, xt, T, cfg.top_k) : 0, x);
+        const qmm_status s = qmm_moe_layer(&up, &down, &cfg, rt, router.data_ptr(), bias, xt, x.data_ptr(), ld, T, y.data_ptr(),
+                                           route ? ids.data_ptr<int32_t>() : nullptr, route ? wt.data_ptr<float>() : nullptr, ws.p, ws.n, stream_of(device));
+        if (s != QMM_OK || !route) return result(s, y);
+        PyObject* t = PyTuple_New(3);
+        if (!t) return nullptr;
+        PyTuple_SET_ITEM(t, 0, THPVariable_Wrap(y));
+        PyTuple_SET_ITEM(t, 1, THPVariable_Wrap(ids));
+        PyTuple_SET_ITEM(t, 2, THPVariable_Wrap(wt));
+        return t;
+    });
+}
+
 // elements from a row of [rows, K] to the next; rows are contiguous and apart
 int64_t row_distance(const at::Tensor& t, const char* text) {
     need(t.dim() == 2 && (t.size(1) <= 1 || t.stride(1) == 1), text);
@@ -375,6 +429,7 @@ PyMethodDef methods[] = {
     {"route", reinterpret_cast<PyCFunction>(reinterpret_cast<void (*)()>(route)), METH_FASTCALL, nullptr},
     {"gate_up", reinterpret_cast<PyCFunction>(reinterpret_cast<void (*)()>(experts<false>)), METH_FASTCALL, nullptr},
     {"down", reinterpret_cast<PyCFunction>(reinterpret_cast<void (*)()>(experts<true>)), METH_FASTCALL, nullptr},
+    {"layer", reinterpret_cast<PyCFunction>(reinterpret_cast<void (*)()>(layer)), METH_FASTCALL, nullptr},
     {"matmul8", reinterpret_cast<PyCFunction>(reinterpret_cast<void (*)()>(matmul8)), METH_FASTCALL, nullptr},
     {"norm", reinterpret_cast<PyCFunction>(reinterpret_cast<void (*)()>(norm)), METH_FASTCALL, nullptr},
     {nullptr, nullptr, 0, nullptr}};

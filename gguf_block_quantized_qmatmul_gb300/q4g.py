@@ -9,6 +9,7 @@ its types, limits and errors).
   moe_route(logits, top_k, ...)     experts, weights and sorted slots   -> Route
   moe_gate_up(w, x, route)          silu(x . Wg^T) * (x . Wu^T) of each token's experts
   moe_down(w, h, route)             weighted sum of the experts' second products
+  moe_layer(up, down, router, x)    all of it for up to 32 tokens, router product included, in two launches
 
 Tensors are CUDA tensors; activations are f32, f16 or bf16 with their last
 dimension contiguous (rows may be further apart).  Work goes to the current
@@ -66,7 +67,9 @@ def declare(lib) -> None:
             ("qmm_moe_gate_up_workspace", [p, i32, i64, i64], sz),
             ("qmm_moe_gate_up", [p, i32, p, i64, p, p, p, sz, p], i32),
             ("qmm_moe_down_workspace", [p, i32, i64, i64], sz),
-            ("qmm_moe_down", [p, i32, p, i64, p, p, p, sz, p], i32)):
+            ("qmm_moe_down", [p, i32, p, i64, p, p, p, sz, p], i32),
+            ("qmm_moe_layer_workspace", [p, p, i32, i64, i64], sz),
+            ("qmm_moe_layer", [p, p, p, i32, p, p, i32, p, i64, i64, p, p, p, p, sz, p], i32)):
         f = getattr(lib, name)
         f.argtypes, f.restype = args, res
 
@@ -88,7 +91,7 @@ class _Binding:
 
     def __getattr__(self, name):
         module = _load_binding()
-        for f in ("matmul", "route", "gate_up", "down", "matmul8", "norm"):
+        for f in ("matmul", "route", "gate_up", "down", "matmul8", "norm", "layer"):
             setattr(self, f, getattr(module, f))
         return getattr(module, name)
 
@@ -281,3 +284,24 @@ def moe_down(w: Q4GWeights, h: torch.Tensor, route: Route, out: torch.Tensor | N
     if type(y) is int:
         _check(y, "qmm_moe_down")
     return y
+
+
+def moe_layer(gate_up: Q4GWeights, down: Q4GWeights, router: torch.Tensor, x: torch.Tensor, top_k: int, score: str = "softmax",
+              bias: torch.Tensor | None = None, groups: int = 1, top_groups: int = 1, group_score: str = "max", renorm: bool = True,
+              scale: float = 1.0, route: bool = False, out: torch.Tensor | None = None, workspace: torch.Tensor | None = None, stream=None):
+    """y [T, N] of x [T, K] for up to 32 tokens, in two launches: logits x . router^T (f32, f16 or bf16 [experts, K]),
+    routed as moe_route does, and the experts' products as moe_gate_up (packed with gate_up=True) and moe_down make them.
+    route=True: (y, Route) without the sorted slots."""
+    if stream is not None:
+        with _on(gate_up.device, stream):
+            return moe_layer(gate_up, down, router, x, top_k, score, bias, groups, top_groups, group_score, renorm, scale, route, out, workspace)
+    y = _binding.layer(gate_up._ptr, gate_up._data, down._ptr, down._data, router, x, bias, top_k, SCORES[score], groups, top_groups,
+                       GROUP_SCORES[group_score], renorm, scale, route, out, workspace)
+    if type(y) is int:
+        _check(y, "qmm_moe_layer")
+    return (y[0], Route(*y[1:])) if route else y
+
+
+def moe_layer_workspace(gate_up: Q4GWeights, down: Q4GWeights, dtype: torch.dtype, T: int, top_k: int) -> int:
+    with torch.cuda.device(gate_up.device):  # a plan depends on its device
+        return int(_lib().qmm_moe_layer_workspace(gate_up._descriptor(), down._descriptor(), FLOATS[dtype], T, top_k))

@@ -383,6 +383,23 @@ size_t qmm_moe_down_workspace(const qmm_q4g* w, qmm_float xtype, int64_t T, int6
 qmm_status qmm_moe_down(const qmm_q4g* w, qmm_float xtype, const void* h, int64_t ldh, const qmm_routing* r, void* y, void* workspace,
                         size_t workspace_bytes, qmm_stream_t stream);
 
+/* A whole layer for up to QMM_MOE_LAYER_MAX_TOKENS tokens in two launches:
+     logits = x . router^T in f32 (router [experts][K] of router_type,
+     contiguous, 16-byte aligned), routed as qmm_moe_route does with cfg and
+     bias; y = what qmm_moe_down makes of qmm_moe_gate_up's h (which is rounded
+     to x's type between the two).
+   gate_up: paired, N = 2 F; down: as many experts, K = F.  ids and weights
+   [T][top_k] (both or neither) take the routing.  y [T][down.N] contiguous.
+   workspace: qmm_moe_layer_workspace(...) bytes, uninitialised; calls that may
+   overlap need one each.  SHAPE also where rows are too long for shared memory
+   (some 20000 values in f32, 60000 in 16 bits).
+   Errors as qmm_q4g_matmul. */
+#define QMM_MOE_LAYER_MAX_TOKENS 32
+size_t qmm_moe_layer_workspace(const qmm_q4g* gate_up, const qmm_q4g* down, qmm_float xtype, int64_t T, int64_t top_k);
+qmm_status qmm_moe_layer(const qmm_q4g* gate_up, const qmm_q4g* down, const qmm_route_config* cfg, qmm_float router_type, const void* router,
+                         const float* bias, qmm_float xtype, const void* x, int64_t ldx, int64_t T, void* y, int32_t* ids, float* weights,
+                         void* workspace, size_t workspace_bytes, qmm_stream_t stream);
+
 /* ---------------------------------------------------------------------------
    8-bit products with one scale per output channel and one per activation row.
    (The pages pair Q8_0 weights with activations quantized in blocks of 32; here
@@ -467,7 +484,7 @@ qmm_status qmm_block_norm(const qmm_norm* n, int64_t T, int64_t K, qmm_stream_t 
    qmm_test_inject arms an injected failure, consumed by the next `count`
    calls that reach it; QMM_INJECT_OFF disarms every kind.
    - QMM_INJECT_LAUNCH_FAILURE: qmm_matmul, qmm_block_sums, qmm_q4g_matmul,
-     qmm_moe_route, qmm_moe_gate_up, qmm_moe_down, qmm_q8c_quantize, qmm_q8c_matmul
+     qmm_moe_route, qmm_moe_gate_up, qmm_moe_down, qmm_moe_layer, qmm_q8c_quantize, qmm_q8c_matmul
      and qmm_block_norm return QMM_ERR_CUDA at once, as if the launch had failed, without any CUDA call
      (the outputs are not touched).
    - QMM_INJECT_STALL: the next decode-kernel launch (qmm_dmma_kernel, the
@@ -478,7 +495,9 @@ qmm_status qmm_block_norm(const qmm_norm* n, int64_t T, int64_t K, qmm_stream_t 
      is undefined; later calls are unaffected.  The next launch of the 4-bit
      or the 8-bit GEMM stalls in the same way: one block (of its pairs, where it works in
      pairs, the second of the first) copies `arg` tiles of its weights and no
-     more.  Whichever is launched first takes the injection.
+     more.  In the next qmm_moe_layer one share of
+     the first products is never reported done.  Whichever is launched first
+     takes the injection.
    qmm_test_set_wait_limit sets the bounded waits' spin limit on the current
    device to 2^log2_clocks SM clocks (16..31; 0 restores the default 2^31,
    about one second), so that an injected stall ends in milliseconds.  It
