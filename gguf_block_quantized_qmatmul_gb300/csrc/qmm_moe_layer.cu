@@ -6,6 +6,7 @@ namespace qmm {
 
 cudaError_t launch_moe_layer_f16(const MoePlan& pl, const MoeParams& p, int smem_max, cudaStream_t s);
 cudaError_t launch_moe_layer_bf16(const MoePlan& pl, const MoeParams& p, int smem_max, cudaStream_t s);
+cudaError_t launch_moe_layer_f32(const MoePlan& pl, const MoeParams& p, int smem_max, cudaStream_t s);
 
 namespace {
 
@@ -38,9 +39,10 @@ __global__ void __launch_bounds__(256) moe_router_kernel(const void* x, int xt, 
                                                          unsigned* counters) {
     __shared__ float red[8][8];
     const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31, e = blockIdx.x;
-    grid_dep_launch();
     const uint8_t* w = static_cast<const uint8_t*>(router) + (long long)e * K * x_size(rt);
+    // the next launch reads x before this one has completed: it may start only now that x is there
     grid_dep_wait();
+    grid_dep_launch();
     if (e == 0 && tid < 4) counters[tid] = 0u;
     for (int t0 = 0; t0 < T; t0 += 8) {
         float acc[8];
@@ -76,61 +78,43 @@ __global__ void __launch_bounds__(256) moe_router_kernel(const void* x, int xt, 
     }
 }
 
-QgCall call_of(int op, const QgWeights& w, int xt, int T, int k) {
-    QgCall c = {};
-    c.op = op;
-    c.w = w;
-    c.xt = xt;
-    c.ldx = w.K;
-    c.M = T * k;
-    c.r.T = T;
-    c.r.top_k = k;
-    return c;
-}
-
-QgRowsParams params_of(const QgRowsPlan& pl, const QgCall& c, void* part) {
-    QgRowsParams p;
-    p.c = c;
-    p.part = static_cast<float*>(part);
-    p.by_slot = pl.by_slot;
-    p.cols = pl.cols;
-    p.np = pl.np;
-    p.wk = pl.wk;
-    p.wr = pl.warps / pl.wk;
-    p.wk_log2 = pl.wk == 1 ? 0 : pl.wk == 2 ? 1 : pl.wk == 4 ? 2 : 3;
-    p.off_zero = pl.off_zero;
-    p.off_red = pl.off_red;
-    p.off_ring = pl.off_ring;
-    return p;
-}
-
 }  // namespace
 
 MoePlan plan_moe_layer(const MoeCall& c, int sms, int smem_max) {
     MoePlan pl;
-    const int T = c.T, k = c.route.top_k, S = T * k, E = c.up.E;
+    const int T = c.T, k = c.route.top_k, S = T * k, E = c.up.E, np = c.xt == X_F32 ? 3 : 1;
     if (T < 1 || T > kMoeMaxTokens || E > kQgRowMaxE) return pl;
-    const int route = round_up((3 * S + 2 * E + 1) * 4, 16), room = smem_max - 4096 - route;
-    // one number of column blocks for both products; a second one pays where experts have more rows than one holds
-    const int np = c.xt == X_F32 ? 3 : 1;
-    for (int nb = (S + E - 1) / E * np > 8 ? 2 : 1; nb >= 1 && !pl.ok; --nb) {
-        pl.up = plan_q4g_rows(call_of(P_GATE_UP, c.up, c.xt, T, k), sms, room, kMoeWarps, nb);
-        pl.down = plan_q4g_rows(call_of(P_DOWN, c.down, c.xt, T, k), sms, room, kMoeWarps, nb);
-        pl.nb = nb;
-        pl.ok = pl.up.ok && pl.down.ok;
-    }
-    if (!pl.ok) return pl;
-    pl.blocks = sms;
-    size_t most = pl.up.smem > pl.down.smem ? pl.up.smem : pl.down.smem;
-    const size_t picks = (size_t)kMoeWarps * E * 4;
-    if (most < picks) most = picks;
-    pl.off_route = (int)((most + 15) / 16 * 16);
+    // shared memory: activations, a zero, the parts of row blocks, the rings, the routing
+    const int seg = qg_seg_bytes(c.up.ng > c.down.ng ? c.up.ng : c.down.ng), ring = kMoeWarps * kMoeDepth * seg;
+    const int route = round_up((6 * S + 2 * E) * 4, 16);
+    const int room = smem_max - kMoeStatic - 1024 - 16 - kMoePart - ring - route;
+    const long long up_row = (long long)np * c.up.KS * 256, down_row = (long long)np * c.down.KS * 256;  // a token's, a slot's staged bytes
+    // a token's second products end to end while few tokens share an expert: no partial sums to add later
+    pl.token = T <= 4 && k * down_row <= room;
+    pl.whole = T * up_row <= room;
+    pl.cols = c.xt == X_F32 ? 2 : 8;
+    if (pl.cols > T) pl.cols = T;
+    while (pl.cols > 1 && ((!pl.whole && pl.cols * up_row > room) || (!pl.token && pl.cols * down_row > room))) --pl.cols;
+    const long long up_item = pl.cols * up_row, down_item = pl.token ? k * down_row : pl.cols * down_row;
+    if (room < 0 || (!pl.whole && up_item > room) || down_item > room) return pl;
+    auto most = [&](long long item) { return (int)(room / item < kMoeItems ? room / item : kMoeItems); };
+    pl.up_items = pl.whole ? kMoeItems : most(up_item);
+    pl.down_items = most(down_item);
+    long long act = pl.whole ? T * up_row : pl.up_items * up_item;
+    if (act < pl.down_items * down_item) act = pl.down_items * down_item;
+    if ((long long)S * c.up.RB * (c.up.KS > c.down.KS ? c.up.KS : c.down.KS) > INT32_MAX || (long long)S * c.down.RB * c.down.KS > INT32_MAX) return pl;
+    pl.off_zero = (int)act;
+    pl.off_part = pl.off_zero + 16;
+    pl.off_ring = pl.off_part + kMoePart;
+    pl.off_route = pl.off_ring + ring;
     pl.smem = (size_t)pl.off_route + route;
+    pl.blocks = sms;
     auto r256 = [](size_t v) { return (v + 255) / 256 * 256; };
     pl.ws_logits = 256;
     pl.ws_h = pl.ws_logits + r256((size_t)T * ((E + 3) / 4 * 4) * 4);
     pl.ws_part = pl.ws_h + r256((size_t)S * c.down.K * x_size(c.xt));
-    pl.workspace = pl.ws_part + pl.down.workspace;
+    pl.workspace = pl.ws_part + (pl.token ? 0 : (size_t)S * c.down.N * 4);
+    pl.ok = true;
     return pl;
 }
 
@@ -151,19 +135,26 @@ cudaError_t launch_moe_layer(const MoePlan& pl, const MoeCall& c, void* ws, unsi
     p.route.c.E = E;
     p.epl16 = E > 128;
     route_lanes(p.route, p.epl16 ? 16 : 4);
-    QgCall up = call_of(P_GATE_UP, c.up, c.xt, c.T, c.route.top_k), down = call_of(P_DOWN, c.down, c.xt, c.T, c.route.top_k);
-    up.x = c.x;
-    up.ldx = c.ldx;
-    up.y = b + pl.ws_h;
-    down.x = up.y;
-    down.y = c.y;
-    p.up = params_of(pl.up, up, nullptr);
-    p.down = params_of(pl.down, down, b + pl.ws_part);
+    p.up = c.up;
+    p.down = c.down;
+    p.x = c.x;
+    p.ldx = c.ldx;
+    p.xt = c.xt;
+    p.h = b + pl.ws_h;
+    p.part = reinterpret_cast<float*>(b + pl.ws_part);
+    p.y = c.y;
     p.counters = counters;
     p.err = err;
+    p.cols = pl.cols;
+    p.whole = pl.whole;
+    p.up_items = pl.up_items;
+    p.down_items = pl.down_items;
+    p.off_zero = pl.off_zero;
+    p.off_part = pl.off_part;
+    p.off_ring = pl.off_ring;
     p.off_route = pl.off_route;
     p.stall = stall;
-    return c.xt == X_F16 ? launch_moe_layer_f16(pl, p, smem_max, s) : launch_moe_layer_bf16(pl, p, smem_max, s);
+    return c.xt == X_F16 ? launch_moe_layer_f16(pl, p, smem_max, s) : c.xt == X_BF16 ? launch_moe_layer_bf16(pl, p, smem_max, s) : launch_moe_layer_f32(pl, p, smem_max, s);
 }
 
 }  // namespace qmm

@@ -3,21 +3,33 @@
 //
 // Mathematics: that of the four calls that it stands for.  l = x R^T in f32;
 // the routing of qmm_moe_route.cu; h = silu(x Wg^T) (x Wu^T) of each token's
-// experts, rounded to the activations' type; y = sum_j p_j (h_j Wd^T).
+// experts, rounded to the activations' type; y = sum_j p_j (h_j Wd^T).  The
+// products are the row kernel's (qmm_q4g_rows.cuh): codes less their zero point
+// are exact operands of f16 or bf16 warp MMAs, group sums are scaled in f32, an
+// f32 activation is three bf16 pieces.
 //
-// A decode step's layer reads a few MB of weights per SM's share, so what
-// stands between the products is what costs: a launch, its ramp and its tail
-// each time.  The first launch forms the logits (a block per expert).  In the
-// second every block routes all tokens for itself (some microseconds of one
-// warp a token, no exchange), then takes shares of the work by tickets: first
-// the shares of the experts' first products, then those of the second ones,
-// which wait until all of the first are reported, and with more than a token an
-// item those of the tokens' sums.  A ticket's holder runs already when it waits,
-// and what it waits for are shares with lower tickets, whose holders do not wait
-// for it: however few blocks are on the GPU at a time, the layer ends.  The
-// weights of a second product are on their way before its block waits, as the
-// experts are known.  The products themselves are the row kernel's
-// (qmm_q4g_rows.cuh, qg_rows_share).
+// A decode step's layer reads a few MB of weights, 100 KB an SM, so what stands
+// between the products is what costs.  The first launch forms the logits (a
+// block per expert).  In the second every block routes all tokens for itself
+// (a warp a token, no exchange), then takes shares of the work by tickets: first
+// shares of the experts' first products, then of the second ones, which wait
+// until all of the first are reported, and, unless an item is a token, of the
+// tokens' sums.  A ticket's holder runs already when it waits, and what it waits
+// for are shares with lower tickets, whose holders do not wait for it: however
+// few blocks are on the GPU at a time, the layer ends.  The tokens are staged
+// beside the first launch, and the second products' weights are on their way
+// before their block waits.
+//
+// A share is row blocks of items, end to end.  An item is an expert with up to 8
+// (f32: 2) of its tokens, the MMA's columns; for up to 4 tokens the second
+// products' items are tokens, whose experts' segments are one long row.  A share's
+// segments of 16 x 128 weights are dealt to the block's warps in equal
+// contiguous runs, wherever row blocks end, so that no warp has more to do than
+// another; each streams its own through a ring of asynchronous copies, and no
+// warp waits for another until the end, where the parts of row blocks that were
+// cut are added in shared memory, in the order of K.  (Whole row blocks to groups of
+// warps, as the row kernel deals them: 16 tokens of 64 experts 31 us for the
+// first products, and 8 more in blocks whose share held two experts.)
 //
 // Waits are bounded: one that gives up raises the error word and its block ends.
 #pragma once
@@ -28,14 +40,25 @@
 namespace qmm {
 
 constexpr int kMoeWarps = 16, kMoeThreads = kMoeWarps * 32;
+constexpr int kMoeDepth = 6;     // segments in a warp's ring
+constexpr int kMoeItems = 8;     // items of a share that are staged together, at most
+constexpr int kMoeStatic = 1024; // the kernel's static arrays, rounded up
+constexpr int kMoePart = kMoeWarps * 2 * 512;  // bytes of the parts of row blocks
 
 struct MoeParams {
     RouteParams route;   // c.ids, c.weights: for the caller, or NULL
-    QgRowsParams up, down;
+    QgWeights up, down;
+    const void* x;
+    long long ldx;
+    int xt;
+    void* h;             // [T top_k][F]
+    float* part;         // [T top_k][N]: the experts' second products, unless items are tokens
+    void* y;
     unsigned* counters;  // [0] tickets, [1] shares of the first products done, [2] of the second
     unsigned* err;
     int epl16;           // experts per lane in the routing: 16, or 4
-    int off_route;
+    int cols, whole, up_items, down_items;
+    int off_zero, off_part, off_ring, off_route;
     int stall;
 };
 
@@ -63,90 +86,345 @@ static __device__ __noinline__ bool moe_wait(const unsigned* p, unsigned n, unsi
     return true;
 }
 
-// The rows of a product that others' shares make: waited for once.
-struct MoeWait {
-    const unsigned* done;  // NULL: nothing to wait for
-    unsigned n;
-    unsigned* err;
-    int* s_ok;
-    __device__ __forceinline__ void route() {}
-    __device__ __forceinline__ bool rows() {
-        if (!done) return true;
-        if (threadIdx.x == 0) *s_ok = moe_wait(done, n, err);
-        __syncthreads();
-        done = nullptr;
-        return *s_ok != 0;
-    }
+// An item of an expert: its tokens' slots are order[first .. first + n).
+struct MoeItem {
+    int expert, first, n;
+};
+// The routing, in shared memory.
+struct MoeShared {
+    const int* ids;         // [T][top_k]
+    const float* weights;
+    const int* order;       // slots by expert
+    const MoeItem* items;
+    int T, k;
 };
 
-template <int NB, bool BF, bool TOKEN>
+// Where a share's segments are: run r (KS segments of one row block of one expert) of a batch that
+// begins with row block rb0 of item i0.
+template <bool TOKEN>
+struct MoeRun {
+    int item, rb, j;  // TOKEN: choice j of token `item`
+    __device__ __forceinline__ MoeRun(const MoeShared& sh, int i0, int rb0, int RB, int r) {
+        int u = r;
+        j = 0;
+        if (TOKEN) {
+            u = r / sh.k;
+            j = r - u * sh.k;
+        }
+        const int b = rb0 + u;
+        const int di = b / RB;
+        item = i0 + di;
+        rb = b - di * RB;
+    }
+    // true: a row block is complete
+    __device__ __forceinline__ bool next(const MoeShared& sh, int RB) {
+        if (TOKEN && ++j < sh.k) return false;
+        j = 0;
+        if (++rb == RB) {
+            rb = 0;
+            ++item;
+        }
+        return true;
+    }
+    __device__ __forceinline__ int expert(const MoeShared& sh) const { return TOKEN ? sh.ids[item * sh.k + j] : sh.items[item].expert; }
+};
+
+// Row blocks w0 .. w1 of one product's items.  UP: the first product, x to h; else the second, h to part
+// (TOKEN: y).  wait() (false: give up) comes before the activations are read.
+template <bool BF, bool F32, int NG, bool UP, bool TOKEN, class Wait>
+__device__ __forceinline__ bool moe_share(const MoeParams& p, const QgWeights& w, uint8_t* sm, const MoeShared& sh, int w0, int w1, Wait wait) {
+    const int tid = threadIdx.x, warp = __shfl_sync(0xffffffffu, tid >> 5, 0), lane = tid & 31, g = lane >> 2, t = lane & 3;
+    constexpr int seg_bytes = qg_seg_bytes(NG), segk = 128 / NG, np = F32 ? 3 : 1;
+    const int KS = w.KS, RB = w.RB, kk = TOKEN ? sh.k : 1;  // runs per row block
+    const long long rb_bytes = (long long)KS * seg_bytes;
+    uint8_t* ring = sm + p.off_ring + warp * (kMoeDepth * seg_bytes);
+    float4* parts = reinterpret_cast<float4*>(sm + p.off_part);  // [warp][2][32]: a row block's part that does not reach its end: 1; that does: 0
+    const uint32_t magic = opaque(kQgMagic<BF>);
+    const bool whole = UP && p.whole;
+    // a staged item: [32 K][columns] of 64 bytes
+    const int item_bytes = (TOKEN ? sh.k : p.cols) * np * KS * 256;
+    const int batch = UP ? (whole ? kMoeItems * 16 : p.up_items) : p.down_items;
+    bool ok = true;
+    for (int b0 = w0; b0 < w1;) {
+        const int i0 = b0 / RB, rb0 = b0 - i0 * RB;
+        const int b1 = min(w1, (i0 + batch) * RB);
+        // this warp's segments of the batch
+        const int units = b1 - b0, per = kk * KS, total = units * per;
+        const int s0 = (int)((long long)warp * total / kMoeWarps), s1 = (int)((long long)(warp + 1) * total / kMoeWarps);
+        int lleft = s1 - s0, lrem = KS - s0 % KS, ls = 0;
+        MoeRun<TOKEN> lr(sh, i0, rb0, RB, s0 / KS);
+        const uint8_t* lp = nullptr;
+        auto place = [&](int seg) { lp = w.data + (long long)lr.expert(sh) * w.expert_stride + lr.rb * rb_bytes + seg * seg_bytes + lane * 16; };
+        if (lleft > 0) place(KS - lrem);
+        const uint32_t to = smem_u32(ring) + lane * 16;
+        auto load = [&]() {  // a group of copies, empty past the end, so that the groups' count is the ring's
+            if (lleft > 0) {
+                const uint32_t d = to + ls * seg_bytes;
+                cp_async16(d, lp);
+                cp_async16(d + kQgTile, lp + kQgTile);
+                if (lane < 4 * NG) cp_async16(d + 2 * kQgTile, lp + 2 * kQgTile);
+                lp += seg_bytes;
+                --lleft;
+                if (--lrem == 0 && lleft > 0) {
+                    lrem = KS;
+                    lr.next(sh, RB);
+                    place(0);
+                }
+            }
+            ls = ls + 1 == kMoeDepth ? 0 : ls + 1;
+            cp_async_commit();
+        };
+#pragma unroll
+        for (int i = 0; i < kMoeDepth - 1; ++i) load();
+        if (!(ok = wait())) break;
+        if (!whole) {
+            const int i1 = (b1 - 1) / RB;
+            for (int it = i0; it <= i1; ++it) {
+                uint8_t* area = sm + (it - i0) * item_bytes;
+                if (TOKEN) {
+                    for (int j = 0; j < sh.k; ++j)
+                        qg_stage(area, p.h, p.xt, w.K, KS, 1, np, j * KS, [&](int) { return ((long long)it * sh.k + j) * w.K; }, tid, kMoeThreads);
+                } else {
+                    const MoeItem m = sh.items[it];
+                    qg_stage(area, UP ? p.x : p.h, p.xt, w.K, KS, m.n, np, 0, [&](int r) {
+                        const int slot = sh.order[m.first + r];
+                        return UP ? slot / sh.k * p.ldx : (long long)slot * w.K;
+                    }, tid, kMoeThreads);
+                }
+            }
+            __syncthreads();
+        }
+
+        float acc[4] = {0.0f, 0.0f, 0.0f, 0.0f};
+        // This lane's activations: at xo, xq bytes from 32 K to the next (0: it has no column).  Column g is
+        // token g of the item, or piece g % 4 of token g / 4.
+        int xo = 0, xq = 0;
+        float wt = 1.0f;
+        auto columns = [&](const MoeRun<TOKEN>& r, int seg) {
+            const int n = TOKEN ? 1 : sh.items[r.item].n, c = F32 ? g >> 2 : g, pc = F32 ? g & 3 : 0;
+            if (c < n && pc < np) {
+                int base, ncol;
+                if (whole) {
+                    ncol = sh.T * np;
+                    base = (sh.order[sh.items[r.item].first + c] / sh.k * np + pc) * 64;
+                } else {
+                    ncol = n * np;
+                    base = (r.item - i0) * item_bytes + (c * np + pc) * 64 + (TOKEN ? r.j * KS * 4 * ncol * 64 : 0);
+                }
+                xq = ncol * 64;
+                xo = base + seg * 4 * xq + t * 16;
+            } else {
+                xq = 0;
+                xo = p.off_zero;
+            }
+            if (TOKEN) wt = sh.weights[r.item * sh.k + r.j];
+        };
+        // a row block's 16 x 8 sums to their place
+        auto put = [&](float v[4], int item, int rb) {
+            if (F32) {  // pieces 0, 1 are one lane's, piece 2 its neighbour's
+#pragma unroll
+                for (int i = 0; i < 4; i += 2) {
+                    v[i] += v[i + 1];
+                    v[i] += __shfl_xor_sync(0xffffffffu, v[i], 1);
+                }
+            }
+            constexpr float unit = BF ? 1.0f / kQgCodeUnit : 1.0f;
+            const int n = TOKEN ? 1 : sh.items[item].n;
+#pragma unroll
+            for (int i = 0; i < (F32 ? 1 : 2); ++i) {
+                const int c = F32 ? t >> 1 : 2 * t + i;
+                if (c >= n || (F32 && (t & 1))) continue;
+                const float lo = v[i] * unit, hi = v[i + 2] * unit;
+                if (UP) {
+                    const int f = rb * 8 + g, F = w.N / 2;
+                    const long long slot = sh.order[sh.items[item].first + c];
+                    if (f < F) x_store(p.h, p.xt, slot * F + f, swiglu(lo, hi));
+                } else {
+                    const int row = rb * 16 + g;
+                    if (TOKEN) {
+                        if (row < w.N) x_store(p.y, p.xt, (long long)item * w.N + row, lo);
+                        if (row + 8 < w.N) x_store(p.y, p.xt, (long long)item * w.N + row + 8, hi);
+                    } else {
+                        float* out = p.part + (long long)sh.order[sh.items[item].first + c] * w.N;
+                        if (row < w.N) out[row] = lo;
+                        if (row + 8 < w.N) out[row + 8] = hi;
+                    }
+                }
+            }
+        };
+        // The row block that this warp completes but did not begin, which it puts in its place at the end.
+        int cut = -1, cut_item = 0, cut_rb = 0;
+        MoeRun<TOKEN> r(sh, i0, rb0, RB, s0 / KS);
+        int cs = 0, seg = s0 % KS;  // ring place, segment in the run
+        int first = s0 - s0 % per, begin = s0;  // where the row block and this warp's part of it begin
+        for (int i = s0; i < s1; seg = 0) {
+            const int end = min(s1, i - seg + KS);
+            const bool run_done = end == i - seg + KS;
+            columns(r, seg);
+            for (; i < end; ++i) {
+                cp_async_wait<kMoeDepth - 2>();
+                __syncwarp();  // every lane's copies of this segment have landed, and the last one has been read
+                load();
+                const uint8_t* sp = ring + cs * seg_bytes;
+                cs = cs + 1 == kMoeDepth ? 0 : cs + 1;
+                const uint4 c0 = reinterpret_cast<const uint4*>(sp)[lane], c1 = reinterpret_cast<const uint4*>(sp + kQgTile)[lane];
+                uint32_t sw[2 * NG];
+                const uint8_t* sq = sp + 2 * kQgTile + g * (8 * NG);
+                if (NG == 1) {
+                    const uint2 u = *reinterpret_cast<const uint2*>(sq);
+                    sw[0] = u.x;
+                    sw[1] = u.y;
+                } else {
+#pragma unroll
+                    for (int q = 0; q < NG / 2; ++q) {
+                        const uint4 u = reinterpret_cast<const uint4*>(sq)[q];
+                        sw[4 * q] = u.x;
+                        sw[4 * q + 1] = u.y;
+                        sw[4 * q + 2] = u.z;
+                        sw[4 * q + 3] = u.w;
+                    }
+                }
+                float gr[4];
+                uint32_t zl = 0, zh = 0;
+#pragma unroll
+                for (int q4 = 0; q4 < 4; ++q4) {  // 32 K a step
+                    const int gi = q4 * 32 / segk;
+                    const uint32_t sw0 = sw[2 * gi], sw1 = sw[2 * gi + 1];
+                    const bool start = q4 * 32 % segk == 0;
+                    if (start) {
+                        zl = qg_zero<BF>(sw0, false);
+                        zh = qg_zero<BF>(sw1, true);
+                    }
+                    const uint4 cw = q4 < 2 ? c0 : c1;
+                    uint32_t a0[4], a1[4];
+                    qg_codes<BF>(q4 & 1 ? cw.z : cw.x, magic, zl, zh, a0);
+                    qg_codes<BF>(q4 & 1 ? cw.w : cw.y, magic, zl, zh, a1);
+                    const uint4 xv = *reinterpret_cast<const uint4*>(sm + xo + q4 * xq);
+                    if (start) qg_mma<BF, true>(gr, a0, xv.x, xv.y);
+                    else qg_mma<BF, false>(gr, a0, xv.x, xv.y);
+                    qg_mma<BF, false>(gr, a1, xv.z, xv.w);
+                    if ((q4 + 1) * 32 % segk == 0) {  // the group's end
+                        const float f0 = TOKEN ? qg_scale(sw0) * wt : qg_scale(sw0), f1 = TOKEN ? qg_scale(sw1) * wt : qg_scale(sw1);
+                        acc[0] = fmaf(f0, gr[0], acc[0]);
+                        acc[1] = fmaf(f0, gr[1], acc[1]);
+                        acc[2] = fmaf(f1, gr[2], acc[2]);
+                        acc[3] = fmaf(f1, gr[3], acc[3]);
+                    }
+                }
+                xo += 4 * xq;
+            }
+            const int item = r.item, rb = r.rb;
+            const bool done = run_done && r.next(sh, RB);
+            if (!done && i < s1) continue;  // TOKEN: the next choice
+            if (done && begin == first) {
+                put(acc, item, rb);
+            } else {
+                parts[(warp * 2 + (done ? 0 : 1)) * 32 + lane] = make_float4(acc[0], acc[1], acc[2], acc[3]);
+                if (done) {
+                    cut = first;
+                    cut_item = item;
+                    cut_rb = rb;
+                }
+            }
+            acc[0] = acc[1] = acc[2] = acc[3] = 0.0f;
+            first = begin = i;
+        }
+        cp_async_wait<0>();
+        __syncthreads();  // all parts are there, and the activations are no longer read
+        if (cut >= 0) {
+            int from = warp - 1;
+            while ((int)((long long)from * total / kMoeWarps) > cut) --from;
+            float v[4] = {0.0f, 0.0f, 0.0f, 0.0f};
+            for (int o = from; o <= warp; ++o) {
+                if ((int)((long long)o * total / kMoeWarps) == (int)((long long)(o + 1) * total / kMoeWarps)) continue;  // no segments
+                const float4 u = parts[(o * 2 + (o == warp ? 0 : 1)) * 32 + lane];
+                v[0] += u.x;
+                v[1] += u.y;
+                v[2] += u.z;
+                v[3] += u.w;
+            }
+            put(v, cut_item, cut_rb);
+        }
+        b0 = b1;
+        if (b0 < w1) __syncthreads();  // the parts have been read
+    }
+    cp_async_wait<0>();
+    return ok;
+}
+
+template <bool BF, bool F32, bool TOKEN>
 __global__ void __launch_bounds__(kMoeThreads, 1) moe_layer_kernel(const __grid_constant__ MoeParams p) {
     extern __shared__ __align__(16) uint8_t sm[];
-    __shared__ int s_e[kQgMaxK];
-    __shared__ float s_wt[kQgMaxK];
-    __shared__ int s_row[64];
-    __shared__ int ts_up[kQgRowMaxE + 1], ts_down[kQgRowMaxE + 1];
-    __shared__ int s_ok;
+    __shared__ int s_ok, s_items;
     __shared__ unsigned s_ticket[2];
     const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
     const int T = p.route.c.T, E = p.route.c.E, k = p.route.c.top_k, S = T * k;
-    int* ids = reinterpret_cast<int*>(sm + p.off_route);      // [S]
-    float* weights = reinterpret_cast<float*>(ids + S);       // [S]
-    int* order = reinterpret_cast<int*>(weights + S);         // [S]
-    int* offsets = order + S;                                 // [E + 1]
-    uint32_t* mask = reinterpret_cast<uint32_t*>(offsets + E + 1);  // [E] the tokens that chose an expert
+    int* ids = reinterpret_cast<int*>(sm + p.off_route);             // [S]
+    float* weights = reinterpret_cast<float*>(ids + S);              // [S]
+    int* order = reinterpret_cast<int*>(weights + S);                // [S]
+    MoeItem* items = reinterpret_cast<MoeItem*>(order + S);          // [S]
+    int* offsets = reinterpret_cast<int*>(items + S);                // [E]
+    uint32_t* mask = reinterpret_cast<uint32_t*>(offsets + E);       // [E] the tokens that chose an expert
+    uint32_t* picks = reinterpret_cast<uint32_t*>(sm + p.off_ring);  // [warps][E], where the rings will be
     for (int e = tid; e < E; e += kMoeThreads) mask[e] = 0u;
+    if (tid == 0) *reinterpret_cast<uint4*>(sm + p.off_zero) = make_uint4(0u, 0u, 0u, 0u);  // what lanes without a column read
     grid_dep_launch();
-    __syncthreads();
+    // The first launch lets this one start only when what it depends on itself has completed, so the
+    // tokens are there.
+    if (p.whole) qg_stage(sm, p.x, p.xt, p.up.K, p.up.KS, T, F32 ? 3 : 1, 0, [&](int r) { return r * p.ldx; }, tid, kMoeThreads);
     grid_dep_wait();
     unsigned next = 0;  // thread 0: the next ticket
     if (tid == 0) next = atomicAdd(p.counters, 1u);
+    __syncthreads();
 
     // ------------------------------ routing ------------------------------
     RouteParams rp = p.route;
     rp.c.ids = ids;
     rp.c.weights = weights;
-    uint32_t* picks = reinterpret_cast<uint32_t*>(sm) + warp * E;  // where the products' rings will be
     for (int t = warp; t < T; t += kMoeWarps) {
-        const int id = p.epl16 ? route_token<16>(rp, t, picks, lane) : route_token<4>(rp, t, picks, lane);
+        const int id = p.epl16 ? route_token<16>(rp, t, picks + warp * E, lane) : route_token<4>(rp, t, picks + warp * E, lane);
         if (lane < k) atomicOr(&mask[id], 1u << t);
     }
     __syncthreads();
-    const bool by_expert = !TOKEN || !p.up.by_slot;
-    if (by_expert && warp == 0) {
-        // slots sorted by expert, by token within one: a count is a mask's population, a rank that of its lower bits
+    if (warp == 0) {
+        // Slots sorted by expert, by token within one: a count is a mask's population, a rank that of its
+        // lower bits.  First positions and items before each expert in one sum's halves (at most 1024).
         const int per = (E + 31) / 32;
-        int mine = 0;
-        for (int i = 0; i < per; ++i)
-            if (lane * per + i < E) mine += __popc(mask[lane * per + i]);
-        int pre = mine;
+        uint32_t mine = 0;
+        for (int i = 0; i < per; ++i) {
+            const int e = lane * per + i, n = e < E ? __popc(mask[e]) : 0;
+            mine += (uint32_t)n | (uint32_t)((n + p.cols - 1) / p.cols) << 16;
+        }
+        uint32_t pre = mine;
 #pragma unroll
         for (int o = 1; o < 32; o <<= 1) {
-            const int u = __shfl_up_sync(0xffffffffu, pre, o);
+            const uint32_t u = __shfl_up_sync(0xffffffffu, pre, o);
             if (lane >= o) pre += u;
         }
-        if (lane == 31) offsets[E] = pre;
+        if (lane == 31) s_items = (int)(pre >> 16);
         pre -= mine;
         for (int i = 0; i < per; ++i) {
             const int e = lane * per + i;
             if (e >= E) break;
-            offsets[e] = pre;
-            pre += __popc(mask[e]);
+            const int n = __popc(mask[e]);
+            offsets[e] = (int)(pre & 0xffffu);
+            for (int c = 0; c < n; c += p.cols) {
+                items[pre >> 16] = MoeItem{e, (int)(pre & 0xffffu) + c, min(p.cols, n - c)};
+                pre += 1u << 16;
+            }
+            pre += (uint32_t)n;
         }
-        __syncwarp();
-        for (int s = lane; s < S; s += 32) {
-            const int t = s / k, e = ids[s];
-            order[offsets[e] + __popc(mask[e] & ((1u << t) - 1u))] = s;
-        }
-        __syncwarp();
-        if (!p.up.by_slot) qg_rows_items(offsets, E, S, p.up.cols, ts_up, lane);
-        if (!TOKEN) qg_rows_items(offsets, E, S, p.down.cols, ts_down, lane);
     }
-    if (blockIdx.x == 0 && p.route.c.ids)
-        for (int s = tid; s < S; s += kMoeThreads) {
-            p.route.c.ids[s] = ids[s];
+    __syncthreads();
+    for (int s = tid; s < S; s += kMoeThreads) {
+        const int t = s / k, e = ids[s];
+        order[offsets[e] + __popc(mask[e] & ((1u << t) - 1u))] = s;
+        if (blockIdx.x == 0 && p.route.c.ids) {
+            p.route.c.ids[s] = e;
             p.route.c.weights[s] = weights[s];
         }
+    }
+    const MoeShared sh = {ids, weights, order, items, T, k};
 
     // ------------------------------ shares ------------------------------
     const unsigned G = gridDim.x, total = TOKEN ? 2 * G : 3 * G;
@@ -157,58 +435,54 @@ __global__ void __launch_bounds__(kMoeThreads, 1) moe_layer_kernel(const __grid_
         if (ticket >= total) break;
         if (tid == 0) next = atomicAdd(p.counters, 1u);
         const unsigned phase = ticket / G, i = ticket - phase * G;
-        if (phase == 2) {
-            // a token's second products, in the order of its choices
-            if (tid == 0) s_ok = moe_wait(p.counters + 2, G, p.err);
+        // what others make: waited for by one thread
+        bool waited = false;
+        auto wait = [&](unsigned which) {
+            if (waited) return true;
+            waited = true;
+            if (tid == 0) s_ok = moe_wait(p.counters + which, G, p.err);
             __syncthreads();
-            if (!s_ok) break;
-            const QgCall& c = p.down.c;
-            const int N = c.w.N;
-            const long long n = (long long)T * N, o1 = (long long)(i + 1) * n / G;
-            for (long long o = (long long)i * n / G + tid; o < o1; o += kMoeThreads) {
-                const int t = (int)(o / N), col = (int)(o - (long long)t * N);
-                float v = 0.0f;
-#pragma unroll 8
-                for (int j = 0; j < k; ++j) v = fmaf(weights[t * k + j], __ldcg(p.down.part + (long long)(t * k + j) * N + col), v);
-                x_store(c.y, c.xt, o, v);
-            }
-            continue;
-        }
-        const bool second = phase == 1;
-        const QgRowsParams& q = second ? p.down : p.up;
-        const int* ts = second ? ts_down : ts_up;
-        const long long items = second ? (TOKEN ? T : ts[E]) : q.by_slot ? S : ts[E];
-        const long long work = items * q.c.w.RB, w0 = i * work / G, w1 = (i + 1) * work / G;
-        const QgRowsShared sh = {s_e, s_wt, s_row, ts, ids, weights, offsets, order};
-        MoeWait wait = {second ? p.counters + 1 : nullptr, G, p.err, &s_ok};
-        if (tid == 0) {
-            s_ok = 1;
-            *reinterpret_cast<uint4*>(sm + q.off_zero) = make_uint4(0u, 0u, 0u, 0u);  // what lanes without a column read
-        }
-        if (second) {
-            if (q.c.w.ng == 1) qg_rows_share<TOKEN ? 1 : NB, BF, 1, TOKEN>(q, sm, sh, w0, w1, wait);
-            else if (q.c.w.ng == 2) qg_rows_share<TOKEN ? 1 : NB, BF, 2, TOKEN>(q, sm, sh, w0, w1, wait);
-            else qg_rows_share<TOKEN ? 1 : NB, BF, 4, TOKEN>(q, sm, sh, w0, w1, wait);
+            return s_ok != 0;
+        };
+        bool ok;
+        if (phase == 0) {
+            const int work = s_items * p.up.RB, w0 = (int)((long long)i * work / G), w1 = (int)((long long)(i + 1) * work / G);
+            auto no = [] { return true; };
+            if (p.up.ng == 1) ok = moe_share<BF, F32, 1, true, false>(p, p.up, sm, sh, w0, w1, no);
+            else if (p.up.ng == 2) ok = moe_share<BF, F32, 2, true, false>(p, p.up, sm, sh, w0, w1, no);
+            else ok = moe_share<BF, F32, 4, true, false>(p, p.up, sm, sh, w0, w1, no);
+        } else if (phase == 1) {
+            const int work = (TOKEN ? T : s_items) * p.down.RB, w0 = (int)((long long)i * work / G), w1 = (int)((long long)(i + 1) * work / G);
+            auto first = [&] { return wait(1u); };
+            if (p.down.ng == 1) ok = moe_share<BF, F32, 1, false, TOKEN>(p, p.down, sm, sh, w0, w1, first);
+            else if (p.down.ng == 2) ok = moe_share<BF, F32, 2, false, TOKEN>(p, p.down, sm, sh, w0, w1, first);
+            else ok = moe_share<BF, F32, 4, false, TOKEN>(p, p.down, sm, sh, w0, w1, first);
         } else {
-            if (q.c.w.ng == 1) qg_rows_share<NB, BF, 1, false>(q, sm, sh, w0, w1, wait);
-            else if (q.c.w.ng == 2) qg_rows_share<NB, BF, 2, false>(q, sm, sh, w0, w1, wait);
-            else qg_rows_share<NB, BF, 4, false>(q, sm, sh, w0, w1, wait);
+            // a token's second products, in the order of its choices
+            if ((ok = wait(2u))) {
+                const int N = p.down.N;
+                const long long n = (long long)T * N, o1 = (long long)(i + 1) * n / G;
+                for (long long o = (long long)i * n / G + tid; o < o1; o += kMoeThreads) {
+                    const int t = (int)(o / N), col = (int)(o - (long long)t * N);
+                    float v = 0.0f;
+#pragma unroll 8
+                    for (int j = 0; j < k; ++j) v = fmaf(weights[t * k + j], __ldcg(p.part + (long long)(t * k + j) * N + col), v);
+                    x_store(p.y, p.xt, o, v);
+                }
+            }
         }
-        cp_async_wait<0>();
+        if (!ok) break;
+        if (phase == 2 || (TOKEN && phase == 1)) continue;
         __syncthreads();  // every thread's results are written
-        if (!s_ok) break;
-        if (tid == 0 && !(TOKEN && second) && !(p.stall && ticket == 0)) {
-            __threadfence();
-            add_release(p.counters + 1 + phase);
-        }
+        if (tid == 0 && !(p.stall && ticket == 0)) add_release(p.counters + 1 + phase);
     }
 }
 
-template <int NB, bool BF, bool TOKEN>
+template <bool BF, bool F32, bool TOKEN>
 cudaError_t moe_layer_go(const MoePlan& pl, const MoeParams& p, int smem_max, cudaStream_t s) {
     static unsigned long long done = 0;
-    auto* k = moe_layer_kernel<NB, BF, TOKEN>;
-    const cudaError_t e = ensure_smem(k, smem_max - 8192, done);
+    auto* k = moe_layer_kernel<BF, F32, TOKEN>;
+    const cudaError_t e = ensure_smem(k, smem_max - kMoeStatic, done);
     if (e != cudaSuccess) return e;
     return launch_pdl(k, (unsigned)pl.blocks, kMoeThreads, pl.smem, s, p);
 }

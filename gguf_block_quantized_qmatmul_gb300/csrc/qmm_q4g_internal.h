@@ -53,8 +53,7 @@ struct QgRowsPlan {
     size_t smem = 0;
     size_t workspace = 0;  // P_DOWN by expert: f32 partial rows [T top_k][N]
 };
-// warps_only: 0, or the one number of warps that may be chosen; nb_most: column blocks, at most
-QgRowsPlan plan_q4g_rows(const QgCall& c, int sms, int smem_max, int warps_only = 0, int nb_most = 4);
+QgRowsPlan plan_q4g_rows(const QgCall& c, int sms, int smem_max);
 cudaError_t launch_q4g_rows(const QgRowsPlan& pl, const QgCall& c, void* ws, int smem_max, cudaStream_t s);
 
 // The tcgen05 GEMM.
@@ -104,9 +103,12 @@ struct MoeCall {
 };
 struct MoePlan {
     bool ok = false;
-    QgRowsPlan up, down;
-    int blocks = 0, nb = 0;
-    int off_route = 0;
+    int token = 0;   // the second products' items are tokens, not experts
+    int cols = 0;    // tokens per item of an expert, at most
+    int whole = 0;   // all tokens' activations are staged at once
+    int up_items = 0, down_items = 0;  // items whose activations fit beside each other
+    int blocks = 0;
+    int off_zero = 0, off_part = 0, off_ring = 0, off_route = 0;
     size_t smem = 0, ws_logits = 0, ws_h = 0, ws_part = 0, workspace = 0;
 };
 MoePlan plan_moe_layer(const MoeCall& c, int sms, int smem_max);

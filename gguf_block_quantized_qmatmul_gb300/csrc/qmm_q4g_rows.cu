@@ -84,7 +84,7 @@ cudaError_t launch_q4g_combine(const float* part, const QgRoute& r, int E, int N
                   : launch_pdl_2d(q4g_combine_kernel<1>, (unsigned)r.T, gy, 256, 0, s, part, r, E, N, y, xt);
 }
 
-QgRowsPlan plan_q4g_rows(const QgCall& c, int sms, int smem_max, int warps_only, int nb_most) {
+QgRowsPlan plan_q4g_rows(const QgCall& c, int sms, int smem_max) {
     QgRowsPlan pl;
     pl.np = c.xt == X_F32 ? 3 : 1;
     if (c.op != P_DENSE && c.w.E > kQgRowMaxE) return pl;
@@ -110,7 +110,7 @@ QgRowsPlan plan_q4g_rows(const QgCall& c, int sms, int smem_max, int warps_only,
     int choices[3] = {8 / pl.np, 16 / pl.np, 32 / pl.np}, nchoice = 3;
     if (c.op != P_DENSE) {
         const long long avg = (slots + c.w.E - 1) / c.w.E;
-        choices[0] = pl.by_slot ? 1 : avg * pl.np <= 4 || nb_most == 1 ? 8 / pl.np : avg * pl.np <= 8 || nb_most == 2 ? 16 / pl.np : 32 / pl.np;
+        choices[0] = pl.by_slot ? 1 : avg * pl.np <= 4 ? 8 / pl.np : avg * pl.np <= 8 ? 16 / pl.np : 32 / pl.np;
         nchoice = 1;
     }
     double best = 0;
@@ -133,7 +133,7 @@ QgRowsPlan plan_q4g_rows(const QgCall& c, int sms, int smem_max, int warps_only,
         if (items < 1) items = 1;
         const int nb = nb_of(cols);
         for (int warps : {24, 16, 8}) {
-            if (warps > qg_row_warps(nb) || need(cols, warps) > room || (warps_only && warps != warps_only)) continue;
+            if (warps > qg_row_warps(nb) || need(cols, warps) > room) continue;
             for (int wk = 1; wk <= 8; wk *= 2) {
                 const int wr = warps / wk, nit = (VS + wk - 1) / wk;
                 if (wr > 15 && wk > 1) continue;  // named barriers

@@ -199,47 +199,14 @@ __device__ __forceinline__ void qg_stage(uint8_t* sm, const void* x, int xt, int
 
 constexpr int kQgMaxK = 32;  // slots of one token, at most
 
-// What a block knows of its call beside the launch's parameters, in shared memory or in the routing.
-struct QgRowsShared {
-    int* s_e;          // [kQgMaxK] TOK: the token's experts (-1: skipped)
-    float* s_wt;       // [kQgMaxK] and their weights
-    int* s_row;        // [64] by expert: the columns' slots
-    const int* ts;     // [E + 1] by expert: items before each
-    const int* ids;    // the routing
-    const float* weights;
-    const int* offsets;
-    const int* order;
-};
-
-// Items before each expert, by one warp: expert e has ceil(count / cols); lane l adds up experts l per.. l per + per
-__device__ __forceinline__ void qg_rows_items(const int* offsets, int E, int slots, int cols, int* ts, int lane) {
-    const int per = (E + 31) / 32;
-    int mine = 0;
-    for (int i = 0; i < per; ++i) {
-        const int e = lane * per + i;
-        if (e < E) mine += (max(min(offsets[e + 1], slots) - max(offsets[e], 0), 0) + cols - 1) / cols;
-    }
-    int pre = mine;
-#pragma unroll
-    for (int o = 1; o < 32; o <<= 1) {
-        const int u = __shfl_up_sync(0xffffffffu, pre, o);
-        if (lane >= o) pre += u;
-    }
-    if (lane == 31) ts[E] = pre;
-    pre -= mine;
-    for (int i = 0; i < per; ++i) {
-        const int e = lane * per + i;
-        if (e >= E) break;
-        ts[e] = pre;
-        pre += (max(min(offsets[e + 1], slots) - max(offsets[e], 0), 0) + cols - 1) / cols;
-    }
-}
-
-// Row blocks w0 .. w1 of the items, end to end: a block's share.  TOK: P_DOWN with a token per item,
-// whose experts' segments are taken end to end.  wait.route() comes before the routing is read,
-// wait.rows() (false: give up) before the activations are, with the first weights on their way.
-template <int NB, bool BF, int NG, bool TOK, class Wait>
-__device__ __forceinline__ void qg_rows_share(const QgRowsParams& p, uint8_t* sm, const QgRowsShared& sh, long long w0, long long w1, Wait& wait) {
+// TOK: P_DOWN with a token per item, whose experts' segments are taken end to end.
+template <int NB, bool BF, int NG, bool TOK>
+__global__ void __launch_bounds__(qg_row_warps(NB) * 32, 1) q4g_rows_kernel(const QgRowsParams p) {
+    extern __shared__ __align__(16) uint8_t sm[];
+    __shared__ int s_e[kQgMaxK];       // TOK: the token's experts (-1: skipped)
+    __shared__ float s_wt[kQgMaxK];    // and their weights
+    __shared__ int s_row[64];          // by expert: the columns' slots
+    __shared__ int ts[kQgRowMaxE + 1]; // by expert: items before each
     const QgCall& c = p.c;
     const QgWeights& w = c.w;
     // the warp's index from one lane, so that what follows from it is known to be uniform
@@ -248,16 +215,48 @@ __device__ __forceinline__ void qg_rows_share(const QgRowsParams& p, uint8_t* sm
     constexpr int seg_bytes = qg_seg_bytes(NG), segk = 128 / NG;
     uint8_t* ring = sm + p.off_ring + warp * (kQgDepth * seg_bytes);
     const uint32_t magic = opaque(kQgMagic<BF>);
-    int* s_e = sh.s_e;
-    float* s_wt = sh.s_wt;
-    int* s_row = sh.s_row;
-    const int* ts = sh.ts;
+    if (tid == 0) *reinterpret_cast<uint4*>(sm + p.off_zero) = make_uint4(0u, 0u, 0u, 0u);  // what lanes without a column read
+    grid_dep_launch();
 
     const int nex = TOK ? c.r.top_k : 1;
     const int VS = nex * w.KS;                             // virtual segments: TOK's experts end to end
     const int nit = (VS + wk - 1) >> p.wk_log2;            // segments per warp and row block
     const long long rb_bytes = (long long)w.KS * seg_bytes;
     const bool by_expert = c.op != P_DENSE && !p.by_slot;
+    int items = c.op == P_DENSE ? (c.M + p.cols - 1) / p.cols : TOK ? c.r.T : c.r.T * c.r.top_k;
+    if (by_expert) {
+        grid_dep_wait();
+        if (warp == 0) {
+            // expert e has ceil(count / cols) items; lane l adds up experts l per.. l per + per
+            const int per = (w.E + 31) / 32, slots = c.r.T * c.r.top_k;
+            int mine = 0;
+            for (int i = 0; i < per; ++i) {
+                const int e = lane * per + i;
+                if (e < w.E) mine += (max(min(c.r.offsets[e + 1], slots) - max(c.r.offsets[e], 0), 0) + p.cols - 1) / p.cols;
+            }
+            int pre = mine;
+#pragma unroll
+            for (int o = 1; o < 32; o <<= 1) {
+                const int u = __shfl_up_sync(0xffffffffu, pre, o);
+                if (lane >= o) pre += u;
+            }
+            if (lane == 31) ts[w.E] = pre;
+            pre -= mine;
+            for (int i = 0; i < per; ++i) {
+                const int e = lane * per + i;
+                if (e >= w.E) break;
+                ts[e] = pre;
+                pre += (max(min(c.r.offsets[e + 1], slots) - max(c.r.offsets[e], 0), 0) + p.cols - 1) / p.cols;
+            }
+        }
+        __syncthreads();
+        items = ts[w.E];
+    }
+    // this block's share: row blocks of items, end to end
+    const long long work = (long long)items * w.RB;
+    const long long w0 = (long long)blockIdx.x * work / gridDim.x, w1 = (long long)(blockIdx.x + 1) * work / gridDim.x;
+
+    bool waited = by_expert;
     float acc[NB][4];
 #pragma unroll
     for (int b = 0; b < NB; ++b)
@@ -274,20 +273,23 @@ __device__ __forceinline__ void qg_rows_share(const QgRowsParams& p, uint8_t* sm
         at += rb1 - rb0;
         // the item: its experts and columns
         int rows = 1, expert = 0, first = 0;
-        wait.route();
+        if (!waited && c.op != P_DENSE) {
+            grid_dep_wait();
+            waited = true;
+        }
         if (TOK) {
             __syncthreads();  // the last item's experts are no longer read
             if (tid < nex) {
                 const int slot = item * nex + tid;
-                const int e = sh.ids[slot];
+                const int e = c.r.ids[slot];
                 s_e[tid] = e >= 0 && e < w.E ? e : -1;
-                s_wt[tid] = sh.weights[slot];
+                s_wt[tid] = c.r.weights[slot];
             }
             __syncthreads();
         } else if (c.op == P_DENSE) {
             rows = min(p.cols, c.M - item * p.cols);
         } else if (p.by_slot) {
-            expert = sh.ids[item];
+            expert = c.r.ids[item];
             if (expert < 0 || expert >= w.E) continue;
         } else {
             int lo = 0, hi = w.E;  // ts[lo] <= item < ts[hi]
@@ -297,7 +299,7 @@ __device__ __forceinline__ void qg_rows_share(const QgRowsParams& p, uint8_t* sm
                 else hi = mid;
             }
             expert = lo;
-            const int slots = c.r.T * c.r.top_k, p0 = max(sh.offsets[lo], 0), n = max(min(sh.offsets[lo + 1], slots) - p0, 0);
+            const int slots = c.r.T * c.r.top_k, p0 = max(c.r.offsets[lo], 0), n = max(min(c.r.offsets[lo + 1], slots) - p0, 0);
             first = p0 + (item - ts[lo]) * p.cols;
             rows = min(p.cols, n - (item - ts[lo]) * p.cols);
         }
@@ -344,11 +346,14 @@ __device__ __forceinline__ void qg_rows_share(const QgRowsParams& p, uint8_t* sm
         };
 #pragma unroll
         for (int i = 0; i < kQgDepth - 1; ++i) load();
-        if (!wait.rows()) break;
+        if (!waited) {
+            grid_dep_wait();
+            waited = true;
+        }
         __syncthreads();  // the last item's activations are no longer read
         if (by_expert) {
             if (tid < rows) {
-                const int slot = sh.order[first + tid];
+                const int slot = c.r.order[first + tid];
                 s_row[tid] = slot >= 0 && slot < c.r.T * c.r.top_k ? slot : 0;
             }
             __syncthreads();
@@ -506,52 +511,7 @@ __device__ __forceinline__ void qg_rows_share(const QgRowsParams& p, uint8_t* sm
             }
         }
     }
-}
-
-// The grid that this one depends on: waited for once, before what it may have written is read.
-struct QgDepWait {
-    bool waited, dense;
-    __device__ __forceinline__ void route() {
-        if (!waited && !dense) {
-            grid_dep_wait();
-            waited = true;
-        }
-    }
-    __device__ __forceinline__ bool rows() {
-        if (!waited) {
-            grid_dep_wait();
-            waited = true;
-        }
-        return true;
-    }
-};
-
-template <int NB, bool BF, int NG, bool TOK>
-__global__ void __launch_bounds__(qg_row_warps(NB) * 32, 1) q4g_rows_kernel(const QgRowsParams p) {
-    extern __shared__ __align__(16) uint8_t sm[];
-    __shared__ int s_e[kQgMaxK];
-    __shared__ float s_wt[kQgMaxK];
-    __shared__ int s_row[64];
-    __shared__ int ts[kQgRowMaxE + 1];
-    const QgCall& c = p.c;
-    const QgWeights& w = c.w;
-    const int tid = threadIdx.x;
-    if (tid == 0) *reinterpret_cast<uint4*>(sm + p.off_zero) = make_uint4(0u, 0u, 0u, 0u);  // what lanes without a column read
-    grid_dep_launch();
-    const bool by_expert = c.op != P_DENSE && !p.by_slot;
-    int items = c.op == P_DENSE ? (c.M + p.cols - 1) / p.cols : TOK ? c.r.T : c.r.T * c.r.top_k;
-    if (by_expert) {
-        grid_dep_wait();
-        if (tid < 32) qg_rows_items(c.r.offsets, w.E, c.r.T * c.r.top_k, p.cols, ts, tid);
-        __syncthreads();
-        items = ts[w.E];
-    }
-    // this block's share: row blocks of items, end to end
-    const long long work = (long long)items * w.RB;
-    const long long w0 = (long long)blockIdx.x * work / gridDim.x, w1 = (long long)(blockIdx.x + 1) * work / gridDim.x;
-    QgDepWait wait = {by_expert, c.op == P_DENSE};
-    qg_rows_share<NB, BF, NG, TOK>(p, sm, QgRowsShared{s_e, s_wt, s_row, ts, c.r.ids, c.r.weights, c.r.offsets, c.r.order}, w0, w1, wait);
-    wait.rows();
+    if (!waited) grid_dep_wait();
 }
 
 }  // namespace qmm

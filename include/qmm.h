@@ -391,8 +391,9 @@ qmm_status qmm_moe_down(const qmm_q4g* w, qmm_float xtype, const void* h, int64_
    gate_up: paired, N = 2 F; down: as many experts, K = F.  ids and weights
    [T][top_k] (both or neither) take the routing.  y [T][down.N] contiguous.
    workspace: qmm_moe_layer_workspace(...) bytes, uninitialised; calls that may
-   overlap need one each.  SHAPE also where rows are too long for shared memory
-   (some 20000 values in f32, 60000 in 16 bits).
+   overlap need one each.  SHAPE also where a row of K or F values does not
+   fit beside the rest in shared memory (from some 9000 values in f32, 28000 in
+   16 bits).
    Errors as qmm_q4g_matmul. */
 #define QMM_MOE_LAYER_MAX_TOKENS 32
 size_t qmm_moe_layer_workspace(const qmm_q4g* gate_up, const qmm_q4g* down, qmm_float xtype, int64_t T, int64_t top_k);
