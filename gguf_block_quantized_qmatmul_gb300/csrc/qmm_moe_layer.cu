@@ -32,49 +32,48 @@ __device__ __forceinline__ void router_load8(const void* row, int type, int k, f
     }
 }
 
-// Logits of all tokens for one expert a block: f32 products and sums in a fixed order, eight tokens at
-// a time.  Bound by latency (one trip to memory, one reduction).  The first block clears the next
-// launch's counters.
+// Logits of four tokens for one expert a block: f32 products and sums in a fixed order.  Bound by
+// latency: the router's row, constant, is asked for before what this grid depends on has completed, the
+// tokens' values after it, all at once; one reduction.  (A block for all tokens of an expert: 9 us for 16.)
+// The first block clears the next launch's counters.
+constexpr int kRouterTokens = 4;
 __global__ void __launch_bounds__(256) moe_router_kernel(const void* x, int xt, long long ldx, int T, int K, const void* router, int rt, float* logits, int ldl,
                                                          unsigned* counters) {
-    __shared__ float red[8][8];
-    const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31, e = blockIdx.x;
+    __shared__ float red[kRouterTokens][8];
+    const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31, e = blockIdx.x, t0 = blockIdx.y * kRouterTokens;
     const uint8_t* w = static_cast<const uint8_t*>(router) + (long long)e * K * x_size(rt);
+    float f[8];
+    if (8 * tid < K) router_load8(w, rt, 8 * tid, f);
     // the next launch reads x before this one has completed: it may start only now that x is there
     grid_dep_wait();
     grid_dep_launch();
-    if (e == 0 && tid < 4) counters[tid] = 0u;
-    for (int t0 = 0; t0 < T; t0 += 8) {
-        float acc[8];
+    if (e == 0 && t0 == 0 && tid < 4) counters[tid] = 0u;
+    float acc[kRouterTokens];
 #pragma unroll
-        for (int t = 0; t < 8; ++t) acc[t] = 0.0f;
-        for (int k = 8 * tid; k < K; k += 2048) {
-            float f[8];
-            router_load8(w, rt, k, f);
+    for (int t = 0; t < kRouterTokens; ++t) acc[t] = 0.0f;
+    for (int k = 8 * tid; k < K;) {
+        float v[kRouterTokens][8];
 #pragma unroll
-            for (int t = 0; t < 8; ++t) {
-                if (t0 + t >= T) break;
-                float v[8];
-                router_load8(static_cast<const uint8_t*>(x) + (t0 + t) * ldx * x_size(xt), xt, k, v);
+        for (int t = 0; t < kRouterTokens; ++t)  // past the last token: that one again
+            router_load8(static_cast<const uint8_t*>(x) + min(t0 + t, T - 1) * ldx * x_size(xt), xt, k, v[t]);
 #pragma unroll
-                for (int i = 0; i < 8; ++i) acc[t] = fmaf(f[i], v[i], acc[t]);
-            }
-        }
+        for (int t = 0; t < kRouterTokens; ++t)
 #pragma unroll
-        for (int t = 0; t < 8; ++t) {
-            if (t0 + t >= T) break;
+            for (int i = 0; i < 8; ++i) acc[t] = fmaf(f[i], v[t][i], acc[t]);
+        if ((k += 2048) < K) router_load8(w, rt, k, f);
+    }
 #pragma unroll
-            for (int o = 16; o; o >>= 1) acc[t] += __shfl_xor_sync(0xffffffffu, acc[t], o);
-            if (lane == 0) red[t][warp] = acc[t];
-        }
-        __syncthreads();
-        if (tid < 8 && t0 + tid < T) {
-            float v = 0.0f;
+    for (int t = 0; t < kRouterTokens; ++t) {
 #pragma unroll
-            for (int i = 0; i < 8; ++i) v += red[tid][i];
-            logits[(long long)(t0 + tid) * ldl + e] = v;
-        }
-        __syncthreads();
+        for (int o = 16; o; o >>= 1) acc[t] += __shfl_xor_sync(0xffffffffu, acc[t], o);
+        if (lane == 0) red[t][warp] = acc[t];
+    }
+    __syncthreads();
+    if (tid < kRouterTokens && t0 + tid < T) {
+        float v = 0.0f;
+#pragma unroll
+        for (int i = 0; i < 8; ++i) v += red[tid][i];
+        logits[(long long)(t0 + tid) * ldl + e] = v;
     }
 }
 
@@ -123,7 +122,7 @@ cudaError_t launch_moe_layer(const MoePlan& pl, const MoeCall& c, void* ws, unsi
     unsigned* counters = reinterpret_cast<unsigned*>(b);
     float* logits = reinterpret_cast<float*>(b + pl.ws_logits);
     const int E = c.up.E, ldl = (E + 3) / 4 * 4;
-    cudaError_t e = launch_pdl(moe_router_kernel, (unsigned)E, 256, 0, s, c.x, c.xt, c.ldx, c.T, c.up.K, c.router, c.rt, logits, ldl, counters);
+    cudaError_t e = launch_pdl_2d(moe_router_kernel, (unsigned)E, (unsigned)((c.T + kRouterTokens - 1) / kRouterTokens), 256, 0, s, c.x, c.xt, c.ldx, c.T, c.up.K, c.router, c.rt, logits, ldl, counters);
     if (e != cudaSuccess) return e;
     MoeParams p;
     p.route = RouteParams();

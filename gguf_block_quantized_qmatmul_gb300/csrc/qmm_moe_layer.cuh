@@ -129,6 +129,57 @@ struct MoeRun {
     __device__ __forceinline__ int expert(const MoeShared& sh) const { return TOKEN ? sh.ids[item * sh.k + j] : sh.items[item].expert; }
 };
 
+// Stages nh x rows quads of 32 values: block h of row r is `left` values (none: <= 0) from element
+// src(r, h, left) of x on, and goes to 64 bytes (a column; f32: three) at h * rows + r.  B 16-byte loads
+// (f32: pairs of them) a thread are in flight.
+template <int B, bool F32, class Src>
+__device__ __forceinline__ void moe_stage(uint8_t* sm, const void* x, int nh, int rows, Src src, int tid) {
+    constexpr int np = F32 ? 3 : 1;
+    const int n = nh * rows * 4;
+    for (int i0 = 0; i0 < n; i0 += B * kMoeThreads) {
+        uint4 u[B][F32 ? 2 : 1];
+#pragma unroll
+        for (int b = 0; b < B; ++b) {
+            const int i = i0 + b * kMoeThreads + tid, quad = i >> 2, h = quad / rows;
+#pragma unroll
+            for (int q = 0; q < (F32 ? 2 : 1); ++q) u[b][q] = make_uint4(0u, 0u, 0u, 0u);
+            if (i < n) {
+                int left;
+                const long long at = src(quad - h * rows, h, left) + 8 * (i & 3);
+                if (8 * (i & 3) < left)
+#pragma unroll
+                    for (int q = 0; q < (F32 ? 2 : 1); ++q) u[b][q] = reinterpret_cast<const uint4*>(static_cast<const uint8_t*>(x) + at * (F32 ? 4 : 2))[q];
+            }
+        }
+#pragma unroll
+        for (int b = 0; b < B; ++b) {
+            const int i = i0 + b * kMoeThreads + tid, j = i & 3;
+            if (i - (tid & 31) >= n) break;  // the whole warp is done
+            uint8_t* to = sm + (long long)(i >> 2) * (np * 64) + j * 16;
+            if constexpr (F32) {
+                float f[8] = {__uint_as_float(u[b][0].x), __uint_as_float(u[b][0].y), __uint_as_float(u[b][0].z), __uint_as_float(u[b][0].w),
+                              __uint_as_float(u[b][1].x), __uint_as_float(u[b][1].y), __uint_as_float(u[b][1].z), __uint_as_float(u[b][1].w)};
+#pragma unroll
+                for (int pc = 0; pc < 3; ++pc) {
+                    uint32_t w[4];
+#pragma unroll
+                    for (int e = 0; e < 8; ++e) {
+                        const uint32_t v = __float_as_uint(f[e]) & 0xffff0000u;
+                        w[e >> 1] = e & 1 ? w[e >> 1] | v : v >> 16;
+                        // the rest is exact; an infinity or NaN has none
+                        f[e] = (v & 0x7f800000u) == 0x7f800000u ? 0.0f : f[e] - __uint_as_float(v);
+                    }
+                    const uint4 q = qg_quad_transpose(w[0], w[1], w[2], w[3], j);
+                    if (i < n) *reinterpret_cast<uint4*>(to + pc * 64) = q;
+                }
+            } else {
+                const uint4 q = qg_quad_transpose(u[b][0].x, u[b][0].y, u[b][0].z, u[b][0].w, j);
+                if (i < n) *reinterpret_cast<uint4*>(to) = q;
+            }
+        }
+    }
+}
+
 // Row blocks w0 .. w1 of one product's items.  UP: the first product, x to h; else the second, h to part
 // (TOKEN: y).  wait() (false: give up) comes before the activations are read.
 template <bool BF, bool F32, int NG, bool UP, bool TOKEN, class Wait>
@@ -181,15 +232,21 @@ __device__ __forceinline__ bool moe_share(const MoeParams& p, const QgWeights& w
             const int i1 = (b1 - 1) / RB;
             for (int it = i0; it <= i1; ++it) {
                 uint8_t* area = sm + (it - i0) * item_bytes;
-                if (TOKEN) {
-                    for (int j = 0; j < sh.k; ++j)
-                        qg_stage(area, p.h, p.xt, w.K, KS, 1, np, j * KS, [&](int) { return ((long long)it * sh.k + j) * w.K; }, tid, kMoeThreads);
+                constexpr int kFlight = F32 ? 2 : 4;
+                if (TOKEN) {  // its choices' rows end to end
+                    const int per_row = KS * 4;
+                    moe_stage<kFlight, F32>(area, p.h, sh.k * per_row, 1, [&](int, int h, int& left) {
+                        const int j = h / per_row, k32 = 32 * (h - j * per_row);
+                        left = w.K - k32;
+                        return ((long long)it * sh.k + j) * w.K + k32;
+                    }, tid);
                 } else {
                     const MoeItem m = sh.items[it];
-                    qg_stage(area, UP ? p.x : p.h, p.xt, w.K, KS, m.n, np, 0, [&](int r) {
+                    moe_stage<kFlight, F32>(area, UP ? p.x : p.h, KS * 4, m.n, [&](int r, int h, int& left) {
                         const int slot = sh.order[m.first + r];
-                        return UP ? slot / sh.k * p.ldx : (long long)slot * w.K;
-                    }, tid, kMoeThreads);
+                        left = w.K - 32 * h;
+                        return (UP ? slot / sh.k * p.ldx : (long long)slot * w.K) + 32 * h;
+                    }, tid);
                 }
             }
             __syncthreads();
@@ -371,7 +428,11 @@ __global__ void __launch_bounds__(kMoeThreads, 1) moe_layer_kernel(const __grid_
     grid_dep_launch();
     // The first launch lets this one start only when what it depends on itself has completed, so the
     // tokens are there.
-    if (p.whole) qg_stage(sm, p.x, p.xt, p.up.K, p.up.KS, T, F32 ? 3 : 1, 0, [&](int r) { return r * p.ldx; }, tid, kMoeThreads);
+    if (p.whole)
+        moe_stage<F32 ? 2 : 4, F32>(sm, p.x, p.up.KS * 4, T, [&](int r, int h, int& left) {
+            left = p.up.K - 32 * h;
+            return r * p.ldx + 32 * h;
+        }, tid);
     grid_dep_wait();
     unsigned next = 0;  // thread 0: the next ticket
     if (tid == 0) next = atomicAdd(p.counters, 1u);
@@ -427,10 +488,11 @@ __global__ void __launch_bounds__(kMoeThreads, 1) moe_layer_kernel(const __grid_
     const MoeShared sh = {ids, weights, order, items, T, k};
 
     // ------------------------------ shares ------------------------------
+    // The next ticket is drawn when a share begins and known to all when it ends, at one barrier.
     const unsigned G = gridDim.x, total = TOKEN ? 2 * G : 3 * G;
+    if (tid == 0) s_ticket[0] = next;
+    __syncthreads();
     for (int it = 0;; ++it) {
-        if (tid == 0) s_ticket[it & 1] = next;
-        __syncthreads();  // and what the last share kept in shared memory is no longer read
         const unsigned ticket = s_ticket[it & 1];
         if (ticket >= total) break;
         if (tid == 0) next = atomicAdd(p.counters, 1u);
@@ -472,9 +534,10 @@ __global__ void __launch_bounds__(kMoeThreads, 1) moe_layer_kernel(const __grid_
             }
         }
         if (!ok) break;
-        if (phase == 2 || (TOKEN && phase == 1)) continue;
-        __syncthreads();  // every thread's results are written
-        if (tid == 0 && !(p.stall && ticket == 0)) add_release(p.counters + 1 + phase);
+        if (tid == 0) s_ticket[(it + 1) & 1] = next;
+        __syncthreads();  // every thread's results are written, and what the share kept in shared memory is no longer read
+        // by the last warp's first thread: its fence takes a while, and only its own warp's next loads wait for it
+        if (tid == kMoeThreads - 32 && phase < (TOKEN ? 1u : 2u) && !(p.stall && ticket == 0)) add_release(p.counters + 1 + phase);
     }
 }
 
