@@ -20,7 +20,7 @@ LIB = os.path.join(BUILD, "libqmm.so")
 BINDING = os.path.join(BUILD, "_qmm_torch.so")  # CPython extension of q4g.py's calls
 ROOT = os.path.dirname(HERE)
 UNITS = ["qmm_api", "qmm_quant", "qmm_stream_q8_0", "qmm_stream_q4_k", "qmm_stream_x_0", "qmm_stream_q6_k", "qmm_gemv_q8_0", "qmm_gemv_q4_k", "qmm_dmma", "qmm_dmma_x_0", "qmm_dmma_q6_k", "qmm_tc", "qmm_tcx", "qmm_tcx_f32", "qmm_static_ws", "qmm_batch", "qmm_batch_mix", "qmm_q4g_api", "qmm_q4g_layout", "qmm_q4g_rows", "qmm_q4g_rows_1", "qmm_q4g_rows_2", "qmm_q4g_rows_4",
-         "qmm_q4g_gemm", "qmm_moe_route", "qmm_q8c_api", "qmm_q8c_layout", "qmm_q8c_quant", "qmm_q8c_rows", "qmm_q8c_gemm", "qmm_norm", "qmm_moe_layer", "qmm_moe_layer_f16", "qmm_moe_layer_bf16",
+         "qmm_q4g_gemm", "qmm_moe_route", "qmm_q8c_api", "qmm_q8c_layout", "qmm_q8c_quant", "qmm_q8c_rows", "qmm_q8c_gemm", "qmm_norm", "qmm_norm_f32", "qmm_norm_f16", "qmm_norm_bf16", "qmm_moe_layer", "qmm_moe_layer_f16", "qmm_moe_layer_bf16",
          "qmm_moe_layer_f32"]
 ARCH = ["-gencode", "arch=compute_103a,code=sm_103a"]
 FLAGS = ["-O3", "-lineinfo", "-std=c++17", "-Xcompiler", "-fPIC", "-Xptxas", "-v"]

@@ -123,9 +123,25 @@ __device__ __forceinline__ void qc_load8(const void* row, int k, int K, bool vec
         for (int i = 0; i < 8; ++i) f[i] = k + i < K ? x_load(row, XT, k + i) : 0.0f;
     }
 }
+// v = x id in -128..128: the sum v + 1.5 2^23 has its nearest integer (ties to even) in the low byte; a
+// tie that went towards zero is put right, so that halves go away from zero, as in q8_code.
+__device__ __forceinline__ uint32_t qc_code_word(float x, float id) {
+    const float magic = 12582912.0f, v = __fmul_rn(x, id);
+    float sum = __fadd_rn(v, magic);
+    const float rest = __fsub_rn(v, __fsub_rn(sum, magic)), half = __uint_as_float((__float_as_uint(v) & 0x80000000u) | 0x3f000000u);
+    if (rest == half) sum = __fadd_rn(sum, __fadd_rn(half, half));
+    return __float_as_uint(sum);
+}
+// Eight codes.  A reciprocal that overflowed, or 0 (a row of zeros, or one that is not finite), takes the long
+// way, where a product may be infinite or NaN.
 __device__ __forceinline__ uint2 qc_codes8(const float f[8], float id) {
-    return make_uint2(pack4(q8_code(f[0], id), q8_code(f[1], id), q8_code(f[2], id), q8_code(f[3], id)),
-                      pack4(q8_code(f[4], id), q8_code(f[5], id), q8_code(f[6], id), q8_code(f[7], id)));
+    if (id > 1e38f || id == 0.0f)
+        return make_uint2(pack4(q8_code(f[0], id), q8_code(f[1], id), q8_code(f[2], id), q8_code(f[3], id)),
+                          pack4(q8_code(f[4], id), q8_code(f[5], id), q8_code(f[6], id), q8_code(f[7], id)));
+    uint32_t w[4];
+#pragma unroll
+    for (int i = 0; i < 4; ++i) w[i] = __byte_perm(qc_code_word(f[2 * i], id), qc_code_word(f[2 * i + 1], id), 0x0040u);
+    return make_uint2(__byte_perm(w[0], w[1], 0x5410u), __byte_perm(w[2], w[3], 0x5410u));
 }
 
 // Four signed bytes as two f16 pairs, exact.
@@ -182,6 +198,13 @@ struct NormCall {
     int T, K, xt, wt;
     float scale, eps, offset;
 };
+struct NormParams {
+    NormCall c;
+    int vec;  // every row, and every one of its 8-value pieces, starts on its natural boundary
+};
 cudaError_t launch_block_norm(const NormCall& c, cudaStream_t s);
+cudaError_t launch_block_norm_f32(const NormParams& p, cudaStream_t s);
+cudaError_t launch_block_norm_f16(const NormParams& p, cudaStream_t s);
+cudaError_t launch_block_norm_bf16(const NormParams& p, cudaStream_t s);
 
 }  // namespace qmm

@@ -182,3 +182,32 @@ def test_norm_and_product_together(q):
     total = rows.codes.cpu().double() @ wq.codes.cpu().double().T
     ref = (total.float() * wq.scales.cpu() * rows.scales.cpu()[:, None]).bfloat16()
     assert torch.equal(y.cpu(), ref)
+
+
+@pytest.mark.parametrize("T,K,dt,wdt,residual,post,gate", [
+    (10000, 256, "bf16", "bf16", True, True, "channel"), (5001, 576, "f16", "f32", True, False, "token"), (20000, 136, "f32", "f32", False, True, "none"),
+    (9000, 392, "bf16", "f32", True, True, "token"), (3000, 1000, "f16", "f16", True, True, "channel"), (2000, 1544, "bf16", "bf16", True, False, "none"),
+    (1300, 2048, "f32", "f32", True, True, "token"), (700, 4096, "bf16", "bf16", True, True, "channel"), (650, 4096, "f32", "f32", False, True, "token"),
+    (400, 6400, "f16", "f32", True, True, "none"), (350, 8192, "f32", "f32", True, True, "token"), (330, 8184, "bf16", "bf16", False, False, "channel"),
+    (4000, 704, "f32", "bf16", True, True, "channel"), (2500, 1020, "bf16", "bf16", True, True, "channel")])
+def test_many_rows(q, T, K, dt, wdt, residual, post, gate):
+    """The kernels that take many rows: every row against the formula, in place and as codes too."""
+    t = make(T, K, dt, wdt, residual, post, gate)
+    r, h, dr, dh = plain(t, 0.7, 1e-5, 0.5)
+    c = {k: v.cuda() for k, v in t.items()}
+    gr, gh = q.block_norm(**c, scale=0.7, eps=1e-5, weight_offset=0.5)
+    near(gr, r, dr, dt)
+    near(gh, h, dh, dt)
+    cr, rows = q.block_norm(**c, scale=0.7, eps=1e-5, weight_offset=0.5, quantize=True)
+    assert torch.equal(cr, gr)
+    if dt == "f32":
+        ref = q.q8c_quantize(gh)
+        assert torch.equal(rows.codes, ref.codes) and torch.equal(rows.scales, ref.scales)
+    d = rows.scales.double().cpu()[:, None]
+    assert ((rows.codes.cpu().double() * d - h).abs() <= dh + d * (0.5 + 2 * 128 * E) + h.abs().amax(1, keepdim=True) * 2 * E).all()
+    if residual:
+        c["y"][3, 5] = float("nan")
+        q.block_norm(**c, scale=0.7, eps=1e-5, weight_offset=0.5, residual_out=c["residual"], out=c["y"])
+        keep = torch.arange(T, device="cuda") != 3
+        assert torch.equal(c["residual"][keep], gr[keep]) and torch.equal(c["y"][keep], gh[keep]) and torch.isnan(c["y"][3]).all()
+    assert q.last_device_error() == 0
