@@ -13,10 +13,13 @@
 // in the same way, so that a row's result depends neither on the kernel nor on
 // the other rows of the call.
 //
-// Laid out, the weights are row blocks of 16 rows, each one contiguous stream
-// of segments of 128 K, two tiles of 64 K: 512 bytes with rows 0..7, 512 with
-// rows 8..15, lane l = 4 g + t of a warp holding K 16 t .. 16 t + 15 of row g
-// (g + 8) at byte 16 l.  A lane's two 16-byte loads are its operands of two
+// Laid out, the weights are row blocks of 16 rows in segments of 128 K, 2 KB
+// each: two tiles of 64 K, of which 512 bytes are rows 0..7 and 512 rows 8..15,
+// lane l = 4 g + t of a warp holding K 16 t .. 16 t + 15 of row g (g + 8) at byte
+// 16 l.  Eight row blocks are a panel, whose segments of the same K are next to
+// each other, 16 KB that the GEMM copies in one piece (a box of eight 2 KB pieces
+// took the copy engine 590 ns, more than the rest of a tile takes); the last
+// panel has as many row blocks as there are.  A lane's two 16-byte loads are its operands of two
 // m16n8k32 integer MMAs (words 2 i, 2 i + 1 of MMA i; the activations' words in
 // the same order) and, turned into f16, of a 16-lane x 128-bit tensor-memory
 // store.  Rows past N and K past the row's end are 0.  Behind the row blocks:
@@ -50,6 +53,9 @@ inline bool qc_describe(long long N, long long K, const void* data, QcWeights& w
     w.norm_off = w.scale_off + (long long)w.RB * 64;
     return true;
 }
+// a row block's first segment, and the bytes from a segment to the next
+__host__ __device__ inline long long qc_row_block(const QcWeights& w, int rb) { return ((long long)(rb & ~7) * w.KS + (rb & 7)) * kQcSeg; }
+__host__ __device__ inline int qc_step(const QcWeights& w, int rb) { return (w.RB - (rb & ~7) < 8 ? w.RB - (rb & ~7) : 8) * kQcSeg; }
 inline size_t qc_bytes(const QcWeights& w) { return (size_t)w.norm_off + 16; }
 
 // Activations of a call: floats, quantized on the way, or codes with a scale per row.
@@ -68,9 +74,9 @@ struct QcCall {
     int yt;
 };
 
-// one result from its integer sum, the same on every path
-__device__ __forceinline__ float qc_scale(int sum, float sw, float sx, float bias) {
-    return __fadd_rn(__fmul_rn(__fmul_rn((float)sum, sw), sx), bias);
+// one result from its integer sum (as the nearest float), the same on every path
+__device__ __forceinline__ float qc_scale(float sum, float sw, float sx, float bias) {
+    return __fadd_rn(__fmul_rn(__fmul_rn(sum, sw), sx), bias);
 }
 
 // The scale of a row from the bits of its largest magnitude (an infinity's or a NaN's are above every
@@ -171,10 +177,10 @@ cudaError_t launch_q8c_prep(const QcRows& a, int K, const QcPrep& p, bool f16, c
 
 struct QcRowsPlan {
     bool ok = false;
-    int cols = 0, nb = 0, warps = 0, wk = 0, depth = 0, blocks = 0, items = 0;
+    int cols = 0, nb = 0, warps = 0, blocks = 0, items = 0;
     int pitch = 0;       // bytes of a staged row
     int prep = 0;        // activations are quantized by a launch of their own
-    int off_zero = 0, off_scale = 0, off_red = 0, off_ring = 0;
+    int off_zero = 0, off_scale = 0, off_part = 0, off_ring = 0;
     size_t smem = 0, workspace = 0;
 };
 QcRowsPlan plan_q8c_rows(const QcCall& c, int sms, int smem_max);

@@ -20,7 +20,7 @@
 // by TMA in 128-byte swizzled tiles.  19 warps' roles:
 //   warp 0      activation tiles, 128 K each
 //   warp 1      eight MMAs a tile
-//   warp 2      raw weights, a box of eight row blocks x 128 K (16 KB)
+//   warp 2      raw weights, a panel's 128 K (16 KB) a copy
 //   warps 3-10  epilogue: results from the accumulator, scaled
 //   warps 11-26 conversion: 32 codes a lane and tile of 64 K, ten instructions for eight
 // Calls with few tiles are split over K; the slices' integer sums go to the
@@ -37,6 +37,11 @@ namespace {
 constexpr int kRaw = 8 * kQcSeg;      // bytes of a raw stage
 constexpr int kRestart = 8;           // tiles of 128 K per accumulation where sums may pass 2^24
 constexpr int kMaxBX = 256;
+constexpr int kXMax = 8, kXMin = 4, kRawMax = 12;  // stages, at most: activations (and at least), raw weights
+constexpr int kBars = (2 * kXMax + 2 * kQgStageMax + 2 * kRawMax + 4) * 8;  // bytes of the mbarriers
+constexpr int kWarpCols = kMaxBX / kQgEpiHalves;                            // columns that an epilogue warp reads out
+constexpr int kTail = kBars + 32 + kQgEpiWarps * kWarpCols * 4;             // behind the rings: mbarriers, three words, the columns' factors
+static_assert(kXMax % kQgGroups == 0 && kRawMax % kQgGroups == 0 && kBars % 16 == 0, "rings of whole turns");
 
 struct GemmParams {
     QcCall c;
@@ -56,7 +61,7 @@ struct Unit {
 };
 
 template <int CG>
-__global__ void __launch_bounds__(kQgThreads, 1) q8c_gemm_kernel(const __grid_constant__ CUtensorMap tx, const __grid_constant__ CUtensorMap tw, const GemmParams p) {
+__global__ void __launch_bounds__(kQgThreads, 1) q8c_gemm_kernel(const __grid_constant__ CUtensorMap tx, const GemmParams p) {
     extern __shared__ __align__(1024) uint8_t smraw[];
     uint8_t* sm = smraw + ((1024 - (smem_u32(smraw) & 1023)) & 1023);
     const QcCall& c = p.c;
@@ -64,22 +69,22 @@ __global__ void __launch_bounds__(kQgThreads, 1) q8c_gemm_kernel(const __grid_co
     const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31, M = c.a.M;
     uint64_t* bars = reinterpret_cast<uint64_t*>(sm + p.off_bar);
     uint64_t* x_full = bars;                       // activation tile landed (of a pair: both halves)
-    uint64_t* x_empty = x_full + kQgXMax;          // and read by the MMAs (commit)
-    uint64_t* full = x_empty + kQgXMax;            // converted weights in tensor memory
+    uint64_t* x_empty = x_full + kXMax;          // and read by the MMAs (commit)
+    uint64_t* full = x_empty + kXMax;            // converted weights in tensor memory
     uint64_t* empty = full + kQgStageMax;          // and read by the MMAs (commit)
     uint64_t* r_full = empty + kQgStageMax;        // raw weights landed
-    uint64_t* r_empty = r_full + kQgRawMax;        // raw stage converted
-    uint64_t* acc_full = r_empty + kQgRawMax;      // accumulator complete (commit)
+    uint64_t* r_empty = r_full + kRawMax;        // raw stage converted
+    uint64_t* acc_full = r_empty + kRawMax;      // accumulator complete (commit)
     uint64_t* acc_empty = acc_full + 2;            // accumulator read
-    static_assert((2 * kQgXMax + 2 * kQgStageMax + 2 * kQgRawMax + 4) * 8 <= 448, "mbarriers overlap the TMEM slot");
-    uint32_t* tslot = reinterpret_cast<uint32_t*>(sm + p.off_bar + 448);
-    uint32_t* s_norm = reinterpret_cast<uint32_t*>(sm + p.off_bar + 464);
-    volatile int* flags = reinterpret_cast<volatile int*>(sm + p.off_bar + 480);
+    uint32_t* tslot = reinterpret_cast<uint32_t*>(sm + p.off_bar + kBars);
+    uint32_t* s_norm = tslot + 1;
+    volatile int* flags = reinterpret_cast<volatile int*>(tslot + 2);
+    float* s_xs = reinterpret_cast<float*>(tslot + 8);  // [epilogue warps][kWarpCols]
     const uint32_t rank = CG == 2 ? cluster_rank() : 0u;
     constexpr int kUnit = 16 * CG;  // the MMA's N is a multiple of 16, a pair's of 32
     const int first_unit = blockIdx.x / CG, unit_step = gridDim.x / CG;
     if (tid == 0) {
-        for (int i = 0; i < kQgXMax; ++i) {
+        for (int i = 0; i < kXMax; ++i) {
             mbar_init(smem_u32(&x_full[i]), 1);
             mbar_init(smem_u32(&x_empty[i]), 1);
         }
@@ -87,7 +92,7 @@ __global__ void __launch_bounds__(kQgThreads, 1) q8c_gemm_kernel(const __grid_co
             mbar_init(smem_u32(&full[i]), 8 * CG);
             mbar_init(smem_u32(&empty[i]), 1);
         }
-        for (int i = 0; i < kQgRawMax; ++i) {
+        for (int i = 0; i < kRawMax; ++i) {
             mbar_init(smem_u32(&r_full[i]), 1);
             mbar_init(smem_u32(&r_empty[i]), 8);
         }
@@ -146,13 +151,15 @@ __global__ void __launch_bounds__(kQgThreads, 1) q8c_gemm_kernel(const __grid_co
             int left = p.stall - 1;
             for (int u = first_unit; u < units && ok; u += unit_step) {
                 const Unit un = place(u);
+                const int bytes = 8 * un.nt < w.RB ? qc_step(w, 8 * un.nt) : 0;
+                const uint8_t* from = w.data + qc_row_block(w, 8 * un.nt);
                 for (int j = un.j0; j < un.j1; ++j) {
                     // injected stall: this block's raw weights end here
                     if (p.stall && blockIdx.x == p.stall_block && --left < 0) ok = false;
                     if (!ok || !(ok = qg_wait(smem_u32(&r_empty[r.s]), r.ph ^ 1u, flags, p.err))) break;
                     const uint32_t bar = smem_u32(&r_full[r.s]);
-                    mbar_arrive_tx(bar, (uint32_t)kRaw);
-                    tma_2d(smem_u32(raw(r.s)), &tw, j * (kQcSeg / 8), 8 * un.nt, bar);
+                    mbar_arrive_tx(bar, (uint32_t)bytes);  // a panel's segments of this K; row blocks past the last one keep what was there
+                    if (bytes > 0) bulk_g2s(smem_u32(raw(r.s)), from + (long long)j * bytes, (uint32_t)bytes, bar);
                     r.next(p.nraw);
                     wrapped |= r.s == 0;
                 }
@@ -162,6 +169,7 @@ __global__ void __launch_bounds__(kQgThreads, 1) q8c_gemm_kernel(const __grid_co
     } else if (warp == 0) {
         // ------------------------------ activations ------------------------------
         if (lane == 0) {
+            asm volatile("prefetch.tensormap [%0];" ::"l"(&tx) : "memory");
             grid_dep_wait();
             QgRing g;
             bool ok = true, wrapped = false;
@@ -248,37 +256,87 @@ __global__ void __launch_bounds__(kQgThreads, 1) q8c_gemm_kernel(const __grid_co
             }
         } else {
             // ------------------------------ epilogue ------------------------------
-            const int ew = warp - kQgEpi0, q = warp & 3, part = ew >> 2;  // columns part * 8, then every (kQgEpiHalves * 8)th
+            // chunks of 8 columns part, part + 2, .. of the unit are this warp's
+            const int ew = warp - kQgEpi0, q = warp & 3, part = ew >> 2;
             const uint32_t tq = (uint32_t)(32 * q) << 16;
             int cc = 0;
             bool ok = true;
             const float* sw = reinterpret_cast<const float*>(w.data + w.scale_off);
+            // A unit's factors, asked for a unit ahead: this lane's row; the columns' go to shared memory, each
+            // warp's own, in the order of its chunks.
+            constexpr int kWords = kWarpCols / 32;
+            float wn_next = 0.0f, bias_next = 0.0f, xs_next[kWords];
+            float* table = s_xs + ew * kWarpCols;
+            auto ask = [&](const Unit& un) {
+                const int n = (8 * un.nt + 2 * q) * 16 + lane;
+                wn_next = n < w.N ? __ldg(sw + n) : 0.0f;
+                bias_next = c.bias && n < w.N ? __ldg(c.bias + n) : 0.0f;
+#pragma unroll
+                for (int i = 0; i < kWords; ++i) {
+                    const int m = kCols * (part + kQgEpiHalves * (4 * i + (lane >> 3))) + (lane & 7);
+                    xs_next[i] = m < un.n ? __ldg(p.xs + un.p0 + m) : 0.0f;
+                }
+            };
+            if (first_unit < units) ask(place(first_unit));
             for (int u = first_unit; u < units && ok; u += unit_step) {
                 const Unit un = place(u);
                 const int nch = (un.n + kCols - 1) / kCols;
                 const int n = (8 * un.nt + 2 * q) * 16 + lane;  // the tile's 128 rows are the lanes of the four quarters
                 const bool on = n < w.N;
-                const float wn = on ? __ldg(sw + n) : 0.0f, bias = on && c.bias ? __ldg(c.bias + n) : 0.0f;
-                auto put = [&](int k, const int v[kCols]) {  // columns kCols k..
+                const float wn = wn_next, bias = bias_next;
+                __syncwarp();  // the last unit's have been read
+#pragma unroll
+                for (int i = 0; i < kWords; ++i) table[32 * i + lane] = xs_next[i];
+                __syncwarp();
+                if (u + unit_step < units) ask(place(u + unit_step));
+                // Columns kCols k.., this warp's from `at` on; whole: sums that a float may not hold.  16-bit results go to
+                // memory four at a time, of four rows: a quad of lanes exchanges its 4 x 8 values (a store a value
+                // and column took three times as long).
+                const bool wide = w.N % 4 == 0;
+                auto put = [&](int k, const float v[kCols], int at, const int* whole) {
                     const int m = un.p0 + kCols * k, left = min(kCols, un.n - kCols * k);
-                    if (!on) return;
                     if (p.ks > 1) {
                         int* to = p.part + ((long long)un.split * M + m) * w.N + n;
 #pragma unroll
-                        for (int i = 0; i < kCols; ++i)
-                            if (i < left) to[(long long)i * w.N] = v[i];
+                        for (int i = 0; i < kCols; ++i, to += w.N)
+                            if (on && i < left) *to = whole ? whole[i] : __float2int_rn(v[i]);
                         return;
                     }
-                    auto as = [&](auto* y) {
-                        using Y = typename std::remove_pointer<decltype(y)>::type;
-                        Y* to = y + (long long)m * w.N + n;
+                    const float4 f0 = *reinterpret_cast<const float4*>(table + at), f1 = *reinterpret_cast<const float4*>(table + at + 4);
+                    const float sx[kCols] = {f0.x, f0.y, f0.z, f0.w, f1.x, f1.y, f1.z, f1.w};
+                    float y[kCols];
 #pragma unroll
-                        for (int i = 0; i < kCols; ++i)
-                            if (i < left) to[(long long)i * w.N] = to_type<Y>(qc_scale(v[i], wn, __ldg(p.xs + m + i), bias));
-                    };
-                    if (c.yt == X_F32) as(static_cast<float*>(c.y));
-                    else if (c.yt == X_F16) as(static_cast<__half*>(c.y));
-                    else as(static_cast<__nv_bfloat16*>(c.y));
+                    for (int i = 0; i < kCols; ++i) y[i] = qc_scale(v[i], wn, sx[i], bias);
+                    if (c.yt == X_F32) {
+                        float* to = static_cast<float*>(c.y) + (long long)m * w.N + n;
+#pragma unroll
+                        for (int i = 0; i < kCols; ++i, to += w.N)
+                            if (on && i < left) *to = y[i];
+                        return;
+                    }
+                    uint32_t h[kCols / 2];  // columns 2 i, 2 i + 1
+#pragma unroll
+                    for (int i = 0; i < kCols / 2; ++i) {
+                        if (c.yt == X_F16) {
+                            const __half2 b = __floats2half2_rn(y[2 * i], y[2 * i + 1]);
+                            h[i] = *reinterpret_cast<const uint32_t*>(&b);
+                        } else {
+                            const __nv_bfloat162 b = __floats2bfloat162_rn(y[2 * i], y[2 * i + 1]);
+                            h[i] = *reinterpret_cast<const uint32_t*>(&b);
+                        }
+                    }
+                    if (wide) {
+                        const uint4 t = qg_quad_transpose(h[0], h[1], h[2], h[3], lane);  // columns 2 l, 2 l + 1 of the quad's rows, l = lane % 4
+                        const int i = 2 * (lane & 3);
+                        uint16_t* to = static_cast<uint16_t*>(c.y) + (long long)(m + i) * w.N + (n - (lane & 3));
+                        if (on && i < left) *reinterpret_cast<uint2*>(to) = make_uint2(__byte_perm(t.x, t.y, 0x5410u), __byte_perm(t.z, t.w, 0x5410u));
+                        if (on && i + 1 < left) *reinterpret_cast<uint2*>(to + w.N) = make_uint2(__byte_perm(t.x, t.y, 0x7632u), __byte_perm(t.z, t.w, 0x7632u));
+                    } else {
+                        uint16_t* to = static_cast<uint16_t*>(c.y) + (long long)m * w.N + n;
+#pragma unroll
+                        for (int i = 0; i < kCols; ++i, to += w.N)
+                            if (on && i < left) *to = (uint16_t)(h[i >> 1] >> (16 * (i & 1)));
+                    }
                 };
                 int sums[kMaxBX / kQgEpiHalves];  // local memory; restarted accumulations only
                 for (int c0 = un.j0; c0 < un.j1; c0 += chunk, ++cc) {
@@ -293,22 +351,23 @@ __global__ void __launch_bounds__(kQgThreads, 1) q8c_gemm_kernel(const __grid_co
 #pragma unroll 1
                     for (int k = part, at = 0; k < nch; k += kQgEpiHalves, at += kCols) {
                         tc_wait_ld();
-                        int v[kCols];
+                        float v[kCols];
 #pragma unroll
                         for (int i = 0; i < kCols; ++i) {
                             asm volatile("" : "+r"(r[i]));  // not used before the wait
-                            v[i] = __float2int_rn(__uint_as_float(r[i]));
+                            v[i] = __uint_as_float(r[i]);
                         }
                         if (k + kQgEpiHalves < nch) tc_ld8(acol + kCols * (k + kQgEpiHalves), r);
-                        if (!begin) {
-#pragma unroll
-                            for (int i = 0; i < kCols; ++i) v[i] += sums[at + i];
-                        }
-                        if (end) {
-                            put(k, v);
+                        if (begin && end) {
+                            put(k, v, at, nullptr);
                         } else {
 #pragma unroll
-                            for (int i = 0; i < kCols; ++i) sums[at + i] = v[i];
+                            for (int i = 0; i < kCols; ++i) {
+                                const int sum = (begin ? 0 : sums[at + i]) + __float2int_rn(v[i]);
+                                sums[at + i] = sum;
+                                v[i] = (float)sum;
+                            }
+                            if (end) put(k, v, at, sums + at);
                         }
                     }
                     __syncwarp();
@@ -421,11 +480,11 @@ __global__ void __launch_bounds__(256) q8c_sum_kernel(const int* part, int ks, i
 #pragma unroll
         for (int s = 0; s < 4; ++s) v += u[s];
     }
-    x_store(y, yt, i, qc_scale(v, __ldg(sw + n), __ldg(xs + m), bias ? __ldg(bias + n) : 0.0f));
+    x_store(y, yt, i, qc_scale((float)v, __ldg(sw + n), __ldg(xs + m), bias ? __ldg(bias + n) : 0.0f));
 }
 
 template <int CG>
-cudaError_t gemm_go(const QcGemmPlan& pl, const CUtensorMap& tx, const CUtensorMap& tw, const GemmParams& p, int smem_max, cudaStream_t s) {
+cudaError_t gemm_go(const QcGemmPlan& pl, const CUtensorMap& tx, const GemmParams& p, int smem_max, cudaStream_t s) {
     static unsigned long long done = 0;
     auto* k = q8c_gemm_kernel<CG>;
     const cudaError_t e = ensure_smem(k, smem_max, done);
@@ -444,7 +503,7 @@ cudaError_t gemm_go(const QcGemmPlan& pl, const CUtensorMap& tx, const CUtensorM
     attr[1].val.clusterDim.z = 1;
     cfg.attrs = attr;
     cfg.numAttrs = CG == 1 ? 1 : 2;
-    return cudaLaunchKernelEx(&cfg, k, tx, tw, p);
+    return cudaLaunchKernelEx(&cfg, k, tx, p);
 }
 
 }  // namespace
@@ -484,15 +543,17 @@ QcGemmPlan plan_q8c_gemm(const QcCall& c, int sms, int smem_max) {
     pl.nacc = pl.bx <= 192 ? 2 : 1;  // with two accumulators the epilogue runs beside the next unit's MMAs
     pl.nstage = (kTcTmemCols - pl.nacc * pl.accw) / 64;
     if (pl.nstage > kQgStageMax) pl.nstage = kQgStageMax;
-    const int stage = pl.bx / pl.cg * 256, room = smem_max - 512 - 1024;
+    const int stage = pl.bx / pl.cg * 256, room = smem_max - kTail - 1024;
     // Both rings are multiples of the converting groups, so that whoever waits for a stage's next
-    // filling has waited for its last one (copies may land out of order).
-    pl.nx = (room - 4 * kRaw) / stage / kQgGroups * kQgGroups;
-    if (pl.nx > kQgXMax) pl.nx = kQgXMax;
-    pl.nraw = (room - pl.nx * stage) / kRaw / kQgGroups * kQgGroups;
-    if (pl.nraw > kQgRawMax) pl.nraw = kQgRawMax;
+    // filling has waited for its last one (copies may land out of order).  Activations come from L2: few stages;
+    // the weights' trip to memory wants as many bytes on their way as there is room for.
+    auto turns = [](int n, int most) { return (n < most ? n : most) / kQgGroups * kQgGroups; };
+    pl.nx = kXMin;
+    if (pl.nx * stage + 4 * kRaw > room) pl.nx = turns((room - 4 * kRaw) / stage, kXMin);
+    pl.nraw = turns((room - pl.nx * stage) / kRaw, kRawMax);
+    pl.nx = turns((room - pl.nraw * kRaw) / stage, kXMax);
     if (pl.nstage < kQgGroups || pl.nx < kQgGroups || pl.nraw < kQgGroups) return pl;
-    pl.smem = (size_t)pl.nx * stage + (size_t)pl.nraw * kRaw + 512 + 1024;
+    pl.smem = (size_t)pl.nx * stage + (size_t)pl.nraw * kRaw + kTail + 1024;
     const long long units = (long long)pl.mtiles * pl.ntiles * pl.ks, workers = sms / pl.cg;
     if (units > (1ll << 30)) return pl;
     pl.grid = (int)(units < workers ? units : workers) * pl.cg;
@@ -514,15 +575,11 @@ cudaError_t launch_q8c_gemm(const QcGemmPlan& pl, const QcCall& c, void* ws, uns
     cudaError_t e = launch_q8c_prep(c.a, c.w.K, QcPrep{wsb, xs, xn, pitch}, true, s);
     if (e != cudaSuccess) return e;
     // activations: 64 K x rows x 1 x pitch / 64; a box has a block's rows (half a pair's) and two of the last
-    CUtensorMap tx, tw;
+    CUtensorMap tx;
     const unsigned long long xdims[4] = {64, (unsigned long long)M, 1, (unsigned long long)pitch / 64};
     const unsigned long long xstrides[3] = {(unsigned long long)pitch * 2, (unsigned long long)pitch * 2 * M, 128};
     const unsigned xbox[4] = {64, (unsigned)(pl.bx / pl.cg), 1, 2};
     if (!make_map_nd(&tx, CU_TENSOR_MAP_DATA_TYPE_FLOAT16, wsb, 4, xdims, xstrides, xbox, CU_TENSOR_MAP_SWIZZLE_128B)) return cudaErrorInvalidValue;
-    // raw weights: row blocks, 8-byte elements, a box of a segment of eight of them
-    if (!make_map(&tw, CU_TENSOR_MAP_DATA_TYPE_UINT64, c.w.data, (unsigned long long)c.w.KS * (kQcSeg / 8), (unsigned long long)c.w.RB,
-                  (unsigned long long)c.w.KS * kQcSeg, kQcSeg / 8, 8, CU_TENSOR_MAP_SWIZZLE_NONE))
-        return cudaErrorInvalidValue;
     GemmParams p;
     p.c = c;
     p.part = reinterpret_cast<int*>(wsb + pl.ws_part);
@@ -542,7 +599,7 @@ cudaError_t launch_q8c_gemm(const QcGemmPlan& pl, const QcCall& c, void* ws, uns
     p.stall_block = (unsigned)pl.cg - 1u;  // of a pair the second one, whose partner finds out by its own waits
     p.off_raw = pl.nx * (pl.bx / pl.cg) * 256;
     p.off_bar = p.off_raw + pl.nraw * kRaw;
-    e = pl.cg == 2 ? gemm_go<2>(pl, tx, tw, p, smem_max, s) : gemm_go<1>(pl, tx, tw, p, smem_max, s);
+    e = pl.cg == 2 ? gemm_go<2>(pl, tx, p, smem_max, s) : gemm_go<1>(pl, tx, p, smem_max, s);
     if (e != cudaSuccess || pl.ks == 1) return e;
     const dim3 grid((unsigned)((c.w.N + 255) / 256), (unsigned)M);
     return launch_pdl_2d(q8c_sum_kernel, grid.x, grid.y, 256, 0, s, (const int*)p.part, pl.ks, M, c.w.N, reinterpret_cast<const float*>(c.w.data + c.w.scale_off),

@@ -13,7 +13,8 @@ __global__ void __launch_bounds__(256) q8c_pack_kernel(const int8_t* __restrict_
     if (threadIdx.x < 16) sq[threadIdx.x] = 0u;
     __syncthreads();
     const int rb = blockIdx.x, n16 = w.KS * 128;  // 16-byte pieces of a row block: KS x 2 tiles x 2 halves x 32 lanes
-    uint4* to = reinterpret_cast<uint4*>(out + (long long)rb * w.KS * kQcSeg);
+    uint8_t* to = out + qc_row_block(w, rb);
+    const int step = qc_step(w, rb);
     for (int i = threadIdx.x; i < n16; i += 256) {
         const int lane = i & 31, row = (lane >> 2) + 8 * (i >> 5 & 1), n = rb * 16 + row, k = (i >> 6) * 64 + (lane & 3) * 16;
         uint4 v = make_uint4(0u, 0u, 0u, 0u);
@@ -29,7 +30,7 @@ __global__ void __launch_bounds__(256) q8c_pack_kernel(const int8_t* __restrict_
                 v = make_uint4(u[0], u[1], u[2], u[3]);
             }
         }
-        to[i] = v;
+        reinterpret_cast<uint4*>(to + (long long)(i >> 7) * step)[i & 127] = v;
         int s = dp4a(v.x, v.x, 0);
         s = dp4a(v.y, v.y, s);
         s = dp4a(v.z, v.z, s);
@@ -46,12 +47,13 @@ __global__ void __launch_bounds__(256) q8c_pack_kernel(const int8_t* __restrict_
 
 __global__ void __launch_bounds__(256) q8c_dequantize_kernel(const QcWeights w, float* out) {
     const int rb = blockIdx.x, n16 = w.KS * 128;
-    const uint4* from = reinterpret_cast<const uint4*>(w.data + (long long)rb * w.KS * kQcSeg);
+    const uint8_t* from = w.data + qc_row_block(w, rb);
+    const int step = qc_step(w, rb);
     const float* scales = reinterpret_cast<const float*>(w.data + w.scale_off) + rb * 16;
     for (int i = threadIdx.x; i < n16; i += 256) {
         const int lane = i & 31, row = (lane >> 2) + 8 * (i >> 5 & 1), n = rb * 16 + row, k = (i >> 6) * 64 + (lane & 3) * 16;
         if (n >= w.N) continue;
-        const uint4 v = from[i];
+        const uint4 v = reinterpret_cast<const uint4*>(from + (long long)(i >> 7) * step)[i & 127];
         const uint32_t u[4] = {v.x, v.y, v.z, v.w};
         const float s = scales[row];
 #pragma unroll

@@ -2,13 +2,15 @@
 //
 // Mathematics.  Integer warp MMAs (16 weight rows x 32 K x 8 activation rows,
 // int32 sums: exact for every K that the layout takes) on the codes as they
-// are; the warps that split a row block's K add their int32 sums, and one f32
+// are; a row block's int32 sums are added where warps split it, and one f32
 // expression makes a result of it (qc_scale).
 //
 // Bound by the weight stream, a byte a weight.  One persistent block an SM
-// over an equal share of the row blocks; every warp streams its segments
-// through its own ring of asynchronous 16-byte copies, two conflict-free
-// 16-byte loads a lane and tile, no conversion.  The integer MMAs (152 TOPS on
+// over an equal share of the row blocks, whose segments are dealt to its warps in
+// equal contiguous runs, wherever row blocks end; every warp streams its own
+// through a ring of asynchronous 16-byte copies, two conflict-free 16-byte loads
+// a lane and tile, no conversion, and waits for no other until the parts of cut
+// row blocks are added at the end.  The integer MMAs (152 TOPS on
 // this GPU) would take 25 us of the 35 that the weights of 28672 x 8192 take
 // from memory, for up to 8 rows.
 // Activations are staged once, as codes, 64 bytes a tile and row (rows a
@@ -30,9 +32,9 @@ constexpr int kStatic = 1024;   // the kernel's static arrays, rounded up
 
 struct RowsParams {
     QcCall c;
-    int cols, wk, wk_log2, wr, pitch, quant;
+    int cols, pitch, quant;
     int kx;  // columns of codes that are there to be read: K, or the padded row of the preparation
-    int off_zero, off_scale, off_red, off_ring;
+    int off_zero, off_scale, off_part, off_ring;
 };
 
 __device__ __forceinline__ void mma_s8_add(int d[4], uint32_t a0, uint32_t a1, uint32_t a2, uint32_t a3, uint32_t b0, uint32_t b1) {
@@ -54,26 +56,29 @@ __device__ __forceinline__ void raw_floats(const uint4 u[2], float f[8]) {
 }
 
 // Quantizes `rows` rows (from row m0) into shared memory; top: a word per row.  Rows are aligned, K a
-// multiple of 8.  Two trips over the values, four pieces of 8 a thread in flight.
+// multiple of 8.  Two trips over the values (one, where they fit the registers), four pieces of 8 a thread in flight.
 template <int XT>
 __device__ __forceinline__ void stage_floats(uint8_t* sm, float* scale, uint32_t* top, const RowsParams& p, int m0, int rows, int tid, int nthr) {
     const int n8 = p.c.w.KS * 16, n = rows * n8, K = p.c.w.K;  // pieces of 8 values; a half warp's are one row's
     const uint8_t* x = static_cast<const uint8_t*>(p.c.a.x) + m0 * p.c.a.ld * x_size(XT);
     if (tid < rows) top[tid] = 0u;
     __syncthreads();
+    uint4 u[4][2];
+    const bool once = n <= 4 * nthr;  // the values stay in registers
 #pragma unroll 1
     for (int pass = 0; pass < 2; ++pass) {
 #pragma unroll 1
         for (int i0 = 0; i0 < n; i0 += 4 * nthr) {
-            uint4 u[4][2];
+            if (pass == 0 || !once) {
 #pragma unroll
-            for (int j = 0; j < 4; ++j) {
-                const int i = i0 + j * nthr + tid, r = i / n8, k = 8 * (i - r * n8);
-                u[j][0] = u[j][1] = make_uint4(0u, 0u, 0u, 0u);
-                if (i >= n || k >= K) continue;
-                const uint4* from = reinterpret_cast<const uint4*>(x + (r * p.c.a.ld + k) * x_size(XT));
-                u[j][0] = __ldg(from);
-                if (XT == X_F32) u[j][1] = __ldg(from + 1);
+                for (int j = 0; j < 4; ++j) {
+                    const int i = i0 + j * nthr + tid, r = i / n8, k = 8 * (i - r * n8);
+                    u[j][0] = u[j][1] = make_uint4(0u, 0u, 0u, 0u);
+                    if (i >= n || k >= K) continue;
+                    const uint4* from = reinterpret_cast<const uint4*>(x + (r * p.c.a.ld + k) * x_size(XT));
+                    u[j][0] = __ldg(from);
+                    if (XT == X_F32) u[j][1] = __ldg(from + 1);
+                }
             }
 #pragma unroll
             for (int j = 0; j < 4; ++j) {
@@ -128,55 +133,41 @@ __global__ void __launch_bounds__(kMaxWarps * 32, 1) q8c_rows_kernel(const RowsP
     __shared__ uint32_t top[32];
     const QcCall& c = p.c;
     const QcWeights& w = c.w;
-    const int tid = threadIdx.x, warp = __shfl_sync(0xffffffffu, tid >> 5, 0), lane = tid & 31, g = lane >> 2, t = lane & 3, nthr = blockDim.x;
-    const int wk = p.wk, wr = p.wr, kw = warp & (wk - 1), rw = warp >> p.wk_log2;
+    const int tid = threadIdx.x, warp = __shfl_sync(0xffffffffu, tid >> 5, 0), lane = tid & 31, g = lane >> 2, t = lane & 3, nthr = blockDim.x, warps = nthr >> 5;
+    const int KS = w.KS;
     uint8_t* ring = sm + p.off_ring + warp * (kDepth * kQcSeg);
     float* scale = reinterpret_cast<float*>(sm + p.off_scale);
-    int* red = reinterpret_cast<int*>(sm + p.off_red);
-    constexpr int kRed = NB * 128;  // sums of a warp: [column][16 rows]
-    int flip = 0;                   // which of its two areas a row block's sums use
+    int4* parts = reinterpret_cast<int4*>(sm + p.off_part);  // [warp][2][NB][32]: a row block's part that does not reach its end: 1; that does: 0
     if (tid == 0) *reinterpret_cast<uint4*>(sm + p.off_zero) = make_uint4(0u, 0u, 0u, 0u);  // what lanes without a column read
     grid_dep_launch();
 
-    const int nit = (w.KS + wk - 1) >> p.wk_log2;  // segments per warp and row block
-    const long long rb_bytes = (long long)w.KS * kQcSeg;
     const int items = (c.a.M + p.cols - 1) / p.cols;
     const long long work = (long long)items * w.RB;  // row blocks of items, end to end: an equal share a block
     const long long w0 = (long long)blockIdx.x * work / gridDim.x, w1 = (long long)(blockIdx.x + 1) * work / gridDim.x;
     const float* sw = reinterpret_cast<const float*>(w.data + w.scale_off);
     bool waited = false;
-    int acc[NB][4];
-#pragma unroll
-    for (int b = 0; b < NB; ++b)
-#pragma unroll
-        for (int i = 0; i < 4; ++i) acc[b][i] = 0;
 
     for (long long at = w0; at < w1;) {
-        cp_async_wait<0>();  // the last item's (empty) groups
         const int item = (int)(at / w.RB), rb0 = (int)(at - (long long)item * w.RB);
         const int rb1 = (int)min((long long)w.RB, rb0 + (w1 - at));
         at += rb1 - rb0;
         const int m0 = item * p.cols, rows = min(p.cols, c.a.M - m0);
-        const int groups = (rb1 - rb0 + wr - 1) / wr;
-        int left = rb0 + rw < rb1 ? ((rb1 - rb0 - rw + wr - 1) / wr) * nit : 0;
-        int li = 0, lv = kw, ls = 0;
-        const uint8_t* lp = w.data + (rb0 + rw) * rb_bytes + kw * kQcSeg + lane * 16;
-        const long long lback = wr * rb_bytes - (long long)nit * wk * kQcSeg;
+        // this warp's segments of the item's row blocks, end to end
+        const int total = (rb1 - rb0) * KS, s0 = (int)((long long)warp * total / warps), s1 = (int)((long long)(warp + 1) * total / warps);
+        int left = s1 - s0, ls = 0, lrb = rb0 + s0 / KS, lrem = KS - s0 % KS, step = qc_step(w, lrb);
+        const uint8_t* lp = w.data + qc_row_block(w, lrb) + (long long)(KS - lrem) * step + lane * 16;
         const uint32_t to = smem_u32(ring) + lane * 16;
         auto load = [&]() {  // a group of copies, empty past the end, so that the groups' count is the ring's
             if (left > 0) {
                 --left;
-                if (lv < w.KS) {
-                    const uint32_t d = to + ls * kQcSeg;
+                const uint32_t d = to + ls * kQcSeg;
 #pragma unroll
-                    for (int i = 0; i < 4; ++i) cp_async16(d + 512 * i, lp + 512 * i);
-                }
-                lv += wk;
-                lp += wk * kQcSeg;
-                if (++li == nit) {
-                    li = 0;
-                    lv = kw;
-                    lp += lback;
+                for (int i = 0; i < 4; ++i) cp_async16(d + 512 * i, lp + 512 * i);
+                lp += step;
+                if (--lrem == 0) {  // the next row block
+                    lrem = KS;
+                    step = qc_step(w, ++lrb);
+                    lp = w.data + qc_row_block(w, lrb) + lane * 16;
                 }
             }
             ls = ls + 1 == kDepth ? 0 : ls + 1;
@@ -188,75 +179,116 @@ __global__ void __launch_bounds__(kMaxWarps * 32, 1) q8c_rows_kernel(const RowsP
             grid_dep_wait();
             waited = true;
         }
-        __syncthreads();  // the last item's activations are no longer read
         if (!p.quant) stage_codes(sm, scale, p, m0, rows, tid, nthr);
         else if (c.a.xt == X_F32) stage_floats<X_F32>(sm, scale, top, p, m0, rows, tid, nthr);
         else if (c.a.xt == X_F16) stage_floats<X_F16>(sm, scale, top, p, m0, rows, tid, nthr);
         else stage_floats<X_BF16>(sm, scale, top, p, m0, rows, tid, nthr);
         __syncthreads();
 
-        // this lane's columns (8 b + g) at offset xp, xq bytes from a tile to the next (0: it has no column)
-        int xp[NB], xq[NB];
+        // what a row block's results need besides their sums, asked for when the row block begins
+        float w0s = 0.0f, w1s = 0.0f, b0 = 0.0f, b1 = 0.0f;
+        auto ask = [&](int rb) {
+            const int n = rb * 16 + g;
+            const bool on0 = n < w.N, on1 = n + 8 < w.N;
+            w0s = on0 ? __ldg(sw + n) : 0.0f;
+            w1s = on1 ? __ldg(sw + n + 8) : 0.0f;
+            b0 = c.bias && on0 ? __ldg(c.bias + n) : 0.0f;
+            b1 = c.bias && on1 ? __ldg(c.bias + n + 8) : 0.0f;
+        };
+        // a row block's 16 x 8 NB sums to their places: column 8 b + 2 t + i, rows g and g + 8
+        auto put = [&](const int (&v)[NB][4], int rb) {
+            const int n = rb * 16 + g;
+            const bool on0 = n < w.N, on1 = n + 8 < w.N;
 #pragma unroll
-        for (int b = 0; b < NB; ++b) {
-            const bool on = 8 * b + g < rows;
-            xq[b] = on ? 64 : 0;
-            xp[b] = on ? (8 * b + g) * p.pitch + t * 16 : p.off_zero;
-        }
-        int crb = rb0 + rw, cs = 0;  // row block, ring place
-        for (int gi = 0; gi < groups; ++gi, crb += wr, flip ^= 1) {
-            if (crb >= rb1) continue;
-            int v = kw, xo[NB];
+            for (int b = 0; b < NB; ++b)
 #pragma unroll
-            for (int b = 0; b < NB; ++b) xo[b] = xp[b] + kw * 2 * xq[b];
-            for (int ci = 0; ci < nit; ++ci, v += wk) {
+                for (int i = 0; i < 2; ++i) {
+                    const int r = 8 * b + 2 * t + i;
+                    if (r >= rows) continue;
+                    const float sx = scale[r];
+                    const long long o = (long long)(m0 + r) * w.N + n;
+                    if (on0) x_store(c.y, c.yt, o, qc_scale((float)v[b][i], w0s, sx, b0));
+                    if (on1) x_store(c.y, c.yt, o + 8, qc_scale((float)v[b][2 + i], w1s, sx, b1));
+                }
+        };
+        int acc[NB][4];
+        auto clear = [&]() {
+#pragma unroll
+            for (int b = 0; b < NB; ++b)
+#pragma unroll
+                for (int i = 0; i < 4; ++i) acc[b][i] = 0;
+        };
+        clear();
+        int cut = -1, cut_rb = 0;  // the row block that this warp completes but did not begin: its first one
+        float cut_w0 = 0.0f, cut_w1 = 0.0f, cut_b0 = 0.0f, cut_b1 = 0.0f;
+        int cs = 0, seg = s0 % KS, rb = rb0 + s0 / KS;  // ring place; segment in the row block
+        bool began = seg == 0;
+        for (int i = s0; i < s1; seg = 0, ++rb) {
+            const int end = min(s1, i - seg + KS);
+            const bool done = end == i - seg + KS;
+            // this lane's columns (8 b + g) at xo, xq bytes from a tile to the next (0: it has no column)
+            int xo[NB], xq[NB];
+#pragma unroll
+            for (int b = 0; b < NB; ++b) {
+                const bool on = 8 * b + g < rows;
+                xq[b] = on ? 64 : 0;
+                xo[b] = on ? (8 * b + g) * p.pitch + t * 16 + seg * 128 : p.off_zero;
+            }
+            const int from = i - seg;
+            if (done) ask(rb);
+            for (; i < end; ++i) {
                 cp_async_wait<kDepth - 2>();
                 __syncwarp();  // every lane's copies of this segment have landed, and the last one has been read
                 load();
                 const uint8_t* sp = ring + cs * kQcSeg + lane * 16;
                 cs = cs + 1 == kDepth ? 0 : cs + 1;
-                if (v < w.KS) {
 #pragma unroll
-                    for (int h = 0; h < 2; ++h) {
-                        const uint4 a = *reinterpret_cast<const uint4*>(sp + 1024 * h), e = *reinterpret_cast<const uint4*>(sp + 1024 * h + 512);
+                for (int h = 0; h < 2; ++h) {
+                    const uint4 a = *reinterpret_cast<const uint4*>(sp + 1024 * h), e = *reinterpret_cast<const uint4*>(sp + 1024 * h + 512);
 #pragma unroll
-                        for (int b = 0; b < NB; ++b) {
-                            const uint4 xv = *reinterpret_cast<const uint4*>(sm + xo[b] + h * xq[b]);
-                            mma_s8_add(acc[b], a.x, e.x, a.y, e.y, xv.x, xv.y);
-                            mma_s8_add(acc[b], a.z, e.z, a.w, e.w, xv.z, xv.w);
-                        }
+                    for (int b = 0; b < NB; ++b) {
+                        const uint4 xv = *reinterpret_cast<const uint4*>(sm + xo[b] + h * xq[b]);
+                        mma_s8_add(acc[b], a.x, e.x, a.y, e.y, xv.x, xv.y);
+                        mma_s8_add(acc[b], a.z, e.z, a.w, e.w, xv.z, xv.w);
                     }
                 }
 #pragma unroll
-                for (int b = 0; b < NB; ++b) xo[b] += wk * 2 * xq[b];
+                for (int b = 0; b < NB; ++b) xo[b] += 2 * xq[b];
             }
-            // the row block's sums
-            int* mine = red + (flip * (nthr / 32) + warp) * kRed;
+            if (done && began) {
+                put(acc, rb);
+            } else {
 #pragma unroll
-            for (int b = 0; b < NB; ++b) {
-                const int col = 8 * b + 2 * t;
-                if (col < rows) {
-                    mine[col * 16 + g] = acc[b][0];
-                    mine[col * 16 + g + 8] = acc[b][2];
+                for (int b = 0; b < NB; ++b) parts[((warp * 2 + (done ? 0 : 1)) * NB + b) * 32 + lane] = make_int4(acc[b][0], acc[b][1], acc[b][2], acc[b][3]);
+                if (done) {
+                    cut = from;
+                    cut_rb = rb;
+                    cut_w0 = w0s, cut_w1 = w1s, cut_b0 = b0, cut_b1 = b1;
                 }
-                if (col + 1 < rows) {
-                    mine[(col + 1) * 16 + g] = acc[b][1];
-                    mine[(col + 1) * 16 + g + 8] = acc[b][3];
-                }
-                acc[b][0] = acc[b][1] = acc[b][2] = acc[b][3] = 0;
             }
-            if (wk == 1) __syncwarp();
-            else asm volatile("bar.sync %0, %1;" ::"r"(1 + rw), "r"(wk * 32) : "memory");
-            const int* from = red + (flip * (nthr / 32) + rw * wk) * kRed;
-            // the warps take turns at a short row block's sums
-            for (int o = ((kw + gi) & (wk - 1)) * 32 + lane; o < rows * 16; o += wk * 32) {
-                int sum = 0;
-#pragma unroll 4
-                for (int k2 = 0; k2 < wk; ++k2) sum += from[k2 * kRed + o];
-                const int n = crb * 16 + (o & 15), r = o >> 4;
-                if (n < w.N) x_store(c.y, c.yt, (long long)(m0 + r) * w.N + n, qc_scale(sum, __ldg(sw + n), scale[r], c.bias ? __ldg(c.bias + n) : 0.0f));
-            }
+            began = true;
+            clear();
         }
+        cp_async_wait<0>();
+        __syncthreads();  // all parts are there, and the activations are no longer read
+        if (cut >= 0) {
+            int o = warp - 1;
+            while ((int)((long long)o * total / warps) > cut) --o;
+            for (; o <= warp; ++o) {
+                if ((int)((long long)o * total / warps) == (int)((long long)(o + 1) * total / warps)) continue;  // no segments
+#pragma unroll
+                for (int b = 0; b < NB; ++b) {
+                    const int4 u = parts[((o * 2 + (o == warp ? 0 : 1)) * NB + b) * 32 + lane];
+                    acc[b][0] += u.x;
+                    acc[b][1] += u.y;
+                    acc[b][2] += u.z;
+                    acc[b][3] += u.w;
+                }
+            }
+            w0s = cut_w0, w1s = cut_w1, b0 = cut_b0, b1 = cut_b1;
+            put(acc, cut_rb);
+        }
+        if (at < w1) __syncthreads();  // the parts and the scales have been read
     }
     if (!waited) grid_dep_wait();
 }
@@ -285,43 +317,36 @@ QcRowsPlan plan_q8c_rows(const QcCall& c, int sms, int smem_max) {
     pl.pitch = w.KS * 128 + 64;
     const long long room = smem_max - kStatic - 1024;
     auto nb_of = [](int cols) { return cols <= 8 ? 1 : cols <= 16 ? 2 : 4; };
-    auto fixed = [&](int cols, int warps) { return (long long)round_up(cols * 4, 16) + 16 + 2ll * warps * nb_of(cols) * 512 + (long long)warps * kDepth * kQcSeg; };
+    auto fixed = [&](int cols, int warps) { return (long long)round_up(cols * 4, 16) + 16 + warps * 1024ll * nb_of(cols) + (long long)warps * kDepth * kQcSeg; };
+    if ((long long)w.RB * w.KS > INT32_MAX) return pl;
     double best = 0;
     for (int most : {8, 16, 32}) {
         int cols = c.a.M < most ? c.a.M : most;
-        while (cols > 1 && (long long)cols * pl.pitch + fixed(cols, 8) > room) --cols;
-        if ((long long)cols * pl.pitch + fixed(cols, 8) > room) continue;
+        while (cols > 1 && cols * (long long)pl.pitch + fixed(cols, 8) > room) --cols;
         const int items = (c.a.M + cols - 1) / cols;
         cols = (c.a.M + items - 1) / items;
         const int nb = nb_of(cols);
         for (int warps : {16, 8}) {
-            if ((long long)cols * pl.pitch + fixed(cols, warps) > room) continue;
-            for (int wk = 1; wk <= warps; wk *= 2) {
-                const int wr = warps / wk, nit = (w.KS + wk - 1) / wk;
-                if (wr > 15 && wk > 1) continue;  // named barriers
-                const long long work = (long long)items * w.RB, blocks = work < sms ? work : sms;
-                const double share = (double)work / blocks;
-                // segments a warp takes in turn and its row blocks' barriers and sums (about one each); an
-                // item's staging
-                const double cost = ceil(share / wr) * (nit + 1.0) * (warps / 8.0) * (nb == 1 ? 1.0 : nb == 2 ? 1.3 : 2.4) + (double)items / blocks * cols * w.KS * 0.1;
-                if (best == 0 || cost < 0.999 * best || (cost <= 1.001 * best && nb <= pl.nb && wk > pl.wk)) {
-                    best = cost;
-                    pl.cols = cols;
-                    pl.nb = nb;
-                    pl.warps = warps;
-                    pl.wk = wk;
-                    pl.blocks = (int)blocks;
-                    pl.items = items;
-                }
+            if (cols * (long long)pl.pitch + fixed(cols, warps) > room) continue;
+            const long long work = (long long)items * w.RB, blocks = work < sms ? work : sms;
+            const double share = (double)((work + blocks - 1) / blocks);  // row blocks
+            // segments of a block, more slowly with more columns; a trip to memory and the staging per item
+            const double cost = share * w.KS * (nb == 1 ? 1.0 : nb == 2 ? 1.4 : 2.6) * (warps == 8 ? 1.4 : 1.0) + (1.0 + (double)(items - 1) * blocks / (items * (double)blocks)) * (40.0 + cols * w.KS * 0.1);
+            if (best == 0 || cost < best) {
+                best = cost;
+                pl.cols = cols;
+                pl.nb = nb;
+                pl.warps = warps;
+                pl.blocks = (int)blocks;
+                pl.items = items;
             }
         }
     }
     if (best == 0) return pl;
-    const long long act = (long long)pl.cols * pl.pitch;
-    pl.off_zero = (int)act;
+    pl.off_zero = pl.cols * pl.pitch;
     pl.off_scale = pl.off_zero + 16;
-    pl.off_red = pl.off_scale + round_up(pl.cols * 4, 16);
-    pl.off_ring = pl.off_red + 2 * pl.warps * pl.nb * 512;
+    pl.off_part = pl.off_scale + round_up(pl.cols * 4, 16);
+    pl.off_ring = pl.off_part + pl.warps * 1024 * pl.nb;
     pl.smem = (size_t)pl.off_ring + (size_t)pl.warps * kDepth * kQcSeg;
     // what is not read 16 bytes at a time goes through the preparation, as does what would take each
     // block longer than a launch: see rows_direct
@@ -345,13 +370,10 @@ cudaError_t launch_q8c_rows(const QcRowsPlan& pl, const QcCall& c, void* ws, int
     p.kx = pl.prep ? c.w.KS * 128 : c.w.K;
     p.quant = p.c.a.scales == nullptr;
     p.cols = pl.cols;
-    p.wk = pl.wk;
-    p.wr = pl.warps / pl.wk;
-    p.wk_log2 = pl.wk == 1 ? 0 : pl.wk == 2 ? 1 : pl.wk == 4 ? 2 : pl.wk == 8 ? 3 : 4;
     p.pitch = pl.pitch;
     p.off_zero = pl.off_zero;
     p.off_scale = pl.off_scale;
-    p.off_red = pl.off_red;
+    p.off_part = pl.off_part;
     p.off_ring = pl.off_ring;
     return pl.nb == 1 ? rows_go<1>(pl, p, smem_max, s) : pl.nb == 2 ? rows_go<2>(pl, p, smem_max, s) : rows_go<4>(pl, p, smem_max, s);
 }
