@@ -188,7 +188,7 @@ cudaError_t launch_q8c_rows(const QcRowsPlan& pl, const QcCall& c, void* ws, int
 
 struct QcGemmPlan {
     bool ok = false;
-    int cg = 0, bx = 0, nacc = 0, accw = 0, mtiles = 0, ntiles = 0, nraw = 0, nx = 0, nstage = 0, grid = 0, ks = 0;
+    int cg = 0, kt = 0, bx = 0, nacc = 0, accw = 0, mtiles = 0, ntiles = 0, nraw = 0, nx = 0, nstage = 0, grid = 0, ks = 0;
     size_t smem = 0, ws_scale = 0, ws_norm = 0, ws_part = 0, workspace = 0;
 };
 QcGemmPlan plan_q8c_gemm(const QcCall& c, int sms, int smem_max);

@@ -18,8 +18,9 @@
 // SM, pairs of blocks (cta_group::2) on 256 weight rows x up to 256 activation
 // rows; converted weights are the A operand in tensor memory, activations come
 // by TMA in 128-byte swizzled tiles.  19 warps' roles:
-//   warp 0      activation tiles, 128 K each
-//   warp 1      eight MMAs a tile
+//   warp 0      activation tiles, 128 K each (256 for up to 128 activation rows: handing a tile from role to role
+//               takes some 600 cycles, more than the MMAs of 128 K take there)
+//   warp 1      eight MMAs per 128 K
 //   warp 2      raw weights, a panel's 128 K (16 KB) a copy
 //   warps 3-10  epilogue: results from the accumulator, scaled
 //   warps 11-26 conversion: 32 codes a lane and tile of 64 K, ten instructions for eight
@@ -34,14 +35,14 @@
 namespace qmm {
 namespace {
 
-constexpr int kRaw = 8 * kQcSeg;      // bytes of a raw stage
-constexpr int kRestart = 8;           // tiles of 128 K per accumulation where sums may pass 2^24
+constexpr int kRaw = 8 * kQcSeg;      // bytes of a panel's 128 K
+constexpr int kRestart = 8;           // times 128 K per accumulation where sums may pass 2^24
 constexpr int kMaxBX = 256;
 constexpr int kXMax = 8, kXMin = 4, kRawMax = 12;  // stages, at most: activations (and at least), raw weights
 constexpr int kBars = (2 * kXMax + 2 * kQgStageMax + 2 * kRawMax + 4) * 8;  // bytes of the mbarriers
 constexpr int kWarpCols = kMaxBX / kQgEpiHalves;                            // columns that an epilogue warp reads out
 constexpr int kTail = kBars + 32 + kQgEpiWarps * kWarpCols * 4;             // behind the rings: mbarriers, three words, the columns' factors
-static_assert(kXMax % kQgGroups == 0 && kRawMax % kQgGroups == 0 && kBars % 16 == 0, "rings of whole turns");
+static_assert(kRawMax % kQgGroups == 0 && kBars % 16 == 0, "rings of whole turns");
 
 struct GemmParams {
     QcCall c;
@@ -50,6 +51,7 @@ struct GemmParams {
     const uint32_t* xn;     // their sums of squares
     unsigned* err;
     int bx, nacc, accw, mtiles, ntiles, nraw, nx, nstage, ks;
+    int ktiles;             // tiles in K
     int off_raw, off_bar;
     int stall;
     unsigned stall_block;
@@ -60,7 +62,8 @@ struct Unit {
     int split, j0, j1;  // K slice, its tiles
 };
 
-template <int CG>
+// KT: 128 K's in a tile
+template <int CG, int KT>
 __global__ void __launch_bounds__(kQgThreads, 1) q8c_gemm_kernel(const __grid_constant__ CUtensorMap tx, const GemmParams p) {
     extern __shared__ __align__(1024) uint8_t smraw[];
     uint8_t* sm = smraw + ((1024 - (smem_u32(smraw) & 1023)) & 1023);
@@ -132,34 +135,36 @@ __global__ void __launch_bounds__(kQgThreads, 1) q8c_gemm_kernel(const __grid_co
         un.nt = (u - st * p.ntiles) * CG + (int)rank;
         un.p0 = st * size;
         un.n = max(min(size, M - un.p0), 0);
-        un.j0 = (int)((long long)un.split * w.KS / p.ks);
-        un.j1 = (int)((long long)(un.split + 1) * w.KS / p.ks);
+        un.j0 = (int)((long long)un.split * p.ktiles / p.ks);
+        un.j1 = (int)((long long)(un.split + 1) * p.ktiles / p.ks);
         return un;
     };
-    // an activation stage: two 64-K halves of the rows; of a pair, each block has half the rows
+    // an activation stage: 64-K pieces of the rows; of a pair, each block has half the rows
     const int half = p.bx / CG * 128;
-    auto stage = [&](int s) { return sm + s * 2 * half; };
-    auto raw = [&](int s) { return sm + p.off_raw + s * kRaw; };
-    // 64-K halves of tile j that hold any K
-    auto halves = [&](int j) { return w.K - j * 128 > 64 ? 2 : 1; };
+    auto stage = [&](int s) { return sm + s * 2 * KT * half; };
+    auto raw = [&](int s) { return sm + p.off_raw + s * KT * kRaw; };
+    // 64-K pieces of tile j that hold any K
+    auto halves = [&](int j) { return min(2 * KT, (w.K - j * 128 * KT + 63) / 64); };
 
     if (warp == 2) {
         // ------------------------------ raw weights: constant, so at once ------------------------------
         if (lane == 0) {
             QgRing r;
             bool ok = true, wrapped = false;
-            int left = p.stall - 1;
+            int left = p.stall - 1;  // in 128 K
             for (int u = first_unit; u < units && ok; u += unit_step) {
                 const Unit un = place(u);
                 const int bytes = 8 * un.nt < w.RB ? qc_step(w, 8 * un.nt) : 0;
                 const uint8_t* from = w.data + qc_row_block(w, 8 * un.nt);
                 for (int j = un.j0; j < un.j1; ++j) {
                     // injected stall: this block's raw weights end here
-                    if (p.stall && blockIdx.x == p.stall_block && --left < 0) ok = false;
+                    if (p.stall && blockIdx.x == p.stall_block && (left -= KT) < 0) ok = false;
                     if (!ok || !(ok = qg_wait(smem_u32(&r_empty[r.s]), r.ph ^ 1u, flags, p.err))) break;
                     const uint32_t bar = smem_u32(&r_full[r.s]);
-                    mbar_arrive_tx(bar, (uint32_t)bytes);  // a panel's segments of this K; row blocks past the last one keep what was there
-                    if (bytes > 0) bulk_g2s(smem_u32(raw(r.s)), from + (long long)j * bytes, (uint32_t)bytes, bar);
+                    // a panel's segments of this K; row blocks, and K, past the last one keep what was there
+                    const uint32_t all = (uint32_t)(bytes * min(KT, w.KS - j * KT));
+                    mbar_arrive_tx(bar, all);
+                    if (all > 0) bulk_g2s(smem_u32(raw(r.s)), from + (long long)j * KT * bytes, all, bar);
                     r.next(p.nraw);
                     wrapped |= r.s == 0;
                 }
@@ -180,9 +185,9 @@ __global__ void __launch_bounds__(kQgThreads, 1) q8c_gemm_kernel(const __grid_co
                     if (!(ok = qg_wait(smem_u32(&x_empty[g.s]), g.ph ^ 1u, flags, p.err))) break;
                     uint32_t bar = smem_u32(&x_full[g.s]);
                     const uint32_t to = smem_u32(stage(g.s));
-                    if (rank == 0) mbar_arrive_tx(bar, (uint32_t)(CG * 2 * half));
+                    if (rank == 0) mbar_arrive_tx(bar, (uint32_t)(CG * 2 * KT * half));
                     if (CG == 2) bar = leader_addr(bar);
-                    tma_4d<CG>(to, &tx, 0, p0, 0, 2 * j, bar);
+                    tma_4d<CG>(to, &tx, 0, p0, 0, 2 * KT * j, bar);
                     g.next(p.nx);
                     wrapped |= g.s == 0;
                 }
@@ -200,7 +205,7 @@ __global__ void __launch_bounds__(kQgThreads, 1) q8c_gemm_kernel(const __grid_co
         asm volatile("bar.sync 1, %0;" ::"n"((kQgEpiWarps + 1) * 32) : "memory");
         const uint32_t wnorm = __ldg(reinterpret_cast<const uint32_t*>(w.data + w.norm_off));
         const bool restart = (unsigned long long)*reinterpret_cast<volatile uint32_t*>(s_norm) * wnorm >= 1ull << 48;
-        const int chunk = restart ? kRestart : w.KS;
+        const int chunk = restart ? kRestart / KT : p.ktiles;
         if (warp == 1) {
             // ------------------------------ MMA issuer ------------------------------
             if (rank == 0) {
@@ -230,13 +235,13 @@ __global__ void __launch_bounds__(kQgThreads, 1) q8c_gemm_kernel(const __grid_co
                             gx.next(p.nx);
                             ready = next;
                             tc_fence_after();
-                            const uint32_t x0 = lo0 + (uint32_t)((sx * 2 * half) >> 4), a0 = tmem + (uint32_t)(p.nacc * p.accw + 64 * s);
+                            const uint32_t x0 = lo0 + (uint32_t)((sx * 2 * KT * half) >> 4), a0 = tmem + (uint32_t)(p.nacc * p.accw + 64 * KT * s);
                             const int nh = halves(c0 + i);
                             __syncwarp();
                             if (lead && ok) {
 #pragma unroll
-                                for (int h = 0; h < 2; ++h) {
-                                    if (h == 1 && nh == 1) break;
+                                for (int h = 0; h < 2 * KT; ++h) {
+                                    if (h >= nh) break;
 #pragma unroll
                                     for (int kk = 0; kk < 4; ++kk)
                                         qg_mma_tc<CG>(dt, a0 + 32 * h + 8 * kk, ((uint64_t)dhi << 32) | (x0 + (uint32_t)(h * half >> 4) + 2 * kk), idesc,
@@ -413,6 +418,7 @@ __global__ void __launch_bounds__(kQgThreads, 1) q8c_gemm_kernel(const __grid_co
         bool ok = true;
         for (int u = first_unit; u < units && ok; u += unit_step) {
             const Unit un = place(u);
+            const int step = 8 * un.nt < w.RB ? qc_step(w, 8 * un.nt) : 0;  // from 128 K to the next
             // The groups take tiles in turn, whatever a unit's number of them: a group that waits for
             // the release of tile t - nstage has waited for t - groups - nstage, so that with nstage >=
             // groups the stage's barrier is at most one phase behind the wait's parity.
@@ -425,7 +431,7 @@ __global__ void __launch_bounds__(kQgThreads, 1) q8c_gemm_kernel(const __grid_co
                 // tested here, needed after the conversion
                 const uint32_t e_ready = mbar_test(smem_u32(&empty[at.s]), at.ph ^ 1u);
                 const uint8_t* seg = raw(ar.s) + (2 * q + hh) * kQcSeg;
-                const uint32_t col = tmem + ((uint32_t)(32 * q + 16 * hh) << 16) + (uint32_t)(p.nacc * p.accw + 64 * at.s);
+                const uint32_t col = tmem + ((uint32_t)(32 * q + 16 * hh) << 16) + (uint32_t)(p.nacc * p.accw + 64 * KT * at.s);
                 uint32_t v[16];
                 convert(seg, v);
                 announce();
@@ -436,10 +442,15 @@ __global__ void __launch_bounds__(kQgThreads, 1) q8c_gemm_kernel(const __grid_co
                 tc_fence_after();
                 __syncwarp();
                 tc_st_frag<16>(col, v);
-                convert(seg + 1024, v);
-                __syncwarp();
-                if (lane == 0) mbar_arrive(smem_u32(&r_empty[ar.s]));
-                tc_st_frag<16>(col + 32, v);
+#pragma unroll
+                for (int h = 1; h < 2 * KT; ++h) {
+                    convert(seg + (h >> 1) * step + 1024 * (h & 1), v);
+                    if (h == 2 * KT - 1) {
+                        __syncwarp();
+                        if (lane == 0) mbar_arrive(smem_u32(&r_empty[ar.s]));
+                    }
+                    tc_st_frag<16>(col + 32 * h, v);
+                }
                 stored = at.s;
                 if (p.nstage <= kQgGroups) announce();  // no stage to spare
             }
@@ -483,10 +494,10 @@ __global__ void __launch_bounds__(256) q8c_sum_kernel(const int* part, int ks, i
     x_store(y, yt, i, qc_scale((float)v, __ldg(sw + n), __ldg(xs + m), bias ? __ldg(bias + n) : 0.0f));
 }
 
-template <int CG>
+template <int CG, int KT>
 cudaError_t gemm_go(const QcGemmPlan& pl, const CUtensorMap& tx, const GemmParams& p, int smem_max, cudaStream_t s) {
     static unsigned long long done = 0;
-    auto* k = q8c_gemm_kernel<CG>;
+    auto* k = q8c_gemm_kernel<CG, KT>;
     const cudaError_t e = ensure_smem(k, smem_max, done);
     if (e != cudaSuccess) return e;
     cudaLaunchConfig_t cfg = {};
@@ -512,8 +523,8 @@ QcGemmPlan plan_q8c_gemm(const QcCall& c, int sms, int smem_max) {
     QcGemmPlan pl;
     const QcWeights& w = c.w;
     const long long M = c.a.M;
-    // Modelled cycles: a tile of 128 K costs its MMAs (half a cycle a column, at least 40 each) or its
-    // conversion (800); a unit its prologue and, without a second accumulator, the epilogue that the
+    // Modelled cycles: a tile costs its MMAs (half a cycle a column, at least 40 each) or its conversion and
+    // handing over (900; of 256 K 1100); a unit its prologue and, without a second accumulator, the epilogue that the
     // next unit's MMAs wait for; slices of K their sums' traffic and a launch.
     double best = 0;
     for (int cg = 1; cg <= 2; ++cg) {
@@ -522,14 +533,16 @@ QcGemmPlan plan_q8c_gemm(const QcCall& c, int sms, int smem_max) {
         for (long long tiles = (M + most - 1) / most; tiles <= 8 + (M + most - 1) / most; ++tiles) {
             const int bx = (int)((M + tiles - 1) / tiles + unit - 1) / unit * unit;
             const long long mt = (M + bx - 1) / bx, un = (long long)ntiles * mt;
-            const double mma = 8.0 * (cg == 1 ? (bx < 40 ? 40.0 : (double)bx) : bx < 80 ? 40.0 : bx / 2.0), tile = mma > 800.0 ? mma : 800.0;
+            const int kt = bx <= 128 ? 2 : 1, ktiles = (w.KS + kt - 1) / kt;
+            const double mma = 8.0 * kt * (cg == 1 ? (bx < 40 ? 40.0 : (double)bx) : bx < 80 ? 40.0 : bx / 2.0), tile = mma > 700.0 + 200.0 * kt ? mma : 700.0 + 200.0 * kt;
             const double once = bx > 192 ? 1500.0 + 12.0 * bx : 1500.0;
-            for (int ks = 1; ks <= w.KS && ks <= 16 && (ks == 1 || un * ks <= 2 * workers); ++ks) {
+            for (int ks = 1; ks <= ktiles && ks <= 16 && (ks == 1 || un * ks <= 2 * workers); ++ks) {
                 const double waves = (double)((un * ks + workers - 1) / workers);
-                const double cost = waves * ((double)((w.KS + ks - 1) / ks) * tile + once) + (ks > 1 ? 4000.0 + 8.0 * ks * M * w.N / 3000.0 : 0.0);
+                const double cost = waves * ((double)((ktiles + ks - 1) / ks) * tile + once) + (ks > 1 ? 4000.0 + 8.0 * ks * M * w.N / 3000.0 : 0.0);
                 if (best == 0 || cost < 0.98 * best) {
                     best = cost;
                     pl.cg = cg;
+                    pl.kt = kt;
                     pl.bx = bx;
                     pl.ks = ks;
                     pl.mtiles = (int)mt;
@@ -541,19 +554,19 @@ QcGemmPlan plan_q8c_gemm(const QcCall& c, int sms, int smem_max) {
     }
     pl.accw = (pl.bx + 31) / 32 * 32;
     pl.nacc = pl.bx <= 192 ? 2 : 1;  // with two accumulators the epilogue runs beside the next unit's MMAs
-    pl.nstage = (kTcTmemCols - pl.nacc * pl.accw) / 64;
+    pl.nstage = (kTcTmemCols - pl.nacc * pl.accw) / (64 * pl.kt);
     if (pl.nstage > kQgStageMax) pl.nstage = kQgStageMax;
-    const int stage = pl.bx / pl.cg * 256, room = smem_max - kTail - 1024;
-    // Both rings are multiples of the converting groups, so that whoever waits for a stage's next
-    // filling has waited for its last one (copies may land out of order).  Activations come from L2: few stages;
+    const int stage = pl.bx / pl.cg * 256 * pl.kt, raw = kRaw * pl.kt, room = smem_max - kTail - 1024;
+    // The raw ring is a multiple of the converting groups, so that whoever waits for a stage's next filling
+    // has waited for its last one (copies may land out of order).  Activations come from L2: few stages;
     // the weights' trip to memory wants as many bytes on their way as there is room for.
     auto turns = [](int n, int most) { return (n < most ? n : most) / kQgGroups * kQgGroups; };
     pl.nx = kXMin;
-    if (pl.nx * stage + 4 * kRaw > room) pl.nx = turns((room - 4 * kRaw) / stage, kXMin);
-    pl.nraw = turns((room - pl.nx * stage) / kRaw, kRawMax);
-    pl.nx = turns((room - pl.nraw * kRaw) / stage, kXMax);
-    if (pl.nstage < kQgGroups || pl.nx < kQgGroups || pl.nraw < kQgGroups) return pl;
-    pl.smem = (size_t)pl.nx * stage + (size_t)pl.nraw * kRaw + kTail + 1024;
+    while (pl.nx > 2 && pl.nx * stage + 4 * raw > room) --pl.nx;
+    pl.nraw = turns((room - pl.nx * stage) / raw, kRawMax);
+    pl.nx = (room - pl.nraw * raw) / stage < kXMax ? (room - pl.nraw * raw) / stage : kXMax;
+    if (pl.nstage < kQgGroups || pl.nx < 2 || pl.nraw < kQgGroups) return pl;
+    pl.smem = (size_t)pl.nx * stage + (size_t)pl.nraw * raw + kTail + 1024;
     const long long units = (long long)pl.mtiles * pl.ntiles * pl.ks, workers = sms / pl.cg;
     if (units > (1ll << 30)) return pl;
     pl.grid = (int)(units < workers ? units : workers) * pl.cg;
@@ -574,11 +587,11 @@ cudaError_t launch_q8c_gemm(const QcGemmPlan& pl, const QcCall& c, void* ws, uns
     uint32_t* xn = reinterpret_cast<uint32_t*>(wsb + pl.ws_norm);
     cudaError_t e = launch_q8c_prep(c.a, c.w.K, QcPrep{wsb, xs, xn, pitch}, true, s);
     if (e != cudaSuccess) return e;
-    // activations: 64 K x rows x 1 x pitch / 64; a box has a block's rows (half a pair's) and two of the last
+    // activations: 64 K x rows x 1 x pitch / 64; a box has a block's rows (half a pair's) and a tile's part of the last
     CUtensorMap tx;
     const unsigned long long xdims[4] = {64, (unsigned long long)M, 1, (unsigned long long)pitch / 64};
     const unsigned long long xstrides[3] = {(unsigned long long)pitch * 2, (unsigned long long)pitch * 2 * M, 128};
-    const unsigned xbox[4] = {64, (unsigned)(pl.bx / pl.cg), 1, 2};
+    const unsigned xbox[4] = {64, (unsigned)(pl.bx / pl.cg), 1, (unsigned)(2 * pl.kt)};
     if (!make_map_nd(&tx, CU_TENSOR_MAP_DATA_TYPE_FLOAT16, wsb, 4, xdims, xstrides, xbox, CU_TENSOR_MAP_SWIZZLE_128B)) return cudaErrorInvalidValue;
     GemmParams p;
     p.c = c;
@@ -597,9 +610,10 @@ cudaError_t launch_q8c_gemm(const QcGemmPlan& pl, const QcCall& c, void* ws, uns
     p.ks = pl.ks;
     p.stall = stall;
     p.stall_block = (unsigned)pl.cg - 1u;  // of a pair the second one, whose partner finds out by its own waits
-    p.off_raw = pl.nx * (pl.bx / pl.cg) * 256;
-    p.off_bar = p.off_raw + pl.nraw * kRaw;
-    e = pl.cg == 2 ? gemm_go<2>(pl, tx, p, smem_max, s) : gemm_go<1>(pl, tx, p, smem_max, s);
+    p.ktiles = (c.w.KS + pl.kt - 1) / pl.kt;
+    p.off_raw = pl.nx * (pl.bx / pl.cg) * 256 * pl.kt;
+    p.off_bar = p.off_raw + pl.nraw * kRaw * pl.kt;
+    e = pl.cg == 2 ? (pl.kt == 2 ? gemm_go<2, 2>(pl, tx, p, smem_max, s) : gemm_go<2, 1>(pl, tx, p, smem_max, s)) : gemm_go<1, 2>(pl, tx, p, smem_max, s);
     if (e != cudaSuccess || pl.ks == 1) return e;
     const dim3 grid((unsigned)((c.w.N + 255) / 256), (unsigned)M);
     return launch_pdl_2d(q8c_sum_kernel, grid.x, grid.y, 256, 0, s, (const int*)p.part, pl.ks, M, c.w.N, reinterpret_cast<const float*>(c.w.data + c.w.scale_off),
