@@ -177,10 +177,10 @@ cudaError_t launch_q8c_prep(const QcRows& a, int K, const QcPrep& p, bool f16, c
 
 struct QcRowsPlan {
     bool ok = false;
-    int cols = 0, nb = 0, warps = 0, blocks = 0, items = 0;
+    int warps = 0, blocks = 0;
     int pitch = 0;       // bytes of a staged row
-    int prep = 0;        // activations are quantized by a launch of their own
-    int off_zero = 0, off_scale = 0, off_part = 0, off_ring = 0;
+    int prep = 0;        // activations are quantized (or aligned) by a launch of their own
+    int off_zero = 0, off_part = 0, off_ring = 0;
     size_t smem = 0, workspace = 0;
 };
 QcRowsPlan plan_q8c_rows(const QcCall& c, int sms, int smem_max);

@@ -22,8 +22,10 @@ qmm_status describe(const qmm_q8c* d, QcWeights& w) {
     return qc_describe(d->N, d->K, d->data, w) ? QMM_OK : QMM_ERR_SHAPE;
 }
 
-// The kernel that a product goes to.  The row kernel streams the weights once per item of up to 32
-// activation rows, and its integer MMAs are slow; the GEMM has some 8 us of fixed cost.
+// The kernel that a product goes to: up to four rows to the row kernel, where they fit its shared memory.
+// Measured (row kernel / GEMM, us, bf16): 576 x 576, 1, 4 and 8 rows 4.5 / 5.5, 5.1 / 5.5, 5.7 / 5.5; 4096 x 4096
+// 7.6 / 10.1, 11.4 / 10.5, 11.9 / 11.0; 14336 x 4096 13.8 / 15.8, 15.8 / 15.9, 18.1 / 15.9; 28672 x 8192 41 / 48, 44 / 49,
+// 48 / 50.  (The GEMM's time hardly depends on the rows until there are more than 64.)
 struct Choice {
     bool gemm = false, ok = false;
     QcRowsPlan rows;
@@ -32,11 +34,9 @@ struct Choice {
 };
 Choice choose(const QcCall& c, int sms, int smem) {
     Choice ch;
-    const long long size = (long long)c.w.N * c.w.K;
-    if (c.a.M <= 16 || c.a.M * size <= 160000000) ch.rows = plan_q8c_rows(c, sms, smem);
+    ch.rows = plan_q8c_rows(c, sms, smem);
     if (!ch.rows.ok) ch.mm = plan_q8c_gemm(c, sms, smem);
-    if (!ch.rows.ok && !ch.mm.ok) ch.rows = plan_q8c_rows(c, sms, smem);
-    ch.gemm = !ch.rows.ok && ch.mm.ok;
+    ch.gemm = !ch.rows.ok;
     ch.ok = ch.rows.ok || ch.mm.ok;
     ch.workspace = ch.gemm ? ch.mm.workspace : ch.rows.workspace;
     return ch;

@@ -350,7 +350,7 @@ PyObject* matmul8(PyObject*, PyObject* const* a, Py_ssize_t n) {
                  "out is contiguous, of the result's shape, type and device");
         }
         // few values in aligned rows need no workspace (include/qmm.h)
-        const bool direct = M <= 16 && w.K % 16 == 0 && (reinterpret_cast<uintptr_t>(x.data_ptr()) | (uintptr_t)(ld * x.element_size())) % 16 == 0 &&
+        const bool direct = M <= QMM_Q8C_DIRECT_ROWS && w.K % 16 == 0 && w.K <= 32768 && (reinterpret_cast<uintptr_t>(x.data_ptr()) | (uintptr_t)(ld * x.element_size())) % 16 == 0 &&
                             (codes || M * w.K <= QMM_Q8C_DIRECT);
         const Workspace ws(a[7], a[7] == Py_None && !direct ? qmm_q8c_matmul_workspace(&w, codes, M) : 0, x);
         return result(qmm_q8c_matmul(&w, xt, x.data_ptr(), ld, scales, M, bias, yt, y.data_ptr(), ws.p, ws.n, stream_of(device)), y);

@@ -421,7 +421,8 @@ typedef struct {
     int64_t N, K;       /* 1 <= K < 2^17, N <= 2^23 */
 } qmm_q8c;
 
-#define QMM_Q8C_DIRECT 32768
+#define QMM_Q8C_DIRECT_ROWS 4
+#define QMM_Q8C_DIRECT 16384
 
 /* Bytes of the laid-out form; 0 for an invalid shape. */
 size_t qmm_q8c_bytes(int64_t N, int64_t K);
@@ -444,8 +445,8 @@ qmm_status qmm_q8c_quantize(qmm_float xtype, const void* x, int64_t ldx, int64_t
    are.  bias: f32 [N] or NULL.  y [M, N] of ytype, contiguous.
    workspace: qmm_q8c_matmul_workspace(w, x_scales != NULL, M) bytes,
    uninitialised; calls that may overlap need one each.  None is needed for up
-   to 16 rows that start on 16-byte boundaries where K is a multiple of 16 and
-   x is codes, or M K <= QMM_Q8C_DIRECT floats.
+   to QMM_Q8C_DIRECT_ROWS rows that start on 16-byte boundaries, of K <= 32768 in
+   a multiple of 16, that are codes or floats with M K <= QMM_Q8C_DIRECT.
    Errors: TYPE, NULL, SHAPE, ALIGN, WORKSPACE, CUDA. */
 size_t qmm_q8c_matmul_workspace(const qmm_q8c* w, int quantized, int64_t M);
 qmm_status qmm_q8c_matmul(const qmm_q8c* w, qmm_float xtype, const void* x, int64_t ldx, const float* x_scales, int64_t M, const float* bias,
