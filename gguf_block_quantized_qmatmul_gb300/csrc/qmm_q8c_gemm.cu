@@ -294,56 +294,67 @@ __global__ void __launch_bounds__(kQgThreads, 1) q8c_gemm_kernel(const __grid_co
                 for (int i = 0; i < kWords; ++i) table[32 * i + lane] = xs_next[i];
                 __syncwarp();
                 if (u + unit_step < units) ask(place(u + unit_step));
-                // Columns kCols k.., this warp's from `at` on; whole: sums that a float may not hold.  16-bit results go to
-                // memory four at a time, of four rows: a quad of lanes exchanges its 4 x 8 values (a store a value
-                // and column took three times as long).
-                const bool wide = w.N % 4 == 0;
-                auto put = [&](int k, const float v[kCols], int at, const int* whole) {
-                    const int m = un.p0 + kCols * k, left = min(kCols, un.n - kCols * k);
-                    if (p.ks > 1) {
-                        int* to = p.part + ((long long)un.split * M + m) * w.N + n;
+                // 16-bit results go to memory four at a time, of four rows: a quad of lanes exchanges its 4 x 8 values
+                // (a store a value and column took three times as long).  What a chunk needs is worked out before it:
+                // this warp's chunks are 16 columns apart, and the kind of result is told apart outside of them.
+                const bool wide = w.N % 4 == 0 && p.ks == 1 && c.yt != X_F32;
+                const int sub = wide ? 2 * (lane & 3) : 0;  // the first of the columns that this lane writes
+                const long long first = (long long)(un.p0 + kCols * part + sub) * w.N + n - (wide ? lane & 3 : 0) + (p.ks > 1 ? (long long)un.split * M * w.N : 0);
+                const long long stride = (long long)kQgEpiHalves * kCols * w.N;
+                const unsigned long long wn2 = f2pack(wn, wn);
+                // Chunk i of this warp (its columns are `left` of eight), as `kind`.  whole: sums that a float may not hold.
+                auto put = [&](auto kind, int i, int left, const float v[kCols], const int* whole) {
+                    using Y = decltype(kind);
+                    const long long o = first + i * stride;
+                    if constexpr (std::is_same<Y, int>::value) {
+                        int* to = p.part + o;
 #pragma unroll
-                        for (int i = 0; i < kCols; ++i, to += w.N)
-                            if (on && i < left) *to = whole ? whole[i] : __float2int_rn(v[i]);
-                        return;
-                    }
-                    const float4 f0 = *reinterpret_cast<const float4*>(table + at), f1 = *reinterpret_cast<const float4*>(table + at + 4);
-                    const float sx[kCols] = {f0.x, f0.y, f0.z, f0.w, f1.x, f1.y, f1.z, f1.w};
-                    float y[kCols];
+                        for (int e = 0; e < kCols; ++e, to += w.N)
+                            if (on && e < left) *to = whole ? whole[e] : __float2int_rn(v[e]);
+                    } else {
+                        const float4 f0 = *reinterpret_cast<const float4*>(table + kCols * i), f1 = *reinterpret_cast<const float4*>(table + kCols * i + 4);
+                        const float sx[kCols] = {f0.x, f0.y, f0.z, f0.w, f1.x, f1.y, f1.z, f1.w};
+                        float y[kCols];
 #pragma unroll
-                    for (int i = 0; i < kCols; ++i) y[i] = qc_scale(v[i], wn, sx[i], bias);
-                    if (c.yt == X_F32) {
-                        float* to = static_cast<float*>(c.y) + (long long)m * w.N + n;
+                        for (int e = 0; e < kCols; e += 2) {  // qc_scale, its products two at a time (a packed sum would be contracted with them)
+                            const unsigned long long r = mul2(mul2(f2pack(v[e], v[e + 1]), wn2), f2pack(sx[e], sx[e + 1]));
+                            y[e] = __fadd_rn(f2lo(r), bias);
+                            y[e + 1] = __fadd_rn(f2hi(r), bias);
+                        }
+                        Y* to = static_cast<Y*>(c.y) + o;
+                        if constexpr (std::is_same<Y, float>::value) {
 #pragma unroll
-                        for (int i = 0; i < kCols; ++i, to += w.N)
-                            if (on && i < left) *to = y[i];
-                        return;
-                    }
-                    uint32_t h[kCols / 2];  // columns 2 i, 2 i + 1
+                            for (int e = 0; e < kCols; ++e, to += w.N)
+                                if (on && e < left) *to = y[e];
+                        } else if (wide) {
+                            uint32_t h[kCols / 2];  // columns 2 e, 2 e + 1
 #pragma unroll
-                    for (int i = 0; i < kCols / 2; ++i) {
-                        if (c.yt == X_F16) {
-                            const __half2 b = __floats2half2_rn(y[2 * i], y[2 * i + 1]);
-                            h[i] = *reinterpret_cast<const uint32_t*>(&b);
+                            for (int e = 0; e < kCols / 2; ++e) {
+                                if constexpr (std::is_same<Y, __half>::value) {
+                                    const __half2 b = __floats2half2_rn(y[2 * e], y[2 * e + 1]);
+                                    h[e] = *reinterpret_cast<const uint32_t*>(&b);
+                                } else {
+                                    const __nv_bfloat162 b = __floats2bfloat162_rn(y[2 * e], y[2 * e + 1]);
+                                    h[e] = *reinterpret_cast<const uint32_t*>(&b);
+                                }
+                            }
+                            const uint4 t = qg_quad_transpose(h[0], h[1], h[2], h[3], lane);  // columns sub, sub + 1 of the quad's rows
+                            if (on && sub < left) *reinterpret_cast<uint2*>(to) = make_uint2(__byte_perm(t.x, t.y, 0x5410u), __byte_perm(t.z, t.w, 0x5410u));
+                            if (on && sub + 1 < left) *reinterpret_cast<uint2*>(to + w.N) = make_uint2(__byte_perm(t.x, t.y, 0x7632u), __byte_perm(t.z, t.w, 0x7632u));
                         } else {
-                            const __nv_bfloat162 b = __floats2bfloat162_rn(y[2 * i], y[2 * i + 1]);
-                            h[i] = *reinterpret_cast<const uint32_t*>(&b);
+#pragma unroll
+                            for (int e = 0; e < kCols; ++e, to += w.N)
+                                if (on && e < left) *to = to_type<Y>(y[e]);
                         }
                     }
-                    if (wide) {
-                        const uint4 t = qg_quad_transpose(h[0], h[1], h[2], h[3], lane);  // columns 2 l, 2 l + 1 of the quad's rows, l = lane % 4
-                        const int i = 2 * (lane & 3);
-                        uint16_t* to = static_cast<uint16_t*>(c.y) + (long long)(m + i) * w.N + (n - (lane & 3));
-                        if (on && i < left) *reinterpret_cast<uint2*>(to) = make_uint2(__byte_perm(t.x, t.y, 0x5410u), __byte_perm(t.z, t.w, 0x5410u));
-                        if (on && i + 1 < left) *reinterpret_cast<uint2*>(to + w.N) = make_uint2(__byte_perm(t.x, t.y, 0x7632u), __byte_perm(t.z, t.w, 0x7632u));
-                    } else {
-                        uint16_t* to = static_cast<uint16_t*>(c.y) + (long long)m * w.N + n;
-#pragma unroll
-                        for (int i = 0; i < kCols; ++i, to += w.N)
-                            if (on && i < left) *to = (uint16_t)(h[i >> 1] >> (16 * (i & 1)));
-                    }
                 };
-                int sums[kMaxBX / kQgEpiHalves];  // local memory; restarted accumulations only
+                auto as_kind = [&](auto f) {
+                    if (p.ks > 1) f(int());
+                    else if (c.yt == X_F32) f(float());
+                    else if (c.yt == X_F16) f(__half());
+                    else f(__nv_bfloat16());
+                };
+                int sums[kWarpCols];  // local memory; restarted accumulations only
                 for (int c0 = un.j0; c0 < un.j1; c0 += chunk, ++cc) {
                     const int ab = p.nacc == 2 ? (cc & 1) : 0, use = p.nacc == 2 ? (cc >> 1) : cc;
                     if (!(ok = qg_wait_warp(smem_u32(&acc_full[ab]), (uint32_t)(use & 1), false, flags, p.err))) break;
@@ -353,27 +364,32 @@ __global__ void __launch_bounds__(kQgThreads, 1) q8c_gemm_kernel(const __grid_co
                     const bool begin = c0 == un.j0, end = c0 + chunk >= un.j1;
                     uint32_t r[kCols];
                     if (part < nch) tc_ld8(acol + kCols * part, r);
+                    auto chunks = [&](auto take) {  // take(chunk of this warp, its columns, their sums)
 #pragma unroll 1
-                    for (int k = part, at = 0; k < nch; k += kQgEpiHalves, at += kCols) {
-                        tc_wait_ld();
-                        float v[kCols];
+                        for (int k = part, i = 0; k < nch; k += kQgEpiHalves, ++i) {
+                            tc_wait_ld();
+                            float v[kCols];
 #pragma unroll
-                        for (int i = 0; i < kCols; ++i) {
-                            asm volatile("" : "+r"(r[i]));  // not used before the wait
-                            v[i] = __uint_as_float(r[i]);
-                        }
-                        if (k + kQgEpiHalves < nch) tc_ld8(acol + kCols * (k + kQgEpiHalves), r);
-                        if (begin && end) {
-                            put(k, v, at, nullptr);
-                        } else {
-#pragma unroll
-                            for (int i = 0; i < kCols; ++i) {
-                                const int sum = (begin ? 0 : sums[at + i]) + __float2int_rn(v[i]);
-                                sums[at + i] = sum;
-                                v[i] = (float)sum;
+                            for (int e = 0; e < kCols; ++e) {
+                                asm volatile("" : "+r"(r[e]));  // not used before the wait
+                                v[e] = __uint_as_float(r[e]);
                             }
-                            if (end) put(k, v, at, sums + at);
+                            if (k + kQgEpiHalves < nch) tc_ld8(acol + kCols * (k + kQgEpiHalves), r);
+                            take(i, un.n - kCols * k, v);
                         }
+                    };
+                    if (begin && end) {
+                        as_kind([&](auto kind) { chunks([&](int i, int left, const float v[kCols]) { put(kind, i, left, v, nullptr); }); });
+                    } else {
+                        chunks([&](int i, int left, float v[kCols]) {
+                            int* sum = sums + kCols * i;
+#pragma unroll
+                            for (int e = 0; e < kCols; ++e) {
+                                sum[e] = (begin ? 0 : sum[e]) + __float2int_rn(v[e]);
+                                v[e] = (float)sum[e];
+                            }
+                            if (end) as_kind([&](auto kind) { put(kind, i, left, v, sum); });
+                        });
                     }
                     __syncwarp();
                     tc_fence_before();
