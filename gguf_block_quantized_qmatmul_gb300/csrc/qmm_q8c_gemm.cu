@@ -22,8 +22,8 @@
 //               takes some 600 cycles, more than the MMAs of 128 K take there)
 //   warp 1      eight MMAs per 128 K
 //   warp 2      raw weights, a panel's 128 K (16 KB) a copy
-//   warps 3-10  epilogue: results from the accumulator, scaled
-//   warps 11-26 conversion: 32 codes a lane and tile of 64 K, ten instructions for eight
+//   8 or 16     epilogue: results from the accumulator, scaled
+//   16 or 8     conversion: 32 codes a lane and tile of 64 K, ten instructions for eight
 // Calls with few tiles are split over K; the slices' integer sums go to the
 // workspace and a last launch adds and scales them.
 //
@@ -40,9 +40,12 @@ constexpr int kRestart = 8;           // times 128 K per accumulation where sums
 constexpr int kMaxBX = 256;
 constexpr int kXMax = 8, kXMin = 4, kRawMax = 12;  // stages, at most: activations (and at least), raw weights
 constexpr int kBars = (2 * kXMax + 2 * kQgStageMax + 2 * kRawMax + 4) * 8;  // bytes of the mbarriers
-constexpr int kWarpCols = kMaxBX / kQgEpiHalves;                            // columns that an epilogue warp reads out
-constexpr int kTail = kBars + 32 + kQgEpiWarps * kWarpCols * 4;             // behind the rings: mbarriers, three words, the columns' factors
-static_assert(kRawMax % kQgGroups == 0 && kBars % 16 == 0, "rings of whole turns");
+// Tiles of 128 K are for many activation rows: their MMAs take 1024 cycles, eight warps convert as fast,
+// and 16 read the accumulator out while the MMAs wait for it (1024 x 14336 x 4096: 3.4 us of a unit's 21 with
+// eight).  Tiles of 256 K are bound by the conversion.
+__host__ __device__ constexpr int epi_warps(int kt) { return kt == 1 ? 16 : 8; }
+constexpr int kTail = kBars + 32 + 4 * kMaxBX * 4;             // behind the rings: mbarriers, three words, the columns' factors
+static_assert(kRawMax % 2 == 0 && kBars % 16 == 0, "rings of whole turns");
 
 struct GemmParams {
     QcCall c;
@@ -67,6 +70,9 @@ template <int CG, int KT>
 __global__ void __launch_bounds__(kQgThreads, 1) q8c_gemm_kernel(const __grid_constant__ CUtensorMap tx, const GemmParams p) {
     extern __shared__ __align__(1024) uint8_t smraw[];
     uint8_t* sm = smraw + ((1024 - (smem_u32(smraw) & 1023)) & 1023);
+    constexpr int kEpiWarps = epi_warps(KT), kEpiHalves = kEpiWarps / 4, kGroups = (24 - kEpiWarps) / 8, kConv0 = kQgEpi0 + kEpiWarps;
+    constexpr int kWarpCols = kMaxBX / kEpiHalves;  // columns that an epilogue warp reads out, at most
+    static_assert(kConv0 + 8 * kGroups == kQgThreads / 32, "every warp has a role");
     const QcCall& c = p.c;
     const QcWeights& w = c.w;
     const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31, M = c.a.M;
@@ -101,7 +107,7 @@ __global__ void __launch_bounds__(kQgThreads, 1) q8c_gemm_kernel(const __grid_co
         }
         for (int i = 0; i < 2; ++i) {
             mbar_init(smem_u32(&acc_full[i]), 1);
-            mbar_init(smem_u32(&acc_empty[i]), kQgEpiWarps * CG);
+            mbar_init(smem_u32(&acc_empty[i]), kEpiWarps * CG);
         }
         flags[0] = 0;
         *s_norm = 0u;
@@ -195,14 +201,14 @@ __global__ void __launch_bounds__(kQgThreads, 1) q8c_gemm_kernel(const __grid_co
             // let every copy land before the block can exit (rank 0's barriers have both blocks')
             if (rank == 0) qg_drain(g, wrapped, p.nx, x_full, flags, p.err);
         }
-    } else if (warp < kQgConv0) {
+    } else if (warp < kConv0) {
         // whether a sum may pass 2^24: the epilogue's and the MMAs' warps look for themselves
         grid_dep_wait();
         uint32_t top = 0;
-        for (int i = (warp == 1 ? 0 : warp - kQgEpi0 + 1) * 32 + lane; i < M; i += (kQgEpiWarps + 1) * 32) top = max(top, __ldg(p.xn + i));
+        for (int i = (warp == 1 ? 0 : warp - kQgEpi0 + 1) * 32 + lane; i < M; i += (kEpiWarps + 1) * 32) top = max(top, __ldg(p.xn + i));
         top = __reduce_max_sync(0xffffffffu, top);
         if (lane == 0) atomicMax(s_norm, top);
-        asm volatile("bar.sync 1, %0;" ::"n"((kQgEpiWarps + 1) * 32) : "memory");
+        asm volatile("bar.sync 1, %0;" ::"n"((kEpiWarps + 1) * 32) : "memory");
         const uint32_t wnorm = __ldg(reinterpret_cast<const uint32_t*>(w.data + w.norm_off));
         const bool restart = (unsigned long long)*reinterpret_cast<volatile uint32_t*>(s_norm) * wnorm >= 1ull << 48;
         const int chunk = restart ? kRestart / KT : p.ktiles;
@@ -278,7 +284,7 @@ __global__ void __launch_bounds__(kQgThreads, 1) q8c_gemm_kernel(const __grid_co
                 bias_next = c.bias && n < w.N ? __ldg(c.bias + n) : 0.0f;
 #pragma unroll
                 for (int i = 0; i < kWords; ++i) {
-                    const int m = kCols * (part + kQgEpiHalves * (4 * i + (lane >> 3))) + (lane & 7);
+                    const int m = kCols * (part + kEpiHalves * (4 * i + (lane >> 3))) + (lane & 7);
                     xs_next[i] = m < un.n ? __ldg(p.xs + un.p0 + m) : 0.0f;
                 }
             };
@@ -300,7 +306,7 @@ __global__ void __launch_bounds__(kQgThreads, 1) q8c_gemm_kernel(const __grid_co
                 const bool wide = w.N % 4 == 0 && p.ks == 1 && c.yt != X_F32;
                 const int sub = wide ? 2 * (lane & 3) : 0;  // the first of the columns that this lane writes
                 const long long first = (long long)(un.p0 + kCols * part + sub) * w.N + n - (wide ? lane & 3 : 0) + (p.ks > 1 ? (long long)un.split * M * w.N : 0);
-                const long long stride = (long long)kQgEpiHalves * kCols * w.N;
+                const long long stride = (long long)kEpiHalves * kCols * w.N;
                 const unsigned long long wn2 = f2pack(wn, wn);
                 // Chunk i of this warp (its columns are `left` of eight), as `kind`.  whole: sums that a float may not hold.
                 auto put = [&](auto kind, int i, int left, const float v[kCols], const int* whole) {
@@ -366,7 +372,7 @@ __global__ void __launch_bounds__(kQgThreads, 1) q8c_gemm_kernel(const __grid_co
                     if (part < nch) tc_ld8(acol + kCols * part, r);
                     auto chunks = [&](auto take) {  // take(chunk of this warp, its columns, their sums)
 #pragma unroll 1
-                        for (int k = part, i = 0; k < nch; k += kQgEpiHalves, ++i) {
+                        for (int k = part, i = 0; k < nch; k += kEpiHalves, ++i) {
                             tc_wait_ld();
                             float v[kCols];
 #pragma unroll
@@ -374,7 +380,7 @@ __global__ void __launch_bounds__(kQgThreads, 1) q8c_gemm_kernel(const __grid_co
                                 asm volatile("" : "+r"(r[e]));  // not used before the wait
                                 v[e] = __uint_as_float(r[e]);
                             }
-                            if (k + kQgEpiHalves < nch) tc_ld8(acol + kCols * (k + kQgEpiHalves), r);
+                            if (k + kEpiHalves < nch) tc_ld8(acol + kCols * (k + kEpiHalves), r);
                             take(i, un.n - kCols * k, v);
                         }
                     };
@@ -403,7 +409,7 @@ __global__ void __launch_bounds__(kQgThreads, 1) q8c_gemm_kernel(const __grid_co
         }
     } else {
         // ------------------------------ conversion ------------------------------
-        const int cw = warp - kQgConv0, q = warp & 3, hh = (cw >> 2) & 1, grp = cw >> 3;  // row block 2 q + hh of a tile
+        const int cw = warp - kConv0, q = warp & 3, hh = (cw >> 2) & 1, grp = cw >> 3;  // row block 2 q + hh of a tile
         QgRing g, r;      // the next tile's weight and raw stage
         int turn = 0;     // the group that it is for
         uint32_t r_ready = 0;  // this group's next raw stage was seen to have landed
@@ -438,7 +444,7 @@ __global__ void __launch_bounds__(kQgThreads, 1) q8c_gemm_kernel(const __grid_co
             // The groups take tiles in turn, whatever a unit's number of them: a group that waits for
             // the release of tile t - nstage has waited for t - groups - nstage, so that with nstage >=
             // groups the stage's barrier is at most one phase behind the wait's parity.
-            for (int j = un.j0; j < un.j1; ++j, turn = turn + 1 == kQgGroups ? 0 : turn + 1) {
+            for (int j = un.j0; j < un.j1; ++j, turn = turn + 1 == kGroups ? 0 : turn + 1) {
                 const QgRing at = g, ar = r;
                 g.next(p.nstage);
                 r.next(p.nraw);
@@ -453,7 +459,7 @@ __global__ void __launch_bounds__(kQgThreads, 1) q8c_gemm_kernel(const __grid_co
                 announce();
                 if (!(ok = qg_wait_warp(smem_u32(&empty[at.s]), at.ph ^ 1u, e_ready, flags, p.err))) break;
                 QgRing rn = r;  // this group's next raw stage
-                rn.skip(kQgGroups - 1, p.nraw);
+                rn.skip(kGroups - 1, p.nraw);
                 r_ready = mbar_test(smem_u32(&r_full[rn.s]), rn.ph);
                 tc_fence_after();
                 __syncwarp();
@@ -468,7 +474,7 @@ __global__ void __launch_bounds__(kQgThreads, 1) q8c_gemm_kernel(const __grid_co
                     tc_st_frag<16>(col + 32 * h, v);
                 }
                 stored = at.s;
-                if (p.nstage <= kQgGroups) announce();  // no stage to spare
+                if (p.nstage <= kGroups) announce();  // no stage to spare
             }
         }
         announce();
@@ -576,12 +582,12 @@ QcGemmPlan plan_q8c_gemm(const QcCall& c, int sms, int smem_max) {
     // The raw ring is a multiple of the converting groups, so that whoever waits for a stage's next filling
     // has waited for its last one (copies may land out of order).  Activations come from L2: few stages;
     // the weights' trip to memory wants as many bytes on their way as there is room for.
-    auto turns = [](int n, int most) { return (n < most ? n : most) / kQgGroups * kQgGroups; };
+    auto turns = [](int n, int most) { return (n < most ? n : most) / 2 * 2; };
     pl.nx = kXMin;
     while (pl.nx > 2 && pl.nx * stage + 4 * raw > room) --pl.nx;
     pl.nraw = turns((room - pl.nx * stage) / raw, kRawMax);
     pl.nx = (room - pl.nraw * raw) / stage < kXMax ? (room - pl.nraw * raw) / stage : kXMax;
-    if (pl.nstage < kQgGroups || pl.nx < 2 || pl.nraw < kQgGroups) return pl;
+    if (pl.nstage < 2 || pl.nx < 2 || pl.nraw < 2) return pl;
     pl.smem = (size_t)pl.nx * stage + (size_t)pl.nraw * raw + kTail + 1024;
     const long long units = (long long)pl.mtiles * pl.ntiles * pl.ks, workers = sms / pl.cg;
     if (units > (1ll << 30)) return pl;
