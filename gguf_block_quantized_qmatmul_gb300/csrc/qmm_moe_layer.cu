@@ -101,6 +101,7 @@ MoePlan plan_moe_layer(const MoeCall& c, int sms, int smem_max) {
     pl.down_items = most(down_item);
     long long act = pl.whole ? T * up_row : pl.up_items * up_item;
     if (act < pl.down_items * down_item) act = pl.down_items * down_item;
+    if ((long long)S * c.up.RB * sms > UINT32_MAX || (long long)S * c.down.RB * sms > UINT32_MAX) return pl;
     if ((long long)S * c.up.RB * (c.up.KS > c.down.KS ? c.up.KS : c.down.KS) > INT32_MAX || (long long)S * c.down.RB * c.down.KS > INT32_MAX) return pl;
     pl.off_zero = (int)act;
     pl.off_part = pl.off_zero + 16;

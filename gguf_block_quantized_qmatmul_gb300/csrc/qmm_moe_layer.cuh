@@ -508,13 +508,15 @@ __global__ void __launch_bounds__(kMoeThreads, 1) moe_layer_kernel(const __grid_
         };
         bool ok;
         if (phase == 0) {
-            const int work = s_items * p.up.RB, w0 = (int)((long long)i * work / G), w1 = (int)((long long)(i + 1) * work / G);
+            const unsigned work = (unsigned)s_items * p.up.RB;  // times the blocks: below 2^32, as planned
+            const int w0 = (int)(i * work / G), w1 = (int)((i + 1) * work / G);
             auto no = [] { return true; };
             if (p.up.ng == 1) ok = moe_share<BF, F32, 1, true, false>(p, p.up, sm, sh, w0, w1, no);
             else if (p.up.ng == 2) ok = moe_share<BF, F32, 2, true, false>(p, p.up, sm, sh, w0, w1, no);
             else ok = moe_share<BF, F32, 4, true, false>(p, p.up, sm, sh, w0, w1, no);
         } else if (phase == 1) {
-            const int work = (TOKEN ? T : s_items) * p.down.RB, w0 = (int)((long long)i * work / G), w1 = (int)((long long)(i + 1) * work / G);
+            const unsigned work = (unsigned)(TOKEN ? T : s_items) * p.down.RB;
+            const int w0 = (int)(i * work / G), w1 = (int)((i + 1) * work / G);
             auto first = [&] { return wait(1u); };
             if (p.down.ng == 1) ok = moe_share<BF, F32, 1, false, TOKEN>(p, p.down, sm, sh, w0, w1, first);
             else if (p.down.ng == 2) ok = moe_share<BF, F32, 2, false, TOKEN>(p, p.down, sm, sh, w0, w1, first);

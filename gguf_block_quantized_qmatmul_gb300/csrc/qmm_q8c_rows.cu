@@ -37,7 +37,7 @@ constexpr int kStatic = 1024;   // the kernel's static arrays, rounded up
 
 struct RowsParams {
     QcCall c;
-    int pitch, quant;
+    int pitch, quant, warps_log2;
     int kx;  // columns of codes that are there to be read: K, or the padded row of the preparation
     int off_zero, off_part, off_ring;
 };
@@ -138,7 +138,7 @@ __global__ void __launch_bounds__(kMaxWarps * 32, 1) q8c_rows_kernel(const RowsP
     __shared__ float scale[kMaxRows];
     const QcCall& c = p.c;
     const QcWeights& w = c.w;
-    const int tid = threadIdx.x, warp = __shfl_sync(0xffffffffu, tid >> 5, 0), lane = tid & 31, g = lane >> 2, t = lane & 3, nthr = blockDim.x, warps = nthr >> 5;
+    const int tid = threadIdx.x, warp = __shfl_sync(0xffffffffu, tid >> 5, 0), lane = tid & 31, g = lane >> 2, t = lane & 3, nthr = blockDim.x;
     const int KS = w.KS, M = c.a.M;
     uint8_t* ring = sm + p.off_ring + warp * (kDepth * kQcSeg);
     int4* parts = reinterpret_cast<int4*>(sm + p.off_part);  // [warp][2][32]: a row block's part that does not reach its end: 1; that does: 0
@@ -146,9 +146,11 @@ __global__ void __launch_bounds__(kMaxWarps * 32, 1) q8c_rows_kernel(const RowsP
     grid_dep_launch();
 
     // an equal share of the row blocks a block, and of its segments a warp
-    const int rb0 = (int)((long long)blockIdx.x * w.RB / gridDim.x), rb1 = (int)((long long)(blockIdx.x + 1) * w.RB / gridDim.x);
+    const int rb0 = (int)(blockIdx.x * (unsigned)w.RB / gridDim.x), rb1 = (int)((blockIdx.x + 1) * (unsigned)w.RB / gridDim.x);  // RB <= 2^19
     const float* sw = reinterpret_cast<const float*>(w.data + w.scale_off);
-    const int total = (rb1 - rb0) * KS, s0 = (int)((long long)warp * total / warps), s1 = (int)((long long)(warp + 1) * total / warps);
+    const int total = (rb1 - rb0) * KS;
+    auto begin = [&](int o) { return (int)((long long)o * total >> p.warps_log2); };  // of warp o's segments
+    const int s0 = begin(warp), s1 = begin(warp + 1);
     int left = s1 - s0, ls = 0, lrb = rb0 + s0 / KS, lrem = KS - s0 % KS, step = qc_step(w, lrb);
     const uint8_t* lp = w.data + qc_row_block(w, lrb) + (long long)(KS - lrem) * step + lane * 16;
     const uint32_t to = smem_u32(ring) + lane * 16;
@@ -244,9 +246,9 @@ __global__ void __launch_bounds__(kMaxWarps * 32, 1) q8c_rows_kernel(const RowsP
     __syncthreads();  // all parts are there
     if (cut >= 0) {
         int o = warp - 1;
-        while ((int)((long long)o * total / warps) > cut) --o;
+        while (begin(o) > cut) --o;
         for (; o <= warp; ++o) {
-            if ((int)((long long)o * total / warps) == (int)((long long)(o + 1) * total / warps)) continue;  // no segments
+            if (begin(o) == begin(o + 1)) continue;  // no segments
             const int4 u = parts[(o * 2 + (o == warp ? 0 : 1)) * 32 + lane];
             acc[0] += u.x;
             acc[1] += u.y;
@@ -302,6 +304,7 @@ cudaError_t launch_q8c_rows(const QcRowsPlan& pl, const QcCall& c, void* ws, int
     p.kx = pl.prep ? c.w.KS * 128 : c.w.K;
     p.quant = p.c.a.scales == nullptr;
     p.pitch = pl.pitch;
+    p.warps_log2 = pl.warps == 8 ? 3 : 4;
     p.off_zero = pl.off_zero;
     p.off_part = pl.off_part;
     p.off_ring = pl.off_ring;
