@@ -85,7 +85,7 @@ MoePlan plan_moe_layer(const MoeCall& c, int sms, int smem_max) {
     if (T < 1 || T > kMoeMaxTokens || E > kQgRowMaxE) return pl;
     // shared memory: activations, a zero, the parts of row blocks, the rings, the routing
     const int seg = qg_seg_bytes(c.up.ng > c.down.ng ? c.up.ng : c.down.ng), ring = kMoeWarps * kMoeDepth * seg;
-    const int route = round_up((6 * S + 2 * E) * 4, 16);
+    const int route = round_up((7 * S + 2 * E) * 4, 16);
     const int room = smem_max - kMoeStatic - 1024 - 16 - kMoePart - ring - route;
     const long long up_row = (long long)np * c.up.KS * 256, down_row = (long long)np * c.down.KS * 256;  // a token's, a slot's staged bytes
     // a token's second products end to end while few tokens share an expert: no partial sums to add later

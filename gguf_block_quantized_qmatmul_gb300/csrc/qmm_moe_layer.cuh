@@ -95,6 +95,7 @@ struct MoeShared {
     const int* ids;         // [T][top_k]
     const float* weights;
     const int* order;       // slots by expert
+    const int* token;       // and their tokens
     const MoeItem* items;
     int T, k;
 };
@@ -243,9 +244,8 @@ __device__ __forceinline__ bool moe_share(const MoeParams& p, const QgWeights& w
                 } else {
                     const MoeItem m = sh.items[it];
                     moe_stage<kFlight, F32>(area, UP ? p.x : p.h, KS * 4, m.n, [&](int r, int h, int& left) {
-                        const int slot = sh.order[m.first + r];
                         left = w.K - 32 * h;
-                        return (UP ? slot / sh.k * p.ldx : (long long)slot * w.K) + 32 * h;
+                        return (UP ? sh.token[m.first + r] * p.ldx : (long long)sh.order[m.first + r] * w.K) + 32 * h;
                     }, tid);
                 }
             }
@@ -263,7 +263,7 @@ __device__ __forceinline__ bool moe_share(const MoeParams& p, const QgWeights& w
                 int base, ncol;
                 if (whole) {
                     ncol = sh.T * np;
-                    base = (sh.order[sh.items[r.item].first + c] / sh.k * np + pc) * 64;
+                    base = (sh.token[sh.items[r.item].first + c] * np + pc) * 64;
                 } else {
                     ncol = n * np;
                     base = (r.item - i0) * item_bytes + (c * np + pc) * 64 + (TOKEN ? r.j * KS * 4 * ncol * 64 : 0);
@@ -420,7 +420,8 @@ __global__ void __launch_bounds__(kMoeThreads, 1) moe_layer_kernel(const __grid_
     float* weights = reinterpret_cast<float*>(ids + S);              // [S]
     int* order = reinterpret_cast<int*>(weights + S);                // [S]
     MoeItem* items = reinterpret_cast<MoeItem*>(order + S);          // [S]
-    int* offsets = reinterpret_cast<int*>(items + S);                // [E]
+    int* token = reinterpret_cast<int*>(items + S);                  // [S]
+    int* offsets = token + S;                                        // [E]
     uint32_t* mask = reinterpret_cast<uint32_t*>(offsets + E);       // [E] the tokens that chose an expert
     uint32_t* picks = reinterpret_cast<uint32_t*>(sm + p.off_ring);  // [warps][E], where the rings will be
     for (int e = tid; e < E; e += kMoeThreads) mask[e] = 0u;
@@ -479,13 +480,15 @@ __global__ void __launch_bounds__(kMoeThreads, 1) moe_layer_kernel(const __grid_
     __syncthreads();
     for (int s = tid; s < S; s += kMoeThreads) {
         const int t = s / k, e = ids[s];
-        order[offsets[e] + __popc(mask[e] & ((1u << t) - 1u))] = s;
+        const int at = offsets[e] + __popc(mask[e] & ((1u << t) - 1u));
+        order[at] = s;
+        token[at] = t;
         if (blockIdx.x == 0 && p.route.c.ids) {
             p.route.c.ids[s] = e;
             p.route.c.weights[s] = weights[s];
         }
     }
-    const MoeShared sh = {ids, weights, order, items, T, k};
+    const MoeShared sh = {ids, weights, order, token, items, T, k};
 
     // ------------------------------ shares ------------------------------
     // The next ticket is drawn when a share begins and known to all when it ends, at one barrier.
