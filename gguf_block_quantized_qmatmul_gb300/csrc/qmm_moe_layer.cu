@@ -85,16 +85,20 @@ MoePlan plan_moe_layer(const MoeCall& c, int sms, int smem_max) {
     if (T < 1 || T > kMoeMaxTokens || E > kQgRowMaxE) return pl;
     // shared memory: activations, a zero, the parts of row blocks, the rings, the routing
     const int seg = qg_seg_bytes(c.up.ng > c.down.ng ? c.up.ng : c.down.ng), ring = kMoeWarps * kMoeDepth * seg;
-    const int route = round_up((7 * S + 2 * E) * 4, 16);
+    const int route = round_up((6 * S + 2 * E) * 4, 16);
     const int room = smem_max - kMoeStatic - 1024 - 16 - kMoePart - ring - route;
-    const long long up_row = (long long)np * c.up.KS * 256, down_row = (long long)np * c.down.KS * 256;  // a token's, a slot's staged bytes
+    const long long up_row = (long long)np * c.up.KS * 256, down_row = (long long)(np == 3 ? 3 : 2) * c.down.KS * 256;  // a token's, a slot's staged bytes
     // a token's second products end to end while few tokens share an expert: no partial sums to add later
     pl.token = T <= 4 && k * down_row <= room;
     pl.whole = T * up_row <= room;
-    pl.cols = c.xt == X_F32 ? 2 : 8;
-    if (pl.cols > T) pl.cols = T;
-    while (pl.cols > 1 && ((!pl.whole && pl.cols * up_row > room) || (!pl.token && pl.cols * down_row > room))) --pl.cols;
-    const long long up_item = pl.cols * up_row, down_item = pl.token ? k * down_row : pl.cols * down_row;
+    auto cols = [&](int most, bool staged, long long row) {
+        int n = most < T ? most : T;
+        while (n > 1 && staged && n * row > room) --n;
+        return n;
+    };
+    pl.up_cols = cols(np == 3 ? 2 : 8, !pl.whole, up_row);
+    pl.down_cols = cols(np == 3 ? 2 : 4, !pl.token, down_row);
+    const long long up_item = pl.up_cols * up_row, down_item = pl.token ? k * down_row : pl.down_cols * down_row;
     if (room < 0 || (!pl.whole && up_item > room) || down_item > room) return pl;
     auto most = [&](long long item) { return (int)(room / item < kMoeItems ? room / item : kMoeItems); };
     pl.up_items = pl.whole ? kMoeItems : most(up_item);
@@ -112,7 +116,7 @@ MoePlan plan_moe_layer(const MoeCall& c, int sms, int smem_max) {
     auto r256 = [](size_t v) { return (v + 255) / 256 * 256; };
     pl.ws_logits = 256;
     pl.ws_h = pl.ws_logits + r256((size_t)T * ((E + 3) / 4 * 4) * 4);
-    pl.ws_part = pl.ws_h + r256((size_t)S * c.down.K * x_size(c.xt));
+    pl.ws_part = pl.ws_h + r256((size_t)S * c.down.K * 4);
     pl.workspace = pl.ws_part + (pl.token ? 0 : (size_t)S * c.down.N * 4);
     pl.ok = true;
     return pl;
@@ -145,7 +149,8 @@ cudaError_t launch_moe_layer(const MoePlan& pl, const MoeCall& c, void* ws, unsi
     p.y = c.y;
     p.counters = counters;
     p.err = err;
-    p.cols = pl.cols;
+    p.up_cols = pl.up_cols;
+    p.down_cols = pl.down_cols;
     p.whole = pl.whole;
     p.up_items = pl.up_items;
     p.down_items = pl.down_items;

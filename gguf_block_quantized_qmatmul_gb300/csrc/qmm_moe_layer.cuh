@@ -3,10 +3,12 @@
 //
 // Mathematics: that of the four calls that it stands for.  l = x R^T in f32;
 // the routing of qmm_moe_route.cu; h = silu(x Wg^T) (x Wu^T) of each token's
-// experts, rounded to the activations' type; y = sum_j p_j (h_j Wd^T).  The
-// products are the row kernel's (qmm_q4g_rows.cuh): codes less their zero point
-// are exact operands of f16 or bf16 warp MMAs, group sums are scaled in f32, an
-// f32 activation is three bf16 pieces.
+// experts; y = sum_j p_j (h_j Wd^T).  The products are the row kernel's
+// (qmm_q4g_rows.cuh): codes less their zero point are exact operands of f16 or
+// bf16 warp MMAs, group sums are scaled in f32, an f32 activation is three bf16
+// pieces.  h is two pieces of a 16-bit type between the two (f32: as it is): rounded to one, its error was as large as the result's
+// own rounding (2.9e-4 for 2.1e-4 in f16).  The pieces are columns that an
+// MMA has anyway.
 //
 // A decode step's layer reads a few MB of weights, 100 KB an SM, so what stands
 // between the products is what costs.  The first launch forms the logits (a
@@ -21,7 +23,7 @@
 // before their block waits.
 //
 // A share is row blocks of items, end to end.  An item is an expert with up to 8
-// (f32: 2) of its tokens, the MMA's columns; for up to 4 tokens the second
+// (h: 4, f32: 2) of its tokens, whose pieces are the MMA's columns; for up to 4 tokens the second
 // products' items are tokens, whose experts' segments are one long row.  A share's
 // segments of 16 x 128 weights are dealt to the block's warps in equal
 // contiguous runs, wherever row blocks end, so that no warp has more to do than
@@ -33,6 +35,8 @@
 //
 // Waits are bounded: one that gives up raises the error word and its block ends.
 #pragma once
+
+#include <type_traits>
 
 #include "qmm_moe_route.cuh"
 #include "qmm_q4g_rows.cuh"
@@ -51,13 +55,13 @@ struct MoeParams {
     const void* x;
     long long ldx;
     int xt;
-    void* h;             // [T top_k][F]
+    void* h;             // [T top_k][F] f32, or [T top_k][2][F] pieces of the activations' type
     float* part;         // [T top_k][N]: the experts' second products, unless items are tokens
     void* y;
     unsigned* counters;  // [0] tickets, [1] shares of the first products done, [2] of the second
     unsigned* err;
     int epl16;           // experts per lane in the routing: 16, or 4
-    int cols, whole, up_items, down_items;
+    int up_cols, down_cols, whole, up_items, down_items;
     int off_zero, off_part, off_ring, off_route;
     int stall;
 };
@@ -86,9 +90,12 @@ static __device__ __noinline__ bool moe_wait(const unsigned* p, unsigned n, unsi
     return true;
 }
 
-// An item of an expert: its tokens' slots are order[first .. first + n).
+// An item of an expert: its tokens' slots are order[first .. first + n).  In one word: 512 experts, 1024 slots.
 struct MoeItem {
-    int expert, first, n;
+    uint32_t v;
+    __device__ __forceinline__ int expert() const { return (int)(v & 511u); }
+    __device__ __forceinline__ int first() const { return (int)(v >> 9 & 1023u); }
+    __device__ __forceinline__ int n() const { return (int)(v >> 19); }
 };
 // The routing, in shared memory.
 struct MoeShared {
@@ -127,48 +134,49 @@ struct MoeRun {
         }
         return true;
     }
-    __device__ __forceinline__ int expert(const MoeShared& sh) const { return TOKEN ? sh.ids[item * sh.k + j] : sh.items[item].expert; }
+    __device__ __forceinline__ int expert(const MoeShared& sh) const { return TOKEN ? sh.ids[item * sh.k + j] : sh.items[item].expert(); }
 };
 
 // Stages nh x rows quads of 32 values: block h of row r is `left` values (none: <= 0) from element
-// src(r, h, left) of x on, and goes to 64 bytes (a column; f32: three) at h * rows + r.  B 16-byte loads
-// (f32: pairs of them) a thread are in flight.
-template <int B, bool F32, class Src>
+// src(r, h, left) of x on, and goes to 64 bytes at h * rows + r.  S32: x is f32, three bf16 pieces of 64 bytes
+// by truncation (exact, no overflow).  B loads a thread are in flight.
+template <int B, bool S32, class Src>
 __device__ __forceinline__ void moe_stage(uint8_t* sm, const void* x, int nh, int rows, Src src, int tid) {
-    constexpr int np = F32 ? 3 : 1;
+    constexpr int NP = S32 ? 3 : 1;
     const int n = nh * rows * 4;
     for (int i0 = 0; i0 < n; i0 += B * kMoeThreads) {
-        uint4 u[B][F32 ? 2 : 1];
+        uint4 u[B][S32 ? 2 : 1];
 #pragma unroll
         for (int b = 0; b < B; ++b) {
             const int i = i0 + b * kMoeThreads + tid, quad = i >> 2, h = quad / rows;
 #pragma unroll
-            for (int q = 0; q < (F32 ? 2 : 1); ++q) u[b][q] = make_uint4(0u, 0u, 0u, 0u);
+            for (int q = 0; q < (S32 ? 2 : 1); ++q) u[b][q] = make_uint4(0u, 0u, 0u, 0u);
             if (i < n) {
                 int left;
                 const long long at = src(quad - h * rows, h, left) + 8 * (i & 3);
                 if (8 * (i & 3) < left)
 #pragma unroll
-                    for (int q = 0; q < (F32 ? 2 : 1); ++q) u[b][q] = reinterpret_cast<const uint4*>(static_cast<const uint8_t*>(x) + at * (F32 ? 4 : 2))[q];
+                    for (int q = 0; q < (S32 ? 2 : 1); ++q) u[b][q] = reinterpret_cast<const uint4*>(static_cast<const uint8_t*>(x) + at * (S32 ? 4 : 2))[q];
             }
         }
 #pragma unroll
         for (int b = 0; b < B; ++b) {
             const int i = i0 + b * kMoeThreads + tid, j = i & 3;
             if (i - (tid & 31) >= n) break;  // the whole warp is done
-            uint8_t* to = sm + (long long)(i >> 2) * (np * 64) + j * 16;
-            if constexpr (F32) {
+            uint8_t* to = sm + (long long)(i >> 2) * (NP * 64) + j * 16;
+            if constexpr (S32) {
                 float f[8] = {__uint_as_float(u[b][0].x), __uint_as_float(u[b][0].y), __uint_as_float(u[b][0].z), __uint_as_float(u[b][0].w),
                               __uint_as_float(u[b][1].x), __uint_as_float(u[b][1].y), __uint_as_float(u[b][1].z), __uint_as_float(u[b][1].w)};
 #pragma unroll
-                for (int pc = 0; pc < 3; ++pc) {
+                for (int pc = 0; pc < NP; ++pc) {
                     uint32_t w[4];
 #pragma unroll
-                    for (int e = 0; e < 8; ++e) {
-                        const uint32_t v = __float_as_uint(f[e]) & 0xffff0000u;
-                        w[e >> 1] = e & 1 ? w[e >> 1] | v : v >> 16;
+                    for (int e = 0; e < 8; e += 2) {
                         // the rest is exact; an infinity or NaN has none
-                        f[e] = (v & 0x7f800000u) == 0x7f800000u ? 0.0f : f[e] - __uint_as_float(v);
+                        const uint32_t lo = __float_as_uint(f[e]) & 0xffff0000u, hi = __float_as_uint(f[e + 1]) & 0xffff0000u;
+                        w[e >> 1] = hi | lo >> 16;
+                        f[e] = (lo & 0x7f800000u) == 0x7f800000u ? 0.0f : f[e] - __uint_as_float(lo);
+                        f[e + 1] = (hi & 0x7f800000u) == 0x7f800000u ? 0.0f : f[e + 1] - __uint_as_float(hi);
                     }
                     const uint4 q = qg_quad_transpose(w[0], w[1], w[2], w[3], j);
                     if (i < n) *reinterpret_cast<uint4*>(to + pc * 64) = q;
@@ -186,7 +194,7 @@ __device__ __forceinline__ void moe_stage(uint8_t* sm, const void* x, int nh, in
 template <bool BF, bool F32, int NG, bool UP, bool TOKEN, class Wait>
 __device__ __forceinline__ bool moe_share(const MoeParams& p, const QgWeights& w, uint8_t* sm, const MoeShared& sh, int w0, int w1, Wait wait) {
     const int tid = threadIdx.x, warp = __shfl_sync(0xffffffffu, tid >> 5, 0), lane = tid & 31, g = lane >> 2, t = lane & 3;
-    constexpr int seg_bytes = qg_seg_bytes(NG), segk = 128 / NG, np = F32 ? 3 : 1;
+    constexpr int seg_bytes = qg_seg_bytes(NG), segk = 128 / NG, np = F32 ? 3 : UP ? 1 : 2, kFlight = F32 ? 2 : 4;
     const int KS = w.KS, RB = w.RB, kk = TOKEN ? sh.k : 1;  // runs per row block
     const long long rb_bytes = (long long)KS * seg_bytes;
     uint8_t* ring = sm + p.off_ring + warp * (kMoeDepth * seg_bytes);
@@ -194,7 +202,7 @@ __device__ __forceinline__ bool moe_share(const MoeParams& p, const QgWeights& w
     const uint32_t magic = opaque(kQgMagic<BF>);
     const bool whole = UP && p.whole;
     // a staged item: [32 K][columns] of 64 bytes
-    const int item_bytes = (TOKEN ? sh.k : p.cols) * np * KS * 256;
+    const int item_bytes = (TOKEN ? sh.k : UP ? p.up_cols : p.down_cols) * np * KS * 256;
     const int batch = UP ? (whole ? kMoeItems * 16 : p.up_items) : p.down_items;
     bool ok = true;
     for (int b0 = w0; b0 < w1;) {
@@ -233,19 +241,20 @@ __device__ __forceinline__ bool moe_share(const MoeParams& p, const QgWeights& w
             const int i1 = (b1 - 1) / RB;
             for (int it = i0; it <= i1; ++it) {
                 uint8_t* area = sm + (it - i0) * item_bytes;
-                constexpr int kFlight = F32 ? 2 : 4;
+                constexpr int pieces = !UP && !F32 ? 2 : 1;  // rows of an activation row
                 if (TOKEN) {  // its choices' rows end to end
                     const int per_row = KS * 4;
-                    moe_stage<kFlight, F32>(area, p.h, sh.k * per_row, 1, [&](int, int h, int& left) {
+                    moe_stage<kFlight, F32>(area, p.h, sh.k * per_row, pieces, [&](int pc, int h, int& left) {
                         const int j = h / per_row, k32 = 32 * (h - j * per_row);
                         left = w.K - k32;
-                        return ((long long)it * sh.k + j) * w.K + k32;
+                        return (((long long)it * sh.k + j) * pieces + pc) * w.K + k32;
                     }, tid);
                 } else {
                     const MoeItem m = sh.items[it];
-                    moe_stage<kFlight, F32>(area, UP ? p.x : p.h, KS * 4, m.n, [&](int r, int h, int& left) {
+                    moe_stage<kFlight, F32>(area, UP ? p.x : p.h, KS * 4, m.n() * pieces, [&](int r, int h, int& left) {
                         left = w.K - 32 * h;
-                        return (UP ? sh.token[m.first + r] * p.ldx : (long long)sh.order[m.first + r] * w.K) + 32 * h;
+                        if (UP) return sh.token[m.first() + r] * p.ldx + 32 * h;
+                        return ((long long)sh.order[m.first() + r / pieces] * pieces + r % pieces) * w.K + 32 * h;
                     }, tid);
                 }
             }
@@ -254,16 +263,16 @@ __device__ __forceinline__ bool moe_share(const MoeParams& p, const QgWeights& w
 
         float acc[4] = {0.0f, 0.0f, 0.0f, 0.0f};
         // This lane's activations: at xo, xq bytes from 32 K to the next (0: it has no column).  Column g is
-        // token g of the item, or piece g % 4 of token g / 4.
+        // token g of the item, or piece g % 2 (3 pieces: g % 4) of token g / 2 (g / 4).
         int xo = 0, xq = 0;
         float wt = 1.0f;
         auto columns = [&](const MoeRun<TOKEN>& r, int seg) {
-            const int n = TOKEN ? 1 : sh.items[r.item].n, c = F32 ? g >> 2 : g, pc = F32 ? g & 3 : 0;
+            const int n = TOKEN ? 1 : sh.items[r.item].n(), c = np == 3 ? g >> 2 : np == 2 ? g >> 1 : g, pc = np == 3 ? g & 3 : np == 2 ? g & 1 : 0;
             if (c < n && pc < np) {
                 int base, ncol;
                 if (whole) {
                     ncol = sh.T * np;
-                    base = (sh.token[sh.items[r.item].first + c] * np + pc) * 64;
+                    base = (sh.token[sh.items[r.item].first() + c] * np + pc) * 64;
                 } else {
                     ncol = n * np;
                     base = (r.item - i0) * item_bytes + (c * np + pc) * 64 + (TOKEN ? r.j * KS * 4 * ncol * 64 : 0);
@@ -278,31 +287,43 @@ __device__ __forceinline__ bool moe_share(const MoeParams& p, const QgWeights& w
         };
         // a row block's 16 x 8 sums to their place
         auto put = [&](float v[4], int item, int rb) {
-            if (F32) {  // pieces 0, 1 are one lane's, piece 2 its neighbour's
+            if (np > 1) {  // pieces 0, 1 are one lane's, piece 2 its neighbour's
 #pragma unroll
                 for (int i = 0; i < 4; i += 2) {
                     v[i] += v[i + 1];
-                    v[i] += __shfl_xor_sync(0xffffffffu, v[i], 1);
+                    if (np == 3) v[i] += __shfl_xor_sync(0xffffffffu, v[i], 1);
                 }
             }
             constexpr float unit = BF ? 1.0f / kQgCodeUnit : 1.0f;
-            const int n = TOKEN ? 1 : sh.items[item].n;
+            const MoeItem it = TOKEN ? MoeItem{0u} : sh.items[item];
+            const int n = TOKEN ? 1 : it.n();
 #pragma unroll
-            for (int i = 0; i < (F32 ? 1 : 2); ++i) {
-                const int c = F32 ? t >> 1 : 2 * t + i;
-                if (c >= n || (F32 && (t & 1))) continue;
+            for (int i = 0; i < (np > 1 ? 1 : 2); ++i) {
+                const int c = np == 3 ? t >> 1 : np == 2 ? t : 2 * t + i;
+                if (c >= n || (np == 3 && (t & 1))) continue;
                 const float lo = v[i] * unit, hi = v[i + 2] * unit;
                 if (UP) {
                     const int f = rb * 8 + g, F = w.N / 2;
-                    const long long slot = sh.order[sh.items[item].first + c];
-                    if (f < F) x_store(p.h, p.xt, slot * F + f, swiglu(lo, hi));
+                    if (f >= F) continue;
+                    const long long slot = sh.order[it.first() + c];
+                    const float v = swiglu(lo, hi);
+                    if constexpr (F32) {
+                        static_cast<float*>(p.h)[slot * F + f] = v;
+                    } else {
+                        using H = typename std::conditional<BF, __nv_bfloat16, __half>::type;
+                        H* to = static_cast<H*>(p.h) + slot * 2 * F + f;
+                        const H one = to_type<H>(v);
+                        const float rest = v - (float)one;
+                        to[0] = one;
+                        to[F] = to_type<H>(fabsf((float)one) < INFINITY ? rest : 0.0f);  // an infinity or NaN has none
+                    }
                 } else {
                     const int row = rb * 16 + g;
                     if (TOKEN) {
                         if (row < w.N) x_store(p.y, p.xt, (long long)item * w.N + row, lo);
                         if (row + 8 < w.N) x_store(p.y, p.xt, (long long)item * w.N + row + 8, hi);
                     } else {
-                        float* out = p.part + (long long)sh.order[sh.items[item].first + c] * w.N;
+                        float* out = p.part + (long long)sh.order[it.first() + c] * w.N;
                         if (row < w.N) out[row] = lo;
                         if (row + 8 < w.N) out[row + 8] = hi;
                     }
@@ -412,16 +433,17 @@ __device__ __forceinline__ bool moe_share(const MoeParams& p, const QgWeights& w
 template <bool BF, bool F32, bool TOKEN>
 __global__ void __launch_bounds__(kMoeThreads, 1) moe_layer_kernel(const __grid_constant__ MoeParams p) {
     extern __shared__ __align__(16) uint8_t sm[];
-    __shared__ int s_ok, s_items;
+    __shared__ int s_ok, s_items[2];  // [1]: of the second products
     __shared__ unsigned s_ticket[2];
     const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
     const int T = p.route.c.T, E = p.route.c.E, k = p.route.c.top_k, S = T * k;
     int* ids = reinterpret_cast<int*>(sm + p.off_route);             // [S]
     float* weights = reinterpret_cast<float*>(ids + S);              // [S]
     int* order = reinterpret_cast<int*>(weights + S);                // [S]
-    MoeItem* items = reinterpret_cast<MoeItem*>(order + S);          // [S]
-    int* token = reinterpret_cast<int*>(items + S);                  // [S]
-    int* offsets = token + S;                                        // [E]
+    int* token = order + S;                                          // [S]
+    MoeItem* items = reinterpret_cast<MoeItem*>(token + S);          // [S] of the first products
+    MoeItem* items2 = items + S;                                     // [S] of the second
+    int* offsets = reinterpret_cast<int*>(items2 + S);               // [E]
     uint32_t* mask = reinterpret_cast<uint32_t*>(offsets + E);       // [E] the tokens that chose an expert
     uint32_t* picks = reinterpret_cast<uint32_t*>(sm + p.off_ring);  // [warps][E], where the rings will be
     for (int e = tid; e < E; e += kMoeThreads) mask[e] = 0u;
@@ -450,31 +472,40 @@ __global__ void __launch_bounds__(kMoeThreads, 1) moe_layer_kernel(const __grid_
     __syncthreads();
     if (warp == 0) {
         // Slots sorted by expert, by token within one: a count is a mask's population, a rank that of its
-        // lower bits.  First positions and items before each expert in one sum's halves (at most 1024).
+        // lower bits.  Slots and both products' items before each expert are one sum's thirds.
         const int per = (E + 31) / 32;
-        uint32_t mine = 0;
-        for (int i = 0; i < per; ++i) {
-            const int e = lane * per + i, n = e < E ? __popc(mask[e]) : 0;
-            mine += (uint32_t)n | (uint32_t)((n + p.cols - 1) / p.cols) << 16;
-        }
-        uint32_t pre = mine;
+        // (TOKEN: the second products' items are the tokens.)
+        using Sum = typename std::conditional<TOKEN, uint32_t, unsigned long long>::type;
+        auto count = [&](int n) {
+            Sum v = (Sum)n | (Sum)((unsigned)(n + p.up_cols - 1) / (unsigned)p.up_cols) << 16;
+            if constexpr (!TOKEN) v |= (Sum)((unsigned)(n + p.down_cols - 1) / (unsigned)p.down_cols) << 32;
+            return v;
+        };
+        Sum mine = 0;
+        for (int i = 0; i < per; ++i)
+            if (lane * per + i < E) mine += count(__popc(mask[lane * per + i]));
+        Sum pre = mine;
 #pragma unroll
         for (int o = 1; o < 32; o <<= 1) {
-            const uint32_t u = __shfl_up_sync(0xffffffffu, pre, o);
+            const Sum u = __shfl_up_sync(0xffffffffu, pre, o);
             if (lane >= o) pre += u;
         }
-        if (lane == 31) s_items = (int)(pre >> 16);
+        if (lane == 31) {
+            s_items[0] = (int)(pre >> 16 & 0xffffu);
+            if constexpr (!TOKEN) s_items[1] = (int)(pre >> 32);
+        }
         pre -= mine;
         for (int i = 0; i < per; ++i) {
             const int e = lane * per + i;
             if (e >= E) break;
-            const int n = __popc(mask[e]);
-            offsets[e] = (int)(pre & 0xffffu);
-            for (int c = 0; c < n; c += p.cols) {
-                items[pre >> 16] = MoeItem{e, (int)(pre & 0xffffu) + c, min(p.cols, n - c)};
-                pre += 1u << 16;
-            }
-            pre += (uint32_t)n;
+            const int n = __popc(mask[e]), first = (int)(pre & 0xffffu);
+            offsets[e] = first;
+            auto list = [&](MoeItem* to, int cols) {
+                for (int c = 0; c < n; c += cols) *to++ = MoeItem{(uint32_t)e | (uint32_t)(first + c) << 9 | (uint32_t)min(cols, n - c) << 19};
+            };
+            list(items + (pre >> 16 & 0xffffu), p.up_cols);
+            if constexpr (!TOKEN) list(items2 + (pre >> 32), p.down_cols);
+            pre += count(n);
         }
     }
     __syncthreads();
@@ -488,7 +519,7 @@ __global__ void __launch_bounds__(kMoeThreads, 1) moe_layer_kernel(const __grid_
             p.route.c.weights[s] = weights[s];
         }
     }
-    const MoeShared sh = {ids, weights, order, token, items, T, k};
+    const MoeShared sh = {ids, weights, order, token, items, T, k}, sh2 = {ids, weights, order, token, items2, T, k};
 
     // ------------------------------ shares ------------------------------
     // The next ticket is drawn when a share begins and known to all when it ends, at one barrier.
@@ -511,19 +542,19 @@ __global__ void __launch_bounds__(kMoeThreads, 1) moe_layer_kernel(const __grid_
         };
         bool ok;
         if (phase == 0) {
-            const unsigned work = (unsigned)s_items * p.up.RB;  // times the blocks: below 2^32, as planned
+            const unsigned work = (unsigned)s_items[0] * p.up.RB;  // times the blocks: below 2^32, as planned
             const int w0 = (int)(i * work / G), w1 = (int)((i + 1) * work / G);
             auto no = [] { return true; };
             if (p.up.ng == 1) ok = moe_share<BF, F32, 1, true, false>(p, p.up, sm, sh, w0, w1, no);
             else if (p.up.ng == 2) ok = moe_share<BF, F32, 2, true, false>(p, p.up, sm, sh, w0, w1, no);
             else ok = moe_share<BF, F32, 4, true, false>(p, p.up, sm, sh, w0, w1, no);
         } else if (phase == 1) {
-            const unsigned work = (unsigned)(TOKEN ? T : s_items) * p.down.RB;
+            const unsigned work = (unsigned)(TOKEN ? T : s_items[1]) * p.down.RB;
             const int w0 = (int)(i * work / G), w1 = (int)((i + 1) * work / G);
             auto first = [&] { return wait(1u); };
-            if (p.down.ng == 1) ok = moe_share<BF, F32, 1, false, TOKEN>(p, p.down, sm, sh, w0, w1, first);
-            else if (p.down.ng == 2) ok = moe_share<BF, F32, 2, false, TOKEN>(p, p.down, sm, sh, w0, w1, first);
-            else ok = moe_share<BF, F32, 4, false, TOKEN>(p, p.down, sm, sh, w0, w1, first);
+            if (p.down.ng == 1) ok = moe_share<BF, F32, 1, false, TOKEN>(p, p.down, sm, sh2, w0, w1, first);
+            else if (p.down.ng == 2) ok = moe_share<BF, F32, 2, false, TOKEN>(p, p.down, sm, sh2, w0, w1, first);
+            else ok = moe_share<BF, F32, 4, false, TOKEN>(p, p.down, sm, sh2, w0, w1, first);
         } else {
             // a token's second products, in the order of its choices
             if ((ok = wait(2u))) {

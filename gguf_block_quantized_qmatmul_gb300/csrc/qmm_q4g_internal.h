@@ -104,7 +104,7 @@ struct MoeCall {
 struct MoePlan {
     bool ok = false;
     int token = 0;   // the second products' items are tokens, not experts
-    int cols = 0;    // tokens per item of an expert, at most
+    int up_cols = 0, down_cols = 0;  // tokens per item of an expert, at most
     int whole = 0;   // all tokens' activations are staged at once
     int up_items = 0, down_items = 0;  // items whose activations fit beside each other
     int blocks = 0;

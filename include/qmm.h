@@ -386,14 +386,16 @@ qmm_status qmm_moe_down(const qmm_q4g* w, qmm_float xtype, const void* h, int64_
 /* A whole layer for up to QMM_MOE_LAYER_MAX_TOKENS tokens in two launches:
      logits = x . router^T in f32 (router [experts][K] of router_type,
      contiguous, 16-byte aligned), routed as qmm_moe_route does with cfg and
-     bias; y = what qmm_moe_down makes of qmm_moe_gate_up's h (which is rounded
-     to x's type between the two).
+     bias; y = sum over j of weights[t][j] (h[t][j] . Wd_e^T), h[t][j] =
+     silu(x_t . Wg_e^T) * (x_t . Wu_e^T), as qmm_moe_gate_up and qmm_moe_down form
+     them, but h keeps 16 bits or more between the two (qmm_moe_gate_up rounds it
+     to x's type).
    gate_up: paired, N = 2 F; down: as many experts, K = F.  ids and weights
    [T][top_k] (both or neither) take the routing.  y [T][down.N] contiguous.
    workspace: qmm_moe_layer_workspace(...) bytes, uninitialised; calls that may
    overlap need one each.  SHAPE also where a row of K or F values does not
-   fit beside the rest in shared memory (from some 9000 values in f32, 28000 in
-   16 bits).
+   fit beside the rest in shared memory (K from some 9000 values in f32 and
+   28000 in 16 bits, F from 9000 and 14000).
    Errors as qmm_q4g_matmul. */
 #define QMM_MOE_LAYER_MAX_TOKENS 32
 size_t qmm_moe_layer_workspace(const qmm_q4g* gate_up, const qmm_q4g* down, qmm_float xtype, int64_t T, int64_t top_k);
