@@ -85,19 +85,24 @@ MoePlan plan_moe_layer(const MoeCall& c, int sms, int smem_max) {
     if (T < 1 || T > kMoeMaxTokens || E > kQgRowMaxE) return pl;
     // shared memory: activations, a zero, the parts of row blocks, the rings, the routing
     const int seg = qg_seg_bytes(c.up.ng > c.down.ng ? c.up.ng : c.down.ng), ring = kMoeWarps * kMoeDepth * seg;
-    const int route = round_up((6 * S + 2 * E) * 4, 16);
+    const int route = round_up((6 * S + 3 * E) * 4, 16);
     const int room = smem_max - kMoeStatic - 1024 - 16 - kMoePart - ring - route;
     const long long up_row = (long long)np * c.up.KS * 256, down_row = (long long)(np == 3 ? 3 : 2) * c.down.KS * 256;  // a token's, a slot's staged bytes
     // a token's second products end to end while few tokens share an expert: no partial sums to add later
     pl.token = T <= 4 && k * down_row <= room;
     pl.whole = T * up_row <= room;
+    // tokens per item: the MMA's columns, or what fits shared memory, a power of two
     auto cols = [&](int most, bool staged, long long row) {
-        int n = most < T ? most : T;
-        while (n > 1 && staged && n * row > room) --n;
+        int n = most;
+        while (n > 1 && staged && (n < T ? n : T) * row > room) n /= 2;
         return n;
     };
-    pl.up_cols = cols(np == 3 ? 2 : 8, !pl.whole, up_row);
-    pl.down_cols = cols(np == 3 ? 2 : 4, !pl.token, down_row);
+    const int up = cols(np == 3 ? 2 : 8, !pl.whole, up_row), down = cols(np == 3 ? 2 : 4, !pl.token, down_row);
+    auto log2 = [](int n) { return n == 8 ? 3 : n == 4 ? 2 : n == 2 ? 1 : 0; };
+    pl.up_log2 = log2(up);
+    pl.down_log2 = log2(down);
+    pl.up_cols = up < T ? up : T;
+    pl.down_cols = down < T ? down : T;
     const long long up_item = pl.up_cols * up_row, down_item = pl.token ? k * down_row : pl.down_cols * down_row;
     if (room < 0 || (!pl.whole && up_item > room) || down_item > room) return pl;
     auto most = [&](long long item) { return (int)(room / item < kMoeItems ? room / item : kMoeItems); };
@@ -149,6 +154,8 @@ cudaError_t launch_moe_layer(const MoePlan& pl, const MoeCall& c, void* ws, unsi
     p.y = c.y;
     p.counters = counters;
     p.err = err;
+    p.up_log2 = pl.up_log2;
+    p.down_log2 = pl.down_log2;
     p.up_cols = pl.up_cols;
     p.down_cols = pl.down_cols;
     p.whole = pl.whole;

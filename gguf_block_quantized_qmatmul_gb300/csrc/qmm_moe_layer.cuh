@@ -61,7 +61,9 @@ struct MoeParams {
     unsigned* counters;  // [0] tickets, [1] shares of the first products done, [2] of the second
     unsigned* err;
     int epl16;           // experts per lane in the routing: 16, or 4
-    int up_cols, down_cols, whole, up_items, down_items;
+    int up_log2, down_log2;  // tokens per item, at most
+    int up_cols, down_cols;  // and how many have room
+    int whole, up_items, down_items;
     int off_zero, off_part, off_ring, off_route;
     int stall;
 };
@@ -443,8 +445,9 @@ __global__ void __launch_bounds__(kMoeThreads, 1) moe_layer_kernel(const __grid_
     int* token = order + S;                                          // [S]
     MoeItem* items = reinterpret_cast<MoeItem*>(token + S);          // [S] of the first products
     MoeItem* items2 = items + S;                                     // [S] of the second
-    int* offsets = reinterpret_cast<int*>(items2 + S);               // [E]
-    uint32_t* mask = reinterpret_cast<uint32_t*>(offsets + E);       // [E] the tokens that chose an expert
+    using Sum = unsigned long long;
+    Sum* before = reinterpret_cast<Sum*>(items2 + S);                // [E] slots, first and second items before an expert's
+    uint32_t* mask = reinterpret_cast<uint32_t*>(before + E);        // [E] the tokens that chose an expert
     uint32_t* picks = reinterpret_cast<uint32_t*>(sm + p.off_ring);  // [warps][E], where the rings will be
     for (int e = tid; e < E; e += kMoeThreads) mask[e] = 0u;
     if (tid == 0) *reinterpret_cast<uint4*>(sm + p.off_zero) = make_uint4(0u, 0u, 0u, 0u);  // what lanes without a column read
@@ -474,13 +477,7 @@ __global__ void __launch_bounds__(kMoeThreads, 1) moe_layer_kernel(const __grid_
         // Slots sorted by expert, by token within one: a count is a mask's population, a rank that of its
         // lower bits.  Slots and both products' items before each expert are one sum's thirds.
         const int per = (E + 31) / 32;
-        // (TOKEN: the second products' items are the tokens.)
-        using Sum = typename std::conditional<TOKEN, uint32_t, unsigned long long>::type;
-        auto count = [&](int n) {
-            Sum v = (Sum)n | (Sum)((unsigned)(n + p.up_cols - 1) / (unsigned)p.up_cols) << 16;
-            if constexpr (!TOKEN) v |= (Sum)((unsigned)(n + p.down_cols - 1) / (unsigned)p.down_cols) << 32;
-            return v;
-        };
+        auto count = [&](int n) { return (Sum)n | (Sum)((n + (1 << p.up_log2) - 1) >> p.up_log2) << 16 | (Sum)((n + (1 << p.down_log2) - 1) >> p.down_log2) << 32; };
         Sum mine = 0;
         for (int i = 0; i < per; ++i)
             if (lane * per + i < E) mine += count(__popc(mask[lane * per + i]));
@@ -492,32 +489,34 @@ __global__ void __launch_bounds__(kMoeThreads, 1) moe_layer_kernel(const __grid_
         }
         if (lane == 31) {
             s_items[0] = (int)(pre >> 16 & 0xffffu);
-            if constexpr (!TOKEN) s_items[1] = (int)(pre >> 32);
+            s_items[1] = (int)(pre >> 32);
         }
         pre -= mine;
         for (int i = 0; i < per; ++i) {
             const int e = lane * per + i;
             if (e >= E) break;
-            const int n = __popc(mask[e]), first = (int)(pre & 0xffffu);
-            offsets[e] = first;
-            auto list = [&](MoeItem* to, int cols) {
-                for (int c = 0; c < n; c += cols) *to++ = MoeItem{(uint32_t)e | (uint32_t)(first + c) << 9 | (uint32_t)min(cols, n - c) << 19};
-            };
-            list(items + (pre >> 16 & 0xffffu), p.up_cols);
-            if constexpr (!TOKEN) list(items2 + (pre >> 32), p.down_cols);
-            pre += count(n);
+            before[e] = pre;
+            pre += count(__popc(mask[e]));
         }
     }
     __syncthreads();
     for (int s = tid; s < S; s += kMoeThreads) {
-        const int t = s / k, e = ids[s];
-        const int at = offsets[e] + __popc(mask[e] & ((1u << t) - 1u));
+        const int t = s / k, e = ids[s], at = (int)(before[e] & 0xffffu) + __popc(mask[e] & ((1u << t) - 1u));
         order[at] = s;
         token[at] = t;
         if (blockIdx.x == 0 && p.route.c.ids) {
             p.route.c.ids[s] = e;
             p.route.c.weights[s] = weights[s];
         }
+    }
+    for (int e = tid; e < E; e += kMoeThreads) {
+        const Sum pre = before[e];
+        const int n = __popc(mask[e]), first = (int)(pre & 0xffffu);
+        auto list = [&](MoeItem* to, int cols) {
+            for (int c = 0; c < n; c += cols) *to++ = MoeItem{(uint32_t)e | (uint32_t)(first + c) << 9 | (uint32_t)min(cols, n - c) << 19};
+        };
+        list(items + (pre >> 16 & 0xffffu), 1 << p.up_log2);
+        list(items2 + (pre >> 32), 1 << p.down_log2);
     }
     const MoeShared sh = {ids, weights, order, token, items, T, k}, sh2 = {ids, weights, order, token, items2, T, k};
 

@@ -188,40 +188,80 @@ __device__ __forceinline__ int route_token(const RouteParams& p, long long tok, 
                 if (e0 + i < c.E && !((kept >> (((unsigned)(e0 + i) * p.group_magic) >> 22)) & 1u)) key[i] = 0u;
         }
     }
-    // the k largest: lane j ends up with choice j; a lane looks for its own largest again
-    // only after it gave it away (the lowest lane of equals has the lowest expert)
+    // the k largest: lane j ends up with choice j (the lowest lane of equals has the lowest expert)
     int my_id = 0;
     float my_score = 0.0f, sum = 0.0f;
-    uint32_t b = 0u;
-    int bi = 0;
-    float bs = 0.0f;
-    auto local = [&]() {
-        b = 0u;
-        bi = 0;
-        bs = 0.0f;
+    if constexpr (EPL <= 4) {
+        // A lane's few experts are put in order first, by pick and then by index; a step is then a reduction, a
+        // ballot and a move, some 80 cycles.  (Looking for a lane's largest again after it gave it away: 380 a step.)
+        int id[EPL];
 #pragma unroll
-        for (int i = 0; i < EPL; ++i) {
-            const bool more = key[i] > b;
-            b = more ? key[i] : b;
-            bi = more ? i : bi;
-            bs = more ? score[i] : bs;
-        }
-    };
-    local();
-    for (int j = 0; j < c.top_k; ++j) {
-        const uint32_t best = __reduce_max_sync(0xffffffffu, b);
-        const int l0 = __ffs(__ballot_sync(0xffffffffu, b == best)) - 1;
-        const int id = __shfl_sync(0xffffffffu, e0 + bi, l0);
-        const float s = __shfl_sync(0xffffffffu, bs, l0);
-        if (lane == l0) {
+        for (int i = 0; i < EPL; ++i) id[i] = e0 + i;
 #pragma unroll
-            for (int i = 0; i < EPL; ++i) key[i] = i == bi ? 0u : key[i];
-            local();
+        for (int n = EPL - 1; n > 0; --n)
+#pragma unroll
+            for (int i = 0; i < n; ++i) {
+                const bool swap = key[i + 1] > key[i];  // equals stay in order
+                const uint32_t k0 = key[i];
+                const float s0 = score[i];
+                const int i0 = id[i];
+                key[i] = swap ? key[i + 1] : k0;
+                key[i + 1] = swap ? k0 : key[i + 1];
+                score[i] = swap ? score[i + 1] : s0;
+                score[i + 1] = swap ? s0 : score[i + 1];
+                id[i] = swap ? id[i + 1] : i0;
+                id[i + 1] = swap ? i0 : id[i + 1];
+            }
+        for (int j = 0; j < c.top_k; ++j) {
+            const uint32_t best = __reduce_max_sync(0xffffffffu, key[0]);
+            const int l0 = __ffs(__ballot_sync(0xffffffffu, key[0] == best)) - 1;
+            const int got = __shfl_sync(0xffffffffu, id[0], l0);
+            const float s = __shfl_sync(0xffffffffu, score[0], l0);
+            const bool mine = lane == l0;
+#pragma unroll
+            for (int i = 0; i + 1 < EPL; ++i) {
+                key[i] = mine ? key[i + 1] : key[i];
+                score[i] = mine ? score[i + 1] : score[i];
+                id[i] = mine ? id[i + 1] : id[i];
+            }
+            key[EPL - 1] = mine ? 0u : key[EPL - 1];
+            sum += s;
+            my_id = lane == j ? got : my_id;
+            my_score = lane == j ? s : my_score;
         }
-        sum += s;
-        if (lane == j) {
-            my_id = id;
-            my_score = s;
+    } else {
+        // a lane looks for its own largest again only after it gave it away
+        uint32_t b = 0u;
+        int bi = 0;
+        float bs = 0.0f;
+        auto local = [&]() {
+            b = 0u;
+            bi = 0;
+            bs = 0.0f;
+#pragma unroll
+            for (int i = 0; i < EPL; ++i) {
+                const bool more = key[i] > b;
+                b = more ? key[i] : b;
+                bi = more ? i : bi;
+                bs = more ? score[i] : bs;
+            }
+        };
+        local();
+        for (int j = 0; j < c.top_k; ++j) {
+            const uint32_t best = __reduce_max_sync(0xffffffffu, b);
+            const int l0 = __ffs(__ballot_sync(0xffffffffu, b == best)) - 1;
+            const int id = __shfl_sync(0xffffffffu, e0 + bi, l0);
+            const float s = __shfl_sync(0xffffffffu, bs, l0);
+            if (lane == l0) {
+#pragma unroll
+                for (int i = 0; i < EPL; ++i) key[i] = i == bi ? 0u : key[i];
+                local();
+            }
+            sum += s;
+            if (lane == j) {
+                my_id = id;
+                my_score = s;
+            }
         }
     }
     if (lane < c.top_k) {

@@ -104,7 +104,8 @@ struct MoeCall {
 struct MoePlan {
     bool ok = false;
     int token = 0;   // the second products' items are tokens, not experts
-    int up_cols = 0, down_cols = 0;  // tokens per item of an expert, at most
+    int up_log2 = 0, down_log2 = 0;  // tokens per item of an expert, at most
+    int up_cols = 0, down_cols = 0;  // and how many have room
     int whole = 0;   // all tokens' activations are staged at once
     int up_items = 0, down_items = 0;  // items whose activations fit beside each other
     int blocks = 0;
