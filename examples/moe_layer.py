@@ -1,8 +1,9 @@
 """A mixture-of-experts block on 4-bit weights, as a model runs it.
 
 Per token: a router (a small f32 product), top-k of E experts, the experts'
-gate and up products with SwiGLU, their down products summed by weight, and a
-dense shared expert beside them.  Prints the error against 64-bit arithmetic
+gate and up products with SwiGLU, their down products summed by weight (up to 32
+tokens: the whole layer in one call), and a dense shared expert beside them.
+With --norm the block stands between its norms, as in a decoder.  Prints the error against 64-bit arithmetic
 and the time of a block as a CUDA graph, for a decode step, a small batch and
 a prompt.
 
@@ -41,9 +42,14 @@ class MoeBlock:
         self.shared_in = random_weights(1, 2 * inner, hidden, group, False, gen)
         self.shared_out = random_weights(1, hidden, inner, group, False, gen)
 
-    def __call__(self, x: torch.Tensor) -> torch.Tensor:
+    def experts(self, x: torch.Tensor) -> torch.Tensor:
+        if x.shape[0] <= 32:
+            return q.moe_layer(self.gate_up, self.down, self.router, x, self.top_k, score="sigmoid", bias=self.bias)
         route = q.moe_route(x.float() @ self.router.T, self.top_k, score="sigmoid", bias=self.bias)
-        y = q.moe_down(self.down, q.moe_gate_up(self.gate_up, x, route), route)
+        return q.moe_down(self.down, q.moe_gate_up(self.gate_up, x, route), route)
+
+    def __call__(self, x: torch.Tensor) -> torch.Tensor:
+        y = self.experts(x)
         both = q.q4g_matmul(self.shared_in, x)
         h = torch.nn.functional.silu(both[:, :self.inner]) * both[:, self.inner:]
         return y + q.q4g_matmul(self.shared_out, h)
@@ -89,6 +95,7 @@ def main() -> None:
     ap.add_argument("--hidden", type=int, default=2048)
     ap.add_argument("--inner", type=int, default=1024)
     ap.add_argument("--dtype", choices=list(DTYPES), default="bf16")
+    ap.add_argument("--norm", action="store_true", help="time the block between its norms")
     a = ap.parse_args()
     block = MoeBlock(a.experts, a.top_k, a.hidden, a.inner)
     for tokens in (1, 16, 2048):
@@ -96,7 +103,11 @@ def main() -> None:
         y, few = block(x), min(tokens, 16)
         ref = block.exact(x[:few])
         err = float((y[:few].double() - ref).norm() / ref.norm())
-        print(f"{tokens:5d} tokens: relative error {err:.1e}, {graph_time(lambda: block(x)):8.1f} us a block")
+        whole = lambda: block(x)  # noqa: E731
+        if a.norm:
+            w = torch.ones(a.hidden, device="cuda")
+            whole = lambda: q.block_norm(block(q.block_norm(x, w)[1]), w, residual=x, post_weight=w)  # noqa: E731
+        print(f"{tokens:5d} tokens: relative error {err:.1e}, {graph_time(whole):8.1f} us a block")
     if q.last_device_error():
         raise SystemExit("a device-side wait gave up")
 

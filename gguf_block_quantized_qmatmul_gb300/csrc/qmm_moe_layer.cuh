@@ -158,7 +158,7 @@ __device__ __forceinline__ void moe_stage(uint8_t* sm, const void* x, int nh, in
                 const long long at = src(quad - h * rows, h, left) + 8 * (i & 3);
                 if (8 * (i & 3) < left)
 #pragma unroll
-                    for (int q = 0; q < (S32 ? 2 : 1); ++q) u[b][q] = reinterpret_cast<const uint4*>(static_cast<const uint8_t*>(x) + at * (S32 ? 4 : 2))[q];
+                    for (int q = 0; q < (S32 ? 2 : 1); ++q) u[b][q] = __ldcg(reinterpret_cast<const uint4*>(static_cast<const uint8_t*>(x) + at * (S32 ? 4 : 2)) + q);  // past L1, which may hold an earlier x or h
             }
         }
 #pragma unroll

@@ -80,7 +80,8 @@ CASES = [
     (4, 512, 3, 64, 32, 64, 32, 32, "bf16", "sigmoid"), (5, 64, 8, 512, 256, 512, 128, 128, "bf16", "softmax"), (5, 3, 1, 32, 32, 1, 32, 32, "f32", "softmax"),
     (7, 100, 7, 320, 160, 333, 32, 32, "f16", "sigmoid"), (16, 64, 8, 1024, 512, 1024, 64, 64, "f16", "softmax"), (16, 8, 8, 256, 128, 256, 128, 64, "f32", "softmax"),
     (17, 8, 2, 512, 256, 512, 64, 128, "bf16", "sigmoid"), (32, 16, 4, 576, 192, 576, 64, 64, "bf16", "softmax"), (32, 300, 8, 256, 128, 256, 64, 32, "f32", "sigmoid"),
-    (32, 1, 1, 160, 96, 100, 32, 32, "f16", "softmax"), (9, 32, 32, 128, 64, 128, 64, 64, "f16", "softmax"), (1, 40, 32, 256, 64, 300, 32, 64, "bf16", "softmax")]
+    (32, 1, 1, 160, 96, 100, 32, 32, "f16", "softmax"), (9, 32, 32, 128, 64, 128, 64, 64, "f16", "softmax"), (32, 512, 32, 64, 32, 40, 32, 32, "f16", "softmax"),
+    (32, 33, 32, 96, 64, 64, 32, 64, "f32", "sigmoid"), (20, 8, 1, 4096, 64, 100, 128, 64, "f32", "softmax"), (1, 40, 32, 256, 64, 300, 32, 64, "bf16", "softmax")]
 
 
 @pytest.mark.parametrize("T,E,k,K,F,N,G,G2,dt,score", CASES)
@@ -194,6 +195,48 @@ def test_rows_apart_canary_stream_graph_and_workspace(q, T):
         assert torch.equal(z, ref) and torch.equal(z2, ref)
 
 
+def test_the_block_of_a_decoder(q):
+    """What these operators are for, as a decode step calls them: norm to 8-bit rows, a projection, norm and residual, the
+    mixture-of-experts layer, norm and residual.  Each against 64 bits from the step before it as it came out, and in a
+    graph the same again."""
+    T, K, E, F, k = 6, 512, 16, 128, 4
+    up, wu, down, wd, x, router = make(q, T, E, K, F, K, 64, 64, "bf16")
+    proj = torch.randn((K, K), generator=rng(20)) / K ** 0.5
+    wp = q.q8c_pack(*q.q8c_quantize(proj.cuda()))
+    n1, n2, n3, post = ((1 + 0.2 * torch.randn(K, generator=rng(21 + i))).bfloat16().cuda() for i in range(4))
+    router, x = router.cuda(), x.cuda()
+
+    def block(x):
+        r0, rows = q.block_norm(x, n1, quantize=True)
+        a = q.q8c_matmul(wp, rows, dtype=torch.bfloat16)
+        r1, h = q.block_norm(a, n2, residual=r0, post_weight=post)
+        m, route = q.moe_layer(up, down, router, h, k, route=True)
+        r2, out = q.block_norm(m, n3, residual=r1, scale=0.5)
+        return rows, a, r1, h, route, m, r2, out
+
+    rows, a, r1, h, route, m, r2, out = block(x)
+    norm = lambda v: v / torch.sqrt((v * v).mean(1, keepdim=True) + 1e-6)  # noqa: E731
+    near = lambda got, ref, tol: float((got.double() - ref).norm()) <= tol * float(ref.norm())  # noqa: E731
+    u = U["bf16"]
+    # the projection: integers, exactly; the norms: one rounding of each result
+    w = q.q8c_dequantize(wp).double()
+    assert near(a, (rows.codes.double() * rows.scales.double()[:, None]) @ w.T, u)
+    assert near(r1, x.double() + norm(a.double()) * post.double(), u)
+    assert near(h, norm(x.double() + norm(a.double()) * post.double()) * n2.double(), u)
+    ref, tol = exact(h.cpu(), route.ids.cpu(), route.weights.cpu(), wu, wd, "bf16")
+    assert ((m.double().cpu() - ref).abs() <= tol).all()
+    assert near(r2, r1.double() + 0.5 * m.double(), u) and near(out, norm(r1.double() + 0.5 * m.double()) * n3.double(), u)
+    g = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(g):
+        again = block(x)[-1]
+    for _ in range(2):
+        again.zero_()
+        g.replay()
+        torch.cuda.synchronize()
+        assert torch.equal(again, out)
+    assert q.last_device_error() == 0
+
+
 def test_refusals_and_empty(q):
     E, K, F, N = 8, 64, 32, 64
     up, _, down, _, x, router = make(q, 4, E, K, F, N, 32, 32, "f16")
@@ -202,6 +245,9 @@ def test_refusals_and_empty(q):
     for bad in (dict(x=x.repeat(9, 1)), dict(top_k=0), dict(top_k=9), dict(gate_up=down), dict(down=up), dict(groups=3), dict(groups=8, top_groups=1, top_k=2)):
         with pytest.raises((q.QmmError, ValueError)):
             q.moe_layer(**{**dict(gate_up=up, down=down, router=router, x=x, top_k=2), **bad})
+    with pytest.raises(q.QmmError) as e:  # rows on no 16-byte boundary
+        q.moe_layer(up, down, router, torch.empty((4, K + 1), dtype=torch.float16, device="cuda")[:, 1:], 2)
+    assert e.value.status == 4
     for bad in (dict(router=router[:7]), dict(router=router.t().contiguous().t()), dict(router=router.cpu()), dict(x=x[:, :32]), dict(bias=torch.zeros(7, device="cuda")),
                 dict(out=torch.empty((4, N), device="cuda"))):
         with pytest.raises(ValueError):

@@ -147,6 +147,17 @@ def test_matmul_types(q, M, xdt, ydt):
     same(y, plain_product(c, d, codes.numpy(), scales.numpy(), None, ydt))
 
 
+@pytest.mark.parametrize("M,N,K", [(3, 128, 640), (40, 1300, 576), (300, 2052, 1024), (33, 400, 8192), (40, 1302, 576)])
+@pytest.mark.parametrize("dt", list(DT))
+def test_bias(q, M, N, K, dt):
+    """The bias is added to the rounded product: no contraction."""
+    codes, scales, w = weights(q, N, K)
+    x = torch.randn((M, K), generator=rng(M)).to(DT[dt])
+    bias = torch.randn(N, generator=rng(9))
+    c, d = plain_codes(x)
+    same(q.q8c_matmul(w, x.cuda(), bias=bias.cuda()), plain_product(c, d, codes.numpy(), scales.numpy(), bias.numpy(), dt))
+
+
 def test_a_row_does_not_depend_on_the_others(q):
     N, K = 2000, 1536
     _, _, w = weights(q, N, K)
