@@ -274,9 +274,10 @@ QcRowsPlan plan_q8c_rows(const QcCall& c, int sms, int smem_max) {
     const QcWeights& w = c.w;
     if (c.a.M > kMaxRows || (long long)w.RB * w.KS > INT32_MAX) return pl;
     pl.pitch = w.KS * 128 + 64;
-    pl.warps = (long long)c.a.M * w.K <= 8192 ? 8 : kMaxWarps;
-    const int act = c.a.M * pl.pitch, rest = pl.warps * 1024 + pl.warps * kDepth * kQcSeg;
-    if (act + 16 + rest > smem_max - kStatic - 1024) return pl;
+    const int act = c.a.M * pl.pitch, room = smem_max - kStatic - 1024 - 16 - act, per_warp = 1024 + kDepth * kQcSeg;
+    pl.warps = (long long)c.a.M * w.K <= 8192 || kMaxWarps * per_warp > room ? 8 : kMaxWarps;  // beside long rows eight fit
+    const int rest = pl.warps * per_warp;
+    if (rest > room) return pl;
     pl.blocks = w.RB < sms ? w.RB : sms;
     pl.off_zero = act;
     pl.off_part = pl.off_zero + 16;

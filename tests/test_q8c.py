@@ -158,6 +158,36 @@ def test_bias(q, M, N, K, dt):
     same(q.q8c_matmul(w, x.cuda(), bias=bias.cuda()), plain_product(c, d, codes.numpy(), scales.numpy(), bias.numpy(), dt))
 
 
+@pytest.mark.parametrize("M,K", [(4, 20736), (3, 28672), (4, 32768), (2, 32768), (1, 100000)])
+def test_few_long_rows_of_codes(q, M, K):
+    """Rows whose codes fill most of a block's shared memory; up to 32768 K they need no workspace, as the header says."""
+    N = 40
+    codes, scales, w = weights(q, N, K, spread=12.0)
+    rows = torch.randint(-127, 128, (M, K), generator=rng(M)).to(torch.int8)
+    sx = 0.5 + torch.rand(M, generator=rng(5))
+    ref = plain_product(rows.numpy().astype(np.int64), sx.numpy(), codes.numpy(), scales.numpy(), None, "f32")
+    x = q.Rows8(rows.cuda(), sx.cuda())
+    same(q.q8c_matmul(w, x), ref)
+    if K <= 32768:
+        same(q.q8c_matmul(w, x, workspace=torch.empty(0, dtype=torch.uint8, device="cuda")), ref)
+
+
+def test_offsets_past_32_bits(q):
+    """Results and activations of more than 2^31 elements: rows of the end and around the boundary against calls of their own."""
+    N, K, M = 2048, 64, 1100000
+    _, _, w = weights(q, N, K)
+    x = torch.randn((M, K), generator=rng(2)).half().cuda()
+    y = q.q8c_matmul(w, x)
+    edge = 2 ** 31 // N
+    for m in (0, edge - 4, edge, M - 8):
+        assert torch.equal(y[m:m + 8], q.q8c_matmul(w, x[m:m + 8]))
+    far = torch.empty((70, 1 << 25), dtype=torch.float16, device="cuda")[:, :K]  # rows 2^25 elements apart
+    far.copy_(x[:70])
+    assert torch.equal(q.q8c_matmul(w, far), y[:70]) and torch.equal(q.q8c_matmul(w, far[-4:]), y[66:70])
+    r = q.q8c_quantize(far)
+    assert torch.equal(q.q8c_matmul(w, r, dtype=torch.float16), y[:70])
+
+
 def test_a_row_does_not_depend_on_the_others(q):
     N, K = 2000, 1536
     _, _, w = weights(q, N, K)
