@@ -17,15 +17,18 @@
 // The structure is the 4-bit GEMM's (qmm_q4g_gemm.cuh): one persistent block an
 // SM, pairs of blocks (cta_group::2) on 256 weight rows x up to 256 activation
 // rows; converted weights are the A operand in tensor memory, activations come
-// by TMA in 128-byte swizzled tiles.  19 warps' roles:
+// by TMA in 128-byte swizzled tiles.  27 warps' roles:
 //   warp 0      activation tiles, 128 K each (256 for up to 128 activation rows: handing a tile from role to role
-//               takes some 600 cycles, more than the MMAs of 128 K take there)
+//               takes some 600 cycles, more than the MMAs of 128 K take there: 37 x 14336 x 4096 17.0 us, with 128 19.5)
 //   warp 1      eight MMAs per 128 K
 //   warp 2      raw weights, a panel's 128 K (16 KB) a copy
 //   8 or 16     epilogue: results from the accumulator, scaled
 //   16 or 8     conversion: 32 codes a lane and tile of 64 K, ten instructions for eight
 // Calls with few tiles are split over K; the slices' integer sums go to the
-// workspace and a last launch adds and scales them.
+// workspace and a last launch adds and scales them (37 x 4096 x 14336: 20 us, whole 39).
+//
+// Bound by the weight stream and the hand-over for few rows (16 x 14336 x 4096 16 us, 3.6 TB/s), by the MMAs for many
+// (1024 x 14336 x 4096 76 us, 1.58 PFLOP/s, the tensor pipe at 71 % of the kernel's cycles); both with the preparation.
 //
 // Waits are bounded, as in the 4-bit GEMM: one that gives up raises the error
 // word, every other role ends, and what was issued is waited for.
@@ -575,7 +578,10 @@ QcGemmPlan plan_q8c_gemm(const QcCall& c, int sms, int smem_max) {
         }
     }
     pl.accw = (pl.bx + 31) / 32 * 32;
-    pl.nacc = pl.bx <= 192 ? 2 : 1;  // with two accumulators the epilogue runs beside the next unit's MMAs
+    // With two accumulators the epilogue runs beside the next unit's MMAs (192 x 28672 x 4096 44 us, with one 47); where
+    // there is no next unit their columns hold converted weights (192 x 14336 x 4096 25, with two 29).
+    const long long units = (long long)pl.mtiles * pl.ntiles * pl.ks, workers = sms / pl.cg;
+    pl.nacc = pl.bx <= 192 && units > workers ? 2 : 1;
     pl.nstage = (kTcTmemCols - pl.nacc * pl.accw) / (64 * pl.kt);
     if (pl.nstage > kQgStageMax) pl.nstage = kQgStageMax;
     const int stage = pl.bx / pl.cg * 256 * pl.kt, raw = kRaw * pl.kt, room = smem_max - kTail - 1024;
@@ -589,7 +595,6 @@ QcGemmPlan plan_q8c_gemm(const QcCall& c, int sms, int smem_max) {
     pl.nx = (room - pl.nraw * raw) / stage < kXMax ? (room - pl.nraw * raw) / stage : kXMax;
     if (pl.nstage < 2 || pl.nx < 2 || pl.nraw < 2) return pl;
     pl.smem = (size_t)pl.nx * stage + (size_t)pl.nraw * raw + kTail + 1024;
-    const long long units = (long long)pl.mtiles * pl.ntiles * pl.ks, workers = sms / pl.cg;
     if (units > (1ll << 30)) return pl;
     pl.grid = (int)(units < workers ? units : workers) * pl.cg;
     auto r256 = [](size_t v) { return (v + 255) / 256 * 256; };

@@ -168,9 +168,11 @@ bool rows_aligned(const QcRows& a, int size) { return (reinterpret_cast<uintptr_
 
 template <int XT, bool F16>
 cudaError_t prep_go(const PrepParams& q, cudaStream_t s) {
-    // 1024 x 4096 bf16 as 256 threads a row; a warp a row where that leaves fewer idle lanes than it costs latency
+    // A product's time with a warp / 256 / 1024 threads a row, us: 512 x 1536 x 576 9.0 / 9.2 / 12.8, 4096 x 1536 x 576
+    // 20 / 26 / 65; 512 x 1536 x 2048 16.8 / 13.7 / 17.4; 16 x 4096 x 4096 - / 11.4 / 10.9, 1024 x 4096 x 4096 - / 33 /
+    // 42; 16 x 4096 x 8192 - / 16.0 / 14.0, 256 x 1536 x 8192 - / 20.6 / 21.5; 64 x 1536 x 14336 - / 19.0 / 16.4.
     if (q.K <= 1024 && q.a.M >= 512) return launch_pdl(q8c_prep_kernel<XT, 32, F16>, (unsigned)((q.a.M + 7) / 8), 256, 0, s, q);
-    if (q.K <= 8192 || q.a.M >= 512) return launch_pdl(q8c_prep_kernel<XT, 256, F16>, (unsigned)q.a.M, 256, 0, s, q);
+    if (q.K < 4096 || q.a.M > q.K / 64) return launch_pdl(q8c_prep_kernel<XT, 256, F16>, (unsigned)q.a.M, 256, 0, s, q);
     return launch_pdl(q8c_prep_kernel<XT, 1024, F16>, (unsigned)q.a.M, 1024, 0, s, q);
 }
 
