@@ -11,30 +11,37 @@
 //
 // Bound by the bytes, each read and written once: a row stays in registers, 8
 // values a thread and piece, through up to three reductions (two sums, a
-// maximum).  Three kernels:
-//   few rows, or rows on no 16-byte boundaries: a block per row, which asks for
-//     everything before its first reduction; bound by a launch, one trip to memory
-//     and the reductions
-//   many long rows: persistent blocks, a row at a time, whose next rows are on
-//     their way into a ring in shared memory by bulk copies; weights and a gate per
-//     channel stay in registers.  (A block per row of 4096: 46 us for 4096 rows in
-//     bf16, loads and reductions in turn.)
-//   many short rows: persistent warps, a row each, the next one in registers
+// maximum).  Three kernels, in all of which a row is dealt to as many threads and
+// summed in the same order, so that its results are the same bits beside
+// any other rows:
+//   block_norm_kernel, a block (short rows: a warp) per row: rows on no 16-byte boundaries, K past 8192, weights of
+//     the other 16-bit type, few long rows; bound by a launch, one trip to memory and the reductions
+//   norm_ring_kernel: persistent blocks, a row at a time, whose next rows are on their way into a ring in shared
+//     memory by bulk copies; weights and a gate per channel stay in registers.  4096 rows of 4096 in bf16, norms on
+//     both sides, a gate per channel: 24.7 us, 5.4 TB/s (a block per row: 46, loads and reductions in turn)
+//   norm_warps_kernel: short rows, a warp each, the next one in registers; 16384 of 576 in f16 20.4 us
 #pragma once
+
+#include <type_traits>
 
 #include "qmm_q8c.cuh"
 
 namespace qmm {
 namespace {
 
-__device__ __forceinline__ void load8(const void* row, int type, int k, int K, bool vec, float f[8]) {
-    if (type == X_F32) qc_load8<X_F32>(row, k, K, vec, f);
-    else if (type == X_F16) qc_load8<X_F16>(row, k, K, vec, f);
-    else qc_load8<X_BF16>(row, k, K, vec, f);
+template <int XT>
+__device__ __forceinline__ uint32_t two16(float a, float b) {
+    if constexpr (XT == X_F16) {
+        const __half2 v = __floats2half2_rn(a, b);
+        return *reinterpret_cast<const uint32_t*>(&v);
+    } else {
+        const __nv_bfloat162 v = __floats2bfloat162_rn(a, b);
+        return *reinterpret_cast<const uint32_t*>(&v);
+    }
 }
 template <int XT>
-__device__ __forceinline__ void store8(void* row, int k, int K, bool vec, const float f[8]) {
-    if (vec && k + 8 <= K) {
+__device__ __forceinline__ void store8(void* row, int k, int K, const float f[8]) {
+    if (k + 8 <= K) {
         if constexpr (XT == X_F32) {
             float4* p = reinterpret_cast<float4*>(static_cast<float*>(row) + k);
             p[0] = make_float4(f[0], f[1], f[2], f[3]);
@@ -42,15 +49,7 @@ __device__ __forceinline__ void store8(void* row, int k, int K, bool vec, const 
         } else {
             uint32_t w[4];
 #pragma unroll
-            for (int i = 0; i < 4; ++i) {
-                if constexpr (XT == X_F16) {
-                    const __half2 v = __floats2half2_rn(f[2 * i], f[2 * i + 1]);
-                    w[i] = *reinterpret_cast<const uint32_t*>(&v);
-                } else {
-                    const __nv_bfloat162 v = __floats2bfloat162_rn(f[2 * i], f[2 * i + 1]);
-                    w[i] = *reinterpret_cast<const uint32_t*>(&v);
-                }
-            }
+            for (int i = 0; i < 4; ++i) w[i] = two16<XT>(f[2 * i], f[2 * i + 1]);
             *reinterpret_cast<uint4*>(static_cast<uint16_t*>(row) + k) = make_uint4(w[0], w[1], w[2], w[3]);
         }
     } else {
@@ -84,75 +83,230 @@ __device__ __forceinline__ uint32_t max_row(uint32_t v, uint32_t* red) {
     return v;
 }
 
-template <int XT, int TPR, int NV>
-__global__ void __launch_bounds__(TPR < 256 ? 256 : TPR) block_norm_kernel(const NormParams p) {
-    __shared__ float red[3][32];  // an area per reduction
-    grid_dep_launch();
-    const NormCall& c = p.c;
-    constexpr int kRows = TPR < 256 ? 256 / TPR : 1;
-    const int lane = threadIdx.x % TPR, K = c.K;
-    const long long row = (long long)blockIdx.x * kRows + threadIdx.x / TPR;
-    const bool vec = p.vec;
-    grid_dep_wait();
-    if (row >= c.T) return;  // whole warps
-    const uint8_t* y = static_cast<const uint8_t*>(c.y) + row * c.ldy * x_size(XT);
-    float v[NV][8], r[NV][8], gate[NV][8];
+__device__ __forceinline__ float root_of(float ss, const NormCall& c) { return 1.0f / sqrtf(fmaf(ss, 1.0f / (float)c.K, c.eps)); }
+
+// A thread's 8 neighbouring values of a row.  VEC: rows start on 16-byte boundaries; else a warp's pieces are taken
+// from the 16-byte words that they lie in: a lane asks for the words that its piece begins in, has what it misses
+// from the next lane (the last one: from memory) and shifts.  A word that is not in the tensor whole is read value
+// by value; other words may hold neighbouring rows' values, which are dropped.  So a thread's values are the same
+// wherever a row starts.  4096 rows of 4095 in bf16, a gate per token: 65 us (eight loads of a value each 122; 32
+// values apart and exchanged through shared memory 98).
+template <int XT, bool VEC>
+struct Piece {
+    static constexpr int kWords = XT == X_F32 ? 8 : 4, kEach = 16 / x_size(XT);  // 4-byte words; values of a 16-byte word
+    uint32_t u[kWords + 4];
+    int o;  // bytes from a 16-byte boundary to the piece, the same for a row
+
+    // The 16-byte word from value k of a row on.  ENDS: only values lo .. hi - 1 from the row's start on are the
+    // tensor's; then value by value, others in place of those that are not there.
+    template <bool ENDS>
+    static __device__ __forceinline__ void word(const uint8_t* row, int k, int lo, int hi, bool on, uint32_t* to) {
+        to[0] = to[1] = to[2] = to[3] = 0u;
+        if (!on) return;
+        if constexpr (!ENDS) {
+            const uint4 v = *reinterpret_cast<const uint4*>(row + k * x_size(XT));
+            to[0] = v.x, to[1] = v.y, to[2] = v.z, to[3] = v.w;
+        } else {
+            auto one = [&](int e) {
+                const int i = max(min(k + e, hi - 1), lo);
+                if constexpr (XT == X_F32) return reinterpret_cast<const uint32_t*>(row)[i];
+                else return (uint32_t)reinterpret_cast<const uint16_t*>(row)[i];
+            };
 #pragma unroll
-    for (int j = 0; j < NV; ++j) qc_load8<XT>(y, 8 * (lane + TPR * j), K, vec, v[j]);
-    if (c.r) {
-        const uint8_t* from = static_cast<const uint8_t*>(c.r) + row * c.ldr * x_size(XT);
-#pragma unroll
-        for (int j = 0; j < NV; ++j) qc_load8<XT>(from, 8 * (lane + TPR * j), K, vec, r[j]);
-    }
-    if (c.gate) {
-        const uint8_t* from = static_cast<const uint8_t*>(c.gate) + row * c.ldg * x_size(XT);
-#pragma unroll
-        for (int j = 0; j < NV; ++j) qc_load8<XT>(from, 8 * (lane + TPR * j), K, vec, gate[j]);
-    }
-    const float mean = 1.0f / (float)K;
-    if (c.post) {
-        float ss = 0.0f;
-#pragma unroll
-        for (int j = 0; j < NV; ++j)
-#pragma unroll
-            for (int e = 0; e < 8; ++e) ss = fmaf(v[j][e], v[j][e], ss);
-        const float rs = 1.0f / sqrtf(fmaf(sum_row<TPR>(ss, red[0]), mean, c.eps));
-#pragma unroll
-        for (int j = 0; j < NV; ++j) {
-            float w[8];
-            load8(c.post, c.wt, 8 * (lane + TPR * j), K, vec, w);
-#pragma unroll
-            for (int e = 0; e < 8; ++e) v[j][e] = v[j][e] * rs * (c.offset + w[e]);
+            for (int i = 0; i < 4; ++i) to[i] = XT == X_F32 ? one(i) : one(2 * i) | one(2 * i + 1) << 16;
         }
     }
-    float ss = 0.0f;
+    // values k .. k + 7: the words that begin in the row
+    template <bool ENDS>
+    __device__ __forceinline__ void load(const void* from, int k, int lo, int hi, int K) {
+        const uint8_t* row = static_cast<const uint8_t*>(from);
+        if constexpr (!VEC) o = (int)(reinterpret_cast<uintptr_t>(row) & 15);
+        const int k0 = k - (VEC ? 0 : o / x_size(XT));
 #pragma unroll
-    for (int j = 0; j < NV; ++j)
-#pragma unroll
-        for (int e = 0; e < 8; ++e) {
-            float a = v[j][e];
-            if (c.gate) a *= gate[j][e];
-            v[j][e] = c.r ? fmaf(c.scale, a, r[j][e]) : c.scale * a;
-            ss = fmaf(v[j][e], v[j][e], ss);
-        }
-    if (c.r_out) {
-        uint8_t* to = static_cast<uint8_t*>(c.r_out) + row * c.ldro * x_size(XT);
-#pragma unroll
-        for (int j = 0; j < NV; ++j) store8<XT>(to, 8 * (lane + TPR * j), K, vec, v[j]);
+        for (int i = 0; i < kWords; i += 4) word<ENDS>(row, k0 + i / 4 * kEach, lo, hi, k0 + i / 4 * kEach < K, u + i);
+        if constexpr (!VEC) word<ENDS>(row, k0 + 8, lo, hi, (threadIdx.x & 31) == 31 && o && k0 + 8 < K, u + kWords);
     }
-    // past the row's end (k >= K) y, r and gate are 0, so the values are; a weight offset does not reach them
-    const float rs = 1.0f / sqrtf(fmaf(sum_row<TPR>(ss, red[1]), mean, c.eps));
+    // Whether the words of a warp's 256 values, this lane's from k on, may lie in the tensor in part: at most 7 values
+    // before and after the row are read.
+    static __device__ __forceinline__ bool ends(bool first, bool last, int k, int K) {
+        if (VEC && K % 8 == 0) return false;
+        k -= 8 * (threadIdx.x & 31);
+        return (first && k == 0) || (last && k + 256 + 8 > K);
+    }
+    // of a row that is a tensor
+    __device__ __forceinline__ void load_one(const void* row, int k, int K) {
+        if (ends((reinterpret_cast<uintptr_t>(row) & 15) != 0, true, k, K)) load<true>(row, k, 0, K, K);
+        else load<false>(row, k, 0, K, K);
+    }
+    // n words of w from `bytes` (< 16) on
+    template <int N>
+    static __device__ __forceinline__ void shift(uint32_t* w, int bytes) {
+#pragma unroll
+        for (int i = 0; i < N + 2; ++i) w[i] = bytes & 8 ? w[i + 2] : w[i];
+#pragma unroll
+        for (int i = 0; i < N + 1; ++i) w[i] = bytes & 4 ? w[i + 1] : w[i];
+        if constexpr (XT != X_F32) {
+#pragma unroll
+            for (int i = 0; i < N; ++i) w[i] = __funnelshift_r(w[i], w[i + 1], 8 * (bytes & 2));
+        }
+    }
+    // 0 from K on
+    __device__ __forceinline__ void get(int k, int K, float f[8]) {
+        if constexpr (!VEC) {
+#pragma unroll
+            for (int i = 0; i < 4; ++i) {
+                const uint32_t next = __shfl_down_sync(0xffffffffu, u[i], 1);
+                if ((threadIdx.x & 31) != 31) u[kWords + i] = next;
+            }
+            shift<kWords>(u, o);
+        }
+        if constexpr (XT == X_F32) {
+#pragma unroll
+            for (int i = 0; i < 8; ++i) f[i] = __uint_as_float(u[i]);
+        } else {
+            qc_words8<XT>(u, f);
+        }
+        if (k + 8 > K) {
+#pragma unroll
+            for (int e = 0; e < 8; ++e) f[e] = k + e < K ? f[e] : 0.0f;
+        }
+    }
+    // values to the row, likewise in whole words but for a warp's ends and the row's
+    __device__ __forceinline__ void store(void* p, int k, int K, const float f[8]) {
+        if constexpr (VEC) {
+            store8<XT>(p, k, K, f);
+            return;
+        }
+        uint8_t* row = static_cast<uint8_t*>(p);
+        const int lane = threadIdx.x & 31, from = (16 - (int)(reinterpret_cast<uintptr_t>(row) & 15)) & 15, head = from / x_size(XT);
+        if constexpr (XT == X_F32) {
+#pragma unroll
+            for (int i = 0; i < 8; ++i) u[i] = __float_as_uint(f[i]);
+        } else {
+#pragma unroll
+            for (int i = 0; i < 4; ++i) u[i] = two16<XT>(f[2 * i], f[2 * i + 1]);
+        }
+#pragma unroll
+        for (int i = 0; i < 4; ++i) u[kWords + i] = __shfl_down_sync(0xffffffffu, u[i], 1);
+        shift<kWords>(u, from);
+        // values head .. 7 of this piece and 0 .. head - 1 of the next one are the words; the first `head` are the last lane's
+        const bool before = head && lane > 0 && k + head <= K;
+        int done = head;  // values up to here are in words
+#pragma unroll
+        for (int i = 0; i < kWords; i += 4) {
+            const int k1 = k + head + i / 4 * kEach;
+            if (k1 + kEach <= K && (i + 4 < kWords || head == 0 || lane < 31)) {
+                *reinterpret_cast<uint4*>(row + (long long)k1 * x_size(XT)) = make_uint4(u[i], u[i + 1], u[i + 2], u[i + 3]);
+                done = head + (i / 4 + 1) * kEach;
+            }
+        }
+#pragma unroll
+        for (int e = 0; e < 8; ++e)
+            if (k + e < K && (e < head ? !before : e >= done)) x_store(row, XT, k + e, f[e]);
+    }
+};
+
+// A row of each.  The first and the last row of a tensor have its ends.
+template <int XT, bool VEC, int TPR, int NV>
+__device__ __forceinline__ void load_rows(const NormCall& c, long long row, int lane, Piece<XT, VEC> y[NV], Piece<XT, VEC> r[NV], Piece<XT, VEC> gate[NV]) {
+    const int before = (int)min(row * c.K, 8ll), after = (int)min((c.T - 1 - row) * c.K, 8ll);
+    auto at = [&](const void* base, long long ld) { return static_cast<const uint8_t*>(base) + row * ld * x_size(XT); };
+#pragma unroll
+    for (int j = 0; j < NV; ++j) {
+        const int k = 8 * (lane + TPR * j);
+        auto load = [&](auto ends) {
+            constexpr bool kEnds = decltype(ends)::value;
+            y[j].template load<kEnds>(at(c.y, c.ldy), k, -before, c.K + after, c.K);
+            if (c.r) r[j].template load<kEnds>(at(c.r, c.ldr), k, -before, c.K + after, c.K);
+            if (c.gate && c.ldg) gate[j].template load<kEnds>(at(c.gate, c.ldg), k, -before, c.K + after, c.K);
+        };
+        if (Piece<XT, VEC>::ends(before < 8, after < 8, k, c.K)) load(std::true_type());
+        else load(std::false_type());
+        if (c.gate && !c.ldg) gate[j].load_one(c.gate, k, c.K);  // for all rows
+    }
+}
+template <int XT, bool VEC, int TPR, int NV>
+__device__ __forceinline__ void store_row(void* row, int lane, int K, const float f[NV][8]) {
+#pragma unroll
+    for (int j = 0; j < NV; ++j) {
+        Piece<XT, VEC> p;
+        p.store(row, 8 * (lane + TPR * j), K, f[j]);
+    }
+}
+template <int WT, bool VEC>
+__device__ __forceinline__ void weight_piece(const void* weight, int k, int K, float f[8]) {
+    Piece<WT, VEC> p;
+    p.load_one(weight, k, K);
+    p.get(k, K, f);
+}
+// v = v root (offset + weight)
+template <bool VEC, int TPR, int NV>
+__device__ __forceinline__ void weigh(const NormCall& c, const void* weight, float root, int lane, float v[NV][8]) {
 #pragma unroll
     for (int j = 0; j < NV; ++j) {
         float w[8];
-        load8(c.pre, c.wt, 8 * (lane + TPR * j), K, vec, w);
+        const int k = 8 * (lane + TPR * j);
+        if (c.wt == X_F32) weight_piece<X_F32, VEC>(weight, k, c.K, w);
+        else if (c.wt == X_F16) weight_piece<X_F16, VEC>(weight, k, c.K, w);
+        else weight_piece<X_BF16, VEC>(weight, k, c.K, w);
 #pragma unroll
-        for (int e = 0; e < 8; ++e) v[j][e] = v[j][e] * rs * (c.offset + w[e]);
+        for (int e = 0; e < 8; ++e) v[j][e] = v[j][e] * root * (c.offset + w[e]);
     }
-    if (!c.codes) {
-        uint8_t* to = static_cast<uint8_t*>(c.h) + row * c.ldh * x_size(XT);
+}
+
+// TPR threads and NV pieces a row, as in the kernels for many rows, and the same operations in the same order:
+// a row's results depend neither on the kernel nor on the other rows.
+template <int XT, int TPR, int NV, bool VEC>
+__global__ void __launch_bounds__(TPR == 32 ? 64 : TPR) block_norm_kernel(const NormParams p) {
+    constexpr int kRows = TPR == 32 ? 2 : 1;
+    __shared__ float red[3][32];  // an area per reduction
+    grid_dep_launch();
+    const NormCall& c = p.c;
+    const int lane = threadIdx.x % TPR, K = c.K;
+    const long long row = (long long)blockIdx.x * kRows + threadIdx.x / TPR;
+    grid_dep_wait();
+    if (row >= c.T) return;  // whole warps; blocks of one row have theirs
+    Piece<XT, VEC> y[NV], r[NV], gate[NV];
+    float v[NV][8];
+    load_rows<XT, VEC, TPR, NV>(c, row, lane, y, r, gate);
 #pragma unroll
-        for (int j = 0; j < NV; ++j) store8<XT>(to, 8 * (lane + TPR * j), K, vec, v[j]);
+    for (int j = 0; j < NV; ++j) y[j].get(8 * (lane + TPR * j), K, v[j]);
+    if (c.post) {
+        float s0 = 0.0f, s1 = 0.0f;
+#pragma unroll
+        for (int j = 0; j < NV; ++j)
+#pragma unroll
+            for (int e = 0; e < 8; e += 2) {
+                s0 = fmaf(v[j][e], v[j][e], s0);
+                s1 = fmaf(v[j][e + 1], v[j][e + 1], s1);
+            }
+        weigh<VEC, TPR, NV>(c, c.post, root_of(sum_row<TPR>(s0 + s1, red[0]), c), lane, v);
+    }
+    float s0 = 0.0f, s1 = 0.0f;
+#pragma unroll
+    for (int j = 0; j < NV; ++j) {
+        float f[8];
+        if (c.gate) {
+            gate[j].get(8 * (lane + TPR * j), K, f);
+#pragma unroll
+            for (int e = 0; e < 8; ++e) v[j][e] *= f[e];
+        }
+#pragma unroll
+        for (int e = 0; e < 8; ++e) f[e] = 0.0f;
+        if (c.r) r[j].get(8 * (lane + TPR * j), K, f);
+#pragma unroll
+        for (int e = 0; e < 8; e += 2) {
+            v[j][e] = fmaf(c.scale, v[j][e], f[e]);
+            v[j][e + 1] = fmaf(c.scale, v[j][e + 1], f[e + 1]);
+            s0 = fmaf(v[j][e], v[j][e], s0);
+            s1 = fmaf(v[j][e + 1], v[j][e + 1], s1);
+        }
+    }
+    if (c.r_out) store_row<XT, VEC, TPR, NV>(static_cast<uint8_t*>(c.r_out) + row * c.ldro * x_size(XT), lane, K, v);
+    // past the row's end (k >= K) y, r and gate are 0, so the values are; a weight offset does not reach them
+    weigh<VEC, TPR, NV>(c, c.pre, root_of(sum_row<TPR>(s0 + s1, red[1]), c), lane, v);
+    if (!c.codes) {
+        store_row<XT, VEC, TPR, NV>(static_cast<uint8_t*>(c.h) + row * c.ldh * x_size(XT), lane, K, v);
         return;
     }
     uint32_t top = 0;
@@ -164,11 +318,12 @@ __global__ void __launch_bounds__(TPR < 256 ? 256 : TPR) block_norm_kernel(const
     float d, id;
     qc_row_scale(max_row<TPR>(top, reinterpret_cast<uint32_t*>(red[2])), d, id);
     int8_t* to = c.codes + row * c.ldh;
+    const bool whole = (reinterpret_cast<uintptr_t>(to) & 7) == 0;
 #pragma unroll
     for (int j = 0; j < NV; ++j) {
         const int k = 8 * (lane + TPR * j);
         const uint2 u = qc_codes8(v[j], id);
-        if (vec && k + 8 <= K) {
+        if ((VEC || whole) && k + 8 <= K) {
             *reinterpret_cast<uint2*>(to + k) = u;
         } else {
 #pragma unroll
@@ -260,7 +415,6 @@ __device__ __forceinline__ float squares(const Raw8<XT> y[NV]) {
     }
     return f2lo(ss) + f2hi(ss);
 }
-__device__ __forceinline__ float root_of(float ss, const NormCall& c) { return 1.0f / sqrtf(fmaf(ss, 1.0f / (float)c.K, c.eps)); }
 
 // One row, from its values to the outputs.  root: 1 / sqrt(mean(y^2) + eps) of this row; AHEAD: becomes that of
 // the next one, whose y next() gives (before the barrier): the sums of r'^2 and of the next y^2 are one
@@ -298,7 +452,7 @@ __device__ __forceinline__ void norm_row(const NormCall& c, long long row, int l
         for (int j = 0; j < NV; ++j) {
             float f[8];
             unpack8(v[j], f);
-            if (8 * (lane + TPR * j) < c.K) store8<XT>(to, 8 * (lane + TPR * j), c.K, true, f);
+            if (8 * (lane + TPR * j) < c.K) store8<XT>(to, 8 * (lane + TPR * j), c.K, f);
         }
     }
     next(y);
@@ -321,7 +475,7 @@ __device__ __forceinline__ void norm_row(const NormCall& c, long long row, int l
         float h[8];
         unpack8(v[j], h);
         if (!c.codes) {
-            if (on) store8<XT>(to, 8 * (lane + TPR * j), c.K, true, h);
+            if (on) store8<XT>(to, 8 * (lane + TPR * j), c.K, h);
         } else if (on) {
 #pragma unroll
             for (int e = 0; e < 8; ++e) top = max(top, qc_abs_bits(h[e]));
@@ -501,11 +655,16 @@ cudaError_t warps_one(const NormCall& c, int sms, cudaStream_t s) {
     return launch_pdl(norm_warps_kernel<XT, WT, NV, POST, GATE>, (unsigned)(rows < most ? rows : most), 256, 0, s, c);
 }
 
+// A warp a row while its values fit the registers, which is up to 768 of 16 bits and 256 of f32 (rows of 576: 4323
+// in f16 8.2 us, with a ring of 128 threads 9.7; in f32 24 and 13); then blocks of as many threads as a row has
+// pieces, but for 16-bit rows of 4096 two pieces each (4096 rows 25.1 us, with 512 threads 27.6; in f32 53.6 and 49.4).
 template <int XT, int WT, bool POST, bool GATE>
 cudaError_t many_go(const NormCall& c, int sms, int smem_max, unsigned* err, cudaStream_t s) {
     if (c.K <= 256) return warps_one<XT, WT, 1, POST, GATE>(c, sms, s);
-    if (c.K <= 512) return warps_one<XT, WT, 2, POST, GATE>(c, sms, s);
-    if (c.K <= 768) return warps_one<XT, WT, 3, POST, GATE>(c, sms, s);
+    if constexpr (XT != X_F32) {
+        if (c.K <= 512) return warps_one<XT, WT, 2, POST, GATE>(c, sms, s);
+        if (c.K <= 768) return warps_one<XT, WT, 3, POST, GATE>(c, sms, s);
+    }
     if (c.K <= 1024) return ring_one<XT, WT, 128, 1, POST, GATE>(c, sms, smem_max, err, s);
     if (c.K <= 2048) return ring_one<XT, WT, 256, 1, POST, GATE>(c, sms, smem_max, err, s);
     if (c.K <= 4096) {
@@ -519,23 +678,45 @@ cudaError_t many(const NormCall& c, int sms, int smem_max, unsigned* err, cudaSt
     if (c.post) return c.gate ? many_go<XT, WT, true, true>(c, sms, smem_max, err, s) : many_go<XT, WT, true, false>(c, sms, smem_max, err, s);
     return c.gate ? many_go<XT, WT, false, true>(c, sms, smem_max, err, s) : many_go<XT, WT, false, false>(c, sms, smem_max, err, s);
 }
+template <int XT, int TPR, int NV, bool VEC>
+cudaError_t few_one(const NormParams& p, cudaStream_t s) {
+    constexpr int rows = TPR == 32 ? 2 : 1;
+    return launch_pdl(block_norm_kernel<XT, TPR, NV, VEC>, (unsigned)((p.c.T + (long long)rows - 1) / rows), TPR * rows, 0, s, p);
+}
+template <int XT, bool VEC>
+cudaError_t few(const NormParams& p, cudaStream_t s) {  // threads and pieces: many_go's
+    const int K = p.c.K;
+    if (K <= 256) return few_one<XT, 32, 1, VEC>(p, s);
+    if constexpr (XT != X_F32) {
+        if (K <= 512) return few_one<XT, 32, 2, VEC>(p, s);
+        if (K <= 768) return few_one<XT, 32, 3, VEC>(p, s);
+    }
+    if (K <= 1024) return few_one<XT, 128, 1, VEC>(p, s);
+    if (K <= 2048) return few_one<XT, 256, 1, VEC>(p, s);
+    if (K <= 4096) {
+        if constexpr (XT == X_F32) return few_one<XT, 512, 1, VEC>(p, s);
+        else return few_one<XT, 256, 2, VEC>(p, s);
+    }
+    if (K <= 8192) return few_one<XT, 1024, 1, VEC>(p, s);
+    return few_one<XT, 1024, 4, VEC>(p, s);
+}
 
+// Rows of up to 4096 (f32: 256) go to the kernels for many rows however few they are, longer ones from two an SM on
+// (block_norm_kernel / those, us, norm on both sides): bf16 1 x 576 3.8 / 2.1, 611 x 576 4.3 / 2.7, 16 x 4096 3.3 / 2.6,
+// 304 x 4096 5.5 / 4.8, 152 x 8192 4.9 / 5.1, 304 x 8192 9.2 / 7.4; f32 1216 x 256 2.6 / 2.2, 16 x 2048 2.4 / 2.6,
+// 304 x 2048 5.1 / 4.4, 4323 x 576 18 / 13, 64 x 8192 5.0 / 6.0.
 template <int XT>
 cudaError_t norm_go(const NormParams& p, cudaStream_t s) {
     const int K = p.c.K;
-    const unsigned T = (unsigned)p.c.T;
     int sms = 0, smem = 0;
     unsigned* err = nullptr;
     const cudaError_t e = device_constants(&err, &sms, &smem);
     if (e != cudaSuccess) return e;
-    if (p.vec && K % 8 == 0 && K <= 8192 && (long long)T * K >= (long long)sms * 16384) {
+    if (p.vec && K % 8 == 0 && K <= 8192 && (K <= (XT == X_F32 ? 256 : 4096) || p.c.T >= 2 * sms)) {
         if (p.c.wt == XT) return many<XT, XT>(p.c, sms, smem, err, s);
         if (p.c.wt == X_F32) return many<XT, X_F32>(p.c, sms, smem, err, s);
     }
-    if (K <= 2048) return launch_pdl(block_norm_kernel<XT, 256, 1>, T, 256, 0, s, p);
-    if (K <= 4096) return launch_pdl(block_norm_kernel<XT, 256, 2>, T, 256, 0, s, p);
-    if (K <= 8192) return launch_pdl(block_norm_kernel<XT, 1024, 1>, T, 1024, 0, s, p);
-    return launch_pdl(block_norm_kernel<XT, 1024, 4>, T, 1024, 0, s, p);
+    return p.vec ? few<XT, true>(p, s) : few<XT, false>(p, s);
 }
 
 }  // namespace

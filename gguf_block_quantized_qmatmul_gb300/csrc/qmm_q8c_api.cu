@@ -132,6 +132,7 @@ qmm_status qmm_block_norm(const qmm_norm* n, int64_t T, int64_t K, qmm_stream_t 
         return QMM_ERR_SHAPE;
     if (T == 0) return QMM_OK;
     if (!n->y || !n->weight || (n->h == nullptr) == (n->codes == nullptr) || (n->codes && !n->scales)) return QMM_ERR_NULL;
+    if (n->h && n->h == n->residual_out) return QMM_ERR_SHAPE;  // two results, one place
     const uintptr_t a = (uintptr_t)x_size((int)n->type), wa = (uintptr_t)x_size((int)n->weight_type);
     if (!aligned(n->y, a) || !aligned(n->residual, a) || !aligned(n->gate, a) || !aligned(n->post_weight, wa) || !aligned(n->weight, wa) ||
         !aligned(n->residual_out, a) || !aligned(n->h, a) || !aligned(n->scales, 4))

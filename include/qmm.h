@@ -464,7 +464,8 @@ qmm_status qmm_q8c_matmul(const qmm_q8c* w, qmm_float xtype, const void* x, int6
    are of `type`, the weights of weight_type.  Rows are ld* elements apart
    (gate: 0 for one row for all).  residual_out may be residual or y, h may be y
    or residual: a row is read whole before it is written; otherwise outputs
-   overlap nothing.  Rows need no alignment beyond their elements'.
+   overlap nothing (both in one place: SHAPE).  Rows need no alignment beyond
+   their elements'.
    Errors: NULL, TYPE, SHAPE, ALIGN, CUDA. */
 #define QMM_NORM_MAX_K 32768
 typedef struct {

@@ -157,6 +157,48 @@ def test_stream_graph_and_empty(q):
     assert e[0].shape == e[1].shape == (0, 640)
 
 
+@pytest.mark.parametrize("K", [1, 31, 200, 256, 400, 577, 760, 1000, 2041, 4096, 5000, 9000])
+@pytest.mark.parametrize("dt,wdt", [("f32", "f32"), ("f16", "f32"), ("bf16", "bf16"), ("bf16", "f16")])
+def test_a_row_does_not_depend_on_its_place(q, K, dt, wdt):
+    """The same bits on every kernel: beside many rows or few, on any alignment, in any row."""
+    T = max(700, 5000 // K)
+    t = {k: v.cuda() for k, v in make(T, K, dt, wdt, gate="token").items()}
+    r, h = q.block_norm(**t, scale=0.7)
+    cr, rows = q.block_norm(**t, scale=0.7, quantize=True)
+    assert torch.equal(cr, r)
+    per_row = ("y", "residual", "gate")
+    for first, n in ((0, 1), (3, 1), (T - 7, 7), (5, 300)):
+        for extra, shift in ((0, 0), (8 - K % 8 + 8, 8), (3, 1)):
+            some = dict(t)
+            for k in per_row:
+                wide = torch.full((n, K + extra), 3.0, dtype=DT[dt], device="cuda")
+                some[k] = wide[:, shift:shift + K]
+                some[k].copy_(t[k][first:first + n])
+            if shift == 1:
+                for k in ("weight", "post_weight"):
+                    some[k] = torch.cat([t[k][:1], t[k]])[1:]
+            a, b = q.block_norm(**some, scale=0.7)
+            assert torch.equal(a, r[first:first + n]) and torch.equal(b, h[first:first + n])
+            a, b = q.block_norm(**some, scale=0.7, quantize=True)
+            assert torch.equal(a, r[first:first + n]) and torch.equal(b.codes, rows.codes[first:first + n]) and torch.equal(b.scales, rows.scales[first:first + n])
+
+
+def test_offsets_past_32_bits(q):
+    """More than 2^31 values, and rows far apart: rows around the boundary against calls of their own."""
+    T, K = 530000, 4096
+    y = torch.empty((T, K), dtype=torch.bfloat16, device="cuda").normal_(generator=torch.Generator("cuda").manual_seed(1))
+    w = torch.rand(K, device="cuda").bfloat16()
+    r, h = q.block_norm(y, w, residual=y, post_weight=w)
+    for t in (0, 2 ** 31 // K - 2, T - 4):
+        a, b = q.block_norm(y[t:t + 4], w, residual=y[t:t + 4], post_weight=w)
+        assert torch.equal(r[t:t + 4], a) and torch.equal(h[t:t + 4], b)
+    del r, h
+    far = y.view(-1).as_strided((60, 576), (1 << 25, 1))
+    a, b = q.block_norm(far, w[:576])
+    near = q.block_norm(far.clone(), w[:576])
+    assert torch.equal(a, near[0]) and torch.equal(b, near[1])
+
+
 def test_refusals(q):
     t = {k: v.cuda() for k, v in make(4, 64, "f16", "f32").items()}
     for bad in (dict(y=t["y"].float()), dict(y=t["y"][:3]), dict(weight=t["weight"][:63]), dict(post_weight=t["weight"].half()), dict(gate=t["gate"].float()),
@@ -164,6 +206,9 @@ def test_refusals(q):
                 dict(residual_out=t["y"].t()), dict(out=t["y"], quantize=True), dict(y=t["y"].t())):
         with pytest.raises(ValueError):
             q.block_norm(**{**t, **bad})
+    with pytest.raises(q.QmmError) as e:  # both results in one place
+        q.block_norm(**t, out=t["y"], residual_out=t["y"])
+    assert e.value.status == 2
     with pytest.raises(q.QmmError) as e:
         x = torch.zeros((1, 32769), device="cuda")
         q.block_norm(x, x[0])
