@@ -88,7 +88,8 @@ MoePlan plan_moe_layer(const MoeCall& c, int sms, int smem_max) {
     const int route = round_up((6 * S + 3 * E) * 4, 16);
     const int room = smem_max - kMoeStatic - 1024 - 16 - kMoePart - ring - route;
     const long long up_row = (long long)np * c.up.KS * 256, down_row = (long long)(np == 3 ? 3 : 2) * c.down.KS * 256;  // a token's, a slot's staged bytes
-    // a token's second products end to end while few tokens share an expert: no partial sums to add later
+    // A token's second products end to end while few tokens share an expert: no partial sums to add later.  (1, 2, 4
+    // tokens of 64 experts: 20.4, 25.6, 35.9 us; by expert 21.0, 27.0, 36.7.)
     pl.token = T <= 4 && k * down_row <= room;
     pl.whole = T * up_row <= room;
     // tokens per item: the MMA's columns, or what fits shared memory, a power of two

@@ -172,7 +172,7 @@ def block_norm(y: torch.Tensor, weight: torch.Tensor, residual: torch.Tensor | N
     v = y / sqrt(mean(y^2) + eps) (weight_offset + post_weight), or y; r' = residual + scale gate v;
     h = r' / sqrt(mean(r'^2) + eps) (weight_offset + weight), as floats or, with quantize, as Rows8.
     gate: [K] or [T, K] of y's type.  weights: [K], both of one type.  out and residual_out may be y or residual, not both the same.
-    Small results (64 KB) share one allocation."""
+    Small results (256 KB) share one allocation, as do codes and their scales."""
     if stream is not None:
         with _on(y.get_device(), stream):
             return block_norm(y, weight, residual, post_weight, gate, scale, eps, weight_offset, quantize, out, residual_out)
