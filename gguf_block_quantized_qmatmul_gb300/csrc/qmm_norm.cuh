@@ -206,24 +206,20 @@ struct Piece {
     }
 };
 
-// A row of each.  The first and the last row of a tensor have its ends.
-template <int XT, bool VEC, int TPR, int NV>
-__device__ __forceinline__ void load_rows(const NormCall& c, long long row, int lane, Piece<XT, VEC> y[NV], Piece<XT, VEC> r[NV], Piece<XT, VEC> gate[NV]) {
-    const int before = (int)min(row * c.K, 8ll), after = (int)min((c.T - 1 - row) * c.K, 8ll);
+// Piece j of a row of y (Y), of residual and gate (RG).  The first and the last row of a tensor have its ends.
+template <bool Y, bool RG, int XT, bool VEC, int TPR>
+__device__ __forceinline__ void load_piece(const NormCall& c, long long row, int lane, int j, Piece<XT, VEC>& y, Piece<XT, VEC>& r, Piece<XT, VEC>& gate) {
+    const int before = (int)min(row * c.K, 8ll), after = (int)min((c.T - 1 - row) * c.K, 8ll), k = 8 * (lane + TPR * j);
     auto at = [&](const void* base, long long ld) { return static_cast<const uint8_t*>(base) + row * ld * x_size(XT); };
-#pragma unroll
-    for (int j = 0; j < NV; ++j) {
-        const int k = 8 * (lane + TPR * j);
-        auto load = [&](auto ends) {
-            constexpr bool kEnds = decltype(ends)::value;
-            y[j].template load<kEnds>(at(c.y, c.ldy), k, -before, c.K + after, c.K);
-            if (c.r) r[j].template load<kEnds>(at(c.r, c.ldr), k, -before, c.K + after, c.K);
-            if (c.gate && c.ldg) gate[j].template load<kEnds>(at(c.gate, c.ldg), k, -before, c.K + after, c.K);
-        };
-        if (Piece<XT, VEC>::ends(before < 8, after < 8, k, c.K)) load(std::true_type());
-        else load(std::false_type());
-        if (c.gate && !c.ldg) gate[j].load_one(c.gate, k, c.K);  // for all rows
-    }
+    auto load = [&](auto ends) {
+        constexpr bool kEnds = decltype(ends)::value;
+        if (Y) y.template load<kEnds>(at(c.y, c.ldy), k, -before, c.K + after, c.K);
+        if (RG && c.r) r.template load<kEnds>(at(c.r, c.ldr), k, -before, c.K + after, c.K);
+        if (RG && c.gate && c.ldg) gate.template load<kEnds>(at(c.gate, c.ldg), k, -before, c.K + after, c.K);
+    };
+    if (Piece<XT, VEC>::ends(before < 8, after < 8, k, c.K)) load(std::true_type());
+    else load(std::false_type());
+    if (RG && c.gate && !c.ldg) gate.load_one(c.gate, k, c.K);  // for all rows
 }
 template <int XT, bool VEC, int TPR, int NV>
 __device__ __forceinline__ void store_row(void* row, int lane, int K, const float f[NV][8]) {
@@ -266,9 +262,11 @@ __global__ void __launch_bounds__(TPR == 32 ? 64 : TPR) block_norm_kernel(const 
     const long long row = (long long)blockIdx.x * kRows + threadIdx.x / TPR;
     grid_dep_wait();
     if (row >= c.T) return;  // whole warps; blocks of one row have theirs
+    constexpr bool kLate = NV > 3;  // residual and gate where they are used, as registers do not hold them (16 x 14336 bf16 8.2 us, with spills 12)
     Piece<XT, VEC> y[NV], r[NV], gate[NV];
     float v[NV][8];
-    load_rows<XT, VEC, TPR, NV>(c, row, lane, y, r, gate);
+#pragma unroll
+    for (int j = 0; j < NV; ++j) load_piece<true, !kLate, XT, VEC, TPR>(c, row, lane, j, y[j], r[j], gate[j]);
 #pragma unroll
     for (int j = 0; j < NV; ++j) y[j].get(8 * (lane + TPR * j), K, v[j]);
     if (c.post) {
@@ -286,6 +284,7 @@ __global__ void __launch_bounds__(TPR == 32 ? 64 : TPR) block_norm_kernel(const 
 #pragma unroll
     for (int j = 0; j < NV; ++j) {
         float f[8];
+        if (kLate) load_piece<false, true, XT, VEC, TPR>(c, row, lane, j, y[j], r[j], gate[j]);
         if (c.gate) {
             gate[j].get(8 * (lane + TPR * j), K, f);
 #pragma unroll
@@ -698,6 +697,7 @@ cudaError_t few(const NormParams& p, cudaStream_t s) {  // threads and pieces: m
         else return few_one<XT, 256, 2, VEC>(p, s);
     }
     if (K <= 8192) return few_one<XT, 1024, 1, VEC>(p, s);
+    if (K <= 16384) return few_one<XT, 1024, 2, VEC>(p, s);  // 16 x 14336 bf16 5.0 us, with four pieces 8.2
     return few_one<XT, 1024, 4, VEC>(p, s);
 }
 
