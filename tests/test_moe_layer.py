@@ -145,6 +145,21 @@ def test_tokens_that_agree_and_masked_experts(q):
     assert ((y.double().cpu() - ref).abs() <= tol).all()
 
 
+@pytest.mark.parametrize("dt,rdt", [("bf16", "f32"), ("f16", "bf16"), ("f32", "bf16"), ("f32", "f16")])
+@pytest.mark.parametrize("T", [1, 3, 11])
+def test_routers_of_other_types(q, T, dt, rdt):
+    E, K, F, N, k = 24, 192, 64, 96, 3
+    up, wu, down, wd, x, _ = make(q, T, E, K, F, N, 64, 64, dt)
+    router = (torch.randint(-8, 9, (E, K), generator=rng(4)) / 64).to(DT[rdt])  # exact in each
+    y, r = q.moe_layer(up, down, router.cuda(), x.cuda(), k, route=True)
+    l = x.double() @ router.double().T
+    best = l.sort(1, descending=True).values[:, :k]
+    err = (K * 2.0 ** -24 * (x.double().abs() @ router.double().abs().T)).max()
+    assert ((l.gather(1, r.ids.cpu().long()) - best).abs() <= 2 * err).all()
+    ref, tol = exact(x, r.ids.cpu(), r.weights.cpu(), wu, wd, dt)
+    assert ((y.double().cpu() - ref).abs() <= tol).all()
+
+
 def test_bad_tokens_stay_to_themselves(q):
     T, E, K, F, N, k = 7, 16, 128, 64, 128, 3
     up, _, down, _, x, router = make(q, T, E, K, F, N, 64, 64, "f32")

@@ -278,11 +278,35 @@ def test_in_a_graph_and_on_a_stream(q, M):
     assert torch.equal(z, 2 * y)
 
 
+@pytest.mark.parametrize("M,N,K", [(2, 2000, 4096), (4, 500, 9000), (40, 1000, 8192), (300, 2000, 1024)])
+def test_calls_at_once(q, M, N, K):
+    """On two streams, and a captured call replayed beside an eager one: each has a workspace of its own."""
+    _, _, w = weights(q, N, K)
+    xs = [torch.randn((M, K), generator=rng(i)).half().cuda() for i in range(3)]
+    ref = [q.q8c_matmul(w, x) for x in xs]
+    g = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(g):
+        z = q.q8c_matmul(w, xs[2])
+    sides = [torch.cuda.Stream() for _ in range(3)]
+    torch.cuda.synchronize()
+    got = []
+    for _ in range(20):
+        got += [(i, q.q8c_matmul(w, xs[i], stream=sides[i])) for i in range(2)]
+        with torch.cuda.stream(sides[2]):
+            z.zero_()
+            g.replay()
+    torch.cuda.synchronize()
+    assert all(torch.equal(y, ref[i]) for i, y in got) and torch.equal(z, ref[2])
+    assert q.last_device_error() == 0
+
+
 def test_empty(q):
     _, _, w = weights(q, 64, 128)
     assert q.q8c_matmul(w, torch.empty((0, 128), device="cuda")).shape == (0, 64)
     e = q.q8c_pack(torch.empty((0, 128), dtype=torch.int8, device="cuda"), torch.empty(0, device="cuda"))
     assert q.q8c_matmul(e, torch.ones((3, 128), device="cuda")).shape == (3, 0)
+    r = q.q8c_quantize(torch.empty((0, 128), device="cuda"))
+    assert r.codes.shape == (0, 128) and q.q8c_matmul(w, r).shape == (0, 64)
     assert q.q8c_quantize(torch.empty((0, 5), device="cuda")).codes.shape == (0, 5)
 
 
