@@ -462,7 +462,8 @@ qmm_status qmm_q8c_matmul(const qmm_q8c* w, qmm_float xtype, const void* x, int6
    the latter quantized row by row as qmm_q8c_matmul does.  h is made of r'
    before that is rounded to its type.  y, residual, gate, residual_out and h
    are of `type`, the weights of weight_type.  Rows are ld* elements apart
-   (gate: 0 for one row for all).  residual_out may be residual or y, h may be y
+   (gate: 0 for one row for all).  A row's results depend neither on T nor on
+   where the rows are.  residual_out may be residual or y, h may be y
    or residual: a row is read whole before it is written; otherwise outputs
    overlap nothing (both in one place: SHAPE).  Rows need no alignment beyond
    their elements'.
