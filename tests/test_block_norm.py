@@ -114,6 +114,20 @@ def test_rows_apart_in_place_and_canary(q):
     assert torch.equal(t["residual"], r) and torch.equal(t["y"], h)
 
 
+@pytest.mark.parametrize("T,K", [(1, 577), (9, 577), (300, 1001), (5, 5001), (3, 14336), (7, 20001), (2, 28672), (400, 9)])
+@pytest.mark.parametrize("dt", list(DT))
+def test_in_place(q, T, K, dt):
+    """r' and h where y and the residual were, rows that share words among them."""
+    t = {k: v.cuda() for k, v in make(T, K, dt, "f32", gate="token").items()}
+    r, h = q.block_norm(**t, scale=0.7)
+    c = {k: v.clone() for k, v in t.items()}
+    q.block_norm(**c, scale=0.7, residual_out=c["residual"], out=c["y"])
+    assert torch.equal(c["residual"], r) and torch.equal(c["y"], h)
+    c = {k: v.clone() for k, v in t.items()}
+    q.block_norm(**c, scale=0.7, residual_out=c["y"], out=c["residual"])
+    assert torch.equal(c["y"], r) and torch.equal(c["residual"], h)
+
+
 def test_rows_that_are_not_finite(q):
     t = {k: v.cuda() for k, v in make(5, 300, "f32", "f32").items()}
     r, h = q.block_norm(**t)
