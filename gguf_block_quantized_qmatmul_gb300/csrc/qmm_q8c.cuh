@@ -192,6 +192,11 @@ struct QcGemmPlan {
     size_t smem = 0, ws_scale = 0, ws_norm = 0, ws_part = 0, workspace = 0;
 };
 QcGemmPlan plan_q8c_gemm(const QcCall& c, int sms, int smem_max);
+// Whether 16-bit results may be stored four neighbours of a row at a time, 8 bytes: y itself is aligned only as its
+// elements are, and rows follow each other without a gap.
+inline bool qc_wide_results(const QcCall& c, int ks) {
+    return c.yt != X_F32 && ks == 1 && c.w.N % 4 == 0 && (reinterpret_cast<uintptr_t>(c.y) & 7) == 0;
+}
 cudaError_t launch_q8c_gemm(const QcGemmPlan& pl, const QcCall& c, void* ws, unsigned* err, int stall, int smem_max, cudaStream_t s);
 
 // Norms around a block; see include/qmm.h (qmm_block_norm).

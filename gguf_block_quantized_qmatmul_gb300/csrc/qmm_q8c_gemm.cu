@@ -59,6 +59,7 @@ struct GemmParams {
     int bx, nacc, accw, mtiles, ntiles, nraw, nx, nstage, ks;
     int ktiles;             // tiles in K
     int off_raw, off_bar;
+    int wide;               // qc_wide_results
     int stall;
     unsigned stall_block;
 };
@@ -303,10 +304,10 @@ __global__ void __launch_bounds__(kQgThreads, 1) q8c_gemm_kernel(const __grid_co
                 for (int i = 0; i < kWords; ++i) table[32 * i + lane] = xs_next[i];
                 __syncwarp();
                 if (u + unit_step < units) ask(place(u + unit_step));
-                // 16-bit results go to memory four at a time, of four rows: a quad of lanes exchanges its 4 x 8 values
+                // 16-bit results go to memory four at a time where their place allows it, of four rows: a quad of lanes exchanges its 4 x 8 values
                 // (a store a value and column took three times as long).  What a chunk needs is worked out before it:
                 // this warp's chunks are 16 columns apart, and the kind of result is told apart outside of them.
-                const bool wide = w.N % 4 == 0 && p.ks == 1 && c.yt != X_F32;
+                const bool wide = p.wide;
                 const int sub = wide ? 2 * (lane & 3) : 0;  // the first of the columns that this lane writes
                 const long long first = (long long)(un.p0 + kCols * part + sub) * w.N + n - (wide ? lane & 3 : 0) + (p.ks > 1 ? (long long)un.split * M * w.N : 0);
                 const long long stride = (long long)kEpiHalves * kCols * w.N;
@@ -635,6 +636,7 @@ cudaError_t launch_q8c_gemm(const QcGemmPlan& pl, const QcCall& c, void* ws, uns
     p.nx = pl.nx;
     p.nstage = pl.nstage;
     p.ks = pl.ks;
+    p.wide = qc_wide_results(c, pl.ks);
     p.stall = stall;
     p.stall_block = (unsigned)pl.cg - 1u;  // of a pair the second one, whose partner finds out by its own waits
     p.ktiles = (c.w.KS + pl.kt - 1) / pl.kt;

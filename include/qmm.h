@@ -444,7 +444,8 @@ qmm_status qmm_q8c_quantize(qmm_float xtype, const void* x, int64_t ldx, int64_t
 
 /* The product.  x: floats of xtype, or, with x_scales (f32 [M]), int8 codes
    (xtype is then not read); rows ldx elements apart, aligned as their elements
-   are.  bias: f32 [N] or NULL.  y [M, N] of ytype, contiguous.
+   are.  bias: f32 [N] or NULL.  y [M, N] of ytype, contiguous, aligned as its
+   elements are.
    workspace: qmm_q8c_matmul_workspace(w, x_scales != NULL, M) bytes,
    uninitialised; calls that may overlap need one each.  None is needed for up
    to QMM_Q8C_DIRECT_ROWS rows that start on 16-byte boundaries, of K <= 32768 in
