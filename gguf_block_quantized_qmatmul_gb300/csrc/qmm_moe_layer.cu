@@ -33,8 +33,9 @@ __device__ __forceinline__ void router_load8(const void* row, int type, int k, f
 }
 
 // Logits of four tokens for one expert a block: f32 products and sums in a fixed order.  Bound by
-// latency: the router's row, constant, is asked for before what this grid depends on has completed, the
-// tokens' values after it, all at once; one reduction.  (A block for all tokens of an expert: 9 us for 16.)
+// latency: the router's row is asked into L2 before what this grid depends on has completed, and read after it, as
+// the router is a caller's floats, which that may write; with it the tokens' values, all at once; one reduction.
+// (A block for all tokens of an expert: 9 us for 16.)
 // The first block clears the next launch's counters.
 constexpr int kRouterTokens = 4;
 __global__ void __launch_bounds__(256) moe_router_kernel(const void* x, int xt, long long ldx, int T, int K, const void* router, int rt, float* logits, int ldl,
@@ -42,11 +43,12 @@ __global__ void __launch_bounds__(256) moe_router_kernel(const void* x, int xt, 
     __shared__ float red[kRouterTokens][8];
     const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31, e = blockIdx.x, t0 = blockIdx.y * kRouterTokens;
     const uint8_t* w = static_cast<const uint8_t*>(router) + (long long)e * K * x_size(rt);
-    float f[8];
-    if (8 * tid < K) router_load8(w, rt, 8 * tid, f);
+    for (int k = 8 * tid; k < K; k += 2048) asm volatile("prefetch.global.L2 [%0];" ::"l"(w + (long long)k * x_size(rt)));
     // the next launch reads x before this one has completed: it may start only now that x is there
     grid_dep_wait();
     grid_dep_launch();
+    float f[8];
+    if (8 * tid < K) router_load8(w, rt, 8 * tid, f);
     if (e == 0 && t0 == 0 && tid < 4) counters[tid] = 0u;
     float acc[kRouterTokens];
 #pragma unroll
