@@ -12,12 +12,12 @@ namespace {
 
 __device__ __forceinline__ void router_load8(const void* row, int type, int k, float f[8]) {
     if (type == X_F32) {
-        const float4 a = __ldg(reinterpret_cast<const float4*>(static_cast<const float*>(row) + k));
-        const float4 b = __ldg(reinterpret_cast<const float4*>(static_cast<const float*>(row) + k) + 1);
+        const float4 a = *reinterpret_cast<const float4*>(static_cast<const float*>(row) + k);
+        const float4 b = *(reinterpret_cast<const float4*>(static_cast<const float*>(row) + k) + 1);
         f[0] = a.x, f[1] = a.y, f[2] = a.z, f[3] = a.w, f[4] = b.x, f[5] = b.y, f[6] = b.z, f[7] = b.w;
         return;
     }
-    const uint4 u = __ldg(reinterpret_cast<const uint4*>(static_cast<const uint16_t*>(row) + k));
+    const uint4 u = *reinterpret_cast<const uint4*>(static_cast<const uint16_t*>(row) + k);
     const uint32_t w[4] = {u.x, u.y, u.z, u.w};
 #pragma unroll
     for (int i = 0; i < 4; ++i) {

@@ -125,7 +125,7 @@ __device__ __forceinline__ int route_token(const RouteParams& p, long long tok, 
             for (int i = 0; i < EPL; ++i) b[i] = __uint_as_float(w[i]);
         } else {
 #pragma unroll
-            for (int i = 0; i < EPL; ++i) b[i] = e0 + i < c.E ? __ldg(c.bias + e0 + i) : 0.0f;
+            for (int i = 0; i < EPL; ++i) b[i] = e0 + i < c.E ? c.bias[e0 + i] : 0.0f;
         }
 #pragma unroll
         for (int i = 0; i < EPL; ++i) key[i] = pick_key(score[i] + b[i]);

@@ -208,12 +208,12 @@ __global__ void __launch_bounds__(kQgThreads, 1) q8c_gemm_kernel(const __grid_co
     } else if (warp < kConv0) {
         // whether a sum may pass 2^24: the epilogue's and the MMAs' warps look for themselves
         grid_dep_wait();
+        const uint32_t wnorm = __ldg(reinterpret_cast<const uint32_t*>(w.data + w.norm_off));
         uint32_t top = 0;
-        for (int i = (warp == 1 ? 0 : warp - kQgEpi0 + 1) * 32 + lane; i < M; i += (kEpiWarps + 1) * 32) top = max(top, __ldg(p.xn + i));
+        for (int i = (warp == 1 ? 0 : warp - kQgEpi0 + 1) * 32 + lane; i < M; i += (kEpiWarps + 1) * 32) top = max(top, p.xn[i]);
         top = __reduce_max_sync(0xffffffffu, top);
         if (lane == 0) atomicMax(s_norm, top);
         asm volatile("bar.sync 1, %0;" ::"n"((kEpiWarps + 1) * 32) : "memory");
-        const uint32_t wnorm = __ldg(reinterpret_cast<const uint32_t*>(w.data + w.norm_off));
         const bool restart = (unsigned long long)*reinterpret_cast<volatile uint32_t*>(s_norm) * wnorm >= 1ull << 48;
         const int chunk = restart ? kRestart / KT : p.ktiles;
         if (warp == 1) {
@@ -285,11 +285,11 @@ __global__ void __launch_bounds__(kQgThreads, 1) q8c_gemm_kernel(const __grid_co
             auto ask = [&](const Unit& un) {
                 const int n = (8 * un.nt + 2 * q) * 16 + lane;
                 wn_next = n < w.N ? __ldg(sw + n) : 0.0f;
-                bias_next = c.bias && n < w.N ? __ldg(c.bias + n) : 0.0f;
+                bias_next = c.bias && n < w.N ? c.bias[n] : 0.0f;
 #pragma unroll
                 for (int i = 0; i < kWords; ++i) {
                     const int m = kCols * (part + kEpiHalves * (4 * i + (lane >> 3))) + (lane & 7);
-                    xs_next[i] = m < un.n ? __ldg(p.xs + un.p0 + m) : 0.0f;
+                    xs_next[i] = m < un.n ? p.xs[un.p0 + m] : 0.0f;
                 }
             };
             if (first_unit < units) ask(place(first_unit));
@@ -509,6 +509,7 @@ __global__ void __launch_bounds__(256) q8c_sum_kernel(const int* part, int ks, i
     const int n = blockIdx.x * 256 + threadIdx.x, m = blockIdx.y;
     if (n >= N) return;
     const long long all = (long long)M * N, i = (long long)m * N + n;
+    const float wn = __ldg(sw + n), sx = xs[m], b = bias ? bias[n] : 0.0f;  // on their way beside the sums
     int v = 0;
     for (int s0 = 0; s0 < ks; s0 += 4) {
         int u[4];
@@ -517,7 +518,7 @@ __global__ void __launch_bounds__(256) q8c_sum_kernel(const int* part, int ks, i
 #pragma unroll
         for (int s = 0; s < 4; ++s) v += u[s];
     }
-    x_store(y, yt, i, qc_scale((float)v, __ldg(sw + n), __ldg(xs + m), bias ? __ldg(bias + n) : 0.0f));
+    x_store(y, yt, i, qc_scale((float)v, wn, sx, b));
 }
 
 template <int CG, int KT>

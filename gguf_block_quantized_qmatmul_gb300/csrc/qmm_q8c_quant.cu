@@ -92,7 +92,7 @@ __global__ void __launch_bounds__(TPR < 256 ? 256 : TPR) q8c_prep_kernel(const P
         if constexpr (XT == X_CODES) {
             const int k = 8 * i;
             if (q.vec && k + 8 <= q.K) {
-                u = __ldg(reinterpret_cast<const uint2*>(x + k));
+                u = *reinterpret_cast<const uint2*>(x + k);
             } else {
 #pragma unroll
                 for (int e = 0; e < 8; ++e) {

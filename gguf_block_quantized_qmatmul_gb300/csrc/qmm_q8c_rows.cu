@@ -81,8 +81,8 @@ __device__ __forceinline__ void stage_floats(uint8_t* sm, float* scale, uint32_t
                     u[j][0] = u[j][1] = make_uint4(0u, 0u, 0u, 0u);
                     if (i >= n || k >= K) continue;
                     const uint4* from = reinterpret_cast<const uint4*>(x + (r * p.c.a.ld + k) * x_size(XT));
-                    u[j][0] = __ldg(from);
-                    if (XT == X_F32) u[j][1] = __ldg(from + 1);
+                    u[j][0] = *from;
+                    if (XT == X_F32) u[j][1] = from[1];
                 }
             }
 #pragma unroll
@@ -121,7 +121,7 @@ __device__ __forceinline__ void stage_codes(uint8_t* sm, float* scale, const Row
         for (int j = 0; j < 4; ++j) {
             const int i = i0 + j * nthr + tid, r = i / n16, k = 16 * (i - r * n16);
             v[j] = make_uint4(0u, 0u, 0u, 0u);
-            if (i < n && k < p.kx) v[j] = __ldg(reinterpret_cast<const uint4*>(x + r * a.ld + k));
+            if (i < n && k < p.kx) v[j] = *reinterpret_cast<const uint4*>(x + r * a.ld + k);
         }
 #pragma unroll
         for (int j = 0; j < 4; ++j) {
@@ -186,8 +186,8 @@ __global__ void __launch_bounds__(kMaxWarps * 32, 1) q8c_rows_kernel(const RowsP
         const bool on0 = n < w.N, on1 = n + 8 < w.N;
         w0 = on0 ? __ldg(sw + n) : 0.0f;
         w1 = on1 ? __ldg(sw + n + 8) : 0.0f;
-        b0 = c.bias && on0 ? __ldg(c.bias + n) : 0.0f;
-        b1 = c.bias && on1 ? __ldg(c.bias + n + 8) : 0.0f;
+        b0 = c.bias && on0 ? c.bias[n] : 0.0f;
+        b1 = c.bias && on1 ? c.bias[n + 8] : 0.0f;
     };
     // a row block's 16 x 8 sums to their places: column 2 t + i, rows g and g + 8
     auto put = [&](const int v[4], int rb) {

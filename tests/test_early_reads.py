@@ -17,3 +17,11 @@ def test_the_router_is_read_after_the_wait():
     body = source("qmm_moe_layer.cu").split("moe_router_kernel(", 1)[1]
     before = body.split("grid_dep_wait();", 1)[0]
     assert "router_load8(" not in before
+
+
+def test_what_an_earlier_grid_may_write_is_not_read_as_constant():
+    """ld.global.nc (__ldg) is for data that nobody writes while the kernel runs, and a kernel that was started early runs
+    while the grid before it writes activations, scales and sums: only what is in the laid-out weights (sw: their scales) goes that way."""
+    for name in ("qmm_q8c_rows.cu", "qmm_q8c_quant.cu", "qmm_q8c_gemm.cu", "qmm_moe_layer.cu", "qmm_moe_layer.cuh", "qmm_moe_route.cuh", "qmm_norm.cuh"):
+        for use in re.findall(r"__ldg\(([^;]*);", source(name)):
+            assert re.match(r"sw \+ n|reinterpret_cast<const uint32_t\*>\(w\.data \+ w\.norm_off\)", use), (name, use)
