@@ -133,6 +133,11 @@ qmm_status qmm_block_norm(const qmm_norm* n, int64_t T, int64_t K, qmm_stream_t 
     if (T == 0) return QMM_OK;
     if (!n->y || !n->weight || (n->h == nullptr) == (n->codes == nullptr) || (n->codes && !n->scales)) return QMM_ERR_NULL;
     if (n->h && n->h == n->residual_out) return QMM_ERR_SHAPE;  // two results, one place
+    // in place, row t's result lies on row t's input and on no other one's
+    auto astray = [&](const void* out, int64_t ld) {
+        return T > 1 && out && ((out == n->y && ld != n->ldy) || (out == n->residual && ld != n->ldr));
+    };
+    if (astray(n->residual_out, n->ldro) || astray(n->h, n->ldh)) return QMM_ERR_SHAPE;
     const uintptr_t a = (uintptr_t)x_size((int)n->type), wa = (uintptr_t)x_size((int)n->weight_type);
     if (!aligned(n->y, a) || !aligned(n->residual, a) || !aligned(n->gate, a) || !aligned(n->post_weight, wa) || !aligned(n->weight, wa) ||
         !aligned(n->residual_out, a) || !aligned(n->h, a) || !aligned(n->scales, 4))

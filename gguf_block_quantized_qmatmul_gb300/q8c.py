@@ -171,7 +171,8 @@ def block_norm(y: torch.Tensor, weight: torch.Tensor, residual: torch.Tensor | N
     """(r', h) of a block's output y [T, K], in one pass:
     v = y / sqrt(mean(y^2) + eps) (weight_offset + post_weight), or y; r' = residual + scale gate v;
     h = r' / sqrt(mean(r'^2) + eps) (weight_offset + weight), as floats or, with quantize, as Rows8.
-    gate: [K] or [T, K] of y's type.  weights: [K], both of one type.  out and residual_out may be y or residual, not both the same.
+    gate: [K] or [T, K] of y's type.  weights: [K], both of one type.  out and residual_out may be y or residual, with its
+    strides, not both the same.
     Small results (256 KB) share one allocation, as do codes and their scales."""
     if stream is not None:
         with _on(y.get_device(), stream):

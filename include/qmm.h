@@ -465,9 +465,9 @@ qmm_status qmm_q8c_matmul(const qmm_q8c* w, qmm_float xtype, const void* x, int6
    are of `type`, the weights of weight_type.  Rows are ld* elements apart
    (gate: 0 for one row for all).  A row's results depend neither on T nor on
    where the rows are.  residual_out may be residual or y, h may be y
-   or residual: a row is read whole before it is written; otherwise outputs
-   overlap nothing (both in one place: SHAPE).  Rows need no alignment beyond
-   their elements'.
+   or residual, with rows the same distance apart (another one: SHAPE): a row is
+   read whole before it is written; otherwise outputs overlap nothing (both in
+   one place: SHAPE).  Rows need no alignment beyond their elements'.
    Errors: NULL, TYPE, SHAPE, ALIGN, CUDA. */
 #define QMM_NORM_MAX_K 32768
 typedef struct {
