@@ -142,6 +142,8 @@ qmm_status qmm_block_norm(const qmm_norm* n, int64_t T, int64_t K, qmm_stream_t 
     if (!aligned(n->y, a) || !aligned(n->residual, a) || !aligned(n->gate, a) || !aligned(n->post_weight, wa) || !aligned(n->weight, wa) ||
         !aligned(n->residual_out, a) || !aligned(n->h, a) || !aligned(n->scales, 4))
         return QMM_ERR_ALIGN;
+    // codes are a byte each: a row's do not lie where its values do
+    if (n->codes && (n->codes == n->residual_out || n->codes == n->y || n->codes == n->residual)) return QMM_ERR_SHAPE;
     if (injected_launch_failure()) return QMM_ERR_CUDA;
     NormCall c;
     c.y = n->y;

@@ -467,7 +467,8 @@ qmm_status qmm_q8c_matmul(const qmm_q8c* w, qmm_float xtype, const void* x, int6
    where the rows are.  residual_out may be residual or y, h may be y
    or residual, with rows the same distance apart (another one: SHAPE): a row is
    read whole before it is written; otherwise outputs overlap nothing (both in
-   one place: SHAPE).  Rows need no alignment beyond their elements'.
+   one place, or codes in a place of y or residual: SHAPE).  Rows need no
+   alignment beyond their elements'.
    Errors: NULL, TYPE, SHAPE, ALIGN, CUDA. */
 #define QMM_NORM_MAX_K 32768
 typedef struct {

@@ -38,3 +38,11 @@ def test_in_place_rows_are_the_same_distance_apart(call, out, ld, at, ld_in):
     assert call(**{out: at, ld: 80, "T": 1}) == CUDA and call(**{out: OTHER, ld: 80}) == CUDA
     # y and residual are one tensor: a result in its place follows both distances
     assert call(**{out: Y, "residual": Y}) == CUDA and call(**{out: Y, "residual": Y, "ldr": 80}) == SHAPE
+
+
+def test_codes_lie_in_no_other_tensors_place(call):
+    ok = dict(h=0, codes=0x500000, scales=0x600000)
+    assert call(**ok) == CUDA and call(**{**ok, "residual_out": R}) == CUDA
+    assert call(**{**ok, "residual_out": OTHER, "codes": OTHER}) == SHAPE
+    for at in (Y, R):
+        assert call(**{**ok, "codes": at}) == SHAPE
