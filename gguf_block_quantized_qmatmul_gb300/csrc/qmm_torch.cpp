@@ -62,13 +62,6 @@ at::Tensor part(const at::Tensor& buffer, int64_t at, at::IntArrayRef sizes) {
     v.unsafeGetTensorImpl()->set_sizes_contiguous(sizes);
     return v;
 }
-// the same of type t, from byte `at` of a buffer on
-at::Tensor rows_of(const at::Tensor& buffer, int64_t at, at::ScalarType t, at::IntArrayRef sizes, at::IntArrayRef strides) {
-    at::Tensor v = at::detail::make_tensor<c10::TensorImpl>(c10::Storage(buffer.storage()), buffer.key_set(), c10::scalarTypeToTypeMeta(t));
-    v.unsafeGetTensorImpl()->set_storage_offset(at / (int64_t)c10::elementSize(t));
-    v.unsafeGetTensorImpl()->set_sizes_and_strides(sizes, strides);
-    return v;
-}
 
 // the weights that `o` describes, at where their tensor's data is now; the tensor's device
 qmm_q4g weights(PyObject* o, PyObject* data, int64_t& device) {
@@ -405,25 +398,25 @@ PyObject* norm(PyObject*, PyObject* const* a, Py_ssize_t n) {
         need(!quantize || a[9] == Py_None, "quantized rows are allocated by the call: no out");
         if (K < 1 || K > QMM_NORM_MAX_K) return PyLong_FromLong(QMM_ERR_SHAPE);
         const c10::cuda::CUDAGuard guard((c10::DeviceIndex)device);
-        // Codes and their scales share an allocation, as do small results, in 16-byte steps: half of a small call's time
-        // is the memory's.
+        // Small float results share an allocation, in 16-byte steps: half of a small call's time is the memory's.
+        // Results of several types have one each: torch.save takes no storage that is seen as two types.
         const at::ScalarType type = y.scalar_type();
         auto r16 = [](int64_t n) { return (n + 15) / 16 * 16; };
-        const int64_t pitch = r16(K), values = r16(T * K * (int64_t)y.element_size()), others = quantize ? T * pitch + T * 4 : values;
-        const bool both = a[10] == Py_None && a[9] == Py_None && values + others <= 262144;
+        const int64_t pitch = r16(K), values = r16(T * K * (int64_t)y.element_size());
+        const bool both = !quantize && a[10] == Py_None && a[9] == Py_None && 2 * values <= 262144;
         at::Tensor buffer, r, h, scales;
-        if (both || quantize) buffer = empty({(both ? values : 0) + others}, at::kByte, y.device());
-        r = both ? rows_of(buffer, 0, type, {T, K}, {K, 1}) : a[10] == Py_None ? empty({T, K}, type, y.device()) : tensor(a[10], "residual_out is a tensor");
+        if (both) buffer = empty({2 * values / (int64_t)y.element_size()}, type, y.device());
+        r = both ? part(buffer, 0, {T, K}) : a[10] == Py_None ? empty({T, K}, type, y.device()) : tensor(a[10], "residual_out is a tensor");
         p.residual_out = rows(r, p.ldro);
         if (quantize) {
-            const int64_t from = both ? values : 0;
-            h = rows_of(buffer, from, at::kChar, {T, K}, {pitch, 1});
-            scales = rows_of(buffer, from + T * pitch, at::kFloat, {T}, {1});
+            h = empty({T, pitch}, at::kChar, y.device());
+            if (pitch != K) h.unsafeGetTensorImpl()->set_sizes_and_strides(at::IntArrayRef({T, K}), at::IntArrayRef({pitch, 1}));
+            scales = empty({T}, at::kFloat, y.device());
             p.codes = static_cast<int8_t*>(h.data_ptr());
             p.scales = static_cast<float*>(scales.data_ptr());
             p.ldh = pitch;
         } else {
-            h = both ? rows_of(buffer, values, type, {T, K}, {K, 1}) : a[9] == Py_None ? empty({T, K}, type, y.device()) : tensor(a[9], "out is a tensor");
+            h = both ? part(buffer, values / (int64_t)y.element_size(), {T, K}) : a[9] == Py_None ? empty({T, K}, type, y.device()) : tensor(a[9], "out is a tensor");
             p.h = rows(h, p.ldh);
         }
         const qmm_status s = qmm_block_norm(&p, T, K, stream_of(device));
