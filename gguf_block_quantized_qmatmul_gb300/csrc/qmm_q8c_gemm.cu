@@ -609,6 +609,9 @@ QcGemmPlan plan_q8c_gemm(const QcCall& c, int sms, int smem_max) {
 }
 
 cudaError_t launch_q8c_gemm(const QcGemmPlan& pl, const QcCall& c, void* ws, unsigned* err, int stall, int smem_max, cudaStream_t s) {
+    // single blocks have up to 128 activation rows, so tiles of 256 K; what no kernel is compiled for is refused
+    auto* go = pl.cg == 2 && pl.kt == 2 ? gemm_go<2, 2> : pl.cg == 2 && pl.kt == 1 ? gemm_go<2, 1> : pl.cg == 1 && pl.kt == 2 ? gemm_go<1, 2> : nullptr;
+    if (!go) return cudaErrorInvalidConfiguration;
     uint8_t* wsb = static_cast<uint8_t*>(ws);
     const int M = c.a.M;
     const long long pitch = (long long)c.w.KS * 128;
@@ -643,7 +646,7 @@ cudaError_t launch_q8c_gemm(const QcGemmPlan& pl, const QcCall& c, void* ws, uns
     p.ktiles = (c.w.KS + pl.kt - 1) / pl.kt;
     p.off_raw = pl.nx * (pl.bx / pl.cg) * 256 * pl.kt;
     p.off_bar = p.off_raw + pl.nraw * kRaw * pl.kt;
-    e = pl.cg == 2 ? (pl.kt == 2 ? gemm_go<2, 2>(pl, tx, p, smem_max, s) : gemm_go<2, 1>(pl, tx, p, smem_max, s)) : gemm_go<1, 2>(pl, tx, p, smem_max, s);
+    e = go(pl, tx, p, smem_max, s);
     if (e != cudaSuccess || pl.ks == 1) return e;
     const dim3 grid((unsigned)((c.w.N + 255) / 256), (unsigned)M);
     return launch_pdl_2d(q8c_sum_kernel, grid.x, grid.y, 256, 0, s, (const int*)p.part, pl.ks, M, c.w.N, reinterpret_cast<const float*>(c.w.data + c.w.scale_off),
