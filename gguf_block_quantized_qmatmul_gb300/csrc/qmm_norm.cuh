@@ -262,7 +262,7 @@ __global__ void __launch_bounds__(TPR == 32 ? 64 : TPR) block_norm_kernel(const 
     const long long row = (long long)blockIdx.x * kRows + threadIdx.x / TPR;
     grid_dep_wait();
     if (row >= c.T) return;  // whole warps; blocks of one row have theirs
-    constexpr bool kLate = NV > 3;  // residual and gate where they are used, as registers do not hold them (16 x 14336 bf16 8.2 us, with spills 12)
+    constexpr bool kLate = NV > 3;  // residual and gate where they are used, as registers do not hold them (rows of 14336 in bf16 as four pieces 8.2 us, with all at once 12)
     Piece<XT, VEC> y[NV], r[NV], gate[NV];
     float v[NV][8];
 #pragma unroll

@@ -271,7 +271,7 @@ __global__ void __launch_bounds__(kQgThreads, 1) q8c_gemm_kernel(const __grid_co
             }
         } else {
             // ------------------------------ epilogue ------------------------------
-            // chunks of 8 columns part, part + 2, .. of the unit are this warp's
+            // chunks of 8 columns part, part + kEpiHalves, .. of the unit are this warp's
             const int ew = warp - kQgEpi0, q = warp & 3, part = ew >> 2;
             const uint32_t tq = (uint32_t)(32 * q) << 16;
             int cc = 0;
@@ -306,7 +306,7 @@ __global__ void __launch_bounds__(kQgThreads, 1) q8c_gemm_kernel(const __grid_co
                 if (u + unit_step < units) ask(place(u + unit_step));
                 // 16-bit results go to memory four at a time where their place allows it, of four rows: a quad of lanes exchanges its 4 x 8 values
                 // (a store a value and column took three times as long).  What a chunk needs is worked out before it:
-                // this warp's chunks are 16 columns apart, and the kind of result is told apart outside of them.
+                // this warp's chunks are kEpiHalves * kCols columns apart, and the kind of result is told apart outside of them.
                 const bool wide = p.wide;
                 const int sub = wide ? 2 * (lane & 3) : 0;  // the first of the columns that this lane writes
                 const long long first = (long long)(un.p0 + kCols * part + sub) * w.N + n - (wide ? lane & 3 : 0) + (p.ks > 1 ? (long long)un.split * M * w.N : 0);

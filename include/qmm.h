@@ -42,6 +42,8 @@
  *    nibble and value l of sub-block 2c+1 in its high nibble.)
  *  - Alignment: quantized buffers, x and workspace must start on a 16-byte
  *    boundary, float outputs on a 4-byte boundary (QMM_ERR_ALIGN).
+ *  - Outputs and workspace overlap neither each other nor an input, except
+ *    where an entry point says so.
  *  - M = 0 or N = 0 is a no-op returning QMM_OK.
  */
 #ifndef QMM_H
@@ -389,7 +391,9 @@ qmm_status qmm_moe_down(const qmm_q4g* w, qmm_float xtype, const void* h, int64_
      bias; y = sum over j of weights[t][j] (h[t][j] . Wd_e^T), h[t][j] =
      silu(x_t . Wg_e^T) * (x_t . Wu_e^T), as qmm_moe_gate_up and qmm_moe_down form
      them, but h keeps 16 bits or more between the two (qmm_moe_gate_up rounds it
-     to x's type).
+     to x's type).  The same call gives the same bits; a token's may differ in
+     its sums' last places beside other tokens, as where a row's f32 sum is cut
+     among warps follows from all of the call's experts.
    gate_up: paired, N = 2 F; down: as many experts, K = F.  ids and weights
    [T][top_k] (both or neither) take the routing.  y [T][down.N] contiguous.
    workspace: qmm_moe_layer_workspace(...) bytes, uninitialised; calls that may

@@ -39,3 +39,17 @@ def test_results_on_no_boundary(q, M, N, K, dt):
         assert torch.equal(out, ref)
         assert bool((buf[:shift] == 7).all()) and bool((buf[shift + M * N:] == 7).all())
     assert q.last_device_error() == 0
+
+
+@pytest.mark.parametrize("M,N,K", [(3, 500, 9001), (40, 1300, 576), (64, 4096, 4096), (300, 2052, 1024), (1024, 9000, 192)])
+def test_workspace_on_any_16_byte_boundary(q, M, N, K):
+    g = torch.Generator().manual_seed(M)
+    w = q.q8c_pack(torch.randint(-127, 128, (N, K), generator=g).to(torch.int8).cuda(), torch.rand(N, generator=g).cuda())
+    x = torch.randn((M, K), generator=g).half().cuda()
+    ref, n = q.q8c_matmul(w, x), q.q8c_matmul_workspace(w, M)
+    assert n > 0
+    for shift in (16, 48):
+        buf = torch.full((n + 80,), 0xA5, dtype=torch.uint8, device="cuda")
+        assert torch.equal(q.q8c_matmul(w, x, workspace=buf[shift:shift + n]), ref)
+        assert bool((buf[:shift] == 0xA5).all()) and bool((buf[shift + n:] == 0xA5).all())
+    assert q.last_device_error() == 0
