@@ -34,7 +34,7 @@
 // first products, and 8 more in blocks whose share held two experts.)
 //
 // Measured (2048 -> 2 x 1024 -> 2048, 8 of 64 experts, us): 1 token in bf16 20 (logits 5, routing 3, products 6 and
-// 4, the wait between them 2), 4 35, 8 46, 16 in f16 57 (28 at the peak; products 24 and 12, 5.6 TB/s), 32 69.
+// 4, the wait between them 2), 4 35, 8 46, 16 in f16 58 (28 at the peak; products 24 and 12, 5.6 TB/s), 32 68.
 //
 // Waits are bounded: one that gives up raises the error word and its block ends.
 #pragma once

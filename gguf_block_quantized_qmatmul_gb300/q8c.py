@@ -173,7 +173,7 @@ def block_norm(y: torch.Tensor, weight: torch.Tensor, residual: torch.Tensor | N
     h = r' / sqrt(mean(r'^2) + eps) (weight_offset + weight), as floats or, with quantize, as Rows8.
     gate: [K] or [T, K] of y's type.  weights: [K], both of one type.  out and residual_out may be y or residual, with its
     strides, not both the same.
-    Small float results (256 KB) share one allocation."""
+    Small float results (256 KB) share one allocation, which lives as long as either does."""
     if stream is not None:
         with _on(y.get_device(), stream):
             return block_norm(y, weight, residual, post_weight, gate, scale, eps, weight_offset, quantize, out, residual_out)
